@@ -24,6 +24,9 @@ __all__ = [
     "sparse_attn_set_wait_limit", "sparse_attn_select_kind", "sparse_attn_forward_kind",
     "sparse_attn_score_select",
     "sparse_attn_decode_step",
+    "PagedCacheDesc", "PagedCache", "sparse_attn_paged_append", "sparse_attn_paged_attend",
+    "sparse_attn_paged_attend_workspace_size", "sparse_attn_paged_evict",
+    "sparse_attn_paged_evict_workspace_size",
 ]
 
 SA_OK = 0
@@ -64,6 +67,17 @@ class _PlanParams(ctypes.Structure):
                 ("granularity", ctypes.POINTER(ctypes.c_int32)),
                 ("head_budget", ctypes.POINTER(ctypes.c_int32)),
                 ("share_kv", ctypes.c_int32)]
+
+
+class PagedCacheDesc(ctypes.Structure):
+    """``sa_paged_cache``: where a paged key-value cache's arrays are."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("k_page_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class SparseAttnError(RuntimeError):
@@ -118,6 +132,18 @@ def _load():
                                                     I32, P]),
         "sparse_attn_decode_step": (ctypes.c_int, [ctypes.POINTER(Shape), P, P, P, P, P, P, P,
                                                    P, I32, P, I32, P, P, P]),
+        "sparse_attn_paged_append": (ctypes.c_int, [ctypes.POINTER(PagedCacheDesc), P, P,
+                                                    ctypes.POINTER(I64), ctypes.POINTER(I64),
+                                                    I32, P, P, P, P, P]),
+        "sparse_attn_paged_attend_workspace_size": (ctypes.c_int, [
+            ctypes.POINTER(PagedCacheDesc), I32, I32, ctypes.POINTER(SZ)]),
+        "sparse_attn_paged_attend": (ctypes.c_int, [ctypes.POINTER(PagedCacheDesc), P, I64, I64,
+                                                    I32, P, I32, P, P, P, SZ, P, P]),
+        "sparse_attn_paged_evict_workspace_size": (ctypes.c_int, [ctypes.POINTER(PagedCacheDesc),
+                                                                  ctypes.POINTER(SZ)]),
+        "sparse_attn_paged_evict": (ctypes.c_int, [ctypes.POINTER(PagedCacheDesc),
+                                                   ctypes.POINTER(I32), I32, I32, P, P, P, P, SZ,
+                                                   P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -397,3 +423,64 @@ def sparse_attn_score_noalloc(shape: Shape, q, k, scores, stream=None):
         _noalloc = fn
     _check(_noalloc(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(scores), _stream(stream)),
            "sparse_attn_score_noalloc")
+
+
+def sparse_attn_paged_append(cache: PagedCacheDesc, k_new, v_new, k_strides, v_strides,
+                             num_new: int, counts, start, lens_out, dev_status, stream=None):
+    """Append new tokens; ``k_new`` / ``v_new`` are device addresses whose
+    (sequence, head, token) strides, in elements, are given."""
+    arr = ctypes.c_int64 * 3
+    _check(_lib.sparse_attn_paged_append(ctypes.byref(cache), k_new, v_new, arr(*k_strides),
+                                         arr(*v_strides), num_new, _ptr(counts), _ptr(start),
+                                         _ptr(lens_out), _ptr(dev_status), _stream(stream)),
+           "sparse_attn_paged_append")
+
+
+def sparse_attn_paged_attend_workspace_size(cache: PagedCacheDesc, num_q_heads: int,
+                                            accumulate: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.sparse_attn_paged_attend_workspace_size(ctypes.byref(cache), num_q_heads,
+                                                        1 if accumulate else 0, ctypes.byref(n)),
+           "sparse_attn_paged_attend_workspace_size")
+    return n.value
+
+
+def sparse_attn_paged_attend(cache: PagedCacheDesc, q, q_stride_b: int, q_stride_h: int,
+                             num_q_heads: int, o, lse, weights_out, ws, ws_bytes: int, dev_status,
+                             stream=None, o_dtype=None):
+    """Attention of one new token per sequence; ``q`` is a device address with
+    the given (sequence, head) strides, in elements."""
+    _check(_lib.sparse_attn_paged_attend(ctypes.byref(cache), q, q_stride_b, q_stride_h,
+                                         num_q_heads, _ptr(o), _out_dtype(o, o_dtype), _ptr(lse),
+                                         _ptr(weights_out), _ptr(ws), ws_bytes, _ptr(dev_status),
+                                         _stream(stream)),
+           "sparse_attn_paged_attend")
+
+
+def sparse_attn_paged_evict_workspace_size(cache: PagedCacheDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.sparse_attn_paged_evict_workspace_size(ctypes.byref(cache), ctypes.byref(n)),
+           "sparse_attn_paged_evict_workspace_size")
+    return n.value
+
+
+def sparse_attn_paged_evict(cache: PagedCacheDesc, keep, sinks: int, recent: int, lens_out,
+                            weights_out, positions_out, ws, ws_bytes: int, dev_status,
+                            stream=None):
+    """Evict by accumulated weight; ``keep`` holds the tokens to keep per KV
+    head (host ints)."""
+    if len(keep) != cache.num_kv_heads:
+        raise ValueError("keep must hold one budget per KV head")
+    _check(_lib.sparse_attn_paged_evict(ctypes.byref(cache), (ctypes.c_int32 * len(keep))(*keep),
+                                        sinks, recent, _ptr(lens_out), _ptr(weights_out),
+                                        _ptr(positions_out), _ptr(ws), ws_bytes,
+                                        _ptr(dev_status), _stream(stream)),
+           "sparse_attn_paged_evict")
+
+
+def __getattr__(name):
+    # PagedCache needs torch, which the C binding itself does not
+    if name == "PagedCache":
+        from .paged import PagedCache
+        return PagedCache
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

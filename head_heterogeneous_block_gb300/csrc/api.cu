@@ -14,6 +14,7 @@
 #include "kernels.h"
 #include "plan_impl.h"
 #include "sparse_attn.h"
+#include "wait_limit.h"
 
 namespace {
 
@@ -51,7 +52,7 @@ void free_device(sa_plan* p) {
 
 using sa_k::cuda_status;
 
-// Operational wait limit of the prefill forward, in ns (0: the kernel default).
+// Operational wait limit of the attention kernels, in ns (0: the kernel default).
 std::atomic<uint64_t> g_wait_ns{0};
 
 int64_t nblocks(const sa_shape* s) { return s->seq_len / s->block; }
@@ -73,6 +74,8 @@ bool has_granularity(const sa_plan* p) {
 }
 
 }  // namespace
+
+uint64_t sa_host::wait_limit() { return g_wait_ns.load(std::memory_order_relaxed); }
 
 namespace {
 

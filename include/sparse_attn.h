@@ -519,6 +519,137 @@ sa_status sparse_attn_score_plan(const sa_shape* shp, const sa_plan* plan,
                                  const void* q, const float* kbar_all,
                                  float* scores, sa_stream_t stream);
 
+/*
+ * A paged key-value cache with a length of its own for every (sequence, KV
+ * head) row r = b*Hkv + g, so that sequences differ in length and heads that
+ * keep different numbers of tokens share one pool.  A page holds `page`
+ * consecutive slots of one row; slot t of row r is row t % page of page
+ * table[r][t / page].  The descriptor is read on the host by each call; the
+ * arrays it points to are device memory of the caller.
+ */
+typedef struct sa_paged_cache {
+  void* k_pages;           /* bf16, page p at k_pages + p*k_page_stride:
+                              [page][d], 16-byte aligned                     */
+  void* v_pages;
+  int32_t* table;          /* [Bt][Hkv][max_pages] page numbers; entries past
+                              a row's last page are not read                 */
+  int32_t* lens;           /* [Bt][Hkv] tokens held by each row              */
+  float* weights;          /* [Bt][Hkv][max_pages*page] accumulated attention
+                              weight of each slot, or NULL                   */
+  int32_t* positions;      /* the same shape: position in its sequence of each
+                              slot's token, or NULL                          */
+  int64_t num_pages;       /* pages in the pools, 1 .. 2^31 - 1              */
+  int64_t k_page_stride;   /* elements between pages: a multiple of 8, at
+                              least page*d, below 2^38                       */
+  int64_t v_page_stride;
+  int32_t page;            /* slots per page: 16, 32, 64, 128 or 256         */
+  int32_t max_pages;       /* table entries of a row                         */
+  int32_t batch;           /* sequences Bt                                   */
+  int32_t num_kv_heads;    /* Hkv                                            */
+  int32_t head_dim;        /* d: 64 or 128                                   */
+} sa_paged_cache;
+
+/*
+ * Append new tokens to a paged cache: token t < counts[b] of sequence b and KV
+ * head g goes to slot lens[r] + t of row r: its key and value, weight 0 (with
+ * weights) and position start[b] + t (with positions).  No other slot changes.
+ *  - k_new, v_new: bf16, element (b, g, t, x) at offset b*strides[0] +
+ *    g*strides[1] + t*strides[2] + x; the host arrays k_strides and v_strides
+ *    hold multiples of 8 (>= 0); 16-byte aligned.  A view of a fused projection
+ *    output, the prefill layout [Hkv][S][d] and a decode step's [Bt][Hkv][d]
+ *    are all of this form.  They must not overlap the pools.
+ *  - num_new: the largest count, >= 1; counts: device [Bt], or NULL for
+ *    num_new tokens of every sequence; start: device [Bt], or NULL: positions
+ *    are then slot numbers.
+ *  - lens_out: device [Bt][Hkv], receives the new lengths; it may be
+ *    cache->lens itself.
+ * The caller has put every page that receives a token into the table; pages
+ * that receive tokens belong to one row each.
+ * dev_status: SA_DEV_BAD_COUNT when a length is outside [0, max_pages*page], a
+ * count outside [0, num_new], or a row has no slots left (all are clamped: the
+ * tokens that do not fit are dropped), SA_DEV_BAD_INDEX when a page number is
+ * outside the pool (the token is dropped; the length still grows).
+ * Errors: INVALID_ARG (NULL pointers, misalignment, strides), SHAPE (sizes),
+ * UNSUPPORTED (page, d), CUDA.
+ */
+sa_status sparse_attn_paged_append(const sa_paged_cache* cache, const void* k_new,
+                                   const void* v_new, const int64_t* k_strides,
+                                   const int64_t* v_strides, int32_t num_new,
+                                   const int32_t* counts, const int32_t* start,
+                                   int32_t* lens_out, int32_t* dev_status, sa_stream_t stream);
+
+/*
+ * Workspace bytes of sparse_attn_paged_attend for `num_q_heads` query heads,
+ * with (accumulate = 1) or without a weights_out.  Host only, except that it
+ * asks the current device for its number of processors.
+ */
+sa_status sparse_attn_paged_attend_workspace_size(const sa_paged_cache* cache,
+                                                  int32_t num_q_heads, int32_t accumulate,
+                                                  size_t* bytes);
+
+/*
+ * Attention of one new token per sequence over a paged cache: for query head h
+ * of KV head g = h / (Hq/Hkv), row r = b*Hkv + g and its n = lens[r] slots,
+ *   s_t = q[b,h] . K[r,t] / sqrt(d),  p_t = exp(s_t - lse[b,h]),
+ *   lse[b,h] = log sum_t exp(s_t),    o[b,h] = sum_t p_t V[r,t].
+ * A row with no slot gives o = 0 and lse = -infinity.  Slots behind a row's
+ * length are never used, whatever their pages hold.
+ *  - q: bf16, element (b, h, x) at b*q_stride_b + h*q_stride_h + x, strides
+ *    multiples of 8 and at least d, below 2^38; 16-byte aligned.
+ *  - o [Bt][Hq][d] in o_dtype; lse [Bt][Hq] fp32 or NULL.
+ *  - weights_out: NULL, or [Bt][Hkv][max_pages*page] (needs cache->weights;
+ *    may be the same array): weights_out[r][t] = weights[r][t] + the sum of p_t
+ *    over the Hq/Hkv query heads of the row, for t < lens[r]; other entries are
+ *    left as they are.
+ *  - ws: at least sparse_attn_paged_attend_workspace_size bytes, 256-byte
+ *    aligned.  Its contents need no preparation and hold nothing between
+ *    calls; calls that may run at the same time need one each.
+ * Softmax, sums and lse are fp32.  The work is split over slots, not rows, and
+ * joined in a fixed order: the same inputs give the same bits.
+ * dev_status: SA_DEV_BAD_COUNT / SA_DEV_BAD_INDEX for lengths and page numbers
+ * out of range (clamped; page 0 is read instead), SA_DEV_TIMEOUT as in
+ * sparse_attn_forward (its limit is sparse_attn_set_wait_limit's),
+ * SA_DEV_BAD_LAUNCH.
+ * Errors: INVALID_ARG, SHAPE (Hq % Hkv, sizes), UNSUPPORTED (page, d), CUDA.
+ */
+sa_status sparse_attn_paged_attend(const sa_paged_cache* cache, const void* q, int64_t q_stride_b,
+                                   int64_t q_stride_h, int32_t num_q_heads, void* o,
+                                   int32_t o_dtype, float* lse, float* weights_out, void* ws,
+                                   size_t ws_bytes, int32_t* dev_status, sa_stream_t stream);
+
+/* Workspace bytes of sparse_attn_paged_evict.  Host only. */
+sa_status sparse_attn_paged_evict_workspace_size(const sa_paged_cache* cache, size_t* bytes);
+
+/*
+ * Evict tokens by accumulated attention weight: row r of KV head g is cut to
+ * m = min(lens[r], keep[g]) tokens.  A row that holds more keeps, in this
+ * order, the tokens at positions below `sinks` and those at the last `recent`
+ * positions (above the row's largest position - recent), then the tokens of
+ * the largest weight; equal ones go to the lower slot.  A NaN weight counts as
+ * below every number.  The kept tokens of slots >= m move into the evicted
+ * slots < m, the lowest into the lowest, with their weights and positions;
+ * kept tokens of slots < m stay, so as few tokens move as can be.  (Attention
+ * does not depend on the order of the slots.)
+ *  - keep: host [Hkv], each >= sinks + recent; Hkv <= 256.
+ *  - lens_out [Bt][Hkv], weights_out, positions_out
+ *    [Bt][Hkv][max_pages*page]: the new state, slots < m of each row (entries
+ *    behind are left as they are); each may be the cache's own array.
+ *    positions_out is NULL when the cache has no positions: a token's position
+ *    is then its slot.
+ *  - The pools change in place; a row's pages must belong to it alone.
+ *  - ws: at least sparse_attn_paged_evict_workspace_size bytes, 16-byte
+ *    aligned, as for sparse_attn_paged_attend.
+ * dev_status: SA_DEV_BAD_COUNT / SA_DEV_BAD_INDEX (a token whose page number is
+ * out of range is not moved).
+ * Errors: INVALID_ARG (NULL pointers, no cache->weights, keep[g] < sinks +
+ * recent, negative sinks or recent, misalignment), SHAPE, UNSUPPORTED (page, d,
+ * Hkv > 256, rows of more than 262144 slots), CUDA.
+ */
+sa_status sparse_attn_paged_evict(const sa_paged_cache* cache, const int32_t* keep, int32_t sinks,
+                                  int32_t recent, int32_t* lens_out, float* weights_out,
+                                  int32_t* positions_out, void* ws, size_t ws_bytes,
+                                  int32_t* dev_status, sa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,483 @@
+"""The paged cache operators on the GPU against the fp64 oracle."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import head_heterogeneous_block_gb300 as sa
+    return sa, torch
+
+
+def _q(torch, seed, b, hq, d, sharp=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(b, hq, d, generator=g) * sharp).bfloat16()
+
+
+def _attend(env, c, hq, out_dtype="bfloat16", weights=False, sharp=1.0, seed=5, **kw):
+    from tests import _paged as P
+    sa, torch = env
+    b, hkv = c["lens"].shape
+    d = c["k"].shape[2]
+    q = _q(torch, seed, b, hq, d, sharp)
+    dev, cache = P.to_gpu(c, sa)
+    out = torch.full((b, hq, d), 7.0, dtype=getattr(torch, out_dtype), device="cuda")
+    lse = torch.full((b, hq), 7.0, device="cuda")
+    w = torch.full_like(dev["weights"], -3.0) if weights else None
+    cache.attend(q.cuda(), out=out, lse=lse, weights_out=w, accumulate=weights, **kw)
+    torch.cuda.synchronize()
+    assert int(cache.dev_status.item()) == 0
+    P.check_attend(c, q, out, lse, w)
+    if weights:
+        # slots behind a row's length stay as they were
+        t = torch.arange(w.shape[-1])
+        behind = t >= c["lens"][..., None]
+        assert (w.cpu()[behind] == -3.0).all()
+    return out, lse, w
+
+
+EDGES = [0, 1, 15, 16, 17, 31, 33, 63, 64, 127, 128, 129, 255, 257, 700, 1025]
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (7, 1, 128)])
+def test_attend_lengths(env, page, hq, hkv, d):
+    from tests import _paged as P
+    c = P.random_cache(page + d, EDGES, hkv, d, page)
+    _attend(env, c, hq, weights=True)
+    _attend(env, c, hq, "float32")
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 8, 9, 12, 16, 17, 20, 32, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_groups(env, G, d):
+    from tests import _paged as P
+    c = P.random_cache(G, [[300, 5], [0, 129], [64, 1000]], 2, d, 32)
+    _attend(env, c, 2 * G, weights=True)
+    _attend(env, c, 2 * G, "float32", weights=True)
+
+
+@pytest.mark.parametrize("lens,hkv", [([20000], 1), ([9000, 1, 4097], 2), ([130] * 200, 4)])
+def test_attend_splits_and_many_rows(env, lens, hkv):
+    from tests import _paged as P
+    c = P.random_cache(3, lens, hkv, 128, 64)
+    _attend(env, c, 4 * hkv, weights=True)
+    _attend(env, c, 4 * hkv, "float32")
+
+
+@pytest.mark.parametrize("sharp", [0.0, 30.0])
+def test_attend_flat_and_sharp_scores(env, sharp):
+    # equal scores everywhere, and scores whose maximum grows far along the row
+    from tests import _paged as P
+    c = P.random_cache(8, [3000, 513], 2, 128, 16)
+    c["k"][:] = (c["k"].float() * 1.0).bfloat16()
+    _attend(env, c, 8, weights=True, sharp=sharp)
+    _attend(env, c, 8, "float32", sharp=sharp)
+
+
+def test_attend_growing_scores(env):
+    # keys that score ever higher towards the row's end: the running maximum
+    # moves in every piece
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(9, [2000], 1, 128, 32, junk=False)
+    q = torch.ones(1, 4, 128).bfloat16()
+    t = torch.arange(2000)
+    p, x = c["table"][0, 0].long()[t // 32], t % 32
+    c["k"][p, x] = (0.02 * (t // 8).float()[:, None].expand(-1, 128)).bfloat16()
+    dev, cache = P.to_gpu(c, sa)
+    out, lse = torch.empty(1, 4, 128, device="cuda"), torch.empty(1, 4, device="cuda")
+    w = torch.zeros_like(dev["weights"])
+    cache.attend(q.cuda(), out=out, lse=lse, weights_out=w)
+    assert int(cache.dev_status.item()) == 0
+    P.check_attend(c, q, out, lse, w)
+
+
+def test_attend_strided_queries_and_interleaved_pools(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(10, [77, 300, 0], 2, 128, 32, interleaved=True)
+    assert c["k"].stride(0) == 2 * 32 * 128
+    dev, cache = P.to_gpu(c, sa)
+    assert dev["k"].stride(0) == 2 * 32 * 128
+    big = _q(torch, 1, 3, 30, 256)
+    q = big[:, 3:27:3, 64:192]
+    out = cache.attend(big.cuda()[:, 3:27:3, 64:192])
+    assert out.dtype == torch.bfloat16 and out.shape == (3, 8, 128)
+    assert int(cache.dev_status.item()) == 0
+    P.check_attend(c, q, out, None)
+
+
+def test_attend_adds_in_place_and_is_repeatable(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(11, [5000, 64, 1], 2, 128, 64)
+    q = _q(torch, 2, 3, 8, 128)
+    outs = []
+    for _ in range(2):
+        dev, cache = P.to_gpu(c, sa)
+        o = cache.attend(q.cuda())
+        outs.append((o, dev["weights"]))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    P.check_attend(c, q, outs[0][0], None, outs[0][1])
+    t = torch.arange(c["weights"].shape[-1])
+    behind = t >= c["lens"][..., None]
+    assert torch.equal(outs[0][1].cpu()[behind], c["weights"][behind])
+    # without accumulation the weights stay
+    dev, cache = P.to_gpu(c, sa)
+    o = cache.attend(q.cuda(), accumulate=False)
+    assert torch.equal(o, outs[0][0]) and torch.equal(dev["weights"].cpu(), c["weights"])
+
+
+def test_attend_propagates_nan_of_live_tokens_only_to_its_row(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(12, [100, 200], 1, 64, 16)
+    t = 37
+    c["v"][c["table"][0, 0, t // 16].long(), t % 16, 3] = float("nan")
+    dev, cache = P.to_gpu(c, sa)
+    o = cache.attend(_q(torch, 3, 2, 4, 64).cuda()).float().cpu()
+    assert torch.isnan(o[0, :, 3]).all()
+    o[0, :, 3] = 0
+    assert torch.isfinite(o).all()
+
+
+def test_attend_far_pages(env):
+    # element offsets beyond 2^31 in both pools
+    from tests import _paged as P
+    sa, torch = env
+    page, d, pages = 64, 128, (1 << 31) // (64 * 128) + 64
+    k = torch.empty(pages, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty(pages, page, d, dtype=torch.bfloat16, device="cuda")
+    c = P.random_cache(13, [500], 1, d, page, spare=0)
+    n = c["k"].shape[0]
+    k[pages - n:], v[pages - n:] = c["k"].cuda(), c["v"].cuda()
+    table = (c["table"] + (pages - n)).cuda()
+    w, pos, lens = c["weights"].cuda(), c["positions"].cuda(), c["lens"].cuda()
+    cache = sa.PagedCache(k, v, table, lens, weights=w, positions=pos)
+    q = _q(torch, 4, 1, 4, d)
+    o = cache.attend(q.cuda(), accumulate=False)
+    P.check_attend(c, q, o, None)
+    # append into the last slots, then evict across them
+    kn = _q(torch, 5, 1, 5, d)[:, None].contiguous()
+    vn = _q(torch, 6, 1, 5, d)[:, None].contiguous()
+    cache.append(kn.cuda(), vn.cuda())
+    from oracle import paged as op
+    ref = op.append(P.f64(c["k"]), P.f64(c["v"]), c["table"].numpy(), c["lens"].numpy(), P.f64(kn),
+                    P.f64(vn), [5], [500], P.f64(c["weights"]), c["positions"].numpy())
+    cache.evict([300], 4, 16)
+    ref = op.evict(ref[0], ref[1], c["table"].numpy(), *ref[2:], [300], 4, 16)
+    assert int(cache.dev_status.item()) == 0
+    used = P.slot_mask(c["table"], torch.as_tensor(ref[2]), page, n)
+    assert np.array_equal(P.f64(k[pages - n:])[used], ref[0][used])
+    assert np.array_equal(P.f64(v[pages - n:])[used], ref[1][used])
+    assert lens.cpu().numpy().tolist() == ref[2].tolist()
+    assert np.array_equal(P.f64(w)[0, 0, :300], ref[3][0, 0, :300])
+
+
+@pytest.mark.parametrize("Bt,hkv,d,page,T", [(3, 2, 128, 16, 1), (70, 8, 128, 32, 1),
+                                             (2, 2, 64, 64, 1), (4, 2, 128, 32, 37),
+                                             (3, 1, 64, 256, 300), (1, 4, 128, 128, 1000)])
+@pytest.mark.parametrize("inplace", [True, False])
+def test_append(env, Bt, hkv, d, page, T, inplace):
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    r = np.random.default_rng(Bt * T)
+    lens = r.integers(0, 400, Bt)
+    counts = r.integers(0, T + 1, Bt).astype(np.int32)
+    counts[0] = T
+    start = r.integers(0, 1000, Bt).astype(np.int32)
+    c = P.random_cache(T, lens + T, hkv, d, page, junk=False)     # pages for all of them
+    c["lens"] = torch.as_tensor(lens, dtype=torch.int32)[:, None].expand(-1, hkv).contiguous()
+    g = torch.Generator().manual_seed(T)
+    qkv = torch.randn(Bt, T, 3 * hkv, d, generator=g).bfloat16()  # a fused projection's output
+    kn, vn = qkv[:, :, hkv:2 * hkv].transpose(1, 2), qkv[:, :, 2 * hkv:].transpose(1, 2)
+    dev, cache = P.to_gpu(c, sa)
+    gq = qkv.cuda()
+    lens_out = None if inplace else torch.full_like(dev["lens"], -1)
+    cache.append(gq[:, :, hkv:2 * hkv].transpose(1, 2), gq[:, :, 2 * hkv:].transpose(1, 2),
+                 counts=torch.as_tensor(counts).cuda(), start=torch.as_tensor(start).cuda(),
+                 lens_out=lens_out)
+    assert int(cache.dev_status.item()) == 0
+    k, v, l, w, p = op.append(P.f64(c["k"]), P.f64(c["v"]), c["table"].numpy(), c["lens"].numpy(),
+                              P.f64(kn), P.f64(vn), counts, start, P.f64(c["weights"]),
+                              c["positions"].numpy())
+    assert np.array_equal(P.f64(dev["k"]), k) and np.array_equal(P.f64(dev["v"]), v)
+    assert np.array_equal((dev["lens"] if inplace else lens_out).cpu().numpy(), l)
+    if not inplace:
+        assert torch.equal(dev["lens"].cpu(), c["lens"])
+    assert np.array_equal(P.f64(dev["weights"]), w)
+    assert np.array_equal(dev["positions"].cpu().numpy(), p)
+
+
+def test_append_defaults_and_overflow(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(21, [10, 32], 1, 64, 16, max_pages=2, junk=False)
+    c["table"][0, 0, 1] = c["table"].max() + 1
+    c["table"][0, 0, 1] = [x for x in range(c["k"].shape[0]) if x not in c["table"].flatten().tolist()][0]
+    dev, cache = P.to_gpu(c, sa)
+    kn = torch.randn(2, 1, 4, 64).bfloat16()
+    cache.append(kn.cuda(), kn.cuda())           # row 1 is full: its tokens are dropped
+    assert int(cache.dev_status.item()) == sa.SA_DEV_BAD_COUNT
+    assert dev["lens"].flatten().tolist() == [14, 32]
+    k = dev["k"].cpu()
+    page, x = c["table"][0, 0, 0].item(), torch.arange(10, 14)
+    assert torch.equal(k[page, x], kn[0, 0])
+    k[page, x] = c["k"][page, x]
+    assert torch.equal(k, c["k"])
+    assert dev["positions"][0, 0, 10:14].tolist() == [10, 11, 12, 13]
+    assert (dev["weights"][0, 0, 10:14] == 0).all()
+
+
+def test_out_of_range_pages_and_lengths_are_flagged_not_used(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(22, [100, 60], 1, 128, 32, junk=False)
+    c["table"][0, 0, 1] = c["k"].shape[0]
+    c["table"][1, 0, 0] = -5
+    before = c["k"].clone()
+    dev, cache = P.to_gpu(c, sa)
+    out = cache.attend(_q(torch, 7, 2, 4, 128).cuda())
+    torch.cuda.synchronize()
+    assert int(cache.dev_status.item()) == sa.SA_DEV_BAD_INDEX
+    assert torch.isfinite(out.float()).all()
+    dev["table"][0, 0, 3] = 1 << 30              # the page that the next tokens go to
+    cache.dev_status.zero_()
+    kn = torch.randn(2, 1, 2, 128).bfloat16().cuda()
+    cache.append(kn, kn, counts=torch.tensor([2, 0], dtype=torch.int32).cuda())
+    assert int(cache.dev_status.item()) == sa.SA_DEV_BAD_INDEX
+    assert torch.equal(dev["k"].cpu(), before)
+    assert dev["lens"].flatten().tolist() == [102, 60]
+    # lengths out of range are clamped
+    for bad, clamped in ((-7, 0), (1 << 30, cache.slots)):
+        dev, cache = P.to_gpu(P.random_cache(22, [100, 60], 1, 128, 32, junk=False), sa)
+        dev["table"].clamp_(min=0)
+        dev["lens"][0, 0] = bad
+        cache.attend(_q(torch, 7, 2, 4, 128).cuda())
+        assert int(cache.dev_status.item()) == sa.SA_DEV_BAD_COUNT
+        cache.dev_status.zero_()
+        cache.evict([40], 2, 2)
+        assert int(cache.dev_status.item()) == sa.SA_DEV_BAD_COUNT
+        assert dev["lens"].flatten().tolist() == [min(clamped, 40), 40]
+
+
+def _evict_case(torch, c, kind, seed):
+    g = torch.Generator().manual_seed(seed)
+    w = c["weights"]
+    if kind == "random":
+        w.copy_(torch.exp(2 * torch.randn(w.shape, generator=g)))
+    elif kind == "ties":
+        w.copy_(torch.randint(0, 3, w.shape, generator=g).float())
+    elif kind == "zeros":
+        w.zero_()
+        w[..., ::2] = -0.0
+    elif kind == "odd":
+        vals = torch.tensor([float("nan"), float("inf"), -float("inf"), -1.0, 0.0, -0.0, 1e-40, 2.0])
+        w.copy_(vals[torch.randint(0, 8, w.shape, generator=g)])
+    pos = torch.argsort(torch.rand(c["positions"].shape, generator=g), -1).int() * 2
+    c["positions"].copy_(pos)
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "zeros", "odd"])
+@pytest.mark.parametrize("lens,keep,sinks,recent,d,page", [
+    ([[300, 40], [0, 1], [64, 1000]], [64, 50], 4, 16, 128, 32),
+    ([[300, 40], [1, 2], [512, 513]], [0, 1], 0, 0, 64, 16),
+    ([[5000, 4100], [2049, 33]], [2048, 700], 0, 100, 128, 64),
+    ([[700, 700]], [700, 699], 10, 0, 64, 256),
+    ([[20000, 9999]], [128, 9000], 4, 64, 64, 128),
+])
+def test_evict(env, kind, lens, keep, sinks, recent, d, page):
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(31, lens, 2, d, page, junk=False)
+    _evict_case(torch, c, kind, 5)
+    ref = op.evict(P.f64(c["k"]), P.f64(c["v"]), c["table"].numpy(), c["lens"].numpy(),
+                   c["weights"].numpy(), c["positions"].numpy(), keep, sinks, recent)
+    t = torch.arange(c["weights"].shape[-1])
+    live = (t < torch.as_tensor(ref[2])[..., None]).numpy()
+    for inplace in (True, False):
+        dev, cache = P.to_gpu(c, sa)
+        outs = {}
+        if not inplace:
+            outs = {"lens_out": torch.full_like(dev["lens"], -9),
+                    "weights_out": torch.full_like(dev["weights"], -9.0),
+                    "positions_out": torch.full_like(dev["positions"], -9)}
+        cache.evict(keep, sinks, recent, **outs)
+        assert int(cache.dev_status.item()) == 0
+        assert np.array_equal(P.f64(dev["k"]), ref[0]) and np.array_equal(P.f64(dev["v"]), ref[1])
+        got = [dev["lens"], dev["weights"], dev["positions"]] if inplace else list(outs.values())
+        assert np.array_equal(got[0].cpu().numpy(), ref[2])
+        assert np.array_equal(got[1].cpu().numpy()[live], ref[3][live], equal_nan=True)
+        assert np.array_equal(got[2].cpu().numpy()[live], ref[4][live])
+        if inplace:
+            assert np.array_equal(got[1].cpu().numpy()[~live], c["weights"].numpy()[~live], equal_nan=True)
+            assert np.array_equal(got[2].cpu().numpy()[~live], c["positions"].numpy()[~live])
+        else:
+            assert (got[1].cpu().numpy()[~live] == -9).all() and (got[2].cpu().numpy()[~live] == -9).all()
+            assert torch.equal(dev["lens"].cpu(), c["lens"])
+            assert np.array_equal(P.f64(dev["weights"]), P.f64(c["weights"]), equal_nan=True)
+
+
+def test_evict_without_positions(env):
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(32, [500, 100], 1, 128, 32, junk=False)
+    dev, _ = P.to_gpu(c, sa)
+    cache = sa.PagedCache(dev["k"], dev["v"], dev["table"], dev["lens"], weights=dev["weights"])
+    cache.evict([120], 8, 32)
+    ref = op.evict(P.f64(c["k"]), P.f64(c["v"]), c["table"].numpy(), c["lens"].numpy(),
+                   c["weights"].numpy(), c["positions"].numpy(), [120], 8, 32)
+    assert int(cache.dev_status.item()) == 0
+    assert np.array_equal(P.f64(dev["k"]), ref[0]) and np.array_equal(dev["lens"].cpu().numpy(), ref[2])
+    assert np.array_equal(dev["weights"].cpu().numpy(), ref[3])
+
+
+def test_decode_loop_with_evictions(env):
+    # append, attend with weights and evict in turn, as a serving loop runs
+    # them; the oracle follows on the GPU's own weights, so that a rounding of
+    # a weight cannot turn into another eviction
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    Bt, hkv, hq, d, page, keep = 2, 2, 8, 128, 16, [48, 80]
+    c = P.random_cache(41, [[60, 90], [33, 100]], hkv, d, page, max_pages=8, spare=20, junk=False)
+    free = [x for x in range(c["k"].shape[0]) if x not in c["table"].flatten().tolist()]
+    for b in range(Bt):
+        for g in range(hkv):
+            for i in range(8):
+                if c["table"][b, g, i] < 0 and i < 7 and free:
+                    c["table"][b, g, i] = free.pop()
+    dev, cache = P.to_gpu(c, sa, num_q_heads=hq)
+    gen = torch.Generator().manual_seed(3)
+    for step in range(24):
+        kn = torch.randn(Bt, hkv, 1, d, generator=gen).bfloat16()
+        vn = torch.randn(Bt, hkv, 1, d, generator=gen).bfloat16()
+        q = torch.randn(Bt, hq, d, generator=gen).bfloat16()
+        start = torch.full((Bt,), 200 + step, dtype=torch.int32)
+        state = {n: dev[n].cpu() for n in ("k", "v", "table", "lens", "weights", "positions")}
+        cache.append(kn.cuda(), vn.cuda(), start=start.cuda())
+        ref = op.append(P.f64(state["k"]), P.f64(state["v"]), state["table"].numpy(),
+                        state["lens"].numpy(), P.f64(kn), P.f64(vn), [1] * Bt, start.numpy(),
+                        P.f64(state["weights"]), state["positions"].numpy())
+        assert np.array_equal(P.f64(dev["k"]), ref[0]) and np.array_equal(dev["lens"].cpu().numpy(), ref[2])
+        after = {n: dev[n].cpu() for n in ("k", "v", "table", "lens", "weights", "positions")}
+        lse = torch.empty(Bt, hq, device="cuda")
+        o = cache.attend(q.cuda(), lse=lse)
+        P.check_attend({**after, "page": page}, q, o, lse, dev["weights"], after["weights"])
+        if step % 8 == 7:
+            state = {n: dev[n].cpu() for n in ("k", "v", "table", "lens", "weights", "positions")}
+            cache.evict(keep, 4, 8)
+            ref = op.evict(P.f64(state["k"]), P.f64(state["v"]), state["table"].numpy(),
+                           state["lens"].numpy(), state["weights"].numpy(),
+                           state["positions"].numpy(), keep, 4, 8)
+            assert np.array_equal(P.f64(dev["k"]), ref[0]) and np.array_equal(P.f64(dev["v"]), ref[1])
+            assert np.array_equal(dev["lens"].cpu().numpy(), ref[2])
+            for b in range(Bt):
+                for g in range(hkv):
+                    m = int(ref[2][b, g])
+                    assert np.array_equal(dev["weights"].cpu().numpy()[b, g, :m], ref[3][b, g, :m])
+                    assert np.array_equal(dev["positions"].cpu().numpy()[b, g, :m], ref[4][b, g, :m])
+    assert int(cache.dev_status.item()) == 0
+
+
+def test_captured_steps_follow_the_state(env):
+    # append + attend captured once; each replay reads the lengths of its time
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(42, [100, 250], 2, 64, 16, max_pages=20, spare=60, junk=False)
+    free = [x for x in range(c["k"].shape[0]) if x not in c["table"].flatten().tolist()]
+    c["table"][c["table"] < 0] = torch.tensor(free[:int((c["table"] < 0).sum())], dtype=torch.int32)
+    dev, cache = P.to_gpu(c, sa, num_q_heads=8)
+    kv = torch.zeros(2, 2, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty(2, 8, 64, device="cuda"), torch.empty(2, 8, device="cuda")
+    lens0 = dev["lens"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.append(kv[0], kv[1])
+        cache.attend(q, out=out, lse=lse)
+    assert torch.equal(dev["lens"], lens0)
+    for step in range(5):
+        kv.copy_(torch.randn(kv.shape, device="cuda"))
+        q.copy_(torch.randn(q.shape, device="cuda"))
+        before = dev["weights"].cpu().clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dev["lens"], lens0 + step + 1)
+        now = {n: dev[n].cpu() for n in ("k", "v", "table", "lens", "weights")}
+        for b in range(2):
+            for h in range(2):
+                before[b, h, int(now["lens"][b, h]) - 1] = 0       # the appended token's weight
+        P.check_attend({**now, "page": 16}, q.cpu(), out, lse, dev["weights"], before)
+    assert int(cache.dev_status.item()) == 0
+
+
+def test_calls_on_a_given_stream(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(43, [900, 30], 2, 128, 32)
+    dev, cache = P.to_gpu(c, sa)
+    q = _q(torch, 9, 2, 8, 128)
+    gq = q.cuda()
+    ref = cache.attend(gq, accumulate=False)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a = cache.attend(gq, accumulate=False, stream=side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        b = cache.attend(gq, accumulate=False)
+    side.synchronize()
+    e = cache.attend(gq, accumulate=False, stream=side.cuda_stream)
+    side.synchronize()
+    for x in (a, b, e):
+        assert torch.equal(x, ref)
+
+
+def test_python_class_refusals(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(44, [20], 2, 64, 16)
+    dev, cache = P.to_gpu(c, sa)
+    q = torch.zeros(1, 8, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in (q.float(), q[:, :7], q[0], q[:, :, :32], q.cpu(), q.expand(2, 8, 64)):
+        with pytest.raises((ValueError, TypeError, sa.SparseAttnError)):
+            cache.attend(bad)
+    with pytest.raises((ValueError, sa.SparseAttnError)):
+        cache.attend(q[:, :1].expand(1, 8, 64))          # heads on top of one another
+    with pytest.raises(TypeError):
+        cache.attend(q, out=torch.empty(1, 8, 64, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError):
+        cache.attend(q, lse=torch.empty(8, device="cuda"))
+    with pytest.raises(ValueError):
+        cache.attend(q, accumulate=False, weights_out=dev["weights"])
+    k = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in ((k.float(), k), (k, k[:, :, :2]), (k[:, :1], k[:, :1]), (k[:, :, :0], k[:, :, :0]), (k.cpu(), k)):
+        with pytest.raises((ValueError, TypeError)):
+            cache.append(*bad)
+    with pytest.raises(ValueError):
+        cache.append(k, k, counts=torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError):
+        cache.evict([10])
+    with pytest.raises(sa.SparseAttnError):
+        cache.evict([10, 3], 2, 2)
+    plain = sa.PagedCache(dev["k"], dev["v"], dev["table"], dev["lens"])
+    with pytest.raises(ValueError):
+        plain.evict([10, 10])
+    with pytest.raises(ValueError):
+        plain.attend(q, accumulate=True)
+    assert int(cache.dev_status.item()) == 0
+    with pytest.raises(ValueError):
+        sa.PagedCache(dev["k"].transpose(1, 2), dev["v"].transpose(1, 2), dev["table"], dev["lens"])
+    with pytest.raises(ValueError):
+        sa.PagedCache(dev["k"], dev["v"], dev["table"], dev["lens"], weights=dev["weights"][..., :-1].contiguous())
