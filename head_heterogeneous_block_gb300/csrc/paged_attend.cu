@@ -63,19 +63,24 @@ constexpr int kTile = 128;             // tokens per tile
 constexpr int kChunk = 16;             // query heads of a row handled together
 constexpr int kThreads = 192;
 constexpr int kInfo = 8;               // tile descriptions in flight
-constexpr int kMaxCtas = 256;
+constexpr int kPerSm = 2;              // CTAs per processor
 constexpr float kMove = 8.f;           // how far a score may pass its reference
 constexpr int kJoinThreads = 512;
+constexpr int kJoinHeads = 4;          // heads of a join block, four warps each
+constexpr int kWeightThreads = 256;
+constexpr int kWeightSteps = 4;        // tokens of a thread
 
 template <int D, int GP, int PARTS>
 struct Cfg {
   static constexpr int kPanels = D / 64;              // 128-byte column panels
   static constexpr int kPanel = kTile * 128;          // bytes of one K/V panel
   static constexpr int kStage = kPanels * kPanel;
-  static constexpr int kStages = D == 128 ? 6 : 10;   // even: K on even stages, V on odd
+  static constexpr int kStages = D == 128 ? 3 : 6;    // tile j: K in stage 2j % kStages, V next
   static constexpr int kNS = 16;                      // columns of S
   static constexpr int kNP = (GP * PARTS + 15) / 16 * 16;   // columns of O, rows of P
   static constexpr int kQ = kPanels * kChunk * 128;   // bytes of one Q tile
+  // two Q tiles, but where only one leaves room for two CTAs on a processor
+  static constexpr int kQs = D == 128 && GP * PARTS > 32 ? 1 : 2;
   static constexpr int kP = 2 * kNP * 128;            // bytes of P (two panels of 64 tokens)
   static constexpr uint32_t kO = 2 * kNS;             // TMEM column of O
   static constexpr uint32_t kTmemCols = 128;
@@ -90,7 +95,7 @@ struct TileInfo {
 enum { kFirst = 1, kLast = 2, kComplete = 4, kSecond = 8 };
 
 struct Shared {
-  uint64_t kv_full[10], kv_empty[10];
+  uint64_t kv_full[6], kv_empty[6];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];
   uint64_t p_full, pv_done;
@@ -105,19 +110,16 @@ struct Shared {
   int failed;          // set by a softmax warp whose wait gave up
 };
 
-// Workspace: header, per-CTA records, row prefixes, row log-sum-exps, partial
-// states, scores.
-struct Header {
-  int32_t total, ctas;
-};
+// Workspace: per-CTA records, row log-sum-exps, partial states, scores.
+// What the join of the row that a CTA's range starts inside of needs: u is -1
+// unless this is the second range of that row.
 struct Record {
-  int32_t u, begin, end, pad;   // the row that the CTA's range starts inside of (-1: none)
+  int32_t u, first, segs;       // the row, its first CTA, its ranges
+  int32_t slot;                 // partial state of the first CTA: its first or second
 };
 struct Work {
-  Header* hdr;
   Record* rec;         // [ctas]
-  int32_t* prefix;     // [U + 1] units before each row
-  float* row_lse2;     // [U][16] of rows that one CTA finished
+  float* row_lse2;     // [U][16]
   float2* part_ml;     // [ctas][2][16]
   float* part_o;       // [ctas][2][16][d]
   float* scores;       // [rows][G][slots], base-2 exponents; only when accumulating
@@ -135,10 +137,8 @@ size_t layout(Work* w, char* base, int64_t rows, int G, int64_t cap, int d, int 
     return p;
   };
   Work x;
-  x.hdr = reinterpret_cast<Header*>(take(sizeof(Header)));
   x.rec = reinterpret_cast<Record*>(take(size_t(ctas) * sizeof(Record)));
-  x.prefix = reinterpret_cast<int32_t*>(take(size_t(U + 1) * 4));
-  x.row_lse2 = reinterpret_cast<float*>(take(size_t(U) * kChunk * 4));
+  x.row_lse2 = reinterpret_cast<float*>(take(accumulate ? size_t(U) * kChunk * 4 : 0));
   x.part_ml = reinterpret_cast<float2*>(take(size_t(ctas) * 2 * kChunk * 8));
   x.part_o = reinterpret_cast<float*>(take(size_t(ctas) * 2 * kChunk * d * 4));
   x.scores = reinterpret_cast<float*>(take(accumulate ? size_t(rows) * G * cap * 4 : 0));
@@ -185,6 +185,28 @@ __device__ __forceinline__ void store_out(const Params& p, size_t at, float v) {
     static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(v);
 }
 
+// A wait's first polls leave the clock alone: reading it costs more than most
+// waits here last.  Short limits go by the clock from the start.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                        uint64_t limit_ns) {
+  if (limit_ns >= 1000000u) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_test_sleep(bar, parity, 2000)) return true;
+  }
+  return mbar_wait(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_on(bar, parity, abort, limit_ns);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+__device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_on(bar, parity, abort, limit_ns));
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
   static_assert(N % 16 == 0, "");
@@ -199,20 +221,24 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
 }
 
 template <int D, int GP, int PARTS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     attend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const Params p) {
   using C = Cfg<D, GP, PARTS>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   launch_dependents();
+  wait_dependency();
   if (smem_u32(smem_raw) & 1023u) {
-    if (threadIdx.x == 0) atomicOr(p.dev_status, SA_DEV_BAD_LAUNCH);
+    if (threadIdx.x == 0) {
+      atomicOr(p.dev_status, SA_DEV_BAD_LAUNCH);
+      p.w.rec[blockIdx.x] = Record{-1, 0, 0, 0};
+    }
     return;
   }
   uint8_t* sKV = smem_raw;
   uint8_t* sP = sKV + C::kStages * C::kStage;
   uint8_t* sQ = sP + C::kP;
-  Shared* sh = reinterpret_cast<Shared*>(sQ + 2 * C::kQ);
+  Shared* sh = reinterpret_cast<Shared*>(sQ + C::kQs * C::kQ);
   volatile int* abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t cta = blockIdx.x;
@@ -245,24 +271,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       max(1, min(int32_t(gridDim.x), (total + p.min_units - 1) / p.min_units));
   const int32_t a = cta < ctas ? range_begin(cta, total, ctas) : 0;
   const int32_t b = cta < ctas ? range_begin(cta + 1, total, ctas) : 0;
-  if ((a < b && a >= before && a < before + mine) || (cta == 0 && p.weights_out)) {
+  if (a < b && a >= before && a < before + mine) {
     int32_t at = before;
     for (int32_t u = ua; u < ub; ++u) {
       const int32_t k = units_of(p, sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status));
-      if (a < b && a >= at && a < at + k) {
+      if (a >= at && a < at + k) {
         sh->u0 = u;
         sh->p0 = at;
-        p.w.rec[cta] = Record{a > at ? u : -1, at, at + k, 0};
+        const int32_t first = owner(at, total, ctas);
+        if (a > at && first == cta - 1)
+          p.w.rec[cta] = Record{u, first, owner(at + k - 1, total, ctas) - first + 1,
+                                at == range_begin(first, total, ctas) ? 0 : 1};
       }
-      if (cta == 0 && p.weights_out) p.w.prefix[u] = at;
       at += k;
     }
   }
   if (tid == 0) {
-    if (cta == 0) {
-      *p.w.hdr = Header{total, ctas};
-      if (p.weights_out) p.w.prefix[p.U] = total;
-    }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->kv_full[s], 1);
       mbar_init(&sh->kv_empty[s], 1);
@@ -272,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->q_empty[s], 1);
       mbar_init(&sh->s_full[s], 1);
     }
-    mbar_init(&sh->p_full, 128);
+    mbar_init(&sh->p_full, 4);                // a warp each
     mbar_init(&sh->pv_done, 1);
     mbar_init(&sh->drain, 1);
     for (int s = 0; s < kInfo; ++s) {
@@ -378,15 +402,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t prow = (cur.t + (lane << p.bx_shift)) & ((1 << p.page_shift) - 1);
       const int slot = i % kInfo;
       if (i >= uint32_t(kInfo))
-        ok = warp_wait(&sh->info_empty[slot], ((i / kInfo) - 1) & 1, abort, p.wait_ns);
+        ok = wait_warp(&sh->info_empty[slot], ((i / kInfo) - 1) & 1, abort, p.wait_ns);
       if (!ok) break;
       if (lane == 0) {
         sh->info[slot] = cur;
         mbar_arrive(&sh->info_full[slot]);
       }
       if (cur.flags & kFirst) {
-        const int qs = qi & 1;
-        if (qi >= 2) ok = warp_wait(&sh->q_empty[qs], ((qi >> 1) - 1) & 1, abort, p.wait_ns);
+        const int qs = qi % C::kQs;
+        if (qi >= uint32_t(C::kQs))
+          ok = wait_warp(&sh->q_empty[qs], ((qi / C::kQs) - 1) & 1, abort, p.wait_ns);
         if (!ok) break;
         if (lane == 0) {
           const int32_t r = cur.u / p.HC;
@@ -403,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kv = 0; kv < 2; ++kv) {
         const int st = issued % C::kStages;
         if (issued >= uint32_t(C::kStages))
-          ok = warp_wait(&sh->kv_empty[st], ((issued / C::kStages) - 1) & 1, abort, p.wait_ns);
+          ok = wait_warp(&sh->kv_empty[st], ((issued / C::kStages) - 1) & 1, abort, p.wait_ns);
         if (!ok) break;
         if (lane == 0)
           mbar_arrive_expect_tx(&sh->kv_full[st], uint32_t(boxes * bx * 128 * C::kPanels));
@@ -424,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       const int slot = i % kInfo;
       if (i >= uint32_t(kInfo))
-        ok = warp_wait(&sh->info_empty[slot], ((i / kInfo) - 1) & 1, abort, p.wait_ns);
+        ok = wait_warp(&sh->info_empty[slot], ((i / kInfo) - 1) & 1, abort, p.wait_ns);
       if (ok && lane == 0) {
         sh->info[slot] = TileInfo{0, 0, 0, 0};
         mbar_arrive(&sh->info_full[slot]);
@@ -438,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copies still in flight land before the CTA's shared memory goes
       for (uint32_t x = issued > uint32_t(C::kStages) ? issued - C::kStages : 0; x < issued; ++x)
         mbar_wait(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, nullptr);
-      for (uint32_t x = qi > 2 ? qi - 2 : 0; x < qi; ++x)
-        mbar_wait(&sh->q_full[x & 1], (x >> 1) & 1, nullptr);
+      for (uint32_t x = qi > uint32_t(C::kQs) ? qi - C::kQs : 0; x < qi; ++x)
+        mbar_wait(&sh->q_full[x % C::kQs], (x / C::kQs) & 1, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------- issuer of both products
@@ -450,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits for tile j's description and returns its length and flags
     auto tile = [&](uint32_t j, int32_t& n, int32_t& flags) -> bool {
       const int slot = j % kInfo;
-      if (!warp_wait(&sh->info_full[slot], (j / kInfo) & 1, abort, p.wait_ns)) return false;
+      if (!wait_warp(&sh->info_full[slot], (j / kInfo) & 1, abort, p.wait_ns)) return false;
       n = sh->info[slot].n;
       flags = sh->info[slot].flags;
       __syncwarp();
@@ -461,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t x = 2 * j;
       const int st = x % C::kStages;
       if ((flags & kFirst) &&
-          !warp_wait(&sh->q_full[seg & 1], (seg >> 1) & 1, abort, p.wait_ns))
+          !wait_warp(&sh->q_full[seg % C::kQs], (seg / C::kQs) & 1, abort, p.wait_ns))
         return false;
-      if (!warp_wait(&sh->kv_full[st], (x / C::kStages) & 1, abort, p.wait_ns)) return false;
+      if (!wait_warp(&sh->kv_full[st], (x / C::kStages) & 1, abort, p.wait_ns)) return false;
       tc_fence_after();
       const uint64_t kd = smem_desc_sw128(smem_u32(sKV + st * C::kStage), 16, 1024);
-      const uint64_t qd = smem_desc_sw128(smem_u32(sQ + (seg & 1) * C::kQ), 16, 1024);
+      const uint64_t qd = smem_desc_sw128(smem_u32(sQ + (seg % C::kQs) * C::kQ), 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(&sh->s_full[j & 1]);
         mma_commit(&sh->kv_empty[st]);
-        if (flags & kLast) mma_commit(&sh->q_empty[seg & 1]);
+        if (flags & kLast) mma_commit(&sh->q_empty[seg % C::kQs]);
       }
       __syncwarp();
       if (flags & kLast) ++seg;
@@ -503,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t x = 2 * j + 1;
       const int st = x % C::kStages;
-      ok = warp_wait(&sh->p_full, j & 1, abort, p.wait_ns) &&
-           warp_wait(&sh->kv_full[st], (x / C::kStages) & 1, abort, p.wait_ns);
+      ok = wait_warp(&sh->p_full, j & 1, abort, p.wait_ns) &&
+           wait_warp(&sh->kv_full[st], (x / C::kStages) & 1, abort, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vd = smem_desc_sw128(smem_u32(sKV + st * C::kStage), C::kPanel, 1024);
@@ -546,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every wait of this tile comes before its one barrier, where the four
       // warps learn together whether one gave up.
       const int slot = j % kInfo;
-      bool fail = !wait_all(&sh->info_full[slot], (j / kInfo) & 1, abort, p.wait_ns);
+      bool fail = !wait_lanes(&sh->info_full[slot], (j / kInfo) & 1, abort, p.wait_ns);
       TileInfo it{0, 0, 0, 0};
       float s[16];
       bool need = false;
@@ -557,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
       }
       if (!fail && it.n > 0) {
-        fail = !wait_all(&sh->s_full[j & 1], (j >> 1) & 1, abort, p.wait_ns);
+        fail = !wait_lanes(&sh->s_full[j & 1], (j >> 1) & 1, abort, p.wait_ns);
         if (!fail) {
           tc_fence_after();
           tmem_load<16>(lanes + (j & 1) * C::kNS, s);
@@ -571,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (it.n < kTile) {
             // the last product step reads value rows up to the next 16th
             const uint32_t x = 2 * j + 1;
-            fail = !wait_all(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, abort, p.wait_ns);
+            fail = !wait_lanes(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, abort, p.wait_ns);
             if (!fail && row >= it.n && row < ((it.n + 15) & ~15)) {
               uint4* v = reinterpret_cast<uint4*>(sKV + (x % C::kStages) * C::kStage + row * 128);
 #pragma unroll
@@ -582,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!fail && j > 0) fail = !wait_all(&sh->pv_done, (j - 1) & 1, abort, p.wait_ns);
+      if (!fail && j > 0) fail = !wait_lanes(&sh->pv_done, (j - 1) & 1, abort, p.wait_ns);
       if (fail) *(volatile int*)&sh->failed = 1;
       const bool any = bar_any(1, 128, need || fail);
       if (any && *(volatile int*)&sh->failed) {
@@ -690,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(&sh->p_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full);
       prev = it;
     }
     if (!ok) {
@@ -707,112 +733,107 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Blocks [0, ctas * 16): the join of the row that the range of CTA c starts
-// inside of, for one head, if c is the second range of that row.  The rest:
-// weights of kJoinThreads tokens of one row.
+// Block (CTA c of the first launch, kJoinHeads heads): if c's range is the
+// second of a row, the join of the row's partial states.  Four warps a head
+// take every fourth state each, at the states' common maximum, and their sums
+// are added in warp order.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int32_t ctas_max,
-                                                            int32_t pieces) {
-  __shared__ float f[kMaxCtas];
-  __shared__ float acc[kJoinThreads];
-  __shared__ float lse2s[1024];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
+  constexpr int kVec = D / 32;                     // elements of a lane
+  constexpr int kWays = kJoinThreads / 32 / kJoinHeads;
+  __shared__ float acc[kJoinHeads][kWays][D], ls[kJoinHeads][kWays];
+  launch_dependents();
   wait_dependency();
-  const int32_t total = p.w.hdr->total, ctas = p.w.hdr->ctas;
-  // segment k of a row whose units are [begin, end): its CTA's partial state
-  auto part_of = [&](int32_t begin, int32_t first, int32_t k) -> size_t {
-    const int second = k == 0 && begin != range_begin(first, total, ctas);
-    return (size_t(first + k) * 2 + second) * kChunk;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Record rec = p.w.rec[blockIdx.x];
+  if (rec.u < 0) return;
+  const int32_t r = rec.u / p.HC, h0 = (rec.u % p.HC) * kChunk;
+  const int hl = warp / kWays, way = warp % kWays;
+  const int h = blockIdx.y * kJoinHeads + hl;      // head of the chunk
+  const bool live = h < min(kChunk, p.G - h0);
+  auto part_of = [&](int32_t k) -> size_t {
+    return (size_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * kChunk + h;
   };
-  const int32_t joins = ctas_max * kChunk;
-  if (int32_t(blockIdx.x) < joins) {
-    const int32_t c = blockIdx.x / kChunk, h = blockIdx.x % kChunk;
-    const Record rec = p.w.rec[c];
-    if (rec.u < 0) return;
-    const int32_t r = rec.u / p.HC, h0 = (rec.u % p.HC) * kChunk;
-    if (h >= p.G - h0) return;
-    const int32_t first = owner(rec.begin, total, ctas);
-    if (first != c - 1) return;
-    const int32_t segs = owner(rec.end - 1, total, ctas) - first + 1;
-    if (warp == 0) {
-      float M = -INFINITY;
-      for (int32_t k = lane; k < segs; k += 32)
-        M = fmaxf(M, p.w.part_ml[part_of(rec.begin, first, k) + h].x);
+  float M = -INFINITY;
+  if (live) {
+    for (int32_t k = lane; k < rec.segs; k += 32) M = fmaxf(M, p.w.part_ml[part_of(k)].x);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float ref = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      for (int32_t k = lane; k < segs; k += 32) {
-        const float2 ml = p.w.part_ml[part_of(rec.begin, first, k) + h];
-        const float x = ex2(ml.x - ref);
-        f[k] = x;
-        L += x * ml.y;
-      }
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, v[kVec];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane == 0) {
-        lse2s[0] = ref + log2f(L);
-        lse2s[1] = L;
-      }
-    }
-    __syncthreads();
-    constexpr int kGroups = kJoinThreads / D;
-    const int x = tid % D, g = tid / D;
-    float sum = 0.f;
+    for (int x = 0; x < kVec; ++x) v[x] = 0.f;
 #pragma unroll 4
-    for (int32_t k = g; k < segs; k += kGroups)
-      sum = fmaf(f[k], p.w.part_o[(part_of(rec.begin, first, k) + h) * D + x], sum);
-    acc[tid] = sum;
-    __syncthreads();
-    const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0 + h;
-    if (g == 0) {
-#pragma unroll
-      for (int y = 1; y < kGroups; ++y) sum += acc[y * D + x];
-      store_out(p, bh * D + x, sum / lse2s[1]);
-    }
-    if (tid == 0 && p.lse) p.lse[bh] = lse2s[0] * 0.6931471805599453f;
-    return;
-  }
-  // ---- weights
-  const int32_t id = blockIdx.x - joins;
-  const int32_t r = id / pieces, t0 = (id % pieces) * kJoinThreads;
-  const int32_t n = sa_paged::row_len(p.lens, r, p.cap, p.dev_status);
-  if (t0 >= n) return;
-  for (int32_t h = warp; h < p.G; h += kJoinThreads / 32) {
-    const int32_t u = r * p.HC + h / kChunk, x = h % kChunk;
-    const int32_t begin = p.w.prefix[u], end = p.w.prefix[u + 1];
-    const int32_t first = owner(begin, total, ctas);
-    const int32_t segs = owner(end - 1, total, ctas) - first + 1;
-    float v;
-    if (segs == 1) {
-      v = p.w.row_lse2[size_t(u) * kChunk + x];
-    } else {
-      float M = -INFINITY;
-      for (int32_t k = lane; k < segs; k += 32)
-        M = fmaxf(M, p.w.part_ml[part_of(begin, first, k) + x].x);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float ref = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      for (int32_t k = lane; k < segs; k += 32) {
-        const float2 ml = p.w.part_ml[part_of(begin, first, k) + x];
-        L += ex2(ml.x - ref) * ml.y;
+    for (int32_t k = way; k < rec.segs; k += kWays) {
+      const size_t at = part_of(k);
+      const float2 ml = p.w.part_ml[at];
+      const float f = ex2(ml.x - ref);
+      L = fmaf(f, ml.y, L);
+      if constexpr (kVec == 4) {
+        const float4 o4 = *reinterpret_cast<const float4*>(p.w.part_o + at * D + lane * 4);
+        v[0] = fmaf(f, o4.x, v[0]);
+        v[1] = fmaf(f, o4.y, v[1]);
+        v[2] = fmaf(f, o4.z, v[2]);
+        v[3] = fmaf(f, o4.w, v[3]);
+      } else {
+        const float2 o2 = *reinterpret_cast<const float2*>(p.w.part_o + at * D + lane * 2);
+        v[0] = fmaf(f, o2.x, v[0]);
+        v[1] = fmaf(f, o2.y, v[1]);
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      v = ref + log2f(L);
     }
-    if (lane == 0) lse2s[h] = v;
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) acc[hl][way][lane * kVec + x] = v[x];
+    if (lane == 0) ls[hl][way] = L;
+    M = ref;
   }
   __syncthreads();
-  const int32_t t = t0 + tid;
-  if (t >= n) return;
-  float sum = 0.f;
-  const float* s = p.w.scores + size_t(r) * p.G * p.cap + t;
+  if (!live) return;
+  float L = 0.f;
+#pragma unroll
+  for (int y = 0; y < kWays; ++y) L += ls[hl][y];
+  const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0 + h;
+  for (int x = way * 32 + lane; x < D; x += kWays * 32) {
+    float sum = 0.f;
+#pragma unroll
+    for (int y = 0; y < kWays; ++y) sum += acc[hl][y][x];
+    store_out(p, bh * D + x, sum / L);
+  }
+  if (way == 0 && lane == 0) {
+    const float lse2 = M + log2f(L);
+    if (p.lse) p.lse[bh] = lse2 * 0.6931471805599453f;
+    if (p.weights_out) p.w.row_lse2[size_t(rec.u) * kChunk + h] = lse2;
+  }
+}
+
+// Block (piece of a row's slots, row): every token's probabilities, summed
+// over the row's heads, added to its weight.
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Params p, int32_t pieces) {
+  launch_dependents();
+  wait_dependency();
+  const int32_t r = blockIdx.x / pieces;
+  const int32_t t0 = (blockIdx.x % pieces) * (kWeightThreads * kWeightSteps) + threadIdx.x;
+  const int32_t n = sa_paged::row_len(p.lens, r, p.cap, p.dev_status);
+  float sum[kWeightSteps];
+#pragma unroll
+  for (int i = 0; i < kWeightSteps; ++i) sum[i] = 0.f;
+  if (t0 >= n) return;
+  const float* s = p.w.scores + size_t(r) * p.G * p.cap;
+  const float* lse2 = p.w.row_lse2 + size_t(r) * p.HC * kChunk;
 #pragma unroll 4
-  for (int32_t h = 0; h < p.G; ++h) sum += ex2(s[size_t(h) * p.cap] - lse2s[h]);
-  const size_t at = size_t(r) * p.cap + t;
-  p.weights_out[at] = p.weights[at] + sum;
+  for (int32_t h = 0; h < p.G; ++h) {
+    const float l = lse2[h];                       // chunks of 16 heads lie end to end
+#pragma unroll
+    for (int i = 0; i < kWeightSteps; ++i) {
+      const int32_t t = t0 + i * kWeightThreads;
+      if (t < n) sum[i] += ex2(s[size_t(h) * p.cap + t] - l);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kWeightSteps; ++i) {
+    const int32_t t = t0 + i * kWeightThreads;
+    const size_t at = size_t(r) * p.cap + t;
+    if (t < n) p.weights_out[at] = p.weights[at] + sum[i];
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -862,9 +883,9 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   constexpr int kRing = C::kStages * C::kStage;
   // d = 64: the second half of the 128-row value operand lies one panel on;
   // its rows of the product are not used, but the last stage's must exist
-  constexpr int kUsed = kRing + C::kP + 2 * C::kQ + int(sizeof(Shared));
+  constexpr int kUsed = kRing + C::kP + C::kQs * C::kQ + int(sizeof(Shared));
   constexpr int kSmem = D == 64 && kUsed < kRing + C::kPanel ? kRing + C::kPanel : kUsed;
-  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kPerSm * (kSmem + 1024) <= 233472, "shared memory budget");
   const sa_paged_cache& c = a.c;
   const int64_t rows = int64_t(c.batch) * c.num_kv_heads;
   Params p{};
@@ -897,27 +918,36 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.weights_out = a.weights_out;
   p.dev_status = a.dev_status;
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  const int ctas = sms * kPerSm;
   layout(&p.w, static_cast<char*>(a.ws), rows, p.G, p.cap, D, ctas, a.weights_out != nullptr);
   auto kern = attend_kernel<D, GP, PARTS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, kSmem, st>>>(tq, tk, tv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int32_t pieces = (p.cap + kJoinThreads - 1) / kJoinThreads;
-  const int64_t blocks = int64_t(ctas) * kChunk + (a.weights_out ? rows * pieces : 0);
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(blocks));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
+  // each launch may start while the one before it in the stream ends, and
+  // waits for it before it touches memory
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, int32_t(ctas), pieces);
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  e = cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(unsigned(ctas), unsigned((p.q_rows + kJoinHeads - 1) / kJoinHeads));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+  if (e != cudaSuccess || !a.weights_out) return e;
+  constexpr int kPiece = kWeightThreads * kWeightSteps;
+  const int32_t pieces = (p.cap + kPiece - 1) / kPiece;
+  if (rows * pieces > INT32_MAX) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(unsigned(rows * pieces));
+  cfg.blockDim = dim3(kWeightThreads);
+  return cudaLaunchKernelEx(&cfg, weights_kernel, p, pieces);
 }
 
 template <int D>
@@ -939,8 +969,7 @@ namespace sa_paged {
 
 size_t attend_workspace(const sa_paged_cache& c, int32_t Hq, bool accumulate, int sms) {
   return layout(nullptr, nullptr, int64_t(c.batch) * c.num_kv_heads, Hq / c.num_kv_heads,
-                int64_t(c.page) * c.max_pages, c.head_dim, sms < kMaxCtas ? sms : kMaxCtas,
-                accumulate);
+                int64_t(c.page) * c.max_pages, c.head_dim, sms * kPerSm, accumulate);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_failed) {

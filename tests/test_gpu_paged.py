@@ -481,3 +481,26 @@ def test_python_class_refusals(env):
         sa.PagedCache(dev["k"].transpose(1, 2), dev["v"].transpose(1, 2), dev["table"], dev["lens"])
     with pytest.raises(ValueError):
         sa.PagedCache(dev["k"], dev["v"], dev["table"], dev["lens"], weights=dev["weights"][..., :-1].contiguous())
+
+
+def test_attend_wait_limit_ends_the_launch(env):
+    # every copy takes longer than 1 ns: the waits give up, the launch ends and
+    # the next one, with the default limit, is right again
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(45, [3000, 200], 2, 128, 32)
+    dev, cache = P.to_gpu(c, sa)
+    q = _q(torch, 9, 2, 8, 128)
+    gq = q.cuda()
+    sa.sparse_attn_set_wait_limit(1)
+    try:
+        cache.attend(gq, accumulate=False)
+        torch.cuda.synchronize()
+    finally:
+        sa.sparse_attn_set_wait_limit(0)
+    assert int(cache.dev_status.item()) & sa.SA_DEV_TIMEOUT
+    cache.dev_status.zero_()
+    out, lse = torch.empty(2, 8, 128, device="cuda"), torch.empty(2, 8, device="cuda")
+    cache.attend(gq, out=out, lse=lse, accumulate=False)
+    assert int(cache.dev_status.item()) == 0
+    P.check_attend(c, q, out, lse)
