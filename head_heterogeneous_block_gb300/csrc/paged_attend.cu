@@ -61,12 +61,9 @@ using sa_paged::AttendArgs;
 
 constexpr int kTile = 128;             // tokens per tile
 constexpr int kChunk = 16;             // query heads of a row handled together
-constexpr int kThreads = 192;
 constexpr int kInfo = 8;               // tile descriptions in flight
-constexpr int kPerSm = 2;              // CTAs per processor
 constexpr float kMove = 8.f;           // how far a score may pass its reference
 constexpr int kJoinThreads = 512;
-constexpr int kJoinHeads = 4;          // heads of a join block, four warps each
 constexpr int kWeightThreads = 256;
 constexpr int kWeightSteps = 4;        // tokens of a thread
 
@@ -75,16 +72,27 @@ struct Cfg {
   static constexpr int kPanels = D / 64;              // 128-byte column panels
   static constexpr int kPanel = kTile * 128;          // bytes of one K/V panel
   static constexpr int kStage = kPanels * kPanel;
-  static constexpr int kStages = D == 128 ? 3 : 6;    // tile j: K in stage 2j % kStages, V next
+  // softmax: kGroups groups of four warps, kHeads heads of a token a thread
+  static constexpr int kHeads = GP < 16 ? 4 : 8;
+  static constexpr int kGroups = GP / kHeads;
+  static constexpr int kThreads = 64 + 128 * kGroups;
+  // CTAs on a processor, the stages and Q tiles that then fit.  Tile j: K in
+  // stage 2j % kStages, V in the next.
+  static constexpr int kPerSm = D == 64 && GP == 4 ? 4 : D == 64 && GP == 8 ? 3 : 2;
+  static constexpr int kStages = D == 128 || GP == 4 ? 3 : GP == 8 ? (PARTS == 2 ? 4 : 3) : 6;
+  static constexpr int kQs = (D == 128 && GP * PARTS > 32) || (D == 64 && GP == 4) ? 1 : 2;
   static constexpr int kNS = 16;                      // columns of S
   static constexpr int kNP = (GP * PARTS + 15) / 16 * 16;   // columns of O, rows of P
   static constexpr int kQ = kPanels * kChunk * 128;   // bytes of one Q tile
-  // two Q tiles, but where only one leaves room for two CTAs on a processor
-  static constexpr int kQs = D == 128 && GP * PARTS > 32 ? 1 : 2;
   static constexpr int kP = 2 * kNP * 128;            // bytes of P (two panels of 64 tokens)
   static constexpr uint32_t kO = 2 * kNS;             // TMEM column of O
   static constexpr uint32_t kTmemCols = 128;
-  static_assert(2 * kNS + kNP <= int(kTmemCols), "tensor memory budget");
+  // V^T has 128 rows to the tensor core; at d = 64 the second 64 read from
+  // 2 KB further on (their rows of O are not used): within shared memory, since
+  // P and Q follow the ring
+  static constexpr uint32_t kVNext = D == 128 ? kPanel : 2048;
+  static_assert(2 * kNS + kNP <= int(kTmemCols) && kPerSm * kTmemCols <= 512, "tensor memory");
+  static_assert(GP % kHeads == 0 && kP + kQs * kQ >= 2048, "");
 };
 
 struct TileInfo {
@@ -102,17 +110,18 @@ struct Shared {
   uint64_t info_full[kInfo], info_empty[kInfo];
   uint64_t drain;
   TileInfo info[kInfo];
-  float red[4][kChunk];
-  int32_t scan[kThreads / 32];
-  int32_t u0, p0;      // first row of the range and the units before it
+  float red[2][4][8];  // [group][quarter][head]
+  int32_t scan[10];
+  int32_t u0, p0, len0;  // first row of the range, the units before it, its length
   uint32_t tmem_base;
   int abort;
-  int failed;          // set by a softmax warp whose wait gave up
+  int failed[2];       // set by a group's warp whose wait gave up
 };
 
-// Workspace: per-CTA records, row log-sum-exps, partial states, scores.
-// What the join of the row that a CTA's range starts inside of needs: u is -1
-// unless this is the second range of that row.
+// Workspace: records, row log-sum-exps, partial states, scores.  A record is
+// what the join of a row needs: u is -1 where nothing is to be joined.  There
+// is one a row when there are no more rows than CTAs, else one a CTA, for the
+// row of whose ranges its own is the second.
 struct Record {
   int32_t u, first, segs;       // the row, its first CTA, its ranges
   int32_t slot;                 // partial state of the first CTA: its first or second
@@ -155,6 +164,7 @@ struct Params {
   int32_t Hkv, Hq, G, HC, U;   // HC: head chunks of a row; U = rows * HC
   int32_t q_rows;              // heads of a Q box
   int32_t min_units;           // least units of a CTA
+  int32_t by_row;              // records: one a row
   float scale_log2;
   void* o;
   int32_t out_f32;
@@ -170,13 +180,16 @@ __device__ __forceinline__ int32_t units_of(const Params& p, int32_t len) {
   return (len + (1 << p.bx_shift) - 1) >> p.bx_shift;
 }
 
-// First unit of CTA c's range, and the CTA whose range holds unit x.
-__device__ __forceinline__ int32_t range_begin(int32_t c, int32_t total, int32_t ctas) {
-  return int32_t(int64_t(c) * total / ctas);
-}
-__device__ __forceinline__ int32_t owner(int32_t x, int32_t total, int32_t ctas) {
-  return int32_t(((int64_t(x) + 1) * ctas - 1) / total);
-}
+// Ranges: the first `rem` CTAs take base + 1 units, the others base.
+struct Ranges {
+  int32_t ctas, base, rem;
+  __device__ __forceinline__ int32_t begin(int32_t c) const { return c * base + min(c, rem); }
+  // the CTA whose range holds unit x
+  __device__ __forceinline__ int32_t owner(int32_t x) const {
+    const int32_t big = rem * (base + 1);
+    return x < big ? x / (base + 1) : rem + (x - big) / base;
+  }
+};
 
 __device__ __forceinline__ void store_out(const Params& p, size_t at, float v) {
   if (p.out_f32)
@@ -187,9 +200,10 @@ __device__ __forceinline__ void store_out(const Params& p, size_t at, float v) {
 
 // A wait's first polls leave the clock alone: reading it costs more than most
 // waits here last.  Short limits go by the clock from the start.
+constexpr uint64_t kClockless = 1000000;
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort,
                                         uint64_t limit_ns) {
-  if (limit_ns >= 1000000u) {
+  if (limit_ns >= kClockless) {
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
       if (mbar_test_sleep(bar, parity, 2000)) return true;
@@ -200,41 +214,41 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
                                           uint64_t limit_ns) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = wait_on(bar, parity, abort, limit_ns);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  __syncwarp();
+  return ok;
 }
+// Every lane waits on a barrier of its choice; true when all came through.
 __device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, volatile int* abort,
                                            uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, wait_on(bar, parity, abort, limit_ns));
+  const bool ok = __all_sync(0xffffffffu, wait_on(bar, parity, abort, limit_ns));
+  __syncwarp();
+  return ok;
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
-  static_assert(N % 16 == 0, "");
-#pragma unroll
-  for (int x = 0; x < N; x += 16) {
-    uint32_t r[16];
-    tmem_ld16(addr + x, r);
-    tmem_ld_wait(r);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[x + i] = __uint_as_float(r[i]);
-  }
+// The barrier of one softmax group.
+template <int kGroups>
+__device__ __forceinline__ bool group_any(int grp, bool flag) {
+  if (kGroups > 1 && grp == 1) return bar_any<2, 128>(flag);
+  return bar_any<1, 128>(flag);
+}
+template <int kGroups>
+__device__ __forceinline__ void group_sync(int grp) {
+  if (kGroups > 1 && grp == 1)
+    bar_sync<2, 128>();
+  else
+    bar_sync<1, 128>();
 }
 
 template <int D, int GP, int PARTS>
-__global__ void __launch_bounds__(kThreads, kPerSm)
+__global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>::kPerSm)
     attend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                  const __grid_constant__ CUtensorMap tv, const Params p) {
+                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ Params p) {
   using C = Cfg<D, GP, PARTS>;
+  constexpr int kThreads = C::kThreads;
+  constexpr int HP = C::kHeads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   launch_dependents();
-  wait_dependency();
-  if (smem_u32(smem_raw) & 1023u) {
-    if (threadIdx.x == 0) {
-      atomicOr(p.dev_status, SA_DEV_BAD_LAUNCH);
-      p.w.rec[blockIdx.x] = Record{-1, 0, 0, 0};
-    }
-    return;
-  }
   uint8_t* sKV = smem_raw;
   uint8_t* sP = sKV + C::kStages * C::kStage;
   uint8_t* sQ = sP + C::kP;
@@ -242,51 +256,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   volatile int* abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t cta = blockIdx.x;
-
-  // ---- this CTA's range: a scan of every row's units
-  const int32_t per = (p.U + kThreads - 1) / kThreads;
-  const int32_t ua = min(p.U, tid * per), ub = min(p.U, ua + per);
-  int32_t mine = 0;
-  for (int32_t u = ua; u < ub; ++u)
-    mine += units_of(p, sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status));
-  int32_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) sh->scan[warp] = incl;
-  if (tid == 0) {
-    sh->u0 = sh->p0 = 0;
-    p.w.rec[cta] = Record{-1, 0, 0, 0};
-  }
-  __syncthreads();
-  int32_t before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sh->scan[w];
-    total += sh->scan[w];
-  }
-  const int32_t ctas =
-      max(1, min(int32_t(gridDim.x), (total + p.min_units - 1) / p.min_units));
-  const int32_t a = cta < ctas ? range_begin(cta, total, ctas) : 0;
-  const int32_t b = cta < ctas ? range_begin(cta + 1, total, ctas) : 0;
-  if (a < b && a >= before && a < before + mine) {
-    int32_t at = before;
-    for (int32_t u = ua; u < ub; ++u) {
-      const int32_t k = units_of(p, sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status));
-      if (a >= at && a < at + k) {
-        sh->u0 = u;
-        sh->p0 = at;
-        const int32_t first = owner(at, total, ctas);
-        if (a > at && first == cta - 1)
-          p.w.rec[cta] = Record{u, first, owner(at + k - 1, total, ctas) - first + 1,
-                                at == range_begin(first, total, ctas) ? 0 : 1};
-      }
-      at += k;
+  if (smem_u32(smem_raw) & 1023u) {
+    wait_dependency();
+    if (tid == 0) {
+      atomicOr(p.dev_status, SA_DEV_BAD_LAUNCH);
+      p.w.rec[cta] = Record{-1, 0, 0, 0};
     }
+    return;
   }
+
+  // ---- what needs none of the inputs, while the launch before this one ends
   if (tid == 0) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->kv_full[s], 1);
       mbar_init(&sh->kv_empty[s], 1);
@@ -295,58 +278,121 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       mbar_init(&sh->q_full[s], 1);
       mbar_init(&sh->q_empty[s], 1);
       mbar_init(&sh->s_full[s], 1);
+      sh->failed[s] = 0;
     }
-    mbar_init(&sh->p_full, 4);                // a warp each
+    mbar_init(&sh->p_full, 4 * C::kGroups);    // a softmax warp each
     mbar_init(&sh->pv_done, 1);
     mbar_init(&sh->drain, 1);
     for (int s = 0; s < kInfo; ++s) {
       mbar_init(&sh->info_full[s], 1);
-      mbar_init(&sh->info_empty[s], 1 + 4);   // the issuer and the softmax warps
+      mbar_init(&sh->info_empty[s], 1 + 4 * C::kGroups);   // the issuer and the softmax warps
     }
     sh->abort = 0;
-    sh->failed = 0;
+    sh->u0 = sh->p0 = sh->len0 = 0;
     fence_mbar_init();
   }
-  // rows without a token
-  for (int32_t u = cta; u < p.U; u += gridDim.x) {
-    if (sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status) > 0) continue;
-    const int32_t r = u / p.HC, h0 = (u % p.HC) * kChunk;
-    const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
-    const int gc = min(kChunk, p.G - h0);
-    for (int x = tid; x < gc * D; x += kThreads) store_out(p, bh * D + x, 0.f);
-    if (p.lse && tid < gc) p.lse[bh + tid] = -INFINITY;
-  }
-  if (a >= b) return;
   if (warp == 1) {
     tmem_alloc(&sh->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
+  wait_dependency();
+
+  // ---- this CTA's range: a scan of every row's units
+  const int32_t per = (p.U + kThreads - 1) / kThreads;
+  const int32_t ua = min(p.U, tid * per), ub = min(p.U, ua + per);
+  int32_t mine = 0, len_a = 0;
+  for (int32_t u = ua; u < ub; ++u) {
+    const int32_t n = sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status);
+    if (u == ua) len_a = n;
+    mine += units_of(p, n);
+  }
+  int32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh->scan[warp] = incl;
+  if (tid == 0 && !p.by_row) p.w.rec[cta] = Record{-1, 0, 0, 0};
+  tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  int32_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh->scan[w];
+    total += sh->scan[w];
+  }
+  Ranges rg;
+  rg.ctas = max(1, min(int32_t(gridDim.x), (total + p.min_units - 1) / p.min_units));
+  rg.base = total / rg.ctas;
+  rg.rem = total - rg.base * rg.ctas;
+  const int32_t a = rg.begin(min(cta, rg.ctas)), b = rg.begin(min(cta + 1, rg.ctas));
   const uint32_t tmem = sh->tmem_base;
+  // rows without a token, taken in turn by the CTAs
+  auto empty_rows = [&](int first_thread, int threads) {
+    for (int32_t u = cta; u < p.U; u += gridDim.x) {
+      if (sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status) > 0) continue;
+      const int32_t r = u / p.HC, h0 = (u % p.HC) * kChunk;
+      const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
+      const int gc = min(kChunk, p.G - h0), x0 = tid - first_thread;
+      for (int x = x0; x < gc * D; x += threads) store_out(p, bh * D + x, 0.f);
+      if (p.lse && x0 < gc) p.lse[bh + x0] = -INFINITY;
+      if (p.by_row && x0 == 0) p.w.rec[u] = Record{-1, 0, 0, 0};
+    }
+  };
+  if (a >= b) {
+    empty_rows(0, kThreads);
+    if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+    return;
+  }
+  if (a >= before && a < before + mine) {
+    int32_t at = before;
+    for (int32_t u = ua; u < ub; ++u) {
+      const int32_t n = u == ua ? len_a
+                                : sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status);
+      const int32_t k = units_of(p, n);
+      if (a >= at && a < at + k) {
+        sh->u0 = u;
+        sh->p0 = at;
+        sh->len0 = n;
+        if (!p.by_row && a > at) {
+          const int32_t first = rg.owner(at);
+          if (first == cta - 1)
+            p.w.rec[cta] = Record{u, first, rg.owner(at + k - 1) - first + 1,
+                                  at == rg.begin(first) ? 0 : 1};
+        }
+      }
+      at += k;
+    }
+  }
+  __syncthreads();
   const int bx = 1 << p.bx_shift;
 
   if (warp == 0) {
     // ------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-    }
     const uint64_t pol = l2_policy_evict_first();
     const uint64_t pol_q = l2_policy_evict_last();
     int32_t u = sh->u0, pu = sh->p0;           // current row and the units before it
+    int32_t len = sh->len0;
     int32_t ubase = u, ulen = 0;               // lane l holds the length of row ubase + l
     auto load_lens = [&]() {
       ulen = ubase + lane < p.U
                  ? sa_paged::row_len(p.lens, (ubase + lane) / p.HC, p.cap, p.dev_status) : 0;
     };
-    load_lens();
-    int32_t len = __shfl_sync(0xffffffffu, ulen, 0);
-    int32_t t = (a - pu) << p.bx_shift;        // next token of the segment, and its end
-    int32_t t1 = min(len, int32_t(min(int64_t(b - pu), int64_t(1) << 30 >> p.bx_shift) << p.bx_shift));
+    auto end_of = [&]() -> int32_t {           // of the row's part in this range
+      return min(len, int32_t(min(int64_t(b - pu) << p.bx_shift, int64_t(1) << 30)));
+    };
+    int32_t seg = 0;                           // row parts before this one
+    // the record of a row that begins in this range
+    auto record = [&]() {
+      if (p.by_row && lane == 0) {
+        const int32_t segs = rg.owner(pu + units_of(p, len) - 1) - cta + 1;
+        p.w.rec[u] = Record{segs > 1 ? u : -1, cta, segs, seg > 0 ? 1 : 0};
+      }
+    };
+    int32_t t = (a - pu) << p.bx_shift, t1 = end_of();
     bool first = true, begins = t == 0;
-    int32_t seg = 0;
     bool more = true;
     // the next tile of the range; n == 0 when it is used up
     auto next = [&]() -> TileInfo {
@@ -363,11 +409,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         }
         len = __shfl_sync(0xffffffffu, ulen, u - ubase);
         t = 0;
-        t1 = min(len, int32_t(min(int64_t(b - pu), int64_t(1) << 30 >> p.bx_shift) << p.bx_shift));
+        t1 = end_of();
         if (len > 0) {
-          first = true;
-          begins = true;
+          first = begins = true;
           ++seg;
+          record();
         }
       }
       if (!more) return TileInfo{0, 0, 0, 0};
@@ -391,14 +437,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     bool ok = true;
     TileInfo cur = next();
     int32_t pg = lookup(cur);
+    load_lens();
+    if (begins) record();
     while (cur.n > 0) {
       const TileInfo nxt = next();
       const int32_t npg = nxt.n > 0 ? lookup(nxt) : 0;
       const int boxes = (cur.n + bx - 1) >> p.bx_shift;
-      if (lane < boxes && (pg < 0 || pg >= p.num_pages)) {
-        atomicOr(p.dev_status, SA_DEV_BAD_INDEX);
-        pg = 0;
-      }
       const int32_t prow = (cur.t + (lane << p.bx_shift)) & ((1 << p.page_shift) - 1);
       const int slot = i % kInfo;
       if (i >= uint32_t(kInfo))
@@ -423,6 +467,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                         r / p.Hkv, pol_q);
         }
         ++qi;
+      }
+      if (lane < boxes && (pg < 0 || pg >= p.num_pages)) {
+        atomicOr(p.dev_status, SA_DEV_BAD_INDEX);
+        pg = 0;
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -482,13 +530,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
       return true;
     };
-    auto issue_s = [&](uint32_t j, int32_t flags) -> bool {
-      const uint32_t x = 2 * j;
-      const int st = x % C::kStages;
-      if ((flags & kFirst) &&
-          !wait_warp(&sh->q_full[seg % C::kQs], (seg / C::kQs) & 1, abort, p.wait_ns))
-        return false;
-      if (!wait_warp(&sh->kv_full[st], (x / C::kStages) & 1, abort, p.wait_ns)) return false;
+    auto issue_s = [&](uint32_t j, int32_t flags) {
+      const int st = (2 * j) % C::kStages;
       tc_fence_after();
       const uint64_t kd = smem_desc_sw128(smem_u32(sKV + st * C::kStage), 16, 1024);
       const uint64_t qd = smem_desc_sw128(smem_u32(sQ + (seg % C::kQs) * C::kQ), 16, 1024);
@@ -506,49 +549,80 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       }
       __syncwarp();
       if (flags & kLast) ++seg;
-      return true;
     };
-    int32_t n = 0, flags = 0;
-    ok = tile(0, n, flags) && (n == 0 || issue_s(0, flags));
-    for (uint32_t j = 0; ok && n > 0; ++j) {
-      int32_t nn = 0, nflags = 0;
-      ok = tile(j + 1, nn, nflags);
-      if (!ok) break;
-      // the next tile's scores go first when its keys are there
-      bool early = false;
-      if (nn > 0) {
-        const uint32_t x = 2 * (j + 1);
-        const uint32_t ready =
-            mbar_test(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1) ? 1u : 0u;
-        early = __shfl_sync(0xffffffffu, ready, 0) != 0;
-        if (early) {
-          ok = issue_s(j + 1, nflags);
-          if (!ok) break;
-        }
-      }
-      const uint32_t x = 2 * j + 1;
-      const int st = x % C::kStages;
-      ok = wait_warp(&sh->p_full, j & 1, abort, p.wait_ns) &&
-           wait_warp(&sh->kv_full[st], (x / C::kStages) & 1, abort, p.wait_ns);
-      if (!ok) break;
+    auto issue_pv = [&](uint32_t j, int32_t n) {
+      const int st = (2 * j + 1) % C::kStages;
       tc_fence_after();
-      const uint64_t vd = smem_desc_sw128(smem_u32(sKV + st * C::kStage), C::kPanel, 1024);
+      const uint64_t vd = smem_desc_sw128(smem_u32(sKV + st * C::kStage), C::kVNext, 1024);
       const uint64_t pd = smem_desc_sw128(smem_u32(sP), 16, 1024);
-      const int steps = (n + 15) >> 4;
       if (elect_one()) {
-        for (int kk = 0; kk < steps; ++kk) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) {
           const uint32_t po = (kk / 4) * C::kNP * 128 + (kk % 4) * 32;
-          mma_ss(tmem + C::kO, vd + uint64_t((kk * 16 * 128) >> 4), pd + uint64_t(po >> 4), idesc_o,
-                 kk > 0 ? 1u : 0u);
+          if (kk * 16 < n)
+            mma_ss(tmem + C::kO, vd + uint64_t((kk * 16 * 128) >> 4), pd + uint64_t(po >> 4),
+                   idesc_o, kk > 0 ? 1u : 0u);
         }
         mma_commit(&sh->pv_done);
         mma_commit(&sh->kv_empty[st]);
       }
       __syncwarp();
-      if (nn > 0 && !early) ok = issue_s(j + 1, nflags);
+    };
+    // Tile j's output product and tile j + 1's scores, each as soon as what it
+    // reads is there: lane 0 polls P, lane 1 V, lane 2 the next K, lane 3 its Q.
+    // Before j = 0 only the scores of tile 0.
+    int32_t n = 0, flags = 0;
+    for (uint32_t j1 = 0;; ++j1) {             // j1 = j + 1
+      int32_t nn = 0, nflags = 0;
+      ok = tile(j1, nn, nflags);
+      if (!ok) break;
+      bool pv_left = j1 > 0, s_left = nn > 0;
+      const uint32_t j = j1 - 1;
+      uint64_t* bar = &sh->p_full;
+      uint32_t par = j & 1;
+      bool used = pv_left;
+      if (lane == 1) {
+        bar = &sh->kv_full[(2 * j + 1) % C::kStages];
+        par = ((2 * j + 1) / C::kStages) & 1;
+      } else if (lane == 2) {
+        bar = &sh->kv_full[(2 * j1) % C::kStages];
+        par = ((2 * j1) / C::kStages) & 1;
+        used = s_left;
+      } else if (lane == 3) {
+        bar = &sh->q_full[seg % C::kQs];
+        par = (seg / C::kQs) & 1;
+        used = s_left && (nflags & kFirst);
+      } else if (lane > 3) {
+        used = false;
+      }
+      uint64_t t0 = 0;
+      uint32_t polls = 0;
+      while (pv_left || s_left) {
+        const uint32_t have = __ballot_sync(0xffffffffu, !used || mbar_test(bar, par));
+        __syncwarp();
+        if (pv_left && (have & 3u) == 3u) {
+          issue_pv(j, n);
+          pv_left = false;
+          if (lane < 2) used = false;
+        } else if (s_left && (have & 12u) == 12u) {
+          issue_s(j1, nflags);
+          s_left = false;
+          if (lane == 2 || lane == 3) used = false;
+        } else if (p.wait_ns < kClockless || (++polls & 1023u) == 0) {
+          const uint64_t now = global_ns();
+          if (t0 == 0) t0 = now;
+          const bool out = *abort || now - t0 > p.wait_ns;
+          if (__any_sync(0xffffffffu, out)) {
+            ok = false;
+            break;
+          }
+        }
+      }
+      if (!ok || nn == 0) break;
       n = nn;
       flags = nflags;
     }
+    (void)flags;
     if (lane == 0) {
       if (!ok) {
         atomicOr(p.dev_status, SA_DEV_TIMEOUT);
@@ -560,95 +634,108 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     }
   } else {
     // ------------------------------------------------- softmax and output
+    const int grp = (warp - 2) >> 2;           // heads [grp * HP, (grp + 1) * HP) of the chunk
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;       // token of the tile, dimension of O
-    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + grp * HP;
     const float c = p.scale_log2;
-    float m[GP], l[GP], o[GP];
-    TileInfo prev{0, 0, 0, 0};
+    float m[HP], l[HP], o[HP];
+    TileInfo prev{0, 0, 0, 0}, it{0, 0, 0, 0};
     bool ok = true;
-    for (uint32_t j = 0;; ++j) {
-      // Every wait of this tile comes before its one barrier, where the four
-      // warps learn together whether one gave up.
+    empty_rows(64, kThreads - 64);
+    // the description of tile j
+    auto describe = [&](uint32_t j) -> bool {
       const int slot = j % kInfo;
-      bool fail = !wait_lanes(&sh->info_full[slot], (j / kInfo) & 1, abort, p.wait_ns);
-      TileInfo it{0, 0, 0, 0};
-      float s[16];
+      if (!wait_lanes(&sh->info_full[slot], (j / kInfo) & 1, abort, p.wait_ns)) return false;
+      it = sh->info[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+      return true;
+    };
+    bool fail = !describe(0);
+    for (uint32_t j = 0;; ++j) {
+      // Every wait of a tile comes before its one barrier, where the group's
+      // four warps learn together whether one gave up.
+      float s[HP];
       bool need = false;
-      int gc = 0;
-      if (!fail) {
-        it = sh->info[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
-      }
-      if (!fail && it.n > 0) {
-        fail = !wait_lanes(&sh->s_full[j & 1], (j >> 1) & 1, abort, p.wait_ns);
-        if (!fail) {
-          tc_fence_after();
-          tmem_load<16>(lanes + (j & 1) * C::kNS, s);
-          gc = min(kChunk, p.G - (it.u % p.HC) * kChunk);
-          need = (it.flags & kFirst) != 0;
+      const int gc = min(kChunk, p.G - (it.u % p.HC) * kChunk) - grp * HP;   // live heads
+      const bool live = !fail && it.n > 0;
+      if (!fail && (live || j > 0)) {
+        // lanes split over the scores, the last output product, and (for a
+        // tile whose value rows have to be cleared) the values
+        const uint32_t x = 2 * j + 1;
+        uint64_t* bar = &sh->s_full[j & 1];
+        uint32_t par = (j >> 1) & 1;
+        if (j > 0 && ((lane & 3) == 1 || !live)) {
+          bar = &sh->pv_done;
+          par = (j - 1) & 1;
+        } else if ((lane & 3) == 2 && it.n < kTile) {
+          bar = &sh->kv_full[x % C::kStages];
+          par = (x / C::kStages) & 1;
+        }
+        fail = !wait_lanes(bar, par, abort, p.wait_ns);
+        tc_fence_after();
+        if (live && !fail) {
+          tmem_load(lanes + (j & 1) * C::kNS, s);
 #pragma unroll
-          for (int h = 0; h < GP; ++h) {
+          for (int h = 0; h < HP; ++h) {
             s[h] = (row < it.n && h < gc) ? s[h] * c : -INFINITY;
             if (!(it.flags & kFirst)) need |= s[h] > m[h] + kMove;
           }
-          if (it.n < kTile) {
-            // the last product step reads value rows up to the next 16th
-            const uint32_t x = 2 * j + 1;
-            fail = !wait_lanes(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, abort, p.wait_ns);
-            if (!fail && row >= it.n && row < ((it.n + 15) & ~15)) {
-              uint4* v = reinterpret_cast<uint4*>(sKV + (x % C::kStages) * C::kStage + row * 128);
+          if (it.flags & kFirst) need = true;
+          // the last product step reads value rows up to the next 16th
+          if (grp == 0 && row >= it.n && row < ((it.n + 15) & ~15)) {
+            uint4* v = reinterpret_cast<uint4*>(sKV + (x % C::kStages) * C::kStage + row * 128);
 #pragma unroll
-              for (int s2 = 0; s2 < C::kPanels; ++s2)
+            for (int s2 = 0; s2 < C::kPanels; ++s2)
 #pragma unroll
-                for (int y = 0; y < 8; ++y) v[s2 * (C::kPanel / 16) + y] = make_uint4(0, 0, 0, 0);
-            }
+              for (int y = 0; y < 8; ++y) v[s2 * (C::kPanel / 16) + y] = make_uint4(0, 0, 0, 0);
           }
         }
       }
-      if (!fail && j > 0) fail = !wait_lanes(&sh->pv_done, (j - 1) & 1, abort, p.wait_ns);
-      if (fail) *(volatile int*)&sh->failed = 1;
-      const bool any = bar_any(1, 128, need || fail);
-      if (any && *(volatile int*)&sh->failed) {
+      if (fail) *(volatile int*)&sh->failed[grp] = 1;
+      const bool any = group_any<C::kGroups>(grp, need || fail);
+      if (any && *(volatile int*)&sh->failed[grp]) {
         ok = false;
         break;
       }
       if (j > 0) {
         // the previous tile's product joins the segment's output
-        tc_fence_after();
-        float x[C::kNP];
-        tmem_load<C::kNP>(lanes + C::kO, x);
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          float add = x[h];
+        for (int q = 0; q < PARTS; ++q) {
+          float x[HP];
+          tmem_load(lanes + C::kO + q * GP, x);
 #pragma unroll
-          for (int q = 1; q < PARTS; ++q) add += x[q * GP + h];
-          o[h] += add;
+          for (int h = 0; h < HP; ++h) o[h] += x[h];
         }
         if (prev.flags & kLast) {
           // ---- the end of a segment
 #pragma unroll
-          for (int h = 0; h < GP; ++h) {
+          for (int h = 0; h < HP; ++h) {
 #pragma unroll
             for (int w = 16; w; w >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
-            if (lane == 0) sh->red[quarter][h] = l[h];
           }
-          bar_sync(1, 128);
-          const int32_t r = prev.u / p.HC, h0 = (prev.u % p.HC) * kChunk;
-          const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
-          const int pc = min(kChunk, p.G - h0);
-          const size_t part = (size_t(cta) * 2 + ((prev.flags & kSecond) ? 1 : 0)) * kChunk;
+          if (lane == 0) {
 #pragma unroll
-          for (int h = 0; h < GP; ++h) {
-            if (h < pc) {
-              const float L = (sh->red[0][h] + sh->red[1][h]) + (sh->red[2][h] + sh->red[3][h]);
+            for (int h = 0; h < HP; ++h) sh->red[grp][quarter][h] = l[h];
+          }
+          group_sync<C::kGroups>(grp);
+          const int32_t r = prev.u / p.HC, h0 = (prev.u % p.HC) * kChunk + grp * HP;
+          const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
+          const size_t part =
+              (size_t(cta) * 2 + ((prev.flags & kSecond) ? 1 : 0)) * kChunk + grp * HP;
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            if (h0 + h < p.G) {
+              const float L = (sh->red[grp][0][h] + sh->red[grp][1][h]) +
+                              (sh->red[grp][2][h] + sh->red[grp][3][h]);
               if (prev.flags & kComplete) {
                 if (row < D) store_out(p, (bh + h) * D + row, o[h] / L);
                 if (row == h) {
                   const float lse2 = (m[h] == -INFINITY ? 0.f : m[h]) + log2f(L);
                   if (p.lse) p.lse[bh + h] = lse2 * 0.6931471805599453f;
-                  if (p.weights_out) p.w.row_lse2[size_t(prev.u) * kChunk + h] = lse2;
+                  if (p.weights_out)
+                    p.w.row_lse2[size_t(prev.u) * kChunk + grp * HP + h] = lse2;
                 }
               } else {
                 if (row < D) p.w.part_o[(part + h) * D + row] = o[h];
@@ -656,13 +743,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
               }
             }
           }
-          bar_sync(1, 128);                    // red is read before it is written again
+          group_sync<C::kGroups>(grp);              // red is read before it is written again
         }
       }
       if (it.n == 0) break;
       if (it.flags & kFirst) {
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
+        for (int h = 0; h < HP; ++h) {
           m[h] = -INFINITY;
           l[h] = 0.f;
           o[h] = 0.f;
@@ -671,46 +758,49 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       if (any) {
         // a new reference: the larger of the old one and the tile's maximum
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          float x = s[h];
-#pragma unroll
-          for (int w = 16; w; w >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-          if (lane == 0) sh->red[quarter][h] = x;
+        for (int h = 0; h < HP; ++h) {
+          const float x = warp_max(s[h]);
+          if (lane == 0) sh->red[grp][quarter][h] = x;
         }
-        bar_sync(1, 128);
+        group_sync<C::kGroups>(grp);
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          const float mn = fmaxf(m[h], fmaxf(fmaxf(sh->red[0][h], sh->red[1][h]),
-                                             fmaxf(sh->red[2][h], sh->red[3][h])));
+        for (int h = 0; h < HP; ++h) {
+          const float mn =
+              fmaxf(m[h], fmaxf(fmaxf(sh->red[grp][0][h], sh->red[grp][1][h]),
+                                fmaxf(sh->red[grp][2][h], sh->red[grp][3][h])));
           const float alpha = mn == m[h] ? 1.f : ex2(m[h] - mn);
           l[h] *= alpha;
           o[h] *= alpha;
           m[h] = mn;
         }
-        bar_sync(1, 128);
+        group_sync<C::kGroups>(grp);
       }
       if (p.weights_out && row < it.n) {
-        const int32_t r = it.u / p.HC, h0 = (it.u % p.HC) * kChunk;
+        const int32_t r = it.u / p.HC, h0 = (it.u % p.HC) * kChunk + grp * HP;
         float* dst = p.w.scores + (size_t(r) * p.G + h0) * p.cap + it.t + row;
 #pragma unroll
-        for (int h = 0; h < GP; ++h)
+        for (int h = 0; h < HP; ++h)
           if (h < gc) dst[size_t(h) * p.cap] = s[h];
       }
       // weights, in parts of bf16: row (part, head) of P, this thread's token
       // its column, in the 128-byte swizzle that the product reads
-      uint8_t* col = sP + (row >> 6) * C::kNP * 128;
-      const uint32_t chunk = uint32_t(row & 63) >> 3, off = uint32_t(row & 7) * 2;
+      uint8_t* col = sP + (row >> 6) * C::kNP * 128 + (row & 7) * 2;
+      const uint32_t chunk = uint32_t(row & 63) >> 3;
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        const float w = ex2(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
-        l[h] += w;
-        float rest = w;
+      for (int h = 0; h < HP; h += 2) {
+        float w0 = ex2(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+        float w1 = ex2(s[h + 1] - (m[h + 1] == -INFINITY ? 0.f : m[h + 1]));
+        l[h] += w0;
+        l[h + 1] += w1;
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
-          const int prow = q * GP + h;
-          const __nv_bfloat16 x = __float2bfloat16_rn(rest);
-          *reinterpret_cast<__nv_bfloat16*>(col + prow * 128 + ((chunk ^ (prow & 7)) << 4) + off) = x;
-          rest -= __bfloat162float(x);
+          const int r0 = q * GP + grp * HP + h, r1 = r0 + 1;
+          const uint32_t pk = pack_bf16x2(w0, w1);
+          *reinterpret_cast<uint16_t*>(col + r0 * 128 + ((chunk ^ (r0 & 7)) << 4)) = uint16_t(pk);
+          *reinterpret_cast<uint16_t*>(col + r1 * 128 + ((chunk ^ (r1 & 7)) << 4)) =
+              uint16_t(pk >> 16);
+          w0 -= __uint_as_float(pk << 16);
+          w1 -= __uint_as_float(pk & 0xFFFF0000u);
         }
       }
       fence_proxy_async_smem();
@@ -718,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->p_full);
       prev = it;
+      fail = !describe(j + 1);
     }
     if (!ok) {
       if (lane == 0) atomicOr(p.dev_status, SA_DEV_TIMEOUT);
@@ -733,72 +824,66 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   }
 }
 
-// Block (CTA c of the first launch, kJoinHeads heads): if c's range is the
-// second of a row, the join of the row's partial states.  Four warps a head
-// take every fourth state each, at the states' common maximum, and their sums
+// Block (record, head): the join of a row's partial states.  Sixteen warps take
+// every sixteenth state each, at the states' common maximum, and their sums
 // are added in warp order.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = D / 32;                     // elements of a lane
-  constexpr int kWays = kJoinThreads / 32 / kJoinHeads;
-  __shared__ float acc[kJoinHeads][kWays][D], ls[kJoinHeads][kWays];
+  constexpr int kWays = kJoinThreads / 32;
+  __shared__ float acc[kWays][D], ls[kWays];
   launch_dependents();
   wait_dependency();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
   const Record rec = p.w.rec[blockIdx.x];
   if (rec.u < 0) return;
   const int32_t r = rec.u / p.HC, h0 = (rec.u % p.HC) * kChunk;
-  const int hl = warp / kWays, way = warp % kWays;
-  const int h = blockIdx.y * kJoinHeads + hl;      // head of the chunk
-  const bool live = h < min(kChunk, p.G - h0);
+  const int h = blockIdx.y;                        // head of the chunk
+  if (h >= p.G - h0) return;
   auto part_of = [&](int32_t k) -> size_t {
     return (size_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * kChunk + h;
   };
   float M = -INFINITY;
-  if (live) {
-    for (int32_t k = lane; k < rec.segs; k += 32) M = fmaxf(M, p.w.part_ml[part_of(k)].x);
+  for (int32_t k = lane; k < rec.segs; k += 32) M = fmaxf(M, p.w.part_ml[part_of(k)].x);
+  M = warp_max(M);
+  if (M == -INFINITY) M = 0.f;
+  float L = 0.f, v[kVec];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, v[kVec];
-#pragma unroll
-    for (int x = 0; x < kVec; ++x) v[x] = 0.f;
+  for (int x = 0; x < kVec; ++x) v[x] = 0.f;
 #pragma unroll 4
-    for (int32_t k = way; k < rec.segs; k += kWays) {
-      const size_t at = part_of(k);
-      const float2 ml = p.w.part_ml[at];
-      const float f = ex2(ml.x - ref);
-      L = fmaf(f, ml.y, L);
-      if constexpr (kVec == 4) {
-        const float4 o4 = *reinterpret_cast<const float4*>(p.w.part_o + at * D + lane * 4);
-        v[0] = fmaf(f, o4.x, v[0]);
-        v[1] = fmaf(f, o4.y, v[1]);
-        v[2] = fmaf(f, o4.z, v[2]);
-        v[3] = fmaf(f, o4.w, v[3]);
-      } else {
-        const float2 o2 = *reinterpret_cast<const float2*>(p.w.part_o + at * D + lane * 2);
-        v[0] = fmaf(f, o2.x, v[0]);
-        v[1] = fmaf(f, o2.y, v[1]);
-      }
+  for (int32_t k = way; k < rec.segs; k += kWays) {
+    const size_t at = part_of(k);
+    const float2 ml = p.w.part_ml[at];
+    const float f = ex2(ml.x - M);
+    L = fmaf(f, ml.y, L);
+    if constexpr (kVec == 4) {
+      const float4 o4 = *reinterpret_cast<const float4*>(p.w.part_o + at * D + lane * 4);
+      v[0] = fmaf(f, o4.x, v[0]);
+      v[1] = fmaf(f, o4.y, v[1]);
+      v[2] = fmaf(f, o4.z, v[2]);
+      v[3] = fmaf(f, o4.w, v[3]);
+    } else {
+      const float2 o2 = *reinterpret_cast<const float2*>(p.w.part_o + at * D + lane * 2);
+      v[0] = fmaf(f, o2.x, v[0]);
+      v[1] = fmaf(f, o2.y, v[1]);
     }
-#pragma unroll
-    for (int x = 0; x < kVec; ++x) acc[hl][way][lane * kVec + x] = v[x];
-    if (lane == 0) ls[hl][way] = L;
-    M = ref;
   }
+#pragma unroll
+  for (int x = 0; x < kVec; ++x) acc[way][lane * kVec + x] = v[x];
+  if (lane == 0) ls[way] = L;
   __syncthreads();
-  if (!live) return;
-  float L = 0.f;
-#pragma unroll
-  for (int y = 0; y < kWays; ++y) L += ls[hl][y];
-  const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0 + h;
-  for (int x = way * 32 + lane; x < D; x += kWays * 32) {
-    float sum = 0.f;
-#pragma unroll
-    for (int y = 0; y < kWays; ++y) sum += acc[hl][y][x];
-    store_out(p, bh * D + x, sum / L);
+  const int x = threadIdx.x;
+  if (x >= D) return;
+  const int ways = min(kWays, rec.segs);
+  float sum = 0.f;
+  L = 0.f;
+  for (int y = 0; y < ways; ++y) {
+    L += ls[y];
+    sum += acc[y][x];
   }
-  if (way == 0 && lane == 0) {
+  const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0 + h;
+  store_out(p, bh * D + x, sum / L);
+  if (x == 0) {
     const float lse2 = M + log2f(L);
     if (p.lse) p.lse[bh] = lse2 * 0.6931471805599453f;
     if (p.weights_out) p.w.row_lse2[size_t(rec.u) * kChunk + h] = lse2;
@@ -807,7 +892,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
 
 // Block (piece of a row's slots, row): every token's probabilities, summed
 // over the row's heads, added to its weight.
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Params p, int32_t pieces) {
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ Params p,
+                                                                 int32_t pieces) {
   launch_dependents();
   wait_dependency();
   const int32_t r = blockIdx.x / pieces;
@@ -881,11 +967,8 @@ template <int D, int GP, int PARTS>
 cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_failed) {
   using C = Cfg<D, GP, PARTS>;
   constexpr int kRing = C::kStages * C::kStage;
-  // d = 64: the second half of the 128-row value operand lies one panel on;
-  // its rows of the product are not used, but the last stage's must exist
-  constexpr int kUsed = kRing + C::kP + C::kQs * C::kQ + int(sizeof(Shared));
-  constexpr int kSmem = D == 64 && kUsed < kRing + C::kPanel ? kRing + C::kPanel : kUsed;
-  static_assert(kPerSm * (kSmem + 1024) <= 233472, "shared memory budget");
+  constexpr int kSmem = kRing + C::kP + C::kQs * C::kQ + int(sizeof(Shared));
+  static_assert(C::kPerSm * (kSmem + 1024) <= 233472, "shared memory budget");
   const sa_paged_cache& c = a.c;
   const int64_t rows = int64_t(c.batch) * c.num_kv_heads;
   Params p{};
@@ -918,7 +1001,8 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.weights_out = a.weights_out;
   p.dev_status = a.dev_status;
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
-  const int ctas = sms * kPerSm;
+  const int ctas = sms * C::kPerSm;
+  p.by_row = p.U <= ctas;
   layout(&p.w, static_cast<char*>(a.ws), rows, p.G, p.cap, D, ctas, a.weights_out != nullptr);
   auto kern = attend_kernel<D, GP, PARTS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -933,11 +1017,11 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   e = cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(unsigned(ctas), unsigned((p.q_rows + kJoinHeads - 1) / kJoinHeads));
+  cfg.gridDim = dim3(unsigned(p.by_row ? p.U : ctas), unsigned(p.q_rows));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
@@ -969,7 +1053,7 @@ namespace sa_paged {
 
 size_t attend_workspace(const sa_paged_cache& c, int32_t Hq, bool accumulate, int sms) {
   return layout(nullptr, nullptr, int64_t(c.batch) * c.num_kv_heads, Hq / c.num_kv_heads,
-                int64_t(c.page) * c.max_pages, c.head_dim, sms * kPerSm, accumulate);
+                int64_t(c.page) * c.max_pages, c.head_dim, sms * 4, accumulate);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_failed) {
