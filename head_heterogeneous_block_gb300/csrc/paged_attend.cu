@@ -78,9 +78,9 @@ struct Cfg {
   static constexpr int kThreads = 64 + 128 * kGroups;
   // CTAs on a processor, the stages and Q tiles that then fit.  Tile j: K in
   // stage 2j % kStages, V in the next.
-  static constexpr int kPerSm = D == 64 && GP == 4 ? 4 : D == 64 && GP == 8 ? 3 : 2;
-  static constexpr int kStages = D == 128 || GP == 4 ? 3 : GP == 8 ? (PARTS == 2 ? 4 : 3) : 6;
-  static constexpr int kQs = (D == 128 && GP * PARTS > 32) || (D == 64 && GP == 4) ? 1 : 2;
+  static constexpr int kPerSm = 2;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kQs = D == 128 && GP * PARTS > 32 ? 1 : 2;
   static constexpr int kNS = 16;                      // columns of S
   static constexpr int kNP = (GP * PARTS + 15) / 16 * 16;   // columns of O, rows of P
   static constexpr int kQ = kPanels * kChunk * 128;   // bytes of one Q tile
@@ -175,6 +175,14 @@ struct Params {
   int32_t* dev_status;
   uint64_t wait_ns;
 };
+
+// The row, and the first head of the chunk, of u.
+__device__ __forceinline__ int32_t row_of(const Params& p, int32_t u) {
+  return p.HC == 1 ? u : u / p.HC;
+}
+__device__ __forceinline__ int32_t head_of(const Params& p, int32_t u) {
+  return p.HC == 1 ? 0 : (u % p.HC) * kChunk;
+}
 
 __device__ __forceinline__ int32_t units_of(const Params& p, int32_t len) {
   return (len + (1 << p.bx_shift) - 1) >> p.bx_shift;
@@ -295,6 +303,8 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     tmem_alloc(&sh->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
+  // keys and values are read once: their lines make way first in L2
+  const uint64_t pol = l2_policy_evict_first();
   wait_dependency();
 
   // ---- this CTA's range: a scan of every row's units
@@ -302,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   const int32_t ua = min(p.U, tid * per), ub = min(p.U, ua + per);
   int32_t mine = 0, len_a = 0;
   for (int32_t u = ua; u < ub; ++u) {
-    const int32_t n = sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status);
+    const int32_t n = sa_paged::row_len(p.lens, row_of(p, u), p.cap, p.dev_status);
     if (u == ua) len_a = n;
     mine += units_of(p, n);
   }
@@ -332,8 +342,8 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   // rows without a token, taken in turn by the CTAs
   auto empty_rows = [&](int first_thread, int threads) {
     for (int32_t u = cta; u < p.U; u += gridDim.x) {
-      if (sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status) > 0) continue;
-      const int32_t r = u / p.HC, h0 = (u % p.HC) * kChunk;
+      if (sa_paged::row_len(p.lens, row_of(p, u), p.cap, p.dev_status) > 0) continue;
+      const int32_t r = row_of(p, u), h0 = head_of(p, u);
       const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
       const int gc = min(kChunk, p.G - h0), x0 = tid - first_thread;
       for (int x = x0; x < gc * D; x += threads) store_out(p, bh * D + x, 0.f);
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     int32_t at = before;
     for (int32_t u = ua; u < ub; ++u) {
       const int32_t n = u == ua ? len_a
-                                : sa_paged::row_len(p.lens, u / p.HC, p.cap, p.dev_status);
+                                : sa_paged::row_len(p.lens, row_of(p, u), p.cap, p.dev_status);
       const int32_t k = units_of(p, n);
       if (a >= at && a < at + k) {
         sh->u0 = u;
@@ -371,14 +381,12 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
 
   if (warp == 0) {
     // ------------------------------------------------- producer
-    const uint64_t pol = l2_policy_evict_first();
-    const uint64_t pol_q = l2_policy_evict_last();
     int32_t u = sh->u0, pu = sh->p0;           // current row and the units before it
     int32_t len = sh->len0;
     int32_t ubase = u, ulen = 0;               // lane l holds the length of row ubase + l
     auto load_lens = [&]() {
       ulen = ubase + lane < p.U
-                 ? sa_paged::row_len(p.lens, (ubase + lane) / p.HC, p.cap, p.dev_status) : 0;
+                 ? sa_paged::row_len(p.lens, row_of(p, ubase + lane), p.cap, p.dev_status) : 0;
     };
     auto end_of = [&]() -> int32_t {           // of the row's part in this range
       return min(len, int32_t(min(int64_t(b - pu) << p.bx_shift, int64_t(1) << 30)));
@@ -430,18 +438,20 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     auto lookup = [&](const TileInfo& x) -> int32_t {
       if ((lane << p.bx_shift) >= x.n) return 0;
       const int32_t slot = x.t + (lane << p.bx_shift);
-      return p.table[int64_t(x.u / p.HC) * p.max_pages + (slot >> p.page_shift)];
+      return p.table[int64_t(row_of(p, x.u)) * p.max_pages + (slot >> p.page_shift)];
     };
     uint32_t i = 0, qi = 0;                    // tiles and Q tiles issued
     uint32_t issued = 0;                       // stages filled
     bool ok = true;
-    TileInfo cur = next();
-    int32_t pg = lookup(cur);
-    load_lens();
-    if (begins) record();
+    TileInfo cur = next(), nxt{0, 0, 0, 0};
+    int32_t pg = lookup(cur), npg = 0;
     while (cur.n > 0) {
-      const TileInfo nxt = next();
-      const int32_t npg = nxt.n > 0 ? lookup(nxt) : 0;
+      // the next tile's pages are looked up while the ring may be full; the
+      // first tile's copies wait for nothing
+      if (i > 0) {
+        nxt = next();
+        npg = lookup(nxt);
+      }
       const int boxes = (cur.n + bx - 1) >> p.bx_shift;
       const int32_t prow = (cur.t + (lane << p.bx_shift)) & ((1 << p.page_shift) - 1);
       const int slot = i % kInfo;
@@ -458,13 +468,13 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
           ok = wait_warp(&sh->q_empty[qs], ((qi / C::kQs) - 1) & 1, abort, p.wait_ns);
         if (!ok) break;
         if (lane == 0) {
-          const int32_t r = cur.u / p.HC;
-          const int32_t h0 = (r % p.Hkv) * p.G + (cur.u % p.HC) * kChunk;
+          const int32_t r = row_of(p, cur.u);
+          const int32_t h0 = (r % p.Hkv) * p.G + head_of(p, cur.u);
           mbar_arrive_expect_tx(&sh->q_full[qs], C::kPanels * p.q_rows * 128);
 #pragma unroll
           for (int s = 0; s < C::kPanels; ++s)
             tma_load_3d(sQ + qs * C::kQ + s * kChunk * 128, &tq, &sh->q_full[qs], s * 64, h0,
-                        r / p.Hkv, pol_q);
+                        r / p.Hkv, pol);
         }
         ++qi;
       }
@@ -490,6 +500,12 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         ++issued;
       }
       if (!ok) break;
+      if (i == 0) {
+        if (begins) record();
+        load_lens();
+        nxt = next();
+        npg = lookup(nxt);
+      }
       ++i;
       cur = nxt;
       pg = npg;
@@ -658,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
       // four warps learn together whether one gave up.
       float s[HP];
       bool need = false;
-      const int gc = min(kChunk, p.G - (it.u % p.HC) * kChunk) - grp * HP;   // live heads
+      const int gc = min(kChunk, p.G - head_of(p, it.u)) - grp * HP;   // live heads
       const bool live = !fail && it.n > 0;
       if (!fail && (live || j > 0)) {
         // lanes split over the scores, the last output product, and (for a
@@ -720,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
             for (int h = 0; h < HP; ++h) sh->red[grp][quarter][h] = l[h];
           }
           group_sync<C::kGroups>(grp);
-          const int32_t r = prev.u / p.HC, h0 = (prev.u % p.HC) * kChunk + grp * HP;
+          const int32_t r = row_of(p, prev.u), h0 = head_of(p, prev.u) + grp * HP;
           const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
           const size_t part =
               (size_t(cta) * 2 + ((prev.flags & kSecond) ? 1 : 0)) * kChunk + grp * HP;
@@ -776,7 +792,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         group_sync<C::kGroups>(grp);
       }
       if (p.weights_out && row < it.n) {
-        const int32_t r = it.u / p.HC, h0 = (it.u % p.HC) * kChunk + grp * HP;
+        const int32_t r = row_of(p, it.u), h0 = head_of(p, it.u) + grp * HP;
         float* dst = p.w.scores + (size_t(r) * p.G + h0) * p.cap + it.t + row;
 #pragma unroll
         for (int h = 0; h < HP; ++h)
@@ -837,7 +853,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
   const Record rec = p.w.rec[blockIdx.x];
   if (rec.u < 0) return;
-  const int32_t r = rec.u / p.HC, h0 = (rec.u % p.HC) * kChunk;
+  const int32_t r = row_of(p, rec.u), h0 = head_of(p, rec.u);
   const int h = blockIdx.y;                        // head of the chunk
   if (h >= p.G - h0) return;
   auto part_of = [&](int32_t k) -> size_t {
