@@ -1,6 +1,7 @@
 // Internal launch interface of the paged key-value cache operators.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -9,6 +10,7 @@
 
 namespace sa_paged {
 
+constexpr int kMaxDevices = 64;       // of a process, for what is set up once a device
 constexpr int kMaxKvHeads = 256;      // budgets travel as a kernel parameter
 constexpr int64_t kMaxEvictSlots = 262144;
 
@@ -53,6 +55,20 @@ struct EvictArgs {
 };
 size_t evict_workspace(const sa_paged_cache& c);
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st);
+
+// Lets `kern` use `bytes` of dynamic shared memory on the current device: once
+// a device, which bit mask `done` (of that kernel) keeps.
+template <class Kernel>
+cudaError_t allow_shared(Kernel* kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < kMaxDevices ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 #ifdef __CUDACC__
 // A row's length, clamped to its table and flagged when it was out of range.

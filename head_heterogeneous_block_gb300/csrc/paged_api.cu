@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "kernels.h"
@@ -52,11 +53,17 @@ sa_status check_heads(const sa_paged_cache* c, int32_t hq) {
   return SA_OK;
 }
 
+// Processors of the current device, asked for once.
 sa_status sm_count(int* sms) {
+  static std::atomic<int> known[sa_paged::kMaxDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
+  const bool kept = dev < sa_paged::kMaxDevices;
+  *sms = kept ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms > 0) return SA_OK;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return SA_ERR_CUDA;
+  if (kept) known[dev].store(*sms, std::memory_order_relaxed);
   return SA_OK;
 }
 

@@ -1021,7 +1021,8 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.by_row = p.U <= ctas;
   layout(&p.w, static_cast<char*>(a.ws), rows, p.G, p.cap, D, ctas, a.weights_out != nullptr);
   auto kern = attend_kernel<D, GP, PARTS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = sa_paged::allow_shared(kern, kSmem, done);
   if (e != cudaSuccess) return e;
   // each launch may start while the one before it in the stream ends, and
   // waits for it before it touches memory

@@ -310,8 +310,8 @@ cudaError_t launch(const EvictArgs& a, int sms, cudaStream_t st) {
     ranks *= 2;
   const int64_t slice = ((cap + ranks - 1) / ranks + 31) & ~int64_t(31);
   if (rows * ranks > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxSlice * 4);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = sa_paged::allow_shared(evict_kernel<D>, kMaxSlice * 4, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(rows * ranks));

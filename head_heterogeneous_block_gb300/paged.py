@@ -16,11 +16,7 @@ from . import (SA_DTYPE_BF16, SA_DTYPE_F32, PagedCacheDesc, _check, _lib,
                sparse_attn_paged_attend_workspace_size, sparse_attn_paged_evict_workspace_size)
 
 _I64x3 = ctypes.c_int64 * 3
-
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class PagedCache:
@@ -50,24 +46,29 @@ class PagedCache:
                                    ("positions", positions, torch.int32, 3)):
             if t is None:
                 continue
-            if t.dtype != dtype:
+            if t.dtype is not dtype:
                 raise TypeError(f"{name} must be {dtype}")
-            _need(t.dim() == nd, f"{name} must have {nd} dimensions")
-            _need(t.device == dev, f"{name} must be on {dev}")
-        _need(dev.type == "cuda", "the cache's tensors must be on a CUDA device")
+            if t.dim() != nd:
+                raise ValueError(f"{name} must have {nd} dimensions")
+            if t.device != dev:
+                raise ValueError(f"{name} must be on {dev}")
+            if t is not k_pages and t is not v_pages and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if dev.type != "cuda":
+            raise ValueError("the cache's tensors must be on a CUDA device")
         pages, page, d = k_pages.shape
-        _need(v_pages.shape == k_pages.shape, "k_pages and v_pages must have the same shape")
+        if v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must have the same shape")
         for t in (k_pages, v_pages):
-            _need(t.stride(2) == 1 and t.stride(1) == d, "a page must be contiguous")
+            if t.stride(2) != 1 or t.stride(1) != d:
+                raise ValueError("a page must be contiguous")
         b, h, max_pages = table.shape
-        _need(tuple(lens.shape) == (b, h), "lens must be [batch, num_kv_heads]")
-        for name, t in (("table", table), ("lens", lens), ("weights", weights),
-                        ("positions", positions)):
-            _need(t is None or t.is_contiguous(), f"{name} must be contiguous")
+        if tuple(lens.shape) != (b, h):
+            raise ValueError("lens must be [batch, num_kv_heads]")
         self.slots = max_pages * page
         for name, t in (("weights", weights), ("positions", positions)):
-            _need(t is None or tuple(t.shape) == (b, h, self.slots),
-                  f"{name} must be [batch, num_kv_heads, max_pages * page]")
+            if t is not None and tuple(t.shape) != (b, h, self.slots):
+                raise ValueError(f"{name} must be [batch, num_kv_heads, max_pages * page]")
         self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
         self.weights, self.positions = weights, positions
         self.batch, self.num_kv_heads, self.head_dim, self.page = b, h, d, page
@@ -79,18 +80,22 @@ class PagedCache:
             k_pages.stride(0) if pages > 1 else one, v_pages.stride(0) if pages > 1 else one,
             page, max_pages, b, h, d)
         self._ref = ctypes.byref(self.desc)
+        self._index = k_pages.get_device()
+        self._shape_b, self._shape_lens = torch.Size((b,)), torch.Size((b, h))
+        self._keep = ctypes.c_int32 * h
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._status = self.dev_status.data_ptr()
         self._ws = None
         self._ws_bytes = 0
-        self._ws_stream = torch.cuda.current_stream(dev).cuda_stream
+        self._ws_stream = _raw_stream(self._index)
         self._need_ws = {}
         if num_q_heads is not None:
             self._workspace(("attend", num_q_heads, weights is not None))
         if weights is not None:
             self._workspace(("evict",))
 
-    # -- helpers
+    # -- helpers (a step's calls are short: checks are written out where a
+    # call per check, or a message built for nothing, would cost more)
     def _workspace(self, key):
         need = self._need_ws.get(key)
         if need is None:
@@ -104,31 +109,26 @@ class PagedCache:
             self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
         return self._ws.data_ptr()
 
-    def _call(self, fn, stream, *args):
-        """fn(*args, stream) with the cache's device current."""
-        dev = self.device
-        if torch.cuda.current_device() != dev.index:
-            with torch.cuda.device(dev):
-                return self._call(fn, stream, *args)
+    def _handle(self, stream):
+        """The stream's handle; the cache's device is current."""
         if stream is None:
-            handle = torch._C._cuda_getCurrentRawStream(dev.index)
+            handle = _raw_stream(self._index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
         if handle != self._ws_stream:
             # the cache's own tensors outlive the work of streams they were
             # not allocated on
-            other = torch.cuda.ExternalStream(handle, device=dev)
+            other = torch.cuda.ExternalStream(handle, device=self.device)
             self.dev_status.record_stream(other)
             if self._ws is not None:
                 self._ws.record_stream(other)
-        status = fn(*args, handle)
-        if status:
-            _check(status, fn.__name__)
+        return handle
 
-    def _row_array(self, t, dtype, shape, name):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    def _own(self, t, dtype, shape, name):
+        """Address of a contiguous tensor of the cache's device."""
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}")
         return t.data_ptr()
 
@@ -139,25 +139,39 @@ class PagedCache:
         of 8, d contiguous) to every row of sequence b, at positions
         ``start[b]``, ``start[b]`` + 1, ... (default: their slots).  The new
         lengths go to ``lens_out`` (default: ``lens``)."""
-        b, h, d = self.batch, self.num_kv_heads, self.head_dim
-        for name, t in (("k", k), ("v", v)):
-            if t.dtype != torch.bfloat16:
-                raise TypeError(f"{name} must be bfloat16")
-            _need(t.dim() == 4 and t.shape[0] == b and t.shape[1] == h and t.shape[3] == d and
-                  t.shape[2] >= 1 and t.stride(3) == 1,
-                  f"{name} must be [batch, num_kv_heads, tokens, d] with d contiguous")
-            _need(t.device == self.device, f"{name} must be on {self.device}")
-        tokens = k.shape[2]
-        _need(v.shape[2] == tokens, "k and v must have the same shape")
-        strides = [_I64x3(*(st if n > 1 else 0 for st, n in zip(t.stride(), t.shape[:3])))
-                   for t in (k, v)]
-        self._call(_lib.sparse_attn_paged_append, stream, self._ref, k.data_ptr(), v.data_ptr(),
-                   strides[0], strides[1], tokens,
-                   None if counts is None else self._row_array(counts, torch.int32, (b,), "counts"),
-                   None if start is None else self._row_array(start, torch.int32, (b,), "start"),
-                   self.desc.lens if lens_out is None else
-                   self._row_array(lens_out, torch.int32, (b, h), "lens_out"),
-                   self._status)
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.append(k, v, counts, start, lens_out, stream)
+        b, h, tokens, d = k.shape if k.dim() == 4 else (0, 0, 0, 0)
+        if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+            raise TypeError("k and v must be bfloat16")
+        if b != self.batch or h != self.num_kv_heads or d != self.head_dim or tokens < 1:
+            raise ValueError("k must be [batch, num_kv_heads, tokens, d]")
+        if v.shape != k.shape:
+            raise ValueError("k and v must have the same shape")
+        k0, k1, k2, k3 = k.stride()
+        v0, v1, v2, v3 = v.stride()
+        if k3 != 1 or v3 != 1:
+            raise ValueError("the last dimension of k and v must be contiguous")
+        if k.get_device() != self._index or v.get_device() != self._index:
+            raise ValueError(f"k and v must be on {self.device}")
+        if b == 1:                          # the stride of an extent of one is not used
+            k0 = v0 = 0
+        if h == 1:
+            k1 = v1 = 0
+        if tokens == 1:
+            k2 = v2 = 0
+        if counts is not None:
+            counts = self._own(counts, torch.int32, self._shape_b, "counts")
+        if start is not None:
+            start = self._own(start, torch.int32, self._shape_b, "start")
+        lens = (self.desc.lens if lens_out is None else
+                self._own(lens_out, torch.int32, self._shape_lens, "lens_out"))
+        status = _lib.sparse_attn_paged_append(
+            self._ref, k.data_ptr(), v.data_ptr(), _I64x3(k0, k1, k2), _I64x3(v0, v1, v2), tokens,
+            counts, start, lens, self._status, self._handle(stream))
+        if status:
+            _check(status, "sparse_attn_paged_append")
 
     def attend(self, q, out=None, lse=None, weights_out=None, accumulate=None, stream=None):
         """Attention of one new token per sequence: q bf16 [batch, num_q_heads,
@@ -167,39 +181,49 @@ class PagedCache:
         given.  ``accumulate`` (default: when the cache has weights) adds each
         token's probability, summed over the row's heads, to its weight, into
         ``weights_out`` (default: ``weights``)."""
-        b, d = self.batch, self.head_dim
-        if q.dtype != torch.bfloat16:
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.attend(q, out, lse, weights_out, accumulate, stream)
+        if q.dtype is not torch.bfloat16:
             raise TypeError("q must be bfloat16")
-        _need(q.dim() == 3 and q.shape[0] == b and q.shape[2] == d and q.stride(2) == 1,
-              "q must be [batch, num_q_heads, d] with d contiguous")
-        _need(q.device == self.device, f"q must be on {self.device}")
-        hq = q.shape[1]
+        b, hq, d = q.shape if q.dim() == 3 else (0, 0, 0)
+        if b != self.batch or d != self.head_dim:
+            raise ValueError("q must be [batch, num_q_heads, d]")
+        q0, q1, q2 = q.stride()
+        if q2 != 1:
+            raise ValueError("the last dimension of q must be contiguous")
+        if q.get_device() != self._index:
+            raise ValueError(f"q must be on {self.device}")
         if out is None:
             out = torch.empty(b, hq, d, dtype=torch.bfloat16, device=self.device)
-            if stream is not None and not isinstance(stream, int):
-                out.record_stream(stream)
-        if out.dtype == torch.bfloat16:
+            if stream is not None:
+                out.record_stream(torch.cuda.ExternalStream(stream, device=self.device)
+                                  if isinstance(stream, int) else stream)
+        if out.dtype is torch.bfloat16:
             o_dtype = SA_DTYPE_BF16
-        elif out.dtype == torch.float32:
+        elif out.dtype is torch.float32:
             o_dtype = SA_DTYPE_F32
         else:
             raise TypeError("out must be bfloat16 or float32")
-        o = self._row_array(out, out.dtype, (b, hq, d), "out")
+        o = self._own(out, out.dtype, q.shape, "out")
         if lse is not None:
-            lse = self._row_array(lse, torch.float32, (b, hq), "lse")
+            lse = self._own(lse, torch.float32, (b, hq), "lse")
         if accumulate is None:
             accumulate = self.weights is not None
         w = None
         if accumulate:
-            _need(self.weights is not None, "the cache has no weights to accumulate into")
+            if self.weights is None:
+                raise ValueError("the cache has no weights to accumulate into")
             w = (self.desc.weights if weights_out is None else
-                 self._row_array(weights_out, torch.float32, tuple(self.weights.shape),
-                                 "weights_out"))
-        else:
-            _need(weights_out is None, "weights_out needs accumulate")
+                 self._own(weights_out, torch.float32, self.weights.shape, "weights_out"))
+        elif weights_out is not None:
+            raise ValueError("weights_out needs accumulate")
         ws = self._workspace(("attend", hq, bool(accumulate)))
-        self._call(_lib.sparse_attn_paged_attend, stream, self._ref, q.data_ptr(), q.stride(0),
-                   q.stride(1), hq, o, o_dtype, lse, w, ws, self._ws_bytes, self._status)
+        status = _lib.sparse_attn_paged_attend(
+            self._ref, q.data_ptr(), q0, q1, hq, o, o_dtype, lse, w, ws, self._ws_bytes,
+            self._status, self._handle(stream))
+        if status:
+            _check(status, "sparse_attn_paged_attend")
         return out
 
     def evict(self, keep, sinks=0, recent=0, lens_out=None, weights_out=None, positions_out=None,
@@ -208,19 +232,26 @@ class PagedCache:
         first ``sinks`` positions, the last ``recent`` ones, then the largest
         weights.  The new state goes to ``lens_out``, ``weights_out`` and
         ``positions_out`` (default: the cache's own tensors)."""
-        _need(self.weights is not None, "eviction needs the cache's weights")
-        _need(len(keep) == self.num_kv_heads, "keep must hold one budget per KV head")
-        shape = tuple(self.weights.shape)
-        if positions_out is not None:
-            _need(self.positions is not None, "positions_out needs the cache's positions")
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.evict(keep, sinks, recent, lens_out, weights_out, positions_out,
+                                  stream)
+        if self.weights is None:
+            raise ValueError("eviction needs the cache's weights")
+        if len(keep) != self.num_kv_heads:
+            raise ValueError("keep must hold one budget per KV head")
+        if positions_out is not None and self.positions is None:
+            raise ValueError("positions_out needs the cache's positions")
+        shape = self.weights.shape
+        lens = (self.desc.lens if lens_out is None else
+                self._own(lens_out, torch.int32, self._shape_lens, "lens_out"))
+        w = (self.desc.weights if weights_out is None else
+             self._own(weights_out, torch.float32, shape, "weights_out"))
+        pos = (self.desc.positions if positions_out is None else
+               self._own(positions_out, torch.int32, shape, "positions_out"))
         ws = self._workspace(("evict",))
-        self._call(_lib.sparse_attn_paged_evict, stream, self._ref,
-                   (ctypes.c_int32 * len(keep))(*keep), sinks, recent,
-                   self.desc.lens if lens_out is None else
-                   self._row_array(lens_out, torch.int32, (self.batch, self.num_kv_heads),
-                                   "lens_out"),
-                   self.desc.weights if weights_out is None else
-                   self._row_array(weights_out, torch.float32, shape, "weights_out"),
-                   self.desc.positions if positions_out is None else
-                   self._row_array(positions_out, torch.int32, shape, "positions_out"),
-                   ws, self._ws_bytes, self._status)
+        status = _lib.sparse_attn_paged_evict(
+            self._ref, self._keep(*keep), sinks, recent, lens, w, pos, ws, self._ws_bytes,
+            self._status, self._handle(stream))
+        if status:
+            _check(status, "sparse_attn_paged_evict")
