@@ -4,10 +4,11 @@
 // `recent` positions, else the weight's bits mapped so that unsigned order is
 // the floats' order (NaN below every number, -0 as +0).  Per row:
 //
-//   select   the m-th largest key T, by four passes of 8 bits from the top: a
-//            histogram of the keys that agree with T so far, and the bin that
-//            holds the m-th.  Tokens above T are kept, and of those equal to T
-//            the lowest slots until m are.
+//   select   the m-th largest key T, digit by digit from the top: a histogram
+//            of the keys that agree with T so far, and the bin that holds the
+//            m-th.  When a bin is kept whole its lower digits do not matter.
+//            Tokens above T are kept, and of those equal to T the lowest slots
+//            until m are.
 //   number   with K(t) the kept slots below t, an evicted slot t < m is hole
 //            t - K(t) and a kept slot t >= m is source K(t) - K(m): one prefix
 //            count gives both lists, in slot order.
@@ -15,19 +16,24 @@
 //            below, so no move reads what another writes, and only the tokens
 //            that have to move are touched.
 //
-// A row is worked on by a cluster of 1 to 8 CTAs, each with a contiguous slice
-// of the slots, whose keys stay in shared memory between the passes (the
-// weights and positions are read from memory once, or twice for positions);
-// histograms and counts are added up over the cluster through distributed
-// shared memory.  Moves are spread over the cluster's warps, 8 steps of loads
-// in flight each.
+// Rows of up to 8192 slots: one CTA, the keys in registers (evict_row_kernel).
+// Its time is a chain of latencies, not of bytes, so it has as few barriers as
+// it can: digits of 11 bits, histograms cleared ahead, lists in shared memory.
+// Longer rows: a cluster of 2 to 8 CTAs, each with a contiguous slice whose
+// keys stay in its shared memory; histograms of 8 bits and counts are added up
+// over the cluster through distributed shared memory (evict_cluster_kernel).
+// The moves of a short row are made by its own CTA; those of long rows, or of
+// few rows with much to move, by a second launch over all processors
+// (move_kernel).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace {
 
@@ -37,7 +43,11 @@ using sa_paged::EvictArgs;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = 8;
-constexpr int kMaxSlice = 32768;       // keys of a CTA: 128 KB of shared memory
+constexpr int kMaxSlice = 32768;       // keys of a cluster's CTA: 128 KB of shared memory
+constexpr int kRowKeys = 16;           // keys of a thread where a CTA has the whole row
+constexpr int kRowSlots = kThreads * kRowKeys;
+constexpr int kBins = 2048;
+constexpr int kMoveThreads = 256;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -45,12 +55,310 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ bool is_forced(const EvictArgs& a, int32_t pos, int32_t newest) {
+  return pos < a.sinks || (a.recent > 0 && int64_t(pos) > int64_t(newest) - a.recent);
+}
+
+// Workspace: the numbers of moves [rows], then two lists of at most cap / 2
+// slots a row.
+struct Work {
+  int32_t* pairs;
+  int32_t* lists;      // [rows][cap]: holes, then sources
+};
+__host__ __device__ __forceinline__ Work work_of(const EvictArgs& a) {
+  const int64_t rows = int64_t(a.c.batch) * a.c.num_kv_heads;
+  int32_t* p = static_cast<int32_t*>(a.ws);
+  return Work{p, p + ((rows + 63) & ~int64_t(63))};
+}
+
+// Moves [g, g + group) of a row, one warp: lane i < group has pair i's slots in
+// (s, t), or s < 0.  A token of d/8 lanes a key (or value) row, 16 bytes a
+// lane; all loads of the group are in flight before its first store.
+template <int D>
+struct Mover {
+  static constexpr int kPiece = D / 8;                  // lanes of one row
+  static constexpr int kPer = 32 / (2 * kPiece);        // tokens of one step
+  static constexpr int kGroup = kSteps * kPer;
+  static __device__ __forceinline__ void move(const EvictArgs& a, int64_t r, int32_t s,
+                                              int32_t t) {
+    const int lane = threadIdx.x & 31;
+    const int32_t cap = a.c.page * a.c.max_pages;
+    const int32_t* table = a.c.table + r * a.c.max_pages;
+    int32_t sp = -1, tp = -1, so = 0, to = 0;
+    if (s >= 0) {
+      sp = table[s / a.c.page];
+      tp = table[t / a.c.page];
+      so = s % a.c.page;
+      to = t % a.c.page;
+      a.weights_out[r * cap + t] = a.c.weights[r * cap + s];
+      if (a.positions_out) a.positions_out[r * cap + t] = a.c.positions[r * cap + s];
+      if (sp < 0 || sp >= a.c.num_pages || tp < 0 || tp >= a.c.num_pages) {
+        atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
+        sp = -1;
+      }
+    }
+    const bool is_v = (lane / kPiece) & 1;
+    const int sub = lane / (2 * kPiece);
+    const int64_t stride = is_v ? a.c.v_page_stride : a.c.k_page_stride;
+    __nv_bfloat16* pool =
+        static_cast<__nv_bfloat16*>(is_v ? a.c.v_pages : a.c.k_pages) + (lane % kPiece) * 8;
+    uint4 val[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int32_t p = __shfl_sync(0xffffffffu, sp, i * kPer + sub);
+      const int32_t x = __shfl_sync(0xffffffffu, so, i * kPer + sub);
+      if (p >= 0) val[i] = *reinterpret_cast<const uint4*>(pool + p * stride + int64_t(x) * D);
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const bool ok = __shfl_sync(0xffffffffu, sp, i * kPer + sub) >= 0;
+      const int32_t p = __shfl_sync(0xffffffffu, tp, i * kPer + sub);
+      const int32_t x = __shfl_sync(0xffffffffu, to, i * kPer + sub);
+      if (ok) *reinterpret_cast<uint4*>(pool + p * stride + int64_t(x) * D) = val[i];
+    }
+  }
+};
+
+// ---------------------------------------------------------------- one CTA a row
+struct RowShared {
+  int32_t hist[3][kBins];
+  uint16_t dst[kRowSlots / 2], src[kRowSlots / 2];
+  int32_t warp_total[kWarps];
+  int32_t warp_count[kWarps][2];
+  int32_t newest;
+  int32_t bin, need, count;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) evict_row_kernel(const __grid_constant__ EvictArgs a,
+                                                             int moves_here) {
+  __shared__ RowShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  sa_dev::launch_dependents();
+  if (tid == 0) sh.newest = INT32_MIN;
+#pragma unroll
+  for (int x = tid; x < 3 * kBins; x += kThreads) (&sh.hist[0][0])[x] = 0;
+  __syncthreads();
+  sa_dev::wait_dependency();
+  const int64_t r = blockIdx.x;
+  const int32_t cap = a.c.page * a.c.max_pages;
+  const int32_t n = sa_paged::row_len(a.c.lens, r, cap, a.dev_status);
+  const int32_t m = min(n, a.keep[r % a.c.num_kv_heads]);
+  const float* w = a.c.weights + r * cap;
+  const int32_t* pos = a.c.positions ? a.c.positions + r * cap : nullptr;
+  float* wo = a.weights_out + r * cap;
+  int32_t* po = a.positions_out ? a.positions_out + r * cap : nullptr;
+  const bool copy_w = wo != w, copy_p = po && po != pos;
+  const Work ws = work_of(a);
+  if (m == n || m == 0) {              // nothing, or everything, goes
+    for (int32_t t = tid; t < m; t += kThreads) {
+      if (copy_w) wo[t] = w[t];
+      if (copy_p) po[t] = pos[t];
+    }
+    if (tid == 0) {
+      a.lens_out[r] = m;
+      if (!moves_here) ws.pairs[r] = 0;
+    }
+    return;
+  }
+
+  // ---- keys: a warp has consecutive slots, 32 a step
+  const int per = (n + kThreads - 1) / kThreads;       // steps
+  const int32_t w0 = warp * per * 32 + lane;           // this lane's first slot
+  uint32_t key[kRowKeys];
+  int32_t q[kRowKeys];
+  int32_t newest = INT32_MIN;
+#pragma unroll
+  for (int j = 0; j < kRowKeys; ++j) {
+    const int32_t t = w0 + j * 32;
+    key[j] = 0;
+    q[j] = INT32_MIN;
+    if (j < per && t < n) {
+      key[j] = weight_key(w[t]);
+      q[j] = pos ? pos[t] : t;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRowKeys; ++j) newest = max(newest, q[j]);
+  newest = __reduce_max_sync(0xffffffffu, newest);
+  if (lane == 0) atomicMax(&sh.newest, newest);
+  __syncthreads();
+  newest = sh.newest;
+  uint32_t live = 0;                   // bit j: slot j of this lane is in the row
+#pragma unroll
+  for (int j = 0; j < kRowKeys; ++j)
+    if (j < per && w0 + j * 32 < n) {
+      live |= 1u << j;
+      if (is_forced(a, q[j], newest)) key[j] = 0xFFFFFFFFu;
+    }
+
+  // ---- select
+  uint32_t T = 0;
+  int32_t need = m;                    // of the keys that agree with T so far
+  bool tied = true;                    // more keys equal T than are kept
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : 2048;
+    const int mine = bins / kThreads;
+    int32_t* hist = sh.hist[pass];
+#pragma unroll
+    for (int j = 0; j < kRowKeys; ++j)
+      if ((live >> j & 1u) && (pass == 0 || (key[j] ^ T) >> (pass == 1 ? 21 : 10) == 0))
+        atomicAdd(&hist[(key[j] >> shift) & (bins - 1)], 1);
+    __syncthreads();
+    // thread x has the x-th group of bins from the top
+    int32_t c[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < mine; ++i) {
+      c[i] = hist[bins - 1 - (tid * mine + i)];
+      sum += c[i];
+    }
+    int32_t before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) sh.warp_total[warp] = before;
+    before -= sum;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x)
+      if (x < warp) before += sh.warp_total[x];
+#pragma unroll
+    for (int i = 0; i < mine; ++i) {
+      if (before < need && before + c[i] >= need) {
+        sh.bin = bins - 1 - (tid * mine + i);
+        sh.need = need - before;
+        sh.count = c[i];
+      }
+      before += c[i];
+    }
+    __syncthreads();
+    T |= uint32_t(sh.bin) << shift;
+    need = sh.need;
+    if (sh.count == need) {
+      tied = false;
+      break;
+    }
+  }
+
+  // ---- number
+  const uint32_t lower = (1u << lane) - 1u;
+  uint32_t kept = 0;                   // bit j
+  if (!tied) {
+#pragma unroll
+    for (int j = 0; j < kRowKeys; ++j)
+      if ((live >> j & 1u) && key[j] >= T) kept |= 1u << j;
+  } else {
+    int32_t ties = 0;
+#pragma unroll
+    for (int j = 0; j < kRowKeys; ++j)
+      ties += __popc(__ballot_sync(0xffffffffu, (live >> j & 1u) && key[j] == T));
+    if (lane == 0) sh.warp_count[warp][0] = ties;
+    __syncthreads();
+    int32_t t = 0;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x)
+      if (x < warp) t += sh.warp_count[x][0];
+#pragma unroll
+    for (int j = 0; j < kRowKeys; ++j) {
+      const bool in = live >> j & 1u, eq = in && key[j] == T;
+      const uint32_t b = __ballot_sync(0xffffffffu, eq);
+      if (in && (key[j] > T || (eq && t + __popc(b & lower) < need))) kept |= 1u << j;
+      t += __popc(b);
+    }
+    __syncthreads();
+  }
+  int32_t count = 0, low = 0;          // kept slots of the warp, and those below m
+#pragma unroll
+  for (int j = 0; j < kRowKeys; ++j) {
+    count += __popc(__ballot_sync(0xffffffffu, kept >> j & 1u));
+    low += __popc(__ballot_sync(0xffffffffu, (kept >> j & 1u) && w0 + j * 32 < m));
+  }
+  if (lane == 0) {
+    sh.warp_count[warp][0] = count;
+    sh.warp_count[warp][1] = low;
+  }
+  __syncthreads();
+  int32_t K = 0, Km = 0;
+#pragma unroll
+  for (int x = 0; x < kWarps; ++x) {
+    if (x < warp) K += sh.warp_count[x][0];
+    Km += sh.warp_count[x][1];
+  }
+  const int32_t pairs = m - Km;
+  int32_t* list = ws.lists + r * cap;
+#pragma unroll
+  for (int j = 0; j < kRowKeys; ++j) {
+    if (j < per) {
+      const uint32_t b = __ballot_sync(0xffffffffu, kept >> j & 1u);
+      const int32_t t = w0 + j * 32, k = K + __popc(b & lower);
+      if (live >> j & 1u) {
+        const bool keep = kept >> j & 1u;
+        if (t < m && !keep) {
+          if (moves_here)
+            sh.dst[t - k] = uint16_t(t);
+          else
+            list[t - k] = t;
+        }
+        if (t >= m && keep) {
+          if (moves_here)
+            sh.src[k - Km] = uint16_t(t);
+          else
+            list[cap / 2 + k - Km] = t;
+        }
+        if (t < m && keep) {
+          if (copy_w) wo[t] = w[t];
+          if (copy_p) po[t] = pos[t];
+        }
+      }
+      K += __popc(b);
+    }
+  }
+  if (tid == 0) {
+    a.lens_out[r] = m;
+    if (!moves_here) ws.pairs[r] = pairs;
+  }
+  if (!moves_here) return;
+  __syncthreads();
+  constexpr int kGroup = Mover<D>::kGroup;
+  for (int32_t g = warp * kGroup; g < pairs; g += kWarps * kGroup) {
+    const bool on = lane < kGroup && g + lane < pairs;
+    Mover<D>::move(a, r, on ? int32_t(sh.src[g + lane]) : -1, on ? int32_t(sh.dst[g + lane]) : 0);
+  }
+}
+
+// Block (piece of a row's moves, row).
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a,
+                                                            int32_t pieces) {
+  constexpr int kGroup = Mover<D>::kGroup;
+  sa_dev::launch_dependents();
+  sa_dev::wait_dependency();
+  const Work ws = work_of(a);
+  const int64_t r = blockIdx.x / pieces;
+  const int32_t pairs = ws.pairs[r];
+  const int lane = threadIdx.x & 31;
+  const int32_t g =
+      (int32_t(blockIdx.x % pieces) * (kMoveThreads / 32) + int32_t(threadIdx.x >> 5)) * kGroup;
+  if (g >= pairs) return;
+  const int32_t cap = a.c.page * a.c.max_pages;
+  const int32_t* list = ws.lists + r * cap;
+  const bool on = lane < kGroup && g + lane < pairs;
+  Mover<D>::move(a, r, on ? list[cap / 2 + g + lane] : -1, on ? list[g + lane] : 0);
+}
+
+// ---------------------------------------------------------------- a cluster a row
+constexpr int kMaxRanks = 8;
+
 struct Shared {
   int32_t hist[2][256];    // by pass parity: the other CTAs may still read the last one
   int32_t warp_count[kWarps][2];
   int32_t bins[8];
   int32_t share[3][2];     // [0] largest position; [1] ties; [2] kept, kept below m
-  int32_t bin, need;
+  int32_t bin, need, count;
 };
 
 // Sum over the CTA of (x, y), by every thread; each warp passes its own counts
@@ -78,13 +386,15 @@ __device__ __forceinline__ int2 before_in_block(Shared& sh, int2 mine, int2& tot
   return before;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    evict_cluster_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ Shared sh;
   extern __shared__ uint32_t keys[];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  sa_dev::launch_dependents();
+  sa_dev::wait_dependency();
   const int64_t r = blockIdx.x / ranks;
   const int32_t cap = a.c.page * a.c.max_pages;
   const int32_t n = sa_paged::row_len(a.c.lens, r, cap, a.dev_status);
@@ -94,13 +404,17 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   float* wo = a.weights_out + r * cap;
   int32_t* po = a.positions_out ? a.positions_out + r * cap : nullptr;
   const bool copy_w = wo != w, copy_p = po && po != pos;
+  const Work ws = work_of(a);
 
   if (m == n || m == 0) {              // nothing, or everything, goes
     for (int32_t t = rank * kThreads + tid; t < m; t += ranks * kThreads) {
       if (copy_w) wo[t] = w[t];
       if (copy_p) po[t] = pos[t];
     }
-    if (rank == 0 && tid == 0) a.lens_out[r] = m;
+    if (rank == 0 && tid == 0) {
+      a.lens_out[r] = m;
+      ws.pairs[r] = 0;
+    }
     return;
   }
 
@@ -112,57 +426,51 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
 
   // ---- keys
   int32_t newest = pos ? INT32_MIN : n - 1;
-#pragma unroll 4
+#pragma unroll 8
   for (int32_t i = tid; i < ns; i += kThreads) {
     keys[i] = weight_key(w[lo + i]);
     if (pos) newest = max(newest, pos[lo + i]);
   }
   if (pos && a.recent > 0) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) newest = max(newest, __shfl_xor_sync(0xffffffffu, newest, o));
+    newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) sh.warp_count[warp][0] = newest;
     __syncthreads();
+#pragma unroll
     for (int x = 0; x < kWarps; ++x) newest = max(newest, sh.warp_count[x][0]);
-    if (ranks > 1) {
-      if (tid == 0) sh.share[0][0] = newest;
-      cluster.sync();
-      for (int x = 0; x < ranks; ++x)
-        newest = max(newest, cluster.map_shared_rank(&sh, x)->share[0][0]);
-    }
+    if (tid == 0) sh.share[0][0] = newest;
+    cluster.sync();
+#pragma unroll
+    for (int x = 0; x < kMaxRanks; ++x)
+      if (x < ranks) newest = max(newest, cluster.map_shared_rank(&sh, x)->share[0][0]);
   }
   if (a.sinks > 0 || a.recent > 0) {
-    const int64_t from = int64_t(newest) - a.recent;
-#pragma unroll 4
-    for (int32_t i = tid; i < ns; i += kThreads) {
-      const int32_t q = pos ? pos[lo + i] : lo + i;
-      if (q < a.sinks || (a.recent > 0 && int64_t(q) > from)) keys[i] = 0xFFFFFFFFu;
-    }
+#pragma unroll 8
+    for (int32_t i = tid; i < ns; i += kThreads)
+      if (is_forced(a, pos ? pos[lo + i] : lo + i, newest)) keys[i] = 0xFFFFFFFFu;
   }
 
   // ---- select
   uint32_t T = 0;
   int32_t need = m;                    // of the keys that agree with T so far
+  bool tied = true;                    // more keys equal T than are kept
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     int32_t* hist = sh.hist[pass & 1];
     if (tid < 256) hist[tid] = 0;
     __syncthreads();
     const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
-#pragma unroll 4
+#pragma unroll 8
     for (int32_t i = tid; i < ns; i += kThreads) {
       const uint32_t k = keys[i];
       if (((k ^ T) & mask) == 0) atomicAdd(&hist[(k >> shift) & 255u], 1);
     }
-    if (ranks > 1)
-      cluster.sync();
-    else
-      __syncthreads();
+    cluster.sync();
     int32_t mine = 0, above = 0;
     if (tid < 256) {
       // thread x has bin 255 - x, so that a prefix sum counts from the top
-      mine = 0;
-      for (int x = 0; x < ranks; ++x)
-        mine += (ranks > 1 ? cluster.map_shared_rank(&sh, x) : &sh)->hist[pass & 1][255 - tid];
+#pragma unroll
+      for (int x = 0; x < kMaxRanks; ++x)
+        if (x < ranks) mine += cluster.map_shared_rank(&sh, x)->hist[pass & 1][255 - tid];
       above = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -177,30 +485,41 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       if (above >= need && above - mine < need) {
         sh.bin = 255 - tid;
         sh.need = need - (above - mine);
+        sh.count = mine;
       }
     }
     __syncthreads();
     T |= uint32_t(sh.bin) << shift;
     need = sh.need;
+    if (sh.count == need) {            // the same in every CTA of the cluster
+      tied = false;
+      break;
+    }
   }
 
-  // ---- number: ties in slot order, then kept slots
-  int32_t ties = 0;
-  for (int32_t i = w0; i < w1; i += 32) {
-    const bool eq = i + lane < w1 && keys[i + lane] == T;
-    ties += __popc(__ballot_sync(0xffffffffu, eq));
-  }
+  // ---- number: ties in slot order where they matter, then kept slots
+  const uint32_t lower = (1u << lane) - 1u;
   int2 total;
-  int32_t tie = before_in_block(sh, make_int2(ties, 0), total).x;
-  if (ranks > 1) {
+  int32_t tie = 0;
+  if (tied) {
+    int32_t ties = 0;
+    for (int32_t i = w0; i < w1; i += 32) {
+      const bool eq = i + lane < w1 && keys[i + lane] == T;
+      ties += __popc(__ballot_sync(0xffffffffu, eq));
+    }
+    tie = before_in_block(sh, make_int2(ties, 0), total).x;
     if (tid == 0) sh.share[1][0] = total.x;
     cluster.sync();
-    for (int x = 0; x < rank; ++x) tie += cluster.map_shared_rank(&sh, x)->share[1][0];
+#pragma unroll
+    for (int x = 0; x < kMaxRanks; ++x)
+      if (x < rank) tie += cluster.map_shared_rank(&sh, x)->share[1][0];
+  } else {
+    __syncthreads();                   // the keys of other threads are read next
   }
-  const uint32_t lower = (1u << lane) - 1u;
   // whether slot i of the slice is kept; t runs over the ties before the warp's place
   auto kept_at = [&](int32_t i, int32_t& t) -> bool {
     const uint32_t k = i + lane < w1 ? keys[i + lane] : 0u;
+    if (!tied) return i + lane < w1 && k >= T;
     const bool eq = i + lane < w1 && k == T;
     const uint32_t b = __ballot_sync(0xffffffffu, eq);
     const bool kept = i + lane < w1 && (k > T || (eq && t + __popc(b & lower) < need));
@@ -216,125 +535,116 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
     count.y += below >= 32 ? __popc(b) : below > 0 ? __popc(b & ((1u << below) - 1u)) : 0;
   }
   int32_t K = before_in_block(sh, count, total).x;
-  int32_t Km = total.y;
-  if (ranks > 1) {
-    if (tid == 0) {
-      sh.share[2][0] = total.x;
-      sh.share[2][1] = total.y;
-    }
-    cluster.sync();
-    Km = 0;
-    for (int x = 0; x < ranks; ++x) {
+  if (tid == 0) {
+    sh.share[2][0] = total.x;
+    sh.share[2][1] = total.y;
+  }
+  cluster.sync();
+  int32_t Km = 0;
+#pragma unroll
+  for (int x = 0; x < kMaxRanks; ++x) {
+    if (x < ranks) {
       const Shared* other = cluster.map_shared_rank(&sh, x);
       if (x < rank) K += other->share[2][0];
       Km += other->share[2][1];
     }
   }
-  const int32_t pairs = m - Km;
-  int32_t* dst_list = static_cast<int32_t*>(a.ws) + r * cap;
-  int32_t* src_list = dst_list + cap / 2;
+  if (rank == 0 && tid == 0) {
+    a.lens_out[r] = m;
+    ws.pairs[r] = m - Km;
+  }
+  int32_t* list = ws.lists + r * cap;
   t = tie;
   for (int32_t i = w0; i < w1; i += 32) {
     const bool kept = kept_at(i, t);
     const uint32_t b = __ballot_sync(0xffffffffu, kept);
     const int32_t slot = lo + i + lane, k = K + __popc(b & lower);
     if (i + lane < w1) {
-      if (slot < m && !kept) dst_list[slot - k] = slot;
-      if (slot >= m && kept) src_list[k - Km] = slot;
-      if (slot < m && kept) {
-        if (copy_w) wo[slot] = w[slot];
-        if (copy_p) po[slot] = pos[slot];
-      }
+      if (slot < m && !kept) list[slot - k] = slot;
+      if (slot >= m && kept) list[cap / 2 + k - Km] = slot;
+      keys[i + lane] = kept;
     }
     K += __popc(b);
   }
-  // every list entry is written, and no CTA reads another's shared memory any more
-  if (ranks > 1)
-    cluster.sync();
-  else
-    __syncthreads();
-  if (rank == 0 && tid == 0) a.lens_out[r] = m;
-
-  // ---- move
-  constexpr int kPiece = D / 8;                  // lanes of one key (or value) row
-  constexpr int kPer = 32 / (2 * kPiece);        // tokens of one step
-  constexpr int kGroup = kSteps * kPer;
-  const int32_t* table = a.c.table + r * a.c.max_pages;
-  const bool is_v = (lane / kPiece) & 1;
-  const int sub = lane / (2 * kPiece);
-  const int64_t stride = is_v ? a.c.v_page_stride : a.c.k_page_stride;
-  __nv_bfloat16* pool =
-      static_cast<__nv_bfloat16*>(is_v ? a.c.v_pages : a.c.k_pages) + (lane % kPiece) * 8;
-  for (int32_t g = (rank * kWarps + warp) * kGroup; g < pairs; g += ranks * kWarps * kGroup) {
-    // lane i < kGroup: pair g + i
-    int32_t sp = -1, tp = -1, so = 0, to = 0;
-    if (lane < kGroup && g + lane < pairs) {
-      const int32_t s = src_list[g + lane], x = dst_list[g + lane];
-      sp = table[s / a.c.page];
-      tp = table[x / a.c.page];
-      so = s % a.c.page;
-      to = x % a.c.page;
-      wo[x] = w[s];
-      if (po) po[x] = pos[s];
-      if (sp < 0 || sp >= a.c.num_pages || tp < 0 || tp >= a.c.num_pages) {
-        atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
-        sp = -1;
+  // the kept slots that stay, where the new state is another array
+  if (copy_w || copy_p) {
+    __syncwarp();
+    const int32_t end = min(w1, m - lo);
+#pragma unroll 4
+    for (int32_t i = w0 + lane; i < end; i += 32) {
+      if (keys[i]) {
+        if (copy_w) wo[lo + i] = w[lo + i];
+        if (copy_p) po[lo + i] = pos[lo + i];
       }
     }
-    uint4 val[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int32_t p = __shfl_sync(0xffffffffu, sp, i * kPer + sub);
-      const int32_t x = __shfl_sync(0xffffffffu, so, i * kPer + sub);
-      if (p >= 0) val[i] = *reinterpret_cast<const uint4*>(pool + p * stride + int64_t(x) * D);
-    }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const bool ok = __shfl_sync(0xffffffffu, sp, i * kPer + sub) >= 0;
-      const int32_t p = __shfl_sync(0xffffffffu, tp, i * kPer + sub);
-      const int32_t x = __shfl_sync(0xffffffffu, to, i * kPer + sub);
-      if (ok) *reinterpret_cast<uint4*>(pool + p * stride + int64_t(x) * D) = val[i];
-    }
   }
+  cluster.sync();                      // no CTA leaves while another reads its counts
 }
 
 template <int D>
 cudaError_t launch(const EvictArgs& a, int sms, cudaStream_t st) {
   const int64_t cap = int64_t(a.c.page) * a.c.max_pages;
   const int64_t rows = int64_t(a.c.batch) * a.c.num_kv_heads;
-  // the least CTAs a row that hold its keys, then more while processors are
-  // left and a slice is worth a CTA's while
-  int ranks = 1;
-  while (ranks < 8 && ((cap + ranks - 1) / ranks > kMaxSlice ||
-                       (rows * ranks < 2 * sms && cap / ranks > 1024)))
-    ranks *= 2;
-  const int64_t slice = ((cap + ranks - 1) / ranks + 31) & ~int64_t(31);
-  if (rows * ranks > INT32_MAX) return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = sa_paged::allow_shared(evict_kernel<D>, kMaxSlice * 4, done);
-  if (e != cudaSuccess) return e;
+  // the most moves that a row can have: no more than it keeps, or loses
+  int64_t most = 0;
+  for (int32_t g = 0; g < a.c.num_kv_heads; ++g)
+    most = std::max(most, std::min<int64_t>(a.keep[g], cap - std::min<int64_t>(a.keep[g], cap)));
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(rows * ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(slice) * 4;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(ranks);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel<D>, a);
+  cfg.blockDim = dim3(kThreads);
+  cudaError_t e;
+  if (cap <= kRowSlots) {
+    // one launch where the rows fill the processors, or have little to move
+    const bool moves_here = rows >= sms || most <= 1024;
+    cfg.gridDim = dim3(unsigned(rows));
+    e = cudaLaunchKernelEx(&cfg, evict_row_kernel<D>, a, int(moves_here));
+    if (e != cudaSuccess || moves_here) return e;
+  } else {
+    // the least CTAs a row that hold its keys, then more while processors are
+    // left and a slice is worth a CTA's while
+    int ranks = 2;
+    while (ranks < kMaxRanks && ((cap + ranks - 1) / ranks > kMaxSlice ||
+                                 (rows * ranks < 2 * sms && cap / ranks > 2048)))
+      ranks *= 2;
+    const int64_t slice = ((cap + ranks - 1) / ranks + 31) & ~int64_t(31);
+    if (rows * ranks > INT32_MAX) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    e = sa_paged::allow_shared(evict_cluster_kernel, kMaxSlice * 4, done);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(unsigned(rows * ranks));
+    cfg.dynamicSmemBytes = size_t(slice) * 4;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, evict_cluster_kernel, a);
+    if (e != cudaSuccess) return e;
+  }
+  constexpr int kPiece = kMoveThreads / 32 * Mover<D>::kGroup;
+  const int64_t pieces = (most + kPiece - 1) / kPiece;
+  if (pieces == 0) return cudaSuccess;
+  if (rows * pieces > INT32_MAX) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(unsigned(rows * pieces));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, move_kernel<D>, a, int32_t(pieces));
 }
 
 }  // namespace
 
 namespace sa_paged {
 
-// Two lists of at most cap / 2 slots a row.
 size_t evict_workspace(const sa_paged_cache& c) {
-  return size_t(c.batch) * c.num_kv_heads * c.page * c.max_pages * sizeof(int32_t);
+  const int64_t rows = int64_t(c.batch) * c.num_kv_heads;
+  return (size_t((rows + 63) & ~int64_t(63)) + size_t(rows) * c.page * c.max_pages) *
+         sizeof(int32_t);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
