@@ -20,8 +20,8 @@
 // Its time is a chain of latencies, not of bytes, so it has as few barriers as
 // it can: digits of 11 bits, histograms cleared ahead, lists in shared memory.
 // Longer rows: a cluster of 2 to 8 CTAs, each with a contiguous slice whose
-// keys stay in its shared memory; histograms of 8 bits and counts are added up
-// over the cluster through distributed shared memory (evict_cluster_kernel).
+// keys stay in its shared memory; histograms and counts are added up over the
+// cluster through distributed shared memory (evict_cluster_kernel).
 // The moves of a short row are made by its own CTA; those of long rows, or of
 // few rows with much to move, by a second launch over all processors
 // (move_kernel).
@@ -48,6 +48,7 @@ constexpr int kRowKeys = 16;           // keys of a thread where a CTA has the w
 constexpr int kRowSlots = kThreads * kRowKeys;
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
+constexpr int kMaxRanks = 8;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -119,25 +120,114 @@ struct Mover {
   }
 };
 
-// ---------------------------------------------------------------- one CTA a row
-struct RowShared {
-  int32_t hist[3][kBins];
-  uint16_t dst[kRowSlots / 2], src[kRowSlots / 2];
+// What the select of a row shares.  Three histograms, cleared ahead, one for
+// each digit.
+struct Select {
+  alignas(16) int32_t hist[3][kBins];
   int32_t warp_total[kWarps];
-  int32_t warp_count[kWarps][2];
-  int32_t newest;
   int32_t bin, need, count;
 };
 
+__device__ __forceinline__ void clear(Select& sel) {
+  int4* h = reinterpret_cast<int4*>(&sel.hist[0][0]);
+#pragma unroll
+  for (int x = 0; x < 3 * kBins / 4 / kThreads; ++x)
+    h[threadIdx.x + x * kThreads] = make_int4(0, 0, 0, 0);
+}
+
+// The `need`-th largest key, by digits of 11, 11 and 10 bits.  each(f) calls
+// f(key) for this thread's keys; with kCluster the CTAs of the cluster hold
+// parts of the row and all find the same.  Returns T, and in `need` how many
+// of the keys equal to T are kept; tied = false: all of them (T's lower bits
+// are then zero where a whole bin is kept, and a key is kept if it is >= T).
+template <bool kCluster, class Each>
+__device__ __forceinline__ uint32_t radix_select(Select& sel, int ranks, Each each, int32_t& need,
+                                                 bool& tied) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kMine = kBins / kThreads;            // bins of a thread
+  static_assert(kMine == 4, "an int4 of bins a thread");
+  uint32_t T = 0;
+  tied = true;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+    int32_t* hist = sel.hist[pass];
+    each([&](uint32_t k) {
+      if (((k ^ T) & mask) == 0) atomicAdd(&hist[(k >> shift) & digit], 1);
+    });
+    if (kCluster)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+    // thread x has the x-th four bins from the top
+    const int at = kBins / 4 - 1 - tid;
+    int4 c = make_int4(0, 0, 0, 0);
+    if (kCluster) {
+#pragma unroll
+      for (int x = 0; x < kMaxRanks; ++x) {
+        if (x < ranks) {
+          const int4 y = reinterpret_cast<const int4*>(
+              cg::this_cluster().map_shared_rank(&sel, x)->hist[pass])[at];
+          c.x += y.x;
+          c.y += y.y;
+          c.z += y.z;
+          c.w += y.w;
+        }
+      }
+    } else {
+      c = reinterpret_cast<const int4*>(hist)[at];
+    }
+    const int32_t sum = (c.x + c.y) + (c.z + c.w);
+    int32_t before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) sel.warp_total[warp] = before;
+    before -= sum;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x)
+      if (x < warp) before += sel.warp_total[x];
+    if (before < need && before + sum >= need) {
+      int b = 4 * at + 3, n = c.w;
+      if (before + n < need) { before += n; --b; n = c.z; }
+      if (before + n < need) { before += n; --b; n = c.y; }
+      if (before + n < need) { before += n; --b; n = c.x; }
+      sel.bin = b;
+      sel.need = need - before;
+      sel.count = n;
+    }
+    __syncthreads();
+    T |= uint32_t(sel.bin) << shift;
+    need = sel.need;
+    if (sel.count == need) {
+      tied = false;
+      break;
+    }
+  }
+  return T;
+}
+
+// ---------------------------------------------------------------- one CTA a row
+struct RowShared {
+  Select sel;
+  uint16_t dst[kRowSlots / 2], src[kRowSlots / 2];
+  int32_t warp_count[kWarps][2];
+  int32_t newest;
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) evict_row_kernel(const __grid_constant__ EvictArgs a,
-                                                             int moves_here) {
+__global__ void __launch_bounds__(kThreads, 2)
+    evict_row_kernel(const __grid_constant__ EvictArgs a, int moves_here) {
   __shared__ RowShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   sa_dev::launch_dependents();
   if (tid == 0) sh.newest = INT32_MIN;
-#pragma unroll
-  for (int x = tid; x < 3 * kBins; x += kThreads) (&sh.hist[0][0])[x] = 0;
+  clear(sh.sel);
   __syncthreads();
   sa_dev::wait_dependency();
   const int64_t r = blockIdx.x;
@@ -166,96 +256,81 @@ __global__ void __launch_bounds__(kThreads, 2) evict_row_kernel(const __grid_con
   const int per = (n + kThreads - 1) / kThreads;       // steps
   const int32_t w0 = warp * per * 32 + lane;           // this lane's first slot
   uint32_t key[kRowKeys];
-  int32_t q[kRowKeys];
-  int32_t newest = INT32_MIN;
+  uint32_t live = 0;                   // bit j: slot j of this lane is in the row
+  {
+    float x[kRowKeys];
+    int32_t q[kRowKeys];
 #pragma unroll
-  for (int j = 0; j < kRowKeys; ++j) {
-    const int32_t t = w0 + j * 32;
-    key[j] = 0;
-    q[j] = INT32_MIN;
-    if (j < per && t < n) {
-      key[j] = weight_key(w[t]);
-      q[j] = pos ? pos[t] : t;
+    for (int j = 0; j < kRowKeys; ++j) {
+      if (j >= per) break;
+      const int32_t t = w0 + j * 32;
+      x[j] = 0.f;
+      q[j] = INT32_MIN;
+      if (t < n) {
+        x[j] = w[t];
+        q[j] = pos ? pos[t] : t;
+        live |= 1u << j;
+      }
+    }
+    int32_t newest = INT32_MIN;
+#pragma unroll
+    for (int j = 0; j < kRowKeys; ++j) {
+      if (j >= per) break;
+      newest = max(newest, q[j]);
+    }
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) atomicMax(&sh.newest, newest);
+    // the new state's slots, as they are: moves overwrite the holes later
+    if (copy_w || copy_p) {
+#pragma unroll
+      for (int j = 0; j < kRowKeys; ++j) {
+        if (j >= per) break;
+        const int32_t t = w0 + j * 32;
+        if (t < m) {
+          if (copy_w) wo[t] = x[j];
+          if (copy_p) po[t] = q[j];
+        }
+      }
+    }
+    __syncthreads();
+    newest = sh.newest;
+#pragma unroll
+    for (int j = 0; j < kRowKeys; ++j) {
+      if (j >= per) break;
+      key[j] = is_forced(a, q[j], newest) ? 0xFFFFFFFFu : weight_key(x[j]);
     }
   }
-#pragma unroll
-  for (int j = 0; j < kRowKeys; ++j) newest = max(newest, q[j]);
-  newest = __reduce_max_sync(0xffffffffu, newest);
-  if (lane == 0) atomicMax(&sh.newest, newest);
-  __syncthreads();
-  newest = sh.newest;
-  uint32_t live = 0;                   // bit j: slot j of this lane is in the row
-#pragma unroll
-  for (int j = 0; j < kRowKeys; ++j)
-    if (j < per && w0 + j * 32 < n) {
-      live |= 1u << j;
-      if (is_forced(a, q[j], newest)) key[j] = 0xFFFFFFFFu;
-    }
 
   // ---- select
-  uint32_t T = 0;
-  int32_t need = m;                    // of the keys that agree with T so far
-  bool tied = true;                    // more keys equal T than are kept
+  int32_t need = m;
+  bool tied;
+  const uint32_t T = radix_select<false>(
+      sh.sel, 1,
+      [&](auto f) {
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bins = pass == 2 ? 1024 : 2048;
-    const int mine = bins / kThreads;
-    int32_t* hist = sh.hist[pass];
-#pragma unroll
-    for (int j = 0; j < kRowKeys; ++j)
-      if ((live >> j & 1u) && (pass == 0 || (key[j] ^ T) >> (pass == 1 ? 21 : 10) == 0))
-        atomicAdd(&hist[(key[j] >> shift) & (bins - 1)], 1);
-    __syncthreads();
-    // thread x has the x-th group of bins from the top
-    int32_t c[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < mine; ++i) {
-      c[i] = hist[bins - 1 - (tid * mine + i)];
-      sum += c[i];
-    }
-    int32_t before = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t x = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += x;
-    }
-    if (lane == 31) sh.warp_total[warp] = before;
-    before -= sum;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x)
-      if (x < warp) before += sh.warp_total[x];
-#pragma unroll
-    for (int i = 0; i < mine; ++i) {
-      if (before < need && before + c[i] >= need) {
-        sh.bin = bins - 1 - (tid * mine + i);
-        sh.need = need - before;
-        sh.count = c[i];
-      }
-      before += c[i];
-    }
-    __syncthreads();
-    T |= uint32_t(sh.bin) << shift;
-    need = sh.need;
-    if (sh.count == need) {
-      tied = false;
-      break;
-    }
-  }
+        for (int j = 0; j < kRowKeys; ++j) {
+          if (j >= per) break;
+          if (live >> j & 1u) f(key[j]);
+        }
+      },
+      need, tied);
 
   // ---- number
   const uint32_t lower = (1u << lane) - 1u;
   uint32_t kept = 0;                   // bit j
   if (!tied) {
 #pragma unroll
-    for (int j = 0; j < kRowKeys; ++j)
+    for (int j = 0; j < kRowKeys; ++j) {
+      if (j >= per) break;
       if ((live >> j & 1u) && key[j] >= T) kept |= 1u << j;
+    }
   } else {
     int32_t ties = 0;
 #pragma unroll
-    for (int j = 0; j < kRowKeys; ++j)
+    for (int j = 0; j < kRowKeys; ++j) {
+      if (j >= per) break;
       ties += __popc(__ballot_sync(0xffffffffu, (live >> j & 1u) && key[j] == T));
+    }
     if (lane == 0) sh.warp_count[warp][0] = ties;
     __syncthreads();
     int32_t t = 0;
@@ -264,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_row_kernel(const __grid_con
       if (x < warp) t += sh.warp_count[x][0];
 #pragma unroll
     for (int j = 0; j < kRowKeys; ++j) {
+      if (j >= per) break;
       const bool in = live >> j & 1u, eq = in && key[j] == T;
       const uint32_t b = __ballot_sync(0xffffffffu, eq);
       if (in && (key[j] > T || (eq && t + __popc(b & lower) < need))) kept |= 1u << j;
@@ -271,12 +347,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_row_kernel(const __grid_con
     }
     __syncthreads();
   }
-  int32_t count = 0, low = 0;          // kept slots of the warp, and those below m
-#pragma unroll
-  for (int j = 0; j < kRowKeys; ++j) {
-    count += __popc(__ballot_sync(0xffffffffu, kept >> j & 1u));
-    low += __popc(__ballot_sync(0xffffffffu, (kept >> j & 1u) && w0 + j * 32 < m));
-  }
+  // kept slots of the warp, and those below m; `low` has this lane's share
+  const int below = min(max((m - w0 + 31) >> 5, 0), per);      // this lane's slots below m
+  int32_t low = __reduce_add_sync(0xffffffffu, __popc(kept & ((1u << below) - 1u)));
+  const int32_t count = __reduce_add_sync(0xffffffffu, __popc(kept));
   if (lane == 0) {
     sh.warp_count[warp][0] = count;
     sh.warp_count[warp][1] = low;
@@ -290,32 +364,24 @@ __global__ void __launch_bounds__(kThreads, 2) evict_row_kernel(const __grid_con
   }
   const int32_t pairs = m - Km;
   int32_t* list = ws.lists + r * cap;
-#pragma unroll
-  for (int j = 0; j < kRowKeys; ++j) {
-    if (j < per) {
-      const uint32_t b = __ballot_sync(0xffffffffu, kept >> j & 1u);
-      const int32_t t = w0 + j * 32, k = K + __popc(b & lower);
-      if (live >> j & 1u) {
-        const bool keep = kept >> j & 1u;
-        if (t < m && !keep) {
-          if (moves_here)
-            sh.dst[t - k] = uint16_t(t);
-          else
-            list[t - k] = t;
-        }
-        if (t >= m && keep) {
-          if (moves_here)
-            sh.src[k - Km] = uint16_t(t);
-          else
-            list[cap / 2 + k - Km] = t;
-        }
-        if (t < m && keep) {
-          if (copy_w) wo[t] = w[t];
-          if (copy_p) po[t] = pos[t];
-        }
-      }
-      K += __popc(b);
+#pragma unroll 1
+  for (int j = 0; j < per; ++j) {
+    const bool keep = kept >> j & 1u;
+    const uint32_t b = __ballot_sync(0xffffffffu, keep);
+    const int32_t t = w0 + j * 32, k = K + __popc(b & lower);
+    if (t < m && !keep) {
+      if (moves_here)
+        sh.dst[t - k] = uint16_t(t);
+      else
+        list[t - k] = t;
     }
+    if (t >= m && keep) {
+      if (moves_here)
+        sh.src[k - Km] = uint16_t(t);
+      else
+        list[cap / 2 + k - Km] = t;
+    }
+    K += __popc(b);
   }
   if (tid == 0) {
     a.lens_out[r] = m;
@@ -351,14 +417,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- a cluster a row
-constexpr int kMaxRanks = 8;
-
 struct Shared {
-  int32_t hist[2][256];    // by pass parity: the other CTAs may still read the last one
+  Select sel;
   int32_t warp_count[kWarps][2];
-  int32_t bins[8];
   int32_t share[3][2];     // [0] largest position; [1] ties; [2] kept, kept below m
-  int32_t bin, need, count;
 };
 
 // Sum over the CTA of (x, y), by every thread; each warp passes its own counts
@@ -394,6 +456,7 @@ __global__ void __launch_bounds__(kThreads)
   const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   sa_dev::launch_dependents();
+  clear(sh.sel);
   sa_dev::wait_dependency();
   const int64_t r = blockIdx.x / ranks;
   const int32_t cap = a.c.page * a.c.max_pages;
@@ -424,12 +487,33 @@ __global__ void __launch_bounds__(kThreads)
   const int32_t part = ((slice + kWarps - 1) / kWarps + 31) & ~31;
   const int32_t w0 = min(ns, warp * part), w1 = min(ns, w0 + part);
 
-  // ---- keys
+  // ---- keys, and the new state's slots as they are: moves overwrite the
+  // holes later
   int32_t newest = pos ? INT32_MIN : n - 1;
-#pragma unroll 8
-  for (int32_t i = tid; i < ns; i += kThreads) {
-    keys[i] = weight_key(w[lo + i]);
-    if (pos) newest = max(newest, pos[lo + i]);
+  constexpr int kBatch = 8;
+  for (int32_t i0 = tid; i0 < ns; i0 += kBatch * kThreads) {
+    float x[kBatch];
+    int32_t q[kBatch];
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int32_t i = i0 + y * kThreads;
+      if (i < ns) {
+        x[y] = w[lo + i];
+        q[y] = pos ? pos[lo + i] : lo + i;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int32_t i = i0 + y * kThreads;
+      if (i < ns) {
+        keys[i] = weight_key(x[y]);
+        newest = max(newest, q[y]);
+        if (lo + i < m) {
+          if (copy_w) wo[lo + i] = x[y];
+          if (copy_p) po[lo + i] = q[y];
+        }
+      }
+    }
   }
   if (pos && a.recent > 0) {
     newest = __reduce_max_sync(0xffffffffu, newest);
@@ -444,58 +528,41 @@ __global__ void __launch_bounds__(kThreads)
       if (x < ranks) newest = max(newest, cluster.map_shared_rank(&sh, x)->share[0][0]);
   }
   if (a.sinks > 0 || a.recent > 0) {
-#pragma unroll 8
-    for (int32_t i = tid; i < ns; i += kThreads)
-      if (is_forced(a, pos ? pos[lo + i] : lo + i, newest)) keys[i] = 0xFFFFFFFFu;
+    for (int32_t i0 = tid; i0 < ns; i0 += kBatch * kThreads) {
+      int32_t q[kBatch];
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const int32_t i = i0 + y * kThreads;
+        if (i < ns) q[y] = pos ? pos[lo + i] : lo + i;
+      }
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const int32_t i = i0 + y * kThreads;
+        if (i < ns && is_forced(a, q[y], newest)) keys[i] = 0xFFFFFFFFu;
+      }
+    }
   }
+  __syncthreads();                     // histograms are clear, keys complete
 
   // ---- select
-  uint32_t T = 0;
-  int32_t need = m;                    // of the keys that agree with T so far
-  bool tied = true;                    // more keys equal T than are kept
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    int32_t* hist = sh.hist[pass & 1];
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
-#pragma unroll 8
-    for (int32_t i = tid; i < ns; i += kThreads) {
-      const uint32_t k = keys[i];
-      if (((k ^ T) & mask) == 0) atomicAdd(&hist[(k >> shift) & 255u], 1);
-    }
-    cluster.sync();
-    int32_t mine = 0, above = 0;
-    if (tid < 256) {
-      // thread x has bin 255 - x, so that a prefix sum counts from the top
+  int32_t need = m;
+  bool tied;
+  const uint32_t T = radix_select<true>(
+      sh.sel, ranks,
+      [&](auto f) {
+        for (int32_t i0 = tid; i0 < ns; i0 += kBatch * kThreads) {
+          uint32_t k[kBatch];
 #pragma unroll
-      for (int x = 0; x < kMaxRanks; ++x)
-        if (x < ranks) mine += cluster.map_shared_rank(&sh, x)->hist[pass & 1][255 - tid];
-      above = mine;
+          for (int y = 0; y < kBatch; ++y) {
+            const int32_t i = i0 + y * kThreads;
+            if (i < ns) k[y] = keys[i];
+          }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t x = __shfl_up_sync(0xffffffffu, above, o);
-        if (lane >= o) above += x;
-      }
-      if (lane == 31) sh.bins[warp] = above;
-    }
-    __syncthreads();
-    if (tid < 256) {
-      for (int x = 0; x < warp; ++x) above += sh.bins[x];
-      if (above >= need && above - mine < need) {
-        sh.bin = 255 - tid;
-        sh.need = need - (above - mine);
-        sh.count = mine;
-      }
-    }
-    __syncthreads();
-    T |= uint32_t(sh.bin) << shift;
-    need = sh.need;
-    if (sh.count == need) {            // the same in every CTA of the cluster
-      tied = false;
-      break;
-    }
-  }
+          for (int y = 0; y < kBatch; ++y)
+            if (i0 + y * kThreads < ns) f(k[y]);
+        }
+      },
+      need, tied);
 
   // ---- number: ties in slot order where they matter, then kept slots
   const uint32_t lower = (1u << lane) - 1u;
@@ -513,28 +580,28 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int x = 0; x < kMaxRanks; ++x)
       if (x < rank) tie += cluster.map_shared_rank(&sh, x)->share[1][0];
-  } else {
-    __syncthreads();                   // the keys of other threads are read next
   }
-  // whether slot i of the slice is kept; t runs over the ties before the warp's place
-  auto kept_at = [&](int32_t i, int32_t& t) -> bool {
-    const uint32_t k = i + lane < w1 ? keys[i + lane] : 0u;
-    if (!tied) return i + lane < w1 && k >= T;
-    const bool eq = i + lane < w1 && k == T;
-    const uint32_t b = __ballot_sync(0xffffffffu, eq);
-    const bool kept = i + lane < w1 && (k > T || (eq && t + __popc(b & lower) < need));
-    t += __popc(b);
-    return kept;
-  };
-  int2 count = make_int2(0, 0);
+  // a warp's own slots become flags: kept or not
+  int32_t count = 0, low = 0;
   int32_t t = tie;
+#pragma unroll 4
   for (int32_t i = w0; i < w1; i += 32) {
-    const uint32_t b = __ballot_sync(0xffffffffu, kept_at(i, t));
-    count.x += __popc(b);
-    const int32_t below = m - (lo + i);          // slots of this step below m
-    count.y += below >= 32 ? __popc(b) : below > 0 ? __popc(b & ((1u << below) - 1u)) : 0;
+    const bool in = i + lane < w1;
+    const uint32_t k = in ? keys[i + lane] : 0u;
+    bool kept = in && k >= T;
+    if (tied) {
+      const bool eq = in && k == T;
+      const uint32_t b = __ballot_sync(0xffffffffu, eq);
+      kept = in && (k > T || (eq && t + __popc(b & lower) < need));
+      t += __popc(b);
+    }
+    if (in) keys[i + lane] = kept;
+    count += kept;
+    low += kept && lo + i + lane < m;
   }
-  int32_t K = before_in_block(sh, count, total).x;
+  count = __reduce_add_sync(0xffffffffu, count);
+  low = __reduce_add_sync(0xffffffffu, low);
+  int32_t K = before_in_block(sh, make_int2(count, low), total).x;
   if (tid == 0) {
     sh.share[2][0] = total.x;
     sh.share[2][1] = total.y;
@@ -554,29 +621,15 @@ __global__ void __launch_bounds__(kThreads)
     ws.pairs[r] = m - Km;
   }
   int32_t* list = ws.lists + r * cap;
-  t = tie;
+#pragma unroll 4
   for (int32_t i = w0; i < w1; i += 32) {
-    const bool kept = kept_at(i, t);
+    const bool in = i + lane < w1;
+    const bool kept = in && keys[i + lane];
     const uint32_t b = __ballot_sync(0xffffffffu, kept);
     const int32_t slot = lo + i + lane, k = K + __popc(b & lower);
-    if (i + lane < w1) {
-      if (slot < m && !kept) list[slot - k] = slot;
-      if (slot >= m && kept) list[cap / 2 + k - Km] = slot;
-      keys[i + lane] = kept;
-    }
+    if (in && slot < m && !kept) list[slot - k] = slot;
+    if (in && slot >= m && kept) list[cap / 2 + k - Km] = slot;
     K += __popc(b);
-  }
-  // the kept slots that stay, where the new state is another array
-  if (copy_w || copy_p) {
-    __syncwarp();
-    const int32_t end = min(w1, m - lo);
-#pragma unroll 4
-    for (int32_t i = w0 + lane; i < end; i += 32) {
-      if (keys[i]) {
-        if (copy_w) wo[lo + i] = w[lo + i];
-        if (copy_p) po[lo + i] = pos[lo + i];
-      }
-    }
   }
   cluster.sync();                      // no CTA leaves while another reads its counts
 }
@@ -600,7 +653,7 @@ cudaError_t launch(const EvictArgs& a, int sms, cudaStream_t st) {
   cudaError_t e;
   if (cap <= kRowSlots) {
     // one launch where the rows fill the processors, or have little to move
-    const bool moves_here = rows >= sms || most <= 1024;
+    const bool moves_here = rows >= sms || most <= 256;
     cfg.gridDim = dim3(unsigned(rows));
     e = cudaLaunchKernelEx(&cfg, evict_row_kernel<D>, a, int(moves_here));
     if (e != cudaSuccess || moves_here) return e;
