@@ -31,6 +31,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <utility>
 
 #include "paged.h"
 #include "ptx.cuh"
@@ -120,8 +121,8 @@ struct Mover {
   }
 };
 
-// What the select of a row shares.  Three histograms, cleared ahead, one for
-// each digit.
+// What the select of a row shares.  Three histograms of the row, cleared
+// ahead, one for each digit.
 struct Select {
   alignas(16) int32_t hist[3][kBins];
   int32_t warp_total[kWarps];
@@ -136,13 +137,15 @@ __device__ __forceinline__ void clear(Select& sel) {
 }
 
 // The `need`-th largest key, by digits of 11, 11 and 10 bits.  each(f) calls
-// f(key) for this thread's keys; with kCluster the CTAs of the cluster hold
-// parts of the row and all find the same.  Returns T, and in `need` how many
+// f(key) for this thread's keys.  With kCluster the CTAs of the cluster hold
+// parts of the row and all find the same: each counts into `local` (cleared)
+// and adds what is not zero to every CTA's histogram (reading all of the
+// others' bins took 10000 cycles a digit).  Returns T, and in `need` how many
 // of the keys equal to T are kept; tied = false: all of them (T's lower bits
 // are then zero where a whole bin is kept, and a key is kept if it is >= T).
 template <bool kCluster, class Each>
-__device__ __forceinline__ uint32_t radix_select(Select& sel, int ranks, Each each, int32_t& need,
-                                                 bool& tied) {
+__device__ __forceinline__ uint32_t radix_select(Select& sel, int32_t* local, int ranks, Each each,
+                                                 int32_t& need, bool& tied) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kMine = kBins / kThreads;            // bins of a thread
   static_assert(kMine == 4, "an int4 of bins a thread");
@@ -153,32 +156,29 @@ __device__ __forceinline__ uint32_t radix_select(Select& sel, int ranks, Each ea
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digit = pass == 2 ? 1023u : 2047u;
     const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-    int32_t* hist = sel.hist[pass];
+    int32_t* hist = kCluster ? local : sel.hist[pass];
     each([&](uint32_t k) {
       if (((k ^ T) & mask) == 0) atomicAdd(&hist[(k >> shift) & digit], 1);
     });
-    if (kCluster)
-      cg::this_cluster().sync();
-    else
-      __syncthreads();
+    __syncthreads();
     // thread x has the x-th four bins from the top
     const int at = kBins / 4 - 1 - tid;
-    int4 c = make_int4(0, 0, 0, 0);
     if (kCluster) {
-#pragma unroll
-      for (int x = 0; x < kMaxRanks; ++x) {
-        if (x < ranks) {
-          const int4 y = reinterpret_cast<const int4*>(
-              cg::this_cluster().map_shared_rank(&sel, x)->hist[pass])[at];
-          c.x += y.x;
-          c.y += y.y;
-          c.z += y.z;
-          c.w += y.w;
+      int4* part = reinterpret_cast<int4*>(local) + at;
+      const int4 y = *part;
+      *part = make_int4(0, 0, 0, 0);
+      if (y.x | y.y | y.z | y.w) {
+        for (int x = 0; x < ranks; ++x) {
+          int32_t* to = cg::this_cluster().map_shared_rank(&sel, x)->hist[pass] + 4 * at;
+          if (y.x) atomicAdd(to, y.x);
+          if (y.y) atomicAdd(to + 1, y.y);
+          if (y.z) atomicAdd(to + 2, y.z);
+          if (y.w) atomicAdd(to + 3, y.w);
         }
       }
-    } else {
-      c = reinterpret_cast<const int4*>(hist)[at];
+      cg::this_cluster().sync();
     }
+    const int4 c = reinterpret_cast<const int4*>(sel.hist[pass])[at];
     const int32_t sum = (c.x + c.y) + (c.z + c.w);
     int32_t before = sum;
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   int32_t need = m;
   bool tied;
   const uint32_t T = radix_select<false>(
-      sh.sel, 1,
+      sh.sel, nullptr, 1,
       [&](auto f) {
 #pragma unroll
         for (int j = 0; j < kRowKeys; ++j) {
@@ -419,8 +419,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 // ---------------------------------------------------------------- a cluster a row
 struct Shared {
   Select sel;
+  alignas(16) int32_t local[kBins];
   int32_t warp_count[kWarps][2];
-  int32_t share[3][2];     // [0] largest position; [1] ties; [2] kept, kept below m
+  // what every CTA of the cluster writes into each
+  int32_t newest;
+  int32_t ties[kMaxRanks], kept[kMaxRanks], low[kMaxRanks];
 };
 
 // Sum over the CTA of (x, y), by every thread; each warp passes its own counts
@@ -457,6 +460,9 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   sa_dev::launch_dependents();
   clear(sh.sel);
+  reinterpret_cast<int4*>(sh.local)[tid] = make_int4(0, 0, 0, 0);
+  if (tid == 0) sh.newest = INT32_MIN;
+  auto ready = cluster.barrier_arrive();       // cleared, for the others to write
   sa_dev::wait_dependency();
   const int64_t r = blockIdx.x / ranks;
   const int32_t cap = a.c.page * a.c.max_pages;
@@ -478,6 +484,7 @@ __global__ void __launch_bounds__(kThreads)
       a.lens_out[r] = m;
       ws.pairs[r] = 0;
     }
+    cluster.barrier_wait(std::move(ready));
     return;
   }
 
@@ -515,17 +522,18 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
+  cluster.barrier_wait(std::move(ready));
   if (pos && a.recent > 0) {
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) sh.warp_count[warp][0] = newest;
     __syncthreads();
+    if (tid < ranks) {
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) newest = max(newest, sh.warp_count[x][0]);
-    if (tid == 0) sh.share[0][0] = newest;
+      for (int x = 0; x < kWarps; ++x) newest = max(newest, sh.warp_count[x][0]);
+      atomicMax(&cluster.map_shared_rank(&sh, tid)->newest, newest);
+    }
     cluster.sync();
-#pragma unroll
-    for (int x = 0; x < kMaxRanks; ++x)
-      if (x < ranks) newest = max(newest, cluster.map_shared_rank(&sh, x)->share[0][0]);
+    newest = sh.newest;
   }
   if (a.sinks > 0 || a.recent > 0) {
     for (int32_t i0 = tid; i0 < ns; i0 += kBatch * kThreads) {
@@ -542,13 +550,11 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  __syncthreads();                     // histograms are clear, keys complete
-
   // ---- select
   int32_t need = m;
   bool tied;
   const uint32_t T = radix_select<true>(
-      sh.sel, ranks,
+      sh.sel, sh.local, ranks,
       [&](auto f) {
         for (int32_t i0 = tid; i0 < ns; i0 += kBatch * kThreads) {
           uint32_t k[kBatch];
@@ -575,11 +581,9 @@ __global__ void __launch_bounds__(kThreads)
       ties += __popc(__ballot_sync(0xffffffffu, eq));
     }
     tie = before_in_block(sh, make_int2(ties, 0), total).x;
-    if (tid == 0) sh.share[1][0] = total.x;
+    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->ties[rank] = total.x;
     cluster.sync();
-#pragma unroll
-    for (int x = 0; x < kMaxRanks; ++x)
-      if (x < rank) tie += cluster.map_shared_rank(&sh, x)->share[1][0];
+    for (int x = 0; x < rank; ++x) tie += sh.ties[x];
   }
   // a warp's own slots become flags: kept or not
   int32_t count = 0, low = 0;
@@ -602,19 +606,15 @@ __global__ void __launch_bounds__(kThreads)
   count = __reduce_add_sync(0xffffffffu, count);
   low = __reduce_add_sync(0xffffffffu, low);
   int32_t K = before_in_block(sh, make_int2(count, low), total).x;
-  if (tid == 0) {
-    sh.share[2][0] = total.x;
-    sh.share[2][1] = total.y;
+  if (tid < ranks) {
+    cluster.map_shared_rank(&sh, tid)->kept[rank] = total.x;
+    cluster.map_shared_rank(&sh, tid)->low[rank] = total.y;
   }
-  cluster.sync();
+  cluster.sync();                      // the last access to another CTA's shared memory
   int32_t Km = 0;
-#pragma unroll
-  for (int x = 0; x < kMaxRanks; ++x) {
-    if (x < ranks) {
-      const Shared* other = cluster.map_shared_rank(&sh, x);
-      if (x < rank) K += other->share[2][0];
-      Km += other->share[2][1];
-    }
+  for (int x = 0; x < ranks; ++x) {
+    if (x < rank) K += sh.kept[x];
+    Km += sh.low[x];
   }
   if (rank == 0 && tid == 0) {
     a.lens_out[r] = m;
@@ -631,7 +631,6 @@ __global__ void __launch_bounds__(kThreads)
     if (in && slot >= m && kept) list[cap / 2 + k - Km] = slot;
     K += __popc(b);
   }
-  cluster.sync();                      // no CTA leaves while another reads its counts
 }
 
 template <int D>
