@@ -126,7 +126,7 @@ struct Mover {
 struct Select {
   alignas(16) int32_t hist[3][kBins];
   int32_t warp_total[kWarps];
-  int32_t bin, need, count;
+  alignas(16) int4 found;              // bin, how many of it are kept, how many it has
 };
 
 __device__ __forceinline__ void clear(Select& sel) {
@@ -138,14 +138,16 @@ __device__ __forceinline__ void clear(Select& sel) {
 
 // The `need`-th largest key, by digits of 11, 11 and 10 bits.  each(f) calls
 // f(key) for this thread's keys.  With kCluster the CTAs of the cluster hold
-// parts of the row and all find the same: each counts into `local` (cleared)
-// and adds what is not zero to every CTA's histogram (reading all of the
-// others' bins took 10000 cycles a digit).  Returns T, and in `need` how many
+// parts of the row: each counts into `local` (cleared) and adds what is not
+// zero to the first CTA's histogram, which finds the bin and tells the others.
+// (Every CTA reading all the others' bins took 10000 cycles a digit, every CTA
+// adding to all the others' 7700.)  Returns T, and in `need` how many
 // of the keys equal to T are kept; tied = false: all of them (T's lower bits
 // are then zero where a whole bin is kept, and a key is kept if it is >= T).
 template <bool kCluster, class Each>
-__device__ __forceinline__ uint32_t radix_select(Select& sel, int32_t* local, int ranks, Each each,
-                                                 int32_t& need, bool& tied) {
+__device__ __forceinline__ uint32_t radix_select(Select& sel, int32_t* local, int rank,
+                                                 int ranks, Each each, int32_t& need,
+                                                 bool& tied) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kMine = kBins / kThreads;            // bins of a thread
   static_assert(kMine == 4, "an int4 of bins a thread");
@@ -168,43 +170,49 @@ __device__ __forceinline__ uint32_t radix_select(Select& sel, int32_t* local, in
       const int4 y = *part;
       *part = make_int4(0, 0, 0, 0);
       if (y.x | y.y | y.z | y.w) {
-        for (int x = 0; x < ranks; ++x) {
-          int32_t* to = cg::this_cluster().map_shared_rank(&sel, x)->hist[pass] + 4 * at;
-          if (y.x) atomicAdd(to, y.x);
-          if (y.y) atomicAdd(to + 1, y.y);
-          if (y.z) atomicAdd(to + 2, y.z);
-          if (y.w) atomicAdd(to + 3, y.w);
-        }
+        int32_t* to = cg::this_cluster().map_shared_rank(&sel, 0)->hist[pass] + 4 * at;
+        if (y.x) atomicAdd(to, y.x);
+        if (y.y) atomicAdd(to + 1, y.y);
+        if (y.z) atomicAdd(to + 2, y.z);
+        if (y.w) atomicAdd(to + 3, y.w);
       }
       cg::this_cluster().sync();
     }
-    const int4 c = reinterpret_cast<const int4*>(sel.hist[pass])[at];
-    const int32_t sum = (c.x + c.y) + (c.z + c.w);
-    int32_t before = sum;
+    if (!kCluster || rank == 0) {
+      const int4 c = reinterpret_cast<const int4*>(sel.hist[pass])[at];
+      const int32_t sum = (c.x + c.y) + (c.z + c.w);
+      int32_t before = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t x = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += x;
-    }
-    if (lane == 31) sel.warp_total[warp] = before;
-    before -= sum;
-    __syncthreads();
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+      }
+      if (lane == 31) sel.warp_total[warp] = before;
+      before -= sum;
+      __syncthreads();
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x)
-      if (x < warp) before += sel.warp_total[x];
-    if (before < need && before + sum >= need) {
-      int b = 4 * at + 3, n = c.w;
-      if (before + n < need) { before += n; --b; n = c.z; }
-      if (before + n < need) { before += n; --b; n = c.y; }
-      if (before + n < need) { before += n; --b; n = c.x; }
-      sel.bin = b;
-      sel.need = need - before;
-      sel.count = n;
+      for (int x = 0; x < kWarps; ++x)
+        if (x < warp) before += sel.warp_total[x];
+      if (before < need && before + sum >= need) {
+        int b = 4 * at + 3, n = c.w;
+        if (before + n < need) { before += n; --b; n = c.z; }
+        if (before + n < need) { before += n; --b; n = c.y; }
+        if (before + n < need) { before += n; --b; n = c.x; }
+        const int4 f = make_int4(b, need - before, n, 0);
+        if (kCluster)
+          for (int x = 0; x < ranks; ++x) cg::this_cluster().map_shared_rank(&sel, x)->found = f;
+        else
+          sel.found = f;
+      }
     }
-    __syncthreads();
-    T |= uint32_t(sel.bin) << shift;
-    need = sel.need;
-    if (sel.count == need) {
+    if (kCluster)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+    const int4 f = sel.found;
+    T |= uint32_t(f.x) << shift;
+    need = f.y;
+    if (f.z == need) {
       tied = false;
       break;
     }
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   int32_t need = m;
   bool tied;
   const uint32_t T = radix_select<false>(
-      sh.sel, nullptr, 1,
+      sh.sel, nullptr, 0, 1,
       [&](auto f) {
 #pragma unroll
         for (int j = 0; j < kRowKeys; ++j) {
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kThreads)
   int32_t need = m;
   bool tied;
   const uint32_t T = radix_select<true>(
-      sh.sel, sh.local, ranks,
+      sh.sel, sh.local, rank, ranks,
       [&](auto f) {
         for (int32_t i0 = tid; i0 < ns; i0 += kBatch * kThreads) {
           uint32_t k[kBatch];
