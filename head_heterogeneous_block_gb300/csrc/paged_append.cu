@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace {
 
@@ -34,11 +35,13 @@ __device__ __forceinline__ int32_t new_tokens(const AppendArgs& a, int64_t r, in
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, int32_t chunks,
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ AppendArgs a, int32_t chunks,
                                                              int write_lens) {
   constexpr int kPiece = D / 8;                 // lanes of one key (or value) row
   constexpr int kPer = 32 / (2 * kPiece);       // tokens of one step
   constexpr int kTokens = kSteps * kPer;        // tokens of a warp
+  sa_dev::launch_dependents();
+  sa_dev::wait_dependency();
   const int lane = threadIdx.x & 31;
   const int64_t task = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t r = task / chunks;
@@ -94,7 +97,9 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
 }
 
 // lens += counts, in place, after the rows' warps have read them.
-__global__ void lens_kernel(const AppendArgs a) {
+__global__ void lens_kernel(const __grid_constant__ AppendArgs a) {
+  sa_dev::launch_dependents();
+  sa_dev::wait_dependency();
   const int64_t r = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (r >= int64_t(a.c.batch) * a.c.num_kv_heads) return;
   const int32_t cap = a.c.page * a.c.max_pages;
@@ -112,9 +117,20 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t blocks = (rows * chunks + kWarps - 1) / kWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const bool late = chunks > 1 && a.lens_out == a.c.lens;
-  append_kernel<D><<<unsigned(blocks), 32 * kWarps, 0, st>>>(a, int32_t(chunks), !late);
-  if (late) lens_kernel<<<unsigned((rows + 255) / 256), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, append_kernel<D>, a, int32_t(chunks), int(!late));
+  if (e != cudaSuccess || !late) return e;
+  cfg.gridDim = dim3(unsigned((rows + 255) / 256));
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, lens_kernel, a);
 }
 
 }  // namespace
