@@ -6,6 +6,9 @@ the computation runs in libsparse_attn's kernels.
                   configuration (the offline profile gives the demands).
 ``DecodeStep``    the same three calls for one decode step over an
                   HBM-resident cache, with the pooled key cache built once.
+``PagedDecodeLayer``  decode over a paged cache whose sequences have lengths of
+                  their own and whose KV heads keep budgets of their own:
+                  append, attend and evict.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ from . import (SA_HEAD_RETRIEVAL, SA_HEAD_STREAMING, Shape, sparse_attn_forward,
                sparse_attn_score_select, sparse_attn_score_workspace_size, sparse_attn_select,
                sparse_attn_decode_step,
                sparse_attn_select_kind)
+from .paged import PageBook, PagedCache
 
 
 class PrefillLayer:
@@ -253,3 +257,124 @@ class HostPipeline:
         self.copy_out.synchronize()
         self.copy_in.synchronize()
         comp.synchronize()
+
+
+def kv_budgets(plan, tokens_per_block: int) -> list:
+    """Tokens that each KV head keeps so that every query head of its group has
+    its block budget: the largest budget of the group, in tokens."""
+    shape = plan.shape
+    budgets = plan.get()["budgets"].reshape(shape.num_kv_heads, -1)
+    return [int(b) * tokens_per_block for b in budgets.max(axis=1)]
+
+
+class PagedDecodeLayer:
+    """One layer's decode over a paged key-value cache.
+
+    Sequences are admitted (``admit``), stepped together (``step``) and
+    released; each KV head g keeps at most ``keep[g]`` tokens of a sequence
+    (budgets of a plan: ``kv_budgets``), or all with ``keep=None``.  A step
+    appends the new token, attends, and adds the attention probabilities to the
+    tokens' weights; once any row holds ``slack`` tokens more than its budget,
+    the rows are cut back to their budgets: the first ``sinks`` positions, the
+    last ``recent`` ones, then the largest weights stay.  Pages that rows give
+    up serve others.
+
+    Calls are ordered on one stream: the current one, or the one of the
+    caller's ``with torch.cuda.stream``."""
+
+    def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page: int,
+                 num_pages: int, max_tokens: int, keep=None, slack: int = 0, sinks: int = 4,
+                 recent: int = 16, device="cuda", out_dtype=torch.bfloat16):
+        if max_tokens < 1 or slack < 0:
+            raise ValueError("max_tokens must be positive, slack not negative")
+        if keep is not None and (len(keep) != num_kv_heads or min(keep) < sinks + recent):
+            raise ValueError("keep must hold at least sinks + recent tokens per KV head")
+        dev = torch.device(device)
+        self.keep, self.slack, self.sinks, self.recent = keep, slack, sinks, recent
+        max_pages = -(-max_tokens // page)
+        slots = (batch, num_kv_heads, max_pages * page)
+        self.k_pages = torch.empty(num_pages, page, head_dim, dtype=torch.bfloat16, device=dev)
+        self.v_pages = torch.empty_like(self.k_pages)
+        self.table = torch.zeros(batch, num_kv_heads, max_pages, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(batch, num_kv_heads, dtype=torch.int32, device=dev)
+        self.weights = self.positions = None
+        if keep is not None:
+            self.weights = torch.zeros(slots, dtype=torch.float32, device=dev)
+            self.positions = torch.zeros(slots, dtype=torch.int32, device=dev)
+        self.cache = self._rows(0, batch, num_q_heads)
+        self.book = PageBook(num_pages, page, batch, num_kv_heads, max_pages)
+        self.next_position = [0] * batch
+        self.active = [False] * batch
+        self.counts = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.start = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.out = torch.empty(batch, num_q_heads, head_dim, dtype=out_dtype, device=dev)
+
+    def _rows(self, b0, b1, num_q_heads=None):
+        part = slice(b0, b1)
+        return PagedCache(self.k_pages, self.v_pages, self.table[part], self.lens[part],
+                          weights=None if self.weights is None else self.weights[part],
+                          positions=None if self.positions is None else self.positions[part],
+                          num_q_heads=num_q_heads)
+
+    def _grow(self, growth):
+        new = self.book.grow(growth)
+        if new:
+            at = torch.tensor(new, dtype=torch.int64)
+            b, g, entry, page = (at[:, i].to(self.table.device) for i in range(4))
+            self.table[b, g, entry] = page.int()
+
+    def admit(self, b: int, k, v, queries=None):
+        """Sequence b starts with the tokens of k, v (bf16 [num_kv_heads, S, d],
+        as the prefill layer has them).  ``queries`` (bf16 [W, num_q_heads, d],
+        the prompt's last ones, say) attend over the whole prompt so that the
+        first eviction knows its tokens' weights."""
+        if self.active[b]:
+            raise ValueError(f"sequence {b} is not free")
+        tokens = k.shape[1]
+        self._grow([tokens if x == b else 0 for x in range(len(self.active))])
+        row = self._rows(b, b + 1)
+        try:
+            row.append(k[None], v[None])
+        except Exception:
+            self.book.shrink(b, [0] * len(self.book.rows[b]))
+            raise
+        self.active[b] = True
+        self.next_position[b] = tokens
+        self._mark()
+        if queries is not None and self.weights is not None:
+            for q in queries:
+                row.attend(q[None])
+        self._cut()
+        self.cache.dev_status.bitwise_or_(row.dev_status)
+
+    def release(self, b: int):
+        """Sequence b ends; its pages are free."""
+        self.book.shrink(b, [0] * len(self.book.rows[b]))
+        self.active[b] = False
+        self.next_position[b] = 0
+        self.lens[b].zero_()
+        self._mark()
+
+    def _mark(self):
+        self.counts.copy_(torch.tensor([int(a) for a in self.active], dtype=torch.int32))
+        self.start.copy_(torch.tensor(self.next_position, dtype=torch.int32))
+
+    def _cut(self):
+        if self.keep is None:
+            return
+        if any(n > k + self.slack for lens in self.book.lens for n, k in zip(lens, self.keep)):
+            self.cache.evict(self.keep, self.sinks, self.recent)
+            for b in range(len(self.active)):
+                self.book.shrink(b, self.keep)
+
+    def step(self, q, k, v, out=None, lse=None):
+        """One token of every active sequence: q bf16 [batch, num_q_heads, d],
+        k and v bf16 [batch, num_kv_heads, d].  Returns the attention output;
+        rows of sequences that are not active get zeros."""
+        self._grow([int(a) for a in self.active])
+        self.cache.append(k[:, :, None], v[:, :, None], counts=self.counts, start=self.start)
+        self.start.add_(self.counts)
+        self.next_position = [p + int(a) for p, a in zip(self.next_position, self.active)]
+        out = self.cache.attend(q, out=self.out if out is None else out, lse=lse)
+        self._cut()
+        return out

@@ -255,3 +255,53 @@ class PagedCache:
             self._status, self._handle(stream))
         if status:
             _check(status, "sparse_attn_paged_evict")
+
+
+class PageBook:
+    """Which pages of a pool belong to which (sequence, KV head) row, on the
+    host.  Pages are handed out lowest first and come back when rows shrink;
+    nothing here touches the device."""
+
+    def __init__(self, num_pages, page, batch, num_kv_heads, max_pages):
+        self.page, self.max_pages = page, max_pages
+        self.free = list(range(num_pages - 1, -1, -1))
+        self.rows = [[[] for _ in range(num_kv_heads)] for _ in range(batch)]
+        self.lens = [[0] * num_kv_heads for _ in range(batch)]
+
+    def _pages(self, tokens):
+        return -(-tokens // self.page)
+
+    def missing(self, growth):
+        """Pages that rows need to grow by ``growth[b]`` tokens each."""
+        return sum(max(0, self._pages(n + growth[b]) - len(row))
+                   for b, rows in enumerate(self.rows)
+                   for row, n in zip(rows, self.lens[b]))
+
+    def grow(self, growth):
+        """Grow every row of sequence b by ``growth[b]`` tokens; returns the new
+        table entries as (sequence, KV head, entry, page) tuples.  Nothing
+        changes when the pages or the table do not suffice."""
+        for b, more in enumerate(growth):
+            if more < 0 or (more and max(self.lens[b]) + more > self.max_pages * self.page):
+                raise ValueError(f"sequence {b} cannot grow by {more} tokens")
+        if self.missing(growth) > len(self.free):
+            raise MemoryError(f"the pool has {len(self.free)} free pages, "
+                              f"{self.missing(growth)} are needed")
+        new = []
+        for b, more in enumerate(growth):
+            if not more:
+                continue
+            for g, row in enumerate(self.rows[b]):
+                self.lens[b][g] += more
+                while len(row) < self._pages(self.lens[b][g]):
+                    new.append((b, g, len(row), self.free[-1]))
+                    row.append(self.free.pop())
+        return new
+
+    def shrink(self, b, lens):
+        """Cut sequence b's rows to at most ``lens[g]`` tokens; their spare
+        pages are free again."""
+        for g, row in enumerate(self.rows[b]):
+            self.lens[b][g] = min(self.lens[b][g], lens[g])
+            while len(row) > self._pages(self.lens[b][g]):
+                self.free.append(row.pop())

@@ -504,3 +504,144 @@ def test_attend_wait_limit_ends_the_launch(env):
     cache.attend(gq, out=out, lse=lse, accumulate=False)
     assert int(cache.dev_status.item()) == 0
     P.check_attend(c, q, out, lse)
+
+
+def test_paged_decode_layer_follows_the_oracle(env):
+    # prompts of two lengths from the prefill layout, steps with evictions to
+    # per-head budgets, a sequence released and another admitted in its place
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    Bt, hkv, hq, d, page, keep = 3, 2, 8, 128, 16, [40, 90]
+    layer = PagedDecodeLayer(Bt, hq, hkv, d, page, num_pages=80, max_tokens=200, keep=keep,
+                             slack=8, sinks=4, recent=8)
+    gen = torch.Generator().manual_seed(7)
+    rnd = lambda *s: torch.randn(*s, generator=gen).bfloat16()
+
+    def state():
+        return {"k": layer.k_pages.cpu(), "v": layer.v_pages.cpu(), "table": layer.table.cpu(),
+                "lens": layer.lens.cpu(), "weights": layer.weights.cpu(),
+                "positions": layer.positions.cpu(), "page": page}
+
+    def rows_of(s, b, g):
+        n = int(s["lens"][b, g])
+        p, x = op.slot_rows(s["table"][b, g].numpy(), np.arange(n), page)
+        return s["k"][p, x], s["positions"][b, g, :n]
+
+    kept = {}                        # (sequence, position) -> key rows, of everything appended
+
+    def admit(b, tokens):
+        k, v = rnd(hkv, tokens, d), rnd(hkv, tokens, d)
+        for t in range(tokens):
+            kept[b, t] = k[:, t]
+        layer.admit(b, k.cuda(), v.cuda(), queries=rnd(3, hq, d).cuda())
+        return tokens
+
+    pos = {0: admit(0, 30), 1: admit(1, 150)}
+    assert layer.lens.tolist() == [[30, 30], [40, 90], [0, 0]]
+    for step in range(40):
+        if step == 15:
+            layer.release(0)
+            del pos[0]
+        if step == 17:
+            pos[0] = admit(0, 70)
+        if step == 20:
+            pos[2] = admit(2, 1)
+        q, k, v = rnd(Bt, hq, d), rnd(Bt, hkv, d), rnd(Bt, hkv, d)
+        before = state()
+        lse = torch.empty(Bt, hq, device="cuda")
+        out = layer.step(q.cuda(), k.cuda(), v.cuda(), lse=lse).clone()
+        for b in pos:
+            kept[b, pos[b]] = k[b]
+            pos[b] += 1
+        assert int(layer.cache.dev_status.item()) == 0
+        now = state()
+        assert now["lens"].tolist() == layer.book.lens
+        # the attention saw the old tokens and the new one (the device table is
+        # only added to: after an eviction it still names the pages read)
+        counts = [int(b in pos) for b in range(Bt)]
+        ref = op.append(P.f64(before["k"]), P.f64(before["v"]), now["table"].numpy(),
+                        before["lens"].numpy(), P.f64(k[:, :, None]), P.f64(v[:, :, None]), counts,
+                        [pos.get(b, 1) - 1 for b in range(Bt)], P.f64(before["weights"]),
+                        before["positions"].numpy())
+        c = {"k": torch.as_tensor(ref[0]), "v": torch.as_tensor(ref[1]), "table": now["table"],
+             "lens": torch.as_tensor(ref[2]), "weights": torch.as_tensor(ref[3]), "page": page}
+        P.check_attend(c, q, out, lse)
+        # what is left are tokens that were appended, each with its own key,
+        # the first and the last positions among them
+        for b in pos:
+            for g in range(hkv):
+                rows, p = rows_of(now, b, g)
+                assert len(set(p.tolist())) == len(p)
+                for row, x in zip(rows, p.tolist()):
+                    assert torch.equal(row, kept[b, x][g])
+                for x in list(range(min(4, pos[b]))) + list(range(max(0, pos[b] - 8), pos[b])):
+                    assert x in p.tolist()
+        for b in range(Bt):
+            if b not in pos:
+                assert (out[b] == 0).all() and (lse[b] == -float("inf")).all()
+
+
+def test_paged_decode_layer_after_the_prefill_layer(env):
+    # the prefill layer's keys and values, a plan's budgets: one layer of a
+    # served prompt, with and without room for everything
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer, PrefillLayer, kv_budgets
+    from tests import _paged as P
+    from tests._parity import to_dev
+    sa, torch = env
+    from workloads import generate, scaled, workload
+    w = scaled(workload(1), 1024)
+    x = generate.prefill_inputs(w)
+    t = {n: to_dev(x[n]) for n in "qkv"}
+    shape = sa.Shape.prefill(w.seq_len, w.block, w.num_q_heads, w.num_kv_heads, w.head_dim)
+    pre = PrefillLayer(shape, 6, demand=[3, 5, 4, 9, 2, 2, 8, 4], num_workers=8)
+    pre(t["q"], t["k"], t["v"])
+    keep = kv_budgets(pre.plan, w.block)
+    budgets = pre.plan.get()["budgets"]
+    assert keep == [int(budgets[:4].max()) * 64, int(budgets[4:].max()) * 64]
+    q = _q(torch, 3, 1, 8, 64)
+    kn, vn = _q(torch, 4, 1, 2, 64), _q(torch, 5, 1, 2, 64)
+    for budget in (None, keep):
+        layer = PagedDecodeLayer(1, 8, 2, 64, 64, num_pages=40, max_tokens=1100, keep=budget,
+                                 slack=0)
+        layer.admit(0, t["k"], t["v"], queries=t["q"].transpose(0, 1)[-4:])
+        lens = [1024, 1024] if budget is None else [min(1024, n) for n in keep]
+        assert layer.lens.tolist() == [lens]
+        lse = torch.empty(1, 8, device="cuda")
+        out = layer.step(q.cuda(), kn.cuda(), vn.cuda(), lse=lse).clone()
+        assert int(layer.cache.dev_status.item()) == 0
+        if budget is None:
+            k = torch.cat([t["k"].cpu(), kn[0][:, None]], 1)
+            v = torch.cat([t["v"].cpu(), vn[0][:, None]], 1)
+            c = {"k": k.view(2, 1025, 64), "v": v.view(2, 1025, 64),
+                 "table": torch.tensor([[[0], [1]]], dtype=torch.int32),
+                 "lens": torch.tensor([[1025, 1025]], dtype=torch.int32), "page": 1025,
+                 "weights": None}
+            P.check_attend(c, q, out, lse)
+        else:
+            assert layer.lens.tolist() == [lens]           # cut back to the budgets
+            assert len(layer.book.free) == 40 - sum(-(-n // 64) for n in lens)
+
+
+def test_paged_decode_layer_refusals(env):
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    sa, torch = env
+    with pytest.raises(ValueError):
+        PagedDecodeLayer(1, 8, 2, 64, 16, 10, 100, keep=[10, 30])
+    with pytest.raises(sa.SparseAttnError):
+        PagedDecodeLayer(1, 8, 2, 64, 24, 10, 100)
+    layer = PagedDecodeLayer(2, 8, 2, 64, 16, 10, 100)
+    k = torch.zeros(2, 70, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(TypeError):
+        layer.admit(0, k.float(), k)
+    assert len(layer.book.free) == 10
+    layer.admit(0, k, k)
+    with pytest.raises(ValueError):
+        layer.admit(0, k, k)
+    with pytest.raises(MemoryError):
+        layer.admit(1, k, k)                               # ten pages are all there are
+    assert layer.active == [True, False] and layer.lens.tolist() == [[70, 70], [0, 0]]
+    layer.release(0)
+    layer.admit(1, k, k)
+    assert layer.lens.tolist() == [[0, 0], [70, 70]]

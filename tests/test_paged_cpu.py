@@ -208,3 +208,45 @@ def test_python_class_refuses_cpu_tensors_and_wrong_types(sa):
         sa.PagedCache(k, k, table.long(), lens)
     with pytest.raises(AttributeError):
         sa.no_such_name
+
+
+# ---------------------------------------------------------------- the page book
+def test_page_book_hands_out_and_takes_back(sa):
+    from head_heterogeneous_block_gb300.paged import PageBook
+    book = PageBook(num_pages=7, page=16, batch=2, num_kv_heads=2, max_pages=3)
+    assert book.grow([17, 0]) == [(0, 0, 0, 0), (0, 0, 1, 1), (0, 1, 0, 2), (0, 1, 1, 3)]
+    assert book.lens == [[17, 17], [0, 0]] and len(book.free) == 3
+    assert book.grow([0, 16]) == [(1, 0, 0, 4), (1, 1, 0, 5)]
+    with pytest.raises(MemoryError):
+        book.grow([0, 1])                       # two pages, one free
+    assert book.lens == [[17, 17], [16, 16]] and len(book.free) == 1
+    with pytest.raises(ValueError):
+        book.grow([32, 0])                      # past the table
+    book.shrink(0, [16, 40])
+    assert book.lens == [[16, 17], [16, 16]] and sorted(book.free) == [1, 6]
+    assert book.grow([0, 1]) == [(1, 0, 1, 1), (1, 1, 1, 6)]
+    book.shrink(1, [0, 0])
+    assert book.rows[1] == [[], []] and sorted(book.free) == [1, 4, 5, 6]
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_page_book_never_shares_a_page(sa, seed):
+    from head_heterogeneous_block_gb300.paged import PageBook
+    r = np.random.default_rng(seed)
+    book = PageBook(num_pages=60, page=16, batch=3, num_kv_heads=2, max_pages=12)
+    table = {}
+    for _ in range(200):
+        if r.random() < 0.7:
+            try:
+                for b, g, e, p in book.grow([int(x) for x in r.integers(0, 20, 3)]):
+                    table[b, g, e] = p
+            except (MemoryError, ValueError):
+                pass
+        else:
+            book.shrink(int(r.integers(0, 3)), [int(x) for x in r.integers(0, 150, 2)])
+        owned = [p for rows in book.rows for row in rows for p in row]
+        assert sorted(owned + book.free) == list(range(60))
+        for b in range(3):
+            for g in range(2):
+                assert len(book.rows[b][g]) == -(-book.lens[b][g] // 16)
+                assert [table[b, g, e] for e in range(len(book.rows[b][g]))] == book.rows[b][g]
