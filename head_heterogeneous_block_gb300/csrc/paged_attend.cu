@@ -121,7 +121,7 @@ struct Shared {
 // Workspace: records, row log-sum-exps, partial states, scores.  A record is
 // what the join of a row needs: u is -1 where nothing is to be joined.  There
 // is one a row when there are no more rows than CTAs, else one a CTA, for the
-// row of whose ranges its own is the second.
+// row that begins in its range and ends in another.
 struct Record {
   int32_t u, first, segs;       // the row, its first CTA, its ranges
   int32_t slot;                 // partial state of the first CTA: its first or second
@@ -165,6 +165,7 @@ struct Params {
   int32_t q_rows;              // heads of a Q box
   int32_t min_units;           // least units of a CTA
   int32_t by_row;              // records: one a row
+  int32_t ctas;                // CTAs of the first launch
   float scale_log2;
   void* o;
   int32_t out_f32;
@@ -176,12 +177,14 @@ struct Params {
   uint64_t wait_ns;
 };
 
-// The row, and the first head of the chunk, of u.
+// The row, and the first head of the chunk, of u.  kOne: rows have one chunk.
+template <bool kOne>
 __device__ __forceinline__ int32_t row_of(const Params& p, int32_t u) {
-  return p.HC == 1 ? u : u / p.HC;
+  return kOne || p.HC == 1 ? u : u / p.HC;
 }
+template <bool kOne>
 __device__ __forceinline__ int32_t head_of(const Params& p, int32_t u) {
-  return p.HC == 1 ? 0 : (u % p.HC) * kChunk;
+  return kOne || p.HC == 1 ? 0 : (u % p.HC) * kChunk;
 }
 
 __device__ __forceinline__ int32_t units_of(const Params& p, int32_t len) {
@@ -199,24 +202,31 @@ struct Ranges {
   }
 };
 
+template <bool kF32>
 __device__ __forceinline__ void store_out(const Params& p, size_t at, float v) {
-  if (p.out_f32)
+  if (kF32)
     static_cast<float*>(p.o)[at] = v;
   else
     static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(v);
 }
 
 // A wait's first polls leave the clock alone: reading it costs more than most
-// waits here last.  Short limits go by the clock from the start.
+// waits here last.  Short limits go by the clock from the start.  What goes by
+// the clock is a call, not a copy at every wait: a launch starts with a cold
+// instruction cache, and its first microseconds go by the code it has to fetch.
 constexpr uint64_t kClockless = 1000000;
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                        uint64_t limit_ns) {
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                       uint64_t limit_ns) {
   if (limit_ns >= kClockless) {
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
       if (mbar_test_sleep(bar, parity, 2000)) return true;
   }
   return mbar_wait(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                        uint64_t limit_ns) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, abort, limit_ns);
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns) {
@@ -255,6 +265,8 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   using C = Cfg<D, GP, PARTS>;
   constexpr int kThreads = C::kThreads;
   constexpr int HP = C::kHeads;
+  constexpr bool kOne = GP < kChunk;
+  constexpr bool kF32 = PARTS == 3;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   launch_dependents();
   uint8_t* sKV = smem_raw;
@@ -278,10 +290,12 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
+#pragma unroll 1
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->kv_full[s], 1);
       mbar_init(&sh->kv_empty[s], 1);
     }
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->q_full[s], 1);
       mbar_init(&sh->q_empty[s], 1);
@@ -291,6 +305,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     mbar_init(&sh->p_full, 4 * C::kGroups);    // a softmax warp each
     mbar_init(&sh->pv_done, 1);
     mbar_init(&sh->drain, 1);
+#pragma unroll 1
     for (int s = 0; s < kInfo; ++s) {
       mbar_init(&sh->info_full[s], 1);
       mbar_init(&sh->info_empty[s], 1 + 4 * C::kGroups);   // the issuer and the softmax warps
@@ -311,8 +326,9 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   const int32_t per = (p.U + kThreads - 1) / kThreads;
   const int32_t ua = min(p.U, tid * per), ub = min(p.U, ua + per);
   int32_t mine = 0, len_a = 0;
+#pragma unroll 1
   for (int32_t u = ua; u < ub; ++u) {
-    const int32_t n = sa_paged::row_len(p.lens, row_of(p, u), p.cap, p.dev_status);
+    const int32_t n = sa_paged::row_len(p.lens, row_of<kOne>(p, u), p.cap, p.dev_status);
     if (u == ua) len_a = n;
     mine += units_of(p, n);
   }
@@ -323,7 +339,6 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     if (lane >= o) incl += x;
   }
   if (lane == 31) sh->scan[warp] = incl;
-  if (tid == 0 && !p.by_row) p.w.rec[cta] = Record{-1, 0, 0, 0};
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -340,38 +355,35 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   const int32_t a = rg.begin(min(cta, rg.ctas)), b = rg.begin(min(cta + 1, rg.ctas));
   const uint32_t tmem = sh->tmem_base;
   // rows without a token, taken in turn by the CTAs
-  auto empty_rows = [&](int first_thread, int threads) {
+  if (warp >= 2) {
+#pragma unroll 1
     for (int32_t u = cta; u < p.U; u += gridDim.x) {
-      if (sa_paged::row_len(p.lens, row_of(p, u), p.cap, p.dev_status) > 0) continue;
-      const int32_t r = row_of(p, u), h0 = head_of(p, u);
+      if (sa_paged::row_len(p.lens, row_of<kOne>(p, u), p.cap, p.dev_status) > 0) continue;
+      const int32_t r = row_of<kOne>(p, u), h0 = head_of<kOne>(p, u);
       const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
-      const int gc = min(kChunk, p.G - h0), x0 = tid - first_thread;
-      for (int x = x0; x < gc * D; x += threads) store_out(p, bh * D + x, 0.f);
+      const int gc = min(kChunk, p.G - h0), x0 = tid - 64;
+#pragma unroll 1
+      for (int x = x0; x < gc * D; x += kThreads - 64) store_out<kF32>(p, bh * D + x, 0.f);
       if (p.lse && x0 < gc) p.lse[bh + x0] = -INFINITY;
       if (p.by_row && x0 == 0) p.w.rec[u] = Record{-1, 0, 0, 0};
     }
-  };
+  }
   if (a >= b) {
-    empty_rows(0, kThreads);
+    if (tid == 0 && !p.by_row) p.w.rec[cta] = Record{-1, 0, 0, 0};
     if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
     return;
   }
   if (a >= before && a < before + mine) {
     int32_t at = before;
+#pragma unroll 1
     for (int32_t u = ua; u < ub; ++u) {
       const int32_t n = u == ua ? len_a
-                                : sa_paged::row_len(p.lens, row_of(p, u), p.cap, p.dev_status);
+                                : sa_paged::row_len(p.lens, row_of<kOne>(p, u), p.cap, p.dev_status);
       const int32_t k = units_of(p, n);
       if (a >= at && a < at + k) {
         sh->u0 = u;
         sh->p0 = at;
         sh->len0 = n;
-        if (!p.by_row && a > at) {
-          const int32_t first = rg.owner(at);
-          if (first == cta - 1)
-            p.w.rec[cta] = Record{u, first, rg.owner(at + k - 1) - first + 1,
-                                  at == rg.begin(first) ? 0 : 1};
-        }
       }
       at += k;
     }
@@ -386,19 +398,12 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     int32_t ubase = u, ulen = 0;               // lane l holds the length of row ubase + l
     auto load_lens = [&]() {
       ulen = ubase + lane < p.U
-                 ? sa_paged::row_len(p.lens, row_of(p, ubase + lane), p.cap, p.dev_status) : 0;
+                 ? sa_paged::row_len(p.lens, row_of<kOne>(p, ubase + lane), p.cap, p.dev_status) : 0;
     };
     auto end_of = [&]() -> int32_t {           // of the row's part in this range
       return min(len, int32_t(min(int64_t(b - pu) << p.bx_shift, int64_t(1) << 30)));
     };
     int32_t seg = 0;                           // row parts before this one
-    // the record of a row that begins in this range
-    auto record = [&]() {
-      if (p.by_row && lane == 0) {
-        const int32_t segs = rg.owner(pu + units_of(p, len) - 1) - cta + 1;
-        p.w.rec[u] = Record{segs > 1 ? u : -1, cta, segs, seg > 0 ? 1 : 0};
-      }
-    };
     int32_t t = (a - pu) << p.bx_shift, t1 = end_of();
     bool first = true, begins = t == 0;
     bool more = true;
@@ -421,7 +426,6 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         if (len > 0) {
           first = begins = true;
           ++seg;
-          record();
         }
       }
       if (!more) return TileInfo{0, 0, 0, 0};
@@ -438,20 +442,28 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     auto lookup = [&](const TileInfo& x) -> int32_t {
       if ((lane << p.bx_shift) >= x.n) return 0;
       const int32_t slot = x.t + (lane << p.bx_shift);
-      return p.table[int64_t(row_of(p, x.u)) * p.max_pages + (slot >> p.page_shift)];
+      return p.table[int64_t(row_of<kOne>(p, x.u)) * p.max_pages + (slot >> p.page_shift)];
     };
     uint32_t i = 0, qi = 0;                    // tiles and Q tiles issued
     uint32_t issued = 0;                       // stages filled
     bool ok = true;
-    TileInfo cur = next(), nxt{0, 0, 0, 0};
-    int32_t pg = lookup(cur), npg = 0;
-    while (cur.n > 0) {
-      // the next tile's pages are looked up while the ring may be full; the
-      // first tile's copies wait for nothing
-      if (i > 0) {
-        nxt = next();
-        npg = lookup(nxt);
+    // The first tile's copies are issued at once; from then on a tile's pages
+    // are looked up before the one ahead of it waits for room in the ring.
+    TileInfo held{0, 0, 0, 0};
+    int32_t held_pg = 0;
+#pragma unroll 1
+    for (uint32_t k = 0;; ++k) {
+      const TileInfo x = next();
+      const int32_t x_pg = lookup(x);
+      const TileInfo cur = k == 0 ? x : held;
+      int32_t pg = k == 0 ? x_pg : held_pg;
+      held = x;
+      held_pg = x_pg;
+      if (k == 1) {
+        if (x.n == 0) break;
+        continue;
       }
+      if (cur.n == 0) break;
       const int boxes = (cur.n + bx - 1) >> p.bx_shift;
       const int32_t prow = (cur.t + (lane << p.bx_shift)) & ((1 << p.page_shift) - 1);
       const int slot = i % kInfo;
@@ -468,8 +480,8 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
           ok = wait_warp(&sh->q_empty[qs], ((qi / C::kQs) - 1) & 1, abort, p.wait_ns);
         if (!ok) break;
         if (lane == 0) {
-          const int32_t r = row_of(p, cur.u);
-          const int32_t h0 = (r % p.Hkv) * p.G + head_of(p, cur.u);
+          const int32_t r = row_of<kOne>(p, cur.u);
+          const int32_t h0 = (r % p.Hkv) * p.G + head_of<kOne>(p, cur.u);
           mbar_arrive_expect_tx(&sh->q_full[qs], C::kPanels * p.q_rows * 128);
 #pragma unroll
           for (int s = 0; s < C::kPanels; ++s)
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         atomicOr(p.dev_status, SA_DEV_BAD_INDEX);
         pg = 0;
       }
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int st = issued % C::kStages;
         if (issued >= uint32_t(C::kStages))
@@ -500,15 +512,17 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         ++issued;
       }
       if (!ok) break;
-      if (i == 0) {
-        if (begins) record();
-        load_lens();
-        nxt = next();
-        npg = lookup(nxt);
-      }
+      if (k == 0) load_lens();
       ++i;
-      cur = nxt;
-      pg = npg;
+      if (k > 0 && x.n == 0) break;
+    }
+    // the record of a row that begins in this range and ends in another; the
+    // rows that end here are the softmax warps' to record
+    if (lane == 0) {
+      const bool cut = begins && pu > b;       // pu: the end of the last row
+      if (cut || !p.by_row)
+        p.w.rec[p.by_row ? u : cta] =
+            Record{cut ? u : -1, cta, cut ? rg.owner(pu - 1) - cta + 1 : 0, seg > 0 ? 1 : 0};
     }
     if (ok) {
       const int slot = i % kInfo;
@@ -525,10 +539,12 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         *abort = 1;
       }
       // copies still in flight land before the CTA's shared memory goes
+#pragma unroll 1
       for (uint32_t x = issued > uint32_t(C::kStages) ? issued - C::kStages : 0; x < issued; ++x)
-        mbar_wait(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, nullptr);
+        wait_long(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, nullptr, kWaitLimitNs);
+#pragma unroll 1
       for (uint32_t x = qi > uint32_t(C::kQs) ? qi - C::kQs : 0; x < qi; ++x)
-        mbar_wait(&sh->q_full[x % C::kQs], (x / C::kQs) & 1, nullptr);
+        wait_long(&sh->q_full[x % C::kQs], (x / C::kQs) & 1, nullptr, kWaitLimitNs);
     }
   } else if (warp == 1) {
     // ------------------------------------------------- issuer of both products
@@ -646,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
       }
       // every product is complete before the tensor memory is freed
       mma_commit(&sh->drain);
-      mbar_wait(&sh->drain, 0, nullptr);
+      wait_long(&sh->drain, 0, nullptr, kWaitLimitNs);
     }
   } else {
     // ------------------------------------------------- softmax and output
@@ -658,7 +674,6 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     float m[HP], l[HP], o[HP];
     TileInfo prev{0, 0, 0, 0}, it{0, 0, 0, 0};
     bool ok = true;
-    empty_rows(64, kThreads - 64);
     // the description of tile j
     auto describe = [&](uint32_t j) -> bool {
       const int slot = j % kInfo;
@@ -674,7 +689,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
       // four warps learn together whether one gave up.
       float s[HP];
       bool need = false;
-      const int gc = min(kChunk, p.G - head_of(p, it.u)) - grp * HP;   // live heads
+      const int gc = min(kChunk, p.G - head_of<kOne>(p, it.u)) - grp * HP;   // live heads
       const bool live = !fail && it.n > 0;
       if (!fail && (live || j > 0)) {
         // lanes split over the scores, the last output product, and (for a
@@ -736,29 +751,37 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
             for (int h = 0; h < HP; ++h) sh->red[grp][quarter][h] = l[h];
           }
           group_sync<C::kGroups>(grp);
-          const int32_t r = row_of(p, prev.u), h0 = head_of(p, prev.u) + grp * HP;
+          const int32_t r = row_of<kOne>(p, prev.u), h0 = head_of<kOne>(p, prev.u) + grp * HP;
           const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
           const size_t part =
               (size_t(cta) * 2 + ((prev.flags & kSecond) ? 1 : 0)) * kChunk + grp * HP;
+          const bool whole = (prev.flags & kComplete) != 0;
+          float mr = 0.f;                      // thread h: head h's reference
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
-            if (h0 + h < p.G) {
-              const float L = (sh->red[grp][0][h] + sh->red[grp][1][h]) +
-                              (sh->red[grp][2][h] + sh->red[grp][3][h]);
-              if (prev.flags & kComplete) {
-                if (row < D) store_out(p, (bh + h) * D + row, o[h] / L);
-                if (row == h) {
-                  const float lse2 = (m[h] == -INFINITY ? 0.f : m[h]) + log2f(L);
-                  if (p.lse) p.lse[bh + h] = lse2 * 0.6931471805599453f;
-                  if (p.weights_out)
-                    p.w.row_lse2[size_t(prev.u) * kChunk + grp * HP + h] = lse2;
-                }
+            if (row == h) mr = m[h];
+            if (h0 + h < p.G && row < D) {
+              if (whole) {
+                const float L = (sh->red[grp][0][h] + sh->red[grp][1][h]) +
+                                (sh->red[grp][2][h] + sh->red[grp][3][h]);
+                store_out<kF32>(p, (bh + h) * D + row, __fdividef(o[h], L));
               } else {
-                if (row < D) p.w.part_o[(part + h) * D + row] = o[h];
-                if (row == h) p.w.part_ml[part + h] = make_float2(m[h], L);
+                p.w.part_o[(part + h) * D + row] = o[h];
               }
             }
           }
+          if (row < HP && h0 + row < p.G) {
+            const float L = (sh->red[grp][0][row] + sh->red[grp][1][row]) +
+                            (sh->red[grp][2][row] + sh->red[grp][3][row]);
+            if (whole) {
+              const float lse2 = (mr == -INFINITY ? 0.f : mr) + log2f(L);
+              if (p.lse) p.lse[bh + row] = lse2 * 0.6931471805599453f;
+              if (p.weights_out) p.w.row_lse2[size_t(prev.u) * kChunk + grp * HP + row] = lse2;
+            } else {
+              p.w.part_ml[part + row] = make_float2(mr, L);
+            }
+          }
+          if (whole && p.by_row && grp == 0 && row == 0) p.w.rec[prev.u] = Record{-1, 0, 0, 0};
           group_sync<C::kGroups>(grp);              // red is read before it is written again
         }
       }
@@ -792,7 +815,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         group_sync<C::kGroups>(grp);
       }
       if (p.weights_out && row < it.n) {
-        const int32_t r = row_of(p, it.u), h0 = head_of(p, it.u) + grp * HP;
+        const int32_t r = row_of<kOne>(p, it.u), h0 = head_of<kOne>(p, it.u) + grp * HP;
         float* dst = p.w.scores + (size_t(r) * p.G + h0) * p.cap + it.t + row;
 #pragma unroll
         for (int h = 0; h < HP; ++h)
@@ -853,7 +876,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
   const Record rec = p.w.rec[blockIdx.x];
   if (rec.u < 0) return;
-  const int32_t r = row_of(p, rec.u), h0 = head_of(p, rec.u);
+  // a launch that gave up may have left no record: whatever is there instead
+  // must not lead out of the workspace
+  if (rec.u >= p.U || rec.first < 0 || rec.segs < 1 || rec.segs > p.ctas ||
+      rec.first > p.ctas - rec.segs || (rec.slot & ~1))
+    return;
+  const int32_t r = row_of<false>(p, rec.u), h0 = head_of<false>(p, rec.u);
   const int h = blockIdx.y;                        // head of the chunk
   if (h >= p.G - h0) return;
   auto part_of = [&](int32_t k) -> size_t {
@@ -898,7 +926,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     sum += acc[y][x];
   }
   const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0 + h;
-  store_out(p, bh * D + x, sum / L);
+  if (p.out_f32)
+    store_out<true>(p, bh * D + x, sum / L);
+  else
+    store_out<false>(p, bh * D + x, sum / L);
   if (x == 0) {
     const float lse2 = M + log2f(L);
     if (p.lse) p.lse[bh] = lse2 * 0.6931471805599453f;
@@ -1019,6 +1050,7 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
   const int ctas = sms * C::kPerSm;
   p.by_row = p.U <= ctas;
+  p.ctas = ctas;
   layout(&p.w, static_cast<char*>(a.ws), rows, p.G, p.cap, D, ctas, a.weights_out != nullptr);
   auto kern = attend_kernel<D, GP, PARTS>;
   static std::atomic<uint64_t> done{0};
