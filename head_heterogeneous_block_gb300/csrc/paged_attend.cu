@@ -103,11 +103,14 @@ struct TileInfo {
 enum { kFirst = 1, kLast = 2, kComplete = 4, kSecond = 8 };
 
 struct Shared {
+  // the barriers, in the order that the kernel's first threads initialise them
+  uint64_t info_empty[kInfo];   // one arrival of the issuer and of each softmax warp
+  uint64_t p_full;              // one of each softmax warp
+  uint64_t info_full[kInfo];    // from here on: one arrival
   uint64_t kv_full[6], kv_empty[6];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];
-  uint64_t p_full, pv_done;
-  uint64_t info_full[kInfo], info_empty[kInfo];
+  uint64_t pv_done;
   uint64_t drain;
   TileInfo info[kInfo];
   float red[2][4][8];  // [group][quarter][head]
@@ -290,28 +293,16 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
-#pragma unroll 1
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh->kv_full[s], 1);
-      mbar_init(&sh->kv_empty[s], 1);
-    }
-#pragma unroll 1
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh->q_full[s], 1);
-      mbar_init(&sh->q_empty[s], 1);
-      mbar_init(&sh->s_full[s], 1);
-      sh->failed[s] = 0;
-    }
-    mbar_init(&sh->p_full, 4 * C::kGroups);    // a softmax warp each
-    mbar_init(&sh->pv_done, 1);
-    mbar_init(&sh->drain, 1);
-#pragma unroll 1
-    for (int s = 0; s < kInfo; ++s) {
-      mbar_init(&sh->info_full[s], 1);
-      mbar_init(&sh->info_empty[s], 1 + 4 * C::kGroups);   // the issuer and the softmax warps
-    }
     sh->abort = 0;
+    sh->failed[0] = sh->failed[1] = 0;
     sh->u0 = sh->p0 = sh->len0 = 0;
+  }
+  constexpr int kBars = 2 * kInfo + 1 + 12 + 6 + 2;
+  static_assert(offsetof(Shared, info) == kBars * sizeof(uint64_t) && kBars <= kThreads, "");
+  if (tid < kBars) {
+    mbar_init(&sh->info_empty[0] + tid, tid < kInfo    ? 1 + 4 * C::kGroups
+                                        : tid == kInfo ? 4 * C::kGroups
+                                                       : 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -320,17 +311,28 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   }
   // keys and values are read once: their lines make way first in L2
   const uint64_t pol = l2_policy_evict_first();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
   wait_dependency();
 
-  // ---- this CTA's range: a scan of every row's units
-  const int32_t per = (p.U + kThreads - 1) / kThreads;
-  const int32_t ua = min(p.U, tid * per), ub = min(p.U, ua + per);
-  int32_t mine = 0, len_a = 0;
+  // ---- this CTA's range: a scan of every row's units.  Up to 128 rows each
+  // warp scans for itself, four rows a lane; more rows are scanned by the CTA.
+  const bool few = p.U <= 128;
+  const int32_t per = few ? 4 : (p.U + kThreads - 1) / kThreads;
+  const int32_t ua = min(p.U, (few ? lane : tid) * per), ub = min(p.U, ua + per);
+  int32_t mine = 0;
+  if (few) {
+    int32_t n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = ua + i < ub ? p.lens[row_of<kOne>(p, ua + i)] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine += units_of(p, max(0, min(n[i], p.cap)));
+  } else {
 #pragma unroll 1
-  for (int32_t u = ua; u < ub; ++u) {
-    const int32_t n = sa_paged::row_len(p.lens, row_of<kOne>(p, u), p.cap, p.dev_status);
-    if (u == ua) len_a = n;
-    mine += units_of(p, n);
+    for (int32_t u = ua; u < ub; ++u)
+      mine += units_of(p, max(0, min(p.lens[row_of<kOne>(p, u)], p.cap)));
   }
   int32_t incl = mine;
 #pragma unroll
@@ -338,22 +340,41 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  if (lane == 31) sh->scan[warp] = incl;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int32_t before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sh->scan[w];
-    total += sh->scan[w];
+  int32_t before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+  if (!few) {
+    if (lane == 31) sh->scan[warp] = incl;
+    __syncthreads();
+    total = 0;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sh->scan[w];
+      total += sh->scan[w];
+    }
   }
   Ranges rg;
   rg.ctas = max(1, min(int32_t(gridDim.x), (total + p.min_units - 1) / p.min_units));
   rg.base = total / rg.ctas;
   rg.rem = total - rg.base * rg.ctas;
   const int32_t a = rg.begin(min(cta, rg.ctas)), b = rg.begin(min(cta + 1, rg.ctas));
-  const uint32_t tmem = sh->tmem_base;
+  // the thread that has the range's first row says where that begins
+  if (a < b && a >= before && a < before + mine && (!few || warp == 0)) {
+    int32_t at = before;
+#pragma unroll 1
+    for (int32_t u = ua; u < ub; ++u) {
+      const int32_t n = max(0, min(p.lens[row_of<kOne>(p, u)], p.cap));
+      if (a < at + units_of(p, n)) {
+        sh->u0 = u;
+        sh->p0 = at;
+        sh->len0 = n;
+        break;
+      }
+      at += units_of(p, n);
+    }
+  }
+  if (few)
+    __syncwarp();
+  else
+    __syncthreads();
   // rows without a token, taken in turn by the CTAs
   if (warp >= 2) {
 #pragma unroll 1
@@ -373,22 +394,6 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
     return;
   }
-  if (a >= before && a < before + mine) {
-    int32_t at = before;
-#pragma unroll 1
-    for (int32_t u = ua; u < ub; ++u) {
-      const int32_t n = u == ua ? len_a
-                                : sa_paged::row_len(p.lens, row_of<kOne>(p, u), p.cap, p.dev_status);
-      const int32_t k = units_of(p, n);
-      if (a >= at && a < at + k) {
-        sh->u0 = u;
-        sh->p0 = at;
-        sh->len0 = n;
-      }
-      at += k;
-    }
-  }
-  __syncthreads();
   const int bx = 1 << p.bx_shift;
 
   if (warp == 0) {
