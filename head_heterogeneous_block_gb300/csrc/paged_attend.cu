@@ -869,13 +869,13 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
 }
 
 // Block (record, head): the join of a row's partial states.  Sixteen warps take
-// every sixteenth state each, at the states' common maximum, and their sums
-// are added in warp order.
-template <int D>
+// every sixteenth state each and bring them to their own maximum; the sixteen
+// results are brought to the row's and added in warp order.
+template <int D, bool kF32>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = D / 32;                     // elements of a lane
   constexpr int kWays = kJoinThreads / 32;
-  __shared__ float acc[kWays][D], ls[kWays];
+  __shared__ float acc[kWays][D], ms[kWays], ls[kWays];
   launch_dependents();
   wait_dependency();
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
@@ -886,57 +886,59 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (rec.u >= p.U || rec.first < 0 || rec.segs < 1 || rec.segs > p.ctas ||
       rec.first > p.ctas - rec.segs || (rec.slot & ~1))
     return;
-  const int32_t r = row_of<false>(p, rec.u), h0 = head_of<false>(p, rec.u);
   const int h = blockIdx.y;                        // head of the chunk
-  if (h >= p.G - h0) return;
-  auto part_of = [&](int32_t k) -> size_t {
-    return (size_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * kChunk + h;
-  };
-  float M = -INFINITY;
-  for (int32_t k = lane; k < rec.segs; k += 32) M = fmaxf(M, p.w.part_ml[part_of(k)].x);
-  M = warp_max(M);
-  if (M == -INFINITY) M = 0.f;
-  float L = 0.f, v[kVec];
+  float m = -INFINITY, l = 0.f, v[kVec];
 #pragma unroll
   for (int x = 0; x < kVec; ++x) v[x] = 0.f;
 #pragma unroll 4
   for (int32_t k = way; k < rec.segs; k += kWays) {
-    const size_t at = part_of(k);
+    const uint32_t at = (uint32_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * kChunk + h;
     const float2 ml = p.w.part_ml[at];
-    const float f = ex2(ml.x - M);
-    L = fmaf(f, ml.y, L);
+    float o[kVec];
     if constexpr (kVec == 4) {
-      const float4 o4 = *reinterpret_cast<const float4*>(p.w.part_o + at * D + lane * 4);
-      v[0] = fmaf(f, o4.x, v[0]);
-      v[1] = fmaf(f, o4.y, v[1]);
-      v[2] = fmaf(f, o4.z, v[2]);
-      v[3] = fmaf(f, o4.w, v[3]);
+      const float4 y = *reinterpret_cast<const float4*>(p.w.part_o + at * D + lane * 4);
+      o[0] = y.x;
+      o[1] = y.y;
+      o[2] = y.z;
+      o[3] = y.w;
     } else {
-      const float2 o2 = *reinterpret_cast<const float2*>(p.w.part_o + at * D + lane * 2);
-      v[0] = fmaf(f, o2.x, v[0]);
-      v[1] = fmaf(f, o2.y, v[1]);
+      const float2 y = *reinterpret_cast<const float2*>(p.w.part_o + at * D + lane * 2);
+      o[0] = y.x;
+      o[1] = y.y;
     }
+    const float mn = fmaxf(m, ml.x);
+    const float f0 = mn == m ? 1.f : ex2(m - mn), f1 = mn == ml.x ? 1.f : ex2(ml.x - mn);
+    l = l * f0 + ml.y * f1;
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) v[x] = v[x] * f0 + o[x] * f1;
+    m = mn;
   }
 #pragma unroll
   for (int x = 0; x < kVec; ++x) acc[way][lane * kVec + x] = v[x];
-  if (lane == 0) ls[way] = L;
+  if (lane == 0) {
+    ms[way] = m;
+    ls[way] = l;
+  }
   __syncthreads();
   const int x = threadIdx.x;
-  if (x >= D) return;
+  const int32_t r = row_of<false>(p, rec.u), hc = head_of<false>(p, rec.u) + h;
+  if (x >= D || hc >= p.G) return;
   const int ways = min(kWays, rec.segs);
-  float sum = 0.f;
-  L = 0.f;
+  float M = ms[0];
+#pragma unroll 1
+  for (int y = 1; y < ways; ++y) M = fmaxf(M, ms[y]);
+  float sum = 0.f, L = 0.f;
+#pragma unroll 1
   for (int y = 0; y < ways; ++y) {
-    L += ls[y];
-    sum += acc[y][x];
+    const float f = ms[y] == M ? 1.f : ex2(ms[y] - M);
+    L = fmaf(ls[y], f, L);
+    sum = fmaf(acc[y][x], f, sum);
   }
-  const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0 + h;
-  if (p.out_f32)
-    store_out<true>(p, bh * D + x, sum / L);
-  else
-    store_out<false>(p, bh * D + x, sum / L);
+  const int32_t b = r / p.Hkv;
+  const size_t bh = size_t(b) * p.Hq + size_t(r - b * p.Hkv) * p.G + hc;
+  store_out<kF32>(p, bh * D + x, __fdividef(sum, L));
   if (x == 0) {
-    const float lse2 = M + log2f(L);
+    const float lse2 = (M == -INFINITY ? 0.f : M) + log2f(L);
     if (p.lse) p.lse[bh] = lse2 * 0.6931471805599453f;
     if (p.weights_out) p.w.row_lse2[size_t(rec.u) * kChunk + h] = lse2;
   }
@@ -1078,7 +1080,7 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   cfg.gridDim = dim3(unsigned(p.by_row ? p.U : ctas), unsigned(p.q_rows));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D, PARTS == 3>, p);
   if (e != cudaSuccess || !a.weights_out) return e;
   constexpr int kPiece = kWeightThreads * kWeightSteps;
   const int32_t pieces = (p.cap + kPiece - 1) / kPiece;
