@@ -46,7 +46,7 @@ sa_status check_cache(const sa_paged_cache* c) {
 sa_status check_heads(const sa_paged_cache* c, int32_t hq) {
   if (hq <= 0 || hq % c->num_kv_heads != 0 || hq / c->num_kv_heads > 1024) return SA_ERR_SHAPE;
   const int64_t rows = int64_t(c->batch) * c->num_kv_heads;
-  const int64_t chunks = (hq / c->num_kv_heads + 15) / 16;
+  const int64_t chunks = (hq / c->num_kv_heads + 31) / 32;
   const int64_t pieces = int64_t(c->page) * c->max_pages / 16;
   if (rows * chunks > (int64_t(1) << 24) || pieces > ((int64_t(1) << 31) - 1) / (rows * chunks))
     return SA_ERR_SHAPE;

@@ -60,7 +60,7 @@ using namespace sa_dev;
 using sa_paged::AttendArgs;
 
 constexpr int kTile = 128;             // tokens per tile
-constexpr int kChunk = 16;             // query heads of a row handled together
+constexpr int kMaxChunk = 32;          // most query heads of a row handled together
 constexpr int kInfo = 8;               // tile descriptions in flight
 constexpr float kMove = 8.f;           // how far a score may pass its reference
 constexpr int kJoinThreads = 512;
@@ -73,20 +73,21 @@ struct Cfg {
   static constexpr int kPanel = kTile * 128;          // bytes of one K/V panel
   static constexpr int kStage = kPanels * kPanel;
   // softmax: kGroups groups of four warps, kHeads heads of a token a thread
+  static constexpr int kChunk = GP < 16 ? 16 : GP;    // columns of S, rows of Q
   static constexpr int kHeads = GP < 16 ? 4 : 8;
   static constexpr int kGroups = GP / kHeads;
   static constexpr int kThreads = 64 + 128 * kGroups;
   // CTAs on a processor, the stages and Q tiles that then fit.  Tile j: K in
   // stage 2j % kStages, V in the next.
-  static constexpr int kPerSm = 2;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kPerSm = GP == 32 ? 1 : 2;
+  static constexpr int kStages = (D == 128 ? 6 : 12) / kPerSm;
   static constexpr int kQs = D == 128 && GP * PARTS > 32 ? 1 : 2;
-  static constexpr int kNS = 16;                      // columns of S
+  static constexpr int kNS = kChunk;                  // columns of S
   static constexpr int kNP = (GP * PARTS + 15) / 16 * 16;   // columns of O, rows of P
   static constexpr int kQ = kPanels * kChunk * 128;   // bytes of one Q tile
   static constexpr int kP = 2 * kNP * 128;            // bytes of P (two panels of 64 tokens)
   static constexpr uint32_t kO = 2 * kNS;             // TMEM column of O
-  static constexpr uint32_t kTmemCols = 128;
+  static constexpr uint32_t kTmemCols = GP == 32 ? 256 : 128;
   // V^T has 128 rows to the tensor core; at d = 64 the second 64 read from
   // 2 KB further on (their rows of O are not used): within shared memory, since
   // P and Q follow the ring
@@ -102,23 +103,24 @@ struct TileInfo {
 };
 enum { kFirst = 1, kLast = 2, kComplete = 4, kSecond = 8 };
 
+template <class C>
 struct Shared {
   // the barriers, in the order that the kernel's first threads initialise them
   uint64_t info_empty[kInfo];   // one arrival of the issuer and of each softmax warp
   uint64_t p_full;              // one of each softmax warp
   uint64_t info_full[kInfo];    // from here on: one arrival
-  uint64_t kv_full[6], kv_empty[6];
+  uint64_t kv_full[C::kStages], kv_empty[C::kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];
   uint64_t pv_done;
   uint64_t drain;
   TileInfo info[kInfo];
-  float red[2][4][8];  // [group][quarter][head]
-  int32_t scan[10];
+  float red[C::kGroups][4][C::kHeads];   // [group][quarter][head]
+  int32_t scan[C::kThreads / 32];
   int32_t u0, p0, len0;  // first row of the range, the units before it, its length
   uint32_t tmem_base;
   int abort;
-  int failed[2];       // set by a group's warp whose wait gave up
+  int failed[C::kGroups];  // set by a group's warp whose wait gave up
 };
 
 // Workspace: records, row log-sum-exps, partial states, scores.  A record is
@@ -131,17 +133,21 @@ struct Record {
 };
 struct Work {
   Record* rec;         // [ctas]
-  float* row_lse2;     // [U][16]
-  float2* part_ml;     // [ctas][2][16]
-  float* part_o;       // [ctas][2][16][d]
+  float* row_lse2;     // [U][chunk]
+  float2* part_ml;     // [ctas][2][chunk]
+  float* part_o;       // [ctas][2][chunk][d]
   float* scores;       // [rows][G][slots], base-2 exponents; only when accumulating
 };
+
+// Query heads of a row handled together: all up to 32, above that 32 at a time.
+int chunk_of(int G) { return G <= 16 ? 16 : kMaxChunk; }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t layout(Work* w, char* base, int64_t rows, int G, int64_t cap, int d, int ctas,
               bool accumulate) {
-  const int64_t U = rows * ((G + kChunk - 1) / kChunk);
+  const int chunk = chunk_of(G);
+  const int64_t U = rows * ((G + chunk - 1) / chunk);
   size_t at = 0;
   auto take = [&](size_t n) {
     char* p = base + at;
@@ -150,9 +156,9 @@ size_t layout(Work* w, char* base, int64_t rows, int G, int64_t cap, int d, int 
   };
   Work x;
   x.rec = reinterpret_cast<Record*>(take(size_t(ctas) * sizeof(Record)));
-  x.row_lse2 = reinterpret_cast<float*>(take(accumulate ? size_t(U) * kChunk * 4 : 0));
-  x.part_ml = reinterpret_cast<float2*>(take(size_t(ctas) * 2 * kChunk * 8));
-  x.part_o = reinterpret_cast<float*>(take(size_t(ctas) * 2 * kChunk * d * 4));
+  x.row_lse2 = reinterpret_cast<float*>(take(accumulate ? size_t(U) * chunk * 4 : 0));
+  x.part_ml = reinterpret_cast<float2*>(take(size_t(ctas) * 2 * chunk * 8));
+  x.part_o = reinterpret_cast<float*>(take(size_t(ctas) * 2 * chunk * d * 4));
   x.scores = reinterpret_cast<float*>(take(accumulate ? size_t(rows) * G * cap * 4 : 0));
   if (w) *w = x;
   return at;
@@ -165,6 +171,7 @@ struct Params {
   int32_t page_shift, max_pages, cap;
   int32_t bx_shift;            // log2 of the tokens of a unit (and of a TMA box)
   int32_t Hkv, Hq, G, HC, U;   // HC: head chunks of a row; U = rows * HC
+  int32_t chunk;               // heads of a chunk
   int32_t q_rows;              // heads of a Q box
   int32_t min_units;           // least units of a CTA
   int32_t by_row;              // records: one a row
@@ -187,7 +194,7 @@ __device__ __forceinline__ int32_t row_of(const Params& p, int32_t u) {
 }
 template <bool kOne>
 __device__ __forceinline__ int32_t head_of(const Params& p, int32_t u) {
-  return kOne || p.HC == 1 ? 0 : (u % p.HC) * kChunk;
+  return kOne || p.HC == 1 ? 0 : (u % p.HC) * p.chunk;
 }
 
 __device__ __forceinline__ int32_t units_of(const Params& p, int32_t len) {
@@ -250,12 +257,18 @@ __device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, volat
 // The barrier of one softmax group.
 template <int kGroups>
 __device__ __forceinline__ bool group_any(int grp, bool flag) {
+  if (kGroups > 3 && grp == 3) return bar_any<4, 128>(flag);
+  if (kGroups > 2 && grp == 2) return bar_any<3, 128>(flag);
   if (kGroups > 1 && grp == 1) return bar_any<2, 128>(flag);
   return bar_any<1, 128>(flag);
 }
 template <int kGroups>
 __device__ __forceinline__ void group_sync(int grp) {
-  if (kGroups > 1 && grp == 1)
+  if (kGroups > 3 && grp == 3)
+    bar_sync<4, 128>();
+  else if (kGroups > 2 && grp == 2)
+    bar_sync<3, 128>();
+  else if (kGroups > 1 && grp == 1)
     bar_sync<2, 128>();
   else
     bar_sync<1, 128>();
@@ -268,14 +281,16 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   using C = Cfg<D, GP, PARTS>;
   constexpr int kThreads = C::kThreads;
   constexpr int HP = C::kHeads;
-  constexpr bool kOne = GP < kChunk;
+  constexpr int kChunk = C::kChunk;
+  constexpr bool kOne = GP < kMaxChunk;
   constexpr bool kF32 = PARTS == 3;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   launch_dependents();
   uint8_t* sKV = smem_raw;
   uint8_t* sP = sKV + C::kStages * C::kStage;
   uint8_t* sQ = sP + C::kP;
-  Shared* sh = reinterpret_cast<Shared*>(sQ + C::kQs * C::kQ);
+  using Sh = Shared<C>;
+  Sh* sh = reinterpret_cast<Sh*>(sQ + C::kQs * C::kQ);
   volatile int* abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t cta = blockIdx.x;
@@ -294,11 +309,11 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
     sh->abort = 0;
-    sh->failed[0] = sh->failed[1] = 0;
+    for (int g = 0; g < C::kGroups; ++g) sh->failed[g] = 0;
     sh->u0 = sh->p0 = sh->len0 = 0;
   }
-  constexpr int kBars = 2 * kInfo + 1 + 12 + 6 + 2;
-  static_assert(offsetof(Shared, info) == kBars * sizeof(uint64_t) && kBars <= kThreads, "");
+  constexpr int kBars = 2 * kInfo + 1 + 2 * C::kStages + 6 + 2;
+  static_assert(offsetof(Sh, info) == kBars * sizeof(uint64_t) && kBars <= kThreads, "");
   if (tid < kBars) {
     mbar_init(&sh->info_empty[0] + tid, tid < kInfo    ? 1 + 4 * C::kGroups
                                         : tid == kInfo ? 4 * C::kGroups
@@ -892,7 +907,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   for (int x = 0; x < kVec; ++x) v[x] = 0.f;
 #pragma unroll 4
   for (int32_t k = way; k < rec.segs; k += kWays) {
-    const uint32_t at = (uint32_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * kChunk + h;
+    const uint32_t at = (uint32_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * p.chunk + h;
     const float2 ml = p.w.part_ml[at];
     float o[kVec];
     if constexpr (kVec == 4) {
@@ -940,7 +955,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (x == 0) {
     const float lse2 = (M == -INFINITY ? 0.f : M) + log2f(L);
     if (p.lse) p.lse[bh] = lse2 * 0.6931471805599453f;
-    if (p.weights_out) p.w.row_lse2[size_t(rec.u) * kChunk + h] = lse2;
+    if (p.weights_out) p.w.row_lse2[size_t(rec.u) * p.chunk + h] = lse2;
   }
 }
 
@@ -958,10 +973,10 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_co
   for (int i = 0; i < kWeightSteps; ++i) sum[i] = 0.f;
   if (t0 >= n) return;
   const float* s = p.w.scores + size_t(r) * p.G * p.cap;
-  const float* lse2 = p.w.row_lse2 + size_t(r) * p.HC * kChunk;
+  const float* lse2 = p.w.row_lse2 + size_t(r) * p.HC * p.chunk;
 #pragma unroll 4
   for (int32_t h = 0; h < p.G; ++h) {
-    const float l = lse2[h];                       // chunks of 16 heads lie end to end
+    const float l = lse2[h];                       // chunks of heads lie end to end
 #pragma unroll
     for (int i = 0; i < kWeightSteps; ++i) {
       const int32_t t = t0 + i * kWeightThreads;
@@ -1021,7 +1036,7 @@ template <int D, int GP, int PARTS>
 cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_failed) {
   using C = Cfg<D, GP, PARTS>;
   constexpr int kRing = C::kStages * C::kStage;
-  constexpr int kSmem = kRing + C::kP + C::kQs * C::kQ + int(sizeof(Shared));
+  constexpr int kSmem = kRing + C::kP + C::kQs * C::kQ + int(sizeof(Shared<C>));
   static_assert(C::kPerSm * (kSmem + 1024) <= 233472, "shared memory budget");
   const sa_paged_cache& c = a.c;
   const int64_t rows = int64_t(c.batch) * c.num_kv_heads;
@@ -1029,8 +1044,9 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.page_shift = log2i(c.page);
   p.bx_shift = c.page < 32 ? p.page_shift : 5;
   p.G = a.Hq / c.num_kv_heads;
-  p.HC = (p.G + kChunk - 1) / kChunk;
-  p.q_rows = p.G < kChunk ? p.G : kChunk;
+  p.chunk = C::kChunk;
+  p.HC = (p.G + p.chunk - 1) / p.chunk;
+  p.q_rows = p.G < p.chunk ? p.G : p.chunk;
   CUtensorMap tq, tk, tv;
   if (!make_map(&tq, a.q, D, a.Hq, c.batch, a.qsh, a.qsb, p.q_rows) ||
       !make_map(&tk, c.k_pages, D, c.page, c.num_pages, D, c.k_page_stride, 1 << p.bx_shift) ||
@@ -1096,11 +1112,13 @@ cudaError_t launch_d(const AttendArgs& a, int sms, cudaStream_t st, bool* encode
   if (a.out_f32) {
     if (G <= 4) return launch<D, 4, 3>(a, sms, st, encode_failed);
     if (G <= 8) return launch<D, 8, 3>(a, sms, st, encode_failed);
-    return launch<D, 16, 3>(a, sms, st, encode_failed);
+    if (G <= 16) return launch<D, 16, 3>(a, sms, st, encode_failed);
+    return launch<D, 32, 3>(a, sms, st, encode_failed);
   }
   if (G <= 4) return launch<D, 4, 2>(a, sms, st, encode_failed);
   if (G <= 8) return launch<D, 8, 2>(a, sms, st, encode_failed);
-  return launch<D, 16, 2>(a, sms, st, encode_failed);
+  if (G <= 16) return launch<D, 16, 2>(a, sms, st, encode_failed);
+  return launch<D, 32, 2>(a, sms, st, encode_failed);
 }
 
 }  // namespace
@@ -1109,7 +1127,7 @@ namespace sa_paged {
 
 size_t attend_workspace(const sa_paged_cache& c, int32_t Hq, bool accumulate, int sms) {
   return layout(nullptr, nullptr, int64_t(c.batch) * c.num_kv_heads, Hq / c.num_kv_heads,
-                int64_t(c.page) * c.max_pages, c.head_dim, sms * 4, accumulate);
+                int64_t(c.page) * c.max_pages, c.head_dim, sms * 2, accumulate);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_failed) {
