@@ -79,9 +79,9 @@ struct Cfg {
   static constexpr int kThreads = 64 + 128 * kGroups;
   // CTAs on a processor, the stages and Q tiles that then fit.  Tile j: K in
   // stage 2j % kStages, V in the next.
-  static constexpr int kPerSm = GP == 32 ? 1 : 2;
+  static constexpr int kPerSm = GP == 32 || (D == 128 && GP * PARTS == 48) ? 1 : 2;
   static constexpr int kStages = (D == 128 ? 6 : 12) / kPerSm;
-  static constexpr int kQs = D == 128 && GP * PARTS > 32 ? 1 : 2;
+  static constexpr int kQs = GP >= 16 ? 1 : 2;
   static constexpr int kNS = kChunk;                  // columns of S
   static constexpr int kNP = (GP * PARTS + 15) / 16 * 16;   // columns of O, rows of P
   static constexpr int kQ = kPanels * kChunk * 128;   // bytes of one Q tile
@@ -115,7 +115,10 @@ struct Shared {
   uint64_t pv_done;
   uint64_t drain;
   TileInfo info[kInfo];
-  float red[C::kGroups][4][C::kHeads];   // [group][quarter][head]
+  // maxima by tile parity, sums by segment parity, [group][quarter][head]: a
+  // group's barrier lies between any use of a buffer and the next writing of it
+  float maxima[2][C::kGroups][4][C::kHeads];
+  float sums[2][C::kGroups][4][C::kHeads];
   int32_t scan[C::kThreads / 32];
   int32_t u0, p0, len0;  // first row of the range, the units before it, its length
   uint32_t tmem_base;
@@ -692,6 +695,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + grp * HP;
     const float c = p.scale_log2;
     float m[HP], l[HP], o[HP];
+    uint32_t seg_in = 0, seg = 0;              // segments summed, and stored
     TileInfo prev{0, 0, 0, 0}, it{0, 0, 0, 0};
     bool ok = true;
     // the description of tile j
@@ -731,9 +735,18 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
             s[h] = (row < it.n && h < gc) ? s[h] * c : -INFINITY;
-            if (!(it.flags & kFirst)) need |= s[h] > m[h] + kMove;
+            if (!(it.flags & kFirst)) need |= s[h] > m[h] + kMove;   // (NaN: no)
           }
-          if (it.flags & kFirst) need = true;
+          // a segment's first tile sets the reference: its maxima are there
+          // when the barrier is passed
+          if (it.flags & kFirst) {
+            need = true;
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+              const float y = warp_max(s[h]);
+              if (lane == 0) sh->maxima[j & 1][grp][quarter][h] = y;
+            }
+          }
           // the last product step reads value rows up to the next 16th
           if (grp == 0 && row >= it.n && row < ((it.n + 15) & ~15)) {
             uint4* v = reinterpret_cast<uint4*>(sKV + (x % C::kStages) * C::kStage + row * 128);
@@ -761,16 +774,8 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
         }
         if (prev.flags & kLast) {
           // ---- the end of a segment
-#pragma unroll
-          for (int h = 0; h < HP; ++h) {
-#pragma unroll
-            for (int w = 16; w; w >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
-          }
-          if (lane == 0) {
-#pragma unroll
-            for (int h = 0; h < HP; ++h) sh->red[grp][quarter][h] = l[h];
-          }
-          group_sync<C::kGroups>(grp);
+          const float(*sum)[HP] = sh->sums[seg & 1][grp];
+          ++seg;
           const int32_t r = row_of<kOne>(p, prev.u), h0 = head_of<kOne>(p, prev.u) + grp * HP;
           const size_t bh = size_t(r / p.Hkv) * p.Hq + size_t(r % p.Hkv) * p.G + h0;
           const size_t part =
@@ -782,8 +787,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
             if (row == h) mr = m[h];
             if (h0 + h < p.G && row < D) {
               if (whole) {
-                const float L = (sh->red[grp][0][h] + sh->red[grp][1][h]) +
-                                (sh->red[grp][2][h] + sh->red[grp][3][h]);
+                const float L = (sum[0][h] + sum[1][h]) + (sum[2][h] + sum[3][h]);
                 store_out<kF32>(p, (bh + h) * D + row, __fdividef(o[h], L));
               } else {
                 p.w.part_o[(part + h) * D + row] = o[h];
@@ -791,8 +795,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
             }
           }
           if (row < HP && h0 + row < p.G) {
-            const float L = (sh->red[grp][0][row] + sh->red[grp][1][row]) +
-                            (sh->red[grp][2][row] + sh->red[grp][3][row]);
+            const float L = (sum[0][row] + sum[1][row]) + (sum[2][row] + sum[3][row]);
             if (whole) {
               const float lse2 = (mr == -INFINITY ? 0.f : mr) + log2f(L);
               if (p.lse) p.lse[bh + row] = lse2 * 0.6931471805599453f;
@@ -802,37 +805,30 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
             }
           }
           if (whole && p.by_row && grp == 0 && row == 0) p.w.rec[prev.u] = Record{-1, 0, 0, 0};
-          group_sync<C::kGroups>(grp);              // red is read before it is written again
         }
       }
       if (it.n == 0) break;
-      if (it.flags & kFirst) {
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          m[h] = -INFINITY;
-          l[h] = 0.f;
-          o[h] = 0.f;
-        }
-      }
       if (any) {
         // a new reference: the larger of the old one and the tile's maximum
+        float(*top)[HP] = sh->maxima[j & 1][grp];
+        const bool first = (it.flags & kFirst) != 0;
+        if (!first) {
 #pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          const float x = warp_max(s[h]);
-          if (lane == 0) sh->red[grp][quarter][h] = x;
+          for (int h = 0; h < HP; ++h) {
+            const float x = warp_max(s[h]);
+            if (lane == 0) top[quarter][h] = x;
+          }
+          group_sync<C::kGroups>(grp);
         }
-        group_sync<C::kGroups>(grp);
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          const float mn =
-              fmaxf(m[h], fmaxf(fmaxf(sh->red[grp][0][h], sh->red[grp][1][h]),
-                                fmaxf(sh->red[grp][2][h], sh->red[grp][3][h])));
-          const float alpha = mn == m[h] ? 1.f : ex2(m[h] - mn);
-          l[h] *= alpha;
-          o[h] *= alpha;
+          const float x = fmaxf(fmaxf(top[0][h], top[1][h]), fmaxf(top[2][h], top[3][h]));
+          const float mn = first ? x : fmaxf(m[h], x);
+          const float alpha = first ? 0.f : mn == m[h] ? 1.f : ex2(m[h] - mn);
+          l[h] = first ? 0.f : l[h] * alpha;
+          o[h] = first ? 0.f : o[h] * alpha;
           m[h] = mn;
         }
-        group_sync<C::kGroups>(grp);
       }
       if (p.weights_out && row < it.n) {
         const int32_t r = row_of<kOne>(p, it.u), h0 = head_of<kOne>(p, it.u) + grp * HP;
@@ -866,6 +862,19 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->p_full);
+      if (it.flags & kLast) {
+        // the segment's sums, while its last product runs
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+#pragma unroll
+          for (int w = 16; w; w >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < HP; ++h) sh->sums[seg_in & 1][grp][quarter][h] = l[h];
+        }
+        ++seg_in;
+      }
       prev = it;
       fail = !describe(j + 1);
     }

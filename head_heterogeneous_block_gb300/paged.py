@@ -251,7 +251,7 @@ class PagedCache:
                self._own(positions_out, torch.int32, shape, "positions_out"))
         ws = self._workspace(("evict",))
         status = _lib.sparse_attn_paged_evict(
-            self._ref, self._keep(*keep), sinks, recent, lens, w, pos, ws, self._ws_bytes,
+            self._ref, self._keep(*map(int, keep)), sinks, recent, lens, w, pos, ws, self._ws_bytes,
             self._status, self._handle(stream))
         if status:
             _check(status, "sparse_attn_paged_evict")

@@ -645,3 +645,152 @@ def test_paged_decode_layer_refusals(env):
     layer.release(0)
     layer.admit(1, k, k)
     assert layer.lens.tolist() == [[0, 0], [70, 70]]
+
+
+def test_attend_sequences_that_share_pages(env):
+    # a common prefix: the same page numbers in two rows' tables, and twice in
+    # one row's
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(51, [200, 200, 200], 1, 128, 32)
+    c["table"][1, 0, :4] = c["table"][0, 0, :4]
+    c["table"][2, 0, 1] = c["table"][2, 0, 0]
+    _attend(env, c, 8, weights=True)
+
+
+def test_two_caches_at_the_same_time_on_two_streams(env):
+    from tests import _paged as P
+    sa, torch = env
+    cases = [P.random_cache(52, [3000, 700], 2, 128, 16), P.random_cache(53, [900, 4100, 5], 2, 64, 64)]
+    qs = [_q(torch, 20 + i, c["lens"].shape[0], 8, c["k"].shape[2]) for i, c in enumerate(cases)]
+    made = [P.to_gpu(c, sa) for c in cases]
+    gq = [q.cuda() for q in qs]
+    outs = [torch.empty(q.shape, device="cuda") for q in qs]
+    ws = [torch.zeros_like(dev["weights"]) for dev, _ in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for (dev, cache), q, o, w, st in zip(made, gq, outs, ws, streams):
+            cache.attend(q, out=o, weights_out=w, stream=st)
+    torch.cuda.synchronize()
+    for c, (dev, cache), q, o, w in zip(cases, made, qs, outs, ws):
+        assert int(cache.dev_status.item()) == 0
+        P.check_attend(c, q, o, None, w)
+
+
+def test_two_graphs_that_share_a_cache(env):
+    # each keeps nothing in the workspace that the other's replay could spoil
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(54, [2500, 100], 2, 128, 32)
+    dev, cache = P.to_gpu(c, sa, num_q_heads=16)
+    qs = [_q(torch, 30, 2, 8, 128), _q(torch, 31, 2, 16, 128)]
+    gq = [q.cuda() for q in qs]
+    outs = [torch.empty(q.shape, device="cuda") for q in qs]
+    ws = [torch.zeros_like(dev["weights"]) for _ in qs]
+    for q, o, w in zip(gq, outs, ws):
+        cache.attend(q, out=o, weights_out=w)
+    graphs = []
+    for q, o, w in zip(gq, outs, ws):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cache.attend(q, out=o, weights_out=w)
+        graphs.append(g)
+    for o in outs:
+        o.fill_(9)
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    assert int(cache.dev_status.item()) == 0
+    for q, o, w in zip(qs, outs, ws):
+        P.check_attend(c, q, o, None, w)
+
+
+def test_evict_captured_and_replayed(env):
+    # a captured eviction works on the lengths and weights of its replay
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(55, [[300, 80], [120, 511]], 2, 64, 32, junk=False)
+    dev, cache = P.to_gpu(c, sa)
+    keep = [100, 64]
+    graph = torch.cuda.CUDAGraph()
+    cache.evict([2000, 2000])                      # keeps everything
+    with torch.cuda.graph(graph):
+        cache.evict(keep, 4, 8)
+    assert torch.equal(dev["lens"].cpu(), c["lens"])
+    for step in range(2):
+        if step:
+            dev["lens"].copy_(torch.tensor([[90, 64], [101, 65]], dtype=torch.int32))
+            dev["weights"].copy_(torch.rand(dev["weights"].shape, device="cuda"))
+        s = {n: dev[n].cpu() for n in ("k", "v", "lens", "weights", "positions")}
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = op.evict(P.f64(s["k"]), P.f64(s["v"]), c["table"].numpy(), s["lens"].numpy(),
+                       s["weights"].numpy(), s["positions"].numpy(), keep, 4, 8)
+        assert np.array_equal(P.f64(dev["k"]), ref[0]) and np.array_equal(P.f64(dev["v"]), ref[1])
+        assert np.array_equal(dev["lens"].cpu().numpy(), ref[2])
+        assert np.array_equal(dev["weights"].cpu().numpy(), ref[3])
+        assert np.array_equal(dev["positions"].cpu().numpy(), ref[4])
+    assert int(cache.dev_status.item()) == 0
+
+
+@pytest.mark.parametrize("lens,hkv", [([8192, 8191], 2), ([8193, 12000], 1), ([70000], 1),
+                                      ([262144], 1)])
+def test_evict_row_lengths_at_the_kernels_borders(env, lens, hkv):
+    # one CTA up to 8192 slots, clusters of 2 to 8 above; few rows with much to
+    # move take a second launch.  Compared through the positions, which name
+    # the tokens.
+    from oracle import paged as op
+    sa, torch = env
+    b, page, d = len(lens), 32, 64
+    cap = -(-max(lens) // page) * page
+    g = torch.Generator().manual_seed(cap)
+    pages = b * hkv * cap // page
+    k = torch.randn(pages, page, d, device="cuda").bfloat16()
+    v = torch.randn(pages, page, d, device="cuda").bfloat16()
+    table = torch.randperm(pages, generator=g).int().view(b, hkv, -1)
+    w = torch.randint(0, 5000, (b, hkv, cap), generator=g).float()      # many ties
+    pos = torch.arange(cap, dtype=torch.int32).expand(b, hkv, cap).contiguous()
+    n = torch.tensor(lens, dtype=torch.int32)[:, None].expand(b, hkv).contiguous()
+    dev = [t.cuda() for t in (table, n, w, pos)]
+    cache = sa.PagedCache(k, v, dev[0], dev[1], weights=dev[2], positions=dev[3])
+    k0, v0 = k.clone(), v.clone()
+    for keep in (cap * 2 // 3, 777):
+        before = [x.cpu() for x in (dev[1], dev[2], dev[3])]
+        cache.evict([keep] * hkv, 4, 32)
+        torch.cuda.synchronize()
+        assert int(cache.dev_status.item()) == 0
+        for x in range(b):
+            for y in range(hkv):
+                m0 = int(before[0][x, y])
+                kept = op.kept_slots(before[1][x, y, :m0].numpy(), before[2][x, y, :m0].numpy(),
+                                     min(m0, keep), 4, 32)
+                m = len(kept)
+                slots = list(range(m))
+                have = set(kept)
+                for hole, src in zip([t for t in range(m) if t not in have],
+                                     [t for t in kept if t >= m]):
+                    slots[hole] = src
+                assert int(dev[1][x, y]) == m
+                assert torch.equal(dev[2][x, y, :m].cpu(), before[1][x, y][slots])
+                assert torch.equal(dev[3][x, y, :m].cpu(), before[2][x, y][slots])
+                # the rows of the pools follow the positions (slots at first)
+                at = dev[0][x, y].long()
+                now = torch.arange(m, device="cuda")
+                was = dev[3][x, y, :m].long()
+                assert torch.equal(k[at[now // page], now % page], k0[at[was // page], was % page])
+                assert torch.equal(v[at[now // page], now % page], v0[at[was // page], was % page])
+
+
+def test_evict_equal_positions_all_forced(env):
+    # more forced tokens than the budget: the lower slots stay
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(56, [200], 1, 64, 16, junk=False)
+    c["positions"].fill_(3)
+    dev, cache = P.to_gpu(c, sa)
+    k0 = dev["k"].clone()
+    cache.evict([50], 0, 4)
+    assert int(dev["lens"]) == 50 and torch.equal(dev["k"], k0)
+    assert torch.equal(dev["weights"].cpu(), c["weights"])
