@@ -99,14 +99,16 @@ class PagedCache:
     def _workspace(self, key):
         need = self._need_ws.get(key)
         if need is None:
-            with torch.cuda.device(self.device):
-                need = (sparse_attn_paged_evict_workspace_size(self.desc) if key[0] == "evict" else
-                        sparse_attn_paged_attend_workspace_size(self.desc, key[1], key[2]))
+            if torch.cuda.current_device() != self._index:
+                with torch.cuda.device(self.device):
+                    return self._workspace(key)
+            need = (sparse_attn_paged_evict_workspace_size(self.desc) if key[0] == "evict" else
+                    sparse_attn_paged_attend_workspace_size(self.desc, key[1], key[2]))
             self._need_ws[key] = need
         if need > self._ws_bytes:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             self._ws_bytes = need
-            self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
+            self._ws_stream = _raw_stream(self._index)
         return self._ws.data_ptr()
 
     def _handle(self, stream):
