@@ -669,7 +669,7 @@ cudaError_t launch(const EvictArgs& a, int sms, cudaStream_t st) {
     // left and a slice is worth a CTA's while
     int ranks = 2;
     while (ranks < kMaxRanks && ((cap + ranks - 1) / ranks > kMaxSlice ||
-                                 (rows * ranks < 2 * sms && cap / ranks > 2048)))
+                                 (rows * ranks < sms && cap / ranks > 2048)))
       ranks *= 2;
     const int64_t slice = ((cap + ranks - 1) / ranks + 31) & ~int64_t(31);
     if (rows * ranks > INT32_MAX) return cudaErrorInvalidValue;
