@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
       is_v ? static_cast<const __nv_bfloat16*>(a.v_new) + b * a.vs[0] + g * a.vs[1] + x
            : static_cast<const __nv_bfloat16*>(a.k_new) + b * a.ks[0] + g * a.ks[1] + x;
   const int64_t ts = is_v ? a.vs[2] : a.ks[2];
+  const int shift = __ffs(a.c.page) - 1;        // pages are powers of two
   __nv_bfloat16* pool = static_cast<__nv_bfloat16*>(is_v ? a.c.v_pages : a.c.k_pages) + x;
   const int64_t stride = is_v ? a.c.v_page_stride : a.c.k_page_stride;
   uint4 val[kSteps];
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
     const int32_t t = t0 + i * kPer + sub;
     if (t < m) {
       val[i] = *reinterpret_cast<const uint4*>(src + t * ts);
-      page[i] = table[(len + t) / a.c.page];
+      page[i] = table[(len + t) >> shift];
     }
   }
   bool bad = false;
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
         bad = true;
       else
         *reinterpret_cast<uint4*>(pool + page[i] * stride +
-                                  int64_t((len + t) % a.c.page) * D) = val[i];
+                                  int64_t((len + t) & (a.c.page - 1)) * D) = val[i];
     }
   }
   if (bad) atomicOr(a.dev_status, SA_DEV_BAD_INDEX);

@@ -86,12 +86,13 @@ struct Mover {
     const int lane = threadIdx.x & 31;
     const int32_t cap = a.c.page * a.c.max_pages;
     const int32_t* table = a.c.table + r * a.c.max_pages;
+    const int shift = __ffs(a.c.page) - 1;              // pages are powers of two
     int32_t sp = -1, tp = -1, so = 0, to = 0;
     if (s >= 0) {
-      sp = table[s / a.c.page];
-      tp = table[t / a.c.page];
-      so = s % a.c.page;
-      to = t % a.c.page;
+      sp = table[s >> shift];
+      tp = table[t >> shift];
+      so = s & (a.c.page - 1);
+      to = t & (a.c.page - 1);
       a.weights_out[r * cap + t] = a.c.weights[r * cap + s];
       if (a.positions_out) a.positions_out[r * cap + t] = a.c.positions[r * cap + s];
       if (sp < 0 || sp >= a.c.num_pages || tp < 0 || tp >= a.c.num_pages) {
