@@ -21,7 +21,7 @@ namespace {
 using sa_paged::AppendArgs;
 
 constexpr int kSteps = 8;
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 // The number of tokens row r appends, clamped to the free slots.
 __device__ __forceinline__ int32_t new_tokens(const AppendArgs& a, int64_t r, int32_t len,
