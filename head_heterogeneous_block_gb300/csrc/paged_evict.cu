@@ -48,7 +48,7 @@ constexpr int kMaxSlice = 32768;       // keys of a cluster's CTA: 128 KB of sha
 constexpr int kRowKeys = 16;           // keys of a thread where a CTA has the whole row
 constexpr int kRowSlots = kThreads * kRowKeys;
 constexpr int kBins = 2048;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 constexpr int kMaxRanks = 8;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -660,8 +660,12 @@ cudaError_t launch(const EvictArgs& a, int sms, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cudaError_t e;
   if (cap <= kRowSlots) {
-    // one launch where the rows fill the processors, or have little to move
-    const bool moves_here = rows >= sms || most <= 256;
+    // One launch where a row can have little to move, or the rows fill the
+    // processors and can have only a kilotoken each.  (256 rows of up to 950
+    // possible and 32 actual moves: 8.5 us, and 15.5 in two launches, whose
+    // blocks are one for each possible piece of a row; 512 rows of 2048 moves:
+    // 109 us, and 106 in two; 16 rows of up to 1024 moves: 15.9, and 8.6.)
+    const bool moves_here = most <= (rows >= sms ? 1024 : 256);
     cfg.gridDim = dim3(unsigned(rows));
     e = cudaLaunchKernelEx(&cfg, evict_row_kernel<D>, a, int(moves_here));
     if (e != cudaSuccess || moves_here) return e;
