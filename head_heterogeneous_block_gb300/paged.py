@@ -17,6 +17,9 @@ from . import (SA_DTYPE_BF16, SA_DTYPE_F32, PagedCacheDesc, _check, _lib,
 
 _I64x3 = ctypes.c_int64 * 3
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_append, _attend, _evict = (_lib.sparse_attn_paged_append, _lib.sparse_attn_paged_attend,
+                            _lib.sparse_attn_paged_evict)
 
 
 class PagedCache:
@@ -85,31 +88,29 @@ class PagedCache:
         self._keep = ctypes.c_int32 * h
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._status = self.dev_status.data_ptr()
-        self._ws = None
-        self._ws_bytes = 0
+        self._ws, self._ws_ptr, self._ws_bytes = None, None, 0
         self._ws_stream = _raw_stream(self._index)
-        self._need_ws = {}
+        self._sized = set()
         if num_q_heads is not None:
-            self._workspace(("attend", num_q_heads, weights is not None))
+            self._size(num_q_heads, weights is not None)
         if weights is not None:
-            self._workspace(("evict",))
+            self._size()
 
     # -- helpers (a step's calls are short: checks are written out where a
     # call per check, or a message built for nothing, would cost more)
-    def _workspace(self, key):
-        need = self._need_ws.get(key)
-        if need is None:
-            if torch.cuda.current_device() != self._index:
-                with torch.cuda.device(self.device):
-                    return self._workspace(key)
-            need = (sparse_attn_paged_evict_workspace_size(self.desc) if key[0] == "evict" else
-                    sparse_attn_paged_attend_workspace_size(self.desc, key[1], key[2]))
-            self._need_ws[key] = need
+    def _size(self, num_q_heads=None, accumulate=False):
+        """Grow the workspace to what ``attend`` with these arguments (None:
+        ``evict``) needs."""
+        if _current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self._size(num_q_heads, accumulate)
+        need = (sparse_attn_paged_evict_workspace_size(self.desc) if num_q_heads is None else
+                sparse_attn_paged_attend_workspace_size(self.desc, num_q_heads, accumulate))
         if need > self._ws_bytes:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            self._ws_bytes = need
+            self._ws_ptr, self._ws_bytes = self._ws.data_ptr(), need
             self._ws_stream = _raw_stream(self._index)
-        return self._ws.data_ptr()
+        self._sized.add((num_q_heads, accumulate))
 
     def _handle(self, stream):
         """The stream's handle; the cache's device is current."""
@@ -141,7 +142,7 @@ class PagedCache:
         of 8, d contiguous) to every row of sequence b, at positions
         ``start[b]``, ``start[b]`` + 1, ... (default: their slots).  The new
         lengths go to ``lens_out`` (default: ``lens``)."""
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.append(k, v, counts, start, lens_out, stream)
         b, h, tokens, d = k.shape if k.dim() == 4 else (0, 0, 0, 0)
@@ -169,9 +170,9 @@ class PagedCache:
             start = self._own(start, torch.int32, self._shape_b, "start")
         lens = (self.desc.lens if lens_out is None else
                 self._own(lens_out, torch.int32, self._shape_lens, "lens_out"))
-        status = _lib.sparse_attn_paged_append(
-            self._ref, k.data_ptr(), v.data_ptr(), _I64x3(k0, k1, k2), _I64x3(v0, v1, v2), tokens,
-            counts, start, lens, self._status, self._handle(stream))
+        status = _append(self._ref, k.data_ptr(), v.data_ptr(), _I64x3(k0, k1, k2),
+                         _I64x3(v0, v1, v2), tokens, counts, start, lens, self._status,
+                         self._handle(stream))
         if status:
             _check(status, "sparse_attn_paged_append")
 
@@ -183,7 +184,7 @@ class PagedCache:
         given.  ``accumulate`` (default: when the cache has weights) adds each
         token's probability, summed over the row's heads, to its weight, into
         ``weights_out`` (default: ``weights``)."""
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.attend(q, out, lse, weights_out, accumulate, stream)
         if q.dtype is not torch.bfloat16:
@@ -220,10 +221,10 @@ class PagedCache:
                  self._own(weights_out, torch.float32, self.weights.shape, "weights_out"))
         elif weights_out is not None:
             raise ValueError("weights_out needs accumulate")
-        ws = self._workspace(("attend", hq, bool(accumulate)))
-        status = _lib.sparse_attn_paged_attend(
-            self._ref, q.data_ptr(), q0, q1, hq, o, o_dtype, lse, w, ws, self._ws_bytes,
-            self._status, self._handle(stream))
+        if (hq, w is not None) not in self._sized:
+            self._size(hq, w is not None)
+        status = _attend(self._ref, q.data_ptr(), q0, q1, hq, o, o_dtype, lse, w, self._ws_ptr,
+                         self._ws_bytes, self._status, self._handle(stream))
         if status:
             _check(status, "sparse_attn_paged_attend")
         return out
@@ -234,7 +235,7 @@ class PagedCache:
         first ``sinks`` positions, the last ``recent`` ones, then the largest
         weights.  The new state goes to ``lens_out``, ``weights_out`` and
         ``positions_out`` (default: the cache's own tensors)."""
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.evict(keep, sinks, recent, lens_out, weights_out, positions_out,
                                   stream)
@@ -251,10 +252,8 @@ class PagedCache:
              self._own(weights_out, torch.float32, shape, "weights_out"))
         pos = (self.desc.positions if positions_out is None else
                self._own(positions_out, torch.int32, shape, "positions_out"))
-        ws = self._workspace(("evict",))
-        status = _lib.sparse_attn_paged_evict(
-            self._ref, self._keep(*map(int, keep)), sinks, recent, lens, w, pos, ws, self._ws_bytes,
-            self._status, self._handle(stream))
+        status = _evict(self._ref, self._keep(*map(int, keep)), sinks, recent, lens, w, pos,
+                        self._ws_ptr, self._ws_bytes, self._status, self._handle(stream))
         if status:
             _check(status, "sparse_attn_paged_evict")
 
