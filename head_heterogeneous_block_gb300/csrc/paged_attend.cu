@@ -6,33 +6,34 @@
 // as the arithmetic stays out of the way.  At G of 7 or 8 that is too much for
 // the CUDA cores at full bandwidth, so both products run on the tensor cores
 // with the tokens (then the value dimensions) as the 128 rows of the tile and
-// the query heads as its 16 columns:
+// the query heads as its 16 columns (32 for G above 16):
 //
-//   S^T [128 tokens x 16 heads] = K [128 x d] Q^T        K and Q from shared memory
-//   O^T [d x heads]             = V^T [d x 128] P^T      V (transposed by its
-//                                                        descriptor) and P from shared memory
+//   S^T [128 tokens x heads] = K [128 x d] Q^T        K and Q from shared memory
+//   O^T [d x heads]          = V^T [d x 128] P^T      V (transposed by its
+//                                                     descriptor) and P from shared memory
 //
-// Split.  The tokens of all rows (sequence, KV head, and for groups above 16
-// heads a chunk of 16 of them) are laid end to end in units of `bx` tokens and
-// cut into equal ranges, one per CTA, one CTA per processor: the lengths
+// Split.  The tokens of all rows (sequence, KV head, and for groups above 32
+// heads a chunk of 32 of them) are laid end to end in units of 16 or 32 tokens
+// and cut into equal ranges, one per CTA, two CTAs per processor: the lengths
 // differ freely between rows and no processor waits for the longest.  A row
 // that lies in one range is finished there; a row that is cut leaves one
 // partial state (maximum, sum, unnormalised output) per range, which the join
 // kernel combines in range order.  Each CTA finds its range by a scan of the
 // lengths, so a captured launch follows the lengths of its time.
 //
-// Roles of a CTA's six warps:
+// Roles of a CTA's warps:
 //   warp 0     producer: walks the range row by row in tiles of 128 tokens,
 //              looks pages up (the next tile's while waiting for room) and
 //              issues TMA loads of each page's piece of K and of V into a ring
-//              of stages, 32 KB each at d = 128, so that about 128 KB are in
-//              flight while one tile is worked on.
-//   warp 1     issues both products.
-//   warps 2-5  softmax and output: a thread owns one token of S (all heads)
-//              and one dimension of O (all heads).  Weights are 2^(s - m) with
-//              a reference m per head that is moved only when a score passes
-//              it by 8 (in powers of two): then, and at a row's first tile,
-//              the tile's maxima are exchanged.  m cancels in the end.
+//              of stages, three of 32 KB at d = 128, so that the processor's
+//              two CTAs have about 128 KB in flight while they work.
+//   warp 1     issues both products, each as soon as what it reads is there.
+//   others     softmax and output, in groups of four warps: a thread owns one
+//              token of S and one dimension of O, for the 4 (8 above G = 8)
+//              heads of its group.  Weights are 2^(s - m) with a reference m
+//              per head that is moved only when a score passes it by 8 (in
+//              powers of two); m cancels in the end.  A tile has one barrier
+//              a group, before which all its waits lie.
 //
 // The weights enter the tensor core in bf16, split in two parts (hi + lo) for
 // bf16 output and in three for fp32 output, as so many groups of columns of
@@ -43,6 +44,20 @@
 // -infinity, and their value rows are zeroed in shared memory up to the next
 // multiple of 16, where the product stops; so nothing a page holds behind a
 // row's length is ever used.
+//
+// Accumulating weights: the scores (in base 2) go to the workspace, 4G bytes a
+// token, and a third launch adds 2^(s - lse), summed over the heads, to each
+// token's weight once every lse is known.
+//
+// Measured (GB300, copy rate 6783 GB/s, read-only traffic goes a little
+// higher): 16 sequences of 64K tokens, 28/4 heads, 2.1 GB: 319 us, 99%; one of
+// 128K, 64/8 heads, 537 MB: 87 us, 91%.  The rest is a fixed 9 us or so: the
+// chain lengths -> page table -> first keys with a cold instruction cache
+// (3 us), the last tile's softmax and store (1 us), the join (2.8 us); it is
+// all there is of one 700-token sequence (8.8 us).  One CTA per processor with
+// twice the stages came 4% (d = 128) to 60% (d = 64) slower, three or four 15
+// to 30% (d = 64); pieces of 64 or 128 tokens instead of 32 the same, of 16
+// tokens 1 to 12% slower.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -894,7 +909,9 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
 
 // Block (record, head): the join of a row's partial states.  Sixteen warps take
 // every sixteenth state each and bring them to their own maximum; the sixteen
-// results are brought to the row's and added in warp order.
+// results are brought to the row's and added in warp order.  A chain of three
+// reads (record, state, nothing else waits): 2.8 us from the end of the first
+// launch at any size, of which the launch is about 1.
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = D / 32;                     // elements of a lane
@@ -969,7 +986,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 // Block (piece of a row's slots, row): every token's probabilities, summed
-// over the row's heads, added to its weight.
+// over the row's heads, added to its weight.  4G + 8 bytes a token; 128 rows of
+// 4352 tokens and 4 heads (13 MB): 4.4 us after the join.
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ Params p,
                                                                  int32_t pieces) {
   launch_dependents();
