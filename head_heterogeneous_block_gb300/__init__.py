@@ -469,8 +469,9 @@ def sparse_attn_paged_evict(cache: PagedCacheDesc, keep, sinks: int, recent: int
                             stream=None):
     """Evict by accumulated weight; ``keep`` holds the tokens to keep per KV
     head (host ints)."""
-    if len(keep) != cache.num_kv_heads:
-        raise ValueError("keep must hold one budget per KV head")
+    keep = [int(k) for k in keep]
+    if len(keep) != cache.num_kv_heads or min(keep) < 0 or max(keep) >= 2**31:
+        raise ValueError("keep must hold one 32-bit budget per KV head")
     _check(_lib.sparse_attn_paged_evict(ctypes.byref(cache), (ctypes.c_int32 * len(keep))(*keep),
                                         sinks, recent, _ptr(lens_out), _ptr(weights_out),
                                         _ptr(positions_out), _ptr(ws), ws_bytes,

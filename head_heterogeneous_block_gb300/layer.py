@@ -280,7 +280,8 @@ class PagedDecodeLayer:
     up serve others.
 
     Calls are ordered on one stream: the current one, or the one of the
-    caller's ``with torch.cuda.stream``."""
+    caller's ``with torch.cuda.stream``.  They hand out pages on the host, so
+    they are not for graph capture; ``PagedCache``'s calls are."""
 
     def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page: int,
                  num_pages: int, max_tokens: int, keep=None, slack: int = 0, sinks: int = 4,

@@ -16,6 +16,7 @@ from . import (SA_DTYPE_BF16, SA_DTYPE_F32, PagedCacheDesc, _check, _lib,
                sparse_attn_paged_attend_workspace_size, sparse_attn_paged_evict_workspace_size)
 
 _I64x3 = ctypes.c_int64 * 3
+_INT32_MAX = 2**31 - 1
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _append, _attend, _evict = (_lib.sparse_attn_paged_append, _lib.sparse_attn_paged_attend,
@@ -241,8 +242,11 @@ class PagedCache:
                                   stream)
         if self.weights is None:
             raise ValueError("eviction needs the cache's weights")
-        if len(keep) != self.num_kv_heads:
-            raise ValueError("keep must hold one budget per KV head")
+        keep = [int(k) for k in keep]
+        if len(keep) != self.num_kv_heads or min(keep) < 0 or max(keep) > _INT32_MAX:
+            raise ValueError("keep must hold one 32-bit budget per KV head")
+        if not (0 <= sinks <= _INT32_MAX and 0 <= recent <= _INT32_MAX):
+            raise ValueError("sinks and recent must be 32-bit and not negative")
         if positions_out is not None and self.positions is None:
             raise ValueError("positions_out needs the cache's positions")
         shape = self.weights.shape
@@ -252,7 +256,7 @@ class PagedCache:
              self._own(weights_out, torch.float32, shape, "weights_out"))
         pos = (self.desc.positions if positions_out is None else
                self._own(positions_out, torch.int32, shape, "positions_out"))
-        status = _evict(self._ref, self._keep(*map(int, keep)), sinks, recent, lens, w, pos,
+        status = _evict(self._ref, self._keep(*keep), sinks, recent, lens, w, pos,
                         self._ws_ptr, self._ws_bytes, self._status, self._handle(stream))
         if status:
             _check(status, "sparse_attn_paged_evict")

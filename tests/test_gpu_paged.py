@@ -471,6 +471,9 @@ def test_python_class_refusals(env):
         cache.evict([10])
     with pytest.raises(sa.SparseAttnError):
         cache.evict([10, 3], 2, 2)
+    for bad in (([2**32 + 50, 50], 0, 0), ([50, -1], 0, 0), ([50, 50], -1, 0), ([50, 50], 0, 2**32)):
+        with pytest.raises(ValueError):
+            cache.evict(*bad)
     plain = sa.PagedCache(dev["k"], dev["v"], dev["table"], dev["lens"])
     with pytest.raises(ValueError):
         plain.evict([10, 10])
