@@ -46,8 +46,8 @@
 // row's length is ever used.
 //
 // Accumulating weights: the scores (in base 2) go to the workspace, 4G bytes a
-// token, and a third launch adds 2^(s - lse), summed over the heads, to each
-// token's weight once every lse is known.
+// token, and the second launch adds 2^(s - lse), summed over the heads, to each
+// token's weight.
 //
 // Measured (GB300, copy rate 6783 GB/s, read-only traffic goes a little
 // higher): 16 sequences of 64K tokens, 28/4 heads, 2.1 GB: 319 us, 99%; one of
@@ -62,6 +62,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -78,9 +79,9 @@ constexpr int kTile = 128;             // tokens per tile
 constexpr int kMaxChunk = 32;          // most query heads of a row handled together
 constexpr int kInfo = 8;               // tile descriptions in flight
 constexpr float kMove = 8.f;           // how far a score may pass its reference
-constexpr int kJoinThreads = 512;
-constexpr int kWeightThreads = 256;
+constexpr int kJoinThreads = 256;
 constexpr int kWeightSteps = 4;        // tokens of a thread
+constexpr int kMaxGroup = 1024;        // query heads of a KV head
 
 template <int D, int GP, int PARTS>
 struct Cfg {
@@ -151,6 +152,7 @@ struct Record {
 };
 struct Work {
   Record* rec;         // [ctas]
+  Record* row_rec;     // [U], one a row, only when accumulating
   float* row_lse2;     // [U][chunk]
   float2* part_ml;     // [ctas][2][chunk]
   float* part_o;       // [ctas][2][chunk][d]
@@ -174,6 +176,7 @@ size_t layout(Work* w, char* base, int64_t rows, int G, int64_t cap, int d, int 
   };
   Work x;
   x.rec = reinterpret_cast<Record*>(take(size_t(ctas) * sizeof(Record)));
+  x.row_rec = reinterpret_cast<Record*>(take(accumulate ? size_t(U) * sizeof(Record) : 0));
   x.row_lse2 = reinterpret_cast<float*>(take(accumulate ? size_t(U) * chunk * 4 : 0));
   x.part_ml = reinterpret_cast<float2*>(take(size_t(ctas) * 2 * chunk * 8));
   x.part_o = reinterpret_cast<float*>(take(size_t(ctas) * 2 * chunk * d * 4));
@@ -192,6 +195,8 @@ struct Params {
   int32_t chunk;               // heads of a chunk
   int32_t q_rows;              // heads of a Q box
   int32_t min_units;           // least units of a CTA
+  int32_t tile_units;          // units of a tile
+  int32_t most_ranges;
   int32_t by_row;              // records: one a row
   int32_t ctas;                // CTAs of the first launch
   float scale_log2;
@@ -219,15 +224,14 @@ __device__ __forceinline__ int32_t units_of(const Params& p, int32_t len) {
   return (len + (1 << p.bx_shift) - 1) >> p.bx_shift;
 }
 
-// Ranges: the first `rem` CTAs take base + 1 units, the others base.
+// Ranges of `per` units: CTA c has [c * per, (c + 1) * per).
 struct Ranges {
-  int32_t ctas, base, rem;
-  __device__ __forceinline__ int32_t begin(int32_t c) const { return c * base + min(c, rem); }
-  // the CTA whose range holds unit x
-  __device__ __forceinline__ int32_t owner(int32_t x) const {
-    const int32_t big = rem * (base + 1);
-    return x < big ? x / (base + 1) : rem + (x - big) / base;
+  int32_t total, per;
+  __device__ __forceinline__ int32_t begin(int32_t c) const {
+    return int32_t(min(uint32_t(c) * uint32_t(per), uint32_t(total)));
   }
+  // the CTA whose range holds unit x
+  __device__ __forceinline__ int32_t owner(int32_t x) const { return x / per; }
 };
 
 template <bool kF32>
@@ -384,11 +388,15 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
       total += sh->scan[w];
     }
   }
+  // Equal ranges over the CTAs, of 64 tokens or of whole tiles: a part of a
+  // tile takes a CTA as long as a whole one (8 rows of 8192 tokens: 13.3 us cut
+  // evenly, 11.9 in whole tiles; 700 tokens each: 8.5 us in ranges of 64, 10.0
+  // in whole tiles).
   Ranges rg;
-  rg.ctas = max(1, min(int32_t(gridDim.x), (total + p.min_units - 1) / p.min_units));
-  rg.base = total / rg.ctas;
-  rg.rem = total - rg.base * rg.ctas;
-  const int32_t a = rg.begin(min(cta, rg.ctas)), b = rg.begin(min(cta + 1, rg.ctas));
+  rg.total = total;
+  rg.per = max(p.min_units, (total + p.most_ranges - 1) / p.most_ranges);
+  if (rg.per > p.min_units) rg.per = (rg.per + p.tile_units - 1) & -p.tile_units;
+  const int32_t a = rg.begin(cta), b = rg.begin(cta + 1);
   // the thread that has the range's first row says where that begins
   if (a < b && a >= before && a < before + mine && (!few || warp == 0)) {
     int32_t at = before;
@@ -558,9 +566,9 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     // rows that end here are the softmax warps' to record
     if (lane == 0) {
       const bool cut = begins && pu > b;       // pu: the end of the last row
-      if (cut || !p.by_row)
-        p.w.rec[p.by_row ? u : cta] =
-            Record{cut ? u : -1, cta, cut ? rg.owner(pu - 1) - cta + 1 : 0, seg > 0 ? 1 : 0};
+      const Record rec{cut ? u : -1, cta, cut ? rg.owner(pu - 1) - cta + 1 : 0, seg > 0 ? 1 : 0};
+      if (cut || !p.by_row) p.w.rec[p.by_row ? u : cta] = rec;
+      if (cut && p.weights_out) p.w.row_rec[u] = rec;
     }
     if (ok) {
       const int slot = i % kInfo;
@@ -819,7 +827,10 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
               p.w.part_ml[part + row] = make_float2(mr, L);
             }
           }
-          if (whole && p.by_row && grp == 0 && row == 0) p.w.rec[prev.u] = Record{-1, 0, 0, 0};
+          if (whole && grp == 0 && row == 0) {
+            if (p.by_row) p.w.rec[prev.u] = Record{-1, 0, 0, 0};
+            if (p.weights_out) p.w.row_rec[prev.u] = Record{-1, 0, 0, 0};
+          }
         }
       }
       if (it.n == 0) break;
@@ -907,33 +918,37 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   }
 }
 
+// Whether a record names a row to be joined.  A launch that gave up may have
+// left none: whatever is there instead must not lead out of the workspace.
+__device__ __forceinline__ bool usable(const Params& p, const Record& rec) {
+  return rec.u >= 0 && rec.u < p.U && rec.first >= 0 && rec.segs >= 1 && rec.segs <= p.ctas &&
+         rec.first <= p.ctas - rec.segs && (rec.slot & ~1) == 0;
+}
+
+// The k-th partial state of a row: the index of its first head.
+__device__ __forceinline__ uint32_t state_of(const Params& p, const Record& rec, int32_t k) {
+  return (uint32_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * p.chunk;
+}
+
 // Block (record, head): the join of a row's partial states.  Sixteen warps take
 // every sixteenth state each and bring them to their own maximum; the sixteen
 // results are brought to the row's and added in warp order.  A chain of three
 // reads (record, state, nothing else waits): 2.8 us from the end of the first
 // launch at any size, of which the launch is about 1.
 template <int D, bool kF32>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+__device__ __forceinline__ void join(const Params& p, int32_t record, int h) {
   constexpr int kVec = D / 32;                     // elements of a lane
   constexpr int kWays = kJoinThreads / 32;
   __shared__ float acc[kWays][D], ms[kWays], ls[kWays];
-  launch_dependents();
-  wait_dependency();
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
-  const Record rec = p.w.rec[blockIdx.x];
-  if (rec.u < 0) return;
-  // a launch that gave up may have left no record: whatever is there instead
-  // must not lead out of the workspace
-  if (rec.u >= p.U || rec.first < 0 || rec.segs < 1 || rec.segs > p.ctas ||
-      rec.first > p.ctas - rec.segs || (rec.slot & ~1))
-    return;
-  const int h = blockIdx.y;                        // head of the chunk
+  const Record rec = p.w.rec[record];
+  if (!usable(p, rec)) return;
   float m = -INFINITY, l = 0.f, v[kVec];
 #pragma unroll
   for (int x = 0; x < kVec; ++x) v[x] = 0.f;
 #pragma unroll 4
   for (int32_t k = way; k < rec.segs; k += kWays) {
-    const uint32_t at = (uint32_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * p.chunk + h;
+    const uint32_t at = state_of(p, rec, k) + h;
     const float2 ml = p.w.part_ml[at];
     float o[kVec];
     if constexpr (kVec == 4) {
@@ -978,43 +993,78 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int32_t b = r / p.Hkv;
   const size_t bh = size_t(b) * p.Hq + size_t(r - b * p.Hkv) * p.G + hc;
   store_out<kF32>(p, bh * D + x, __fdividef(sum, L));
-  if (x == 0) {
-    const float lse2 = (M == -INFINITY ? 0.f : M) + log2f(L);
-    if (p.lse) p.lse[bh] = lse2 * 0.6931471805599453f;
-    if (p.weights_out) p.w.row_lse2[size_t(rec.u) * p.chunk + h] = lse2;
-  }
+  if (x == 0 && p.lse)
+    p.lse[bh] = ((M == -INFINITY ? 0.f : M) + log2f(L)) * 0.6931471805599453f;
 }
 
-// Block (piece of a row's slots, row): every token's probabilities, summed
-// over the row's heads, added to its weight.  4G + 8 bytes a token; 128 rows of
-// 4352 tokens and 4 heads (13 MB): 4.4 us after the join.
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ Params p,
-                                                                 int32_t pieces) {
-  launch_dependents();
-  wait_dependency();
-  const int32_t r = blockIdx.x / pieces;
-  const int32_t t0 = (blockIdx.x % pieces) * (kWeightThreads * kWeightSteps) + threadIdx.x;
+// A piece of a row's slots: every token's probabilities, summed over the row's
+// heads, added to its weight.  4G + 8 bytes a token.  It runs beside the joins,
+// so it adds up the log-sum-exps of cut rows for itself.
+__device__ __forceinline__ void add_weights(const Params& p, int32_t r, int32_t t0) {
+  __shared__ float lse2s[kMaxGroup];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t n = sa_paged::row_len(p.lens, r, p.cap, p.dev_status);
-  float sum[kWeightSteps];
-#pragma unroll
-  for (int i = 0; i < kWeightSteps; ++i) sum[i] = 0.f;
   if (t0 >= n) return;
-  const float* s = p.w.scores + size_t(r) * p.G * p.cap;
-  const float* lse2 = p.w.row_lse2 + size_t(r) * p.HC * p.chunk;
-#pragma unroll 4
-  for (int32_t h = 0; h < p.G; ++h) {
-    const float l = lse2[h];                       // chunks of heads lie end to end
+  for (int32_t h = warp; h < p.G; h += kJoinThreads / 32) {
+    const int32_t u = r * p.HC + h / p.chunk, x = h % p.chunk;
+    const Record rec = p.w.row_rec[u];
+    float v;
+    if (rec.u < 0) {
+      v = p.w.row_lse2[size_t(u) * p.chunk + x];
+    } else {
+      float m = -INFINITY, l = 0.f;
+      if (usable(p, rec)) {
+        for (int32_t k = lane; k < rec.segs; k += 32) {
+          const float2 ml = p.w.part_ml[state_of(p, rec, k) + x];
+          const float mn = fmaxf(m, ml.x);
+          l = l * (mn == m ? 1.f : ex2(m - mn)) + ml.y * (mn == ml.x ? 1.f : ex2(ml.x - mn));
+          m = mn;
+        }
+      }
+      const float M = warp_max(m);
+      l *= m == M ? 1.f : ex2(m - M);
 #pragma unroll
-    for (int i = 0; i < kWeightSteps; ++i) {
-      const int32_t t = t0 + i * kWeightThreads;
-      if (t < n) sum[i] += ex2(s[size_t(h) * p.cap + t] - l);
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      v = (M == -INFINITY ? 0.f : M) + log2f(l);
     }
+    if (lane == 0) lse2s[h] = v;
   }
+  const int32_t t = t0 + threadIdx.x;
+  const float* s = p.w.scores + size_t(r) * p.G * p.cap + t;
+  const size_t at = size_t(r) * p.cap + t;
+  float sum[kWeightSteps], old[kWeightSteps];
 #pragma unroll
   for (int i = 0; i < kWeightSteps; ++i) {
-    const int32_t t = t0 + i * kWeightThreads;
-    const size_t at = size_t(r) * p.cap + t;
-    if (t < n) p.weights_out[at] = p.weights[at] + sum[i];
+    sum[i] = 0.f;
+    if (t + i * kJoinThreads < n) old[i] = p.weights[at + i * kJoinThreads];
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int32_t h = 0; h < p.G; ++h) {
+    const float l = lse2s[h];
+#pragma unroll
+    for (int i = 0; i < kWeightSteps; ++i)
+      if (t + i * kJoinThreads < n)
+        sum[i] += ex2(s[size_t(h) * p.cap + i * kJoinThreads] - l);
+  }
+#pragma unroll
+  for (int i = 0; i < kWeightSteps; ++i)
+    if (t + i * kJoinThreads < n) p.weights_out[at + i * kJoinThreads] = old[i] + sum[i];
+}
+
+// The second launch.  Blocks [0, joins): join of (record, head); the others:
+// weights of (row, piece).
+template <int D, bool kF32, bool kWeights>
+__global__ void __launch_bounds__(kJoinThreads)
+    finish_kernel(const __grid_constant__ Params p, int32_t joins, int32_t pieces) {
+  launch_dependents();
+  wait_dependency();
+  const int32_t id = blockIdx.x;
+  if (!kWeights || id < joins) {
+    join<D, kF32>(p, id / p.q_rows, id % p.q_rows);
+  } else {
+    const int32_t r = (id - joins) / pieces;
+    add_weights(p, r, (id - joins - r * pieces) * (kJoinThreads * kWeightSteps));
   }
 }
 
@@ -1090,6 +1140,7 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.Hq = a.Hq;
   p.U = int32_t(rows * p.HC);
   p.min_units = 64 >> p.bx_shift;
+  p.tile_units = kTile >> p.bx_shift;
   p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
   p.o = a.o;
   p.out_f32 = a.out_f32;
@@ -1099,6 +1150,9 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.dev_status = a.dev_status;
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
   const int ctas = sms * C::kPerSm;
+  // no more than 128 ranges a row on average: one row of 16000 tokens takes
+  // 13.7 us in 250 ranges, whose join is long, and 11.0 in 125
+  p.most_ranges = int32_t(std::min<int64_t>(ctas, int64_t(p.U) * 128));
   p.by_row = p.U <= ctas;
   p.ctas = ctas;
   layout(&p.w, static_cast<char*>(a.ws), rows, p.G, p.cap, D, ctas, a.weights_out != nullptr);
@@ -1120,17 +1174,17 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   cfg.dynamicSmemBytes = kSmem;
   e = cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(unsigned(p.by_row ? p.U : ctas), unsigned(p.q_rows));
+  const int64_t joins = int64_t(p.by_row ? p.U : ctas) * p.q_rows;
+  constexpr int kPiece = kJoinThreads * kWeightSteps;
+  const int32_t pieces = (p.cap + kPiece - 1) / kPiece;
+  const int64_t blocks = joins + (a.weights_out ? rows * pieces : 0);
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(unsigned(blocks));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<D, PARTS == 3>, p);
-  if (e != cudaSuccess || !a.weights_out) return e;
-  constexpr int kPiece = kWeightThreads * kWeightSteps;
-  const int32_t pieces = (p.cap + kPiece - 1) / kPiece;
-  if (rows * pieces > INT32_MAX) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3(unsigned(rows * pieces));
-  cfg.blockDim = dim3(kWeightThreads);
-  return cudaLaunchKernelEx(&cfg, weights_kernel, p, pieces);
+  return a.weights_out
+             ? cudaLaunchKernelEx(&cfg, finish_kernel<D, PARTS == 3, true>, p, int32_t(joins), pieces)
+             : cudaLaunchKernelEx(&cfg, finish_kernel<D, PARTS == 3, false>, p, int32_t(joins), pieces);
 }
 
 template <int D>
