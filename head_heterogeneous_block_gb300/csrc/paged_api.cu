@@ -34,11 +34,12 @@ sa_status check_cache(const sa_paged_cache* c) {
   if (!aligned(c->table, 4) || !aligned(c->lens, 4) || !aligned(c->weights, 4) ||
       !aligned(c->positions, 4))
     return SA_ERR_INVALID_ARG;
-  // slots of a row, rows, and 16-slot pieces of all rows are 32-bit counts
+  // slots of a row, rows, and 16-slot pieces of all rows are 32-bit counts, with
+  // room for sums
   const int64_t cap = int64_t(c->page) * c->max_pages;
   const int64_t rows = int64_t(c->batch) * c->num_kv_heads;
   if (cap > (int64_t(1) << 30) || rows > (int64_t(1) << 24) ||
-      cap / 16 > ((int64_t(1) << 31) - 1) / rows)
+      cap / 16 > (int64_t(1) << 30) / rows)
     return SA_ERR_SHAPE;
   return SA_OK;
 }
@@ -48,7 +49,7 @@ sa_status check_heads(const sa_paged_cache* c, int32_t hq) {
   const int64_t rows = int64_t(c->batch) * c->num_kv_heads;
   const int64_t chunks = (hq / c->num_kv_heads + 31) / 32;
   const int64_t pieces = int64_t(c->page) * c->max_pages / 16;
-  if (rows * chunks > (int64_t(1) << 24) || pieces > ((int64_t(1) << 31) - 1) / (rows * chunks))
+  if (rows * chunks > (int64_t(1) << 24) || pieces > (int64_t(1) << 30) / (rows * chunks))
     return SA_ERR_SHAPE;
   return SA_OK;
 }

@@ -13,9 +13,9 @@
 //                                                     descriptor) and P from shared memory
 //
 // Split.  The tokens of all rows (sequence, KV head, and for groups above 32
-// heads a chunk of 32 of them) are laid end to end in units of 16 or 32 tokens
-// and cut into equal ranges, one per CTA, two CTAs per processor: the lengths
-// differ freely between rows and no processor waits for the longest.  A row
+// heads a chunk of 32 of them) are laid end to end in tiles of 128 (64 where
+// there are few) and cut into equal ranges, one per CTA, two CTAs per processor:
+// the lengths differ freely between rows and no processor waits for the longest.  A row
 // that lies in one range is finished there; a row that is cut leaves one
 // partial state (maximum, sum, unnormalised output) per range, which the join
 // kernel combines in range order.  Each CTA finds its range by a scan of the
@@ -62,7 +62,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -75,7 +74,8 @@ namespace {
 using namespace sa_dev;
 using sa_paged::AttendArgs;
 
-constexpr int kTile = 128;             // tokens per tile
+constexpr int kTileShift = 7;
+constexpr int kTile = 1 << kTileShift; // tokens per tile
 constexpr int kMaxChunk = 32;          // most query heads of a row handled together
 constexpr int kInfo = 8;               // tile descriptions in flight
 constexpr float kMove = 8.f;           // how far a score may pass its reference
@@ -190,13 +190,11 @@ struct Params {
   const int32_t* lens;
   int64_t num_pages;
   int32_t page_shift, max_pages, cap;
-  int32_t bx_shift;            // log2 of the tokens of a unit (and of a TMA box)
+  int32_t bx_shift;            // log2 of the tokens of a TMA box
   int32_t Hkv, Hq, G, HC, U;   // HC: head chunks of a row; U = rows * HC
   int32_t chunk;               // heads of a chunk
   int32_t q_rows;              // heads of a Q box
-  int32_t min_units;           // least units of a CTA
-  int32_t tile_units;          // units of a tile
-  int32_t most_ranges;
+  int32_t most_ranges;         // CTAs that get work
   int32_t by_row;              // records: one a row
   int32_t ctas;                // CTAs of the first launch
   float scale_log2;
@@ -220,8 +218,9 @@ __device__ __forceinline__ int32_t head_of(const Params& p, int32_t u) {
   return kOne || p.HC == 1 ? 0 : (u % p.HC) * p.chunk;
 }
 
-__device__ __forceinline__ int32_t units_of(const Params& p, int32_t len) {
-  return (len + (1 << p.bx_shift) - 1) >> p.bx_shift;
+// Units of 2^shift tokens of a row.
+__device__ __forceinline__ int32_t units_of(int shift, int32_t len) {
+  return (len + (1 << shift) - 1) >> shift;
 }
 
 // Ranges of `per` units: CTA c has [c * per, (c + 1) * per).
@@ -354,22 +353,33 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
   const uint32_t tmem = sh->tmem_base;
   wait_dependency();
 
-  // ---- this CTA's range: a scan of every row's units.  Up to 128 rows each
-  // warp scans for itself, four rows a lane; more rows are scanned by the CTA.
+  // ---- this CTA's range: a scan of every row's units, which are tiles (a part
+  // of a tile takes a CTA as long as a whole one), or 64 tokens where that
+  // still leaves a CTA for each.  (8 rows of 8192 tokens: 13.3 us cut into equal
+  // numbers of tokens, 11.9 into tiles; of 700 tokens: 10.0 us in tiles, 8.5 in
+  // 64s.)  Up to 128 rows each warp scans for itself, four rows a lane; more
+  // rows are scanned by the CTA.
   const bool few = p.U <= 128;
   const int32_t per = few ? 4 : (p.U + kThreads - 1) / kThreads;
   const int32_t ua = min(p.U, (few ? lane : tid) * per), ub = min(p.U, ua + per);
   int32_t mine = 0;
+  int us = kTileShift;                         // log2 of a unit's tokens
   if (few) {
-    int32_t n[4];
+    int32_t n[4], halves = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) n[i] = ua + i < ub ? p.lens[row_of<kOne>(p, ua + i)] : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine += units_of(p, max(0, min(n[i], p.cap)));
+    for (int i = 0; i < 4; ++i) {
+      n[i] = max(0, min(n[i], p.cap));
+      halves += units_of(kTileShift - 1, n[i]);
+    }
+    if (int32_t(__reduce_add_sync(0xffffffffu, halves)) <= p.most_ranges) us = kTileShift - 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine += units_of(us, n[i]);
   } else {
 #pragma unroll 1
     for (int32_t u = ua; u < ub; ++u)
-      mine += units_of(p, max(0, min(p.lens[row_of<kOne>(p, u)], p.cap)));
+      mine += units_of(us, max(0, min(p.lens[row_of<kOne>(p, u)], p.cap)));
   }
   int32_t incl = mine;
 #pragma unroll
@@ -388,14 +398,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
       total += sh->scan[w];
     }
   }
-  // Equal ranges over the CTAs, of 64 tokens or of whole tiles: a part of a
-  // tile takes a CTA as long as a whole one (8 rows of 8192 tokens: 13.3 us cut
-  // evenly, 11.9 in whole tiles; 700 tokens each: 8.5 us in ranges of 64, 10.0
-  // in whole tiles).
-  Ranges rg;
-  rg.total = total;
-  rg.per = max(p.min_units, (total + p.most_ranges - 1) / p.most_ranges);
-  if (rg.per > p.min_units) rg.per = (rg.per + p.tile_units - 1) & -p.tile_units;
+  const Ranges rg{total, max(1, (total + p.most_ranges - 1) / p.most_ranges)};
   const int32_t a = rg.begin(cta), b = rg.begin(cta + 1);
   // the thread that has the range's first row says where that begins
   if (a < b && a >= before && a < before + mine && (!few || warp == 0)) {
@@ -403,13 +406,13 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
 #pragma unroll 1
     for (int32_t u = ua; u < ub; ++u) {
       const int32_t n = max(0, min(p.lens[row_of<kOne>(p, u)], p.cap));
-      if (a < at + units_of(p, n)) {
+      if (a < at + units_of(us, n)) {
         sh->u0 = u;
         sh->p0 = at;
         sh->len0 = n;
         break;
       }
-      at += units_of(p, n);
+      at += units_of(us, n);
     }
   }
   if (few)
@@ -447,16 +450,16 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
                  ? sa_paged::row_len(p.lens, row_of<kOne>(p, ubase + lane), p.cap, p.dev_status) : 0;
     };
     auto end_of = [&]() -> int32_t {           // of the row's part in this range
-      return min(len, int32_t(min(int64_t(b - pu) << p.bx_shift, int64_t(1) << 30)));
+      return min(len, int32_t(min(int64_t(b - pu) << us, int64_t(1) << 30)));
     };
     int32_t seg = 0;                           // row parts before this one
-    int32_t t = (a - pu) << p.bx_shift, t1 = end_of();
+    int32_t t = (a - pu) << us, t1 = end_of();
     bool first = true, begins = t == 0;
     bool more = true;
     // the next tile of the range; n == 0 when it is used up
     auto next = [&]() -> TileInfo {
       while (more && t >= t1) {
-        pu += units_of(p, len);
+        pu += units_of(us, len);
         if (pu >= b || u + 1 >= p.U) {
           more = false;
           break;
@@ -1139,8 +1142,6 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.Hkv = c.num_kv_heads;
   p.Hq = a.Hq;
   p.U = int32_t(rows * p.HC);
-  p.min_units = 64 >> p.bx_shift;
-  p.tile_units = kTile >> p.bx_shift;
   p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
   p.o = a.o;
   p.out_f32 = a.out_f32;
@@ -1150,9 +1151,9 @@ cudaError_t launch(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_f
   p.dev_status = a.dev_status;
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
   const int ctas = sms * C::kPerSm;
-  // no more than 128 ranges a row on average: one row of 16000 tokens takes
-  // 13.7 us in 250 ranges, whose join is long, and 11.0 in 125
-  p.most_ranges = int32_t(std::min<int64_t>(ctas, int64_t(p.U) * 128));
+  // a single row takes no more ranges than there are processors: its join is
+  // one long chain (65536 tokens: 18.6 us in 304 ranges, 15.3 in 128)
+  p.most_ranges = p.U > 1 ? ctas : sms;
   p.by_row = p.U <= ctas;
   p.ctas = ctas;
   layout(&p.w, static_cast<char*>(a.ws), rows, p.G, p.cap, D, ctas, a.weights_out != nullptr);
