@@ -35,7 +35,9 @@ class PagedCache:
 
     ``num_q_heads`` only sizes the workspace ahead of the first ``attend``
     (before a graph capture, say).  The calls of one PagedCache share its
-    workspace: they must not run at the same time on several streams.
+    workspace: they must not run at the same time on several streams, nor may
+    the replays of graphs that hold them.  A graph that captured a call needs
+    its PagedCache, and its tensors, to live.
     ``dev_status`` collects the device's error bits (``SA_DEV_*``)."""
 
     def __init__(self, k_pages, v_pages, table, lens, weights=None, positions=None,
@@ -90,6 +92,7 @@ class PagedCache:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._status = self.dev_status.data_ptr()
         self._ws, self._ws_ptr, self._ws_bytes = None, None, 0
+        self._outgrown = []
         self._ws_stream = _raw_stream(self._index)
         self._sized = set()
         if num_q_heads is not None:
@@ -108,6 +111,8 @@ class PagedCache:
         need = (sparse_attn_paged_evict_workspace_size(self.desc) if num_q_heads is None else
                 sparse_attn_paged_attend_workspace_size(self.desc, num_q_heads, accumulate))
         if need > self._ws_bytes:
+            if self._ws is not None:        # graphs captured with it still use it
+                self._outgrown.append(self._ws)
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             self._ws_ptr, self._ws_bytes = self._ws.data_ptr(), need
             self._ws_stream = _raw_stream(self._index)

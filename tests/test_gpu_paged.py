@@ -797,3 +797,27 @@ def test_evict_equal_positions_all_forced(env):
     cache.evict([50], 0, 4)
     assert int(dev["lens"]) == 50 and torch.equal(dev["k"], k0)
     assert torch.equal(dev["weights"].cpu(), c["weights"])
+
+
+def test_a_captured_call_keeps_its_workspace(env):
+    # the workspace grows after a capture; the graph's replays still own theirs
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(57, [3000, 300], 2, 128, 32)
+    dev, cache = P.to_gpu(c, sa, with_weights=False, num_q_heads=8)
+    q = _q(torch, 40, 2, 8, 128)
+    gq, out = q.cuda(), torch.zeros(2, 8, 128, device="cuda")
+    cache.attend(gq, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(gq, out=out)
+    before = cache._ws_bytes
+    cache.attend(_q(torch, 41, 2, 64, 128).cuda())
+    assert cache._ws_bytes > before
+    torch.cuda.synchronize()
+    junk = [torch.zeros(before // 4, dtype=torch.int32, device="cuda") for _ in range(4)]
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(int(j.count_nonzero()) == 0 for j in junk)
+    P.check_attend(c, q, out, None)
