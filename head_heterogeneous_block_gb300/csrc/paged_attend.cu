@@ -933,8 +933,8 @@ __device__ __forceinline__ uint32_t state_of(const Params& p, const Record& rec,
   return (uint32_t(rec.first + k) * 2 + (k == 0 ? rec.slot : 0)) * p.chunk;
 }
 
-// Block (record, head): the join of a row's partial states.  Sixteen warps take
-// every sixteenth state each and bring them to their own maximum; the sixteen
+// Block (record, head): the join of a row's partial states.  Eight warps take
+// every eighth state each and bring them to their own maximum; the eight
 // results are brought to the row's and added in warp order.  A chain of three
 // reads (record, state, nothing else waits): 2.8 us from the end of the first
 // launch at any size, of which the launch is about 1.

@@ -193,6 +193,18 @@ class PagedCache:
         if _current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.attend(q, out, lse, weights_out, accumulate, stream)
+        if stream is not None and (stream if isinstance(stream, int) else
+                                   stream.cuda_stream) != _raw_stream(self._index):
+            # what is allocated here (the output, a larger workspace) comes from
+            # the launching stream's memory: the current stream may still be at
+            # work in what it freed
+            caller, made = torch.cuda.current_stream(), out is None
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)
+                                   if isinstance(stream, int) else stream):
+                out = self.attend(q, out, lse, weights_out, accumulate)
+            if made:
+                out.record_stream(caller)
+            return out
         if q.dtype is not torch.bfloat16:
             raise TypeError("q must be bfloat16")
         b, hq, d = q.shape if q.dim() == 3 else (0, 0, 0)
@@ -205,9 +217,6 @@ class PagedCache:
             raise ValueError(f"q must be on {self.device}")
         if out is None:
             out = torch.empty(b, hq, d, dtype=torch.bfloat16, device=self.device)
-            if stream is not None:
-                out.record_stream(torch.cuda.ExternalStream(stream, device=self.device)
-                                  if isinstance(stream, int) else stream)
         if out.dtype is torch.bfloat16:
             o_dtype = SA_DTYPE_BF16
         elif out.dtype is torch.float32:
@@ -230,7 +239,7 @@ class PagedCache:
         if (hq, w is not None) not in self._sized:
             self._size(hq, w is not None)
         status = _attend(self._ref, q.data_ptr(), q0, q1, hq, o, o_dtype, lse, w, self._ws_ptr,
-                         self._ws_bytes, self._status, self._handle(stream))
+                         self._ws_bytes, self._status, self._handle(None))
         if status:
             _check(status, "sparse_attn_paged_attend")
         return out

@@ -821,3 +821,26 @@ def test_a_captured_call_keeps_its_workspace(env):
     torch.cuda.synchronize()
     assert all(int(j.count_nonzero()) == 0 for j in junk)
     P.check_attend(c, q, out, None)
+
+
+def test_another_streams_call_takes_no_memory_the_current_one_still_uses(env):
+    # the current stream has freed a block and is still to write it
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(58, [700, 90], 2, 128, 32)
+    dev, cache = P.to_gpu(c, sa, with_weights=False)
+    q = _q(torch, 42, 2, 8, 128)
+    gq = q.cuda()
+    need = sa.sparse_attn_paged_attend_workspace_size(cache.desc, 8, False)
+    torch.cuda.synchronize()
+    for other in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        torch.cuda._sleep(20_000_000)
+        busy = [torch.full((need,), 7, dtype=torch.uint8, device="cuda"),
+                torch.full((2, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")]
+        spans = [(x.data_ptr(), x.data_ptr() + x.nbytes) for x in busy]
+        del busy
+        out = cache.attend(gq, stream=other)
+        for x in (out, cache._ws):
+            assert all(x.data_ptr() + x.nbytes <= a or b <= x.data_ptr() for a, b in spans)
+        torch.cuda.synchronize()
+        P.check_attend(c, q, out, None)
