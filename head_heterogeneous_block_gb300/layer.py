@@ -336,15 +336,16 @@ class PagedDecodeLayer:
         row = self._rows(b, b + 1)
         try:
             row.append(k[None], v[None])
+            if queries is not None and self.weights is not None:
+                for q in queries:
+                    row.attend(q[None])
         except Exception:
             self.book.shrink(b, [0] * len(self.book.rows[b]))
+            self.lens[b].zero_()
             raise
         self.active[b] = True
         self.next_position[b] = tokens
         self._mark()
-        if queries is not None and self.weights is not None:
-            for q in queries:
-                row.attend(q[None])
         self._cut()
         self.cache.dev_status.bitwise_or_(row.dev_status)
 
@@ -370,12 +371,24 @@ class PagedDecodeLayer:
 
     def step(self, q, k, v, out=None, lse=None):
         """One token of every active sequence: q bf16 [batch, num_q_heads, d],
-        k and v bf16 [batch, num_kv_heads, d].  Returns the attention output;
-        rows of sequences that are not active get zeros."""
+        k and v bf16 [batch, num_kv_heads, d].  Returns the attention output
+        (without ``out`` a tensor of the layer's, which its next step
+        overwrites); rows of sequences that are not active get zeros.  A step
+        whose arguments are refused changes nothing."""
+        lens = [list(row) for row in self.book.lens]
         self._grow([int(a) for a in self.active])
-        self.cache.append(k[:, :, None], v[:, :, None], counts=self.counts, start=self.start)
+        appended = False
+        try:
+            self.cache.append(k[:, :, None], v[:, :, None], counts=self.counts, start=self.start)
+            appended = True
+            out = self.cache.attend(q, out=self.out if out is None else out, lse=lse)
+        except Exception:
+            if appended:
+                self.lens.sub_(self.counts[:, None])
+            for b, row in enumerate(lens):
+                self.book.shrink(b, row)
+            raise
         self.start.add_(self.counts)
         self.next_position = [p + int(a) for p, a in zip(self.next_position, self.active)]
-        out = self.cache.attend(q, out=self.out if out is None else out, lse=lse)
         self._cut()
         return out

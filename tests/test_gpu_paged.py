@@ -844,3 +844,33 @@ def test_another_streams_call_takes_no_memory_the_current_one_still_uses(env):
             assert all(x.data_ptr() + x.nbytes <= a or b <= x.data_ptr() for a, b in spans)
         torch.cuda.synchronize()
         P.check_attend(c, q, out, None)
+
+
+def test_paged_decode_layer_refused_calls_change_nothing(env):
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    from tests import _paged as P
+    sa, torch = env
+    layer = PagedDecodeLayer(2, 8, 2, 64, 16, 20, 200, keep=[40, 40], slack=80)
+    gen = torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=gen).bfloat16()
+    k, v = rnd(2, 32, 64), rnd(2, 32, 64)
+    with pytest.raises(ValueError):                        # queries of the wrong width
+        layer.admit(0, k.cuda(), v.cuda(), queries=rnd(1, 8, 128).cuda())
+    assert not layer.active[0] and len(layer.book.free) == 20 and not layer.lens.any()
+    layer.admit(0, k.cuda(), v.cuda())
+    q, k1, v1 = rnd(2, 8, 64), rnd(2, 2, 64), rnd(2, 2, 64)
+    gq, gk, gv = q.cuda(), k1.cuda(), v1.cuda()
+    for bad in ((gq, gk.float(), gv), (gq[:1], gk, gv), (gq.float(), gk, gv)):
+        with pytest.raises((TypeError, ValueError)):       # the new token opens a page
+            layer.step(*bad)
+        assert layer.lens.tolist() == layer.book.lens == [[32, 32], [0, 0]]
+        assert len(layer.book.free) == 16 and layer.start.tolist() == [32, 0]
+    lse = torch.empty(2, 8, device="cuda")
+    out = layer.step(gq, gk, gv, lse=lse)
+    assert layer.lens.tolist() == layer.book.lens == [[33, 33], [0, 0]]
+    c = {"k": torch.zeros(3, 33, 64).bfloat16(), "v": torch.zeros(3, 33, 64).bfloat16(),
+         "table": torch.tensor([[[0], [1]], [[2], [2]]], dtype=torch.int32),
+         "lens": torch.tensor([[33, 33], [0, 0]], dtype=torch.int32), "page": 33, "weights": None}
+    c["k"][:2] = torch.cat([k, k1[0][:, None]], 1)
+    c["v"][:2] = torch.cat([v, v1[0][:, None]], 1)
+    P.check_attend(c, q, out, lse)
