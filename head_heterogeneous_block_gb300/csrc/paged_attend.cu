@@ -54,7 +54,7 @@
 // 128K, 64/8 heads, 537 MB: 87 us, 91%.  The rest is a fixed 9 us or so: the
 // chain lengths -> page table -> first keys with a cold instruction cache
 // (3 us), the last tile's softmax and store (1 us), the join (2.8 us); it is
-// all there is of one 700-token sequence (8.8 us).  One CTA per processor with
+// all there is of one 700-token sequence (8.5 us).  One CTA per processor with
 // twice the stages came 4% (d = 128) to 60% (d = 64) slower, three or four 15
 // to 30% (d = 64); pieces of 64 or 128 tokens instead of 32 the same, of 16
 // tokens 1 to 12% slower.
