@@ -118,6 +118,11 @@ class PagedCache:
             self._ws_stream = _raw_stream(self._index)
         self._sized.add((num_q_heads, accumulate))
 
+    def _stream(self, handle):
+        # (an external stream of handle 0 would be a new stream)
+        return (torch.cuda.ExternalStream(handle, device=self.device) if handle else
+                torch.cuda.default_stream(self.device))
+
     def _handle(self, stream):
         """The stream's handle; the cache's device is current."""
         if stream is None:
@@ -127,7 +132,7 @@ class PagedCache:
         if handle != self._ws_stream:
             # the cache's own tensors outlive the work of streams they were
             # not allocated on
-            other = torch.cuda.ExternalStream(handle, device=self.device)
+            other = self._stream(handle)
             self.dev_status.record_stream(other)
             if self._ws is not None:
                 self._ws.record_stream(other)
@@ -199,8 +204,7 @@ class PagedCache:
             # the launching stream's memory: the current stream may still be at
             # work in what it freed
             caller, made = torch.cuda.current_stream(), out is None
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)
-                                   if isinstance(stream, int) else stream):
+            with torch.cuda.stream(self._stream(stream) if isinstance(stream, int) else stream):
                 out = self.attend(q, out, lse, weights_out, accumulate)
             if made:
                 out.record_stream(caller)

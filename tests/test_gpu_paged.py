@@ -874,3 +874,20 @@ def test_paged_decode_layer_refused_calls_change_nothing(env):
     c["k"][:2] = torch.cat([k, k1[0][:, None]], 1)
     c["v"][:2] = torch.cat([v, v1[0][:, None]], 1)
     P.check_attend(c, q, out, lse)
+
+
+def test_handle_zero_is_the_default_stream(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(59, [300], 2, 64, 16)
+    dev, cache = P.to_gpu(c, sa, with_weights=False, num_q_heads=4)
+    q = _q(torch, 43, 1, 4, 64)
+    late = q.cuda()
+    gq = torch.zeros_like(late)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    gq.copy_(late)                                 # the default stream's, still to come
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out = cache.attend(gq, stream=0)
+    torch.cuda.synchronize()
+    P.check_attend(c, q, out, None)
