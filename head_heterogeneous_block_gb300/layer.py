@@ -309,6 +309,19 @@ class PagedDecodeLayer:
         self.counts = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.start = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.out = torch.empty(batch, num_q_heads, head_dim, dtype=out_dtype, device=dev)
+        self._streams = {torch.cuda.current_stream(dev)}
+
+    def _follow(self):
+        """The layer's tensors outlive the work of streams they were not
+        allocated on."""
+        stream = torch.cuda.current_stream(self.lens.device)
+        if stream in self._streams:
+            return
+        self._streams.add(stream)
+        for t in (self.k_pages, self.v_pages, self.table, self.lens, self.weights,
+                  self.positions, self.counts, self.start, self.out):
+            if t is not None:
+                t.record_stream(stream)
 
     def _rows(self, b0, b1, num_q_heads=None):
         part = slice(b0, b1)
@@ -331,6 +344,7 @@ class PagedDecodeLayer:
         first eviction knows its tokens' weights."""
         if self.active[b]:
             raise ValueError(f"sequence {b} is not free")
+        self._follow()
         tokens = k.shape[1]
         self._grow([tokens if x == b else 0 for x in range(len(self.active))])
         row = self._rows(b, b + 1)
@@ -351,6 +365,7 @@ class PagedDecodeLayer:
 
     def release(self, b: int):
         """Sequence b ends; its pages are free."""
+        self._follow()
         self.book.shrink(b, [0] * len(self.book.rows[b]))
         self.active[b] = False
         self.next_position[b] = 0
@@ -375,6 +390,7 @@ class PagedDecodeLayer:
         (without ``out`` a tensor of the layer's, which its next step
         overwrites); rows of sequences that are not active get zeros.  A step
         whose arguments are refused changes nothing."""
+        self._follow()
         lens = [list(row) for row in self.book.lens]
         self._grow([int(a) for a in self.active])
         appended = False

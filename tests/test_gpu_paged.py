@@ -891,3 +891,26 @@ def test_handle_zero_is_the_default_stream(env):
         out = cache.attend(gq, stream=0)
     torch.cuda.synchronize()
     P.check_attend(c, q, out, None)
+
+
+def test_paged_decode_layer_gone_while_another_stream_works(env):
+    # the layer is dropped with its step still queued on a side stream: its
+    # memory is not handed to the first stream before that step has run
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    sa, torch = env
+    layer = PagedDecodeLayer(1, 8, 2, 64, 16, 20, 200)
+    k, q = torch.zeros(2, 40, 64).bfloat16().cuda(), torch.zeros(1, 8, 64).bfloat16().cuda()
+    layer.admit(0, k, k)
+    out = torch.zeros(1, 8, 64, device="cuda")
+    spans = [(t.data_ptr(), t.data_ptr() + t.nbytes) for t in (layer.k_pages, layer.v_pages)]
+    size = layer.k_pages.nbytes
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        layer.step(q, k[None, :, 0], k[None, :, 0], out=out)
+        torch.cuda._sleep(20_000_000)
+    del layer
+    for _ in range(8):
+        x = torch.empty(size, dtype=torch.uint8, device="cuda")
+        assert all(x.data_ptr() + size <= a or b <= x.data_ptr() for a, b in spans)
+    torch.cuda.synchronize()
