@@ -66,6 +66,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "give_up.h"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -139,7 +140,7 @@ struct Shared {
   int32_t u0, p0, len0;  // first row of the range, the units before it, its length
   uint32_t tmem_base;
   int abort;
-  int failed[C::kGroups];  // set by a group's warp whose wait gave up
+  GiveUp failed[C::kGroups];  // raised by a group's warp whose wait gave up
 };
 
 // Workspace: records, row log-sum-exps, partial states, scores.  A record is
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
     sh->abort = 0;
-    for (int g = 0; g < C::kGroups; ++g) sh->failed[g] = 0;
+    for (int g = 0; g < C::kGroups; ++g) sh->failed[g].clear();
     sh->u0 = sh->p0 = sh->len0 = 0;
   }
   constexpr int kBars = 2 * kInfo + 1 + 2 * C::kStages + 6 + 2;
@@ -783,9 +784,9 @@ __global__ void __launch_bounds__(Cfg<D, GP, PARTS>::kThreads, Cfg<D, GP, PARTS>
           }
         }
       }
-      if (fail) *(volatile int*)&sh->failed[grp] = 1;
+      if (fail) sh->failed[grp].raise(j);
       const bool any = group_any<C::kGroups>(grp, need || fail);
-      if (any && *(volatile int*)&sh->failed[grp]) {
+      if (any && sh->failed[grp].raised(j)) {
         ok = false;
         break;
       }
