@@ -70,6 +70,12 @@ cudaError_t allow_shared(Kernel* kern, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
+// Whether n bytes at p and m bytes at q (either may be NULL) share memory.
+inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
+
 #ifdef __CUDACC__
 // A row's length, clamped to its table and flagged when it was out of range.
 __device__ __forceinline__ int32_t row_len(const int32_t* lens, int64_t r, int32_t cap,

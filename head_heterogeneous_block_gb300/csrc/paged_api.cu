@@ -97,6 +97,11 @@ sa_status sparse_attn_paged_append(const sa_paged_cache* cache, const void* k_ne
     a.ks[i] = k_strides[i];
     a.vs[i] = v_strides[i];
   }
+  // a row's new length must not replace another row's count
+  const size_t per_seq = size_t(cache->batch) * 4;
+  if (sa_paged::overlap(lens_out, per_seq * cache->num_kv_heads, counts, per_seq) &&
+      !(cache->num_kv_heads == 1 && lens_out == counts))
+    return SA_ERR_INVALID_ARG;
   a.num_new = num_new;
   a.counts = counts;
   a.start = start;

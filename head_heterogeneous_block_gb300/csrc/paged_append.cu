@@ -7,7 +7,9 @@
 // kSteps steps are in flight before the first store.  With one such warp per
 // row (a decode step) the warp also writes the row's new length, so the length
 // array may be updated in place; with several, a row's warps all read the old
-// length, and an in-place update is a second, tiny launch after them.
+// length, and an in-place update is a second, tiny launch after them.  So it is
+// where the new lengths go into what other warps still read: the start
+// positions (the old lengths of one sequence, say) or the counts.
 //
 // Measured against the copy rate (6783 GB/s): 32767 tokens, 8 heads, d = 128:
 // 42 us, 94%; 57 sequences of 1147 tokens, 16 heads, d = 64: 83 us, 97%; a
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   }
 }
 
-// lens += counts, in place, after the rows' warps have read them.
+// The new lengths, after the rows' warps have read what they replace.
 __global__ void lens_kernel(const __grid_constant__ AppendArgs a) {
   sa_dev::launch_dependents();
   sa_dev::wait_dependency();
@@ -123,7 +125,10 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t chunks = (most + kTokens - 1) / kTokens;
   const int64_t blocks = (rows * chunks + kWarps - 1) / kWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const bool late = chunks > 1 && a.lens_out == a.c.lens;
+  const size_t out = size_t(rows) * 4, per_seq = size_t(a.c.batch) * 4;
+  const bool late = (chunks > 1 && a.lens_out == a.c.lens) ||
+                    sa_paged::overlap(a.lens_out, out, a.start, per_seq) ||
+                    sa_paged::overlap(a.lens_out, out, a.counts, per_seq);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

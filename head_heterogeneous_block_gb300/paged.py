@@ -152,7 +152,8 @@ class PagedCache:
         (bf16 [batch, num_kv_heads, tokens, d], any strides that are multiples
         of 8, d contiguous) to every row of sequence b, at positions
         ``start[b]``, ``start[b]`` + 1, ... (default: their slots).  The new
-        lengths go to ``lens_out`` (default: ``lens``)."""
+        lengths go to ``lens_out`` (default: ``lens``), which may share memory
+        with ``start`` but not with another row's ``counts``."""
         if _current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.append(k, v, counts, start, lens_out, stream)

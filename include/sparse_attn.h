@@ -562,15 +562,17 @@ typedef struct sa_paged_cache {
  *    num_new tokens of every sequence; start: device [Bt], or NULL: positions
  *    are then slot numbers.
  *  - lens_out: device [Bt][Hkv], receives the new lengths; it may be
- *    cache->lens itself.
+ *    cache->lens itself, and may hold start (the old lengths of one sequence,
+ *    say, which are then read before they change).  It must not overlap counts,
+ *    unless it is that array (Hkv = 1).
  * The caller has put every page that receives a token into the table; pages
  * that receive tokens belong to one row each.
  * dev_status: SA_DEV_BAD_COUNT when a length is outside [0, max_pages*page], a
  * count outside [0, num_new], or a row has no slots left (all are clamped: the
  * tokens that do not fit are dropped), SA_DEV_BAD_INDEX when a page number is
  * outside the pool (the token is dropped; the length still grows).
- * Errors: INVALID_ARG (NULL pointers, misalignment, strides), SHAPE (sizes),
- * UNSUPPORTED (page, d), CUDA.
+ * Errors: INVALID_ARG (NULL pointers, misalignment, strides, lens_out over
+ * counts), SHAPE (sizes), UNSUPPORTED (page, d), CUDA.
  */
 sa_status sparse_attn_paged_append(const sa_paged_cache* cache, const void* k_new,
                                    const void* v_new, const int64_t* k_strides,

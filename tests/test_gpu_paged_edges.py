@@ -46,3 +46,51 @@ def test_attend_of_short_sequences_ends_when_waits_give_up(env):
     cache.attend(gq, out=out, lse=lse)
     assert int(cache.dev_status.item()) == 0
     P.check_attend(c, q, out, lse)
+
+
+@pytest.mark.parametrize("Bt,hkv,T", [(1, 8, 1), (1, 8, 300), (70, 1, 1), (5, 1, 300), (1, 1, 1)])
+@pytest.mark.parametrize("inplace", [True, False])
+def test_append_at_the_old_lengths(env, Bt, hkv, T, inplace):
+    # start is a view of the lengths (of one sequence, or with one KV head):
+    # they are read before the new ones replace them, in place or in lens_out
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    lens = np.arange(40, 40 + Bt)
+    c = P.random_cache(T, lens + T, hkv, 64, 32, junk=False)
+    c["lens"] = torch.as_tensor(lens, dtype=torch.int32)[:, None].expand(-1, hkv).contiguous()
+    dev, cache = P.to_gpu(c, sa)
+    kn = torch.randn(Bt, hkv, T, 64, generator=torch.Generator().manual_seed(T)).bfloat16()
+    out = dev["lens"] if inplace else dev["lens"] + 1000
+    start = out[:, 0]
+    assert start.is_contiguous() and start.data_ptr() == out.data_ptr()
+    ref = op.append(P.f64(c["k"]), P.f64(c["v"]), c["table"].numpy(), c["lens"].numpy(), P.f64(kn),
+                    P.f64(kn), [T] * Bt, start.cpu().numpy(), P.f64(c["weights"]),
+                    c["positions"].numpy())
+    cache.append(kn.cuda(), kn.cuda(), start=start, lens_out=None if inplace else out)
+    assert int(cache.dev_status.item()) == 0
+    assert np.array_equal(P.f64(dev["k"]), ref[0]) and np.array_equal(P.f64(dev["v"]), ref[1])
+    assert np.array_equal(out.cpu().numpy(), ref[2])
+    assert np.array_equal(dev["positions"].cpu().numpy(), ref[4])
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_append_into_the_counts(env, T):
+    # with one KV head the new lengths may replace the counts they come from
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(T, [50 + T, 3 + T, 90 + T], 1, 64, 32, junk=False)
+    c["lens"] = torch.tensor([[50], [3], [90]], dtype=torch.int32)
+    dev, cache = P.to_gpu(c, sa)
+    counts = torch.tensor([T, 0, max(1, T - 1)], dtype=torch.int32, device="cuda")
+    want = (dev["lens"][:, 0] + counts).tolist()
+    kn = torch.randn(3, 1, T, 64, device="cuda").bfloat16()
+    cache.append(kn, kn, counts=counts, lens_out=counts[:, None])
+    assert int(cache.dev_status.item()) == 0
+    assert counts.tolist() == want and dev["lens"].flatten().tolist() == [50, 3, 90]
+    at, x = dev["table"][2, 0, (90 + counts[2] - 91) // 32].long(), (counts[2].item() - 1) % 32
+    assert torch.equal(dev["k"][at, x], kn[2, 0, counts[2].item() - 91])
+    two = P.to_gpu(P.random_cache(1, [50, 60], 2, 64, 32, junk=False), sa)[1]
+    kn = torch.zeros(2, 2, 1, 64, device="cuda").bfloat16()
+    with pytest.raises(sa.SparseAttnError):            # row (0, 1) would replace sequence 1's count
+        two.append(kn, kn, counts=two.lens.view(-1)[1:3])
