@@ -100,11 +100,16 @@ struct Mover {
       tp = table[t >> shift];
       so = s & (a.c.page - 1);
       to = t & (a.c.page - 1);
-      a.weights_out[r * cap + t] = a.c.weights[r * cap + s];
-      if (a.positions_out) a.positions_out[r * cap + t] = a.c.positions[r * cap + s];
+      // (read beside the pages: a chain of loads less)
+      const float w = a.c.weights[r * cap + s];
+      const int32_t pos = a.positions_out ? a.c.positions[r * cap + s] : 0;
       if (sp < 0 || sp >= a.c.num_pages || tp < 0 || tp >= a.c.num_pages) {
+        // the token stays where it is, and so does what the hole holds
         atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
         sp = -1;
+      } else {
+        a.weights_out[r * cap + t] = w;
+        if (a.positions_out) a.positions_out[r * cap + t] = pos;
       }
     }
     const bool is_v = (lane / kPiece) & 1;

@@ -641,8 +641,9 @@ sa_status sparse_attn_paged_evict_workspace_size(const sa_paged_cache* cache, si
  *  - The pools change in place; a row's pages must belong to it alone.
  *  - ws: at least sparse_attn_paged_evict_workspace_size bytes, 16-byte
  *    aligned, as for sparse_attn_paged_attend.
- * dev_status: SA_DEV_BAD_COUNT / SA_DEV_BAD_INDEX (a token whose page number is
- * out of range is not moved).
+ * dev_status: SA_DEV_BAD_COUNT / SA_DEV_BAD_INDEX (where the page of a token that
+ * would move, or of the slot that it would move to, is out of range, nothing of
+ * it moves: that slot keeps its token, weight and position).
  * Errors: INVALID_ARG (NULL pointers, no cache->weights, keep[g] < sinks +
  * recent, negative sinks or recent, misalignment), SHAPE, UNSUPPORTED (page, d,
  * Hkv > 256, rows of more than 262144 slots), CUDA.

@@ -94,3 +94,37 @@ def test_append_into_the_counts(env, T):
     kn = torch.zeros(2, 2, 1, 64, device="cuda").bfloat16()
     with pytest.raises(sa.SparseAttnError):            # row (0, 1) would replace sequence 1's count
         two.append(kn, kn, counts=two.lens.view(-1)[1:3])
+
+
+@pytest.mark.parametrize("cap_pages", [7, 300])            # moved by the row's CTA, and by a second launch
+@pytest.mark.parametrize("inplace", [True, False])
+def test_evict_leaves_slots_of_bad_pages_whole(env, cap_pages, inplace):
+    # a token that cannot move, for its own page or the hole's, leaves the
+    # hole's key, value, weight and position together
+    from tests import _paged as P
+    sa, torch = env
+    n, keep = 200, 60
+    c = P.random_cache(61, [n, n, n], 1, 64, 32, max_pages=cap_pages, junk=False)
+    c["weights"][:] = torch.arange(c["weights"].shape[-1]).float()     # the last ones stay
+    c["table"][0, 0, 1] = -3                       # holes 32 to 59
+    c["table"][1, 0, 5] = c["k"].shape[0]          # sources 160 to 191
+    dev, cache = P.to_gpu(c, sa)
+    k0 = dev["k"].cpu()
+    outs = {} if inplace else {"weights_out": torch.zeros_like(dev["weights"]),
+                               "positions_out": torch.zeros_like(dev["positions"])}
+    cache.evict([keep], 0, 0, **outs)
+    torch.cuda.synchronize()
+    assert int(cache.dev_status.item()) == sa.SA_DEV_BAD_INDEX
+    w, pos = (outs["weights_out"], outs["positions_out"]) if not inplace else (dev["weights"], dev["positions"])
+    k1 = dev["k"].cpu()
+    assert dev["lens"].flatten().tolist() == [keep] * 3
+    for b in range(3):
+        for t in range(keep):                      # slot t takes the token of slot 140 + t
+            s = 140 + t
+            stays = (b == 0 and t >= 32) or (b == 1 and 160 <= s < 192)
+            holds = t if stays else s
+            assert w[b, 0, t].item() == holds and pos[b, 0, t].item() == holds
+            page = c["table"][b, 0, t // 32].item()
+            if 0 <= page < k0.shape[0]:
+                was = c["table"][b, 0, holds // 32].item()
+                assert torch.equal(k1[page, t % 32], k0[was, holds % 32])
