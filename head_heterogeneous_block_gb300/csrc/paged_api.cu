@@ -54,6 +54,15 @@ sa_status check_heads(const sa_paged_cache* c, int32_t hq) {
   return SA_OK;
 }
 
+// What eviction serves: budgets are a kernel parameter, a row's keys lie in a
+// cluster's shared memory.
+sa_status check_evict(const sa_paged_cache* c) {
+  if (c->num_kv_heads > sa_paged::kMaxKvHeads ||
+      int64_t(c->page) * c->max_pages > sa_paged::kMaxEvictSlots)
+    return SA_ERR_UNSUPPORTED;
+  return SA_OK;
+}
+
 // Processors of the current device, asked for once.
 sa_status sm_count(int* sms) {
   static std::atomic<int> known[sa_paged::kMaxDevices];
@@ -174,6 +183,8 @@ sa_status sparse_attn_paged_evict_workspace_size(const sa_paged_cache* cache, si
   if (!bytes) return SA_ERR_INVALID_ARG;
   sa_status s = check_cache(cache);
   if (s != SA_OK) return s;
+  s = check_evict(cache);
+  if (s != SA_OK) return s;
   *bytes = sa_paged::evict_workspace(*cache);
   return SA_OK;
 }
@@ -184,6 +195,8 @@ sa_status sparse_attn_paged_evict(const sa_paged_cache* cache, const int32_t* ke
                                   int32_t* dev_status, sa_stream_t stream) {
   sa_status s = check_cache(cache);
   if (s != SA_OK) return s;
+  s = check_evict(cache);
+  if (s != SA_OK) return s;
   if (!keep || !cache->weights || !lens_out || !weights_out || !ws || !dev_status)
     return SA_ERR_INVALID_ARG;
   if ((cache->positions != nullptr) != (positions_out != nullptr)) return SA_ERR_INVALID_ARG;
@@ -191,9 +204,6 @@ sa_status sparse_attn_paged_evict(const sa_paged_cache* cache, const int32_t* ke
   if (!aligned(lens_out, 4) || !aligned(weights_out, 4) || !aligned(positions_out, 4) ||
       !aligned(ws, 16) || !aligned(dev_status, 4))
     return SA_ERR_INVALID_ARG;
-  if (cache->num_kv_heads > sa_paged::kMaxKvHeads ||
-      int64_t(cache->page) * cache->max_pages > sa_paged::kMaxEvictSlots)
-    return SA_ERR_UNSUPPORTED;
   sa_paged::EvictArgs a;
   for (int32_t g = 0; g < cache->num_kv_heads; ++g) {
     if (keep[g] < 0 || int64_t(keep[g]) < int64_t(sinks) + recent) return SA_ERR_INVALID_ARG;

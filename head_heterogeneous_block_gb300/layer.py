@@ -12,6 +12,8 @@ the computation runs in libsparse_attn's kernels.
 """
 from __future__ import annotations
 
+import operator
+
 import torch
 
 from . import (SA_HEAD_RETRIEVAL, SA_HEAD_STREAMING, Shape, sparse_attn_forward,
@@ -20,7 +22,7 @@ from . import (SA_HEAD_RETRIEVAL, SA_HEAD_STREAMING, Shape, sparse_attn_forward,
                sparse_attn_score_select, sparse_attn_score_workspace_size, sparse_attn_select,
                sparse_attn_decode_step,
                sparse_attn_select_kind)
-from .paged import PageBook, PagedCache
+from .paged import MAX_EVICT_KV_HEADS, MAX_EVICT_SLOTS, PageBook, PagedCache
 
 
 class PrefillLayer:
@@ -288,11 +290,22 @@ class PagedDecodeLayer:
                  recent: int = 16, device="cuda", out_dtype=torch.bfloat16):
         if max_tokens < 1 or slack < 0:
             raise ValueError("max_tokens must be positive, slack not negative")
-        if keep is not None and (len(keep) != num_kv_heads or min(keep) < sinks + recent):
-            raise ValueError("keep must hold at least sinks + recent tokens per KV head")
+        max_pages = -(-max_tokens // page)
+        if keep is not None:
+            # what an eviction would refuse, in the middle of a step, is refused here
+            sinks, recent = operator.index(sinks), operator.index(recent)
+            if sinks < 0 or recent < 0:
+                raise ValueError("sinks and recent must not be negative")
+            if len(keep) != num_kv_heads or min(keep) < sinks + recent:
+                raise ValueError("keep must hold at least sinks + recent tokens per KV head")
+            slots = max_pages * page
+            if min(keep) + slack < slots and (
+                    slots > MAX_EVICT_SLOTS or num_kv_heads > MAX_EVICT_KV_HEADS or
+                    max(keep) >= 2**31):
+                raise ValueError(f"eviction serves rows of at most {MAX_EVICT_SLOTS} tokens, at "
+                                 f"most {MAX_EVICT_KV_HEADS} KV heads and 32-bit budgets")
         dev = torch.device(device)
         self.keep, self.slack, self.sinks, self.recent = keep, slack, sinks, recent
-        max_pages = -(-max_tokens // page)
         slots = (batch, num_kv_heads, max_pages * page)
         self.k_pages = torch.empty(num_pages, page, head_dim, dtype=torch.bfloat16, device=dev)
         self.v_pages = torch.empty_like(self.k_pages)

@@ -17,6 +17,8 @@ from . import (SA_DTYPE_BF16, SA_DTYPE_F32, PagedCacheDesc, _check, _lib,
 
 _I64x3 = ctypes.c_int64 * 3
 _INT32_MAX = 2**31 - 1
+# what eviction serves (attention goes further)
+MAX_EVICT_SLOTS, MAX_EVICT_KV_HEADS = 262144, 256
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _append, _attend, _evict = (_lib.sparse_attn_paged_append, _lib.sparse_attn_paged_attend,
@@ -34,7 +36,8 @@ class PagedCache:
     ``positions`` int32 of the same shape, or None
 
     ``num_q_heads`` only sizes the workspace ahead of the first ``attend``
-    (before a graph capture, say).  The calls of one PagedCache share its
+    (before a graph capture, say).  Rows of more than 262144 slots, or more
+    than 256 KV heads, can have weights but not be evicted from.  The calls of one PagedCache share its
     workspace: they must not run at the same time on several streams, nor may
     the replays of graphs that hold them.  A graph that captured a call needs
     its PagedCache, and its tensors, to live.
@@ -97,7 +100,7 @@ class PagedCache:
         self._sized = set()
         if num_q_heads is not None:
             self._size(num_q_heads, weights is not None)
-        if weights is not None:
+        if weights is not None and self.slots <= MAX_EVICT_SLOTS and h <= MAX_EVICT_KV_HEADS:
             self._size()
 
     # -- helpers (a step's calls are short: checks are written out where a

@@ -619,7 +619,11 @@ sa_status sparse_attn_paged_attend(const sa_paged_cache* cache, const void* q, i
                                    int32_t o_dtype, float* lse, float* weights_out, void* ws,
                                    size_t ws_bytes, int32_t* dev_status, sa_stream_t stream);
 
-/* Workspace bytes of sparse_attn_paged_evict.  Host only. */
+/*
+ * Workspace bytes of sparse_attn_paged_evict.  Host only.
+ * Errors: INVALID_ARG, SHAPE, UNSUPPORTED (a cache that
+ * sparse_attn_paged_evict does not serve).
+ */
 sa_status sparse_attn_paged_evict_workspace_size(const sa_paged_cache* cache, size_t* bytes);
 
 /*

@@ -128,3 +128,17 @@ def test_evict_leaves_slots_of_bad_pages_whole(env, cap_pages, inplace):
             if 0 <= page < k0.shape[0]:
                 was = c["table"][b, 0, holds // 32].item()
                 assert torch.equal(k1[page, t % 32], k0[was, holds % 32])
+
+
+def test_rows_too_long_for_eviction_still_attend(env):
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(62, [300, 77], 2, 64, 32, max_pages=262144 // 32 + 1)
+    dev, cache = P.to_gpu(c, sa, num_q_heads=4)
+    q = _q(torch, 51, 2, 4, 64)
+    o = cache.attend(q.cuda())
+    assert int(cache.dev_status.item()) == 0
+    P.check_attend(c, q, o, None, dev["weights"])
+    with pytest.raises(sa.SparseAttnError) as e:
+        cache.evict([100, 100])
+    assert e.value.status == 3 and torch.equal(dev["lens"].cpu(), c["lens"])

@@ -12,3 +12,35 @@ def test_append_refuses_lengths_over_the_counts(sa):  # noqa: F811
     for at in (P, P + 4, P + 12, P - 4):
         assert _append(sa, desc(sa), counts=at, lens_out=P, start=None) == 1
     assert _append(sa, desc(sa, num_kv_heads=1), counts=P + 4, lens_out=P, start=None) == 1
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(), 0), (dict(max_pages=262144 // 32), 0), (dict(max_pages=262144 // 32 + 1), 3),
+    (dict(num_kv_heads=256), 0), (dict(num_kv_heads=257), 3),
+])
+def test_the_eviction_workspace_of_what_eviction_serves(sa, change, status):  # noqa: F811
+    n = ctypes.c_size_t()
+    d = desc(sa, **change)
+    assert sa._lib.sparse_attn_paged_evict_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status
+    d.weights = None                               # the query needs no arrays but the cache's
+    assert sa._lib.sparse_attn_paged_evict_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status
+
+
+@pytest.mark.parametrize("change", [
+    dict(max_tokens=300000), dict(max_tokens=262145), dict(num_kv_heads=257, keep=[64] * 257),
+    dict(sinks=-1), dict(recent=-4), dict(keep=[64, 2**31]), dict(keep=[64, 19]), dict(keep=[64]),
+])
+def test_decode_layer_refuses_what_eviction_cannot_serve(sa, change):  # noqa: F811
+    # before anything is allocated: nowhere near a device
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    args = dict(batch=1, num_q_heads=8, num_kv_heads=2, head_dim=64, page=16, num_pages=10,
+                max_tokens=1000, keep=[64, 80], device="cpu")
+    with pytest.raises(ValueError, match="keep|eviction|sinks"):
+        PagedDecodeLayer(**{**args, **change})
+    for kind in (dict(sinks=4.0), dict(recent="16")):
+        with pytest.raises(TypeError):
+            PagedDecodeLayer(**{**args, **kind})
+    # budgets that no row can pass need no eviction: the first refusal is the device's
+    for fine in (dict(max_tokens=262144), dict(max_tokens=300000, keep=[300000] * 2)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            PagedDecodeLayer(**{**args, **fine})
