@@ -293,6 +293,7 @@ class PagedDecodeLayer:
         max_pages = -(-max_tokens // page)
         if keep is not None:
             # what an eviction would refuse, in the middle of a step, is refused here
+            keep = [int(k) for k in keep]          # the layer's own, whole numbers as evict takes
             sinks, recent = operator.index(sinks), operator.index(recent)
             if sinks < 0 or recent < 0:
                 raise ValueError("sinks and recent must not be negative")

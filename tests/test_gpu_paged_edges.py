@@ -142,3 +142,15 @@ def test_rows_too_long_for_eviction_still_attend(env):
     with pytest.raises(sa.SparseAttnError) as e:
         cache.evict([100, 100])
     assert e.value.status == 3 and torch.equal(dev["lens"].cpu(), c["lens"])
+
+
+def test_paged_decode_layer_copies_its_budgets(env):
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    sa, torch = env
+    keep = np.array([40.5, 60.0])
+    layer = PagedDecodeLayer(1, 8, 2, 64, 16, 20, 200, keep=keep)
+    keep[:] = 0
+    k = torch.zeros(2, 100, 64, dtype=torch.bfloat16, device="cuda")
+    layer.admit(0, k, k)
+    assert layer.lens.tolist() == layer.book.lens == [[40, 60]]
+    assert len(layer.book.free) == 20 - 3 - 4
