@@ -96,7 +96,8 @@ class PagedCache:
         self._status = self.dev_status.data_ptr()
         self._ws, self._ws_ptr, self._ws_bytes = None, None, 0
         self._outgrown = []
-        self._ws_stream = _raw_stream(self._index)
+        # the streams that the status word and the workspace were allocated on
+        self._status_stream = self._ws_stream = _raw_stream(self._index)
         self._sized = set()
         if num_q_heads is not None:
             self._size(num_q_heads, weights is not None)
@@ -132,13 +133,12 @@ class PagedCache:
             handle = _raw_stream(self._index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if handle != self._ws_stream:
-            # the cache's own tensors outlive the work of streams they were
-            # not allocated on
-            other = self._stream(handle)
-            self.dev_status.record_stream(other)
-            if self._ws is not None:
-                self._ws.record_stream(other)
+        # the cache's own tensors outlive the work of streams they were not
+        # allocated on
+        if handle != self._status_stream:
+            self.dev_status.record_stream(self._stream(handle))
+        if handle != self._ws_stream and self._ws is not None:
+            self._ws.record_stream(self._stream(handle))
         return handle
 
     def _own(self, t, dtype, shape, name):

@@ -154,3 +154,33 @@ def test_paged_decode_layer_copies_its_budgets(env):
     layer.admit(0, k, k)
     assert layer.lens.tolist() == layer.book.lens == [[40, 60]]
     assert len(layer.book.free) == 20 - 3 - 4
+
+
+def _reused(torch, address):
+    """Whether the current stream's small allocations are given the address."""
+    got = [torch.empty(1, dtype=torch.int32, device="cuda") for _ in range(8192)]
+    return any(x.data_ptr() == address for x in got)
+
+
+def test_status_word_outlives_work_of_the_workspaces_stream(env):
+    # the status word comes from one stream, the workspace from the first
+    # attend on another; the cache is dropped with that stream at work
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(63, [700, 90], 2, 128, 32)
+    q = _q(torch, 52, 2, 40, 128).cuda()
+    for first in (None, 8):                        # the workspace made, or outgrown, there
+        dev, cache = P.to_gpu(c, sa, with_weights=False, num_q_heads=first)
+        before = cache._ws_bytes
+        out = torch.empty(2, 40, 128, dtype=torch.bfloat16, device="cuda")
+        address = cache.dev_status.data_ptr()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        cache.attend(q, out=out, stream=side)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(600_000_000)
+        cache.attend(q, out=out, stream=side)
+        assert cache._ws_bytes > before
+        del cache
+        assert not _reused(torch, address) and not side.query()
+        torch.cuda.synchronize()
