@@ -333,7 +333,7 @@ class PagedDecodeLayer:
             return
         self._streams.add(stream)
         for t in (self.k_pages, self.v_pages, self.table, self.lens, self.weights,
-                  self.positions, self.counts, self.start, self.out):
+                  self.positions, self.counts, self.start, self.out, self.cache.dev_status):
             if t is not None:
                 t.record_stream(stream)
 

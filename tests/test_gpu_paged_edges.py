@@ -184,3 +184,20 @@ def test_status_word_outlives_work_of_the_workspaces_stream(env):
         del cache
         assert not _reused(torch, address) and not side.query()
         torch.cuda.synchronize()
+
+
+def test_layers_status_word_outlives_work_of_another_stream(env):
+    # an admission on another stream ORs its status word into the layer's
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    sa, torch = env
+    layer = PagedDecodeLayer(1, 8, 2, 64, 16, 20, 200)
+    k = torch.zeros(2, 40, 64, dtype=torch.bfloat16, device="cuda")
+    address = layer.cache.dev_status.data_ptr()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        layer.admit(0, k, k)
+        torch.cuda._sleep(600_000_000)
+    del layer
+    assert not _reused(torch, address) and not side.query()
+    torch.cuda.synchronize()
