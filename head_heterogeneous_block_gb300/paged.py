@@ -127,12 +127,18 @@ class PagedCache:
         return (torch.cuda.ExternalStream(handle, device=self.device) if handle else
                 torch.cuda.default_stream(self.device))
 
+    def _given(self, stream):
+        """Handle of a ``stream`` argument: a handle, or a stream of the
+        cache's device."""
+        if isinstance(stream, int):
+            return stream
+        if stream.device_index != self._index:
+            raise ValueError(f"stream must be on {self.device}")
+        return stream.cuda_stream
+
     def _handle(self, stream):
         """The stream's handle; the cache's device is current."""
-        if stream is None:
-            handle = _raw_stream(self._index)
-        else:
-            handle = stream if isinstance(stream, int) else stream.cuda_stream
+        handle = _raw_stream(self._index) if stream is None else self._given(stream)
         # the cache's own tensors outlive the work of streams they were not
         # allocated on
         if handle != self._status_stream:
@@ -202,8 +208,7 @@ class PagedCache:
         if _current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.attend(q, out, lse, weights_out, accumulate, stream)
-        if stream is not None and (stream if isinstance(stream, int) else
-                                   stream.cuda_stream) != _raw_stream(self._index):
+        if stream is not None and self._given(stream) != _raw_stream(self._index):
             # what is allocated here (the output, a larger workspace) comes from
             # the launching stream's memory: the current stream may still be at
             # work in what it freed

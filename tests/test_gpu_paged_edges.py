@@ -201,3 +201,22 @@ def test_layers_status_word_outlives_work_of_another_stream(env):
     del layer
     assert not _reused(torch, address) and not side.query()
     torch.cuda.synchronize()
+
+
+def test_streams_of_another_device_are_refused(env):
+    from types import SimpleNamespace
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(64, [40], 2, 64, 16, max_pages=4)
+    dev, cache = P.to_gpu(c, sa)
+    state = {n: dev[n].clone() for n in ("lens", "weights", "positions")}
+    other = SimpleNamespace(device_index=dev["k"].get_device() + 1, cuda_stream=0)
+    q = torch.zeros(1, 8, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: cache.append(k, k, stream=other), lambda: cache.attend(q, stream=other),
+                 lambda: cache.evict([10, 10], stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    torch.cuda.synchronize()
+    for n, t in state.items():
+        assert torch.equal(dev[n], t)
