@@ -10,7 +10,9 @@ has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sys
 
 import numpy as np
 
@@ -24,10 +26,14 @@ __all__ = [
     "sparse_attn_set_wait_limit", "sparse_attn_select_kind", "sparse_attn_forward_kind",
     "sparse_attn_score_select",
     "sparse_attn_decode_step",
-    "PagedCacheDesc", "PagedCache", "sparse_attn_paged_append", "sparse_attn_paged_attend",
+    "PagedCacheDesc", "sparse_attn_paged_append", "sparse_attn_paged_attend",
     "sparse_attn_paged_attend_workspace_size", "sparse_attn_paged_evict",
     "sparse_attn_paged_evict_workspace_size",
 ]
+# PagedCache needs torch, which the C binding itself does not: `import *` asks
+# for it only where there is one
+if sys.modules.get("torch", True) and importlib.util.find_spec("torch"):
+    __all__.append("PagedCache")
 
 SA_OK = 0
 SA_MODE_PREFILL, SA_MODE_DECODE = 0, 1
@@ -480,7 +486,6 @@ def sparse_attn_paged_evict(cache: PagedCacheDesc, keep, sinks: int, recent: int
 
 
 def __getattr__(name):
-    # PagedCache needs torch, which the C binding itself does not
     if name == "PagedCache":
         from .paged import PagedCache
         return PagedCache

@@ -44,3 +44,16 @@ def test_decode_layer_refuses_what_eviction_cannot_serve(sa, change):  # noqa: F
     for fine in (dict(max_tokens=262144), dict(max_tokens=300000, keep=[300000] * 2)):
         with pytest.raises(ValueError, match="CUDA device"):
             PagedDecodeLayer(**{**args, **fine})
+
+
+@pytest.mark.parametrize("torch", [True, False])
+def test_star_import_with_and_without_torch(sa, torch):  # noqa: F811
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("" if torch else "import sys; sys.modules['torch'] = None\n") + (
+        "from head_heterogeneous_block_gb300 import *\n"
+        f"assert callable(sparse_attn_paged_append) and ('PagedCache' in globals()) is {torch}\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
