@@ -220,3 +220,21 @@ def test_streams_of_another_device_are_refused(env):
     torch.cuda.synchronize()
     for n, t in state.items():
         assert torch.equal(dev[n], t)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 5, 8, 9, 16, 17, 32, 40])
+def test_fp32_outputs_have_all_parts_of_the_weights(env, G, d):
+    # scores without an error to hide behind: see the bound's derivation
+    from tests import _paged_fp32 as F
+    sa, torch = env
+    from tests import _paged as P
+    for lens, hkv, unit in (([0, 1, 24, 64, 100, 128, 300, 1000], 2, 64), ([64, 24, 128, 1] * 40, 1, 128)):
+        c, q = F.inputs(d + G, lens, hkv, G, d, 32)
+        dev, cache = P.to_gpu(c, sa, with_weights=False)
+        out = torch.empty(q.shape, device="cuda")
+        cache.attend(q.cuda(), out=out)
+        assert int(cache.dev_status.item()) == 0
+        over = F.check(c, q, out, unit)
+        assert (over <= 1).all(), over.max()
+        assert (out[np.array(lens) == 0] == 0).all()
