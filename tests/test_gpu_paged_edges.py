@@ -238,3 +238,74 @@ def test_fp32_outputs_have_all_parts_of_the_weights(env, G, d):
         over = F.check(c, q, out, unit)
         assert (over <= 1).all(), over.max()
         assert (out[np.array(lens) == 0] == 0).all()
+
+
+def test_binding_functions_give_what_the_class_gives(env):
+    # the torch-free functions, on addresses and explicit strides
+    from tests import _paged as P
+    sa, torch = env
+    c = P.random_cache(65, [[50, 200], [0, 77]], 2, 64, 16, max_pages=16, spare=50, junk=False)
+    free = [x for x in range(c["k"].shape[0]) if x not in c["table"].flatten().tolist()]
+    c["table"][c["table"] < 0] = torch.tensor(free[:int((c["table"] < 0).sum())], dtype=torch.int32)
+    q = _q(torch, 53, 2, 8, 64).cuda()
+    qkv = torch.randn(2, 3, 6, 64, device="cuda").bfloat16()
+    k, v = qkv[:, :, 2:4].transpose(1, 2), qkv[:, :, 4:].transpose(1, 2)
+    counts = torch.tensor([3, 2], dtype=torch.int32, device="cuda")
+    start = torch.tensor([900, 800], dtype=torch.int32, device="cuda")
+    states, outs = [], []
+    for binding in (False, True):
+        dev, cache = P.to_gpu(c, sa, num_q_heads=8)
+        out, lse = torch.empty(2, 8, 64, device="cuda"), torch.empty(2, 8, device="cuda")
+        if binding:
+            d = cache.desc
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            need = max(sa.sparse_attn_paged_attend_workspace_size(d, 8, True),
+                       sa.sparse_attn_paged_evict_workspace_size(d))
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            stream = torch.cuda.current_stream()
+            sa.sparse_attn_paged_append(d, k.data_ptr(), v.data_ptr(), k.stride()[:3], v.stride()[:3],
+                                        3, counts, start, dev["lens"], st, stream=stream)
+            sa.sparse_attn_paged_attend(d, q.data_ptr(), *q.stride()[:2], 8, out, lse, dev["weights"],
+                                        ws, need, st, stream=stream)
+            sa.sparse_attn_paged_evict(d, [40, 60], 4, 8, dev["lens"], dev["weights"],
+                                       dev["positions"], ws, need, st, stream=stream)
+            assert int(st.item()) == 0
+        else:
+            cache.append(k, v, counts=counts, start=start)
+            cache.attend(q, out=out, lse=lse)
+            cache.evict([40, 60], 4, 8)
+        assert int(cache.dev_status.item()) == 0
+        torch.cuda.synchronize()
+        states.append(dev)
+        outs.append((out, lse))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert states[0]["lens"].tolist() == [[40, 60], [2, 60]]
+    for n in states[0]:
+        assert torch.equal(states[0][n], states[1][n]), n
+
+
+def test_weights_that_an_admission_leaves(env):
+    # each query attends over the whole prompt, later tokens included
+    from head_heterogeneous_block_gb300.layer import PagedDecodeLayer
+    from oracle import paged as op
+    from tests import _paged as P
+    sa, torch = env
+    S, W, hkv, hq, d = 150, 5, 2, 8, 64
+    g = torch.Generator().manual_seed(66)
+    k, v = (torch.randn(hkv, S, d, generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(W, hq, d, generator=g).bfloat16()
+    layer = PagedDecodeLayer(2, hq, hkv, d, 16, num_pages=40, max_tokens=200, keep=[200, 200])
+    layer.admit(1, k.cuda(), v.cuda(), queries=q.cuda())
+    assert int(layer.cache.dev_status.item()) == 0 and layer.lens.tolist() == [[0, 0], [S, S]]
+    got = P.f64(layer.weights)
+    table, lens = np.arange(hkv, dtype=np.int32)[None, :, None], np.full((1, hkv), S, np.int32)
+    want, tol = np.zeros((hkv, S)), np.zeros((hkv, S))
+    for i in range(W):
+        _, _, w, _, absqk = op.attend(P.f64(q[i:i + 1]), P.f64(k), P.f64(v), table, lens,
+                                      np.zeros((1, hkv, S)))
+        E = absqk[0].reshape(hkv, -1).max(1)[:, None] * (d + 8) * 2.0 ** -23
+        want += w[0]
+        tol += (2 * E + 2.0 ** -20 + S * 2.0 ** -23) * w[0]
+    tol += W * 2.0 ** -22 * want                   # as many additions to the weight
+    assert (np.abs(got[1, :, :S] - want) <= tol).all()
+    assert (got[0] == 0).all() and (got[1, :, S:] == 0).all()

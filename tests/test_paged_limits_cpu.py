@@ -57,3 +57,21 @@ def test_star_import_with_and_without_torch(sa, torch):  # noqa: F811
         f"assert callable(sparse_attn_paged_append) and ('PagedCache' in globals()) is {torch}\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_binding_functions_raise_on_a_refusal(sa):  # noqa: F811
+    d = desc(sa)
+    with pytest.raises(sa.SparseAttnError) as e:
+        sa.sparse_attn_paged_append(d, P, P, (1024, 128, 4), (1024, 128, 256), 4, None, None, P, P,
+                                    stream=0)
+    assert e.value.status == 1
+    with pytest.raises(sa.SparseAttnError) as e:
+        sa.sparse_attn_paged_attend(d, P, 1024, 128, 7, P, None, None, P, 1 << 40, P,
+                                    o_dtype=sa.SA_DTYPE_BF16, stream=0)
+    assert e.value.status == 2
+    with pytest.raises(sa.SparseAttnError) as e:
+        sa.sparse_attn_paged_evict(d, [50, 19], 4, 16, P, P, P, P, 1 << 40, P, stream=0)
+    assert e.value.status == 1
+    for keep in ([50], [50, -1], [50, 2**31]):
+        with pytest.raises(ValueError):
+            sa.sparse_attn_paged_evict(d, keep, 4, 16, P, P, P, P, 1 << 40, P, stream=0)
