@@ -86,7 +86,7 @@ __device__ __forceinline__ bool attend_warp(const Row& r, const float (&q4)[4],
   for (int x = warp; x < units; x += kWarps) {
     const uint32_t c = base + uint32_t(used);
     const int s = int(c % kStages);
-    if (!sa_dev::wait_all(&full[s], (c / kStages) & 1u, nullptr, r.limit)) {
+    if (!sa_dev::wait_all<true>(&full[s], (c / kStages) & 1u, nullptr, r.limit)) {
       ok = false;
       break;
     }

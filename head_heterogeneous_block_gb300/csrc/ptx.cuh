@@ -73,15 +73,20 @@ __device__ __forceinline__ bool mbar_test_sleep(uint64_t* bar, uint32_t parity, 
 
 // Wait until the phase with the given parity has completed.  Returns false if
 // the wait gave up (time limit, or *abort set by another role).  The hardware
-// suspend between polls is capped by the limit, so a short limit is honoured
-// at about its own scale.
+// suspend between polls is given the limit as its hint, but may last for a
+// copy's whole time whatever the hint: with kShort, limits below kSuspendNs
+// are polled for without it, and so run out at their own scale.
+constexpr uint64_t kSuspendNs = 2000;
+template <bool kShort = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_test(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   const uint32_t hint = limit_ns < 20000u ? uint32_t(limit_ns) : 20000u;
   for (;;) {
-    if (mbar_test_sleep(bar, parity, hint)) return true;
+    if (kShort && limit_ns < kSuspendNs ? mbar_test(bar, parity)
+                                        : mbar_test_sleep(bar, parity, hint))
+      return true;
     if (abort && *abort) return false;
     if (global_ns() - t0 > limit_ns) return false;
   }
@@ -108,9 +113,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // Every lane waits; the warp gives up together if any lane gave up, so that
 // no lane goes on alone into a warp-collective (.sync.aligned) instruction.
+template <bool kShort = false>
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          uint64_t limit_ns = kWaitLimitNs) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+  return __all_sync(0xffffffffu, mbar_wait<kShort>(bar, parity, abort, limit_ns));
 }
 
 // Named barrier kId of kCount threads; true for all when any passed true.
