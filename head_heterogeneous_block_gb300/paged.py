@@ -96,8 +96,9 @@ class PagedCache:
         self._status = self.dev_status.data_ptr()
         self._ws, self._ws_ptr, self._ws_bytes = None, None, 0
         self._outgrown = []
-        # the streams that the status word and the workspace were allocated on
-        self._status_stream = self._ws_stream = _raw_stream(self._index)
+        # the streams that the status word and the workspace were allocated on,
+        # and the one that both were (None: they differ)
+        self._status_stream = self._ws_stream = self._home = _raw_stream(self._index)
         self._sized = set()
         if num_q_heads is not None:
             self._size(num_q_heads, weights is not None)
@@ -120,6 +121,7 @@ class PagedCache:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             self._ws_ptr, self._ws_bytes = self._ws.data_ptr(), need
             self._ws_stream = _raw_stream(self._index)
+            self._home = self._ws_stream if self._ws_stream == self._status_stream else None
         self._sized.add((num_q_heads, accumulate))
 
     def _stream(self, handle):
@@ -139,12 +141,13 @@ class PagedCache:
     def _handle(self, stream):
         """The stream's handle; the cache's device is current."""
         handle = _raw_stream(self._index) if stream is None else self._given(stream)
-        # the cache's own tensors outlive the work of streams they were not
-        # allocated on
-        if handle != self._status_stream:
-            self.dev_status.record_stream(self._stream(handle))
-        if handle != self._ws_stream and self._ws is not None:
-            self._ws.record_stream(self._stream(handle))
+        if handle != self._home:
+            # the cache's own tensors outlive the work of streams they were
+            # not allocated on
+            if handle != self._status_stream:
+                self.dev_status.record_stream(self._stream(handle))
+            if handle != self._ws_stream and self._ws is not None:
+                self._ws.record_stream(self._stream(handle))
         return handle
 
     def _own(self, t, dtype, shape, name):
