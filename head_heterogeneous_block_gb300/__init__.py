@@ -32,7 +32,7 @@ __all__ = [
 ]
 # PagedCache needs torch, which the C binding itself does not: `import *` asks
 # for it only where there is one
-if sys.modules.get("torch", True) and importlib.util.find_spec("torch"):
+if (sys.modules["torch"] if "torch" in sys.modules else importlib.util.find_spec("torch")) is not None:
     __all__.append("PagedCache")
 
 SA_OK = 0
