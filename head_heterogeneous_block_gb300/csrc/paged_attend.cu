@@ -51,7 +51,9 @@
 //
 // Measured (GB300, copy rate 6783 GB/s, read-only traffic goes a little
 // higher): 16 sequences of 64K tokens, 28/4 heads, 2.1 GB: 319 us, 99%; one of
-// 128K, 64/8 heads, 537 MB: 87 us, 91%.  The rest is a fixed 9 us or so: the
+// 128K, 64/8 heads, 537 MB: 87 us, 91%.  537 MB in 32 rows or more, by query
+// heads of a KV head, bf16 and fp32 output: 4 heads 85 and 86 us, 8: 88 and 88,
+// 16: 87 and 97, 32: 110 and 111 (at 32, and 16 in fp32, one CTA a processor).  The rest is a fixed 9 us or so: the
 // chain lengths -> page table -> first keys with a cold instruction cache
 // (3 us), the last tile's softmax and store (1 us), the join (2.8 us); it is
 // all there is of one 700-token sequence (8.5 us).  One CTA per processor with

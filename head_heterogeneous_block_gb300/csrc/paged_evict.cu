@@ -27,9 +27,10 @@
 // few rows with much to move, by a second launch over all processors
 // (move_kernel).
 //
-// Measured: 256 rows of 544 to 2080 slots cut by 32: 8.0 us, 1.9 of them for
-// the bytes; 16 rows of 2048 to 4096 cut to 512 to 1024: 8.6 us in two
-// launches; 32 rows of 32768 cut to 1024 to 8192: 34 us, 16 for the select (a
+// Measured: 256 rows of 544 to 2080 slots cut by 32: 7.7 us, 1.9 of them for
+// the bytes (the kernels go by the table, not by the lengths: with 4096 slots
+// to a row of the table 23 us, with 16384 or more 35); 16 rows of 2048 to 4096
+// cut to 512 to 1024: 8.3 us in two launches; 32 rows of 32768 cut to 1024 to 8192: 34 us, 16 for the select (a
 // chain of cluster barriers, each with a histogram added up across it) and 18
 // for the moves' 109 MB, 6.0 TB/s.
 

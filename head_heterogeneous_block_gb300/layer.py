@@ -1,5 +1,5 @@
-"""Whole-layer drivers over the C ABI: buffers come from PyTorch, every step of
-the computation runs in libsparse_attn's kernels.
+"""Whole-layer drivers over the C ABI: buffers come from PyTorch, scores,
+selections, attention, appends and evictions run in libsparse_attn's kernels.
 
 ``PrefillLayer``  Index -> Select -> Attention for one prefill layer
                   (score, select, forward) on a plan built once per
@@ -8,7 +8,8 @@ the computation runs in libsparse_attn's kernels.
                   HBM-resident cache, with the pooled key cache built once.
 ``PagedDecodeLayer``  decode over a paged cache whose sequences have lengths of
                   their own and whose KV heads keep budgets of their own:
-                  append, attend and evict.
+                  append, attend and evict.  (Its page table, counts and
+                  positions are brought up to date by PyTorch operations.)
 """
 from __future__ import annotations
 
@@ -279,7 +280,11 @@ class PagedDecodeLayer:
     tokens' weights; once any row holds ``slack`` tokens more than its budget,
     the rows are cut back to their budgets: the first ``sinks`` positions, the
     last ``recent`` ones, then the largest weights stay.  Pages that rows give
-    up serve others.
+    up serve others.  Eviction serves ``max_tokens`` of up to 262144 and up to
+    256 KV heads.
+
+    With ``keep`` the layer holds a workspace of 4 * batch * num_q_heads *
+    max_tokens bytes for the attention probabilities, whatever its rows hold.
 
     Calls are ordered on one stream: the current one, or the one of the
     caller's ``with torch.cuda.stream``.  They hand out pages on the host, so
@@ -354,8 +359,9 @@ class PagedDecodeLayer:
     def admit(self, b: int, k, v, queries=None):
         """Sequence b starts with the tokens of k, v (bf16 [num_kv_heads, S, d],
         as the prefill layer has them).  ``queries`` (bf16 [W, num_q_heads, d],
-        the prompt's last ones, say) attend over the whole prompt so that the
-        first eviction knows its tokens' weights."""
+        the prompt's last ones, say) attend so that the first eviction knows its
+        tokens' weights: each over the whole prompt, without a causal mask, one
+        after the other."""
         if self.active[b]:
             raise ValueError(f"sequence {b} is not free")
         self._follow()

@@ -294,8 +294,8 @@ class PagedCache:
 
 class PageBook:
     """Which pages of a pool belong to which (sequence, KV head) row, on the
-    host.  Pages are handed out lowest first and come back when rows shrink;
-    nothing here touches the device."""
+    host.  Pages come back when rows shrink, and those that came back last are
+    handed out first; nothing here touches the device."""
 
     def __init__(self, num_pages, page, batch, num_kv_heads, max_pages):
         self.page, self.max_pages = page, max_pages

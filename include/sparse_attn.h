@@ -583,7 +583,11 @@ sa_status sparse_attn_paged_append(const sa_paged_cache* cache, const void* k_ne
 /*
  * Workspace bytes of sparse_attn_paged_attend for `num_q_heads` query heads,
  * with (accumulate = 1) or without a weights_out.  Host only, except that it
- * asks the current device for its number of processors.
+ * asks the current device for its number of processors.  Without accumulation
+ * it is some 10 MB at most, whatever the rows hold; with it come 4 bytes for
+ * every query head and slot of the table: batch*Hq*max_pages*page*4 (32
+ * sequences, 32 heads and 32768 slots: 134 MB).  Caches whose calls do not
+ * overlap can use one workspace.
  */
 sa_status sparse_attn_paged_attend_workspace_size(const sa_paged_cache* cache,
                                                   int32_t num_q_heads, int32_t accumulate,
