@@ -10,6 +10,7 @@ has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import importlib.util
 import os
 import sys
@@ -29,11 +30,13 @@ __all__ = [
     "PagedCacheDesc", "sparse_attn_paged_append", "sparse_attn_paged_attend",
     "sparse_attn_paged_attend_workspace_size", "sparse_attn_paged_evict",
     "sparse_attn_paged_evict_workspace_size",
+    "PackedShape", "sparse_attn_packed_forward", "sparse_attn_packed_workspace_size",
 ]
-# PagedCache needs torch, which the C binding itself does not: `import *` asks
+# these classes need torch, which the C binding itself does not: `import *` asks
 # for it only where there is one
+_CLASSES = {"PagedCache": "paged", "PackedAttention": "packed"}
 if (sys.modules["torch"] if "torch" in sys.modules else importlib.util.find_spec("torch")) is not None:
-    __all__.append("PagedCache")
+    __all__.extend(_CLASSES)
 
 SA_OK = 0
 SA_MODE_PREFILL, SA_MODE_DECODE = 0, 1
@@ -43,7 +46,7 @@ SCHEDULES = {"lpt": SA_SCHED_LPT, "lpt_grouped": SA_SCHED_LPT_GROUPED,
 SA_HEAD_RETRIEVAL, SA_HEAD_STREAMING = 0, 1
 SA_DTYPE_BF16, SA_DTYPE_F32 = 0, 1
 SA_DEV_BAD_INDEX, SA_DEV_BAD_COUNT, SA_DEV_TIMEOUT, SA_DEV_BAD_ITEM, SA_DEV_BAD_LAUNCH = 1, 2, 4, 8, 16
-SA_DEV_RANGE = 32
+SA_DEV_RANGE, SA_DEV_NO_PAGES = 32, 64
 
 
 class Shape(ctypes.Structure):
@@ -84,6 +87,14 @@ class PagedCacheDesc(ctypes.Structure):
                 ("v_page_stride", ctypes.c_int64), ("page", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class PackedShape(ctypes.Structure):
+    """``sa_packed_shape``: sizes and strides of packed sequences."""
+    _fields_ = ([(f"{t}_stride_{x}", ctypes.c_int64) for t in "qkvo" for x in "th"] +
+                [(n, ctypes.c_int32) for n in ("total_q", "total_k", "batch", "num_q_heads",
+                                               "num_kv_heads", "head_dim")] +
+                [("scale", ctypes.c_float)])
 
 
 class SparseAttnError(RuntimeError):
@@ -150,6 +161,10 @@ def _load():
         "sparse_attn_paged_evict": (ctypes.c_int, [ctypes.POINTER(PagedCacheDesc),
                                                    ctypes.POINTER(I32), I32, I32, P, P, P, P, SZ,
                                                    P, P]),
+        "sparse_attn_packed_workspace_size": (ctypes.c_int, [ctypes.POINTER(PackedShape),
+                                                             ctypes.POINTER(SZ)]),
+        "sparse_attn_packed_forward": (ctypes.c_int, [ctypes.POINTER(PackedShape), P, P, P, P, P,
+                                                      P, P, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -485,8 +500,24 @@ def sparse_attn_paged_evict(cache: PagedCacheDesc, keep, sinks: int, recent: int
            "sparse_attn_paged_evict")
 
 
+def sparse_attn_packed_workspace_size(shape: PackedShape) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.sparse_attn_packed_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "sparse_attn_packed_workspace_size")
+    return n.value
+
+
+def sparse_attn_packed_forward(shape: PackedShape, q, k, v, cu_q, cu_k, o, lse, ws, ws_bytes: int,
+                               dev_status, stream=None):
+    """Causal attention of packed sequences; ``q``, ``k``, ``v`` and ``o`` are
+    device addresses with the strides of ``shape``."""
+    _check(_lib.sparse_attn_packed_forward(ctypes.byref(shape), q, k, v, _ptr(cu_q), _ptr(cu_k),
+                                           o, _ptr(lse), _ptr(ws), ws_bytes, _ptr(dev_status),
+                                           _stream(stream)),
+           "sparse_attn_packed_forward")
+
+
 def __getattr__(name):
-    if name == "PagedCache":
-        from .paged import PagedCache
-        return PagedCache
+    if name in _CLASSES:
+        return getattr(importlib.import_module(f".{_CLASSES[name]}", __name__), name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,1452 @@
+// Causal attention of packed prompts of different lengths, on sm_103a.
+//
+//   S = Q K^T,  P = 2^(S c - m),  O = P V / sum P      (c = scale log2 e)
+//
+// per tile of up to 128 query rows and per block of 128 keys: 4 d operations a
+// (query, key) pair against 4 d / 128 bytes from L2, so the tensor cores bound
+// it from a few hundred keys a query on, and the chain of one block's steps
+// bounds short prompts.
+//
+// Tiles.  A tile's rows are `tokens` consecutive tokens of one sequence times
+// `heads` query heads of one KV head (row = token * heads + head): K and V are
+// loaded once for all of them, and a prompt of 40 tokens fills two tiles of 32
+// tokens x 4 heads where four tiles of one head each would be a third full.
+// heads is the largest divisor of the group up to 16 that leaves at most 3 of
+// the 128 rows unused (7 heads: 18 tokens, 126 rows).
+//
+// Schedule.  One CTA per processor takes items (a tile, a range of its key
+// blocks) from a counter.  A first, one-CTA launch reads the lengths and lists
+// the tiles, those with most key blocks first (a counting sort), so that what is
+// left at the end is short; KV head by KV head where the keys and values of all
+// heads would not stay in L2.  A tile that has more blocks than a processor's
+// fair share of all blocks is cut into ranges: each leaves its maximum, sums and
+// unnormalised output, and the CTA that finishes last joins them in order.
+// Where every tile gets a CTA of its own and no range is long, the CTAs find
+// their tiles themselves and there is no first launch.
+//
+// Roles of the twenty warps: 0 producer (items, Q, K), 1 issues Q K^T into
+// one of three S buffers of tensor memory, 2 producer of V, 3 issues P V (P in
+// tensor memory over its S, O accumulates in tensor memory) and stores full
+// output tiles, 4-19 softmax: four column groups of four warps, a thread owns
+// one row and a quarter of its columns.
+//
+// Softmax.  The reference m of a row is its maximum over the item's first
+// block, exchanged once between the groups; later weights may pass 1 and m
+// cancels in O / l.  bf16 has fp32's exponents, so that is exact until a sum
+// passes 2^126 (or O overflows).  An item with such a row is done again after
+// the others ("careful"): first Q K^T alone for the rows' true maxima, then as
+// before with these as m.  It costs 1.5 times an item, whatever the values, and
+// nothing on the common path, which is bound by the softmax warps' issue slots.
+// The weights are rounded to bf16 for the tensor cores; the sum that divides O
+// adds the rounded ones, so that a row of one dominant weight gives its value
+// exactly.  The log-sum-exp adds the unrounded ones.
+//
+// Masked places.  Scores of keys that a row does not see become -infinity
+// whatever they are.  Their values meet weights of 0 in the tensor core, which
+// infinities and NaN survive: in the blocks where the mask cuts (at most two a
+// tile), the softmax warps zero such elements of V in shared memory, and the
+// rows that do see them add them back from global memory at the end.
+//
+// Every wait is bounded; on a timeout the CTA flags SA_DEV_TIMEOUT, lets its
+// copies and MMAs drain, frees its tensor memory and exits.  No CTA waits for
+// another.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "packed.h"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace sa_dev;
+using sa_packed::Args;
+
+constexpr int kRows = 128;            // query rows of a tile
+constexpr int kBK = 128;              // keys of a block
+constexpr int kSoftmaxThreads = 512;
+constexpr int kThreads = 128 + kSoftmaxThreads;
+constexpr int kNI = 4;                // item descriptions in flight
+constexpr int kBatch = 2048;          // items between two looks at what is to be done again
+constexpr int kMinRange = 8;          // key blocks: shorter ranges cost more to join than they save
+constexpr int kBins = 1024;
+constexpr int kScheduleThreads = 1024;
+constexpr int kSeqShared = 4096;      // sequences whose first tiles stay in shared memory
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;            // 128-byte column panels
+  static constexpr int kQPanel = kRows * 128;
+  static constexpr int kKVPanel = kBK * 128;
+  static constexpr int kQBytes = kPanels * kQPanel;
+  static constexpr int kKVBytes = kPanels * kKVPanel;
+  static constexpr int kNQ = 2;
+  static constexpr int kNK = D == 128 ? 2 : 4;      // 32 or 16 KB each
+  static constexpr int kNV = kNK;
+  static constexpr int kNS = 3;
+  static constexpr int kCols = kBK / 4;             // S columns of a softmax group
+  static constexpr int kOCols = D / 4;
+  static constexpr uint32_t kO = kNS * kBK;         // TMEM column of O
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr int kData = kNQ * kQBytes + (kNK + kNV) * kKVBytes;
+};
+
+// One tile, or a range of its key blocks, in the schedule.
+struct __align__(16) Entry {
+  int32_t q0, ntok;       // its tokens (rows of q)
+  int32_t kbeg;           // first key of the sequence (row of k)
+  int32_t lim0;           // last key, from kbeg, that its first token sees (may be negative)
+  int32_t b0, n;          // key blocks
+  int32_t split;          // first partial slot of the tile's ranges, -1: the whole tile
+  int32_t part;           // range | ranges << 16
+};
+
+struct Header {
+  int32_t counter;        // items handed out beyond each CTA's first
+  int32_t entries;
+  int32_t by_head;        // KV head by KV head
+};
+
+struct __align__(16) Item {
+  Entry e;
+  int32_t head0, g, hg;   // first query head, KV head, group of heads
+  int32_t mt;             // blocks before the first masked one
+  int32_t pos;            // place in the batch of items
+  int32_t careful;
+};
+enum { kEnd = 0, kMarker = -1 };      // values of e.n that are not items
+
+struct Shared {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[3], p_full[3], pv_done[3];
+  uint64_t o_last;        // a phase per item: its last P V is complete
+  uint64_t o_free;        // a phase per item: O is in registers
+  uint64_t xch_bar;       // exchanges between the softmax groups
+  uint64_t stage_bar[2];  // items in turn: its output is staged or stored
+  uint64_t part_bar;      // a phase per range: its partial state is written
+  uint64_t tick_bar;      //   and whether it was the tile's last is known
+  uint64_t batch_done;    // a phase per marker: every epilogue before it is through
+  uint64_t drain_qk, drain_pv;
+  uint64_t info_full[kNI], info_empty[kNI];
+  Item info[kNI];
+  int32_t ids[kBatch];    // items of the batch
+  uint32_t redo[kBatch / 32];
+  float xch[2][4][kRows];
+  float xch_l[2][4][kRows];   // unrounded sums, for the log-sum-exp
+  int32_t stage_q0[2], stage_h[2];   // where the tile staged in Q stage x goes; q0 < 0: nowhere
+  int32_t bad_v[2];       // item (by its number, from 1) that met infinities or NaN in masked blocks
+  int32_t last;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct Params {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* o;
+  float* lse;
+  const Header* header;
+  int32_t* counter;
+  const Entry* entries;
+  int32_t* tickets;       // per partial slot; the tile's first one counts
+  float* part_o;          // [slot][128][D]
+  float4* part_ml;        // [slot][128]: m, rounded sum, unrounded sum
+  int64_t v_st, v_sh, o_st, o_sh;
+  int32_t total_q, total_k, batch, Hq, group, tile_heads, tile_tokens;
+  int32_t head_groups;    // tiles' heads: Hq / tile_heads
+  int32_t direct;         // no schedule: a CTA finds its tile
+  float scale_log2;
+  int32_t* dev_status;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ void raise_abort(Shared* sh, const Params& p) {
+  atomicOr(p.dev_status, SA_DEV_TIMEOUT);
+  *(volatile int*)&sh->abort = 1;
+}
+
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t issued, uint32_t stages) {
+  const uint32_t first = issued > stages ? issued - stages : 0;
+  for (uint32_t x = first; x < issued; ++x)
+    mbar_wait(&full[x % stages], (x / stages) & 1, nullptr);
+}
+
+// Key blocks that a tile's last token sees, one at least (an all-masked block
+// then gives the tile's empty rows).
+__device__ __forceinline__ int32_t blocks_of(int32_t lim0, int32_t ntok) {
+  const int32_t seen = lim0 + ntok;
+  return seen <= 0 ? 1 : (seen + kBK - 1) / kBK;
+}
+
+__device__ __forceinline__ int32_t clamp_to(int32_t x, int32_t hi) { return min(max(x, 0), hi); }
+
+// ------------------------------------------------------------- the schedule
+struct ScheduleParams {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  Header* header;
+  int4* seqs;             // [batch]: first query, queries, first key, keys
+  int32_t* tile0;         // [batch] first tile of each sequence
+  Entry* entries;
+  int32_t* tickets;
+  int32_t total_q, total_k, batch, tile_tokens, head_groups, workers, bin_shift, by_head;
+  int32_t max_slots, max_entries;
+  int32_t* dev_status;
+};
+
+// Inclusive scans over the block of a maximum (two at once) and of a sum.
+__device__ __forceinline__ int32_t warp_scan_max(int32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = max(x, y);
+  }
+  return x;
+}
+__device__ __forceinline__ int32_t warp_scan_sum(int32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// The sequence that tile t belongs to: the last one whose first tile is <= t.
+__device__ __forceinline__ int32_t seq_of_tile(const int32_t* tile0, int32_t batch, int32_t t) {
+  int32_t lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (tile0[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ Entry tile_entry(const int4& s, int32_t tile, int32_t tokens) {
+  Entry e;
+  const int32_t at = tile * tokens;
+  e.q0 = s.x + at;
+  e.ntok = min(tokens, s.y - at);
+  e.kbeg = s.z;
+  e.lim0 = at + s.w - s.y;
+  e.b0 = 0;
+  e.n = blocks_of(e.lim0, e.ntok);
+  e.split = -1;
+  e.part = 0;
+  return e;
+}
+
+__global__ void __launch_bounds__(kScheduleThreads)
+    schedule_kernel(const __grid_constant__ ScheduleParams p) {
+  __shared__ int32_t tile0_s[kSeqShared];
+  __shared__ int32_t bins[kBins];
+  __shared__ int32_t wq[32], wk[32], wt[32];
+  __shared__ unsigned long long total;
+  __shared__ int32_t slots, extra;
+  launch_dependents();
+  wait_dependency();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // sequences: starts that never decrease, and the tiles before each
+  int32_t carry_q = clamp_to(p.cu_q[0], p.total_q), carry_k = clamp_to(p.cu_k[0], p.total_k);
+  int32_t carry_t = 0;
+  bool bad = p.cu_q[0] != carry_q || p.cu_k[0] != carry_k;
+  if (tid == 0) {
+    total = 0;
+    slots = extra = 0;
+  }
+  bins[tid] = 0;
+  for (int32_t base = 0; base < p.batch; base += kScheduleThreads) {
+    const int32_t s = base + tid;
+    int32_t q = 0, k = 0;
+    if (s < p.batch) {
+      const int32_t rq = p.cu_q[s + 1], rk = p.cu_k[s + 1];
+      q = clamp_to(rq, p.total_q);
+      k = clamp_to(rk, p.total_k);
+      bad |= q != rq || k != rk;
+    }
+    int32_t mq = warp_scan_max(q, lane), mk = warp_scan_max(k, lane);
+    if (lane == 31) {
+      wq[warp] = mq;
+      wk[warp] = mk;
+    }
+    __syncthreads();
+    int32_t before_q = carry_q, before_k = carry_k, top_q = carry_q, top_k = carry_k;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) {
+        before_q = max(before_q, wq[w]);
+        before_k = max(before_k, wk[w]);
+      }
+      top_q = max(top_q, wq[w]);
+      top_k = max(top_k, wk[w]);
+    }
+    mq = max(mq, before_q);
+    mk = max(mk, before_k);
+    int32_t q0 = __shfl_up_sync(0xffffffffu, mq, 1), k0 = __shfl_up_sync(0xffffffffu, mk, 1);
+    if (lane == 0) {
+      q0 = before_q;
+      k0 = before_k;
+    }
+    bad |= s < p.batch && (q < q0 || k < k0);
+    const int32_t nq = s < p.batch ? mq - q0 : 0;
+    const int32_t tiles = (nq + p.tile_tokens - 1) / p.tile_tokens;
+    const int32_t st = warp_scan_sum(tiles, lane);
+    if (lane == 31) wt[warp] = st;
+    __syncthreads();
+    int32_t before_t = carry_t, all_t = carry_t;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before_t += wt[w];
+      all_t += wt[w];
+    }
+    if (s < p.batch) {
+      p.seqs[s] = make_int4(q0, nq, k0, mk - k0);
+      const int32_t first = before_t + st - tiles;
+      p.tile0[s] = first;
+      if (s < kSeqShared) tile0_s[s] = first;
+    }
+    carry_q = top_q;
+    carry_k = top_k;
+    carry_t = all_t;
+    __syncthreads();
+  }
+  if (bad) atomicOr(p.dev_status, SA_DEV_BAD_COUNT);
+  const int32_t tiles = carry_t;
+  const int32_t* tile0 = p.batch <= kSeqShared ? tile0_s : p.tile0;
+  auto entry = [&](int32_t t) {
+    const int32_t s = seq_of_tile(tile0, p.batch, t);
+    return tile_entry(p.seqs[s], t - tile0[s], p.tile_tokens);
+  };
+  // a processor's share of all blocks
+  unsigned long long mine = 0;
+  for (int32_t t = tid; t < tiles; t += kScheduleThreads) mine += unsigned(entry(t).n);
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0 && mine) atomicAdd(&total, mine);
+  __syncthreads();
+  const unsigned long long share =
+      (total * unsigned(p.head_groups) + unsigned(p.workers) - 1) / unsigned(p.workers);
+  const int32_t range = int32_t(max(share, (unsigned long long)kMinRange));
+  auto ranges_of = [&](int32_t n) { return n > range ? (n + range - 1) / range : 1; };
+  // longest first: a counting sort by the blocks of a tile's ranges
+  auto bin_of = [&](int32_t n) { return kBins - 1 - min(n >> p.bin_shift, kBins - 1); };
+  for (int32_t t = tid; t < tiles; t += kScheduleThreads) {
+    const int32_t n = entry(t).n, r = ranges_of(n);
+    atomicAdd(&bins[bin_of((n + r - 1) / r)], r);
+  }
+  __syncthreads();
+  {
+    const int32_t mine_n = bins[tid];
+    const int32_t sc = warp_scan_sum(mine_n, lane);
+    if (lane == 31) wt[warp] = sc;
+    __syncthreads();
+    int32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += wt[w];
+    bins[tid] = before + sc - mine_n;
+  }
+  __syncthreads();
+  for (int32_t t = tid; t < tiles; t += kScheduleThreads) {
+    Entry e = entry(t);
+    const int32_t n = e.n, r = ranges_of(n);
+    const int32_t at = atomicAdd(&bins[bin_of((n + r - 1) / r)], r);
+    if (r > 1) {
+      e.split = atomicAdd(&slots, r);
+      atomicAdd(&extra, r - 1);
+    }
+    for (int32_t i = 0; i < r; ++i) {
+      e.b0 = int32_t(int64_t(i) * n / r);
+      e.n = int32_t(int64_t(i + 1) * n / r) - e.b0;
+      e.part = i | r << 16;
+      // (always within: sum of ranges of cut tiles x head groups <= 2 workers)
+      if (at + i < p.max_entries) p.entries[at + i] = e;
+      if (e.split >= 0)
+        for (int32_t h = 0; h < p.head_groups; ++h) {
+          const int64_t x = int64_t(e.split + i) * p.head_groups + h;
+          if (x < p.max_slots) p.tickets[x] = 0;
+        }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) *p.header = Header{0, min(tiles + extra, p.max_entries), p.by_head};
+}
+
+// A direct CTA's tile: the warp walks the sequences.  False: there is none.
+__device__ __forceinline__ bool find_tile(const Params& p, int32_t tile, int lane, Entry* out) {
+  int32_t carry_q = clamp_to(__ldcg(p.cu_q), p.total_q), carry_k = clamp_to(__ldcg(p.cu_k), p.total_k);
+  int32_t carry_t = 0;
+  bool bad = __ldcg(p.cu_q) != carry_q || __ldcg(p.cu_k) != carry_k;
+  bool found = false;
+  for (int32_t base = 0; base < p.batch && !found; base += 32) {
+    const int32_t s = base + lane;
+    int32_t q = 0, k = 0;
+    if (s < p.batch) {
+      const int32_t rq = __ldcg(&p.cu_q[s + 1]), rk = __ldcg(&p.cu_k[s + 1]);
+      q = clamp_to(rq, p.total_q);
+      k = clamp_to(rk, p.total_k);
+      bad |= q != rq || k != rk;
+    }
+    const int32_t mq = max(warp_scan_max(q, lane), carry_q);
+    const int32_t mk = max(warp_scan_max(k, lane), carry_k);
+    int32_t q0 = __shfl_up_sync(0xffffffffu, mq, 1), k0 = __shfl_up_sync(0xffffffffu, mk, 1);
+    if (lane == 0) {
+      q0 = carry_q;
+      k0 = carry_k;
+    }
+    bad |= s < p.batch && (q < q0 || k < k0);
+    const int32_t nq = s < p.batch ? mq - q0 : 0;
+    const int32_t tiles = (nq + p.tile_tokens - 1) / p.tile_tokens;
+    const int32_t after = carry_t + warp_scan_sum(tiles, lane);
+    const uint32_t here = __ballot_sync(0xffffffffu, tile >= after - tiles && tile < after);
+    if (here) {
+      const int src = __ffs(here) - 1;
+      int4 seq;
+      seq.x = __shfl_sync(0xffffffffu, q0, src);
+      seq.y = __shfl_sync(0xffffffffu, nq, src);
+      seq.z = __shfl_sync(0xffffffffu, k0, src);
+      seq.w = __shfl_sync(0xffffffffu, mk - k0, src);
+      *out = tile_entry(seq, tile - __shfl_sync(0xffffffffu, after - tiles, src), p.tile_tokens);
+      found = true;
+    }
+    carry_q = __shfl_sync(0xffffffffu, mq, 31);
+    carry_k = __shfl_sync(0xffffffffu, mk, 31);
+    carry_t = __shfl_sync(0xffffffffu, after, 31);
+  }
+  if (bad) atomicOr(p.dev_status, SA_DEV_BAD_COUNT);
+  return found;
+}
+
+// Whether any of the two bf16 values is an infinity or NaN (an exponent of all ones).
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+template <int D, bool kLse>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_attention_kernel(const __grid_constant__ CUtensorMap tq,
+                            const __grid_constant__ CUtensorMap tk,
+                            const __grid_constant__ CUtensorMap tv,
+                            const __grid_constant__ CUtensorMap to,
+                            const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.dev_status, SA_DEV_BAD_LAUNCH);
+    return;
+  }
+  uint8_t* sQ = smem_raw;
+  uint8_t* sK = sQ + C::kNQ * C::kQBytes;
+  uint8_t* sV = sK + C::kNK * C::kKVBytes;
+  Shared* sh = reinterpret_cast<Shared*>(sV + C::kNV * C::kKVBytes);
+  volatile int* abort = &sh->abort;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh->q_full[s], 1);
+      mbar_init(&sh->q_empty[s], 2);   // the last Q K^T, and the output tile leaving the stage
+      mbar_init(&sh->stage_bar[s], kSoftmaxThreads);
+    }
+    for (int s = 0; s < C::kNK; ++s) {
+      mbar_init(&sh->k_full[s], 1);
+      mbar_init(&sh->k_empty[s], 1);
+      mbar_init(&sh->v_full[s], 1);
+      mbar_init(&sh->v_empty[s], 1);
+    }
+    for (int s = 0; s < C::kNS; ++s) {
+      mbar_init(&sh->s_full[s], 1);
+      mbar_init(&sh->p_full[s], kSoftmaxThreads);
+      mbar_init(&sh->pv_done[s], 1);
+    }
+    for (int s = 0; s < kNI; ++s) {
+      mbar_init(&sh->info_full[s], 1);
+      mbar_init(&sh->info_empty[s], 3 + kSoftmaxThreads / 32);
+    }
+    mbar_init(&sh->o_last, 1);
+    mbar_init(&sh->o_free, kSoftmaxThreads);
+    mbar_init(&sh->xch_bar, kSoftmaxThreads);
+    mbar_init(&sh->part_bar, kSoftmaxThreads);
+    mbar_init(&sh->tick_bar, 1);
+    mbar_init(&sh->batch_done, kSoftmaxThreads);
+    mbar_init(&sh->drain_qk, 1);
+    mbar_init(&sh->drain_pv, 1);
+    sh->abort = 0;
+    sh->bad_v[0] = sh->bad_v[1] = 0;
+    fence_mbar_init();
+  }
+  for (int x = threadIdx.x; x < kBatch / 32; x += kThreads) sh->redo[x] = 0;
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------- producer: items, Q, K
+    if (lane == 0) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&to);
+    }
+    const uint64_t pol_kv = l2_policy_evict_last();
+    const uint64_t pol_q = l2_policy_evict_first();
+    uint32_t ii = 0, qi = 0, kiss = 0;   // descriptions, items and K blocks so far
+    bool ok = true;
+    wait_dependency();                   // the schedule, and what the inputs come from
+    const int32_t entries = p.direct ? 0 : __ldcg(&p.header->entries);
+    const bool by_head = p.direct ? false : __ldcg(&p.header->by_head) != 0;
+    const int64_t items = p.direct ? int64_t(gridDim.x) : int64_t(entries) * p.head_groups;
+
+    // room for a description in the ring; lane 0 then fills it
+    auto slot_free = [&]() -> bool {
+      return ii < uint32_t(kNI) ||
+             mbar_wait(&sh->info_empty[ii % kNI], ((ii / kNI) - 1) & 1, abort, p.wait_ns);
+    };
+    auto publish = [&](const Item& it) {
+      sh->info[ii % kNI] = it;
+      mbar_arrive(&sh->info_full[ii % kNI]);
+    };
+    auto special = [&](int32_t what) -> bool {
+      bool good = true;
+      if (lane == 0) {
+        good = slot_free();
+        if (good) {
+          Item it{};
+          it.e.n = what;
+          publish(it);
+        }
+      }
+      ++ii;
+      return __shfl_sync(0xffffffffu, good, 0);
+    };
+    // loads one item's Q and K blocks
+    auto run_item = [&](int32_t id, int32_t pos, int32_t careful) -> bool {
+      int32_t hg, x;
+      Entry e;
+      if (p.direct) {
+        hg = id % p.head_groups;
+        x = id / p.head_groups;
+        if (!find_tile(p, x, lane, &e)) return true;
+      } else {
+        if (by_head) {
+          hg = id / entries;
+          x = id - hg * entries;
+        } else {
+          x = id / p.head_groups;
+          hg = id - x * p.head_groups;
+        }
+        const int4* at = reinterpret_cast<const int4*>(&p.entries[x]);
+        const int4 lo = __ldcg(at), hi = __ldcg(at + 1);
+        e = Entry{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      }
+      const int32_t head0 = hg * p.tile_heads, g = head0 / p.group;
+      bool good = true;
+      if (lane == 0) {
+        good = slot_free();
+        if (good) {
+          Item it;
+          it.e = e;
+          it.head0 = head0;
+          it.g = g;
+          it.hg = hg;
+          it.mt = max(0, (e.lim0 + 1) / kBK - e.b0);
+          it.pos = pos;
+          it.careful = careful;
+          publish(it);
+          const uint32_t qs = qi % C::kNQ;
+          if (qi >= uint32_t(C::kNQ) &&
+              !mbar_wait(&sh->q_empty[qs], ((qi / C::kNQ) - 1) & 1, abort, p.wait_ns))
+            good = false;
+          if (good) {
+            // the box is tile_heads x tile_tokens rows; what it covers behind
+            // the tensor counts as loaded (zeros)
+            mbar_arrive_expect_tx(&sh->q_full[qs],
+                                  uint32_t(C::kPanels * 128 * p.tile_heads * p.tile_tokens));
+#pragma unroll
+            for (int s = 0; s < C::kPanels; ++s)
+              tma_load_3d(sQ + qs * C::kQBytes + s * C::kQPanel, &tq, &sh->q_full[qs], s * 64,
+                          head0, e.q0, pol_q);
+            ++qi;
+          }
+        }
+        if (good) {
+          const int32_t blocks = careful ? 2 * e.n : e.n;
+          for (int32_t t = 0; t < blocks; ++t) {
+            const int32_t j = e.b0 + (t >= e.n ? t - e.n : t);
+            const uint32_t ks = kiss % C::kNK;
+            if (kiss >= uint32_t(C::kNK) &&
+                !mbar_wait(&sh->k_empty[ks], ((kiss / C::kNK) - 1) & 1, abort, p.wait_ns)) {
+              good = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&sh->k_full[ks], C::kKVBytes);
+#pragma unroll
+            for (int s = 0; s < C::kPanels; ++s)
+              tma_load_3d(sK + ks * C::kKVBytes + s * C::kKVPanel, &tk, &sh->k_full[ks], s * 64,
+                          g, e.kbeg + j * kBK, pol_kv);
+            ++kiss;
+          }
+        }
+      }
+      ++ii;
+      return __shfl_sync(0xffffffffu, good, 0);
+    };
+
+    int64_t id = blockIdx.x;
+    uint32_t batches = 0;
+    while (ok && id < items) {
+      // a batch of items, then those of them that are to be done again
+      int32_t pos = 0;
+      for (; pos < kBatch && id < items; ++pos) {
+        int32_t next = 0;
+        if (lane == 0) {
+          if (!p.direct) next = atomicAdd(p.counter, 1);
+          sh->ids[pos] = int32_t(id);
+        }
+        ok = run_item(int32_t(id), pos, 0);
+        if (!ok) break;
+        id = p.direct ? items : int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
+      }
+      if (ok) ok = special(kMarker);
+      if (ok) ok = warp_wait(&sh->batch_done, batches & 1, abort, p.wait_ns);
+      ++batches;
+      for (int32_t w = 0; ok && w < (pos + 31) / 32; ++w) {
+        uint32_t bits = *(volatile uint32_t*)&sh->redo[w];
+        __syncwarp();
+        if (lane == 0) sh->redo[w] = 0;
+        while (ok && bits) {
+          const int32_t at = 32 * w + __ffs(bits) - 1;
+          bits &= bits - 1;
+          ok = run_item(*(volatile int32_t*)&sh->ids[at], at, 1);
+        }
+      }
+    }
+    if (ok) ok = special(kEnd);
+    if (lane == 0) {
+      if (!ok) raise_abort(sh, p);
+      // copies still in flight must land before this CTA's shared memory goes
+      drain_ring(sh->q_full, qi, C::kNQ);
+      drain_ring(sh->k_full, kiss, C::kNK);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------- producer: V
+    const uint64_t pol_kv = l2_policy_evict_last();
+    uint32_t ii = 0, viss = 0;
+    bool ok = true;
+    for (;; ++ii) {
+      const int slot = ii % kNI;
+      if (!warp_wait(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const int32_t n = sh->info[slot].e.n, g = sh->info[slot].g;
+      const int32_t row0 = sh->info[slot].e.kbeg + sh->info[slot].e.b0 * kBK;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+      if (n == kEnd) break;
+      if (lane == 0) {
+        for (int32_t t = 0; t < n; ++t) {
+          const uint32_t vs = viss % C::kNV;
+          if (viss >= uint32_t(C::kNV) &&
+              !mbar_wait(&sh->v_empty[vs], ((viss / C::kNV) - 1) & 1, abort, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&sh->v_full[vs], C::kKVBytes);
+#pragma unroll
+          for (int s = 0; s < C::kPanels; ++s)
+            tma_load_3d(sV + vs * C::kKVBytes + s * C::kKVPanel, &tv, &sh->v_full[vs], s * 64, g,
+                        row0 + t * kBK, pol_kv);
+          ++viss;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      if (!ok) raise_abort(sh, p);
+      drain_ring(sh->v_full, viss, C::kNV);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------- Q K^T issuer
+    constexpr uint32_t idesc_qk = idesc_bf16(kRows, kBK, 0, 0);
+    uint32_t ii = 0, qi = 0, stage = 0, phase = 0, kb = 0, kst = 0, kph = 0;
+    bool ok = true;
+    for (;; ++ii) {
+      const int slot = ii % kNI;
+      if (!warp_wait(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const int32_t n = sh->info[slot].e.n, careful = sh->info[slot].careful;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+      if (n == kEnd) break;
+      if (n == kMarker) continue;
+      const int32_t blocks = careful ? 2 * n : n;
+      const uint32_t qs = qi % C::kNQ;
+      if (!warp_wait(&sh->q_full[qs], (qi / C::kNQ) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ + qs * C::kQBytes), 16, 1024);
+      for (int32_t t = 0; t < blocks; ++t) {
+        // lane 0: K of this block; lane 1: P V of three blocks ago (same S buffer)
+        const bool reuse = kb >= 3;
+        uint64_t* bar = &sh->k_full[kst];
+        uint32_t par = kph;
+        if (lane == 1 && reuse) {
+          bar = &sh->pv_done[stage];
+          par = phase ^ 1u;
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, mbar_test(bar, par));
+        if (!(have & 1u) && !warp_wait(&sh->k_full[kst], kph, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        if (reuse && !(have & 2u) &&
+            !warp_wait(&sh->pv_done[stage], phase ^ 1u, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t kdesc = smem_desc_sw128(smem_u32(sK + kst * C::kKVBytes), 16, 1024);
+        const uint32_t s_tmem = tmem + stage * kBK;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qoff = (kk / 4) * C::kQPanel + (kk % 4) * 32;
+            const uint32_t koff = (kk / 4) * C::kKVPanel + (kk % 4) * 32;
+            mma_ss(s_tmem, qdesc + uint64_t(qoff >> 4), kdesc + uint64_t(koff >> 4), idesc_qk,
+                   kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&sh->s_full[stage]);
+          mma_commit(&sh->k_empty[kst]);
+          if (t == blocks - 1) mma_commit(&sh->q_empty[qs]);
+        }
+        __syncwarp();
+        ++kb;
+        if (++stage == 3) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++kst == C::kNK) {
+          kst = 0;
+          kph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      ++qi;
+    }
+    if (lane == 0) {
+      if (!ok) raise_abort(sh, p);
+      mma_commit(&sh->drain_qk);   // complete before the tensor memory is freed
+      mbar_wait(&sh->drain_qk, 0, nullptr);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------- P V issuer
+    constexpr uint32_t idesc_pv = idesc_bf16(kRows, D, 0, 1);   // P (TMEM), V MN-major
+    uint32_t ii = 0, qi = 0, stage = 0, phase = 0, vstage = 0, vphase = 0;
+    bool ok = true;
+    // This warp also writes the staged output tiles, one TMA store per panel,
+    // and releases their Q stages, while it would wait for P.  Item x is staged
+    // after the first block of item x+1, so it is stored before block 1 of item
+    // x+1 (or the first block of item x+2).  Item x+1 may be staged before this
+    // warp has looked at item x, item x+2 not: two barriers in turn.
+    uint32_t spq = 0;
+    auto store_upto = [&](uint32_t upto) -> bool {
+      for (; spq < upto; ++spq) {
+        if (!warp_wait(&sh->stage_bar[spq & 1], (spq >> 1) & 1, abort, p.wait_ns)) return false;
+        if (lane == 0) {
+          const int32_t q0 = sh->stage_q0[spq & 1], h0 = sh->stage_h[spq & 1];
+          if (q0 >= 0) {
+            const uint8_t* stg = sQ + (spq % C::kNQ) * C::kQBytes;
+            const uint64_t pol = l2_policy_evict_first();
+#pragma unroll
+            for (int s = 0; s < C::kPanels; ++s)
+              tma_store_3d_hint(&to, stg + s * C::kQPanel, s * 64, h0, q0, pol);
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+          mbar_arrive(&sh->q_empty[spq % C::kNQ]);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    for (;; ++ii) {
+      const int slot = ii % kNI;
+      if (!warp_wait(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const int32_t n = sh->info[slot].e.n;
+      const int32_t lead = sh->info[slot].careful ? n : 0;   // blocks without P V
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+      if (n == kEnd) break;
+      if (n == kMarker) {
+        // every tile before it is stored, and complete before a careful item
+        // may write its rows again
+        ok = store_upto(qi);
+        if (!ok) break;
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+        continue;
+      }
+      for (int32_t t = 0; t < lead + n; ++t) {
+        if (!store_upto(t == 0 ? (qi > 0 ? qi - 1 : 0) : qi)) {
+          ok = false;
+          break;
+        }
+        const bool skip = t < lead, first = t == lead;
+        const bool need_o = first && qi > 0;   // the previous epilogue has read O
+        // lane 0: P, lane 1: V, lane 2: O
+        uint64_t* bar = &sh->p_full[stage];
+        uint32_t par = phase;
+        if (lane == 1 && !skip) {
+          bar = &sh->v_full[vstage];
+          par = vphase;
+        }
+        if (lane == 2 && need_o) {
+          bar = &sh->o_free;
+          par = (qi - 1) & 1;
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, mbar_test(bar, par));
+        if (!(have & 1u) && !warp_wait(&sh->p_full[stage], phase, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        if (!skip && !(have & 2u) && !warp_wait(&sh->v_full[vstage], vphase, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        if (need_o && !(have & 4u) && !warp_wait(&sh->o_free, (qi - 1) & 1, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (skip) {
+          if (elect_one()) mma_commit(&sh->pv_done[stage]);
+        } else {
+          const uint64_t vdesc =
+              smem_desc_sw128(smem_u32(sV + vstage * C::kKVBytes), C::kKVPanel, 1024);
+          const uint32_t s_col = tmem + stage * kBK;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              // keys [16kk, 16kk+16) belong to group 16kk / kCols, whose P starts
+              // at that group's first S column
+              const int grp = (kk * 16) / C::kCols;
+              const uint32_t a_col = s_col + grp * C::kCols + (kk * 16 - grp * C::kCols) / 2;
+              mma_ts(tmem + C::kO, a_col, vdesc + uint64_t((kk * 16 * 128) >> 4), idesc_pv,
+                     (first && kk == 0) ? 0u : 1u);
+            }
+            mma_commit(&sh->v_empty[vstage]);
+            mma_commit(&sh->pv_done[stage]);
+            if (t == lead + n - 1) mma_commit(&sh->o_last);
+          }
+          if (++vstage == C::kNV) {
+            vstage = 0;
+            vphase ^= 1u;
+          }
+        }
+        __syncwarp();
+        if (++stage == 3) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      ++qi;
+    }
+    if (ok) ok = store_upto(qi);
+    if (lane == 0) {
+      if (!ok) raise_abort(sh, p);
+      bulk_wait_all();   // the stores read this CTA's shared memory
+      mma_commit(&sh->drain_pv);
+      mbar_wait(&sh->drain_pv, 0, nullptr);
+    }
+  } else {
+    // ------------------------------------------------- softmax groups
+    const int grp = (warp - 4) >> 2;              // column group 0..3
+    const int quarter = warp & 3;                 // TMEM lane quarter of this warp
+    const int row = quarter * 32 + lane;
+    const int tok = row / p.tile_heads;           // token and head of this row's query
+    const int head = row - tok * p.tile_heads;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const float c = p.scale_log2;
+    uint32_t ii = 0, qi = 0, xn = 0, parts = 0;   // xn: uses of the exchange buffer
+    uint32_t sst = 0, sph = 0, vb = 0;            // S ring; V blocks
+    bool ok = true;
+
+    // The largest of this thread's scores.
+    auto row_max = [&](const float (&s)[C::kCols]) {
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int x = 4; x + 8 <= C::kCols; x += 8)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) mx[a] = max3(mx[a], s[x + a], s[x + 4 + a]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) mx[a] = fmaxf(mx[a], s[C::kCols - 4 + a]);
+      return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+    };
+    // The row's maximum from the groups' ones.  Use xn writes buffer xn & 1:
+    // every thread read use xn-2 before it posted use xn-1, which this thread
+    // saw complete.
+    auto exchange_max = [&](float mx, float* out) -> bool {
+      float* xb = &sh->xch[xn & 1][0][0];
+      xb[grp * 128 + row] = mx;
+      mbar_arrive(&sh->xch_bar);
+      if (!wait_all(&sh->xch_bar, xn & 1, abort, p.wait_ns)) return false;
+      *out = max3(fmaxf(xb[row], xb[128 + row]), xb[256 + row], xb[384 + row]);
+      ++xn;
+      return true;
+    };
+    auto load_s = [&](float (&s)[C::kCols]) {
+      uint32_t sr[32];
+      static_assert(C::kCols == 32, "group width");
+      tmem_ld32(lanes + sst * kBK + grp * C::kCols, sr);
+      tmem_ld_wait(sr);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(sr[x]);
+    };
+    auto next_s = [&]() {
+      if (++sst == uint32_t(C::kNS)) {
+        sst = 0;
+        sph ^= 1u;
+      }
+    };
+    // Infinities and NaN of V blocks that the mask cuts become 0 in shared
+    // memory (this thread's share of the stage); the item is marked.
+    auto clean_v = [&](uint32_t item) {
+      uint8_t* stage = sV + (vb % C::kNV) * C::kKVBytes;
+      const int x = (warp - 4) * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < C::kKVBytes / 16 / kSoftmaxThreads; ++i) {
+        uint4* at = reinterpret_cast<uint4*>(stage) + x + i * kSoftmaxThreads;
+        uint4 w = *at;
+        uint32_t b0 = not_finite(w.x), b1 = not_finite(w.y), b2 = not_finite(w.z),
+                 b3 = not_finite(w.w);
+        if (b0 | b1 | b2 | b3) {
+          // 0x8000 in each bad half -> 0xffff
+          auto wipe = [](uint32_t v, uint32_t b) { return v & ~((b >> 15) * 0xffffu); };
+          *at = make_uint4(wipe(w.x, b0), wipe(w.y, b1), wipe(w.z, b2), wipe(w.w, b3));
+          *(volatile int32_t*)&sh->bad_v[item & 1] = int32_t(item + 1);
+          fence_proxy_async_smem();
+        }
+      }
+    };
+
+    // An item's epilogue runs after the next item's first block: by then its
+    // last P V has finished, and that item's first P V waits for the release of
+    // O as before.  Its description stays in the ring until then.
+    bool pend = false;
+    uint32_t pslot = 0, pq = 0;
+    float pl = 0.f, plx = 0.f, pm = 0.f;
+    auto epilogue = [&]() -> bool {
+      float* xb = &sh->xch[xn & 1][0][0];
+      float* xl = &sh->xch_l[xn & 1][0][0];
+      xb[grp * 128 + row] = pl;
+      if (kLse) xl[grp * 128 + row] = plx;
+      mbar_arrive(&sh->xch_bar);
+      if (!wait_all(&sh->o_last, pq & 1, abort, p.wait_ns)) return false;
+      tc_fence_after();
+      uint32_t r[C::kOCols];
+      if constexpr (C::kOCols == 32) {
+        tmem_ld32(lanes + C::kO + grp * C::kOCols, r);
+      } else {
+        tmem_ld16(lanes + C::kO + grp * C::kOCols, r);
+      }
+      tmem_ld_wait(r);
+      tc_fence_before();
+      mbar_arrive(&sh->o_free);
+      if (!wait_all(&sh->xch_bar, xn & 1, abort, p.wait_ns)) return false;
+      ++xn;
+      const Item& it = sh->info[pslot];
+      float l = (xb[row] + xb[128 + row]) + (xb[256 + row] + xb[384 + row]);
+      float lx = kLse ? (xl[row] + xl[128 + row]) + (xl[256 + row] + xl[384 + row]) : 0.f;
+      const int32_t lim = it.e.lim0 + tok;
+      const bool live = tok < it.e.ntok;                     // a query of the tile
+      const bool some = lim >= it.e.b0 * kBK;                // that sees a key of the range
+      const int col = grp * C::kOCols;
+      if (live && some && *(volatile int32_t*)&sh->bad_v[pq & 1] == int32_t(pq + 1)) {
+        // what clean_v took out of the values that this row sees
+        const __nv_bfloat16* v = p.v + it.g * p.v_sh + col;
+        const int32_t end = min(lim + 1, (it.e.b0 + it.e.n) * kBK);
+        for (int32_t u = (it.e.b0 + it.mt) * kBK; u < end; ++u) {
+          const __nv_bfloat16* vr = v + (int64_t(it.e.kbeg) + u) * p.v_st;
+#pragma unroll
+          for (int x = 0; x < C::kOCols; ++x) {
+            const float y = __bfloat162float(vr[x]);
+            if (!(fabsf(y) <= 3.4e38f)) r[x] = __float_as_uint(__uint_as_float(r[x]) + y);
+          }
+        }
+      }
+      // the range that the first pass keeps: the sum up to 2^126 (so that no
+      // weight overflowed) and O finite
+      float osum = 0.f;
+#pragma unroll
+      for (int x = 0; x < C::kOCols; ++x) osum += __uint_as_float(r[x]);
+      const bool keep = it.careful || !live || !some || (l <= 0x1p126f && fabsf(osum) <= 3.0e38f);
+      if (!keep) atomicOr(&sh->redo[it.pos >> 5], 1u << (it.pos & 31));
+      float m = pm;
+      if (!some) {
+        l = 1.f;
+        lx = 0.f;
+        m = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < C::kOCols; ++x) r[x] = 0u;
+      }
+      bool out = live;                                       // this row's result is in r, l, lx, m
+      if (it.e.split >= 0) {
+        // a range: its state goes to the workspace; the tile's last range joins
+        const int32_t ranges = it.e.part >> 16;
+        const int64_t slot0 = int64_t(it.e.split) * p.head_groups + it.hg;
+        const int64_t slot = slot0 + int64_t(it.e.part & 0xffff) * p.head_groups;
+        if (live) {
+          float4* po = reinterpret_cast<float4*>(p.part_o + (slot * kRows + row) * D + col);
+#pragma unroll
+          for (int x = 0; x < C::kOCols / 4; ++x)
+            po[x] = make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                                __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
+          if (grp == 0) p.part_ml[slot * kRows + row] = make_float4(m, some ? l : 0.f, lx, 0.f);
+        }
+        __threadfence();
+        mbar_arrive(&sh->part_bar);
+        if (warp == 4) {
+          if (!warp_wait(&sh->part_bar, parts & 1, abort, p.wait_ns)) return false;
+          if (lane == 0) {
+            const bool again =
+                (*(volatile uint32_t*)&sh->redo[it.pos >> 5] >> (it.pos & 31)) & 1u;
+            bool last = false;
+            if (!again) {
+              __threadfence();
+              last = atomicAdd(&p.tickets[slot0], 1) == ranges - 1;
+              __threadfence();
+            }
+            *(volatile int32_t*)&sh->last = last;
+            mbar_arrive(&sh->tick_bar);
+          }
+          __syncwarp();
+        }
+        if (!wait_all(&sh->tick_bar, parts & 1, abort, p.wait_ns)) return false;
+        ++parts;
+        out = live && *(volatile int32_t*)&sh->last;
+        if (out) {
+          __threadfence();
+          // a range's weight is 2^(m + log2 l); its output is divided by its own
+          // sum first, as that may be as large as fp32 goes
+          auto state = [&](int32_t i) {
+            return __ldcg(&p.part_ml[(slot0 + int64_t(i) * p.head_groups) * kRows + row]);
+          };
+          m = -INFINITY;
+          for (int32_t i = 0; i < ranges; ++i) {
+            const float4 ml = state(i);
+            if (ml.y != 0.f) m = fmaxf(m, ml.x + log2f(ml.y));
+          }
+          l = lx = 0.f;
+          float acc[C::kOCols];
+#pragma unroll
+          for (int x = 0; x < C::kOCols; ++x) acc[x] = 0.f;
+          for (int32_t i = 0; i < ranges; ++i) {
+            const float4 ml = state(i);
+            if (ml.y == 0.f) continue;               // sees no key of this range
+            const float w = ex2(ml.x + log2f(ml.y) - m), own = 1.f / ml.y;
+            l += w;
+            lx = fmaf(w, ml.z * own, lx);
+            const float4* po = reinterpret_cast<const float4*>(
+                p.part_o + ((slot0 + int64_t(i) * p.head_groups) * kRows + row) * D + col);
+#pragma unroll
+            for (int x = 0; x < C::kOCols / 4; ++x) {
+              const float4 y = __ldcg(&po[x]);
+              acc[4 * x] = fmaf(w, y.x * own, acc[4 * x]);
+              acc[4 * x + 1] = fmaf(w, y.y * own, acc[4 * x + 1]);
+              acc[4 * x + 2] = fmaf(w, y.z * own, acc[4 * x + 2]);
+              acc[4 * x + 3] = fmaf(w, y.w * own, acc[4 * x + 3]);
+            }
+          }
+          if (l == 0.f) l = 1.f;                     // sees no key at all: 0
+#pragma unroll
+          for (int x = 0; x < C::kOCols; ++x) r[x] = __float_as_uint(acc[x]);
+        }
+      }
+      if (kLse && out && grp == 0)
+        p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
+            m == -INFINITY ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
+      // A full tile is staged in its Q stage (128-byte swizzled, as TMA stores
+      // read it); rows of other tiles go out as they are
+      const float inv = 1.f / l;
+      const bool staged = it.e.split < 0 && it.e.ntok == p.tile_tokens;
+      if (out) {
+        uint4* direct = reinterpret_cast<uint4*>(
+            p.o + (int64_t(it.e.q0) + tok) * p.o_st + int64_t(it.head0 + head) * p.o_sh + col);
+        uint8_t* stg = sQ + (pq % C::kNQ) * C::kQBytes + row * 128;
+#pragma unroll
+        for (int x = 0; x < C::kOCols / 8; ++x) {
+          uint32_t ob[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            ob[y] = pack_bf16x2(__uint_as_float(r[8 * x + 2 * y]) * inv,
+                                __uint_as_float(r[8 * x + 2 * y + 1]) * inv);
+          const int c16 = (col + 8 * x) / 8, panel = c16 / 8, chunk = c16 % 8;
+          uint4* dst = staged ? reinterpret_cast<uint4*>(stg + panel * C::kQPanel +
+                                                         ((chunk ^ (row & 7)) << 4))
+                              : direct + x;
+          *dst = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+      }
+      if (staged) fence_proxy_async_smem();
+      if (warp == 4 && lane == 0) {
+        sh->stage_q0[pq & 1] = staged ? it.e.q0 : -1;
+        sh->stage_h[pq & 1] = it.head0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[pslot]);
+      mbar_arrive(&sh->stage_bar[pq & 1]);   // the P V issuer goes on from here
+      return true;
+    };
+
+    for (;; ++ii) {
+      const uint32_t slot = ii % kNI;
+      if (!wait_all(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const int32_t n = sh->info[slot].e.n;
+      if (n <= 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+        if (n == kEnd) break;
+        if (pend && !epilogue()) {
+          ok = false;
+          break;
+        }
+        pend = false;
+        mbar_arrive(&sh->batch_done);
+        continue;
+      }
+      const int32_t mt = sh->info[slot].mt;
+      // last visible column of this thread's quarter of the first block
+      int32_t vis0 = sh->info[slot].e.lim0 + tok - sh->info[slot].e.b0 * kBK - grp * C::kCols;
+      const bool careful = sh->info[slot].careful != 0;
+      float m_used = -INFINITY;
+      if (careful) {
+        // the rows' maxima over all blocks, without P V
+        if (pend && !epilogue()) {
+          ok = false;
+          break;
+        }
+        pend = false;
+        float mx = -INFINITY;
+        for (int32_t t = 0; t < n; ++t) {
+          if (!wait_all(&sh->s_full[sst], sph, abort, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float s[C::kCols];
+          load_s(s);
+#pragma unroll
+          for (int x = 0; x < C::kCols; ++x)
+            if (t >= mt && x > vis0 - t * kBK) s[x] = -INFINITY;
+          mx = fmaxf(mx, row_max(s));
+          tc_fence_before();
+          mbar_arrive(&sh->p_full[sst]);
+          next_s();
+        }
+        if (!ok) break;
+        if (!exchange_max(mx, &m_used)) {
+          ok = false;
+          break;
+        }
+        m_used *= c;
+      }
+      // the normaliser in partial sums: of rounded weights, and of unrounded ones
+      float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+      float x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+      for (int32_t t = 0; t < n; ++t) {
+        if (!wait_all(&sh->s_full[sst], sph, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[C::kCols];
+        load_s(s);
+        if (t >= mt) {
+          const int32_t vis = vis0 - t * kBK;
+#pragma unroll
+          for (int x = 0; x < C::kCols; ++x)
+            if (x > vis) s[x] = -INFINITY;
+          if (!wait_all(&sh->v_full[vb % C::kNV], (vb / C::kNV) & 1, abort, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          clean_v(qi);
+        }
+        ++vb;
+        if (t == 0 && !careful) {
+          if (!exchange_max(row_max(s), &m_used)) {
+            ok = false;
+            break;
+          }
+          m_used *= c;
+        }
+        {
+          uint32_t pk[C::kCols / 2];
+          const float nm = -m_used;
+#pragma unroll
+          for (int x = 0; x < C::kCols / 2; ++x) {
+            float a0, a1;
+            fma2(a0, a1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+            pk[x] = pack_bf16x2(a0, a1);
+            if (x & 1) {
+              add_bf16x2(sum2, sum3, pk[x]);
+              if (kLse) add2(x2, x3, a0, a1);
+            } else {
+              add_bf16x2(sum0, sum1, pk[x]);
+              if (kLse) add2(x0, x1, a0, a1);
+            }
+          }
+          tmem_st16(lanes + sst * kBK + grp * C::kCols, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sh->p_full[sst]);
+        next_s();
+        if (t == 0 && pend) {
+          if (!epilogue()) {
+            ok = false;
+            break;
+          }
+          pend = false;
+        }
+      }
+      if (!ok) break;
+      pend = true;
+      pslot = slot;
+      pl = (sum0 + sum1) + (sum2 + sum3);
+      plx = (x0 + x1) + (x2 + x3);
+      pm = m_used;
+      pq = qi;
+      ++qi;
+    }
+    if (ok && pend) ok = epilogue();
+    if (!ok) raise_abort(sh, p);
+    // a role that gave up may have left a tensor-memory access in flight
+    tmem_ld_wait();
+    tmem_st_wait();
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn fn = known.load(std::memory_order_relaxed);
+  if (fn) return fn;
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                       &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess) {
+    fn = reinterpret_cast<EncodeFn>(ptr);
+    known.store(fn, std::memory_order_relaxed);
+  }
+  return fn;
+}
+
+// [tokens, heads, d] bf16 view, boxes of 64 columns x box_heads x box_tokens,
+// 128-byte swizzle.  The stride of an extent of one is not used.
+bool make_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t heads, int d, int64_t st,
+              int64_t shd, int box_heads, int box_tokens) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? shd : d) * 2,
+                                 cuuint64_t(tokens > 1 ? st : d) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Partial slots: cut tiles' ranges x head groups (at most two a processor).
+int64_t slots_of(int sms) { return 2 * int64_t(sms); }
+
+struct Layout {
+  size_t header, seqs, tile0, entries, tickets, part_ml, part_o, end;
+  int64_t max_entries;
+};
+
+Layout layout_of(const sa_packed_shape& s, int sms) {
+  Layout l;
+  l.max_entries = sa_packed::most_tiles(s) + slots_of(sms);
+  l.header = 0;
+  l.tickets = up(sizeof(Header));
+  l.seqs = l.tickets + up(size_t(slots_of(sms)) * 4);
+  l.tile0 = l.seqs + up(size_t(s.batch) * 16);
+  l.entries = l.tile0 + up(size_t(s.batch) * 4);
+  l.part_ml = l.entries + up(size_t(l.max_entries) * sizeof(Entry));
+  l.part_o = l.part_ml + up(size_t(slots_of(sms)) * kRows * 16);
+  l.end = l.part_o + up(size_t(slots_of(sms)) * kRows * size_t(s.head_dim) * 4);
+  return l;
+}
+
+template <int D, bool kLse>
+cudaError_t launch_attention(const Args& a, const Params& p, unsigned grid, const CUtensorMap& tq,
+                             const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                             cudaStream_t st) {
+  using C = Cfg<D>;
+  constexpr int kSmem = C::kData + int(sizeof(Shared));
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static std::atomic<uint64_t> done{0};
+  auto kern = packed_attention_kernel<D, kLse>;
+  cudaError_t e = sa_paged::allow_shared(kern, kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, to, p);
+}
+
+template <int D>
+cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_failed) {
+  const sa_packed_shape& s = a.s;
+  const sa_packed::Tile tile = sa_packed::tile_of(s);
+  const Layout lay = layout_of(s, sms);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  const int64_t head_groups = s.num_q_heads / tile.heads;
+  const int64_t tiles = sa_packed::most_tiles(s);
+  const int64_t key_blocks = (int64_t(s.total_k) + kBK - 1) / kBK;
+
+  // no keys at all: the map only has to be valid, every score is masked
+  const bool none = s.total_k == 0;
+  CUtensorMap tq, tk, tv, to;
+  if (!make_map(&tq, a.q, s.total_q, s.num_q_heads, D, s.q_stride_t, s.q_stride_h, tile.heads,
+                tile.tokens) ||
+      !make_map(&tk, none ? a.q : a.k, none ? 1 : s.total_k, none ? 1 : s.num_kv_heads, D,
+                s.k_stride_t, s.k_stride_h, 1, kBK) ||
+      !make_map(&tv, none ? a.q : a.v, none ? 1 : s.total_k, none ? 1 : s.num_kv_heads, D,
+                s.v_stride_t, s.v_stride_h, 1, kBK) ||
+      !make_map(&to, a.o, s.total_q, s.num_q_heads, D, s.o_stride_t, s.o_stride_h, tile.heads,
+                tile.tokens)) {
+    *encode_failed = true;
+    return cudaErrorInvalidValue;
+  }
+  Params p;
+  p.cu_q = a.cu_q;
+  p.cu_k = a.cu_k;
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.header = reinterpret_cast<const Header*>(ws + lay.header);
+  p.counter = &reinterpret_cast<Header*>(ws + lay.header)->counter;
+  p.entries = reinterpret_cast<const Entry*>(ws + lay.entries);
+  p.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets);
+  p.part_ml = reinterpret_cast<float4*>(ws + lay.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+  p.v_st = s.v_stride_t;
+  p.v_sh = s.num_kv_heads > 1 ? s.v_stride_h : 0;
+  p.o_st = s.o_stride_t;
+  p.o_sh = s.num_q_heads > 1 ? s.o_stride_h : 0;
+  p.total_q = s.total_q;
+  p.total_k = s.total_k;
+  p.batch = s.batch;
+  p.Hq = s.num_q_heads;
+  p.group = s.num_q_heads / s.num_kv_heads;
+  p.tile_heads = tile.heads;
+  p.tile_tokens = tile.tokens;
+  p.head_groups = int32_t(head_groups);
+  // every tile its own CTA, and no tile would be cut
+  p.direct = tiles * head_groups <= sms && key_blocks <= kMinRange;
+  p.scale_log2 = float(double(s.scale) * 1.4426950408889634);
+  p.dev_status = a.dev_status;
+  p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
+  unsigned grid = unsigned(sms);
+  if (p.direct) {
+    grid = unsigned(tiles * head_groups);
+  } else {
+    ScheduleParams sp;
+    sp.cu_q = a.cu_q;
+    sp.cu_k = a.cu_k;
+    sp.header = reinterpret_cast<Header*>(ws + lay.header);
+    sp.seqs = reinterpret_cast<int4*>(ws + lay.seqs);
+    sp.tile0 = reinterpret_cast<int32_t*>(ws + lay.tile0);
+    sp.entries = reinterpret_cast<Entry*>(ws + lay.entries);
+    sp.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets);
+    sp.total_q = s.total_q;
+    sp.total_k = s.total_k;
+    sp.batch = s.batch;
+    sp.tile_tokens = tile.tokens;
+    sp.head_groups = int32_t(head_groups);
+    sp.workers = sms;
+    sp.bin_shift = 0;
+    while ((key_blocks >> sp.bin_shift) >= kBins) ++sp.bin_shift;
+    // keys and values of all heads against half of L2
+    sp.by_head = int64_t(s.total_k) * s.num_kv_heads * D * 4 > (int64_t(64) << 20);
+    sp.max_slots = int32_t(slots_of(sms));
+    sp.max_entries = int32_t(lay.max_entries);
+    sp.dev_status = a.dev_status;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kScheduleThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, schedule_kernel, sp);
+    if (e != cudaSuccess) return e;
+  }
+  return a.lse ? launch_attention<D, true>(a, p, grid, tq, tk, tv, to, st)
+               : launch_attention<D, false>(a, p, grid, tq, tk, tv, to, st);
+}
+
+}  // namespace
+
+namespace sa_packed {
+
+size_t workspace(const sa_packed_shape& s, int sms) { return layout_of(s, sms).end; }
+
+cudaError_t launch(const Args& a, int sms, cudaStream_t st, bool* encode_failed) {
+  return a.s.head_dim == 128 ? launch_d<128>(a, sms, st, encode_failed)
+                             : launch_d<64>(a, sms, st, encode_failed);
+}
+
+}  // namespace sa_packed

@@ -56,6 +56,9 @@ struct EvictArgs {
 size_t evict_workspace(const sa_paged_cache& c);
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st);
 
+// Processors of the current device, asked for once.
+sa_status sm_count(int* sms);
+
 // Lets `kern` use `bytes` of dynamic shared memory on the current device: once
 // a device, which bit mask `done` (of that kernel) keeps.
 template <class Kernel>

@@ -63,12 +63,18 @@ sa_status check_evict(const sa_paged_cache* c) {
   return SA_OK;
 }
 
-// Processors of the current device, asked for once.
+using sa_k::cuda_status;
+using sa_paged::sm_count;
+
+}  // namespace
+
+namespace sa_paged {
+
 sa_status sm_count(int* sms) {
-  static std::atomic<int> known[sa_paged::kMaxDevices];
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
-  const bool kept = dev < sa_paged::kMaxDevices;
+  const bool kept = dev < kMaxDevices;
   *sms = kept ? known[dev].load(std::memory_order_relaxed) : 0;
   if (*sms > 0) return SA_OK;
   if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -77,9 +83,7 @@ sa_status sm_count(int* sms) {
   return SA_OK;
 }
 
-using sa_k::cuda_status;
-
-}  // namespace
+}  // namespace sa_paged
 
 extern "C" {
 

@@ -90,10 +90,11 @@ enum {
   SA_DEV_BAD_ITEM = 8,       /* a schedule entry outside the item range      */
   SA_DEV_BAD_LAUNCH = 16,    /* the kernel found its shared memory misaligned
                                 and did nothing; outputs are not written     */
-  SA_DEV_RANGE = 32          /* rows beyond the tensor-core pass's range
+  SA_DEV_RANGE = 32,         /* rows beyond the tensor-core pass's range
                                 (a row sum above 2^126 or O overflowed) could
                                 not all be recomputed exactly: a worker list
                                 longer than 32768 items; outputs invalid     */
+  SA_DEV_NO_PAGES = 64       /* the pool had too few pages for a sequence    */
 };
 
 typedef struct sa_shape {
@@ -660,6 +661,64 @@ sa_status sparse_attn_paged_evict(const sa_paged_cache* cache, const int32_t* ke
                                   int32_t recent, int32_t* lens_out, float* weights_out,
                                   int32_t* positions_out, void* ws, size_t ws_bytes,
                                   int32_t* dev_status, sa_stream_t stream);
+
+/*
+ * Dense causal attention of packed sequences.  Sequence s has the queries
+ * cu_q[s] .. cu_q[s+1] and the keys cu_k[s] .. cu_k[s+1] of the packed tensors;
+ * its queries are its last tokens, so with n queries and m keys query i sees
+ * the keys u <= i + m - n (a chunk of a prompt has m > n).  For query head h of
+ * KV head g = h / (Hq/Hkv):
+ *   o[t,h] = sum_u p_u v[u,g],  p_u = exp(scale q[t,h] . k[u,g] - lse[t,h]).
+ * A query that sees no key (n > m) gives o = 0 and lse = -infinity.  Values of
+ * keys that a query does not see never reach it, infinities and NaN included.
+ * Rows of q, o and lse in no sequence are not used and not written.
+ */
+typedef struct sa_packed_shape {
+  int64_t q_stride_t;      /* element (t, h, x) of q at t*q_stride_t +        */
+  int64_t q_stride_h;      /*   h*q_stride_h + x, and so on: multiples of 8,  */
+  int64_t k_stride_t;      /*   at least head_dim, below 2^38; the stride of  */
+  int64_t k_stride_h;      /*   an extent of one is not used.  A fused        */
+  int64_t v_stride_t;      /*   projection's views and the prefill layout     */
+  int64_t v_stride_h;      /*   [H][S][d] are all of this form                */
+  int64_t o_stride_t;
+  int64_t o_stride_h;
+  int32_t total_q;         /* tokens of q and o, 0 .. 2^30                    */
+  int32_t total_k;         /* tokens of k and v, 0 .. 2^30                    */
+  int32_t batch;           /* sequences, 1 .. 2^20                            */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;    /* divides num_q_heads                             */
+  int32_t head_dim;        /* 64 or 128                                       */
+  float scale;             /* of the scores: positive and finite              */
+} sa_packed_shape;
+
+/*
+ * Workspace bytes of sparse_attn_packed_forward.  Host only, except that it
+ * asks the current device for its number of processors.  A larger total_q and
+ * batch never need less, so one workspace can serve the largest of many calls.
+ */
+sa_status sparse_attn_packed_workspace_size(const sa_packed_shape* shp, size_t* bytes);
+
+/*
+ *  - q, k, v: bf16, 16-byte aligned; o: bf16, 16-byte aligned, not overlapping
+ *    the inputs; lse: fp32 [total_q][num_q_heads], contiguous, or NULL.
+ *  - cu_q, cu_k: device int32 [batch + 1], not decreasing; they may be the same.
+ *    The lengths are read on the device: a captured call follows them.
+ *  - ws: at least sparse_attn_packed_workspace_size bytes, 256-byte aligned.  It
+ *    needs no preparation and holds nothing between calls; calls that may run
+ *    at the same time need one each.
+ * Scores, softmax and sums are fp32; the weights are rounded to bf16 for the
+ * product with the values, and their normaliser is the sum of the rounded ones.
+ * The same inputs give the same bits.
+ * dev_status: SA_DEV_BAD_COUNT when cu_q or cu_k decreases or leaves
+ * [0, total] (clamped), SA_DEV_TIMEOUT as in sparse_attn_forward (its limit is
+ * sparse_attn_set_wait_limit's), SA_DEV_BAD_LAUNCH.
+ * Errors: INVALID_ARG (NULL, misalignment, strides, scale), SHAPE (sizes,
+ * Hq % Hkv), UNSUPPORTED (d), CUDA.
+ */
+sa_status sparse_attn_packed_forward(const sa_packed_shape* shp, const void* q, const void* k,
+                                     const void* v, const int32_t* cu_q, const int32_t* cu_k,
+                                     void* o, float* lse, void* ws, size_t ws_bytes,
+                                     int32_t* dev_status, sa_stream_t stream);
 
 #ifdef __cplusplus
 }
