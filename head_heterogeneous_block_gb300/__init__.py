@@ -30,11 +30,14 @@ __all__ = [
     "PagedCacheDesc", "sparse_attn_paged_append", "sparse_attn_paged_attend",
     "sparse_attn_paged_attend_workspace_size", "sparse_attn_paged_evict",
     "sparse_attn_paged_evict_workspace_size",
+    "PagePoolDesc", "PageGrowth", "sparse_attn_paged_grow", "sparse_attn_paged_grow_workspace_size",
+    "RotaryDesc", "sparse_attn_rotary", "sparse_attn_rotary_store",
     "PackedShape", "sparse_attn_packed_forward", "sparse_attn_packed_workspace_size",
 ]
 # these classes need torch, which the C binding itself does not: `import *` asks
 # for it only where there is one
-_CLASSES = {"PagedCache": "paged", "PackedAttention": "packed"}
+_CLASSES = {"PagedCache": "paged", "PagePool": "pages", "Rotary": "rotary",
+            "PackedAttention": "packed"}
 if (sys.modules["torch"] if "torch" in sys.modules else importlib.util.find_spec("torch")) is not None:
     __all__.extend(_CLASSES)
 
@@ -87,6 +90,30 @@ class PagedCacheDesc(ctypes.Structure):
                 ("v_page_stride", ctypes.c_int64), ("page", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class PagePoolDesc(ctypes.Structure):
+    """``sa_page_pool``: where the pages of a paged cache are accounted for."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("table", "lens", "owned", "free_pages",
+                                                "free_count", "weights", "positions")] +
+                [("num_pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                 ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32),
+                 ("num_kv_heads", ctypes.c_int32)])
+
+
+class PageGrowth(ctypes.Structure):
+    """``sa_page_growth``: new tokens, and where their pages and slots go."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("cu", "counts", "ended", "start", "slots",
+                                                "token_positions", "granted", "lens_out",
+                                                "owned_out", "free_count_out", "start_out")] +
+                [("tokens", ctypes.c_int32)])
+
+
+class RotaryDesc(ctypes.Structure):
+    """``sa_rotary``: frequencies and pairs of rotary positions."""
+    _fields_ = [("turns", ctypes.c_void_p), ("factor", ctypes.c_float),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 class PackedShape(ctypes.Structure):
@@ -161,6 +188,15 @@ def _load():
         "sparse_attn_paged_evict": (ctypes.c_int, [ctypes.POINTER(PagedCacheDesc),
                                                    ctypes.POINTER(I32), I32, I32, P, P, P, P, SZ,
                                                    P, P]),
+        "sparse_attn_paged_grow_workspace_size": (ctypes.c_int, [ctypes.POINTER(PagePoolDesc),
+                                                                 ctypes.POINTER(SZ)]),
+        "sparse_attn_paged_grow": (ctypes.c_int, [ctypes.POINTER(PagePoolDesc),
+                                                  ctypes.POINTER(PageGrowth), P, SZ, P, P]),
+        "sparse_attn_rotary": (ctypes.c_int, [ctypes.POINTER(RotaryDesc), I32, I32, I32, P] +
+                               [P, ctypes.POINTER(I64)] * 4 + [P]),
+        "sparse_attn_rotary_store": (ctypes.c_int, [ctypes.POINTER(RotaryDesc), I32, I32, P] +
+                                     [P, ctypes.POINTER(I64)] * 5 +
+                                     [ctypes.POINTER(PagedCacheDesc), P, P, P]),
         "sparse_attn_packed_workspace_size": (ctypes.c_int, [ctypes.POINTER(PackedShape),
                                                              ctypes.POINTER(SZ)]),
         "sparse_attn_packed_forward": (ctypes.c_int, [ctypes.POINTER(PackedShape), P, P, P, P, P,
@@ -498,6 +534,51 @@ def sparse_attn_paged_evict(cache: PagedCacheDesc, keep, sinks: int, recent: int
                                         _ptr(positions_out), _ptr(ws), ws_bytes,
                                         _ptr(dev_status), _stream(stream)),
            "sparse_attn_paged_evict")
+
+
+def sparse_attn_paged_grow_workspace_size(pool: PagePoolDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.sparse_attn_paged_grow_workspace_size(ctypes.byref(pool), ctypes.byref(n)),
+           "sparse_attn_paged_grow_workspace_size")
+    return n.value
+
+
+def sparse_attn_paged_grow(pool: PagePoolDesc, growth: PageGrowth, ws, ws_bytes: int, dev_status,
+                           stream=None):
+    """Pages and slots of new tokens, rows' spare pages given back."""
+    _check(_lib.sparse_attn_paged_grow(ctypes.byref(pool), ctypes.byref(growth), _ptr(ws),
+                                       ws_bytes, _ptr(dev_status), _stream(stream)),
+           "sparse_attn_paged_grow")
+
+
+def _strides2(s):
+    return None if s is None else (ctypes.c_int64 * 2)(*s)
+
+
+def sparse_attn_rotary(rot: RotaryDesc, tokens: int, num_q_heads: int, num_kv_heads: int,
+                       positions, q, q_strides, k, k_strides, q_out, q_out_strides, k_out,
+                       k_out_strides, stream=None):
+    """Rotary positions of queries and keys; ``q``, ``k``, ``q_out`` and
+    ``k_out`` are device addresses with the given (token, head) strides, in
+    elements."""
+    _check(_lib.sparse_attn_rotary(ctypes.byref(rot), tokens, num_q_heads, num_kv_heads,
+                                   _ptr(positions), q, _strides2(q_strides), k,
+                                   _strides2(k_strides), q_out, _strides2(q_out_strides), k_out,
+                                   _strides2(k_out_strides), _stream(stream)),
+           "sparse_attn_rotary")
+
+
+def sparse_attn_rotary_store(rot: RotaryDesc, tokens: int, num_q_heads: int, positions, q,
+                             q_strides, k, k_strides, v, v_strides, q_out, q_out_strides, k_out,
+                             k_out_strides, cache: PagedCacheDesc, slots, dev_status, stream=None):
+    """The same, and the rotated keys and the values go to the cache's
+    ``slots`` (``k_out`` may be None)."""
+    _check(_lib.sparse_attn_rotary_store(
+        ctypes.byref(rot), tokens, num_q_heads, _ptr(positions), q, _strides2(q_strides), k,
+        _strides2(k_strides), v, _strides2(v_strides), q_out, _strides2(q_out_strides), k_out,
+        _strides2(k_out_strides), ctypes.byref(cache), _ptr(slots), _ptr(dev_status),
+        _stream(stream)),
+        "sparse_attn_rotary_store")
 
 
 def sparse_attn_packed_workspace_size(shape: PackedShape) -> int:

@@ -27,7 +27,7 @@ class DeviceOperator:
         # the streams that the status word and the workspace were allocated on
         self._status_stream = self._ws_stream = _raw_stream(self._index)
 
-    def _grow(self, need):
+    def _need(self, need):
         """A workspace of at least ``need`` bytes; the device is current."""
         if need <= self._ws_bytes:
             return

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "sparse_attn.h"
@@ -42,6 +43,52 @@ struct AttendArgs {
 };
 size_t attend_workspace(const sa_paged_cache& c, int32_t Hq, bool accumulate, int sms);
 cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st, bool* encode_failed);
+
+struct GrowArgs {
+  int32_t* table;
+  const int32_t* lens;
+  const int32_t* owned;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  float* weights;                     // or NULL
+  int32_t* slot_positions;            // or NULL
+  const int32_t* cu;                  // [batch + 1], or NULL: spans of `span` tokens
+  const int32_t* counts;              // or NULL
+  const uint8_t* ended;               // or NULL
+  const int32_t* start;               // or NULL
+  int64_t* slots;                     // [Hkv][tokens]
+  int32_t* positions;                 // [tokens] or NULL
+  int32_t* granted;                   // [batch] or NULL
+  int32_t* lens_out;
+  int32_t* owned_out;
+  int32_t* free_count_out;
+  int32_t* start_out;                 // or NULL
+  int64_t num_pages;
+  int32_t page, page_shift, max_pages, batch, Hkv, tokens, span;
+  void* ws;
+  int32_t* dev_status;
+};
+size_t grow_workspace(int32_t batch, int32_t num_kv_heads);
+cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st);
+
+struct RotaryArgs {
+  const uint64_t* turns;              // [rot / 2]
+  const int32_t* positions;           // [tokens]
+  const __nv_bfloat16* q;             // token, head strides beside each
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;             // with slots
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;               // or NULL
+  int64_t qs[2], ks[2], vs[2], qos[2], kos[2];
+  const int64_t* slots;               // [Hkv][tokens] or NULL: no store
+  __nv_bfloat16* k_pages;
+  __nv_bfloat16* v_pages;
+  int64_t k_page_stride, v_page_stride, num_slots;
+  int32_t page_shift, tokens, Hq, Hkv, d, rot, interleaved;
+  float factor;
+  int32_t* dev_status;                // with slots
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int sms, cudaStream_t st);
 
 struct EvictArgs {
   sa_paged_cache c;

@@ -1,9 +1,10 @@
-// C ABI entry points of the paged key-value cache: argument checks, then the
-// launches of paged_append.cu, paged_attend.cu and paged_evict.cu.
+// C ABI entry points of the paged key-value cache and of the rotary positions:
+// argument checks, then the launches of paged_*.cu and rotary.cu.
 
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "kernels.h"
@@ -61,6 +62,96 @@ sa_status check_evict(const sa_paged_cache* c) {
       int64_t(c->page) * c->max_pages > sa_paged::kMaxEvictSlots)
     return SA_ERR_UNSUPPORTED;
   return SA_OK;
+}
+
+sa_status check_pool(const sa_page_pool* p) {
+  if (!p || !p->table || !p->lens || !p->owned || !p->free_pages || !p->free_count)
+    return SA_ERR_INVALID_ARG;
+  if (p->page <= 0 || p->max_pages <= 0 || p->batch <= 0 || p->num_kv_heads <= 0 ||
+      p->num_pages <= 0 || p->num_pages >= (int64_t(1) << 30))
+    return SA_ERR_SHAPE;
+  if (p->page < 16 || p->page > 256 || (p->page & (p->page - 1))) return SA_ERR_UNSUPPORTED;
+  if (!aligned(p->table, 4) || !aligned(p->lens, 4) || !aligned(p->owned, 4) ||
+      !aligned(p->free_pages, 4) || !aligned(p->free_count, 4) || !aligned(p->weights, 4) ||
+      !aligned(p->positions, 4))
+    return SA_ERR_INVALID_ARG;
+  // slots of a row, and the pages of all rows, are 32-bit counts with room for sums
+  const int64_t rows = int64_t(p->batch) * p->num_kv_heads;
+  if (rows > (1 << 20) || int64_t(p->page) * p->max_pages > (int64_t(1) << 30) ||
+      p->max_pages > (int64_t(1) << 30) / rows)
+    return SA_ERR_SHAPE;
+  return SA_OK;
+}
+
+// Checks and arguments of the two rotary calls, but for the store's.
+sa_status rotary_args(const sa_rotary* rot, int32_t tokens, int32_t hq, int32_t hkv,
+                      const int32_t* positions, const void* q, const int64_t* qs, const void* k,
+                      const int64_t* ks, void* q_out, const int64_t* qos, void* k_out,
+                      const int64_t* kos, bool store, sa_paged::RotaryArgs* a) {
+  if (!rot) return SA_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > (1 << 30) || hq < 1 || hkv < 1 || hq > (1 << 20) || hkv > (1 << 20))
+    return SA_ERR_SHAPE;
+  if (rot->head_dim != 64 && rot->head_dim != 128) return SA_ERR_UNSUPPORTED;
+  if (rot->rot_dim < 16 || rot->rot_dim > rot->head_dim || rot->rot_dim % 16)
+    return SA_ERR_UNSUPPORTED;
+  if (rot->interleaved != 0 && rot->interleaved != 1) return SA_ERR_INVALID_ARG;
+  if (!std::isfinite(rot->factor)) return SA_ERR_INVALID_ARG;
+  if (!rot->turns || !qs || !ks || !qos || (!store && !kos) || (k_out && !kos))
+    return SA_ERR_INVALID_ARG;
+  if (tokens > 0 && (!positions || !q || !k || !q_out || (!store && !k_out)))
+    return SA_ERR_INVALID_ARG;
+  if (!aligned(rot->turns, 8) || !aligned(positions, 4) || !aligned(q, 16) || !aligned(k, 16) ||
+      !aligned(q_out, 16) || !aligned(k_out, 16))
+    return SA_ERR_INVALID_ARG;
+  // the stride of an extent of one is not used
+  auto strides = [&](const int64_t* s, int32_t heads, int64_t least, int64_t* to) {
+    to[0] = tokens > 1 ? s[0] : 0;
+    to[1] = heads > 1 ? s[1] : 0;
+    for (int i = 0; i < 2; ++i)
+      if ((i ? heads : tokens) > 1 && (to[i] % 8 || to[i] < least || to[i] >= kMaxStride))
+        return false;
+    return true;
+  };
+  if (!strides(qs, hq, 0, a->qs) || !strides(ks, hkv, 0, a->ks) ||
+      !strides(qos, hq, rot->head_dim, a->qos))
+    return SA_ERR_INVALID_ARG;
+  a->kos[0] = a->kos[1] = 0;
+  if (k_out && !strides(kos, hkv, rot->head_dim, a->kos)) return SA_ERR_INVALID_ARG;
+  auto same = [](const int64_t* x, const int64_t* y) { return x[0] == y[0] && x[1] == y[1]; };
+  if (tokens > 0) {
+    if ((q_out == q && !same(a->qs, a->qos)) || (k_out == k && !same(a->ks, a->kos)) ||
+        q_out == k || k_out == q || q_out == k_out)
+      return SA_ERR_INVALID_ARG;
+  }
+  a->turns = rot->turns;
+  a->factor = rot->factor;
+  a->d = rot->head_dim;
+  a->rot = rot->rot_dim;
+  a->interleaved = rot->interleaved;
+  a->tokens = tokens;
+  a->Hq = hq;
+  a->Hkv = hkv;
+  a->positions = positions;
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k = static_cast<const __nv_bfloat16*>(k);
+  a->q_out = static_cast<__nv_bfloat16*>(q_out);
+  a->k_out = static_cast<__nv_bfloat16*>(k_out);
+  a->v = nullptr;
+  a->slots = nullptr;
+  a->k_pages = a->v_pages = nullptr;
+  a->vs[0] = a->vs[1] = a->k_page_stride = a->v_page_stride = a->num_slots = 0;
+  a->page_shift = 0;
+  a->dev_status = nullptr;
+  return SA_OK;
+}
+
+sa_status run_rotary(const sa_paged::RotaryArgs& a, sa_stream_t stream) {
+  if (a.tokens == 0) return SA_OK;
+  int sms = 0;
+  const sa_status s = sa_paged::sm_count(&sms);
+  if (s != SA_OK) return s;
+  return sa_k::cuda_status(
+      sa_paged::launch_rotary(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 using sa_k::cuda_status;
@@ -226,6 +317,109 @@ sa_status sparse_attn_paged_evict(const sa_paged_cache* cache, const int32_t* ke
   a.ws = ws;
   a.dev_status = dev_status;
   return cuda_status(sa_paged::launch_evict(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sa_status sparse_attn_rotary(const sa_rotary* rot, int32_t tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, const int32_t* positions, const void* q,
+                             const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                             void* q_out, const int64_t* q_out_strides, void* k_out,
+                             const int64_t* k_out_strides, sa_stream_t stream) {
+  sa_paged::RotaryArgs a;
+  const sa_status s =
+      rotary_args(rot, tokens, num_q_heads, num_kv_heads, positions, q, q_strides, k, k_strides,
+                  q_out, q_out_strides, k_out, k_out_strides, false, &a);
+  return s != SA_OK ? s : run_rotary(a, stream);
+}
+
+sa_status sparse_attn_rotary_store(const sa_rotary* rot, int32_t tokens, int32_t num_q_heads,
+                                   const int32_t* positions, const void* q,
+                                   const int64_t* q_strides, const void* k,
+                                   const int64_t* k_strides, const void* v,
+                                   const int64_t* v_strides, void* q_out,
+                                   const int64_t* q_out_strides, void* k_out,
+                                   const int64_t* k_out_strides, const sa_paged_cache* cache,
+                                   const int64_t* slots, int32_t* dev_status, sa_stream_t stream) {
+  sa_status s = check_cache(cache);
+  if (s != SA_OK) return s;
+  sa_paged::RotaryArgs a;
+  s = rotary_args(rot, tokens, num_q_heads, cache->num_kv_heads, positions, q, q_strides, k,
+                  k_strides, q_out, q_out_strides, k_out, k_out_strides, true, &a);
+  if (s != SA_OK) return s;
+  if (rot->head_dim != cache->head_dim) return SA_ERR_SHAPE;
+  if (!v_strides || !dev_status || (tokens > 0 && (!v || !slots))) return SA_ERR_INVALID_ARG;
+  if (!aligned(v, 16) || !aligned(slots, 8) || !aligned(dev_status, 4)) return SA_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    const bool used = (i ? cache->num_kv_heads : tokens) > 1;
+    if (used && (v_strides[i] < 0 || v_strides[i] % 8 || v_strides[i] >= kMaxStride))
+      return SA_ERR_INVALID_ARG;
+    a.vs[i] = used ? v_strides[i] : 0;
+  }
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.slots = slots;
+  a.k_pages = static_cast<__nv_bfloat16*>(cache->k_pages);
+  a.v_pages = static_cast<__nv_bfloat16*>(cache->v_pages);
+  a.k_page_stride = cache->k_page_stride;
+  a.v_page_stride = cache->v_page_stride;
+  a.page_shift = __builtin_ctz(unsigned(cache->page));
+  a.num_slots = cache->num_pages * cache->page;
+  a.dev_status = dev_status;
+  return run_rotary(a, stream);
+}
+
+sa_status sparse_attn_paged_grow_workspace_size(const sa_page_pool* pool, size_t* bytes) {
+  if (!bytes) return SA_ERR_INVALID_ARG;
+  const sa_status s = check_pool(pool);
+  if (s != SA_OK) return s;
+  *bytes = sa_paged::grow_workspace(pool->batch, pool->num_kv_heads);
+  return SA_OK;
+}
+
+sa_status sparse_attn_paged_grow(const sa_page_pool* pool, const sa_page_growth* g, void* ws,
+                                 size_t ws_bytes, int32_t* dev_status, sa_stream_t stream) {
+  const sa_status s = check_pool(pool);
+  if (s != SA_OK) return s;
+  if (!g || !g->lens_out || !g->owned_out || !g->free_count_out || !ws || !dev_status)
+    return SA_ERR_INVALID_ARG;
+  if (g->tokens < 0 || g->tokens > (1 << 30) || (!g->cu && g->tokens % pool->batch))
+    return SA_ERR_SHAPE;
+  if (g->tokens > 0 && !g->slots) return SA_ERR_INVALID_ARG;
+  if (!aligned(g->cu, 4) || !aligned(g->counts, 4) || !aligned(g->start, 4) ||
+      !aligned(g->slots, 8) || !aligned(g->token_positions, 4) || !aligned(g->granted, 4) ||
+      !aligned(g->lens_out, 4) || !aligned(g->owned_out, 4) || !aligned(g->free_count_out, 4) ||
+      !aligned(g->start_out, 4) || !aligned(ws, 256) || !aligned(dev_status, 4))
+    return SA_ERR_INVALID_ARG;
+  if (ws_bytes < sa_paged::grow_workspace(pool->batch, pool->num_kv_heads))
+    return SA_ERR_INVALID_ARG;
+  sa_paged::GrowArgs a;
+  a.table = pool->table;
+  a.lens = pool->lens;
+  a.owned = pool->owned;
+  a.free_pages = pool->free_pages;
+  a.free_count = pool->free_count;
+  a.weights = pool->weights;
+  a.slot_positions = pool->positions;
+  a.cu = g->cu;
+  a.counts = g->counts;
+  a.ended = g->ended;
+  a.start = g->start;
+  a.slots = g->slots;
+  a.positions = g->token_positions;
+  a.granted = g->granted;
+  a.lens_out = g->lens_out;
+  a.owned_out = g->owned_out;
+  a.free_count_out = g->free_count_out;
+  a.start_out = g->start_out;
+  a.num_pages = pool->num_pages;
+  a.page = pool->page;
+  a.page_shift = __builtin_ctz(unsigned(pool->page));
+  a.max_pages = pool->max_pages;
+  a.batch = pool->batch;
+  a.Hkv = pool->num_kv_heads;
+  a.tokens = g->tokens;
+  a.span = g->tokens / pool->batch;
+  a.ws = ws;
+  a.dev_status = dev_status;
+  return cuda_status(sa_paged::launch_grow(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

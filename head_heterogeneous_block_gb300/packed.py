@@ -35,7 +35,7 @@ class PackedAttention(DeviceOperator):
         """Grow the workspace to what calls of these sizes need, and those so
         far; the device is current."""
         tokens, batch = max(tokens, self._tokens), max(batch, self._batch)
-        self._grow(sparse_attn_packed_workspace_size(PackedShape(
+        self._need(sparse_attn_packed_workspace_size(PackedShape(
             total_q=tokens, batch=batch, num_q_heads=self.num_q_heads,
             num_kv_heads=self.num_kv_heads, head_dim=self.head_dim, scale=self.scale)))
         self._tokens, self._batch = tokens, batch

@@ -1,0 +1,190 @@
+"""Rotary positions over the C ABI's ``sparse_attn_rotary*`` calls: the
+frequencies and their scalings, and the operator class."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import RotaryDesc, _check, _lib
+from ._device import DeviceOperator
+
+_I64x2 = ctypes.c_int64 * 2
+_rotary, _store = _lib.sparse_attn_rotary, _lib.sparse_attn_rotary_store
+
+
+def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
+    """Radians a position of each of the ``rot_dim / 2`` pairs (floats), and the
+    factor on the rotated values.  ``scaling`` stretches them for contexts
+    longer than the model was trained on: None, or a dict with ``type``
+
+    ``linear``      every frequency divided by ``factor`` (positions interpolated)
+    ``ntk``         the base raised to base * factor^(rot_dim / (rot_dim - 2)):
+                    the highest frequency stays, the lowest is divided by factor
+    ``wavelength``  with the turns that a pair makes over ``original`` positions:
+                    below ``low`` divided by factor, above ``high`` kept, between
+                    them blended in proportion to the turns
+    ``yarn``        kept for pairs of more than ``beta_fast`` (32) turns over
+                    ``original`` positions, divided by factor below
+                    ``beta_slow`` (1), blended in proportion to the pair's number
+                    between them; values times ``attention_factor`` (0.1
+                    ln(factor) + 1)
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    base = float(base)
+    if not (base > 1.0 and math.isfinite(base)):
+        raise ValueError("base must be finite and above 1")
+    scaling = dict(scaling) if scaling else {"type": "none"}
+    kind = scaling.pop("type", None)
+
+    def get(name, default=None):
+        value = scaling.pop(name, default)
+        if value is None:
+            raise ValueError(f"scaling {kind!r} needs {name!r}")
+        if not (float(value) > 0 and math.isfinite(float(value))):
+            raise ValueError(f"scaling {name!r} must be positive and finite")
+        return float(value)
+
+    multiplier = 1.0
+    pairs = range(rot_dim // 2)
+    if kind == "ntk":
+        factor = get("factor")
+        if rot_dim > 2:
+            base *= factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * i / rot_dim) for i in pairs]
+    if kind == "linear":
+        factor = get("factor")
+        freq = [f / factor for f in freq]
+    elif kind == "wavelength":
+        factor, low, high, original = get("factor"), get("low"), get("high"), get("original")
+        if not low < high:
+            raise ValueError("scaling 'low' must be below 'high'")
+        keep = [min(1.0, max(0.0, (f * original / (2 * math.pi) - low) / (high - low)))
+                for f in freq]
+        freq = [f * x + f / factor * (1.0 - x) for f, x in zip(freq, keep)]
+    elif kind == "yarn":
+        factor, original = get("factor"), get("original")
+        fast, slow = get("beta_fast", 32.0), get("beta_slow", 1.0)
+        multiplier = get("attention_factor", 0.1 * math.log(factor) + 1.0)
+        if fast < slow:
+            raise ValueError("scaling 'beta_fast' must not be below 'beta_slow'")
+
+        def pair(turns):
+            return rot_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot_dim - 1)
+        slowed = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in pairs]
+        freq = [f * (1.0 - x) + f / factor * x for f, x in zip(freq, slowed)]
+    elif kind not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {kind!r}")
+    if scaling:
+        raise ValueError(f"scaling {kind!r} does not take {sorted(scaling)}")
+    return freq, multiplier
+
+
+class Rotary(DeviceOperator):
+    """Rotary positions of queries and keys: the first ``rot_dim`` of
+    ``head_dim`` elements (default: all), in pairs (i, i + rot_dim/2) or, with
+    ``interleaved``, (2i, 2i + 1).  ``base`` and ``scaling`` as
+    ``rotary_frequencies`` takes them."""
+
+    def __init__(self, head_dim, rot_dim=None, base=10000.0, interleaved=False, scaling=None,
+                 device="cuda"):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if head_dim not in (64, 128):
+            raise ValueError("head_dim must be 64 or 128")
+        if rot_dim % 16 or not 16 <= rot_dim <= head_dim:
+            raise ValueError("rot_dim must be a multiple of 16 up to head_dim")
+        self.frequencies, self.factor = rotary_frequencies(rot_dim, base, scaling)
+        super().__init__(device)
+        self.head_dim, self.rot_dim, self.interleaved = head_dim, rot_dim, bool(interleaved)
+        # fractions of a turn a position, in 2^-64ths (as the signed 64-bit numbers of torch)
+        turns = [round(f / (2 * math.pi) * 2.0**64) % 2**64 for f in self.frequencies]
+        self.turns = torch.tensor([t - 2**64 if t >= 2**63 else t for t in turns],
+                                  dtype=torch.int64, device=self.device)
+        self._desc = RotaryDesc(self.turns.data_ptr(), self.factor, head_dim, rot_dim,
+                                int(self.interleaved))
+        self._ref = ctypes.byref(self._desc)
+
+    def _follow(self):
+        handle = self._handle()
+        if handle != self._status_stream:
+            self.turns.record_stream(self._stream(handle))
+        return handle
+
+    def _heads(self, t, name):
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [tokens, heads, {self.head_dim}]")
+        return t.shape[1]
+
+    def _like(self, t):
+        return torch.empty(t.shape, dtype=torch.bfloat16, device=self.device)
+
+    def __call__(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """q bf16 [tokens, num_q_heads, d], k bf16 [tokens, num_kv_heads, d] (any
+        strides that are multiples of 8, d contiguous) and positions int32
+        [tokens].  Returns (``q_out``, ``k_out``): new tensors without them;
+        each may be its input, which then changes in place."""
+        if self._elsewhere(stream):
+            return self._on(stream, lambda: self(q, k, positions, q_out, k_out))
+        d = self.head_dim
+        hq, hkv = self._heads(q, "q"), self._heads(k, "k")
+        qp, q0, q1 = self._rows(q, hq, d, "q")
+        kp, k0, k1 = self._rows(k, hkv, d, "k")
+        tokens = q.shape[0]
+        if k.shape[0] != tokens:
+            raise ValueError("q and k must have the same number of tokens")
+        q_out = self._like(q) if q_out is None else q_out
+        k_out = self._like(k) if k_out is None else k_out
+        qop, qo0, qo1 = self._rows(q_out, hq, d, "q_out")
+        kop, ko0, ko1 = self._rows(k_out, hkv, d, "k_out")
+        if q_out.shape[0] != tokens or k_out.shape[0] != tokens:
+            raise ValueError("q_out and k_out must have the shapes of q and k")
+        pp = self._own(positions, torch.int32, (tokens,), "positions")
+        status = _rotary(self._ref, tokens, hq, hkv, pp, qp, _I64x2(q0, q1), kp, _I64x2(k0, k1),
+                         qop, _I64x2(qo0, qo1), kop, _I64x2(ko0, ko1), self._follow())
+        if status:
+            _check(status, "sparse_attn_rotary")
+        return q_out, k_out
+
+    def store(self, q, k, v, positions, cache, slots, q_out=None, k_out=None, stream=None):
+        """As a call, and in the same pass each token's rotated key and its value
+        (v bf16 [tokens, num_kv_heads, d]) go to ``slots`` of ``cache`` (a
+        ``PagedCache``): int64 [num_kv_heads, tokens], as ``PagePool.grow`` makes
+        them; nothing is stored where a slot is -1.  Without ``k_out`` the cache
+        has the only copy of the rotated keys.  Returns (``q_out``, ``k_out``).
+        A slot outside the pools stores nothing and sets ``SA_DEV_BAD_INDEX`` in
+        ``dev_status``."""
+        if self._elsewhere(stream):
+            return self._on(stream, lambda: self.store(q, k, v, positions, cache, slots, q_out,
+                                                       k_out))
+        d, hkv = self.head_dim, cache.num_kv_heads
+        if cache.head_dim != d:
+            raise ValueError(f"the cache's head_dim must be {d}")
+        if cache.device != self.device:
+            raise ValueError(f"the cache must be on {self.device}")
+        hq = self._heads(q, "q")
+        qp, q0, q1 = self._rows(q, hq, d, "q")
+        kp, k0, k1 = self._rows(k, hkv, d, "k")
+        vp, v0, v1 = self._rows(v, hkv, d, "v")
+        tokens = q.shape[0]
+        if k.shape[0] != tokens or v.shape[0] != tokens:
+            raise ValueError("q, k and v must have the same number of tokens")
+        q_out = self._like(q) if q_out is None else q_out
+        qop, qo0, qo1 = self._rows(q_out, hq, d, "q_out")
+        kop, kos = None, None
+        if k_out is not None:
+            kop, *kos = self._rows(k_out, hkv, d, "k_out")
+            kos = _I64x2(*kos)
+        if q_out.shape[0] != tokens or (k_out is not None and k_out.shape[0] != tokens):
+            raise ValueError("q_out and k_out must have the shapes of q and k")
+        pp = self._own(positions, torch.int32, (tokens,), "positions")
+        sp = self._own(slots, torch.int64, (hkv, tokens), "slots")
+        status = _store(self._ref, tokens, hq, pp, qp, _I64x2(q0, q1), kp, _I64x2(k0, k1), vp,
+                        _I64x2(v0, v1), qop, _I64x2(qo0, qo1), kop, kos, cache._ref, sp,
+                        self._status, self._follow())
+        if status:
+            _check(status, "sparse_attn_rotary_store")
+        return q_out, k_out

@@ -663,6 +663,137 @@ sa_status sparse_attn_paged_evict(const sa_paged_cache* cache, const int32_t* ke
                                   int32_t* dev_status, sa_stream_t stream);
 
 /*
+ * The pages of a paged cache, kept on the device: which are free, and how many
+ * entries of its table each row owns.
+ */
+typedef struct sa_page_pool {
+  int32_t* table;          /* [Bt][Hkv][max_pages], as sa_paged_cache's       */
+  int32_t* lens;           /* [Bt][Hkv] tokens of each row                    */
+  int32_t* owned;          /* [Bt][Hkv] pages of each row                     */
+  int32_t* free_pages;     /* [num_pages]: the first free_count are free      */
+  int32_t* free_count;     /* [1]                                             */
+  float* weights;          /* [Bt][Hkv][max_pages*page] or NULL               */
+  int32_t* positions;      /* the same shape, or NULL                         */
+  int64_t num_pages;       /* 1 .. 2^30 - 1                                   */
+  int32_t page;            /* 16, 32, 64, 128 or 256                          */
+  int32_t max_pages;
+  int32_t batch;
+  int32_t num_kv_heads;    /* batch * num_kv_heads <= 2^20                    */
+} sa_page_pool;
+
+/*
+ * New tokens: the `tokens` rows of a packed or padded tensor.  Sequence b has
+ * the span cu[b] .. cu[b+1] of them (cu NULL: tokens/batch each) and uses its
+ * first counts[b] (NULL: all).  All arrays are device memory; an output may be
+ * the input that it replaces.
+ */
+typedef struct sa_page_growth {
+  const int32_t* cu;       /* [Bt + 1], not decreasing, or NULL               */
+  const int32_t* counts;   /* [Bt] or NULL                                    */
+  const uint8_t* ended;    /* [Bt] or NULL: not 0 = the sequence is emptied
+                              first (a new one takes its place)               */
+  const int32_t* start;    /* [Bt] positions of the first new tokens (taken as
+                              0 where ended), or NULL: the longest row's
+                              length                                          */
+  int64_t* slots;          /* [Hkv][tokens], out: slot of each token in the
+                              pools, page number * page + row of the page; -1
+                              for tokens that get none                        */
+  int32_t* token_positions;/* [tokens] or NULL, out: start[b] + i; 0 for
+                              tokens that get no slot                         */
+  int32_t* granted;        /* [Bt] or NULL, out: tokens that got slots        */
+  int32_t* lens_out;       /* [Bt][Hkv]                                       */
+  int32_t* owned_out;      /* [Bt][Hkv]                                       */
+  int32_t* free_count_out; /* [1]                                             */
+  int32_t* start_out;      /* [Bt] or NULL, out: start + granted              */
+  int32_t tokens;
+} sa_page_growth;
+
+/*
+ * Workspace bytes of sparse_attn_paged_grow.  Host only.
+ */
+sa_status sparse_attn_paged_grow_workspace_size(const sa_page_pool* pool, size_t* bytes);
+
+/*
+ * Pages and slots of new tokens.  Row r of sequence b, which holds n tokens (0
+ * if ended) and is to hold c more, needs ceil((n + c) / page) pages.
+ *  - Rows give back what they own beyond that (after an eviction, say, or at the
+ *    end of their sequence; c may be 0): their last table entries.
+ *  - Rows want what is missing.  Pages are taken from the end of the list that
+ *    the free ones and then those given back make (rows, then entries, in
+ *    order), by rows and entries in order; the rest of the list is free after.
+ *  - A sequence whose pages, and those wanted before it, pass what the list has
+ *    gets none and keeps its length (granted 0, SA_DEV_NO_PAGES); so does every
+ *    later one that wants pages.  It still gives back.
+ * New slots get weight 0 and their token's position (with weights, positions).
+ * Page numbers do not depend on timing: the same inputs give the same tables.
+ * ws: at least sparse_attn_paged_grow_workspace_size bytes, 256-byte aligned, as
+ * for sparse_attn_paged_attend.
+ * dev_status: SA_DEV_NO_PAGES; SA_DEV_BAD_COUNT for lengths, owned pages,
+ * counts or free_count out of range (clamped; a row holds at most what its pages
+ * do), for a decreasing cu (no token gets a slot), for more tokens than a row's
+ * table has slots (the sequence gets none) and for more free and owned pages than
+ * there are; SA_DEV_BAD_INDEX for page numbers out of range (slot -1).
+ * Errors: INVALID_ARG (NULL, misalignment), SHAPE (sizes; tokens not a multiple
+ * of batch without cu), UNSUPPORTED (page), CUDA.
+ */
+sa_status sparse_attn_paged_grow(const sa_page_pool* pool, const sa_page_growth* growth, void* ws,
+                                 size_t ws_bytes, int32_t* dev_status, sa_stream_t stream);
+
+/*
+ * Rotary positions.  Of each head of d elements the first rot_dim are turned in
+ * pairs (x, y), elements (i, i + rot_dim/2) or, interleaved, (2i, 2i + 1), into
+ *   factor * (x cos a - y sin a, y cos a + x sin a),  a = position * f_i;
+ * the others are passed on.
+ */
+typedef struct sa_rotary {
+  const uint64_t* turns;   /* device [rot_dim/2]: f_i / 2 pi * 2^64, rounded,
+                              modulo 2^64                                     */
+  float factor;            /* on the rotated values; finite                   */
+  int32_t head_dim;        /* 64 or 128                                       */
+  int32_t rot_dim;         /* a multiple of 16, 16 .. head_dim                */
+  int32_t interleaved;     /* 0 or 1                                          */
+} sa_rotary;
+
+/*
+ *  - q, k: bf16, element (t, h, x) at t*strides[0] + h*strides[1] + x, t <
+ *    tokens; q_out, k_out likewise: strides multiples of 8 (>= 0 for the inputs,
+ *    at least head_dim for the outputs; the stride of an extent of one is not
+ *    used); 16-byte aligned.  An output may be its input (same address and
+ *    strides); otherwise outputs overlap neither the inputs nor each other.
+ *  - positions: device int32 [tokens], any value.
+ * An angle is within 2^-24 of a half turn at any position; values are fp32,
+ * rounded once to bf16.
+ * Errors: INVALID_ARG (NULL, misalignment, strides, outputs of the same
+ * address, factor), SHAPE (sizes), UNSUPPORTED (head_dim, rot_dim), CUDA.
+ */
+sa_status sparse_attn_rotary(const sa_rotary* rot, int32_t tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, const int32_t* positions, const void* q,
+                             const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                             void* q_out, const int64_t* q_out_strides, void* k_out,
+                             const int64_t* k_out_strides, sa_stream_t stream);
+
+/*
+ * The same, and each token's rotated key and its value go to the paged cache in
+ * the same pass: those of KV head g to slot slots[g*tokens + t] of the pools
+ * (page number * page + row of the page), nothing where it is -1.  Only the
+ * pools change: lengths, weights and positions are sparse_attn_paged_grow's,
+ * which also makes the slots.
+ *  - v: bf16 with v_strides as k; k_out: may be NULL (the cache's copy alone).
+ *  - slots: device int64 [num_kv_heads][tokens], each one token's alone.
+ * dev_status: SA_DEV_BAD_INDEX for a slot outside the pools (nothing is stored).
+ * Errors: as above, and those of the cache (its head_dim and num_kv_heads are
+ * the call's).
+ */
+sa_status sparse_attn_rotary_store(const sa_rotary* rot, int32_t tokens, int32_t num_q_heads,
+                                   const int32_t* positions, const void* q,
+                                   const int64_t* q_strides, const void* k,
+                                   const int64_t* k_strides, const void* v,
+                                   const int64_t* v_strides, void* q_out,
+                                   const int64_t* q_out_strides, void* k_out,
+                                   const int64_t* k_out_strides, const sa_paged_cache* cache,
+                                   const int64_t* slots, int32_t* dev_status, sa_stream_t stream);
+
+/*
  * Dense causal attention of packed sequences.  Sequence s has the queries
  * cu_q[s] .. cu_q[s+1] and the keys cu_k[s] .. cu_k[s+1] of the packed tensors;
  * its queries are its last tokens, so with n queries and m keys query i sees
