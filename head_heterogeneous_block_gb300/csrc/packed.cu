@@ -71,13 +71,26 @@ using sa_packed::Args;
 constexpr int kRows = 128;            // query rows of a tile
 constexpr int kBK = 128;              // keys of a block
 constexpr int kSoftmaxThreads = 512;
-constexpr int kThreads = 128 + kSoftmaxThreads;
+constexpr int kOutThreads = 128;
+constexpr int kThreads = 128 + kSoftmaxThreads + kOutThreads;
 constexpr int kNI = 4;                // item descriptions in flight
 constexpr int kBatch = 2048;          // items between two looks at what is to be done again
-constexpr int kMinRange = 8;          // key blocks: shorter ranges cost more to join than they save
+constexpr int kDirectBlocks = 8;      // key blocks of a tile that is not worth cutting
+constexpr int kRounds = 4;            // of head groups, so that a round's keys and values stay in L2
+constexpr int kItemCost = 2;          // what an item costs beside its blocks, in blocks
 constexpr int kBins = 1024;
 constexpr int kScheduleThreads = 1024;
-constexpr int kSeqShared = 4096;      // sequences whose first tiles stay in shared memory
+constexpr int kSeqShared = 1024;      // sequences that stay in shared memory
+constexpr int kTileRegs = 4;          // tiles of a thread that it remembers
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 16;         // rows of a join unit
+
+// Registers of a thread by role, together the launch's 768 x 80: the control
+// warps give up what the output warps, a whole row each, need.
+constexpr int kControlRegs = 64, kSoftmaxRegs = 80, kOutRegs = 96;
+static_assert(128 * kControlRegs + kSoftmaxThreads * kSoftmaxRegs + kOutThreads * kOutRegs <=
+                  kThreads * 80,
+              "a larger sum would wait forever");
 
 template <int D>
 struct Cfg {
@@ -91,7 +104,6 @@ struct Cfg {
   static constexpr int kNV = kNK;
   static constexpr int kNS = 3;
   static constexpr int kCols = kBK / 4;             // S columns of a softmax group
-  static constexpr int kOCols = D / 4;
   static constexpr uint32_t kO = kNS * kBK;         // TMEM column of O
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kData = kNQ * kQBytes + (kNK + kNV) * kKVBytes;
@@ -103,24 +115,33 @@ struct __align__(16) Entry {
   int32_t kbeg;           // first key of the sequence (row of k)
   int32_t lim0;           // last key, from kbeg, that its first token sees (may be negative)
   int32_t b0, n;          // key blocks
-  int32_t split;          // first partial slot of the tile's ranges, -1: the whole tile
-  int32_t part;           // range | ranges << 16
+  int32_t slot;           // of a range: its place among the partial states; -1: the whole tile
+  int32_t hg;             // with ranges: head group within the round
+};
+
+// A tile that was cut.
+struct __align__(16) Cut {
+  int32_t q0, ntok, hg;
+  int32_t slot, ranges;   // partial states, in key order
+  int32_t pad[3];
 };
 
 struct Header {
   int32_t counter;        // items handed out beyond each CTA's first
-  int32_t entries;
-  int32_t by_head;        // KV head by KV head
+  int32_t entries;        // tiles (without ranges)
+  int32_t cuts;
 };
 
 struct __align__(16) Item {
   Entry e;
-  int32_t head0, g, hg;   // first query head, KV head, group of heads
+  int32_t head0, g;       // first query head, KV head
   int32_t mt;             // blocks before the first masked one
   int32_t pos;            // place in the batch of items
-  int32_t careful;
+  int32_t careful;        // kAgain bits
+  int32_t pad[3];
 };
 enum { kEnd = 0, kMarker = -1 };      // values of e.n that are not items
+enum { kClean = 1, kMaxima = 2 };     // done again: with V cleaned, and with true maxima
 
 struct Shared {
   uint64_t q_full[2], q_empty[2];
@@ -129,23 +150,27 @@ struct Shared {
   uint64_t o_last;        // a phase per item: its last P V is complete
   uint64_t o_free;        // a phase per item: O is in registers
   uint64_t xch_bar;       // exchanges between the softmax groups
-  uint64_t stage_bar[2];  // items in turn: its output is staged or stored
-  uint64_t part_bar;      // a phase per range: its partial state is written
-  uint64_t tick_bar;      //   and whether it was the tile's last is known
-  uint64_t batch_done;    // a phase per marker: every epilogue before it is through
+  uint64_t sum_full[2], sum_empty[2];   // items in turn: the rows' sums
+  uint64_t stage_bar[2];  // items in turn: the output is staged or stored
+  uint64_t batch_done;    // a phase per marker: every output before it is through
   uint64_t drain_qk, drain_pv;
   uint64_t info_full[kNI], info_empty[kNI];
   Item info[kNI];
   int32_t ids[kBatch];    // items of the batch
-  uint32_t redo[kBatch / 32];
+  uint32_t again[kBatch / 32], maxima[kBatch / 32];   // to be done again; with true maxima
   float xch[2][4][kRows];
-  float xch_l[2][4][kRows];   // unrounded sums, for the log-sum-exp
+  float sum[2][4][kRows];     // per softmax group: sums of rounded weights
+  float sum_x[2][4][kRows];   // and of unrounded ones, for the log-sum-exp
+  float ref[2][kRows];        // the rows' references
   int32_t stage_q0[2], stage_h[2];   // where the tile staged in Q stage x goes; q0 < 0: nowhere
   int32_t bad_v[2];       // item (by its number, from 1) that met infinities or NaN in masked blocks
-  int32_t last;
   uint32_t tmem_base;
   int abort;
 };
+
+// How a CTA gets its work: its one tile, tiles from a counter (those with most
+// blocks first), or an equal share of all blocks.
+enum { kDirect = 0, kTiles = 1, kRanges = 2 };
 
 struct Params {
   const int32_t* cu_q;
@@ -156,13 +181,15 @@ struct Params {
   const Header* header;
   int32_t* counter;
   const Entry* entries;
-  int32_t* tickets;       // per partial slot; the tile's first one counts
-  float* part_o;          // [slot][128][D]
-  float4* part_ml;        // [slot][128]: m, rounded sum, unrounded sum
+  const int32_t* first;   // with ranges: [grid + 1] first entry of each CTA's share of a round
+  float4* part_o;         // [slot][D / 4][128]
+  float4* part_ml;        // [slot][128]: reference, rounded sum, unrounded sum
   int64_t v_st, v_sh, o_st, o_sh;
   int32_t total_q, total_k, batch, Hq, group, tile_heads, tile_tokens;
   int32_t head_groups;    // tiles' heads: Hq / tile_heads
-  int32_t direct;         // no schedule: a CTA finds its tile
+  int32_t mode;           // kDirect, kTiles or kRanges
+  int32_t by_head;        // tiles: KV head by KV head
+  int32_t rounds, round_groups, round_slots;   // ranges
   float scale_log2;
   int32_t* dev_status;
   uint64_t wait_ns;
@@ -195,14 +222,16 @@ struct ScheduleParams {
   Header* header;
   int4* seqs;             // [batch]: first query, queries, first key, keys
   int32_t* tile0;         // [batch] first tile of each sequence
+  int64_t* cost0;         // [tiles] cost of the tiles before (ranges)
   Entry* entries;
-  int32_t* tickets;
-  int32_t total_q, total_k, batch, tile_tokens, head_groups, workers, bin_shift, by_head;
-  int32_t max_slots, max_entries;
+  int32_t* first;         // [workers + 1]
+  Cut* cuts;
+  int32_t total_q, total_k, batch, tile_tokens, workers, bin_shift;
+  int32_t mode, round_groups;   // head groups of a round
   int32_t* dev_status;
 };
 
-// Inclusive scans over the block of a maximum (two at once) and of a sum.
+// Inclusive scans over a warp.
 __device__ __forceinline__ int32_t warp_scan_max(int32_t x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -239,18 +268,19 @@ __device__ __forceinline__ Entry tile_entry(const int4& s, int32_t tile, int32_t
   e.lim0 = at + s.w - s.y;
   e.b0 = 0;
   e.n = blocks_of(e.lim0, e.ntok);
-  e.split = -1;
-  e.part = 0;
+  e.slot = -1;
+  e.hg = 0;
   return e;
 }
 
 __global__ void __launch_bounds__(kScheduleThreads)
     schedule_kernel(const __grid_constant__ ScheduleParams p) {
+  __shared__ int4 seqs_s[kSeqShared];
   __shared__ int32_t tile0_s[kSeqShared];
   __shared__ int32_t bins[kBins];
   __shared__ int32_t wq[32], wk[32], wt[32];
-  __shared__ unsigned long long total;
-  __shared__ int32_t slots, extra;
+  __shared__ long long wc[32];
+  __shared__ int32_t slots, cuts;
   launch_dependents();
   wait_dependency();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -258,11 +288,11 @@ __global__ void __launch_bounds__(kScheduleThreads)
   int32_t carry_q = clamp_to(p.cu_q[0], p.total_q), carry_k = clamp_to(p.cu_k[0], p.total_k);
   int32_t carry_t = 0;
   bool bad = p.cu_q[0] != carry_q || p.cu_k[0] != carry_k;
-  if (tid == 0) {
-    total = 0;
-    slots = extra = 0;
-  }
+  if (tid == 0) slots = cuts = 0;
   bins[tid] = 0;
+  const bool near = p.batch <= kSeqShared;
+  int4* seqs = near ? seqs_s : p.seqs;
+  int32_t* tile0 = near ? tile0_s : p.tile0;
   for (int32_t base = 0; base < p.batch; base += kScheduleThreads) {
     const int32_t s = base + tid;
     int32_t q = 0, k = 0;
@@ -278,15 +308,16 @@ __global__ void __launch_bounds__(kScheduleThreads)
       wk[warp] = mk;
     }
     __syncthreads();
-    int32_t before_q = carry_q, before_k = carry_k, top_q = carry_q, top_k = carry_k;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) {
-        before_q = max(before_q, wq[w]);
-        before_k = max(before_k, wk[w]);
-      }
-      top_q = max(top_q, wq[w]);
-      top_k = max(top_k, wk[w]);
+    const int32_t aq = max(warp_scan_max(wq[lane], lane), carry_q);
+    const int32_t ak = max(warp_scan_max(wk[lane], lane), carry_k);
+    int32_t before_q = __shfl_sync(0xffffffffu, aq, warp ? warp - 1 : 0);
+    int32_t before_k = __shfl_sync(0xffffffffu, ak, warp ? warp - 1 : 0);
+    if (warp == 0) {
+      before_q = carry_q;
+      before_k = carry_k;
     }
+    const int32_t top_q = __shfl_sync(0xffffffffu, aq, 31);
+    const int32_t top_k = __shfl_sync(0xffffffffu, ak, 31);
     mq = max(mq, before_q);
     mk = max(mk, before_k);
     int32_t q0 = __shfl_up_sync(0xffffffffu, mq, 1), k0 = __shfl_up_sync(0xffffffffu, mk, 1);
@@ -300,16 +331,13 @@ __global__ void __launch_bounds__(kScheduleThreads)
     const int32_t st = warp_scan_sum(tiles, lane);
     if (lane == 31) wt[warp] = st;
     __syncthreads();
-    int32_t before_t = carry_t, all_t = carry_t;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before_t += wt[w];
-      all_t += wt[w];
-    }
+    const int32_t at = warp_scan_sum(wt[lane], lane) + carry_t;
+    int32_t before_t = __shfl_sync(0xffffffffu, at, warp ? warp - 1 : 0);
+    if (warp == 0) before_t = carry_t;
+    const int32_t all_t = __shfl_sync(0xffffffffu, at, 31);
     if (s < p.batch) {
-      p.seqs[s] = make_int4(q0, nq, k0, mk - k0);
-      const int32_t first = before_t + st - tiles;
-      p.tile0[s] = first;
-      if (s < kSeqShared) tile0_s[s] = first;
+      seqs[s] = make_int4(q0, nq, k0, mk - k0);
+      tile0[s] = before_t + st - tiles;
     }
     carry_q = top_q;
     carry_k = top_k;
@@ -318,61 +346,191 @@ __global__ void __launch_bounds__(kScheduleThreads)
   }
   if (bad) atomicOr(p.dev_status, SA_DEV_BAD_COUNT);
   const int32_t tiles = carry_t;
-  const int32_t* tile0 = p.batch <= kSeqShared ? tile0_s : p.tile0;
   auto entry = [&](int32_t t) {
     const int32_t s = seq_of_tile(tile0, p.batch, t);
-    return tile_entry(p.seqs[s], t - tile0[s], p.tile_tokens);
+    return tile_entry(seqs[s], t - tile0[s], p.tile_tokens);
   };
-  // a processor's share of all blocks
-  unsigned long long mine = 0;
-  for (int32_t t = tid; t < tiles; t += kScheduleThreads) mine += unsigned(entry(t).n);
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0 && mine) atomicAdd(&total, mine);
-  __syncthreads();
-  const unsigned long long share =
-      (total * unsigned(p.head_groups) + unsigned(p.workers) - 1) / unsigned(p.workers);
-  const int32_t range = int32_t(max(share, (unsigned long long)kMinRange));
-  auto ranges_of = [&](int32_t n) { return n > range ? (n + range - 1) / range : 1; };
-  // longest first: a counting sort by the blocks of a tile's ranges
-  auto bin_of = [&](int32_t n) { return kBins - 1 - min(n >> p.bin_shift, kBins - 1); };
-  for (int32_t t = tid; t < tiles; t += kScheduleThreads) {
-    const int32_t n = entry(t).n, r = ranges_of(n);
-    atomicAdd(&bins[bin_of((n + r - 1) / r)], r);
-  }
-  __syncthreads();
-  {
-    const int32_t mine_n = bins[tid];
-    const int32_t sc = warp_scan_sum(mine_n, lane);
-    if (lane == 31) wt[warp] = sc;
+  // exclusive scan of one value a thread, and its total
+  auto scan_block = [&](int64_t x, int64_t* all) -> int64_t {
+    int64_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    if (lane == 31) wc[warp] = y;
     __syncthreads();
-    int32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += wt[w];
-    bins[tid] = before + sc - mine_n;
+    int64_t w = wc[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += z;
+    }
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+    *all = __shfl_sync(0xffffffffu, w, 31);
+    __syncthreads();
+    return (warp ? before : 0) + y - x;
+  };
+
+  if (p.mode == kTiles) {
+    // most blocks first: a counting sort of the tiles
+    auto bin_of = [&](int32_t n) { return kBins - 1 - min(n >> p.bin_shift, kBins - 1); };
+    Entry mine[kTileRegs];
+#pragma unroll
+    for (int i = 0; i < kTileRegs; ++i) {
+      const int32_t t = tid + i * kScheduleThreads;
+      if (t < tiles) {
+        mine[i] = entry(t);
+        atomicAdd(&bins[bin_of(mine[i].n)], 1);
+      }
+    }
+    for (int32_t t = tid + kTileRegs * kScheduleThreads; t < tiles; t += kScheduleThreads)
+      atomicAdd(&bins[bin_of(entry(t).n)], 1);
+    __syncthreads();
+    int64_t all;
+    const int64_t at = scan_block(bins[tid], &all);
+    bins[tid] = int32_t(at);
+    __syncthreads();
+    auto put = [&](const Entry& e) { p.entries[atomicAdd(&bins[bin_of(e.n)], 1)] = e; };
+#pragma unroll
+    for (int i = 0; i < kTileRegs; ++i)
+      if (tid + i * kScheduleThreads < tiles) put(mine[i]);
+    for (int32_t t = tid + kTileRegs * kScheduleThreads; t < tiles; t += kScheduleThreads)
+      put(entry(t));
+    if (tid == 0) *p.header = Header{0, tiles, 0};
+    return;
+  }
+
+  // Ranges: the blocks of a round's tiles (head groups one behind the other),
+  // an item's cost before each tile's, in equal shares.  A share's end inside a
+  // tile cuts it, unless one side would have few blocks.
+  int64_t cost = 0;
+  for (int32_t base = 0; base < tiles; base += kScheduleThreads) {
+    const int32_t t = base + tid;
+    int64_t all;
+    const int64_t before = scan_block(t < tiles ? entry(t).n + kItemCost : 0, &all);
+    if (t < tiles) p.cost0[t] = cost + before;
+    cost += all;
   }
   __syncthreads();
-  for (int32_t t = tid; t < tiles; t += kScheduleThreads) {
-    Entry e = entry(t);
-    const int32_t n = e.n, r = ranges_of(n);
-    const int32_t at = atomicAdd(&bins[bin_of((n + r - 1) / r)], r);
-    if (r > 1) {
-      e.split = atomicAdd(&slots, r);
-      atomicAdd(&extra, r - 1);
+  const int64_t total = cost * p.round_groups;
+  const int64_t share = max((total + p.workers - 1) / p.workers, int64_t(2 * kItemCost + 2));
+  const int32_t least = int32_t(min(share / 8 + 1, int64_t(4)));
+  // first block of tile [at, at + n + kItemCost) that belongs to share k or a later one
+  auto cut_at = [&](int64_t at, int32_t n, int64_t k) -> int32_t {
+    const int64_t b = k * share - at - kItemCost;
+    return b < least ? 0 : n - b < least ? n : int32_t(b);
+  };
+  int64_t placed = 0;
+  const int64_t virt = int64_t(tiles) * p.round_groups;
+  for (int64_t base = 0; base < virt; base += kScheduleThreads) {
+    const int64_t v = base + tid;
+    Entry e;
+    int32_t n = 0, ranges = 0;
+    int64_t at = 0, k0 = 0, k1 = -1;
+    if (v < virt) {
+      const int32_t hg = int32_t(v / tiles), t = int32_t(v - int64_t(hg) * tiles);
+      e = entry(t);
+      e.hg = hg;
+      n = e.n;
+      at = hg * cost + p.cost0[t];
+      k0 = at / share;
+      k1 = (at + n + kItemCost - 1) / share;
+      for (int64_t k = k0; k <= k1; ++k) {
+        const int32_t from = k == k0 ? 0 : cut_at(at, n, k);
+        const int32_t to = k == k1 ? n : cut_at(at, n, k + 1);
+        ranges += to > from;
+      }
     }
-    for (int32_t i = 0; i < r; ++i) {
-      e.b0 = int32_t(int64_t(i) * n / r);
-      e.n = int32_t(int64_t(i + 1) * n / r) - e.b0;
-      e.part = i | r << 16;
-      // (always within: sum of ranges of cut tiles x head groups <= 2 workers)
-      if (at + i < p.max_entries) p.entries[at + i] = e;
-      if (e.split >= 0)
-        for (int32_t h = 0; h < p.head_groups; ++h) {
-          const int64_t x = int64_t(e.split + i) * p.head_groups + h;
-          if (x < p.max_slots) p.tickets[x] = 0;
-        }
+    int64_t all;
+    int64_t x = placed + scan_block(ranges, &all);
+    placed += all;
+    if (v < virt) {
+      int32_t slot = -1;
+      if (ranges > 1) {
+        slot = atomicAdd(&slots, ranges);
+        p.cuts[atomicAdd(&cuts, 1)] = Cut{e.q0, e.ntok, e.hg, slot, ranges, {0, 0, 0}};
+      }
+      for (int64_t k = k0; k <= k1; ++k) {
+        const int32_t from = k == k0 ? 0 : cut_at(at, n, k);
+        const int32_t to = k == k1 ? n : cut_at(at, n, k + 1);
+        if (to <= from) continue;
+        e.b0 = from;
+        e.n = to - from;
+        e.slot = slot < 0 ? -1 : slot++;
+        atomicAdd(&bins[k], 1);              // entries of share k
+        p.entries[x++] = e;
+      }
     }
   }
   __syncthreads();
-  if (tid == 0) *p.header = Header{0, min(tiles + extra, p.max_entries), p.by_head};
+  int64_t all;
+  const int64_t before = scan_block(tid < p.workers ? bins[tid] : 0, &all);
+  if (tid <= p.workers) p.first[tid] = int32_t(before);
+  if (tid == 0) *p.header = Header{0, tiles, cuts};
+}
+
+// Joins the ranges of the tiles that were cut, in key order: a range's weight is
+// 2^(m + log2 l), its output is divided by its own sum first, as that may be as
+// large as fp32 goes.
+struct JoinParams {
+  const Header* header;
+  const Cut* cuts;
+  const float4* part_o;
+  const float4* part_ml;
+  __nv_bfloat16* o;
+  float* lse;
+  int64_t o_st, o_sh;
+  int32_t Hq, tile_heads, rounds, round_groups, round_slots;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinParams p) {
+  launch_dependents();
+  wait_dependency();
+  constexpr int kUnits = kRows / kJoinRows;
+  const int64_t units = int64_t(__ldcg(&p.header->cuts)) * p.rounds * kUnits;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t c = u / kUnits;
+    const int32_t round = int32_t(c % p.rounds);
+    const Cut cut = p.cuts[c / p.rounds];
+    const int64_t slot0 = int64_t(round) * p.round_slots + cut.slot;
+    for (int x = threadIdx.x; x < kJoinRows * (D / 4); x += kJoinThreads) {
+      const int row = int(u % kUnits) * kJoinRows + x % kJoinRows, c4 = x / kJoinRows;
+      const int tok = row / p.tile_heads, head = row - tok * p.tile_heads;
+      if (tok >= cut.ntok) continue;
+      const float4* ml = p.part_ml + slot0 * kRows + row;
+      const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
+      float m = -INFINITY;
+      for (int32_t i = 0; i < cut.ranges; ++i) {
+        const float4 y = __ldcg(ml + int64_t(i) * kRows);
+        if (y.y != 0.f) m = fmaxf(m, y.x + log2f(y.y));
+      }
+      float l = 0.f, lx = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int32_t i = 0; i < cut.ranges; ++i) {
+        const float4 y = __ldcg(ml + int64_t(i) * kRows);
+        const float4 z = __ldcg(po + int64_t(i) * (D / 4) * kRows);
+        if (y.y == 0.f) continue;                  // sees no key of this range
+        const float w = ex2(y.x + log2f(y.y) - m), own = 1.f / y.y;
+        l += w;
+        lx = fmaf(w, y.z * own, lx);
+        acc.x = fmaf(w, z.x * own, acc.x);
+        acc.y = fmaf(w, z.y * own, acc.y);
+        acc.z = fmaf(w, z.z * own, acc.z);
+        acc.w = fmaf(w, z.w * own, acc.w);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // sees no key at all: 0
+      const int64_t t = int64_t(cut.q0) + tok;
+      const int32_t h = (round * p.round_groups + cut.hg) * p.tile_heads + head;
+      const uint2 out = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                   pack_bf16x2(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = out;
+      if (p.lse && c4 == 0)
+        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
+    }
+  }
 }
 
 // A direct CTA's tile: the warp walks the sequences.  False: there is none.
@@ -451,7 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->q_full[s], 1);
       mbar_init(&sh->q_empty[s], 2);   // the last Q K^T, and the output tile leaving the stage
-      mbar_init(&sh->stage_bar[s], kSoftmaxThreads);
+      mbar_init(&sh->sum_full[s], kSoftmaxThreads);
+      mbar_init(&sh->sum_empty[s], kOutThreads);
+      mbar_init(&sh->stage_bar[s], kOutThreads);
     }
     for (int s = 0; s < C::kNK; ++s) {
       mbar_init(&sh->k_full[s], 1);
@@ -466,21 +626,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kNI; ++s) {
       mbar_init(&sh->info_full[s], 1);
-      mbar_init(&sh->info_empty[s], 3 + kSoftmaxThreads / 32);
+      mbar_init(&sh->info_empty[s], 3 + (kSoftmaxThreads + kOutThreads) / 32);
     }
     mbar_init(&sh->o_last, 1);
-    mbar_init(&sh->o_free, kSoftmaxThreads);
+    mbar_init(&sh->o_free, kOutThreads);
     mbar_init(&sh->xch_bar, kSoftmaxThreads);
-    mbar_init(&sh->part_bar, kSoftmaxThreads);
-    mbar_init(&sh->tick_bar, 1);
-    mbar_init(&sh->batch_done, kSoftmaxThreads);
+    mbar_init(&sh->batch_done, kOutThreads);
     mbar_init(&sh->drain_qk, 1);
     mbar_init(&sh->drain_pv, 1);
     sh->abort = 0;
     sh->bad_v[0] = sh->bad_v[1] = 0;
     fence_mbar_init();
   }
-  for (int x = threadIdx.x; x < kBatch / 32; x += kThreads) sh->redo[x] = 0;
+  for (int x = threadIdx.x; x < kBatch / 32; x += kThreads) sh->again[x] = sh->maxima[x] = 0;
   if (warp == 1) {
     tmem_alloc(&sh->tmem_base, C::kTmemCols);
     tmem_relinquish();
@@ -491,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------- producer: items, Q, K
+    registers_dec<kControlRegs>();
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
@@ -502,9 +661,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ii = 0, qi = 0, kiss = 0;   // descriptions, items and K blocks so far
     bool ok = true;
     wait_dependency();                   // the schedule, and what the inputs come from
-    const int32_t entries = p.direct ? 0 : __ldcg(&p.header->entries);
-    const bool by_head = p.direct ? false : __ldcg(&p.header->by_head) != 0;
-    const int64_t items = p.direct ? int64_t(gridDim.x) : int64_t(entries) * p.head_groups;
+    // items: the direct CTA's tile, places in the list of tiles times head groups,
+    // or the entries of this CTA's share, round by round
+    const int32_t entries = p.mode == kTiles ? __ldcg(&p.header->entries) : 0;
+    int32_t from = 0, to = 0;
+    if (p.mode == kRanges) {
+      from = __ldcg(&p.first[blockIdx.x]);
+      to = __ldcg(&p.first[blockIdx.x + 1]);
+    }
+    const int64_t items = p.mode == kDirect   ? int64_t(gridDim.x)
+                          : p.mode == kTiles ? int64_t(entries) * p.head_groups
+                                             : int64_t(to - from) * p.rounds;
 
     // room for a description in the ring; lane 0 then fills it
     auto slot_free = [&]() -> bool {
@@ -532,12 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto run_item = [&](int32_t id, int32_t pos, int32_t careful) -> bool {
       int32_t hg, x;
       Entry e;
-      if (p.direct) {
+      if (p.mode == kDirect) {
         hg = id % p.head_groups;
         x = id / p.head_groups;
         if (!find_tile(p, x, lane, &e)) return true;
       } else {
-        if (by_head) {
+        if (p.mode == kRanges) {
+          hg = id / (to - from);             // the round
+          x = from + id - hg * (to - from);
+        } else if (p.by_head) {
           hg = id / entries;
           x = id - hg * entries;
         } else {
@@ -547,6 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int4* at = reinterpret_cast<const int4*>(&p.entries[x]);
         const int4 lo = __ldcg(at), hi = __ldcg(at + 1);
         e = Entry{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (p.mode == kRanges) {
+          if (e.slot >= 0) e.slot += hg * p.round_slots;
+          hg = hg * p.round_groups + e.hg;
+        }
       }
       const int32_t head0 = hg * p.tile_heads, g = head0 / p.group;
       bool good = true;
@@ -557,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.e = e;
           it.head0 = head0;
           it.g = g;
-          it.hg = hg;
           it.mt = max(0, (e.lim0 + 1) / kBK - e.b0);
           it.pos = pos;
           it.careful = careful;
@@ -579,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (good) {
-          const int32_t blocks = careful ? 2 * e.n : e.n;
+          const int32_t blocks = careful & kMaxima ? 2 * e.n : e.n;
           for (int32_t t = 0; t < blocks; ++t) {
             const int32_t j = e.b0 + (t >= e.n ? t - e.n : t);
             const uint32_t ks = kiss % C::kNK;
@@ -601,7 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __shfl_sync(0xffffffffu, good, 0);
     };
 
-    int64_t id = blockIdx.x;
+    const bool counted = p.mode == kTiles;
+    int64_t id = p.mode == kRanges ? 0 : int64_t(blockIdx.x);
     uint32_t batches = 0;
     while (ok && id < items) {
       // a batch of items, then those of them that are to be done again
@@ -609,24 +783,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; pos < kBatch && id < items; ++pos) {
         int32_t next = 0;
         if (lane == 0) {
-          if (!p.direct) next = atomicAdd(p.counter, 1);
+          if (counted) next = atomicAdd(p.counter, 1);
           sh->ids[pos] = int32_t(id);
         }
         ok = run_item(int32_t(id), pos, 0);
         if (!ok) break;
-        id = p.direct ? items : int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
+        id = counted              ? int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0)
+             : p.mode == kRanges ? id + 1
+                                  : items;
       }
       if (ok) ok = special(kMarker);
       if (ok) ok = warp_wait(&sh->batch_done, batches & 1, abort, p.wait_ns);
       ++batches;
       for (int32_t w = 0; ok && w < (pos + 31) / 32; ++w) {
-        uint32_t bits = *(volatile uint32_t*)&sh->redo[w];
+        uint32_t bits = *(volatile uint32_t*)&sh->again[w];
+        const uint32_t maxima = *(volatile uint32_t*)&sh->maxima[w];
         __syncwarp();
-        if (lane == 0) sh->redo[w] = 0;
+        if (lane == 0) sh->again[w] = sh->maxima[w] = 0;
         while (ok && bits) {
-          const int32_t at = 32 * w + __ffs(bits) - 1;
+          const int at = __ffs(bits) - 1;
           bits &= bits - 1;
-          ok = run_item(*(volatile int32_t*)&sh->ids[at], at, 1);
+          ok = run_item(*(volatile int32_t*)&sh->ids[32 * w + at], 32 * w + at,
+                        kClean | ((maxima >> at) & 1 ? kMaxima : 0));
         }
       }
     }
@@ -639,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------- producer: V
+    registers_dec<kControlRegs>();
     const uint64_t pol_kv = l2_policy_evict_last();
     uint32_t ii = 0, viss = 0;
     bool ok = true;
@@ -678,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------- Q K^T issuer
+    registers_dec<kControlRegs>();
     constexpr uint32_t idesc_qk = idesc_bf16(kRows, kBK, 0, 0);
     uint32_t ii = 0, qi = 0, stage = 0, phase = 0, kb = 0, kst = 0, kph = 0;
     bool ok = true;
@@ -692,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
       if (n == kEnd) break;
       if (n == kMarker) continue;
-      const int32_t blocks = careful ? 2 * n : n;
+      const int32_t blocks = careful & kMaxima ? 2 * n : n;
       const uint32_t qs = qi % C::kNQ;
       if (!warp_wait(&sh->q_full[qs], (qi / C::kNQ) & 1, abort, p.wait_ns)) {
         ok = false;
@@ -754,18 +934,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 3) {
     // ------------------------------------------------- P V issuer
+    registers_dec<kControlRegs>();
     constexpr uint32_t idesc_pv = idesc_bf16(kRows, D, 0, 1);   // P (TMEM), V MN-major
     uint32_t ii = 0, qi = 0, stage = 0, phase = 0, vstage = 0, vphase = 0;
     bool ok = true;
     // This warp also writes the staged output tiles, one TMA store per panel,
-    // and releases their Q stages, while it would wait for P.  Item x is staged
-    // after the first block of item x+1, so it is stored before block 1 of item
-    // x+1 (or the first block of item x+2).  Item x+1 may be staged before this
-    // warp has looked at item x, item x+2 not: two barriers in turn.
+    // and releases their Q stages, while it would wait for P.  Item x must be
+    // stored before P V of item x+2 is issued (then no output warp can be two
+    // items ahead on the same barrier); until then it is looked for between blocks.
     uint32_t spq = 0;
-    auto store_upto = [&](uint32_t upto) -> bool {
+    auto store_upto = [&](uint32_t upto, bool wait) -> bool {
       for (; spq < upto; ++spq) {
-        if (!warp_wait(&sh->stage_bar[spq & 1], (spq >> 1) & 1, abort, p.wait_ns)) return false;
+        uint64_t* bar = &sh->stage_bar[spq & 1];
+        const uint32_t par = (spq >> 1) & 1;
+        if (!wait && !__shfl_sync(0xffffffffu, lane == 0 && mbar_test(bar, par), 0)) return true;
+        if (wait && !warp_wait(bar, par, abort, p.wait_ns)) return false;
         if (lane == 0) {
           const int32_t q0 = sh->stage_q0[spq & 1], h0 = sh->stage_h[spq & 1];
           if (q0 >= 0) {
@@ -790,21 +973,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const int32_t n = sh->info[slot].e.n;
-      const int32_t lead = sh->info[slot].careful ? n : 0;   // blocks without P V
+      const int32_t lead = sh->info[slot].careful & kMaxima ? n : 0;   // blocks without P V
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
       if (n == kEnd) break;
       if (n == kMarker) {
         // every tile before it is stored, and complete before a careful item
         // may write its rows again
-        ok = store_upto(qi);
+        ok = store_upto(qi, true);
         if (!ok) break;
         if (lane == 0) bulk_wait_all();
         __syncwarp();
         continue;
       }
       for (int32_t t = 0; t < lead + n; ++t) {
-        if (!store_upto(t == 0 ? (qi > 0 ? qi - 1 : 0) : qi)) {
+        if (!(t == 0 && qi > 0 ? store_upto(qi - 1, true) : store_upto(qi, false))) {
           ok = false;
           break;
         }
@@ -869,23 +1052,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++qi;
     }
-    if (ok) ok = store_upto(qi);
+    if (ok) ok = store_upto(qi, true);
     if (lane == 0) {
       if (!ok) raise_abort(sh, p);
       bulk_wait_all();   // the stores read this CTA's shared memory
       mma_commit(&sh->drain_pv);
       mbar_wait(&sh->drain_pv, 0, nullptr);
     }
-  } else {
+  } else if (warp < 20) {
     // ------------------------------------------------- softmax groups
     const int grp = (warp - 4) >> 2;              // column group 0..3
     const int quarter = warp & 3;                 // TMEM lane quarter of this warp
     const int row = quarter * 32 + lane;
-    const int tok = row / p.tile_heads;           // token and head of this row's query
-    const int head = row - tok * p.tile_heads;
-    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const int tok = row / p.tile_heads;           // token of this row's query
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + grp * C::kCols;
     const float c = p.scale_log2;
-    uint32_t ii = 0, qi = 0, xn = 0, parts = 0;   // xn: uses of the exchange buffer
+    uint32_t ii = 0, qi = 0, xn = 0;              // xn: uses of the exchange buffer
     uint32_t sst = 0, sph = 0, vb = 0;            // S ring; V blocks
     bool ok = true;
 
@@ -915,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_s = [&](float (&s)[C::kCols]) {
       uint32_t sr[32];
       static_assert(C::kCols == 32, "group width");
-      tmem_ld32(lanes + sst * kBK + grp * C::kCols, sr);
+      tmem_ld32(lanes + sst * kBK, sr);
       tmem_ld_wait(sr);
 #pragma unroll
       for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(sr[x]);
@@ -926,12 +1108,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         sph ^= 1u;
       }
     };
-    // Infinities and NaN of V blocks that the mask cuts become 0 in shared
+    // Infinities and NaN of a V block that the mask cuts become 0 in shared
     // memory (this thread's share of the stage); the item is marked.
     auto clean_v = [&](uint32_t item) {
       uint8_t* stage = sV + (vb % C::kNV) * C::kKVBytes;
       const int x = (warp - 4) * 32 + lane;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < C::kKVBytes / 16 / kSoftmaxThreads; ++i) {
         uint4* at = reinterpret_cast<uint4*>(stage) + x + i * kSoftmaxThreads;
         uint4 w = *at;
@@ -947,206 +1129,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
 
-    // An item's epilogue runs after the next item's first block: by then its
-    // last P V has finished, and that item's first P V waits for the release of
-    // O as before.  Its description stays in the ring until then.
-    bool pend = false;
-    uint32_t pslot = 0, pq = 0;
-    float pl = 0.f, plx = 0.f, pm = 0.f;
-    auto epilogue = [&]() -> bool {
-      float* xb = &sh->xch[xn & 1][0][0];
-      float* xl = &sh->xch_l[xn & 1][0][0];
-      xb[grp * 128 + row] = pl;
-      if (kLse) xl[grp * 128 + row] = plx;
-      mbar_arrive(&sh->xch_bar);
-      if (!wait_all(&sh->o_last, pq & 1, abort, p.wait_ns)) return false;
-      tc_fence_after();
-      uint32_t r[C::kOCols];
-      if constexpr (C::kOCols == 32) {
-        tmem_ld32(lanes + C::kO + grp * C::kOCols, r);
-      } else {
-        tmem_ld16(lanes + C::kO + grp * C::kOCols, r);
-      }
-      tmem_ld_wait(r);
-      tc_fence_before();
-      mbar_arrive(&sh->o_free);
-      if (!wait_all(&sh->xch_bar, xn & 1, abort, p.wait_ns)) return false;
-      ++xn;
-      const Item& it = sh->info[pslot];
-      float l = (xb[row] + xb[128 + row]) + (xb[256 + row] + xb[384 + row]);
-      float lx = kLse ? (xl[row] + xl[128 + row]) + (xl[256 + row] + xl[384 + row]) : 0.f;
-      const int32_t lim = it.e.lim0 + tok;
-      const bool live = tok < it.e.ntok;                     // a query of the tile
-      const bool some = lim >= it.e.b0 * kBK;                // that sees a key of the range
-      const int col = grp * C::kOCols;
-      if (live && some && *(volatile int32_t*)&sh->bad_v[pq & 1] == int32_t(pq + 1)) {
-        // what clean_v took out of the values that this row sees
-        const __nv_bfloat16* v = p.v + it.g * p.v_sh + col;
-        const int32_t end = min(lim + 1, (it.e.b0 + it.e.n) * kBK);
-        for (int32_t u = (it.e.b0 + it.mt) * kBK; u < end; ++u) {
-          const __nv_bfloat16* vr = v + (int64_t(it.e.kbeg) + u) * p.v_st;
-#pragma unroll
-          for (int x = 0; x < C::kOCols; ++x) {
-            const float y = __bfloat162float(vr[x]);
-            if (!(fabsf(y) <= 3.4e38f)) r[x] = __float_as_uint(__uint_as_float(r[x]) + y);
-          }
-        }
-      }
-      // the range that the first pass keeps: the sum up to 2^126 (so that no
-      // weight overflowed) and O finite
-      float osum = 0.f;
-#pragma unroll
-      for (int x = 0; x < C::kOCols; ++x) osum += __uint_as_float(r[x]);
-      const bool keep = it.careful || !live || !some || (l <= 0x1p126f && fabsf(osum) <= 3.0e38f);
-      if (!keep) atomicOr(&sh->redo[it.pos >> 5], 1u << (it.pos & 31));
-      float m = pm;
-      if (!some) {
-        l = 1.f;
-        lx = 0.f;
-        m = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < C::kOCols; ++x) r[x] = 0u;
-      }
-      bool out = live;                                       // this row's result is in r, l, lx, m
-      if (it.e.split >= 0) {
-        // a range: its state goes to the workspace; the tile's last range joins
-        const int32_t ranges = it.e.part >> 16;
-        const int64_t slot0 = int64_t(it.e.split) * p.head_groups + it.hg;
-        const int64_t slot = slot0 + int64_t(it.e.part & 0xffff) * p.head_groups;
-        if (live) {
-          float4* po = reinterpret_cast<float4*>(p.part_o + (slot * kRows + row) * D + col);
-#pragma unroll
-          for (int x = 0; x < C::kOCols / 4; ++x)
-            po[x] = make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
-                                __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
-          if (grp == 0) p.part_ml[slot * kRows + row] = make_float4(m, some ? l : 0.f, lx, 0.f);
-        }
-        __threadfence();
-        mbar_arrive(&sh->part_bar);
-        if (warp == 4) {
-          if (!warp_wait(&sh->part_bar, parts & 1, abort, p.wait_ns)) return false;
-          if (lane == 0) {
-            const bool again =
-                (*(volatile uint32_t*)&sh->redo[it.pos >> 5] >> (it.pos & 31)) & 1u;
-            bool last = false;
-            if (!again) {
-              __threadfence();
-              last = atomicAdd(&p.tickets[slot0], 1) == ranges - 1;
-              __threadfence();
-            }
-            *(volatile int32_t*)&sh->last = last;
-            mbar_arrive(&sh->tick_bar);
-          }
-          __syncwarp();
-        }
-        if (!wait_all(&sh->tick_bar, parts & 1, abort, p.wait_ns)) return false;
-        ++parts;
-        out = live && *(volatile int32_t*)&sh->last;
-        if (out) {
-          __threadfence();
-          // a range's weight is 2^(m + log2 l); its output is divided by its own
-          // sum first, as that may be as large as fp32 goes
-          auto state = [&](int32_t i) {
-            return __ldcg(&p.part_ml[(slot0 + int64_t(i) * p.head_groups) * kRows + row]);
-          };
-          m = -INFINITY;
-          for (int32_t i = 0; i < ranges; ++i) {
-            const float4 ml = state(i);
-            if (ml.y != 0.f) m = fmaxf(m, ml.x + log2f(ml.y));
-          }
-          l = lx = 0.f;
-          float acc[C::kOCols];
-#pragma unroll
-          for (int x = 0; x < C::kOCols; ++x) acc[x] = 0.f;
-          for (int32_t i = 0; i < ranges; ++i) {
-            const float4 ml = state(i);
-            if (ml.y == 0.f) continue;               // sees no key of this range
-            const float w = ex2(ml.x + log2f(ml.y) - m), own = 1.f / ml.y;
-            l += w;
-            lx = fmaf(w, ml.z * own, lx);
-            const float4* po = reinterpret_cast<const float4*>(
-                p.part_o + ((slot0 + int64_t(i) * p.head_groups) * kRows + row) * D + col);
-#pragma unroll
-            for (int x = 0; x < C::kOCols / 4; ++x) {
-              const float4 y = __ldcg(&po[x]);
-              acc[4 * x] = fmaf(w, y.x * own, acc[4 * x]);
-              acc[4 * x + 1] = fmaf(w, y.y * own, acc[4 * x + 1]);
-              acc[4 * x + 2] = fmaf(w, y.z * own, acc[4 * x + 2]);
-              acc[4 * x + 3] = fmaf(w, y.w * own, acc[4 * x + 3]);
-            }
-          }
-          if (l == 0.f) l = 1.f;                     // sees no key at all: 0
-#pragma unroll
-          for (int x = 0; x < C::kOCols; ++x) r[x] = __float_as_uint(acc[x]);
-        }
-      }
-      if (kLse && out && grp == 0)
-        p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
-            m == -INFINITY ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
-      // A full tile is staged in its Q stage (128-byte swizzled, as TMA stores
-      // read it); rows of other tiles go out as they are
-      const float inv = 1.f / l;
-      const bool staged = it.e.split < 0 && it.e.ntok == p.tile_tokens;
-      if (out) {
-        uint4* direct = reinterpret_cast<uint4*>(
-            p.o + (int64_t(it.e.q0) + tok) * p.o_st + int64_t(it.head0 + head) * p.o_sh + col);
-        uint8_t* stg = sQ + (pq % C::kNQ) * C::kQBytes + row * 128;
-#pragma unroll
-        for (int x = 0; x < C::kOCols / 8; ++x) {
-          uint32_t ob[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            ob[y] = pack_bf16x2(__uint_as_float(r[8 * x + 2 * y]) * inv,
-                                __uint_as_float(r[8 * x + 2 * y + 1]) * inv);
-          const int c16 = (col + 8 * x) / 8, panel = c16 / 8, chunk = c16 % 8;
-          uint4* dst = staged ? reinterpret_cast<uint4*>(stg + panel * C::kQPanel +
-                                                         ((chunk ^ (row & 7)) << 4))
-                              : direct + x;
-          *dst = make_uint4(ob[0], ob[1], ob[2], ob[3]);
-        }
-      }
-      if (staged) fence_proxy_async_smem();
-      if (warp == 4 && lane == 0) {
-        sh->stage_q0[pq & 1] = staged ? it.e.q0 : -1;
-        sh->stage_h[pq & 1] = it.head0;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->info_empty[pslot]);
-      mbar_arrive(&sh->stage_bar[pq & 1]);   // the P V issuer goes on from here
-      return true;
-    };
-
     for (;; ++ii) {
       const uint32_t slot = ii % kNI;
       if (!wait_all(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
         ok = false;
         break;
       }
-      const int32_t n = sh->info[slot].e.n;
-      if (n <= 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
-        if (n == kEnd) break;
-        if (pend && !epilogue()) {
-          ok = false;
-          break;
-        }
-        pend = false;
-        mbar_arrive(&sh->batch_done);
-        continue;
-      }
-      const int32_t mt = sh->info[slot].mt;
+      const int32_t n = sh->info[slot].e.n, mt = sh->info[slot].mt;
       // last visible column of this thread's quarter of the first block
-      int32_t vis0 = sh->info[slot].e.lim0 + tok - sh->info[slot].e.b0 * kBK - grp * C::kCols;
-      const bool careful = sh->info[slot].careful != 0;
+      const int32_t vis0 =
+          sh->info[slot].e.lim0 + tok - sh->info[slot].e.b0 * kBK - grp * C::kCols;
+      const int32_t careful = sh->info[slot].careful;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+      if (n == kEnd) break;
+      if (n == kMarker) continue;
       float m_used = -INFINITY;
-      if (careful) {
+      if (careful & kMaxima) {
         // the rows' maxima over all blocks, without P V
-        if (pend && !epilogue()) {
-          ok = false;
-          break;
-        }
-        pend = false;
         float mx = -INFINITY;
         for (int32_t t = 0; t < n; ++t) {
           if (!wait_all(&sh->s_full[sst], sph, abort, p.wait_ns)) {
@@ -1187,14 +1187,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < C::kCols; ++x)
             if (x > vis) s[x] = -INFINITY;
-          if (!wait_all(&sh->v_full[vb % C::kNV], (vb / C::kNV) & 1, abort, p.wait_ns)) {
-            ok = false;
-            break;
+          if (careful) {
+            if (!wait_all(&sh->v_full[vb % C::kNV], (vb / C::kNV) & 1, abort, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            clean_v(qi);
           }
-          clean_v(qi);
         }
         ++vb;
-        if (t == 0 && !careful) {
+        if (t == 0 && !(careful & kMaxima)) {
           if (!exchange_max(row_max(s), &m_used)) {
             ok = false;
             break;
@@ -1219,34 +1221,175 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (kLse) add2(x0, x1, a0, a1);
             }
           }
-          tmem_st16(lanes + sst * kBK + grp * C::kCols, pk);
+          tmem_st16(lanes + sst * kBK, pk);
         }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sh->p_full[sst]);
         next_s();
-        if (t == 0 && pend) {
-          if (!epilogue()) {
-            ok = false;
-            break;
-          }
-          pend = false;
-        }
       }
       if (!ok) break;
-      pend = true;
-      pslot = slot;
-      pl = (sum0 + sum1) + (sum2 + sum3);
-      plx = (x0 + x1) + (x2 + x3);
-      pm = m_used;
-      pq = qi;
+      // the sums of this item, once the output warps have read those of the
+      // item before the last
+      const uint32_t w = qi & 1;
+      if (qi >= 2 && !wait_all(&sh->sum_empty[w], ((qi >> 1) - 1) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      sh->sum[w][grp][row] = (sum0 + sum1) + (sum2 + sum3);
+      if (kLse) sh->sum_x[w][grp][row] = (x0 + x1) + (x2 + x3);
+      if (grp == 0) sh->ref[w][row] = m_used;
+      mbar_arrive(&sh->sum_full[w]);
       ++qi;
     }
-    if (ok && pend) ok = epilogue();
     if (!ok) raise_abort(sh, p);
     // a role that gave up may have left a tensor-memory access in flight
     tmem_ld_wait();
     tmem_st_wait();
+    tc_fence_before();
+  } else {
+    // ------------------------------------------------- output
+    registers_inc<kOutRegs>();
+    const int row = (warp & 3) * 32 + lane;       // a thread's row, whole
+    const int tok = row / p.tile_heads;
+    const int head = row - tok * p.tile_heads;
+    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + C::kO;
+    uint32_t ii = 0, qi = 0;
+    bool ok = true;
+    for (;; ++ii) {
+      const uint32_t slot = ii % kNI;
+      if (!wait_all(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const Item& it = sh->info[slot];            // released at the end
+      const int32_t n = it.e.n;
+      if (n <= 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+        if (n == kEnd) break;
+        mbar_arrive(&sh->batch_done);
+        continue;
+      }
+      const uint32_t w = qi & 1;
+      if (!wait_all(&sh->sum_full[w], (qi >> 1) & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      float l = (sh->sum[w][0][row] + sh->sum[w][1][row]) +
+                (sh->sum[w][2][row] + sh->sum[w][3][row]);
+      float lx = kLse ? (sh->sum_x[w][0][row] + sh->sum_x[w][1][row]) +
+                            (sh->sum_x[w][2][row] + sh->sum_x[w][3][row])
+                      : 0.f;
+      float m = sh->ref[w][row];
+      mbar_arrive(&sh->sum_empty[w]);
+      const int32_t lim = it.e.lim0 + tok;
+      const bool live = tok < it.e.ntok;                     // a query of the tile
+      const bool some = lim >= it.e.b0 * kBK;                // that sees a key of the range
+      const bool whole = it.e.slot < 0;
+      const bool staged = whole && it.e.ntok == p.tile_tokens;
+      // (a NaN is not in range either)
+      const bool in_range = l <= 0x1p126f;
+      if (!some) {
+        l = whole ? 1.f : 0.f;
+        lx = 0.f;
+        m = -INFINITY;
+      }
+      const float inv = whole ? 1.f / l : 1.f;
+      __nv_bfloat16* direct = p.o + (int64_t(it.e.q0) + tok) * p.o_st +
+                              int64_t(it.head0 + head) * p.o_sh;
+      uint8_t* stg = sQ + (qi % C::kNQ) * C::kQBytes + row * 128;
+      float4* part = p.part_o + int64_t(whole ? 0 : it.e.slot) * (D / 4) * kRows + row;
+      float osum = 0.f;
+      // 32 columns of O: a full tile is staged in its Q stage (128-byte
+      // swizzled, as TMA stores read it), rows of other tiles go out as they are,
+      // ranges unnormalised and fp32 to their slot
+      auto emit = [&](uint32_t (&r)[32], int col) {
+        if (!some) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = 0u;
+        }
+        if (it.careful && live && some &&
+            *(volatile int32_t*)&sh->bad_v[w] == int32_t(qi + 1)) {
+          // what clean_v took out of the values that this row sees
+          const __nv_bfloat16* v = p.v + it.g * p.v_sh + col;
+          const int32_t end = min(lim + 1, (it.e.b0 + n) * kBK);
+          for (int32_t u = (it.e.b0 + it.mt) * kBK; u < end; ++u) {
+            const __nv_bfloat16* vr = v + (int64_t(it.e.kbeg) + u) * p.v_st;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float y = __bfloat162float(vr[x]);
+              if (!(fabsf(y) <= 3.4e38f)) r[x] = __float_as_uint(__uint_as_float(r[x]) + y);
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) osum += __uint_as_float(r[x]);
+        if (!live) return;
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            part[(col / 4 + x) * kRows] =
+                make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                            __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
+          return;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t ob[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            ob[y] = pack_bf16x2(__uint_as_float(r[8 * x + 2 * y]) * inv,
+                                __uint_as_float(r[8 * x + 2 * y + 1]) * inv);
+          const int c16 = col / 8 + x;
+          uint4* dst = staged ? reinterpret_cast<uint4*>(stg + c16 / 8 * C::kQPanel +
+                                                         ((c16 % 8 ^ (row & 7)) << 4))
+                              : reinterpret_cast<uint4*>(direct + col) + x;
+          *dst = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+      };
+      if (!wait_all(&sh->o_last, qi & 1, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int col = 0; col < D; col += 32) {
+        uint32_t r[32];
+        tmem_ld32(lanes + col, r);
+        tmem_ld_wait(r);
+        if (col == D - 32) {
+          // O is read: the next item's first P V may overwrite it
+          tc_fence_before();
+          mbar_arrive(&sh->o_free);
+        }
+        emit(r, col);
+      }
+      // the range that the first pass keeps: the sum up to 2^126 (so that no
+      // weight overflowed) and O finite
+      if (!it.careful && live && some && !(in_range && fabsf(osum) <= 3.0e38f)) {
+        const uint32_t bit = 1u << (it.pos & 31);
+        atomicOr(&sh->again[it.pos >> 5], bit);
+        if (!in_range) atomicOr(&sh->maxima[it.pos >> 5], bit);
+      }
+      if (!whole) {
+        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float4(m, l, lx, 0.f);
+      } else if (kLse && live) {
+        p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
+            some ? (m + log2f(lx)) * 0.6931471805599453f : -INFINITY;
+      }
+      if (staged) fence_proxy_async_smem();
+      if (row == 0) {
+        sh->stage_q0[w] = staged ? it.e.q0 : -1;
+        sh->stage_h[w] = it.head0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
+      mbar_arrive(&sh->stage_bar[w]);   // the P V issuer goes on from here
+      ++qi;
+    }
+    if (!ok) raise_abort(sh, p);
+    tmem_ld_wait();
     tc_fence_before();
   }
 
@@ -1298,30 +1441,65 @@ bool make_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t heads,
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Partial slots: cut tiles' ranges x head groups (at most two a processor).
-int64_t slots_of(int sms) { return 2 * int64_t(sms); }
+// CTAs that share the work (the schedule counts them in its bins).
+int workers_of(int sms) { return std::min(sms, kBins - 1); }
+
+// Tiles are cut where sequences have more keys than queries, on the whole: the
+// tiles of whole prompts have from one block to all, and taking the long ones
+// first leaves an even end.
+bool may_cut(const sa_packed_shape& s) { return s.total_k > s.total_q; }
 
 struct Layout {
-  size_t header, seqs, tile0, entries, tickets, part_ml, part_o, end;
-  int64_t max_entries;
+  size_t header, seqs, tile0, entries, cost0, first, cuts, part_ml, part_o, end;
+  int64_t max_entries, round_slots;
 };
 
 Layout layout_of(const sa_packed_shape& s, int sms) {
   Layout l;
-  l.max_entries = sa_packed::most_tiles(s) + slots_of(sms);
+  const int64_t tiles = sa_packed::most_tiles(s), workers = workers_of(sms);
+  l.max_entries = tiles * (s.num_q_heads / sa_packed::tile_of(s).heads) + 2 * workers;
+  l.round_slots = 2 * workers;        // a cut tile of r ranges takes r - 1 of the shares' ends
   l.header = 0;
-  l.tickets = up(sizeof(Header));
-  l.seqs = l.tickets + up(size_t(slots_of(sms)) * 4);
+  l.seqs = up(sizeof(Header));
   l.tile0 = l.seqs + up(size_t(s.batch) * 16);
   l.entries = l.tile0 + up(size_t(s.batch) * 4);
-  l.part_ml = l.entries + up(size_t(l.max_entries) * sizeof(Entry));
-  l.part_o = l.part_ml + up(size_t(slots_of(sms)) * kRows * 16);
-  l.end = l.part_o + up(size_t(slots_of(sms)) * kRows * size_t(s.head_dim) * 4);
+  l.cost0 = l.entries + up(size_t(l.max_entries) * sizeof(Entry));
+  l.first = l.cost0 + up(size_t(tiles) * 8);
+  l.cuts = l.first + up(size_t(workers + 1) * 4);
+  l.part_ml = l.cuts + up(size_t(workers) * sizeof(Cut));
+  l.part_o = l.part_ml + up(size_t(kRounds * l.round_slots) * kRows * 16);
+  l.end = l.part_o + up(size_t(kRounds * l.round_slots) * kRows * size_t(s.head_dim) * 4);
   return l;
 }
 
+// Rounds of head groups: as many as keep a round's keys and values within half of
+// L2, or about, but a divisor of the groups.
+int rounds_of(const sa_packed_shape& s, int64_t head_groups) {
+  const int64_t bytes = int64_t(s.total_k) * s.num_kv_heads * s.head_dim * 4;
+  int rounds = 1;
+  for (int r = 2; r <= kRounds && bytes / rounds > (int64_t(64) << 20); ++r)
+    if (head_groups % r == 0) rounds = r;
+  return rounds;
+}
+
+template <class Kernel, class... Params>
+cudaError_t launch_kernel(Kernel* kern, unsigned grid, int threads, int smem, cudaStream_t st,
+                          const Params&... params) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, params...);
+}
+
 template <int D, bool kLse>
-cudaError_t launch_attention(const Args& a, const Params& p, unsigned grid, const CUtensorMap& tq,
+cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& tq,
                              const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                              cudaStream_t st) {
   using C = Cfg<D>;
@@ -1331,17 +1509,7 @@ cudaError_t launch_attention(const Args& a, const Params& p, unsigned grid, cons
   auto kern = packed_attention_kernel<D, kLse>;
   cudaError_t e = sa_paged::allow_shared(kern, kSmem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, to, p);
+  return launch_kernel(kern, grid, kThreads, kSmem, st, tq, tk, tv, to, p);
 }
 
 template <int D>
@@ -1368,18 +1536,22 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
     *encode_failed = true;
     return cudaErrorInvalidValue;
   }
+  const bool ranges = may_cut(s);
+  const int workers = workers_of(sms);
+  const int rounds = ranges ? rounds_of(s, head_groups) : 1;
+  auto at = [&](size_t offset) { return static_cast<void*>(ws + offset); };
   Params p;
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k;
   p.v = static_cast<const __nv_bfloat16*>(a.v);
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
-  p.header = reinterpret_cast<const Header*>(ws + lay.header);
-  p.counter = &reinterpret_cast<Header*>(ws + lay.header)->counter;
-  p.entries = reinterpret_cast<const Entry*>(ws + lay.entries);
-  p.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets);
-  p.part_ml = reinterpret_cast<float4*>(ws + lay.part_ml);
-  p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+  p.header = static_cast<const Header*>(at(lay.header));
+  p.counter = &static_cast<Header*>(at(lay.header))->counter;
+  p.entries = static_cast<const Entry*>(at(lay.entries));
+  p.first = static_cast<const int32_t*>(at(lay.first));
+  p.part_ml = static_cast<float4*>(at(lay.part_ml));
+  p.part_o = static_cast<float4*>(at(lay.part_o));
   p.v_st = s.v_stride_t;
   p.v_sh = s.num_kv_heads > 1 ? s.v_stride_h : 0;
   p.o_st = s.o_stride_t;
@@ -1392,50 +1564,61 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   p.tile_heads = tile.heads;
   p.tile_tokens = tile.tokens;
   p.head_groups = int32_t(head_groups);
-  // every tile its own CTA, and no tile would be cut
-  p.direct = tiles * head_groups <= sms && key_blocks <= kMinRange;
+  // keys and values of all heads against half of L2
+  p.by_head = int64_t(s.total_k) * s.num_kv_heads * D * 4 > (int64_t(64) << 20);
+  p.rounds = rounds;
+  p.round_groups = int32_t(head_groups / rounds);
+  p.round_slots = int32_t(lay.round_slots);
   p.scale_log2 = float(double(s.scale) * 1.4426950408889634);
   p.dev_status = a.dev_status;
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
-  unsigned grid = unsigned(sms);
-  if (p.direct) {
-    grid = unsigned(tiles * head_groups);
-  } else {
-    ScheduleParams sp;
-    sp.cu_q = a.cu_q;
-    sp.cu_k = a.cu_k;
-    sp.header = reinterpret_cast<Header*>(ws + lay.header);
-    sp.seqs = reinterpret_cast<int4*>(ws + lay.seqs);
-    sp.tile0 = reinterpret_cast<int32_t*>(ws + lay.tile0);
-    sp.entries = reinterpret_cast<Entry*>(ws + lay.entries);
-    sp.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets);
-    sp.total_q = s.total_q;
-    sp.total_k = s.total_k;
-    sp.batch = s.batch;
-    sp.tile_tokens = tile.tokens;
-    sp.head_groups = int32_t(head_groups);
-    sp.workers = sms;
-    sp.bin_shift = 0;
-    while ((key_blocks >> sp.bin_shift) >= kBins) ++sp.bin_shift;
-    // keys and values of all heads against half of L2
-    sp.by_head = int64_t(s.total_k) * s.num_kv_heads * D * 4 > (int64_t(64) << 20);
-    sp.max_slots = int32_t(slots_of(sms));
-    sp.max_entries = int32_t(lay.max_entries);
-    sp.dev_status = a.dev_status;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(kScheduleThreads);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, schedule_kernel, sp);
-    if (e != cudaSuccess) return e;
+  // every tile its own CTA, none worth cutting
+  if (tiles * head_groups <= sms && (!ranges || key_blocks <= kDirectBlocks)) {
+    p.mode = kDirect;
+    return a.lse ? launch_attention<D, true>(p, unsigned(tiles * head_groups), tq, tk, tv, to, st)
+                 : launch_attention<D, false>(p, unsigned(tiles * head_groups), tq, tk, tv, to, st);
   }
-  return a.lse ? launch_attention<D, true>(a, p, grid, tq, tk, tv, to, st)
-               : launch_attention<D, false>(a, p, grid, tq, tk, tv, to, st);
+  p.mode = ranges ? kRanges : kTiles;
+  ScheduleParams sp;
+  sp.cu_q = a.cu_q;
+  sp.cu_k = a.cu_k;
+  sp.header = static_cast<Header*>(at(lay.header));
+  sp.seqs = static_cast<int4*>(at(lay.seqs));
+  sp.tile0 = static_cast<int32_t*>(at(lay.tile0));
+  sp.cost0 = static_cast<int64_t*>(at(lay.cost0));
+  sp.entries = static_cast<Entry*>(at(lay.entries));
+  sp.first = static_cast<int32_t*>(at(lay.first));
+  sp.cuts = static_cast<Cut*>(at(lay.cuts));
+  sp.total_q = s.total_q;
+  sp.total_k = s.total_k;
+  sp.batch = s.batch;
+  sp.tile_tokens = tile.tokens;
+  sp.workers = workers;
+  sp.bin_shift = 0;
+  while ((key_blocks >> sp.bin_shift) >= kBins) ++sp.bin_shift;
+  sp.mode = p.mode;
+  sp.round_groups = p.round_groups;
+  sp.dev_status = a.dev_status;
+  cudaError_t e = launch_kernel(schedule_kernel, 1, kScheduleThreads, 0, st, sp);
+  if (e != cudaSuccess) return e;
+  e = a.lse ? launch_attention<D, true>(p, unsigned(workers), tq, tk, tv, to, st)
+            : launch_attention<D, false>(p, unsigned(workers), tq, tk, tv, to, st);
+  if (e != cudaSuccess || !ranges) return e;
+  JoinParams jp;
+  jp.header = p.header;
+  jp.cuts = sp.cuts;
+  jp.part_o = p.part_o;
+  jp.part_ml = p.part_ml;
+  jp.o = p.o;
+  jp.lse = p.lse;
+  jp.o_st = p.o_st;
+  jp.o_sh = p.o_sh;
+  jp.Hq = p.Hq;
+  jp.tile_heads = p.tile_heads;
+  jp.rounds = p.rounds;
+  jp.round_groups = p.round_groups;
+  jp.round_slots = p.round_slots;
+  return launch_kernel(join_kernel<D>, unsigned(8 * workers), kJoinThreads, 0, st, jp);
 }
 
 }  // namespace

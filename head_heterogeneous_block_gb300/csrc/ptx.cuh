@@ -146,6 +146,17 @@ __device__ __forceinline__ void wait_dependency() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Registers of a thread from here on: every warp of the warpgroup gives some up,
+// or waits until it gets more.  All shares together may not pass the launch's.
+template <int kCount>
+__device__ __forceinline__ void registers_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+template <int kCount>
+__device__ __forceinline__ void registers_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
