@@ -76,7 +76,7 @@ constexpr int kThreads = 128 + kSoftmaxThreads + kOutThreads;
 constexpr int kNI = 4;                // item descriptions in flight
 constexpr int kBatch = 2048;          // items between two looks at what is to be done again
 constexpr int kDirectBlocks = 8;      // key blocks of a tile that is not worth cutting
-constexpr int kRounds = 4;            // of head groups, so that a round's keys and values stay in L2
+constexpr int kRounds = 8;            // at most, of head groups, so that a round's keys and values stay in L2
 constexpr int kItemCost = 2;          // what an item costs beside its blocks, in blocks
 constexpr int kBins = 1024;
 constexpr int kScheduleThreads = 1024;
@@ -87,7 +87,7 @@ constexpr int kJoinRows = 16;         // rows of a join unit
 
 // Registers of a thread by role, together the launch's 768 x 80: the control
 // warps give up what the output warps, a whole row each, need.
-constexpr int kControlRegs = 64, kSoftmaxRegs = 80, kOutRegs = 96;
+constexpr int kControlRegs = 56, kSoftmaxRegs = 72, kOutRegs = 136;
 static_assert(128 * kControlRegs + kSoftmaxThreads * kSoftmaxRegs + kOutThreads * kOutRegs <=
                   kThreads * 80,
               "a larger sum would wait forever");
@@ -156,6 +156,7 @@ struct Shared {
   uint64_t drain_qk, drain_pv;
   uint64_t info_full[kNI], info_empty[kNI];
   Item info[kNI];
+  Entry ahead[2];         // entries on their way
   int32_t ids[kBatch];    // items of the batch
   uint32_t again[kBatch / 32], maxima[kBatch / 32];   // to be done again; with true maxima
   float xch[2][4][kRows];
@@ -222,7 +223,7 @@ struct ScheduleParams {
   Header* header;
   int4* seqs;             // [batch]: first query, queries, first key, keys
   int32_t* tile0;         // [batch] first tile of each sequence
-  int64_t* cost0;         // [tiles] cost of the tiles before (ranges)
+  int32_t* cost0;         // [tiles] cost of the tiles before (ranges)
   Entry* entries;
   int32_t* first;         // [workers + 1]
   Cut* cuts;
@@ -279,7 +280,6 @@ __global__ void __launch_bounds__(kScheduleThreads)
   __shared__ int32_t tile0_s[kSeqShared];
   __shared__ int32_t bins[kBins];
   __shared__ int32_t wq[32], wk[32], wt[32];
-  __shared__ long long wc[32];
   __shared__ int32_t slots, cuts;
   launch_dependents();
   wait_dependency();
@@ -351,22 +351,12 @@ __global__ void __launch_bounds__(kScheduleThreads)
     return tile_entry(seqs[s], t - tile0[s], p.tile_tokens);
   };
   // exclusive scan of one value a thread, and its total
-  auto scan_block = [&](int64_t x, int64_t* all) -> int64_t {
-    int64_t y = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    if (lane == 31) wc[warp] = y;
+  auto scan_block = [&](int32_t x, int32_t* all) -> int32_t {
+    const int32_t y = warp_scan_sum(x, lane);
+    if (lane == 31) wt[warp] = y;
     __syncthreads();
-    int64_t w = wc[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += z;
-    }
-    const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+    const int32_t w = warp_scan_sum(wt[lane], lane);
+    const int32_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
     *all = __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
     return (warp ? before : 0) + y - x;
@@ -387,9 +377,8 @@ __global__ void __launch_bounds__(kScheduleThreads)
     for (int32_t t = tid + kTileRegs * kScheduleThreads; t < tiles; t += kScheduleThreads)
       atomicAdd(&bins[bin_of(entry(t).n)], 1);
     __syncthreads();
-    int64_t all;
-    const int64_t at = scan_block(bins[tid], &all);
-    bins[tid] = int32_t(at);
+    int32_t all;
+    bins[tid] = scan_block(bins[tid], &all);
     __syncthreads();
     auto put = [&](const Entry& e) { p.entries[atomicAdd(&bins[bin_of(e.n)], 1)] = e; };
 #pragma unroll
@@ -403,60 +392,58 @@ __global__ void __launch_bounds__(kScheduleThreads)
 
   // Ranges: the blocks of a round's tiles (head groups one behind the other),
   // an item's cost before each tile's, in equal shares.  A share's end inside a
-  // tile cuts it, unless one side would have few blocks.
-  int64_t cost = 0;
+  // tile cuts it, unless one side would have few blocks.  (All below 2^31.)
+  int32_t cost = 0;
   for (int32_t base = 0; base < tiles; base += kScheduleThreads) {
     const int32_t t = base + tid;
-    int64_t all;
-    const int64_t before = scan_block(t < tiles ? entry(t).n + kItemCost : 0, &all);
+    int32_t all;
+    const int32_t before = scan_block(t < tiles ? entry(t).n + kItemCost : 0, &all);
     if (t < tiles) p.cost0[t] = cost + before;
     cost += all;
   }
   __syncthreads();
-  const int64_t total = cost * p.round_groups;
-  const int64_t share = max((total + p.workers - 1) / p.workers, int64_t(2 * kItemCost + 2));
-  const int32_t least = int32_t(min(share / 8 + 1, int64_t(4)));
+  const int32_t share =
+      max((cost * p.round_groups + p.workers - 1) / p.workers, 2 * kItemCost + 2);
+  const int32_t least = min(share / 8 + 1, 4);
   // first block of tile [at, at + n + kItemCost) that belongs to share k or a later one
-  auto cut_at = [&](int64_t at, int32_t n, int64_t k) -> int32_t {
-    const int64_t b = k * share - at - kItemCost;
-    return b < least ? 0 : n - b < least ? n : int32_t(b);
+  auto cut_at = [&](int32_t at, int32_t n, int32_t k) -> int32_t {
+    const int32_t b = k * share - at - kItemCost;
+    return b < least ? 0 : n - b < least ? n : b;
   };
-  int64_t placed = 0;
-  const int64_t virt = int64_t(tiles) * p.round_groups;
-  for (int64_t base = 0; base < virt; base += kScheduleThreads) {
-    const int64_t v = base + tid;
-    Entry e;
-    int32_t n = 0, ranges = 0;
-    int64_t at = 0, k0 = 0, k1 = -1;
-    if (v < virt) {
-      const int32_t hg = int32_t(v / tiles), t = int32_t(v - int64_t(hg) * tiles);
-      e = entry(t);
-      e.hg = hg;
-      n = e.n;
-      at = hg * cost + p.cost0[t];
-      k0 = at / share;
-      k1 = (at + n + kItemCost - 1) / share;
-      for (int64_t k = k0; k <= k1; ++k) {
-        const int32_t from = k == k0 ? 0 : cut_at(at, n, k);
-        const int32_t to = k == k1 ? n : cut_at(at, n, k + 1);
-        ranges += to > from;
+  int32_t placed = 0;
+  for (int32_t hg = 0; hg < p.round_groups; ++hg) {
+    for (int32_t base = 0; base < tiles; base += kScheduleThreads) {
+      const int32_t t = base + tid;
+      Entry e;
+      int32_t n = 0, ranges = 0, at = 0, k0 = 0, k1 = -1;
+      if (t < tiles) {
+        e = entry(t);
+        e.hg = hg;
+        n = e.n;
+        at = hg * cost + p.cost0[t];
+        k0 = at / share;
+        k1 = (at + n + kItemCost - 1) / share;
+        for (int32_t k = k0; k <= k1; ++k) {
+          const int32_t first = k == k0 ? 0 : cut_at(at, n, k);
+          const int32_t end = k == k1 ? n : cut_at(at, n, k + 1);
+          ranges += end > first;
+        }
       }
-    }
-    int64_t all;
-    int64_t x = placed + scan_block(ranges, &all);
-    placed += all;
-    if (v < virt) {
+      int32_t all;
+      int32_t x = placed + scan_block(ranges, &all);
+      placed += all;
+      if (t >= tiles) continue;
       int32_t slot = -1;
       if (ranges > 1) {
         slot = atomicAdd(&slots, ranges);
         p.cuts[atomicAdd(&cuts, 1)] = Cut{e.q0, e.ntok, e.hg, slot, ranges, {0, 0, 0}};
       }
-      for (int64_t k = k0; k <= k1; ++k) {
-        const int32_t from = k == k0 ? 0 : cut_at(at, n, k);
-        const int32_t to = k == k1 ? n : cut_at(at, n, k + 1);
-        if (to <= from) continue;
-        e.b0 = from;
-        e.n = to - from;
+      for (int32_t k = k0; k <= k1; ++k) {
+        const int32_t first = k == k0 ? 0 : cut_at(at, n, k);
+        const int32_t end = k == k1 ? n : cut_at(at, n, k + 1);
+        if (end <= first) continue;
+        e.b0 = first;
+        e.n = end - first;
         e.slot = slot < 0 ? -1 : slot++;
         atomicAdd(&bins[k], 1);              // entries of share k
         p.entries[x++] = e;
@@ -464,9 +451,9 @@ __global__ void __launch_bounds__(kScheduleThreads)
     }
   }
   __syncthreads();
-  int64_t all;
-  const int64_t before = scan_block(tid < p.workers ? bins[tid] : 0, &all);
-  if (tid <= p.workers) p.first[tid] = int32_t(before);
+  int32_t all;
+  const int32_t before = scan_block(tid < p.workers ? bins[tid] : 0, &all);
+  if (tid <= p.workers) p.first[tid] = before;
   if (tid == 0) *p.header = Header{0, tiles, cuts};
 }
 
@@ -656,160 +643,171 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tv);
       tma_prefetch_desc(&to);
     }
-    const uint64_t pol_kv = l2_policy_evict_last();
-    const uint64_t pol_q = l2_policy_evict_first();
-    uint32_t ii = 0, qi = 0, kiss = 0;   // descriptions, items and K blocks so far
-    bool ok = true;
     wait_dependency();                   // the schedule, and what the inputs come from
-    // items: the direct CTA's tile, places in the list of tiles times head groups,
-    // or the entries of this CTA's share, round by round
-    const int32_t entries = p.mode == kTiles ? __ldcg(&p.header->entries) : 0;
-    int32_t from = 0, to = 0;
-    if (p.mode == kRanges) {
-      from = __ldcg(&p.first[blockIdx.x]);
-      to = __ldcg(&p.first[blockIdx.x + 1]);
-    }
-    const int64_t items = p.mode == kDirect   ? int64_t(gridDim.x)
-                          : p.mode == kTiles ? int64_t(entries) * p.head_groups
-                                             : int64_t(to - from) * p.rounds;
-
-    // room for a description in the ring; lane 0 then fills it
-    auto slot_free = [&]() -> bool {
-      return ii < uint32_t(kNI) ||
-             mbar_wait(&sh->info_empty[ii % kNI], ((ii / kNI) - 1) & 1, abort, p.wait_ns);
-    };
-    auto publish = [&](const Item& it) {
-      sh->info[ii % kNI] = it;
-      mbar_arrive(&sh->info_full[ii % kNI]);
-    };
-    auto special = [&](int32_t what) -> bool {
-      bool good = true;
-      if (lane == 0) {
-        good = slot_free();
-        if (good) {
-          Item it{};
-          it.e.n = what;
-          publish(it);
-        }
+    Entry tile0;
+    const bool found = p.mode == kDirect &&
+                       find_tile(p, int32_t(blockIdx.x) / p.head_groups, lane, &tile0);
+    if (lane == 0) {
+      const uint64_t pol_kv = l2_policy_evict_last();
+      const uint64_t pol_q = l2_policy_evict_first();
+      uint32_t ii = 0, qi = 0, kiss = 0;   // descriptions, items and K blocks so far
+      // items: the direct CTA's tile, places in the list of tiles times head
+      // groups, or the entries of this CTA's share, round by round
+      int32_t entries = 0, from = 0, to = 0;
+      int64_t items = found ? 1 : 0;
+      if (p.mode == kTiles) {
+        entries = __ldcg(&p.header->entries);
+        items = int64_t(entries) * p.head_groups;
+      } else if (p.mode == kRanges) {
+        from = __ldcg(&p.first[blockIdx.x]);
+        to = __ldcg(&p.first[blockIdx.x + 1]);
+        items = int64_t(to - from) * p.rounds;
       }
-      ++ii;
-      return __shfl_sync(0xffffffffu, good, 0);
-    };
-    // loads one item's Q and K blocks
-    auto run_item = [&](int32_t id, int32_t pos, int32_t careful) -> bool {
-      int32_t hg, x;
-      Entry e;
-      if (p.mode == kDirect) {
-        hg = id % p.head_groups;
-        x = id / p.head_groups;
-        if (!find_tile(p, x, lane, &e)) return true;
-      } else {
-        if (p.mode == kRanges) {
-          hg = id / (to - from);             // the round
-          x = from + id - hg * (to - from);
-        } else if (p.by_head) {
-          hg = id / entries;
-          x = id - hg * entries;
-        } else {
-          x = id / p.head_groups;
-          hg = id - x * p.head_groups;
+      // An item's entry is copied to shared memory (place x & 1), without waiting;
+      // landed() waits for it.
+      auto head_of = [&](int32_t id) {
+        return p.mode == kRanges ? id / (to - from)          // the round
+               : p.mode == kDirect ? int32_t(blockIdx.x) % p.head_groups
+               : p.by_head         ? id / entries
+                                   : id % p.head_groups;
+      };
+      auto fetch = [&](int64_t id64, uint32_t x) {
+        const int32_t id = int32_t(id64);
+        if (p.mode == kDirect) {
+          sh->ahead[x & 1] = tile0;
+          return;
         }
-        const int4* at = reinterpret_cast<const int4*>(&p.entries[x]);
-        const int4 lo = __ldcg(at), hi = __ldcg(at + 1);
-        e = Entry{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const int32_t at = p.mode == kRanges ? from + id % (to - from)
+                           : p.by_head       ? id % entries
+                                             : id / p.head_groups;
+        async_copy_16(&sh->ahead[x & 1], &p.entries[at]);
+        async_copy_16(reinterpret_cast<uint8_t*>(&sh->ahead[x & 1]) + 16,
+                      reinterpret_cast<const uint8_t*>(&p.entries[at]) + 16);
+      };
+      auto landed = [&]() { async_wait_all(); };
+      // waits, or only looks (what a look does not find is not an error)
+      bool ok = true;
+      auto ready = [&](uint64_t* bar, uint32_t use, uint32_t ring, bool wait) -> bool {
+        if (use < ring) return true;
+        const uint32_t par = ((use / ring) - 1) & 1;
+        if (!wait) return mbar_test(bar, par);
+        ok = mbar_wait(bar, par, abort, p.wait_ns);
+        return ok;
+      };
+      // an item's description and its Q tile, once there is room for both
+      auto publish = [&](int32_t id, uint32_t x, int32_t pos, int32_t careful,
+                         bool wait) -> bool {
+        const uint32_t slot = ii % kNI, qs = qi % C::kNQ;
+        if (!ready(&sh->info_empty[slot], ii, kNI, wait) ||
+            !ready(&sh->q_empty[qs], qi, C::kNQ, wait))
+          return false;
+        landed();
+        Item* it = &sh->info[slot];
+        Entry e = sh->ahead[x & 1];
+        int32_t hg = head_of(id);
         if (p.mode == kRanges) {
           if (e.slot >= 0) e.slot += hg * p.round_slots;
           hg = hg * p.round_groups + e.hg;
         }
-      }
-      const int32_t head0 = hg * p.tile_heads, g = head0 / p.group;
-      bool good = true;
-      if (lane == 0) {
-        good = slot_free();
-        if (good) {
-          Item it;
-          it.e = e;
-          it.head0 = head0;
-          it.g = g;
-          it.mt = max(0, (e.lim0 + 1) / kBK - e.b0);
-          it.pos = pos;
-          it.careful = careful;
-          publish(it);
-          const uint32_t qs = qi % C::kNQ;
-          if (qi >= uint32_t(C::kNQ) &&
-              !mbar_wait(&sh->q_empty[qs], ((qi / C::kNQ) - 1) & 1, abort, p.wait_ns))
-            good = false;
-          if (good) {
-            // the box is tile_heads x tile_tokens rows; what it covers behind
-            // the tensor counts as loaded (zeros)
-            mbar_arrive_expect_tx(&sh->q_full[qs],
-                                  uint32_t(C::kPanels * 128 * p.tile_heads * p.tile_tokens));
+        const int32_t head0 = hg * p.tile_heads;
+        it->e = e;
+        it->head0 = head0;
+        it->g = head0 / p.group;
+        it->mt = max(0, (e.lim0 + 1) / kBK - e.b0);
+        it->pos = pos;
+        it->careful = careful;
+        sh->ids[pos] = id;
+        mbar_arrive(&sh->info_full[slot]);
+        ++ii;
+        // the box is tile_heads x tile_tokens rows; what it covers behind the
+        // tensor counts as loaded (zeros)
+        mbar_arrive_expect_tx(&sh->q_full[qs],
+                              uint32_t(C::kPanels * 128 * p.tile_heads * p.tile_tokens));
 #pragma unroll
-            for (int s = 0; s < C::kPanels; ++s)
-              tma_load_3d(sQ + qs * C::kQBytes + s * C::kQPanel, &tq, &sh->q_full[qs], s * 64,
-                          head0, e.q0, pol_q);
-            ++qi;
-          }
-        }
-        if (good) {
-          const int32_t blocks = careful & kMaxima ? 2 * e.n : e.n;
-          for (int32_t t = 0; t < blocks; ++t) {
-            const int32_t j = e.b0 + (t >= e.n ? t - e.n : t);
-            const uint32_t ks = kiss % C::kNK;
-            if (kiss >= uint32_t(C::kNK) &&
-                !mbar_wait(&sh->k_empty[ks], ((kiss / C::kNK) - 1) & 1, abort, p.wait_ns)) {
-              good = false;
-              break;
+        for (int s = 0; s < C::kPanels; ++s)
+          tma_load_3d(sQ + qs * C::kQBytes + s * C::kQPanel, &tq, &sh->q_full[qs], s * 64,
+                      head0, e.q0, pol_q);
+        ++qi;
+        return true;
+      };
+      auto special = [&](int32_t what) {
+        const uint32_t slot = ii % kNI;
+        if (!ready(&sh->info_empty[slot], ii, kNI, true)) return;
+        sh->info[slot].e.n = what;
+        mbar_arrive(&sh->info_full[slot]);
+        ++ii;
+      };
+      auto load_k = [&](int32_t g, int32_t key) {
+        const uint32_t ks = kiss % C::kNK;
+        if (!ready(&sh->k_empty[ks], kiss, C::kNK, true)) return;
+        mbar_arrive_expect_tx(&sh->k_full[ks], C::kKVBytes);
+#pragma unroll
+        for (int s = 0; s < C::kPanels; ++s)
+          tma_load_3d(sK + ks * C::kKVBytes + s * C::kKVPanel, &tk, &sh->k_full[ks], s * 64, g,
+                      key, pol_kv);
+        ++kiss;
+      };
+      // Items are looked up ahead, so that no load or atomic is waited for
+      // between two of them, and the next one's Q is on its way while this one's
+      // K blocks are.  (The first two of a CTA are dealt out forth and back.)
+      const bool counted = p.mode == kTiles;
+      const int32_t grid = int32_t(gridDim.x), me = int32_t(blockIdx.x);
+      int64_t id0 = counted ? me : 0, id1 = counted ? 2 * grid - 1 - me : 1, id2 = 2;
+      if (counted) id2 = 2 * grid + atomicAdd(p.counter, 1);
+      uint32_t batches = 0, x = 0;         // x: items fetched, but for this one
+      if (id0 < items) {
+        fetch(id0, 0);
+        for (bool more = true; ok && more;) {
+          // a batch of items, then those of them that are to be done again
+          int32_t pos = 0;
+          publish(int32_t(id0), x, 0, 0, true);
+          while (ok) {
+            const Entry* e = &sh->ahead[x & 1];
+            const int32_t g = sh->info[(ii - 1) % kNI].g, n = e->n;
+            const int32_t key0 = e->kbeg + e->b0 * kBK;
+            more = id1 < items;
+            if (more) fetch(id1, x + 1);
+            const bool ahead = more && pos + 1 < kBatch;
+            bool out = false;
+            for (int32_t t = 0; ok && t < n; ++t) {
+              load_k(g, key0 + t * kBK);
+              if (t > 0 && ok && ahead && !out)
+                out = publish(int32_t(id1), x + 1, pos + 1, 0, false);
             }
-            mbar_arrive_expect_tx(&sh->k_full[ks], C::kKVBytes);
-#pragma unroll
-            for (int s = 0; s < C::kPanels; ++s)
-              tma_load_3d(sK + ks * C::kKVBytes + s * C::kKVPanel, &tk, &sh->k_full[ks], s * 64,
-                          g, e.kbeg + j * kBK, pol_kv);
-            ++kiss;
+            if (ok && ahead && !out) publish(int32_t(id1), x + 1, pos + 1, 0, true);
+            if (!more) break;
+            ++x;
+            id0 = id1;
+            id1 = id2;
+            id2 = counted ? int64_t(2 * grid + atomicAdd(p.counter, 1)) : id2 + 1;
+            if (!ahead) break;
+            ++pos;
+          }
+          if (ok) special(kMarker);
+          if (ok) ok = mbar_wait(&sh->batch_done, batches & 1, abort, p.wait_ns);
+          ++batches;
+          for (int32_t w = 0; ok && w < pos / 32 + 1; ++w) {
+            uint32_t bits = *(volatile uint32_t*)&sh->again[w];
+            const uint32_t maxima = *(volatile uint32_t*)&sh->maxima[w];
+            sh->again[w] = sh->maxima[w] = 0;
+            while (ok && bits) {
+              const int at = __ffs(bits) - 1;
+              bits &= bits - 1;
+              const int32_t twice = (maxima >> at) & 1;
+              // (the next batch's first item may be in the other place)
+              fetch(sh->ids[32 * w + at], x + 1);
+              publish(sh->ids[32 * w + at], x + 1, 32 * w + at,
+                      kClean | (twice ? kMaxima : 0), true);
+              const Entry* e = &sh->ahead[(x + 1) & 1];
+              const int32_t g = sh->info[(ii - 1) % kNI].g, n = e->n;
+              const int32_t key0 = e->kbeg + e->b0 * kBK;
+              for (int32_t t = 0; ok && t < n + twice * n; ++t)
+                load_k(g, key0 + (t >= n ? t - n : t) * kBK);
+            }
           }
         }
       }
-      ++ii;
-      return __shfl_sync(0xffffffffu, good, 0);
-    };
-
-    const bool counted = p.mode == kTiles;
-    int64_t id = p.mode == kRanges ? 0 : int64_t(blockIdx.x);
-    uint32_t batches = 0;
-    while (ok && id < items) {
-      // a batch of items, then those of them that are to be done again
-      int32_t pos = 0;
-      for (; pos < kBatch && id < items; ++pos) {
-        int32_t next = 0;
-        if (lane == 0) {
-          if (counted) next = atomicAdd(p.counter, 1);
-          sh->ids[pos] = int32_t(id);
-        }
-        ok = run_item(int32_t(id), pos, 0);
-        if (!ok) break;
-        id = counted              ? int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0)
-             : p.mode == kRanges ? id + 1
-                                  : items;
-      }
-      if (ok) ok = special(kMarker);
-      if (ok) ok = warp_wait(&sh->batch_done, batches & 1, abort, p.wait_ns);
-      ++batches;
-      for (int32_t w = 0; ok && w < (pos + 31) / 32; ++w) {
-        uint32_t bits = *(volatile uint32_t*)&sh->again[w];
-        const uint32_t maxima = *(volatile uint32_t*)&sh->maxima[w];
-        __syncwarp();
-        if (lane == 0) sh->again[w] = sh->maxima[w] = 0;
-        while (ok && bits) {
-          const int at = __ffs(bits) - 1;
-          bits &= bits - 1;
-          ok = run_item(*(volatile int32_t*)&sh->ids[32 * w + at], 32 * w + at,
-                        kClean | ((maxima >> at) & 1 ? kMaxima : 0));
-        }
-      }
-    }
-    if (ok) ok = special(kEnd);
-    if (lane == 0) {
+      if (ok) special(kEnd);
       if (!ok) raise_abort(sh, p);
       // copies still in flight must land before this CTA's shared memory goes
       drain_ring(sh->q_full, qi, C::kNQ);
@@ -968,6 +966,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (;; ++ii) {
       const int slot = ii % kNI;
+      // the next description may come only after the tile before this one has
+      // left its Q stage
+      const uint64_t t0 = spq < qi ? global_ns() : 0;
+      while (ok && spq < qi &&
+             !__shfl_sync(0xffffffffu,
+                          lane == 0 && mbar_test(&sh->info_full[slot], (ii / kNI) & 1), 0)) {
+        store_upto(qi, false);
+        ok = !__any_sync(0xffffffffu, *abort || global_ns() - t0 > p.wait_ns);
+      }
+      if (!ok) break;
       if (!warp_wait(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
         ok = false;
         break;
@@ -1061,6 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 20) {
     // ------------------------------------------------- softmax groups
+    registers_dec<kSoftmaxRegs>();
     const int grp = (warp - 4) >> 2;              // column group 0..3
     const int quarter = warp & 3;                 // TMEM lane quarter of this warp
     const int row = quarter * 32 + lane;
@@ -1300,17 +1309,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                               int64_t(it.head0 + head) * p.o_sh;
       uint8_t* stg = sQ + (qi % C::kNQ) * C::kQBytes + row * 128;
       float4* part = p.part_o + int64_t(whole ? 0 : it.e.slot) * (D / 4) * kRows + row;
-      float osum = 0.f;
+      const bool blank = __any_sync(0xffffffffu, !some);     // rarely: a branch
+      const bool dirty = it.careful && *(volatile int32_t*)&sh->bad_v[w] == int32_t(qi + 1);
+      float osum = 0.f, osum2 = 0.f;
       // 32 columns of O: a full tile is staged in its Q stage (128-byte
       // swizzled, as TMA stores read it), rows of other tiles go out as they are,
       // ranges unnormalised and fp32 to their slot
       auto emit = [&](uint32_t (&r)[32], int col) {
-        if (!some) {
+        if (blank && !some) {
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = 0u;
         }
-        if (it.careful && live && some &&
-            *(volatile int32_t*)&sh->bad_v[w] == int32_t(qi + 1)) {
+        if (dirty && live && some) {
           // what clean_v took out of the values that this row sees
           const __nv_bfloat16* v = p.v + it.g * p.v_sh + col;
           const int32_t end = min(lim + 1, (it.e.b0 + n) * kBK);
@@ -1324,7 +1334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int x = 0; x < 32; ++x) osum += __uint_as_float(r[x]);
+        for (int x = 0; x < 32; x += 2)
+          add2(osum, osum2, __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
         if (!live) return;
         if (!whole) {
 #pragma unroll
@@ -1338,9 +1349,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 4; ++x) {
           uint32_t ob[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            ob[y] = pack_bf16x2(__uint_as_float(r[8 * x + 2 * y]) * inv,
-                                __uint_as_float(r[8 * x + 2 * y + 1]) * inv);
+          for (int y = 0; y < 4; ++y) {
+            float a0, a1;
+            mul2(a0, a1, __uint_as_float(r[8 * x + 2 * y]),
+                 __uint_as_float(r[8 * x + 2 * y + 1]), inv, inv);
+            ob[y] = pack_bf16x2(a0, a1);
+          }
           const int c16 = col / 8 + x;
           uint4* dst = staged ? reinterpret_cast<uint4*>(stg + c16 / 8 * C::kQPanel +
                                                          ((c16 % 8 ^ (row & 7)) << 4))
@@ -1353,21 +1367,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      // the whole row at once: the next item's first P V may then overwrite O
+      uint32_t r[D / 32][32];
 #pragma unroll
-      for (int col = 0; col < D; col += 32) {
-        uint32_t r[32];
-        tmem_ld32(lanes + col, r);
-        tmem_ld_wait(r);
-        if (col == D - 32) {
-          // O is read: the next item's first P V may overwrite it
-          tc_fence_before();
-          mbar_arrive(&sh->o_free);
-        }
-        emit(r, col);
-      }
+      for (int x = 0; x < D / 32; ++x) tmem_ld32(lanes + 32 * x, r[x]);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) tmem_ld_wait(r[x]);
+      tc_fence_before();
+      mbar_arrive(&sh->o_free);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) emit(r[x], 32 * x);
       // the range that the first pass keeps: the sum up to 2^126 (so that no
       // weight overflowed) and O finite
-      if (!it.careful && live && some && !(in_range && fabsf(osum) <= 3.0e38f)) {
+      if (!it.careful && live && some && !(in_range && fabsf(osum + osum2) <= 3.0e38f)) {
         const uint32_t bit = 1u << (it.pos & 31);
         atomicOr(&sh->again[it.pos >> 5], bit);
         if (!in_range) atomicOr(&sh->maxima[it.pos >> 5], bit);
@@ -1446,8 +1458,24 @@ int workers_of(int sms) { return std::min(sms, kBins - 1); }
 
 // Tiles are cut where sequences have more keys than queries, on the whole: the
 // tiles of whole prompts have from one block to all, and taking the long ones
-// first leaves an even end.
-bool may_cut(const sa_packed_shape& s) { return s.total_k > s.total_q; }
+// first leaves an even end.  (The schedule adds up their blocks in 32 bits.)
+bool may_cut(const sa_packed_shape& s) {
+  const int64_t blocks = (int64_t(s.total_k) + kBK - 1) / kBK + kItemCost;
+  const int64_t tiles =
+      sa_packed::most_tiles(s) * (s.num_q_heads / sa_packed::tile_of(s).heads);
+  return s.total_k > s.total_q && tiles < (int64_t(1) << 30) / blocks;
+}
+
+// Rounds of head groups: as many as keep a round's keys and values within half of
+// L2, or about, but a divisor of the groups.
+int rounds_of(const sa_packed_shape& s) {
+  const int64_t head_groups = s.num_q_heads / sa_packed::tile_of(s).heads;
+  const int64_t bytes = int64_t(s.total_k) * s.num_kv_heads * s.head_dim * 4;
+  int rounds = 1;
+  for (int r = 2; r <= kRounds && bytes / rounds > (int64_t(64) << 20); ++r)
+    if (head_groups % r == 0) rounds = r;
+  return rounds;
+}
 
 struct Layout {
   size_t header, seqs, tile0, entries, cost0, first, cuts, part_ml, part_o, end;
@@ -1464,22 +1492,13 @@ Layout layout_of(const sa_packed_shape& s, int sms) {
   l.tile0 = l.seqs + up(size_t(s.batch) * 16);
   l.entries = l.tile0 + up(size_t(s.batch) * 4);
   l.cost0 = l.entries + up(size_t(l.max_entries) * sizeof(Entry));
-  l.first = l.cost0 + up(size_t(tiles) * 8);
+  l.first = l.cost0 + up(size_t(tiles) * 4);
   l.cuts = l.first + up(size_t(workers + 1) * 4);
   l.part_ml = l.cuts + up(size_t(workers) * sizeof(Cut));
-  l.part_o = l.part_ml + up(size_t(kRounds * l.round_slots) * kRows * 16);
-  l.end = l.part_o + up(size_t(kRounds * l.round_slots) * kRows * size_t(s.head_dim) * 4);
+  const size_t slots = size_t(rounds_of(s) * l.round_slots);
+  l.part_o = l.part_ml + up(slots * kRows * 16);
+  l.end = l.part_o + up(slots * kRows * size_t(s.head_dim) * 4);
   return l;
-}
-
-// Rounds of head groups: as many as keep a round's keys and values within half of
-// L2, or about, but a divisor of the groups.
-int rounds_of(const sa_packed_shape& s, int64_t head_groups) {
-  const int64_t bytes = int64_t(s.total_k) * s.num_kv_heads * s.head_dim * 4;
-  int rounds = 1;
-  for (int r = 2; r <= kRounds && bytes / rounds > (int64_t(64) << 20); ++r)
-    if (head_groups % r == 0) rounds = r;
-  return rounds;
 }
 
 template <class Kernel, class... Params>
@@ -1538,7 +1557,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   }
   const bool ranges = may_cut(s);
   const int workers = workers_of(sms);
-  const int rounds = ranges ? rounds_of(s, head_groups) : 1;
+  const int rounds = ranges ? rounds_of(s) : 1;
   auto at = [&](size_t offset) { return static_cast<void*>(ws + offset); };
   Params p;
   p.cu_q = a.cu_q;
@@ -1585,7 +1604,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   sp.header = static_cast<Header*>(at(lay.header));
   sp.seqs = static_cast<int4*>(at(lay.seqs));
   sp.tile0 = static_cast<int32_t*>(at(lay.tile0));
-  sp.cost0 = static_cast<int64_t*>(at(lay.cost0));
+  sp.cost0 = static_cast<int32_t*>(at(lay.cost0));
   sp.entries = static_cast<Entry*>(at(lay.entries));
   sp.first = static_cast<int32_t*>(at(lay.first));
   sp.cuts = static_cast<Cut*>(at(lay.cuts));

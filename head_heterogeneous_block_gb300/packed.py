@@ -18,27 +18,29 @@ class PackedAttention(DeviceOperator):
     the other: grouped query heads, every key (the block-sparse ``PrefillLayer``
     takes one sequence and the blocks that its plan selects).
 
-    ``scale`` of the scores: 1 / sqrt(head_dim) by default.  ``tokens`` and
-    ``batch`` size the workspace ahead of the first call (before a graph
-    capture, say) for calls of up to so many queries and sequences."""
+    ``scale`` of the scores: 1 / sqrt(head_dim) by default.  ``tokens``,
+    ``batch`` and ``keys`` (default: ``tokens``) size the workspace ahead of the
+    first call (before a graph capture, say) for calls of up to so many queries,
+    sequences and keys."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, scale=None, tokens=0, batch=1,
-                 device="cuda"):
+                 keys=None, device="cuda"):
         super().__init__(device)
         self.num_q_heads, self.num_kv_heads, self.head_dim = num_q_heads, num_kv_heads, head_dim
         self.scale = 1.0 / math.sqrt(head_dim) if scale is None else float(scale)
-        self._tokens = self._batch = 0
+        self._tokens = self._batch = self._keys = 0
         with torch.cuda.device(self.device):
-            self._size(tokens, batch)
+            self._size(tokens, batch, tokens if keys is None else keys)
 
-    def _size(self, tokens, batch):
+    def _size(self, tokens, batch, keys):
         """Grow the workspace to what calls of these sizes need, and those so
         far; the device is current."""
         tokens, batch = max(tokens, self._tokens), max(batch, self._batch)
+        keys = max(keys, self._keys)
         self._need(sparse_attn_packed_workspace_size(PackedShape(
-            total_q=tokens, batch=batch, num_q_heads=self.num_q_heads,
+            total_q=tokens, total_k=keys, batch=batch, num_q_heads=self.num_q_heads,
             num_kv_heads=self.num_kv_heads, head_dim=self.head_dim, scale=self.scale)))
-        self._tokens, self._batch = tokens, batch
+        self._tokens, self._batch, self._keys = tokens, batch, keys
 
     def __call__(self, q, k, v, cu_q, cu_k=None, out=None, lse=None, stream=None):
         """q bf16 [tokens, num_q_heads, d]; k, v bf16 [keys, num_kv_heads, d]
@@ -70,8 +72,8 @@ class PackedAttention(DeviceOperator):
         if out.shape[0] != tokens:
             raise ValueError("out must have q's shape")
         lp = self._own(lse, torch.float32, (tokens, heads), "lse")
-        if tokens > self._tokens or ends - 1 > self._batch:
-            self._size(tokens, ends - 1)
+        if tokens > self._tokens or ends - 1 > self._batch or keys > self._keys:
+            self._size(tokens, ends - 1, keys)
         shape = PackedShape(q0, q1, k0, k1, v0, v1, o0, o1, tokens, keys, ends - 1, heads, kv_heads,
                             d, self.scale)
         status = _forward(ctypes.byref(shape), qp, kp, vp, cq, ck, op, lp, self._ws_ptr, self._ws_bytes,
