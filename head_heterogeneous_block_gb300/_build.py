@@ -1,15 +1,19 @@
-"""Build libsparse_attn.so in-tree with nvcc (sm_103a) and g++.
+"""Build libsparse_attn.so in-tree with nvcc (sm_103a) and g++, and the native
+calls of the torch classes beside it.
 
 Translation units are compiled in parallel into ``_build/`` and linked into
-``head_heterogeneous_block_gb300/_lib/libsparse_attn.so``.  Rebuilds only
-what changed (by modification time of sources and headers).
+``head_heterogeneous_block_gb300/_lib/libsparse_attn.so`` and, where there is a
+torch, ``_lib/_calls.so``.  Rebuilds only what changed (by modification time of
+sources and headers).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(ROOT, "_build", "obj")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libsparse_attn.so")
+CALLS_SRC = os.path.join(PKG, "binding", "calls.cpp")
+CALLS = os.path.join(LIB_DIR, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -43,6 +49,12 @@ def _newest_header() -> float:
             if f.endswith((".h", ".cuh")):
                 t = max(t, os.path.getmtime(os.path.join(d, f)))
     return t
+
+
+def _torch():
+    """The torch package's folder, found without importing it; None: there is none."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
 def _compile(cmd):
@@ -71,6 +83,18 @@ def build(verbose: bool = False, force: bool = False) -> str:
         objs.append(obj)
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr):
             jobs.append(["g++", *common, "-fPIC", "-Wall", "-c", src, "-o", obj])
+    torch = _torch()
+    calls_obj = os.path.join(OBJ, "calls.o")
+    if torch is not None:
+        newest = max(os.path.getmtime(CALLS_SRC), hdr,
+                     os.path.getmtime(os.path.join(torch, "version.py")))
+        if force or not os.path.exists(calls_obj) or os.path.getmtime(calls_obj) < newest:
+            dirs = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+                    os.path.join(torch, "include", "torch", "csrc", "api", "include")]
+            # (first: it takes as long as the largest kernel)
+            jobs.insert(0, ["g++", "-O2", "-std=c++17", f"-I{INCLUDE}",
+                            *(f"-isystem{d}" for d in dirs), "-fPIC", "-Wall", "-c", CALLS_SRC,
+                            "-o", calls_obj])
     if jobs:
         with ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
             results = list(ex.map(_compile, jobs))
@@ -86,6 +110,15 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(LIB + ".tmp", LIB)
+    if torch is not None and (jobs or not os.path.exists(CALLS)):
+        lib = os.path.join(torch, "lib")
+        link = ["g++", "-shared", "-o", CALLS + ".tmp", calls_obj, f"-L{LIB_DIR}",
+                "-l:libsparse_attn.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-ltorch_python",
+                "-ltorch_cpu", "-lc10"]
+        r = subprocess.run(link, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+        os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 

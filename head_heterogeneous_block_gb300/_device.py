@@ -1,11 +1,32 @@
 """What the operator classes share: a status word and a workspace on one
-device, and the stream that a call goes to."""
+device, the stream that a call goes to, and their native calls."""
 from __future__ import annotations
+
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
+from . import library_path
+from ._build import CALLS
+
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+
+
+def _load_calls():
+    if not os.path.exists(CALLS):
+        raise ImportError(f"{CALLS} is missing: build it with __graft_entry__.build() (it stands "
+                          f"beside {library_path()}; there is no fallback)")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    loader.exec_module(module)
+    return module
+
+
+calls = _load_calls()
+NEEDS_WORKSPACE = -1         # of calls.packed: larger than the workspace was sized for
 
 
 class DeviceOperator:
@@ -58,6 +79,10 @@ class DeviceOperator:
             self._ws.record_stream(self._stream(handle))
         return handle
 
+    def _elsewhere(self, stream):
+        """Whether a call has to go through ``_on``."""
+        return stream is not None or _current_device() != self._index
+
     def _on(self, stream, call):
         """``call()`` with the device and ``stream`` (None: the current one)
         current; a tensor that it returns may be used on the caller's stream."""
@@ -74,12 +99,6 @@ class DeviceOperator:
                     t.record_stream(caller)
             return out
 
-    def _elsewhere(self, stream):
-        """Whether a call has to go through ``_on``."""
-        return (_current_device() != self._index or
-                stream is not None and (stream if isinstance(stream, int) else stream.cuda_stream)
-                != _raw_stream(self._index))
-
     def _own(self, t, dtype, shape, name):
         """Address of a contiguous tensor of this device (None: NULL)."""
         if t is None:
@@ -89,16 +108,3 @@ class DeviceOperator:
         if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}")
         return t.data_ptr()
-
-    def _rows(self, t, heads, head_dim, name):
-        """Address and (token, head) strides of a bf16 [tokens, heads, d] view."""
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16")
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-            raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}]")
-        st, sh, one = t.stride()
-        if one != 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-        if t.get_device() != self._index:
-            raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr(), st, sh

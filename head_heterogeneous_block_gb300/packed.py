@@ -2,15 +2,12 @@
 ``sparse_attn_packed_*`` calls."""
 from __future__ import annotations
 
-import ctypes
 import math
 
 import torch
 
-from . import PackedShape, _check, _lib, sparse_attn_packed_workspace_size
-from ._device import DeviceOperator
-
-_forward = _lib.sparse_attn_packed_forward
+from . import PackedShape, _check, sparse_attn_packed_workspace_size
+from ._device import NEEDS_WORKSPACE, DeviceOperator, calls
 
 
 class PackedAttention(DeviceOperator):
@@ -41,6 +38,8 @@ class PackedAttention(DeviceOperator):
             total_q=tokens, total_k=keys, batch=batch, num_q_heads=self.num_q_heads,
             num_kv_heads=self.num_kv_heads, head_dim=self.head_dim, scale=self.scale)))
         self._tokens, self._batch, self._keys = tokens, batch, keys
+        self._sizes = (self._index, self.num_q_heads, self.num_kv_heads, self.head_dim, self.scale,
+                       tokens, batch, keys)
 
     def __call__(self, q, k, v, cu_q, cu_k=None, out=None, lse=None, stream=None):
         """q bf16 [tokens, num_q_heads, d]; k, v bf16 [keys, num_kv_heads, d]
@@ -55,29 +54,13 @@ class PackedAttention(DeviceOperator):
         captured call follows them."""
         if self._elsewhere(stream):
             return self._on(stream, lambda: self(q, k, v, cu_q, cu_k, out, lse))
-        heads, kv_heads, d = self.num_q_heads, self.num_kv_heads, self.head_dim
-        qp, q0, q1 = self._rows(q, heads, d, "q")
-        kp, k0, k1 = self._rows(k, kv_heads, d, "k")
-        vp, v0, v1 = self._rows(v, kv_heads, d, "v")
-        tokens, keys, ends = q.shape[0], k.shape[0], cu_q.numel()
-        if v.shape[0] != keys:
-            raise ValueError("k and v must have the same number of tokens")
-        if ends < 2:
-            raise ValueError("cu_q must be [batch + 1]")
-        cq = self._own(cu_q, torch.int32, (ends,), "cu_q")
-        ck = cq if cu_k is None else self._own(cu_k, torch.int32, (ends,), "cu_k")
         if out is None:
-            out = torch.empty(tokens, heads, d, dtype=torch.bfloat16, device=self.device)
-        op, o0, o1 = self._rows(out, heads, d, "out")
-        if out.shape[0] != tokens:
-            raise ValueError("out must have q's shape")
-        lp = self._own(lse, torch.float32, (tokens, heads), "lse")
-        if tokens > self._tokens or ends - 1 > self._batch or keys > self._keys:
-            self._size(tokens, ends - 1, keys)
-        shape = PackedShape(q0, q1, k0, k1, v0, v1, o0, o1, tokens, keys, ends - 1, heads, kv_heads,
-                            d, self.scale)
-        status = _forward(ctypes.byref(shape), qp, kp, vp, cq, ck, op, lp, self._ws_ptr, self._ws_bytes,
-                          self._status, self._handle())
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+        status = calls.packed(*self._sizes, q, k, v, cu_q, cu_k, out, lse, self._ws_ptr,
+                              self._ws_bytes, self._status, self._handle())
+        if status == NEEDS_WORKSPACE:
+            self._size(q.shape[0], cu_q.numel() - 1, k.shape[0])
+            return self(q, k, v, cu_q, cu_k, out, lse)
         if status:
             _check(status, "sparse_attn_packed_forward")
         return out

@@ -6,10 +6,8 @@ import ctypes
 
 import torch
 
-from . import (PageGrowth, PagePoolDesc, _check, _lib, sparse_attn_paged_grow_workspace_size)
-from ._device import DeviceOperator
-
-_grow = _lib.sparse_attn_paged_grow
+from . import PagePoolDesc, _check, sparse_attn_paged_grow_workspace_size
+from ._device import DeviceOperator, calls
 
 
 class PagePool(DeviceOperator):
@@ -57,7 +55,7 @@ class PagePool(DeviceOperator):
             self._own(free_count, i32, (1,), "free_count"),
             self._own(weights, torch.float32, slots, "weights"),
             self._own(positions, i32, slots, "positions"), self.num_pages, page, max_pages, b, h)
-        self._ref = ctypes.byref(self._desc)
+        self._desc_ptr = ctypes.addressof(self._desc)
         self._made = () if num_pages is None else (free_pages, free_count, owned)
         with torch.cuda.device(self.device):
             self._need(sparse_attn_paged_grow_workspace_size(self._desc))
@@ -93,29 +91,12 @@ class PagePool(DeviceOperator):
             return self._on(stream, lambda: self.grow(
                 slots, cu, counts, ended, start, positions, granted, lens_out, owned_out,
                 free_count_out, start_out))
-        b, h, i32, own = self.batch, self.num_kv_heads, torch.int32, self._own
-        if slots.dim() != 2:
-            raise ValueError("slots must be [num_kv_heads, tokens]")
-        tokens = slots.shape[1]
-        if cu is None and tokens % b:
-            raise ValueError("without cu, tokens must be a multiple of the batch")
-        start_p = own(start, i32, (b,), "start")
-        d = self._desc
-        growth = PageGrowth(
-            own(cu, i32, (b + 1,), "cu"), own(counts, i32, (b,), "counts"),
-            own(ended, torch.bool, (b,), "ended"), start_p,
-            own(slots, torch.int64, (h, tokens), "slots"),
-            own(positions, i32, (tokens,), "positions"), own(granted, i32, (b,), "granted"),
-            d.lens if lens_out is None else own(lens_out, i32, (b, h), "lens_out"),
-            d.owned if owned_out is None else own(owned_out, i32, (b, h), "owned_out"),
-            d.free_count if free_count_out is None else own(free_count_out, i32, (1,),
-                                                            "free_count_out"),
-            start_p if start_out is None else own(start_out, i32, (b,), "start_out"), tokens)
         handle = self._handle()
         if handle != self._status_stream:
             for t in self._made:
                 t.record_stream(self._stream(handle))
-        status = _grow(self._ref, ctypes.byref(growth), self._ws_ptr, self._ws_bytes, self._status,
-                       handle)
+        status = calls.grow(self._desc_ptr, self._index, slots, cu, counts, ended, start,
+                            positions, granted, lens_out, owned_out, free_count_out, start_out,
+                            self._ws_ptr, self._ws_bytes, self._status, handle)
         if status:
             _check(status, "sparse_attn_paged_grow")

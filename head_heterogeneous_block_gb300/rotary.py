@@ -7,11 +7,8 @@ import math
 
 import torch
 
-from . import RotaryDesc, _check, _lib
-from ._device import DeviceOperator
-
-_I64x2 = ctypes.c_int64 * 2
-_rotary, _store = _lib.sparse_attn_rotary, _lib.sparse_attn_rotary_store
+from . import RotaryDesc, _check
+from ._device import DeviceOperator, calls
 
 
 def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
@@ -106,18 +103,13 @@ class Rotary(DeviceOperator):
                                   dtype=torch.int64, device=self.device)
         self._desc = RotaryDesc(self.turns.data_ptr(), self.factor, head_dim, rot_dim,
                                 int(self.interleaved))
-        self._ref = ctypes.byref(self._desc)
+        self._desc_ptr = ctypes.addressof(self._desc)
 
     def _follow(self):
         handle = self._handle()
         if handle != self._status_stream:
             self.turns.record_stream(self._stream(handle))
         return handle
-
-    def _heads(self, t, name):
-        if t.dim() != 3:
-            raise ValueError(f"{name} must be [tokens, heads, {self.head_dim}]")
-        return t.shape[1]
 
     def _like(self, t):
         return torch.empty(t.shape, dtype=torch.bfloat16, device=self.device)
@@ -129,22 +121,10 @@ class Rotary(DeviceOperator):
         each may be its input, which then changes in place."""
         if self._elsewhere(stream):
             return self._on(stream, lambda: self(q, k, positions, q_out, k_out))
-        d = self.head_dim
-        hq, hkv = self._heads(q, "q"), self._heads(k, "k")
-        qp, q0, q1 = self._rows(q, hq, d, "q")
-        kp, k0, k1 = self._rows(k, hkv, d, "k")
-        tokens = q.shape[0]
-        if k.shape[0] != tokens:
-            raise ValueError("q and k must have the same number of tokens")
         q_out = self._like(q) if q_out is None else q_out
         k_out = self._like(k) if k_out is None else k_out
-        qop, qo0, qo1 = self._rows(q_out, hq, d, "q_out")
-        kop, ko0, ko1 = self._rows(k_out, hkv, d, "k_out")
-        if q_out.shape[0] != tokens or k_out.shape[0] != tokens:
-            raise ValueError("q_out and k_out must have the shapes of q and k")
-        pp = self._own(positions, torch.int32, (tokens,), "positions")
-        status = _rotary(self._ref, tokens, hq, hkv, pp, qp, _I64x2(q0, q1), kp, _I64x2(k0, k1),
-                         qop, _I64x2(qo0, qo1), kop, _I64x2(ko0, ko1), self._follow())
+        status = calls.rotary(self._desc_ptr, self._index, self.head_dim, q, k, positions, q_out,
+                              k_out, self._follow())
         if status:
             _check(status, "sparse_attn_rotary")
         return q_out, k_out
@@ -160,31 +140,15 @@ class Rotary(DeviceOperator):
         if self._elsewhere(stream):
             return self._on(stream, lambda: self.store(q, k, v, positions, cache, slots, q_out,
                                                        k_out))
-        d, hkv = self.head_dim, cache.num_kv_heads
-        if cache.head_dim != d:
-            raise ValueError(f"the cache's head_dim must be {d}")
+        if cache.head_dim != self.head_dim:
+            raise ValueError(f"the cache's head_dim must be {self.head_dim}")
         if cache.device != self.device:
             raise ValueError(f"the cache must be on {self.device}")
-        hq = self._heads(q, "q")
-        qp, q0, q1 = self._rows(q, hq, d, "q")
-        kp, k0, k1 = self._rows(k, hkv, d, "k")
-        vp, v0, v1 = self._rows(v, hkv, d, "v")
-        tokens = q.shape[0]
-        if k.shape[0] != tokens or v.shape[0] != tokens:
-            raise ValueError("q, k and v must have the same number of tokens")
         q_out = self._like(q) if q_out is None else q_out
-        qop, qo0, qo1 = self._rows(q_out, hq, d, "q_out")
-        kop, kos = None, None
-        if k_out is not None:
-            kop, *kos = self._rows(k_out, hkv, d, "k_out")
-            kos = _I64x2(*kos)
-        if q_out.shape[0] != tokens or (k_out is not None and k_out.shape[0] != tokens):
-            raise ValueError("q_out and k_out must have the shapes of q and k")
-        pp = self._own(positions, torch.int32, (tokens,), "positions")
-        sp = self._own(slots, torch.int64, (hkv, tokens), "slots")
-        status = _store(self._ref, tokens, hq, pp, qp, _I64x2(q0, q1), kp, _I64x2(k0, k1), vp,
-                        _I64x2(v0, v1), qop, _I64x2(qo0, qo1), kop, kos, cache._ref, sp,
-                        self._status, self._follow())
+        status = calls.rotary_store(self._desc_ptr, self._index, self.head_dim,
+                                    cache.num_kv_heads, q, k, v, positions,
+                                    ctypes.addressof(cache.desc), slots, q_out, k_out,
+                                    self._status, self._follow())
         if status:
             _check(status, "sparse_attn_rotary_store")
         return q_out, k_out
