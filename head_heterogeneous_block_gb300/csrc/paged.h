@@ -65,6 +65,7 @@ struct GrowArgs {
   int32_t* start_out;                 // or NULL
   int64_t num_pages;
   int32_t page, page_shift, max_pages, batch, Hkv, tokens, span;
+  uint32_t inv_heads;                 // 2^32 / Hkv, rounded up; 0: divide
   void* ws;
   int32_t* dev_status;
 };

@@ -417,6 +417,11 @@ sa_status sparse_attn_paged_grow(const sa_page_pool* pool, const sa_page_growth*
   a.Hkv = pool->num_kv_heads;
   a.tokens = g->tokens;
   a.span = g->tokens / pool->batch;
+  // exact for rows below 2^20 (their product with the error, below Hkv, stays below
+  // 2^32)
+  a.inv_heads = a.Hkv > 1 && a.Hkv <= 4096
+                    ? uint32_t(((uint64_t(1) << 32) + uint32_t(a.Hkv) - 1) / uint32_t(a.Hkv))
+                    : 0;
   a.ws = ws;
   a.dev_status = dev_status;
   return cuda_status(sa_paged::launch_grow(a, reinterpret_cast<cudaStream_t>(stream)));

@@ -13,8 +13,8 @@
 // row; then each (head, token) pair looks its page up by itself.  For few pairs
 // that is the same CTA, with the records in shared memory: a decode step is one
 // launch, and the chain of loads (counts and lengths; pages; slots) bounds it.
-// For many it is a second launch over all processors, bound by the 8-byte slots
-// that it writes.  Nothing that is read there is written there: pages are taken
+// For many it is a second launch over all processors, whose blocks keep the
+// records in shared memory and which the 8-byte slots that it writes bound.  Nothing that is read there is written there: pages are taken
 // from rows that give back, or below the old count of free ones, and put into
 // rows that want some, or above that count.
 
@@ -27,11 +27,16 @@ namespace {
 
 using sa_paged::GrowArgs;
 
-constexpr int kThreads = 1024;
-constexpr int kInlinePairs = 8192;    // (head, token) pairs that the first CTA does itself
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+static_assert(kWarps <= 32, "one warp scans the warps' sums");
+constexpr int kInlinePairs = 4096;    // (head, token) pairs that the first CTA does itself
 constexpr int kRecords = 2048;        // rows whose records then stay in shared memory
-constexpr int kSeqRecords = 1024;
+constexpr int kSeqRecords = kThreads; // a thread's sequence each
 constexpr int kSpread = 256;          // threads of a block of the second launch
+constexpr int kSpreadHeads = 4;       // heads of a thread's token that it looks up together
+constexpr int kSpreadRows = 1024;     // rows and sequences whose records its blocks keep
+constexpr int kSpreadSeqs = 512;
 
 struct Head {
   int32_t free, back, taken;          // F, R, G
@@ -44,6 +49,11 @@ struct Tables {
 
 __device__ __forceinline__ int32_t clamp_to(int32_t x, int32_t lo, int32_t hi) {
   return min(max(x, lo), hi);
+}
+
+// Sequence of row r: r / Hkv, by its reciprocal where that is exact.
+__device__ __forceinline__ int32_t seq_of_row(const GrowArgs& a, int32_t r) {
+  return a.inv_heads ? int32_t(__umulhi(uint32_t(r), a.inv_heads)) : r / a.Hkv;
 }
 
 __device__ __forceinline__ int32_t scan_warp(int32_t x, int lane) {
@@ -67,87 +77,111 @@ __device__ __forceinline__ int32_t page_at(const GrowArgs& a, const Tables& w, i
     if (w.row[mid].w <= x) lo = mid; else hi = mid;
   }
   const int4 r = w.row[lo];
-  const int32_t need = (r.x + w.seq[lo / a.Hkv].y + a.page - 1) >> a.page_shift;
+  const int32_t need = (r.x + w.seq[seq_of_row(a, lo)].y + a.page - 1) >> a.page_shift;
   return a.table[int64_t(lo) * a.max_pages + need + (x - r.w)];
 }
 
-// Slot (and what goes with it) of token t for KV head g.
-__device__ __forceinline__ void place(const GrowArgs& a, const Tables& w, const Head& h, int32_t g,
-                                      int32_t t, bool* bad) {
-  int32_t b;
-  if (a.cu) {
-    int32_t lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int32_t mid = (lo + hi) >> 1;
-      if (w.seq[mid].x <= t) lo = mid; else hi = mid;
-    }
-    b = lo;
-  } else {
-    b = t / a.span;
+// The sequence whose span token t is in, or the last one before it.
+__device__ __forceinline__ int32_t seq_of(const GrowArgs& a, const Tables& w, int32_t t) {
+  if (!a.cu) return a.span == 1 ? t : t / max(a.span, 1);
+  int32_t lo = 0, hi = a.batch;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (w.seq[mid].x <= t) lo = mid; else hi = mid;
   }
+  return lo;
+}
+
+// A token's place in a row: looked up first, then written, so that a thread's
+// look-ups are under way together.
+struct Place {
+  int64_t row = 0;
+  int32_t at = 0, page = 0, position = 0;
+  bool live = false, fresh = false;   // gets a slot; from a page that is new to the row
+};
+
+// Token t of sequence b for KV head g.  next: what pages the rows' next slots are
+// in, and top: the last of the free pages, the very last first (as far as these
+// are at hand: NULL and 0 where not).
+__device__ __forceinline__ Place look_up(const GrowArgs& a, const Tables& w, const Head& h,
+                                         int32_t g, int32_t t, int32_t b, const int32_t* next,
+                                         const int32_t* top, int32_t tops) {
+  Place p;
   const int4 s = w.seq[b];
   const int32_t i = t - s.x;
+  p.live = i >= 0 && i < s.z;
+  if (!p.live) return p;
+  const int32_t r = b * a.Hkv + g;
+  const int4 row = w.row[r];
+  p.row = r;
+  p.at = row.x + i;
+  p.position = s.w + i;
+  const int32_t e = p.at >> a.page_shift;
+  if (e < row.y) {
+    p.page = next && e == row.x >> a.page_shift ? next[r] : a.table[p.row * a.max_pages + e];
+  } else {
+    p.fresh = true;
+    const int32_t nth = row.z + e - row.y;         // from the stack's top
+    p.page = nth >= h.back && nth - h.back < tops
+                 ? top[nth - h.back]
+                 : page_at(a, w, h.free, h.free + h.back - 1 - nth);
+  }
+  return p;
+}
+
+// Writes the slot (and what goes with it) of token t for KV head g.
+__device__ __forceinline__ void put(const GrowArgs& a, const Place& p, int32_t g, int32_t t,
+                                    bool* bad) {
   int64_t slot = -1;
-  if (i >= 0 && i < s.z) {
-    const int64_t r = int64_t(b) * a.Hkv + g;
-    const int4 row = w.row[r];
-    const int32_t at = row.x + i, e = at >> a.page_shift;
-    int32_t page;
-    if (e < row.y) {
-      page = a.table[r * a.max_pages + e];
-    } else {
-      page = page_at(a, w, h.free, h.free + h.back - 1 - (row.z + e - row.y));
-      // (what a row holds ends within its own pages, so a new page starts with a
-      // new token)
-      if ((at & (a.page - 1)) == 0) a.table[r * a.max_pages + e] = page;
-    }
-    if (page >= 0 && page < a.num_pages)
-      slot = (int64_t(page) << a.page_shift) + (at & (a.page - 1));
+  if (p.live) {
+    const int32_t in_page = p.at & (a.page - 1);
+    // (what a row holds ends within its own pages, so a new page starts with a
+    // new token)
+    if (p.fresh && in_page == 0) a.table[p.row * a.max_pages + (p.at >> a.page_shift)] = p.page;
+    if (p.page >= 0 && p.page < a.num_pages)
+      slot = (int64_t(p.page) << a.page_shift) + in_page;
     else
       *bad = true;
-    const int64_t cell = r * (int64_t(a.max_pages) << a.page_shift) + at;
+    const int64_t cell = p.row * (int64_t(a.max_pages) << a.page_shift) + p.at;
     if (a.weights) a.weights[cell] = 0.f;
-    if (a.slot_positions) a.slot_positions[cell] = s.w + i;
+    if (a.slot_positions) a.slot_positions[cell] = p.position;
   }
   a.slots[int64_t(g) * a.tokens + t] = slot;
-  if (g == 0 && a.positions) a.positions[t] = i >= 0 && i < s.z ? s.w + i : 0;
+  if (g == 0 && a.positions) a.positions[t] = p.live ? p.position : 0;
 }
 
 // Pages given back that nobody took become free: row r's part of them.
 __device__ __forceinline__ void put_back(const GrowArgs& a, const Tables& w, const Head& h,
                                          int32_t r, int lane) {
   const int4 row = w.row[r];
-  const int32_t need = (row.x + w.seq[r / a.Hkv].y + a.page - 1) >> a.page_shift;
+  const int32_t need = (row.x + w.seq[seq_of_row(a, r)].y + a.page - 1) >> a.page_shift;
   for (int32_t k = lane; k < row.y - need && row.w + k < h.back - h.taken &&
                          h.free + row.w + k < a.num_pages; k += 32)
     a.free_pages[h.free + row.w + k] = a.table[int64_t(r) * a.max_pages + need + k];
 }
 
+// near: all sequences and rows fit into shared memory; inl: so do the tokens' slots
+// go with this launch.
+template <bool near, bool inl>
 __global__ void __launch_bounds__(kThreads)
-    grow_kernel(const __grid_constant__ GrowArgs a, Tables ws, int32_t inl) {
-  __shared__ int4 seq_s[kSeqRecords], row_s[kRecords];
-  __shared__ int32_t sum_w[32], sum_b[32];
+    grow_kernel(const __grid_constant__ GrowArgs a, Tables ws) {
+  __shared__ int4 seq_s[near ? kSeqRecords : 1], row_s[near ? kRecords : 1];
+  __shared__ int32_t sum_w[kWarps], sum_b[kWarps], most_s[near ? kSeqRecords : 1];
+  __shared__ int32_t top_s[inl ? kThreads : 1], next_s[inl ? kRecords : 1];
   __shared__ int32_t taken_s;
   sa_dev::launch_dependents();
   sa_dev::wait_dependency();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t rows = a.batch * a.Hkv, cap = a.max_pages << a.page_shift;
   Tables w = ws;
-  if (inl) {
+  if (near) {
     w.seq = seq_s;
     w.row = row_s;
   }
-  bool bad = false;
-  if (tid == 0) taken_s = 0;
-  int32_t free = *a.free_count;
-  if (free < 0 || free > a.num_pages) {
-    bad = true;
-    free = clamp_to(free, 0, int32_t(a.num_pages));
-  }
+  bool bad = false, bad_cu = false;
 
-  // what row r holds and owns
-  auto row_state = [&](int32_t r, bool ended, int32_t* held, int32_t* owned) {
-    int32_t n = a.lens[r], o = a.owned[r];
+  // What row r holds and owns, emptied where its sequence ended.
+  auto clean_row = [&](int32_t n, int32_t o, bool ended) -> int4 {
     if (o < 0 || o > a.max_pages) {
       bad = true;
       o = clamp_to(o, 0, a.max_pages);
@@ -157,51 +191,95 @@ __global__ void __launch_bounds__(kThreads)
       bad = true;
       n = clamp_to(n, 0, most);
     }
-    *held = ended ? 0 : n;
-    *owned = o;
+    return make_int4(ended ? 0 : n, o, 0, 0);
   };
+  auto ended = [&](int32_t b) { return a.ended && a.ended[b]; };
 
-  // spans that overlap would leave new pages unnamed: nobody gets any then
-  bool bad_cu = false;
-  if (a.cu)
-    for (int32_t b = tid; b <= a.batch; b += kThreads) {
-      const int32_t c = a.cu[b];
-      bad_cu |= c < 0 || c > a.tokens || (b > 0 && c < a.cu[b - 1]);
+  // Every load that depends on nothing first (then the rows' lengths are read).
+  int32_t free = *a.free_count;
+  if (tid == 0) taken_s = 0;
+  // (near: a thread has one sequence)
+  int32_t c0 = 0, c1 = 0, cnt = 0, start = 0;
+  bool end = false;
+  if (near && tid < a.batch) {
+    if (a.cu) {
+      c0 = a.cu[tid];
+      c1 = a.cu[tid + 1];
     }
+    if (a.counts) cnt = a.counts[tid];
+    if (a.start) start = a.start[tid];
+    end = ended(tid);
+    most_s[tid] = 0;
+  }
+  for (int32_t r = tid; r < rows; r += kThreads)
+    w.row[r] = clean_row(a.lens[r], a.owned[r], ended(seq_of_row(a, r)));
+  if (free < 0 || free > a.num_pages) {
+    bad = true;
+    free = clamp_to(free, 0, int32_t(a.num_pages));
+  }
+  // the pages that rows go on with, and those that the stack hands out first
+  // unless others were given back: on their way until the slots need them
+  constexpr int kMine = inl ? kRecords / kThreads : 1;
+  const int32_t tops = min(free, kThreads);
+  int32_t top = 0, next[kMine];
+  if (inl) {
+    if (tid < tops) top = a.free_pages[free - 1 - tid];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int32_t r = tid + i * kThreads;
+      next[i] = 0;
+      if (r < rows) {
+        const int32_t e = w.row[r].x >> a.page_shift;
+        if (e < w.row[r].y) next[i] = a.table[int64_t(r) * a.max_pages + e];
+      }
+    }
+  }
+  // spans that overlap would leave new pages unnamed: nobody gets any then
+  if (near) {
+    bad_cu = a.cu && tid < a.batch && (c0 < 0 || c1 < c0 || c1 > a.tokens);
+  } else if (a.cu) {
+    for (int32_t b = tid; b < a.batch; b += kThreads)
+      bad_cu |= a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.tokens;
+  }
   bad_cu = __syncthreads_or(bad_cu);
   bad |= bad_cu;
-
+  // the longest row of each sequence
+  if (near) {
+    for (int32_t r = tid; r < rows; r += kThreads) atomicMax(&most_s[seq_of_row(a, r)], w.row[r].x);
+    __syncthreads();
+  }
   // sequences: their tokens' span and what they ask for
   for (int32_t b = tid; b < a.batch; b += kThreads) {
-    int32_t first, span;
-    if (a.cu) {
-      first = bad_cu ? 0 : a.cu[b];
-      span = bad_cu ? 0 : a.cu[b + 1] - first;
+    int32_t first = b * a.span, span = a.span, most = 0;
+    if (near) {
+      most = most_s[b];
     } else {
-      first = b * a.span;
-      span = a.span;
+      if (a.cu) {
+        c0 = a.cu[b];
+        c1 = a.cu[b + 1];
+      }
+      if (a.counts) cnt = a.counts[b];
+      if (a.start) start = a.start[b];
+      end = ended(b);
+      for (int32_t g = 0; g < a.Hkv; ++g) most = max(most, w.row[b * a.Hkv + g].x);
+    }
+    if (a.cu) {
+      first = bad_cu ? 0 : c0;
+      span = bad_cu ? 0 : c1 - c0;
     }
     int32_t c = span;
     if (a.counts) {
-      c = a.counts[b];
+      c = cnt;
       if (c < 0 || c > span) {
         bad = true;
         c = clamp_to(c, 0, span);
       }
     }
-    const bool ended = a.ended && a.ended[b];
-    int32_t most = 0;
-    for (int32_t g = 0; g < a.Hkv; ++g) {
-      int32_t held, owned;
-      row_state(b * a.Hkv + g, ended, &held, &owned);
-      most = max(most, held);
-    }
     if (c > cap - most) {              // more than the row's table holds: none
       bad = true;
       c = 0;
     }
-    const int32_t start = a.start ? (ended ? 0 : a.start[b]) : most;
-    w.seq[b] = make_int4(first, c, 0, start);
+    w.seq[b] = make_int4(first, c, 0, a.start ? (end ? 0 : start) : most);
   }
   __syncthreads();
 
@@ -211,9 +289,9 @@ __global__ void __launch_bounds__(kThreads)
     const int32_t r = base + tid;
     int32_t held = 0, owned = 0, want = 0, back = 0;
     if (r < rows) {
-      const int32_t b = r / a.Hkv;
-      row_state(r, a.ended && a.ended[b], &held, &owned);
-      const int32_t need = (held + w.seq[b].y + a.page - 1) >> a.page_shift;
+      held = w.row[r].x;
+      owned = w.row[r].y;
+      const int32_t need = (held + w.seq[seq_of_row(a, r)].y + a.page - 1) >> a.page_shift;
       want = max(0, need - owned);
       back = max(0, owned - need);
     }
@@ -223,7 +301,8 @@ __global__ void __launch_bounds__(kThreads)
       sum_b[warp] = ib;
     }
     __syncthreads();
-    const int32_t tw = scan_warp(sum_w[lane], lane), tb = scan_warp(sum_b[lane], lane);
+    const int32_t tw = scan_warp(lane < kWarps ? sum_w[lane] : 0, lane);
+    const int32_t tb = scan_warp(lane < kWarps ? sum_b[lane] : 0, lane);
     const int32_t before_w = __shfl_sync(0xffffffffu, tw, warp ? warp - 1 : 0);
     const int32_t before_b = __shfl_sync(0xffffffffu, tb, warp ? warp - 1 : 0);
     if (r < rows)
@@ -249,9 +328,14 @@ __global__ void __launch_bounds__(kThreads)
     if (a.granted) a.granted[b] = s.z;
     if (a.start_out) a.start_out[b] = s.w + s.z;
   }
+  if (inl) {
+    top_s[tid] = top;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) next_s[tid + i * kThreads] = next[i];
+  }
   __syncthreads();
   for (int32_t r = tid; r < rows; r += kThreads) {
-    const int4 row = w.row[r], s = w.seq[r / a.Hkv];
+    const int4 row = w.row[r], s = w.seq[seq_of_row(a, r)];
     a.lens_out[r] = row.x + s.z;
     const int32_t need = (row.x + s.y + a.page - 1) >> a.page_shift;
     // without a grant a row keeps what it has of the pages that it asked for
@@ -262,14 +346,21 @@ __global__ void __launch_bounds__(kThreads)
     *a.free_count_out = min(h.free + h.back - h.taken, int32_t(a.num_pages));
     if (!inl) *ws.head = h;
   }
+  if (near && !inl) {                  // for the second launch
+    for (int32_t b = tid; b < a.batch; b += kThreads) ws.seq[b] = w.seq[b];
+    for (int32_t r = tid; r < rows; r += kThreads) ws.row[r] = w.row[r];
+  }
   bool bad_page = false;
   if (inl) {
-    for (int32_t x = tid; x < a.tokens * a.Hkv; x += kThreads) {
-      const int32_t g = x / a.tokens;
-      place(a, w, h, g, x - g * a.tokens, &bad_page);
+    // 32 tokens of a head a warp at a time
+    const int32_t chunks = (a.tokens + 31) / 32;
+    for (int32_t u = warp; u < a.Hkv * chunks; u += kWarps) {
+      const int32_t g = u / chunks, t = (u - g * chunks) * 32 + lane;
+      if (t < a.tokens)
+        put(a, look_up(a, w, h, g, t, seq_of(a, w, t), next_s, top_s, tops), g, t, &bad_page);
     }
     if (h.back > h.taken)
-      for (int32_t r = warp; r < rows; r += kThreads / 32) put_back(a, w, h, r, lane);
+      for (int32_t r = warp; r < rows; r += kWarps) put_back(a, w, h, r, lane);
   }
   if (bad) atomicOr(a.dev_status, SA_DEV_BAD_COUNT);
   if (bad_page) atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
@@ -277,18 +368,39 @@ __global__ void __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kSpread)
     spread_kernel(const __grid_constant__ GrowArgs a, Tables w) {
+  __shared__ int4 seq_s[kSpreadSeqs], row_s[kSpreadRows];
   sa_dev::launch_dependents();
   sa_dev::wait_dependency();
+  const int32_t rows = a.batch * a.Hkv;
   const Head h = *w.head;
+  if (a.batch <= kSpreadSeqs && rows <= kSpreadRows) {
+    for (int32_t b = threadIdx.x; b < a.batch; b += kSpread) seq_s[b] = w.seq[b];
+    for (int32_t r = threadIdx.x; r < rows; r += kSpread) row_s[r] = w.row[r];
+    w.seq = seq_s;
+    w.row = row_s;
+    __syncthreads();
+  }
   bool bad = false;
   const int32_t t = int32_t(blockIdx.x) * kSpread + int32_t(threadIdx.x);
-  if (t < a.tokens)
-    for (int32_t g = blockIdx.y; g < a.Hkv; g += gridDim.y) place(a, w, h, g, t, &bad);
+  if (t < a.tokens) {
+    const int32_t b = seq_of(a, w, t);
+    // a block's heads: an equal part of all
+    const int32_t g1 = int32_t(int64_t(a.Hkv) * (blockIdx.y + 1) / gridDim.y);
+    for (int32_t g0 = int32_t(int64_t(a.Hkv) * blockIdx.y / gridDim.y); g0 < g1;
+         g0 += kSpreadHeads) {
+      Place p[kSpreadHeads];
+#pragma unroll
+      for (int i = 0; i < kSpreadHeads; ++i)
+        if (g0 + i < g1) p[i] = look_up(a, w, h, g0 + i, t, b, nullptr, nullptr, 0);
+#pragma unroll
+      for (int i = 0; i < kSpreadHeads; ++i)
+        if (g0 + i < g1) put(a, p[i], g0 + i, t, &bad);
+    }
+  }
   if (h.back > h.taken) {
     const int64_t warps = int64_t(gridDim.x) * gridDim.y * (kSpread / 32);
     int64_t r = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kSpread / 32) + (threadIdx.x >> 5);
-    for (; r < int64_t(a.batch) * a.Hkv; r += warps)
-      put_back(a, w, h, int32_t(r), threadIdx.x & 31);
+    for (; r < rows; r += warps) put_back(a, w, h, int32_t(r), threadIdx.x & 31);
   }
   if (bad) atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
 }
@@ -308,8 +420,8 @@ cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st) {
   Tables w{reinterpret_cast<Head*>(ws), reinterpret_cast<int4*>(ws + 256),
            reinterpret_cast<int4*>(ws + 256 + up(size_t(a.batch) * 16))};
   const int64_t rows = int64_t(a.batch) * a.Hkv;
-  const bool inl = int64_t(a.tokens) * a.Hkv <= kInlinePairs && rows <= kRecords &&
-                   a.batch <= kSeqRecords;
+  const bool near = rows <= kRecords && a.batch <= kSeqRecords;
+  const bool inl = near && int64_t(a.tokens) * a.Hkv <= kInlinePairs;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -319,10 +431,15 @@ cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, grow_kernel, a, w, int32_t(inl));
+  cudaError_t e = inl    ? cudaLaunchKernelEx(&cfg, grow_kernel<true, true>, a, w)
+                  : near ? cudaLaunchKernelEx(&cfg, grow_kernel<true, false>, a, w)
+                         : cudaLaunchKernelEx(&cfg, grow_kernel<false, false>, a, w);
   if (e != cudaSuccess || inl) return e;
-  cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, (int64_t(a.tokens) + kSpread - 1) / kSpread)),
-                     unsigned(std::min(a.Hkv, 256)));
+  // blocks of 256 tokens; their heads are split where there are few of them
+  const int64_t blocks = std::max<int64_t>(1, (int64_t(a.tokens) + kSpread - 1) / kSpread);
+  const int64_t parts = (a.Hkv + kSpreadHeads - 1) / kSpreadHeads;
+  cfg.gridDim = dim3(unsigned(blocks),
+                     unsigned(std::min<int64_t>({parts, std::max<int64_t>(1, 1024 / blocks), 256})));
   cfg.blockDim = dim3(kSpread);
   return cudaLaunchKernelEx(&cfg, spread_kernel, a, w);
 }

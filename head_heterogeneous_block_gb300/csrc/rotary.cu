@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.h"
 #include "ptx.cuh"
@@ -176,11 +177,20 @@ template <int D>
 cudaError_t launch_d(const RotaryArgs& a, int sms, cudaStream_t st) {
   constexpr int kHeads = 32 / (D / 16);
   const int32_t all = (a.Hq + a.Hkv + (a.slots ? a.Hkv : 0) + kHeads - 1) / kHeads;
-  // few tokens: a step a warp, for latency; many: up to 12 steps, which share
-  // the token's sines
-  if (int64_t(a.tokens) * all <= int64_t(sms) * 16) return launch<D, 1>(a, 1, all, st);
-  const int32_t chunks = (all + 11) / 12;
-  return launch<D, 4>(a, (all + chunks - 1) / chunks, chunks, st);
+  // Steps of all tokens a processor: up to 16 (64 tokens of 32 + 8 heads, d =
+  // 128: 2.2 us) a step a warp, for latency; up to 48 two (512 tokens: 3.5 us,
+  // against 4.0 with one and 4.2 with four); up to 220 four (2049 tokens: 7.8
+  // us, against 9.0 with two and 9.3 with twelve); then twelve, which share the
+  // token's sines (16384 tokens: 68 us, against 74 with four)
+  const int64_t load = int64_t(a.tokens) * all / sms;
+  auto with = [&](int32_t steps, auto unroll) {
+    const int32_t chunks = (all + steps - 1) / steps;
+    return launch<D, decltype(unroll)::value>(a, (all + chunks - 1) / chunks, chunks, st);
+  };
+  if (load <= 16) return with(1, std::integral_constant<int, 1>{});
+  if (load <= 48) return with(2, std::integral_constant<int, 2>{});
+  if (load <= 220) return with(4, std::integral_constant<int, 2>{});
+  return with(12, std::integral_constant<int, 4>{});
 }
 
 }  // namespace

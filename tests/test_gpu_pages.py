@@ -217,3 +217,26 @@ def test_streams_and_graphs(sa):
         side.wait_stream(torch.cuda.current_stream())
     assert all(torch.equal(d[k], end[k]) for k in end)
     assert int(pool.dev_status.item()) == 0
+
+
+def test_steps_one_behind_the_other_on_used_shared_memory(sa):
+    # other kernels leave their own values in shared memory, and launches overlap
+    b, h, page = 64, 8, 16
+    s = state(9, b, h, page, 501, 8000, free=b * h)
+    d, pool = to_gpu(sa, s)
+    att = sa.PackedAttention(8, 2, 64)
+    q = torch.randn(300, 8, 64, device="cuda").bfloat16()
+    cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+    slots = torch.zeros(h, b, dtype=torch.int64, device="cuda")
+    out = {k: torch.zeros_like(d[k]) for k in ("lens", "owned", "free_count")}
+    ref = opg.grow(s["table"], s["lens"], s["owned"], s["free"], page, [(x, x + 1) for x in range(b)], tokens=b)
+    for _ in range(40):
+        att(q, q[:, :2], q[:, 2:4], cu)
+        for _ in range(3):
+            pool.grow(slots, lens_out=out["lens"], owned_out=out["owned"], free_count_out=out["free_count"])
+    torch.cuda.synchronize()
+    assert int(pool.dev_status.item()) == 0
+    np.testing.assert_array_equal(slots.cpu().numpy(), ref["slots"])
+    np.testing.assert_array_equal(out["lens"].cpu().numpy(), ref["lens"])
+    np.testing.assert_array_equal(out["owned"].cpu().numpy(), ref["owned"])
+    assert int(out["free_count"]) == len(ref["free"])
