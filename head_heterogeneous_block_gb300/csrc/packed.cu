@@ -74,7 +74,7 @@ constexpr int kSoftmaxThreads = 512;
 constexpr int kOutThreads = 128;
 constexpr int kThreads = 128 + kSoftmaxThreads + kOutThreads;
 constexpr int kNI = 4;                // item descriptions in flight
-constexpr int kBatch = 2048;          // items between two looks at what is to be done again
+constexpr int kBatch = 512;           // items between two looks at what is to be done again
 constexpr int kDirectBlocks = 8;      // key blocks of a tile that is not worth cutting
 constexpr int kRounds = 8;            // at most, of head groups, so that a round's keys and values stay in L2
 constexpr int kItemCost = 2;          // what an item costs beside its blocks, in blocks
@@ -87,7 +87,7 @@ constexpr int kJoinRows = 16;         // rows of a join unit
 
 // Registers of a thread by role, together the launch's 768 x 80: the control
 // warps give up what the output warps, a whole row each, need.
-constexpr int kControlRegs = 56, kSoftmaxRegs = 72, kOutRegs = 136;
+constexpr int kControlRegs = 64, kSoftmaxRegs = 72, kOutRegs = 128;
 static_assert(128 * kControlRegs + kSoftmaxThreads * kSoftmaxRegs + kOutThreads * kOutRegs <=
                   kThreads * 80,
               "a larger sum would wait forever");
@@ -106,7 +106,7 @@ struct Cfg {
   static constexpr int kCols = kBK / 4;             // S columns of a softmax group
   static constexpr uint32_t kO = kNS * kBK;         // TMEM column of O
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr int kData = kNQ * kQBytes + (kNK + kNV) * kKVBytes;
+  static constexpr int kData = kNQ * kQBytes + (kNK + kNV) * kKVBytes + kQPanel;
 };
 
 // One tile, or a range of its key blocks, in the schedule.
@@ -151,7 +151,7 @@ struct Shared {
   uint64_t o_free;        // a phase per item: O is in registers
   uint64_t xch_bar;       // exchanges between the softmax groups
   uint64_t sum_full[2], sum_empty[2];   // items in turn: the rows' sums
-  uint64_t stage_bar[2];  // items in turn: the output is staged or stored
+  uint64_t stage_full, stage_empty;     // a phase per panel of an output tile
   uint64_t batch_done;    // a phase per marker: every output before it is through
   uint64_t drain_qk, drain_pv;
   uint64_t info_full[kNI], info_empty[kNI];
@@ -163,7 +163,6 @@ struct Shared {
   float sum[2][4][kRows];     // per softmax group: sums of rounded weights
   float sum_x[2][4][kRows];   // and of unrounded ones, for the log-sum-exp
   float ref[2][kRows];        // the rows' references
-  int32_t stage_q0[2], stage_h[2];   // where the tile staged in Q stage x goes; q0 < 0: nowhere
   int32_t bad_v[2];       // item (by its number, from 1) that met infinities or NaN in masked blocks
   uint32_t tmem_base;
   int abort;
@@ -586,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem_raw;
   uint8_t* sK = sQ + C::kNQ * C::kQBytes;
   uint8_t* sV = sK + C::kNK * C::kKVBytes;
-  Shared* sh = reinterpret_cast<Shared*>(sV + C::kNV * C::kKVBytes);
+  uint8_t* sO = sV + C::kNV * C::kKVBytes;       // a panel of an output tile
+  Shared* sh = reinterpret_cast<Shared*>(sO + C::kQPanel);
   volatile int* abort = &sh->abort;
 
   const int warp = threadIdx.x >> 5;
@@ -595,10 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->q_full[s], 1);
-      mbar_init(&sh->q_empty[s], 2);   // the last Q K^T, and the output tile leaving the stage
+      mbar_init(&sh->q_empty[s], 1);
       mbar_init(&sh->sum_full[s], kSoftmaxThreads);
       mbar_init(&sh->sum_empty[s], kOutThreads);
-      mbar_init(&sh->stage_bar[s], kOutThreads);
     }
     for (int s = 0; s < C::kNK; ++s) {
       mbar_init(&sh->k_full[s], 1);
@@ -615,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->info_full[s], 1);
       mbar_init(&sh->info_empty[s], 3 + (kSoftmaxThreads + kOutThreads) / 32);
     }
+    mbar_init(&sh->stage_full, kOutThreads);
+    mbar_init(&sh->stage_empty, 1);
     mbar_init(&sh->o_last, 1);
     mbar_init(&sh->o_free, kOutThreads);
     mbar_init(&sh->xch_bar, kSoftmaxThreads);
@@ -936,46 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_pv = idesc_bf16(kRows, D, 0, 1);   // P (TMEM), V MN-major
     uint32_t ii = 0, qi = 0, stage = 0, phase = 0, vstage = 0, vphase = 0;
     bool ok = true;
-    // This warp also writes the staged output tiles, one TMA store per panel,
-    // and releases their Q stages, while it would wait for P.  Item x must be
-    // stored before P V of item x+2 is issued (then no output warp can be two
-    // items ahead on the same barrier); until then it is looked for between blocks.
-    uint32_t spq = 0;
-    auto store_upto = [&](uint32_t upto, bool wait) -> bool {
-      for (; spq < upto; ++spq) {
-        uint64_t* bar = &sh->stage_bar[spq & 1];
-        const uint32_t par = (spq >> 1) & 1;
-        if (!wait && !__shfl_sync(0xffffffffu, lane == 0 && mbar_test(bar, par), 0)) return true;
-        if (wait && !warp_wait(bar, par, abort, p.wait_ns)) return false;
-        if (lane == 0) {
-          const int32_t q0 = sh->stage_q0[spq & 1], h0 = sh->stage_h[spq & 1];
-          if (q0 >= 0) {
-            const uint8_t* stg = sQ + (spq % C::kNQ) * C::kQBytes;
-            const uint64_t pol = l2_policy_evict_first();
-#pragma unroll
-            for (int s = 0; s < C::kPanels; ++s)
-              tma_store_3d_hint(&to, stg + s * C::kQPanel, s * 64, h0, q0, pol);
-            bulk_commit_group();
-            bulk_wait_read_all();
-          }
-          mbar_arrive(&sh->q_empty[spq % C::kNQ]);
-        }
-        __syncwarp();
-      }
-      return true;
-    };
     for (;; ++ii) {
       const int slot = ii % kNI;
-      // the next description may come only after the tile before this one has
-      // left its Q stage
-      const uint64_t t0 = spq < qi ? global_ns() : 0;
-      while (ok && spq < qi &&
-             !__shfl_sync(0xffffffffu,
-                          lane == 0 && mbar_test(&sh->info_full[slot], (ii / kNI) & 1), 0)) {
-        store_upto(qi, false);
-        ok = !__any_sync(0xffffffffu, *abort || global_ns() - t0 > p.wait_ns);
-      }
-      if (!ok) break;
       if (!warp_wait(&sh->info_full[slot], (ii / kNI) & 1, abort, p.wait_ns)) {
         ok = false;
         break;
@@ -985,20 +948,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
       if (n == kEnd) break;
-      if (n == kMarker) {
-        // every tile before it is stored, and complete before a careful item
-        // may write its rows again
-        ok = store_upto(qi, true);
-        if (!ok) break;
-        if (lane == 0) bulk_wait_all();
-        __syncwarp();
-        continue;
-      }
+      if (n == kMarker) continue;
       for (int32_t t = 0; t < lead + n; ++t) {
-        if (!(t == 0 && qi > 0 ? store_upto(qi - 1, true) : store_upto(qi, false))) {
-          ok = false;
-          break;
-        }
         const bool skip = t < lead, first = t == lead;
         const bool need_o = first && qi > 0;   // the previous epilogue has read O
         // lane 0: P, lane 1: V, lane 2: O
@@ -1060,10 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++qi;
     }
-    if (ok) ok = store_upto(qi, true);
     if (lane == 0) {
       if (!ok) raise_abort(sh, p);
-      bulk_wait_all();   // the stores read this CTA's shared memory
       mma_commit(&sh->drain_pv);
       mbar_wait(&sh->drain_pv, 0, nullptr);
     }
@@ -1263,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = row / p.tile_heads;
     const int head = row - tok * p.tile_heads;
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + C::kO;
-    uint32_t ii = 0, qi = 0;
+    uint32_t ii = 0, qi = 0, panels = 0;   // panels: staged so far
     bool ok = true;
     for (;; ++ii) {
       const uint32_t slot = ii % kNI;
@@ -1277,6 +1226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
         if (n == kEnd) break;
+        // complete before a careful item may write its rows again
+        if (row == 0) bulk_wait_all();
         mbar_arrive(&sh->batch_done);
         continue;
       }
@@ -1307,15 +1258,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = whole ? 1.f / l : 1.f;
       __nv_bfloat16* direct = p.o + (int64_t(it.e.q0) + tok) * p.o_st +
                               int64_t(it.head0 + head) * p.o_sh;
-      uint8_t* stg = sQ + (qi % C::kNQ) * C::kQBytes + row * 128;
       float4* part = p.part_o + int64_t(whole ? 0 : it.e.slot) * (D / 4) * kRows + row;
       const bool blank = __any_sync(0xffffffffu, !some);     // rarely: a branch
       const bool dirty = it.careful && *(volatile int32_t*)&sh->bad_v[w] == int32_t(qi + 1);
       float osum = 0.f, osum2 = 0.f;
-      // 32 columns of O: a full tile is staged in its Q stage (128-byte
-      // swizzled, as TMA stores read it), rows of other tiles go out as they are,
-      // ranges unnormalised and fp32 to their slot
-      auto emit = [&](uint32_t (&r)[32], int col) {
+      // 32 columns of O, normalised and packed; of a range, as they are to its slot
+      uint32_t ob[D / 2];
+      auto finish = [&](uint32_t (&r)[32], int col) {
         if (blank && !some) {
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = 0u;
@@ -1336,8 +1285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 32; x += 2)
           add2(osum, osum2, __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
-        if (!live) return;
         if (!whole) {
+          if (!live) return;
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             part[(col / 4 + x) * kRows] =
@@ -1346,20 +1295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           return;
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t ob[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float a0, a1;
-            mul2(a0, a1, __uint_as_float(r[8 * x + 2 * y]),
-                 __uint_as_float(r[8 * x + 2 * y + 1]), inv, inv);
-            ob[y] = pack_bf16x2(a0, a1);
-          }
-          const int c16 = col / 8 + x;
-          uint4* dst = staged ? reinterpret_cast<uint4*>(stg + c16 / 8 * C::kQPanel +
-                                                         ((c16 % 8 ^ (row & 7)) << 4))
-                              : reinterpret_cast<uint4*>(direct + col) + x;
-          *dst = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        for (int x = 0; x < 16; ++x) {
+          float a0, a1;
+          mul2(a0, a1, __uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]), inv, inv);
+          ob[col / 2 + x] = pack_bf16x2(a0, a1);
         }
       };
       if (!wait_all(&sh->o_last, qi & 1, abort, p.wait_ns)) {
@@ -1367,16 +1306,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      // the whole row at once: the next item's first P V may then overwrite O
-      uint32_t r[D / 32][32];
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) tmem_ld32(lanes + 32 * x, r[x]);
+      for (int s = 0; s < C::kPanels; ++s) {
+        uint32_t r0[32], r1[32];
+        tmem_ld32(lanes + 64 * s, r0);
+        tmem_ld32(lanes + 64 * s + 32, r1);
+        tmem_ld_wait(r0);
+        tmem_ld_wait(r1);
+        if (s == C::kPanels - 1) {
+          // O is read: the next item's first P V may overwrite it
+          tc_fence_before();
+          mbar_arrive(&sh->o_free);
+        }
+        finish(r0, 64 * s);
+        finish(r1, 64 * s + 32);
+      }
+      if (staged) {
+        // panel by panel through the buffer, 128-byte swizzled as TMA stores read it
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) tmem_ld_wait(r[x]);
-      tc_fence_before();
-      mbar_arrive(&sh->o_free);
+        for (int s = 0; s < C::kPanels; ++s) {
+          if (panels > 0 && !wait_all(&sh->stage_empty, (panels - 1) & 1, abort, p.wait_ns)) {
+            ok = false;
+            break;
+          }
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) emit(r[x], 32 * x);
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(sO + row * 128 + ((x ^ (row & 7)) << 4)) =
+                make_uint4(ob[32 * s + 4 * x], ob[32 * s + 4 * x + 1], ob[32 * s + 4 * x + 2],
+                           ob[32 * s + 4 * x + 3]);
+          fence_proxy_async_smem();
+          mbar_arrive(&sh->stage_full);
+          if (warp == 20) {
+            if (!warp_wait(&sh->stage_full, panels & 1, abort, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              // evict-first: the output is not read here again
+              tma_store_3d_hint(&to, sO, s * 64, it.head0, it.e.q0, l2_policy_evict_first());
+              bulk_commit_group();
+              bulk_wait_read_all();
+              mbar_arrive(&sh->stage_empty);
+            }
+            __syncwarp();
+          }
+          ++panels;
+        }
+        if (!ok) break;
+      } else if (whole && live) {
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+          reinterpret_cast<uint4*>(direct)[x] =
+              make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
+      }
       // the range that the first pass keeps: the sum up to 2^126 (so that no
       // weight overflowed) and O finite
       if (!it.careful && live && some && !(in_range && fabsf(osum + osum2) <= 3.0e38f)) {
@@ -1390,17 +1372,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
             some ? (m + log2f(lx)) * 0.6931471805599453f : -INFINITY;
       }
-      if (staged) fence_proxy_async_smem();
-      if (row == 0) {
-        sh->stage_q0[w] = staged ? it.e.q0 : -1;
-        sh->stage_h[w] = it.head0;
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
-      mbar_arrive(&sh->stage_bar[w]);   // the P V issuer goes on from here
       ++qi;
     }
     if (!ok) raise_abort(sh, p);
+    if (row == 0) bulk_wait_all();   // the stores read this CTA's shared memory
     tmem_ld_wait();
     tc_fence_before();
   }
