@@ -14,42 +14,66 @@
 // heads is the largest divisor of the group up to 16 that leaves at most 3 of
 // the 128 rows unused (7 heads: 18 tokens, 126 rows).
 //
-// Schedule.  One CTA per processor takes items (a tile, a range of its key
-// blocks) from a counter.  A first, one-CTA launch reads the lengths and lists
-// the tiles, those with most key blocks first (a counting sort), so that what is
-// left at the end is short; KV head by KV head where the keys and values of all
-// heads would not stay in L2.  A tile that has more blocks than a processor's
-// fair share of all blocks is cut into ranges: each leaves its maximum, sums and
-// unnormalised output, and the CTA that finishes last joins them in order.
-// Where every tile gets a CTA of its own and no range is long, the CTAs find
-// their tiles themselves and there is no first launch.
+// Schedule.  One CTA per processor runs items: a tile, or a range of its key
+// blocks.  A first, one-CTA launch reads the lengths (a captured call follows
+// them) and either
+//   lists the tiles, those with most key blocks first (a counting sort), for the
+//   CTAs to take from a counter; KV head by KV head where the keys and values of
+//   all heads would not stay in L2: whole prompts, whose short tiles make an even
+//   end; or,
+//   where sequences have more keys than queries, cuts all blocks into equal
+//   shares, a CTA each; tiles at a share's end are cut, their ranges leave their
+//   reference, sums and unnormalised output, and a third launch joins them in key
+//   order.  Head groups go round by round, so that a round's keys and values stay
+//   in L2: chunks of 509 tokens behind 32K to 64K, 64/8 heads: 1.36 ms, against
+//   1.43 from the counter (512 items of two lengths do not divide by 152) and
+//   1.53 with rounds of 100 MB instead of 50.
+// Where every tile gets a CTA of its own the CTAs find their tiles themselves and
+// there is no first launch.
 //
-// Roles of the twenty warps: 0 producer (items, Q, K), 1 issues Q K^T into
-// one of three S buffers of tensor memory, 2 producer of V, 3 issues P V (P in
-// tensor memory over its S, O accumulates in tensor memory) and stores full
-// output tiles, 4-19 softmax: four column groups of four warps, a thread owns
-// one row and a quarter of its columns.
+// Roles of the 24 warps: 0 producer (items, Q, K; it looks items up ahead and
+// loads the next one's Q while this one's K blocks are on their way), 1 issues
+// Q K^T into one of three S buffers of tensor memory, 2 producer of V, 3 issues
+// P V (P in tensor memory over its S, O accumulates in tensor memory), 4-19
+// softmax: four column groups of four warps, a thread has one row and a quarter
+// of its columns, 20-23 output: a thread has a row of O.  Registers are dealt out
+// by role.
 //
 // Softmax.  The reference m of a row is its maximum over the item's first
 // block, exchanged once between the groups; later weights may pass 1 and m
 // cancels in O / l.  bf16 has fp32's exponents, so that is exact until a sum
-// passes 2^126 (or O overflows).  An item with such a row is done again after
-// the others ("careful"): first Q K^T alone for the rows' true maxima, then as
-// before with these as m.  It costs 1.5 times an item, whatever the values, and
-// nothing on the common path, which is bound by the softmax warps' issue slots.
-// The weights are rounded to bf16 for the tensor cores; the sum that divides O
-// adds the rounded ones, so that a row of one dominant weight gives its value
-// exactly.  The log-sum-exp adds the unrounded ones.
+// passes 2^126 (or O overflows).  An item with such a row is done again behind
+// the others: first Q K^T alone for the rows' true maxima, then as before with
+// these as m.  It costs 1.5 times an item, whatever the values, and nothing on the
+// common path.  The weights are rounded to bf16 for the tensor cores; the sum that
+// divides O adds the rounded ones, so that a row of one dominant weight gives its
+// value exactly.  The log-sum-exp adds the unrounded ones.
 //
 // Masked places.  Scores of keys that a row does not see become -infinity
 // whatever they are.  Their values meet weights of 0 in the tensor core, which
-// infinities and NaN survive: in the blocks where the mask cuts (at most two a
-// tile), the softmax warps zero such elements of V in shared memory, and the
-// rows that do see them add them back from global memory at the end.
+// infinities and NaN survive: a row whose O is not finite has its item done again
+// too, with such elements of V zeroed in shared memory in the blocks where the
+// mask cuts (at most two a tile); the rows that do see them add them back from
+// global memory at the end.
 //
 // Every wait is bounded; on a timeout the CTA flags SA_DEV_TIMEOUT, lets its
 // copies and MMAs drain, frees its tensor memory and exits.  No CTA waits for
 // another.
+//
+// Measured (GB300; bf16 peak 1937 TFLOP/s, masked halves of blocks not counted as
+// work): a prompt of 32768 tokens, 32/8 heads, d = 128: 5.9 ms, 1480 TFLOP/s, 76%;
+// 16 prompts of 1 to 4096, 28/4 heads: 478 us, 1340 TFLOP/s, 69%; the chunks
+// above: 1210 TFLOP/s, 62%; 24 prompts of 1 to 1024, 8/2 heads, d = 64: 30 us; one
+// of 41 tokens: 10 us.  The tensor pipe is busy 49% of the 16 prompts' time, issue
+// slots 48%: what is left is the chain from S through softmax and P V back to the
+// S buffer, of which three are in flight (512 columns hold no fourth), Q K^T's
+// operands in shared memory (a step of 128 x 128 x 16 takes some 100 cycles where
+// 64 are ideal), and 1.4 us an item at its ends.  Two sets of eight softmax warps
+// on every other block each came 3% slower for the 16 prompts and 1% for the long
+// one.  The 16 prompts, step by step: 513 us with softmax warps that also write
+// the output and scan V in every block that the mask cuts; 505 with output warps;
+// 482 with the output through a buffer of its own instead of the items' Q stages,
+// whose next loads then waited for it.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -137,7 +161,7 @@ struct __align__(16) Item {
   int32_t head0, g;       // first query head, KV head
   int32_t mt;             // blocks before the first masked one
   int32_t pos;            // place in the batch of items
-  int32_t careful;        // kAgain bits
+  int32_t careful;        // kClean, kMaxima
   int32_t pad[3];
 };
 enum { kEnd = 0, kMarker = -1 };      // values of e.n that are not items
@@ -164,7 +188,8 @@ struct Shared {
   float sum_x[2][4][kRows];   // and of unrounded ones, for the log-sum-exp
   float ref[2][kRows];        // the rows' references
   int32_t any_again;      // one item: it is to be done again
-  int32_t bad_v[2];       // item (by its number, from 1) that met infinities or NaN in masked blocks
+  int32_t bad_v[kNI];     // per description: the item (by its number, from 1) that met
+                          // infinities or NaN in masked blocks
   uint32_t tmem_base;
   int abort;
 };
@@ -625,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->drain_qk, 1);
     mbar_init(&sh->drain_pv, 1);
     sh->abort = 0;
-    sh->bad_v[0] = sh->bad_v[1] = sh->any_again = 0;
+    for (int s = 0; s < kNI; ++s) sh->bad_v[s] = 0;
+    sh->any_again = 0;
     fence_mbar_init();
   }
   for (int x = threadIdx.x; x < kBatch / 32; x += kThreads) sh->again[x] = sh->maxima[x] = 0;
@@ -1091,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Infinities and NaN of a V block that the mask cuts become 0 in shared
     // memory (this thread's share of the stage); the item is marked.
-    auto clean_v = [&](uint32_t item) {
+    auto clean_v = [&](uint32_t item, uint32_t slot) {
       uint8_t* stage = sV + (vb % C::kNV) * C::kKVBytes;
       const int x = (warp - 4) * 32 + lane;
 #pragma unroll 1
@@ -1104,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 0x8000 in each bad half -> 0xffff
           auto wipe = [](uint32_t v, uint32_t b) { return v & ~((b >> 15) * 0xffffu); };
           *at = make_uint4(wipe(w.x, b0), wipe(w.y, b1), wipe(w.z, b2), wipe(w.w, b3));
-          *(volatile int32_t*)&sh->bad_v[item & 1] = int32_t(item + 1);
+          *(volatile int32_t*)&sh->bad_v[slot] = int32_t(item + 1);
           fence_proxy_async_smem();
         }
       }
@@ -1176,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            clean_v(qi);
+            clean_v(qi, slot);
           }
         }
         ++vb;
@@ -1287,7 +1313,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                               int64_t(it.head0 + head) * p.o_sh;
       float4* part = p.part_o + int64_t(whole ? 0 : it.e.slot) * (D / 4) * kRows + row;
       const bool blank = __any_sync(0xffffffffu, !some);     // rarely: a branch
-      const bool dirty = it.careful && *(volatile int32_t*)&sh->bad_v[w] == int32_t(qi + 1);
+      // (the softmax warps may be two items ahead, but not at the next item of this
+      // description's place)
+      const bool dirty =
+          it.careful && *(volatile int32_t*)&sh->bad_v[slot] == int32_t(qi + 1);
       float osum = 0.f, osum2 = 0.f;
       // 32 columns of O, normalised and packed; of a range, as they are to its slot
       uint32_t ob[D / 2];

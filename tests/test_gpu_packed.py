@@ -242,3 +242,31 @@ def test_a_wait_that_runs_out(sa):
     att.dev_status.zero_()
     tp.same(att(q, k, v, cq, ck), ref)
     assert int(att.dev_status.item()) == 0
+
+
+def test_more_items_than_a_batch_of_a_cta(sa):
+    # one token a sequence: the output is its value; some values are infinite, so that their items are done again
+    n, heads, d = 6000, 16, 64
+    q, k, v, cq, ck = tp.inputs(20, [1] * n, [1] * n, heads, heads, d, device="cuda")
+    v[::37, 3, 5] = float("inf")
+    v[::41, 7, 9] = float("nan")
+    out, lse = run(sa, heads, heads, d, q, k, v, cq, ck)
+    assert torch.equal(out.nan_to_num(7.0, 8.0, 9.0), v.nan_to_num(7.0, 8.0, 9.0))
+    ref = (q.double() * k.double()).sum(-1) / d ** 0.5
+    bound = (q.double() * k.double()).abs().sum(-1) / d ** 0.5 * (d + 8) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * ref.abs()
+    assert ((lse.double() - ref).abs() <= bound).all()
+
+
+def test_calls_of_other_sizes_one_behind_the_other(sa):
+    # one workspace, several of its sizes, schedules and joins, without a synchronisation between
+    att = sa.PackedAttention(8, 2, 64)
+    todo = [([41], [41]), ([700, 3, 300], [700, 3, 300]), ([20, 5], [6000, 900]), ([1] * 40, [33] * 40), ([2000], [2000]),
+            ([64], [4000]), ([0, 7], [0, 7])]
+    cases = [tp.inputs(30 + i, a, b, 8, 2, 64, device="cuda") for i, (a, b) in enumerate(todo)]
+    lse = [torch.zeros(x[0].shape[:2], device="cuda") for x in cases]
+    for _ in range(3):
+        outs = [att(*x, lse=y) for x, y in zip(cases, lse)]
+    torch.cuda.synchronize()
+    assert int(att.dev_status.item()) == 0
+    for x, o, y, (a, b) in zip(cases, outs, lse, todo):
+        tp.check(tp.reference(*x), o, y, a, b, 64)
