@@ -106,8 +106,9 @@ constexpr int kBins = 1024;
 constexpr int kScheduleThreads = 1024;
 constexpr int kSeqShared = 1024;      // sequences that stay in shared memory
 constexpr int kTileRegs = 4;          // tiles of a thread that it remembers
-constexpr int kJoinThreads = 128;
-constexpr int kJoinRows = 16;         // rows of a join unit
+constexpr int kMaxWorkers = 256;      // CTAs that share the work: a tile has no more ranges
+constexpr int kJoinRows = 8;          // rows of a CTA's part of a join
+constexpr int64_t kL2Share = int64_t(64) << 20;   // keys and values that stay in L2: half of it
 
 // Registers of a thread by role, together the launch's 768 x 80: the control
 // warps give up what the output warps, a whole row each, need.
@@ -154,6 +155,7 @@ struct Header {
   int32_t counter;        // items handed out beyond each CTA's first
   int32_t entries;        // tiles (without ranges)
   int32_t cuts;
+  int32_t rounds;         // with ranges: of head groups
 };
 
 struct __align__(16) Item {
@@ -215,7 +217,7 @@ struct Params {
   int32_t head_groups;    // tiles' heads: Hq / tile_heads
   int32_t mode;           // kDirect, kTiles or kRanges
   int32_t by_head;        // tiles: KV head by KV head
-  int32_t rounds, round_groups, round_slots;   // ranges
+  int32_t round_slots;    // ranges
   float scale_log2;
   int32_t* dev_status;
   uint64_t wait_ns;
@@ -253,9 +255,19 @@ struct ScheduleParams {
   int32_t* first;         // [workers + 1]
   Cut* cuts;
   int32_t total_q, total_k, batch, tile_tokens, workers, bin_shift;
-  int32_t mode, round_groups;   // head groups of a round
+  int32_t mode, head_groups;
+  int64_t key_bytes;      // of a key and its value, all heads
   int32_t* dev_status;
 };
+
+// Rounds of head groups: as many as keep the keys and values of a round that are
+// read again within their share of L2, but a divisor of the groups.
+__host__ __device__ inline int32_t rounds_of(int64_t bytes, int32_t head_groups) {
+  int32_t rounds = 1;
+  for (int32_t r = 2; r <= kRounds && bytes / rounds > kL2Share; ++r)
+    if (head_groups % r == 0) rounds = r;
+  return rounds;
+}
 
 // Inclusive scans over a warp.
 __device__ __forceinline__ int32_t warp_scan_max(int32_t x, int lane) {
@@ -306,6 +318,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
   __shared__ int32_t bins[kBins];
   __shared__ int32_t wq[32], wk[32], wt[32];
   __shared__ int32_t slots, cuts;
+  __shared__ unsigned long long shared_keys;   // of sequences of several tiles
   launch_dependents();
   wait_dependency();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -313,7 +326,10 @@ __global__ void __launch_bounds__(kScheduleThreads)
   int32_t carry_q = clamp_to(p.cu_q[0], p.total_q), carry_k = clamp_to(p.cu_k[0], p.total_k);
   int32_t carry_t = 0;
   bool bad = p.cu_q[0] != carry_q || p.cu_k[0] != carry_k;
-  if (tid == 0) slots = cuts = 0;
+  if (tid == 0) {
+    slots = cuts = 0;
+    shared_keys = 0;
+  }
   bins[tid] = 0;
   const bool near = p.batch <= kSeqShared;
   int4* seqs = near ? seqs_s : p.seqs;
@@ -363,6 +379,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
     if (s < p.batch) {
       seqs[s] = make_int4(q0, nq, k0, mk - k0);
       tile0[s] = before_t + st - tiles;
+      if (p.mode == kRanges && tiles > 1) atomicAdd(&shared_keys, (unsigned long long)(mk - k0));
     }
     carry_q = top_q;
     carry_k = top_k;
@@ -411,10 +428,12 @@ __global__ void __launch_bounds__(kScheduleThreads)
       if (tid + i * kScheduleThreads < tiles) put(mine[i]);
     for (int32_t t = tid + kTileRegs * kScheduleThreads; t < tiles; t += kScheduleThreads)
       put(entry(t));
-    if (tid == 0) *p.header = Header{0, tiles, 0};
+    if (tid == 0) *p.header = Header{0, tiles, 0, 1};
     return;
   }
 
+  const int32_t rounds = rounds_of(int64_t(shared_keys) * p.key_bytes, p.head_groups);
+  const int32_t round_groups = p.head_groups / rounds;
   // Ranges: the blocks of a round's tiles (head groups one behind the other),
   // an item's cost before each tile's, in equal shares.  A share's end inside a
   // tile cuts it, unless one side would have few blocks.  (All below 2^31.)
@@ -428,7 +447,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
   }
   __syncthreads();
   const int32_t share =
-      max((cost * p.round_groups + p.workers - 1) / p.workers, 2 * kItemCost + 2);
+      max((cost * round_groups + p.workers - 1) / p.workers, 2 * kItemCost + 2);
   const int32_t least = min(share / 8 + 1, 4);
   // first block of tile [at, at + n + kItemCost) that belongs to share k or a later one
   auto cut_at = [&](int32_t at, int32_t n, int32_t k) -> int32_t {
@@ -436,7 +455,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
     return b < least ? 0 : n - b < least ? n : b;
   };
   int32_t placed = 0;
-  for (int32_t hg = 0; hg < p.round_groups; ++hg) {
+  for (int32_t hg = 0; hg < round_groups; ++hg) {
     for (int32_t base = 0; base < tiles; base += kScheduleThreads) {
       const int32_t t = base + tid;
       Entry e;
@@ -479,12 +498,14 @@ __global__ void __launch_bounds__(kScheduleThreads)
   int32_t all;
   const int32_t before = scan_block(tid < p.workers ? bins[tid] : 0, &all);
   if (tid <= p.workers) p.first[tid] = before;
-  if (tid == 0) *p.header = Header{0, tiles, cuts};
+  if (tid == 0) *p.header = Header{0, tiles, cuts, rounds};
 }
 
 // Joins the ranges of the tiles that were cut, in key order: a range's weight is
 // 2^(m + log2 l), its output is divided by its own sum first, as that may be as
-// large as fp32 goes.
+// large as fp32 goes.  A CTA takes 8 rows of a tile, a thread four columns of one:
+// the weights of a row's ranges once, to shared memory, then the sums over ranges,
+// eight loads under way.
 struct JoinParams {
   const Header* header;
   const Cut* cuts;
@@ -493,55 +514,100 @@ struct JoinParams {
   __nv_bfloat16* o;
   float* lse;
   int64_t o_st, o_sh;
-  int32_t Hq, tile_heads, rounds, round_groups, round_slots;
+  int32_t Hq, tile_heads, head_groups, round_slots;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinParams p) {
+__global__ void __launch_bounds__(kJoinRows * D / 4)
+    join_kernel(const __grid_constant__ JoinParams p) {
+  constexpr int kThreadsJ = kJoinRows * D / 4;
+  constexpr int kUnits = kRows / kJoinRows;
+  // a range's weight, and what its output is divided by, inverted
+  __shared__ float2 weight[kMaxWorkers][kJoinRows];
+  __shared__ float top[kThreadsJ / 32][kJoinRows], total[kThreadsJ / 32][kJoinRows][2];
   launch_dependents();
   wait_dependency();
-  constexpr int kUnits = kRows / kJoinRows;
-  const int64_t units = int64_t(__ldcg(&p.header->cuts)) * p.rounds * kUnits;
+  const int32_t rounds = __ldcg(&p.header->rounds);
+  const int64_t units = int64_t(__ldcg(&p.header->cuts)) * rounds * kUnits;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t c = u / kUnits;
-    const int32_t round = int32_t(c % p.rounds);
-    const Cut cut = p.cuts[c / p.rounds];
+    const int32_t round = int32_t(c % rounds);
+    const int4* at = reinterpret_cast<const int4*>(&p.cuts[c / rounds]);
+    const int4 a0 = __ldcg(at), a1 = __ldcg(at + 1);
+    const Cut cut{a0.x, a0.y, a0.z, a0.w, a1.x, {0, 0, 0}};
+    const int row0 = int(u % kUnits) * kJoinRows;
+    if (row0 / p.tile_heads >= cut.ntok) continue;           // no query in these rows
     const int64_t slot0 = int64_t(round) * p.round_slots + cut.slot;
-    for (int x = threadIdx.x; x < kJoinRows * (D / 4); x += kJoinThreads) {
-      const int row = int(u % kUnits) * kJoinRows + x % kJoinRows, c4 = x / kJoinRows;
-      const int tok = row / p.tile_heads, head = row - tok * p.tile_heads;
-      if (tok >= cut.ntok) continue;
-      const float4* ml = p.part_ml + slot0 * kRows + row;
-      const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
-      float m = -INFINITY;
-      for (int32_t i = 0; i < cut.ranges; ++i) {
-        const float4 y = __ldcg(ml + int64_t(i) * kRows);
-        if (y.y != 0.f) m = fmaxf(m, y.x + log2f(y.y));
-      }
-      float l = 0.f, lx = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int32_t i = 0; i < cut.ranges; ++i) {
-        const float4 y = __ldcg(ml + int64_t(i) * kRows);
-        const float4 z = __ldcg(po + int64_t(i) * (D / 4) * kRows);
-        if (y.y == 0.f) continue;                  // sees no key of this range
-        const float w = ex2(y.x + log2f(y.y) - m), own = 1.f / y.y;
-        l += w;
-        lx = fmaf(w, y.z * own, lx);
-        acc.x = fmaf(w, z.x * own, acc.x);
-        acc.y = fmaf(w, z.y * own, acc.y);
-        acc.z = fmaf(w, z.z * own, acc.z);
-        acc.w = fmaf(w, z.w * own, acc.w);
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // sees no key at all: 0
+    const int r = tid % kJoinRows, row = row0 + r;
+    // the references and sums of this row's ranges: a thread has every
+    // (threads / 8)-th of them
+    const float4* ml = p.part_ml + slot0 * kRows + row;
+    float m = -INFINITY;
+    for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
+      const float4 y = __ldcg(ml + int64_t(i) * kRows);
+      // (a sum of 0: the row sees no key of this range)
+      const float e = y.y == 0.f ? -INFINITY : y.x + log2f(y.y);
+      m = fmaxf(m, e);
+      weight[i][r] = make_float2(e, y.y == 0.f ? 0.f : 1.f / y.y);
+    }
+    // lanes 8 apart have the same row
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    if (lane < kJoinRows) top[warp][lane] = m;
+    __syncthreads();
+    m = top[0][r];
+#pragma unroll
+    for (int w = 1; w < kThreadsJ / 32; ++w) m = fmaxf(m, top[w][r]);
+    float l = 0.f, lx = 0.f;
+    for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
+      const float2 y = weight[i][r];
+      // (every reference -infinity, or NaN: so is the result)
+      const float w = y.y == 0.f ? 0.f : ex2(y.x - m);
+      l += w;
+      lx = fmaf(w, __ldcg(ml + int64_t(i) * kRows).z * y.y, lx);
+      weight[i][r] = make_float2(w, y.y);
+    }
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      lx += __shfl_xor_sync(0xffffffffu, lx, o);
+    }
+    if (lane < kJoinRows) {
+      total[warp][lane][0] = l;
+      total[warp][lane][1] = lx;
+    }
+    __syncthreads();
+    l = lx = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreadsJ / 32; ++w) {
+      l += total[w][r][0];
+      lx += total[w][r][1];
+    }
+    const int c4 = tid / kJoinRows;
+    const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int32_t i = 0; i < cut.ranges; ++i) {
+      const float4 z = __ldcg(po + int64_t(i) * (D / 4) * kRows);
+      const float2 y = weight[i][r];
+      if (y.y == 0.f) continue;
+      acc.x = fmaf(y.x, z.x * y.y, acc.x);
+      acc.y = fmaf(y.x, z.y * y.y, acc.y);
+      acc.z = fmaf(y.x, z.z * y.y, acc.z);
+      acc.w = fmaf(y.x, z.w * y.y, acc.w);
+    }
+    const int tok = row / p.tile_heads, head = row - tok * p.tile_heads;
+    if (tok < cut.ntok) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;            // sees no key at all: 0
       const int64_t t = int64_t(cut.q0) + tok;
-      const int32_t h = (round * p.round_groups + cut.hg) * p.tile_heads + head;
-      const uint2 out = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                                   pack_bf16x2(acc.z * inv, acc.w * inv));
-      *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = out;
+      const int32_t h = (round * (p.head_groups / rounds) + cut.hg) * p.tile_heads + head;
+      *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = make_uint2(
+          pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (p.lse && c4 == 0)
         p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
     }
+    __syncthreads();                                         // before the weights change
   }
 }
 
@@ -691,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ii = 0, qi = 0, kiss = 0;   // descriptions, items and K blocks so far
       // items: the direct CTA's tile, places in the list of tiles times head
       // groups, or the entries of this CTA's share, round by round
-      int32_t entries = 0, from = 0, to = 0;
+      int32_t entries = 0, from = 0, to = 0, round_groups = 0;
       int64_t items = found ? 1 : 0;
       if (p.mode == kTiles) {
         entries = __ldcg(&p.header->entries);
@@ -699,7 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (p.mode == kRanges) {
         from = __ldcg(&p.first[blockIdx.x]);
         to = __ldcg(&p.first[blockIdx.x + 1]);
-        items = int64_t(to - from) * p.rounds;
+        const int32_t rounds = __ldcg(&p.header->rounds);
+        round_groups = p.head_groups / rounds;
+        items = int64_t(to - from) * rounds;
       }
       // An item's entry is copied to shared memory (place x & 1), without waiting;
       // landed() waits for it.
@@ -745,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int32_t hg = head_of(id);
         if (p.mode == kRanges) {
           if (e.slot >= 0) e.slot += hg * p.round_slots;
-          hg = hg * p.round_groups + e.hg;
+          hg = hg * round_groups + e.hg;
         }
         const int32_t head0 = hg * p.tile_heads;
         it->e = e;
@@ -1487,8 +1555,8 @@ bool make_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t heads,
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// CTAs that share the work (the schedule counts them in its bins).
-int workers_of(int sms) { return std::min(sms, kBins - 1); }
+static_assert(kMaxWorkers < kBins, "the schedule counts shares in its bins");
+int workers_of(int sms) { return std::min(sms, kMaxWorkers); }
 
 // Tiles are cut where sequences have more keys than queries, on the whole: the
 // tiles of whole prompts have from one block to all, and taking the long ones
@@ -1500,15 +1568,9 @@ bool may_cut(const sa_packed_shape& s) {
   return s.total_k > s.total_q && tiles < (int64_t(1) << 30) / blocks;
 }
 
-// Rounds of head groups: as many as keep a round's keys and values within half of
-// L2, or about, but a divisor of the groups.
-int rounds_of(const sa_packed_shape& s) {
-  const int64_t head_groups = s.num_q_heads / sa_packed::tile_of(s).heads;
-  const int64_t bytes = int64_t(s.total_k) * s.num_kv_heads * s.head_dim * 4;
-  int rounds = 1;
-  for (int r = 2; r <= kRounds && bytes / rounds > (int64_t(64) << 20); ++r)
-    if (head_groups % r == 0) rounds = r;
-  return rounds;
+// Bytes of a key and its value, all heads.
+int64_t key_bytes(const sa_packed_shape& s) {
+  return int64_t(s.num_kv_heads) * s.head_dim * 4;
 }
 
 struct Layout {
@@ -1529,7 +1591,9 @@ Layout layout_of(const sa_packed_shape& s, int sms) {
   l.first = l.cost0 + up(size_t(tiles) * 4);
   l.cuts = l.first + up(size_t(workers + 1) * 4);
   l.part_ml = l.cuts + up(size_t(workers) * sizeof(Cut));
-  const size_t slots = size_t(rounds_of(s) * l.round_slots);
+  const int64_t head_groups = s.num_q_heads / sa_packed::tile_of(s).heads;
+  const size_t slots =
+      size_t(rounds_of(s.total_k * key_bytes(s), int32_t(head_groups)) * l.round_slots);
   l.part_o = l.part_ml + up(slots * kRows * 16);
   l.end = l.part_o + up(slots * kRows * size_t(s.head_dim) * 4);
   return l;
@@ -1591,7 +1655,6 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   }
   const bool ranges = may_cut(s);
   const int workers = workers_of(sms);
-  const int rounds = ranges ? rounds_of(s) : 1;
   auto at = [&](size_t offset) { return static_cast<void*>(ws + offset); };
   Params p;
   p.cu_q = a.cu_q;
@@ -1617,10 +1680,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   p.tile_heads = tile.heads;
   p.tile_tokens = tile.tokens;
   p.head_groups = int32_t(head_groups);
-  // keys and values of all heads against half of L2
-  p.by_head = int64_t(s.total_k) * s.num_kv_heads * D * 4 > (int64_t(64) << 20);
-  p.rounds = rounds;
-  p.round_groups = int32_t(head_groups / rounds);
+  p.by_head = s.total_k * key_bytes(s) > kL2Share;
   p.round_slots = int32_t(lay.round_slots);
   p.scale_log2 = float(double(s.scale) * 1.4426950408889634);
   p.dev_status = a.dev_status;
@@ -1651,7 +1711,8 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   sp.bin_shift = 0;
   while ((key_blocks >> sp.bin_shift) >= kBins) ++sp.bin_shift;
   sp.mode = p.mode;
-  sp.round_groups = p.round_groups;
+  sp.head_groups = p.head_groups;
+  sp.key_bytes = key_bytes(s);
   sp.dev_status = a.dev_status;
   cudaError_t e = launch_kernel(schedule_kernel, 1, kScheduleThreads, 0, st, sp);
   if (e != cudaSuccess) return e;
@@ -1669,10 +1730,9 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   jp.o_sh = p.o_sh;
   jp.Hq = p.Hq;
   jp.tile_heads = p.tile_heads;
-  jp.rounds = p.rounds;
-  jp.round_groups = p.round_groups;
+  jp.head_groups = p.head_groups;
   jp.round_slots = p.round_slots;
-  return launch_kernel(join_kernel<D>, unsigned(8 * workers), kJoinThreads, 0, st, jp);
+  return launch_kernel(join_kernel<D>, unsigned(4 * workers), kJoinRows * D / 4, 0, st, jp);
 }
 
 }  // namespace
