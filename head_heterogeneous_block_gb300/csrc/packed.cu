@@ -177,7 +177,6 @@ struct Shared {
   uint64_t o_free;        // a phase per item: O is in registers
   uint64_t xch_bar;       // exchanges between the softmax groups
   uint64_t sum_full[2], sum_empty[2];   // items in turn: the rows' sums
-  uint64_t stage_full, stage_empty;     // a phase per panel of an output tile
   uint64_t batch_done;    // a phase per marker: every output before it is through
   uint64_t drain_qk, drain_pv;
   uint64_t info_full[kNI], info_empty[kNI];
@@ -189,6 +188,7 @@ struct Shared {
   float sum[2][4][kRows];     // per softmax group: sums of rounded weights
   float sum_x[2][4][kRows];   // and of unrounded ones, for the log-sum-exp
   float ref[2][kRows];        // the rows' references
+  int64_t row_at[kRows];      // a tile's row in o, from its first
   int32_t any_again;      // one item: it is to be done again
   int32_t bad_v[kNI];     // per description: the item (by its number, from 1) that met
                           // infinities or NaN in masked blocks
@@ -667,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     packed_attention_kernel(const __grid_constant__ CUtensorMap tq,
                             const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv,
-                            const __grid_constant__ CUtensorMap to,
                             const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -678,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem_raw;
   uint8_t* sK = sQ + C::kNQ * C::kQBytes;
   uint8_t* sV = sK + C::kNK * C::kKVBytes;
-  uint8_t* sO = sV + C::kNV * C::kKVBytes;       // a panel of an output tile
+  uint8_t* sO = sV + C::kNV * C::kKVBytes;       // a panel of an output tile, 4 KB a warp
   Shared* sh = reinterpret_cast<Shared*>(sO + C::kQPanel);
   volatile int* abort = &sh->abort;
 
@@ -707,8 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->info_full[s], 1);
       mbar_init(&sh->info_empty[s], 3 + (kSoftmaxThreads + kOutThreads) / 32);
     }
-    mbar_init(&sh->stage_full, kOutThreads);
-    mbar_init(&sh->stage_empty, 1);
     mbar_init(&sh->o_last, 1);
     mbar_init(&sh->o_free, kOutThreads);
     mbar_init(&sh->xch_bar, kSoftmaxThreads);
@@ -721,6 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   for (int x = threadIdx.x; x < kBatch / 32; x += kThreads) sh->again[x] = sh->maxima[x] = 0;
+  if (threadIdx.x < kRows) {
+    const int tok = int(threadIdx.x) / p.tile_heads;
+    sh->row_at[threadIdx.x] = tok * p.o_st + (int(threadIdx.x) - tok * p.tile_heads) * p.o_sh;
+  }
   if (warp == 1) {
     tmem_alloc(&sh->tmem_base, C::kTmemCols);
     tmem_relinquish();
@@ -745,7 +746,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
-      tma_prefetch_desc(&to);
     }
     wait_dependency();                   // the schedule, and what the inputs come from
     Entry tile0;
@@ -1332,7 +1332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = row / p.tile_heads;
     const int head = row - tok * p.tile_heads;
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + C::kO;
-    uint32_t ii = 0, qi = 0, panels = 0;   // panels: staged so far
+    uint32_t ii = 0, qi = 0;
     bool ok = true;
     for (;; ++ii) {
       const uint32_t slot = ii % kNI;
@@ -1346,8 +1346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
         if (n == kEnd) break;
-        // complete before a careful item may write its rows again
-        if (row == 0) bulk_wait_all();
         mbar_arrive(&sh->batch_done);
         if (!go_on(&ok)) break;
         continue;
@@ -1368,7 +1366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = tok < it.e.ntok;                     // a query of the tile
       const bool some = lim >= it.e.b0 * kBK;                // that sees a key of the range
       const bool whole = it.e.slot < 0;
-      const bool staged = whole && it.e.ntok == p.tile_tokens;
       // (a NaN is not in range either)
       const bool in_range = l <= 0x1p126f;
       if (!some) {
@@ -1377,8 +1374,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = -INFINITY;
       }
       const float inv = whole ? 1.f / l : 1.f;
-      __nv_bfloat16* direct = p.o + (int64_t(it.e.q0) + tok) * p.o_st +
-                              int64_t(it.head0 + head) * p.o_sh;
       float4* part = p.part_o + int64_t(whole ? 0 : it.e.slot) * (D / 4) * kRows + row;
       const bool blank = __any_sync(0xffffffffu, !some);     // rarely: a branch
       // (the softmax warps may be two items ahead, but not at the next item of this
@@ -1445,43 +1440,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         finish(r0, 64 * s);
         finish(r1, 64 * s + 32);
       }
-      if (staged) {
-        // panel by panel through the buffer, 128-byte swizzled as TMA stores read it
+      if (whole) {
+        // panel by panel through the warp's buffer (16-byte chunks of a row are
+        // swapped by its number, so that neither side meets bank conflicts), out in
+        // whole 128-byte rows: 8 lanes a row
+        const int rows = it.e.ntok * p.tile_heads;
+        __nv_bfloat16* o = p.o + int64_t(it.e.q0) * p.o_st + int64_t(it.head0) * p.o_sh +
+                           (lane & 7) * 8;
+        uint8_t* mine = sO + (row - lane) * 128;
 #pragma unroll
         for (int s = 0; s < C::kPanels; ++s) {
-          if (panels > 0 && !wait_all(&sh->stage_empty, (panels - 1) & 1, abort, p.wait_ns)) {
-            ok = false;
-            break;
-          }
+          __syncwarp();
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            *reinterpret_cast<uint4*>(sO + row * 128 + ((x ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(mine + lane * 128 + ((x ^ (lane & 7)) << 4)) =
                 make_uint4(ob[32 * s + 4 * x], ob[32 * s + 4 * x + 1], ob[32 * s + 4 * x + 2],
                            ob[32 * s + 4 * x + 3]);
-          fence_proxy_async_smem();
-          mbar_arrive(&sh->stage_full);
-          if (warp == 20) {
-            if (!warp_wait(&sh->stage_full, panels & 1, abort, p.wait_ns)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              // evict-first: the output is not read here again
-              tma_store_3d_hint(&to, sO, s * 64, it.head0, it.e.q0, l2_policy_evict_first());
-              bulk_commit_group();
-              bulk_wait_read_all();
-              mbar_arrive(&sh->stage_empty);
-            }
-            __syncwarp();
-          }
-          ++panels;
-        }
-        if (!ok) break;
-      } else if (whole && live) {
+          __syncwarp();
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x)
-          reinterpret_cast<uint4*>(direct)[x] =
-              make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
+          for (int x = 0; x < 8; ++x) {
+            const int y = 4 * x + (lane >> 3), at = row - lane + y;
+            if (at < rows)
+              *reinterpret_cast<uint4*>(o + sh->row_at[at] + 64 * s) =
+                  *reinterpret_cast<const uint4*>(mine + y * 128 +
+                                                  (((lane & 7) ^ (y & 7)) << 4));
+          }
+        }
       }
       // the range that the first pass keeps: the sum up to 2^126 (so that no
       // weight overflowed) and O finite
@@ -1502,7 +1486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++qi;
     }
     if (!ok) raise_abort(sh, p);
-    if (row == 0) bulk_wait_all();   // the stores read this CTA's shared memory
     tmem_ld_wait();
     tc_fence_before();
   }
@@ -1617,8 +1600,7 @@ cudaError_t launch_kernel(Kernel* kern, unsigned grid, int threads, int smem, cu
 
 template <int D, bool kLse, bool kOne>
 cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& tq,
-                             const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                             cudaStream_t st) {
+                             const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using C = Cfg<D>;
   constexpr int kSmem = C::kData + int(sizeof(Shared));
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -1626,7 +1608,7 @@ cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& 
   auto kern = packed_attention_kernel<D, kLse, kOne>;
   cudaError_t e = sa_paged::allow_shared(kern, kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, grid, kThreads, kSmem, st, tq, tk, tv, to, p);
+  return launch_kernel(kern, grid, kThreads, kSmem, st, tq, tk, tv, p);
 }
 
 template <int D>
@@ -1641,15 +1623,13 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
 
   // no keys at all: the map only has to be valid, every score is masked
   const bool none = s.total_k == 0;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv;
   if (!make_map(&tq, a.q, s.total_q, s.num_q_heads, D, s.q_stride_t, s.q_stride_h, tile.heads,
                 tile.tokens) ||
       !make_map(&tk, none ? a.q : a.k, none ? 1 : s.total_k, none ? 1 : s.num_kv_heads, D,
                 s.k_stride_t, s.k_stride_h, 1, kBK) ||
       !make_map(&tv, none ? a.q : a.v, none ? 1 : s.total_k, none ? 1 : s.num_kv_heads, D,
-                s.v_stride_t, s.v_stride_h, 1, kBK) ||
-      !make_map(&to, a.o, s.total_q, s.num_q_heads, D, s.o_stride_t, s.o_stride_h, tile.heads,
-                tile.tokens)) {
+                s.v_stride_t, s.v_stride_h, 1, kBK)) {
     *encode_failed = true;
     return cudaErrorInvalidValue;
   }
@@ -1689,8 +1669,8 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   if (tiles * head_groups <= sms && (!ranges || key_blocks <= kDirectBlocks)) {
     p.mode = kDirect;
     const unsigned grid = unsigned(tiles * head_groups);
-    return a.lse ? launch_attention<D, true, true>(p, grid, tq, tk, tv, to, st)
-                 : launch_attention<D, false, true>(p, grid, tq, tk, tv, to, st);
+    return a.lse ? launch_attention<D, true, true>(p, grid, tq, tk, tv, st)
+                 : launch_attention<D, false, true>(p, grid, tq, tk, tv, st);
   }
   p.mode = ranges ? kRanges : kTiles;
   ScheduleParams sp;
@@ -1716,8 +1696,8 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   sp.dev_status = a.dev_status;
   cudaError_t e = launch_kernel(schedule_kernel, 1, kScheduleThreads, 0, st, sp);
   if (e != cudaSuccess) return e;
-  e = a.lse ? launch_attention<D, true, false>(p, unsigned(workers), tq, tk, tv, to, st)
-            : launch_attention<D, false, false>(p, unsigned(workers), tq, tk, tv, to, st);
+  e = a.lse ? launch_attention<D, true, false>(p, unsigned(workers), tq, tk, tv, st)
+            : launch_attention<D, false, false>(p, unsigned(workers), tq, tk, tv, st);
   if (e != cudaSuccess || !ranges) return e;
   JoinParams jp;
   jp.header = p.header;
