@@ -1382,24 +1382,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.careful && *(volatile int32_t*)&sh->bad_v[slot] == int32_t(qi + 1);
       float osum = 0.f, osum2 = 0.f;
       // 32 columns of O, normalised and packed; of a range, as they are to its slot
-      uint32_t ob[D / 2];
+      uint32_t ob[32];
       auto finish = [&](uint32_t (&r)[32], int col) {
         if (blank && !some) {
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = 0u;
-        }
-        if (dirty && live && some) {
-          // what clean_v took out of the values that this row sees
-          const __nv_bfloat16* v = p.v + it.g * p.v_sh + col;
-          const int32_t end = min(lim + 1, (it.e.b0 + n) * kBK);
-          for (int32_t u = (it.e.b0 + it.mt) * kBK; u < end; ++u) {
-            const __nv_bfloat16* vr = v + (int64_t(it.e.kbeg) + u) * p.v_st;
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float y = __bfloat162float(vr[x]);
-              if (!(fabsf(y) <= 3.4e38f)) r[x] = __float_as_uint(__uint_as_float(r[x]) + y);
-            }
-          }
         }
 #pragma unroll
         for (int x = 0; x < 32; x += 2)
@@ -1417,7 +1404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 16; ++x) {
           float a0, a1;
           mul2(a0, a1, __uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]), inv, inv);
-          ob[col / 2 + x] = pack_bf16x2(a0, a1);
+          ob[(col & 32) / 2 + x] = pack_bf16x2(a0, a1);
         }
       };
       if (!wait_all(&sh->o_last, qi & 1, abort, p.wait_ns)) {
@@ -1425,7 +1412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-#pragma unroll
+      const int rows = it.e.ntok * p.tile_heads;
+      __nv_bfloat16* o = p.o + int64_t(it.e.q0) * p.o_st + int64_t(it.head0) * p.o_sh +
+                         (lane & 7) * 8;
+      uint8_t* mine = sO + (row - lane) * 128;
+#pragma unroll 1
       for (int s = 0; s < C::kPanels; ++s) {
         uint32_t r0[32], r1[32];
         tmem_ld32(lanes + 64 * s, r0);
@@ -1439,32 +1430,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         finish(r0, 64 * s);
         finish(r1, 64 * s + 32);
+        if (!whole) continue;
+        // through the warp's buffer (16-byte chunks of a row are swapped by its
+        // number, so that neither side meets bank conflicts), out in whole 128-byte
+        // rows: 8 lanes a row
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          *reinterpret_cast<uint4*>(mine + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+              make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int y = 4 * x + (lane >> 3), at = row - lane + y;
+          if (at < rows)
+            *reinterpret_cast<uint4*>(o + sh->row_at[at] + 64 * s) =
+                *reinterpret_cast<const uint4*>(mine + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+        }
       }
-      if (whole) {
-        // panel by panel through the warp's buffer (16-byte chunks of a row are
-        // swapped by its number, so that neither side meets bank conflicts), out in
-        // whole 128-byte rows: 8 lanes a row
-        const int rows = it.e.ntok * p.tile_heads;
-        __nv_bfloat16* o = p.o + int64_t(it.e.q0) * p.o_st + int64_t(it.head0) * p.o_sh +
-                           (lane & 7) * 8;
-        uint8_t* mine = sO + (row - lane) * 128;
-#pragma unroll
-        for (int s = 0; s < C::kPanels; ++s) {
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            *reinterpret_cast<uint4*>(mine + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-                make_uint4(ob[32 * s + 4 * x], ob[32 * s + 4 * x + 1], ob[32 * s + 4 * x + 2],
-                           ob[32 * s + 4 * x + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int y = 4 * x + (lane >> 3), at = row - lane + y;
-            if (at < rows)
-              *reinterpret_cast<uint4*>(o + sh->row_at[at] + 64 * s) =
-                  *reinterpret_cast<const uint4*>(mine + y * 128 +
-                                                  (((lane & 7) ^ (y & 7)) << 4));
-          }
+      if (dirty) {
+        // what clean_v took out of the values that a row sees comes back, now that
+        // the row is written
+        __syncwarp();
+        if (live && some) {
+          const __nv_bfloat16* v = p.v + it.g * p.v_sh;
+          __nv_bfloat16* mine_o = p.o + int64_t(it.e.q0) * p.o_st + int64_t(it.head0) * p.o_sh +
+                                  sh->row_at[row];
+          const int32_t end = min(lim + 1, (it.e.b0 + n) * kBK);
+          for (int32_t u = (it.e.b0 + it.mt) * kBK; u < end; ++u)
+#pragma unroll 1
+            for (int x = 0; x < D; ++x) {
+              const float y = __bfloat162float(v[(int64_t(it.e.kbeg) + u) * p.v_st + x]);
+              if (fabsf(y) <= 3.4e38f) continue;
+              if (whole) {
+                mine_o[x] = __float2bfloat16_rn(__bfloat162float(mine_o[x]) + y);
+              } else {
+                float* at = reinterpret_cast<float*>(&part[(x / 4) * kRows]) + x % 4;
+                *at += y;
+              }
+            }
         }
       }
       // the range that the first pass keeps: the sum up to 2^126 (so that no
