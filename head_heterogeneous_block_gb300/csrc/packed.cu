@@ -1381,32 +1381,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool dirty =
           it.careful && *(volatile int32_t*)&sh->bad_v[slot] == int32_t(qi + 1);
       float osum = 0.f, osum2 = 0.f;
-      // 32 columns of O, normalised and packed; of a range, as they are to its slot
-      uint32_t ob[32];
-      auto finish = [&](uint32_t (&r)[32], int col) {
-        if (blank && !some) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) r[x] = 0u;
-        }
-#pragma unroll
-        for (int x = 0; x < 32; x += 2)
-          add2(osum, osum2, __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
-        if (!whole) {
-          if (!live) return;
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            part[(col / 4 + x) * kRows] =
-                make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
-                            __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
-          return;
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float a0, a1;
-          mul2(a0, a1, __uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]), inv, inv);
-          ob[(col & 32) / 2 + x] = pack_bf16x2(a0, a1);
-        }
-      };
       if (!wait_all(&sh->o_last, qi & 1, abort, p.wait_ns)) {
         ok = false;
         break;
@@ -1416,37 +1390,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       __nv_bfloat16* o = p.o + int64_t(it.e.q0) * p.o_st + int64_t(it.head0) * p.o_sh +
                          (lane & 7) * 8;
       uint8_t* mine = sO + (row - lane) * 128;
+      // 32 columns at a time, in a short loop: five roles share a scheduler's
+      // instruction cache, and the same code unrolled took three times as long
 #pragma unroll 1
-      for (int s = 0; s < C::kPanels; ++s) {
-        uint32_t r0[32], r1[32];
-        tmem_ld32(lanes + 64 * s, r0);
-        tmem_ld32(lanes + 64 * s + 32, r1);
-        tmem_ld_wait(r0);
-        tmem_ld_wait(r1);
-        if (s == C::kPanels - 1) {
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(lanes + 32 * c, r);
+        tmem_ld_wait(r);
+        if (c == D / 32 - 1) {
           // O is read: the next item's first P V may overwrite it
           tc_fence_before();
           mbar_arrive(&sh->o_free);
         }
-        finish(r0, 64 * s);
-        finish(r1, 64 * s + 32);
-        if (!whole) continue;
-        // through the warp's buffer (16-byte chunks of a row are swapped by its
-        // number, so that neither side meets bank conflicts), out in whole 128-byte
-        // rows: 8 lanes a row
-        __syncwarp();
+        if (blank && !some) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          *reinterpret_cast<uint4*>(mine + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-              make_uint4(ob[4 * x], ob[4 * x + 1], ob[4 * x + 2], ob[4 * x + 3]);
-        __syncwarp();
+          for (int x = 0; x < 32; ++x) r[x] = 0u;
+        }
 #pragma unroll
+        for (int x = 0; x < 32; x += 2)
+          add2(osum, osum2, __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+        if (!whole) {
+          // a range's columns, as they are, to its slot
+          if (live) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              part[(8 * c + x) * kRows] =
+                  make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                              __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
+          }
+          continue;
+        }
+        // through the warp's buffer, 64 columns at a time (16-byte chunks of a row
+        // are swapped by its number, so that neither side meets bank conflicts)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t ob[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float a0, a1;
+            mul2(a0, a1, __uint_as_float(r[8 * x + 2 * y]),
+                 __uint_as_float(r[8 * x + 2 * y + 1]), inv, inv);
+            ob[y] = pack_bf16x2(a0, a1);
+          }
+          *reinterpret_cast<uint4*>(mine + lane * 128 +
+                                    ((((c & 1) * 4 + x) ^ (lane & 7)) << 4)) =
+              make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+        if (!(c & 1)) continue;
+        // out in whole 128-byte rows: 8 lanes a row
+        __syncwarp();
+#pragma unroll 4
         for (int x = 0; x < 8; ++x) {
           const int y = 4 * x + (lane >> 3), at = row - lane + y;
           if (at < rows)
-            *reinterpret_cast<uint4*>(o + sh->row_at[at] + 64 * s) =
+            *reinterpret_cast<uint4*>(o + sh->row_at[at] + 32 * (c - 1)) =
                 *reinterpret_cast<const uint4*>(mine + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
         }
+        __syncwarp();
       }
       if (dirty) {
         // what clean_v took out of the values that a row sees comes back, now that
