@@ -61,19 +61,24 @@
 // another.
 //
 // Measured (GB300; bf16 peak 1937 TFLOP/s, masked halves of blocks not counted as
-// work): a prompt of 32768 tokens, 32/8 heads, d = 128: 5.9 ms, 1480 TFLOP/s, 76%;
-// 16 prompts of 1 to 4096, 28/4 heads: 478 us, 1340 TFLOP/s, 69%; the chunks
-// above: 1210 TFLOP/s, 62%; 24 prompts of 1 to 1024, 8/2 heads, d = 64: 30 us; one
-// of 41 tokens: 10 us.  The tensor pipe is busy 49% of the 16 prompts' time, issue
-// slots 48%: what is left is the chain from S through softmax and P V back to the
-// S buffer, of which three are in flight (512 columns hold no fourth), Q K^T's
-// operands in shared memory (a step of 128 x 128 x 16 takes some 100 cycles where
-// 64 are ideal), and 1.4 us an item at its ends.  Two sets of eight softmax warps
-// on every other block each came 3% slower for the 16 prompts and 1% for the long
-// one.  The 16 prompts, step by step: 513 us with softmax warps that also write
-// the output and scan V in every block that the mask cuts; 505 with output warps;
-// 482 with the output through a buffer of its own instead of the items' Q stages,
-// whose next loads then waited for it.
+// work): a prompt of 32768 tokens, 32/8 heads, d = 128: 5.9 to 6.1 ms, 1440 to 1490
+// TFLOP/s, 75 to 77%; 16 prompts of 1 to 4096, 28/4 heads: 468 us, 1370 TFLOP/s, 71%;
+// the chunks above: 1200 TFLOP/s, 62%; 24 prompts of 1 to 1024, 8/2 heads, d = 64:
+// 28 us; one of 41 tokens: 9.1 us; 16 tokens behind 128K keys, 64/8 heads: 118 us of
+// 79 at the copy rate.  With 16 prompts the tensor pipe is busy 49% of the time,
+// issue slots 48%: what is left is the chain from S through softmax and P V back to
+// the S buffer, of which three are in flight (512 columns hold no fourth), Q K^T's
+// operands in shared memory (a step of 128 x 128 x 16 takes some 100 cycles where 64
+// are ideal), and an item's ends.  Two sets of eight softmax warps on every other
+// block each came 3% slower for the 16 prompts and 1% for the long one.
+//
+// The 16 prompts, step by step: 513 us with softmax warps that also write the output
+// and scan V in every block that the mask cuts; 505 with output warps; 482 with the
+// output through a buffer of its own instead of the items' Q stages, whose next
+// loads then waited for it; 468 with 64 columns of a row in registers at a time
+// instead of all.  Items of one block (256 prompts of 32 tokens, 32/8 heads) take as
+// long as their output does: 84 us with TMA stores, whose reads of the buffer it
+// waited for, 68 with whole rows in registers, 61 with a short loop.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1391,7 +1396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (lane & 7) * 8;
       uint8_t* mine = sO + (row - lane) * 128;
       // 32 columns at a time, in a short loop: five roles share a scheduler's
-      // instruction cache, and the same code unrolled took three times as long
+      // instruction cache
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];

@@ -390,6 +390,23 @@ sa_status sparse_attn_paged_grow(const sa_page_pool* pool, const sa_page_growth*
     return SA_ERR_INVALID_ARG;
   if (ws_bytes < sa_paged::grow_workspace(pool->batch, pool->num_kv_heads))
     return SA_ERR_INVALID_ARG;
+  // the slots are written while lengths and counts are read
+  const size_t seqs = size_t(pool->batch) * 4, rows = seqs * pool->num_kv_heads;
+  const struct {
+    const void* p;
+    size_t n;
+  } out[] = {{g->slots, size_t(g->tokens) * pool->num_kv_heads * 8},
+             {g->token_positions, size_t(g->tokens) * 4}},
+    other[] = {{pool->lens, rows}, {pool->owned, rows}, {pool->free_count, 4},
+               {pool->free_pages, size_t(pool->num_pages) * 4},
+               {pool->table, rows * pool->max_pages}, {g->cu, seqs + 4}, {g->counts, seqs},
+               {g->ended, size_t(pool->batch)}, {g->start, seqs}, {g->lens_out, rows},
+               {g->owned_out, rows}, {g->free_count_out, 4}, {g->start_out, seqs},
+               {g->granted, seqs}};
+  for (const auto& o : out)
+    for (const auto& x : other)
+      if (sa_paged::overlap(o.p, o.n, x.p, x.n)) return SA_ERR_INVALID_ARG;
+  if (sa_paged::overlap(out[0].p, out[0].n, out[1].p, out[1].n)) return SA_ERR_INVALID_ARG;
   sa_paged::GrowArgs a;
   a.table = pool->table;
   a.lens = pool->lens;

@@ -9,14 +9,23 @@
 // page waits for another.  A sequence whose pages would pass the stack's end
 // gets none, nor does any later one that wants some.
 //
-// One CTA does the sums over sequences and rows and leaves a 16-byte record a
-// row; then each (head, token) pair looks its page up by itself.  For few pairs
-// that is the same CTA, with the records in shared memory: a decode step is one
-// launch, and the chain of loads (counts and lengths; pages; slots) bounds it.
-// For many it is a second launch over all processors, whose blocks keep the
-// records in shared memory and which the 8-byte slots that it writes bound.  Nothing that is read there is written there: pages are taken
-// from rows that give back, or below the old count of free ones, and put into
-// rows that want some, or above that count.
+// A CTA does the sums over sequences and rows and then looks each (head, token)
+// pair's page up.  For few pairs there is one CTA: a decode step is one launch,
+// and its chain of loads (counts and lengths; pages; slots) and barriers bounds
+// it.  For many, every CTA does the same sums for itself, which costs no time that
+// one would not take, and a part of the pairs; the first one also has the new
+// state, which a second, small launch puts in place where it replaces what other
+// CTAs still read.  Rows and sequences beyond shared memory: one CTA leaves its
+// sums in the workspace, a second launch does the pairs.  Pages are read from rows
+// that give back, or below the old count of free ones, and written to rows that
+// want some, or above that count.
+//
+// Measured (GB300, in a replayed graph): a decode step of 64 sequences, 8 heads:
+// 4.1 us; 16 prompts of 62K tokens in all, 8 heads: 5.9 us, 7.3 in place; 32
+// sequences, 4 heads, a quarter of them ended, chunks of up to 2048 tokens: 7.3 us,
+// 8.7 in place (first one CTA's sums, then the pairs in a launch of their own: 8.7
+// and 9.4 us either way).  The bytes would take 0.1, 0.7 and 0.2 us; a launch with
+// one dependent load takes 2, the sums 2, a look-up and its slots 1.5.
 
 #include <algorithm>
 
@@ -33,7 +42,7 @@ static_assert(kWarps <= 32, "one warp scans the warps' sums");
 constexpr int kInlinePairs = 4096;    // (head, token) pairs that the first CTA does itself
 constexpr int kRecords = 2048;        // rows whose records then stay in shared memory
 constexpr int kSeqRecords = kThreads; // a thread's sequence each
-constexpr int kSpread = 256;          // threads of a block of the second launch
+constexpr int kSpread = 256;          // tokens of a CTA, threads of a block of the second launch
 constexpr int kSpreadHeads = 4;       // heads of a thread's token that it looks up together
 constexpr int kSpreadRows = 1024;     // rows and sequences whose records its blocks keep
 constexpr int kSpreadSeqs = 512;
@@ -150,6 +159,21 @@ __device__ __forceinline__ void put(const GrowArgs& a, const Place& p, int32_t g
   if (g == 0 && a.positions) a.positions[t] = p.live ? p.position : 0;
 }
 
+// Token t's slots for heads g0 .. g1.
+__device__ __forceinline__ void place_heads(const GrowArgs& a, const Tables& w, const Head& h,
+                                            int32_t t, int32_t g0, int32_t g1, bool* bad) {
+  const int32_t b = seq_of(a, w, t);
+  for (int32_t g = g0; g < g1; g += kSpreadHeads) {
+    Place p[kSpreadHeads];
+#pragma unroll
+    for (int i = 0; i < kSpreadHeads; ++i)
+      if (g + i < g1) p[i] = look_up(a, w, h, g + i, t, b, nullptr, nullptr, 0);
+#pragma unroll
+    for (int i = 0; i < kSpreadHeads; ++i)
+      if (g + i < g1) put(a, p[i], g + i, t, bad);
+  }
+}
+
 // Pages given back that nobody took become free: row r's part of them.
 __device__ __forceinline__ void put_back(const GrowArgs& a, const Tables& w, const Head& h,
                                          int32_t r, int lane) {
@@ -160,11 +184,15 @@ __device__ __forceinline__ void put_back(const GrowArgs& a, const Tables& w, con
     a.free_pages[h.free + row.w + k] = a.table[int64_t(r) * a.max_pages + need + k];
 }
 
-// near: all sequences and rows fit into shared memory; inl: so do the tokens' slots
-// go with this launch.
-template <bool near, bool inl>
+// kInline: one CTA does it all.  kMany: each does the sums and a part of the pairs;
+// the new state goes to the workspace if `late`.  kFirst: the first of two launches.
+enum { kInline = 0, kMany = 1, kFirst = 2 };
+
+template <int kMode>
 __global__ void __launch_bounds__(kThreads)
-    grow_kernel(const __grid_constant__ GrowArgs a, Tables ws) {
+    grow_kernel(const __grid_constant__ GrowArgs a, Tables ws, int32_t late) {
+  constexpr bool near = kMode != kFirst;   // all sequences and rows in shared memory
+  constexpr bool inl = kMode == kInline;
   __shared__ int4 seq_s[near ? kSeqRecords : 1], row_s[near ? kRecords : 1];
   __shared__ int32_t sum_w[kWarps], sum_b[kWarps], most_s[near ? kSeqRecords : 1];
   __shared__ int32_t top_s[inl ? kThreads : 1], next_s[inl ? kRecords : 1];
@@ -325,6 +353,10 @@ __global__ void __launch_bounds__(kThreads)
     s.z = ok ? s.y : 0;
     if (ok && to != from) atomicMax(&taken_s, to);
     w.seq[b] = s;
+    if (kMode == kMany && (late || blockIdx.x > 0)) {
+      if (late && blockIdx.x == 0) ws.seq[b] = make_int4(s.z, s.w + s.z, 0, 0);
+      continue;
+    }
     if (a.granted) a.granted[b] = s.z;
     if (a.start_out) a.start_out[b] = s.w + s.z;
   }
@@ -334,21 +366,28 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kMine; ++i) next_s[tid + i * kThreads] = next[i];
   }
   __syncthreads();
-  for (int32_t r = tid; r < rows; r += kThreads) {
-    const int4 row = w.row[r], s = w.seq[seq_of_row(a, r)];
-    a.lens_out[r] = row.x + s.z;
-    const int32_t need = (row.x + s.y + a.page - 1) >> a.page_shift;
-    // without a grant a row keeps what it has of the pages that it asked for
-    a.owned_out[r] = s.z == s.y ? need : min(row.y, need);
-  }
   const Head h{free, carry_b, taken_s};
-  if (tid == 0) {
-    *a.free_count_out = min(h.free + h.back - h.taken, int32_t(a.num_pages));
-    if (!inl) *ws.head = h;
-  }
-  if (near && !inl) {                  // for the second launch
-    for (int32_t b = tid; b < a.batch; b += kThreads) ws.seq[b] = w.seq[b];
-    for (int32_t r = tid; r < rows; r += kThreads) ws.row[r] = w.row[r];
+  if (kMode != kMany || blockIdx.x == 0) {
+    for (int32_t r = tid; r < rows; r += kThreads) {
+      const int4 row = w.row[r], s = w.seq[seq_of_row(a, r)];
+      const int32_t need = (row.x + s.y + a.page - 1) >> a.page_shift;
+      // without a grant a row keeps what it has of the pages that it asked for
+      const int32_t len = row.x + s.z, owned = s.z == s.y ? need : min(row.y, need);
+      if (kMode == kMany && late) {
+        ws.row[r] = make_int4(len, owned, 0, 0);
+      } else {
+        a.lens_out[r] = len;
+        a.owned_out[r] = owned;
+      }
+    }
+    if (tid == 0) {
+      const int32_t left = min(h.free + h.back - h.taken, int32_t(a.num_pages));
+      if (kMode == kMany && late)
+        ws.head->free = left;
+      else
+        *a.free_count_out = left;
+      if (kMode == kFirst) *ws.head = h;
+    }
   }
   bool bad_page = false;
   if (inl) {
@@ -359,9 +398,19 @@ __global__ void __launch_bounds__(kThreads)
       if (t < a.tokens)
         put(a, look_up(a, w, h, g, t, seq_of(a, w, t), next_s, top_s, tops), g, t, &bad_page);
     }
-    if (h.back > h.taken)
-      for (int32_t r = warp; r < rows; r += kWarps) put_back(a, w, h, r, lane);
   }
+  if (kMode == kMany) {
+    // 256 tokens a CTA, two halves of the heads
+    const int32_t t = int32_t(blockIdx.x) * kSpread + tid % kSpread;
+    constexpr int kParts = kThreads / kSpread;
+    if (t < a.tokens)
+      place_heads(a, w, h, t, a.Hkv * (tid / kSpread) / kParts,
+                  a.Hkv * (tid / kSpread + 1) / kParts, &bad_page);
+  }
+  if (kMode != kFirst && h.back > h.taken)
+    for (int32_t r = int32_t(blockIdx.x) * kWarps + warp; r < rows;
+         r += int32_t(gridDim.x) * kWarps)
+      put_back(a, w, h, r, lane);
   if (bad) atomicOr(a.dev_status, SA_DEV_BAD_COUNT);
   if (bad_page) atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
 }
@@ -382,27 +431,50 @@ __global__ void __launch_bounds__(kSpread)
   }
   bool bad = false;
   const int32_t t = int32_t(blockIdx.x) * kSpread + int32_t(threadIdx.x);
-  if (t < a.tokens) {
-    const int32_t b = seq_of(a, w, t);
-    // a block's heads: an equal part of all
-    const int32_t g1 = int32_t(int64_t(a.Hkv) * (blockIdx.y + 1) / gridDim.y);
-    for (int32_t g0 = int32_t(int64_t(a.Hkv) * blockIdx.y / gridDim.y); g0 < g1;
-         g0 += kSpreadHeads) {
-      Place p[kSpreadHeads];
-#pragma unroll
-      for (int i = 0; i < kSpreadHeads; ++i)
-        if (g0 + i < g1) p[i] = look_up(a, w, h, g0 + i, t, b, nullptr, nullptr, 0);
-#pragma unroll
-      for (int i = 0; i < kSpreadHeads; ++i)
-        if (g0 + i < g1) put(a, p[i], g0 + i, t, &bad);
-    }
-  }
+  if (t < a.tokens)                    // a block's heads: an equal part of all
+    place_heads(a, w, h, t, int32_t(int64_t(a.Hkv) * blockIdx.y / gridDim.y),
+                int32_t(int64_t(a.Hkv) * (blockIdx.y + 1) / gridDim.y), &bad);
   if (h.back > h.taken) {
     const int64_t warps = int64_t(gridDim.x) * gridDim.y * (kSpread / 32);
     int64_t r = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kSpread / 32) + (threadIdx.x >> 5);
     for (; r < rows; r += warps) put_back(a, w, h, int32_t(r), threadIdx.x & 31);
   }
   if (bad) atomicOr(a.dev_status, SA_DEV_BAD_INDEX);
+}
+
+// The new state that the first CTA left, put in place.
+__global__ void __launch_bounds__(kSpread)
+    settle_kernel(const __grid_constant__ GrowArgs a, Tables w) {
+  sa_dev::launch_dependents();
+  sa_dev::wait_dependency();
+  const int32_t x = int32_t(blockIdx.x) * kSpread + int32_t(threadIdx.x);
+  if (x < a.batch * a.Hkv) {
+    const int4 r = w.row[x];
+    a.lens_out[x] = r.x;
+    a.owned_out[x] = r.y;
+  }
+  if (x < a.batch) {
+    const int4 s = w.seq[x];
+    if (a.granted) a.granted[x] = s.x;
+    if (a.start_out) a.start_out[x] = s.y;
+  }
+  if (x == 0) *a.free_count_out = w.head->free;
+}
+
+// Whether the new state shares memory with what the other CTAs still read.
+bool replaces(const GrowArgs& a) {
+  const size_t seqs = size_t(a.batch) * 4, rows = seqs * a.Hkv;
+  const struct {
+    const void* p;
+    size_t n;
+  } out[] = {{a.lens_out, rows}, {a.owned_out, rows}, {a.free_count_out, 4}, {a.start_out, seqs},
+             {a.granted, seqs}},
+    in[] = {{a.lens, rows}, {a.owned, rows}, {a.free_count, 4}, {a.cu, seqs + 4},
+            {a.counts, seqs}, {a.ended, size_t(a.batch)}, {a.start, seqs}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (sa_paged::overlap(o.p, o.n, i.p, i.n)) return true;
+  return false;
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -422,6 +494,7 @@ cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.batch) * a.Hkv;
   const bool near = rows <= kRecords && a.batch <= kSeqRecords;
   const bool inl = near && int64_t(a.tokens) * a.Hkv <= kInlinePairs;
+  const int64_t blocks = std::max<int64_t>(1, (int64_t(a.tokens) + kSpread - 1) / kSpread);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -431,12 +504,19 @@ cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = inl    ? cudaLaunchKernelEx(&cfg, grow_kernel<true, true>, a, w)
-                  : near ? cudaLaunchKernelEx(&cfg, grow_kernel<true, false>, a, w)
-                         : cudaLaunchKernelEx(&cfg, grow_kernel<false, false>, a, w);
-  if (e != cudaSuccess || inl) return e;
+  if (inl) return cudaLaunchKernelEx(&cfg, grow_kernel<kInline>, a, w, 0);
+  if (near) {
+    const bool late = replaces(a);
+    cfg.gridDim = dim3(unsigned(blocks));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, grow_kernel<kMany>, a, w, int32_t(late));
+    if (e != cudaSuccess || !late) return e;
+    cfg.gridDim = dim3(unsigned((rows + kSpread - 1) / kSpread));
+    cfg.blockDim = dim3(kSpread);
+    return cudaLaunchKernelEx(&cfg, settle_kernel, a, w);
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, grow_kernel<kFirst>, a, w, 0);
+  if (e != cudaSuccess) return e;
   // blocks of 256 tokens; their heads are split where there are few of them
-  const int64_t blocks = std::max<int64_t>(1, (int64_t(a.tokens) + kSpread - 1) / kSpread);
   const int64_t parts = (a.Hkv + kSpreadHeads - 1) / kSpreadHeads;
   cfg.gridDim = dim3(unsigned(blocks),
                      unsigned(std::min<int64_t>({parts, std::max<int64_t>(1, 1024 / blocks), 256})));

@@ -18,6 +18,11 @@
 // out as many as there are lanes to share them and gets the rest from the
 // others.  Lanes behind `rot` pass their 16 elements on.
 
+// Measured (GB300): 32767 tokens, 32/8 heads, d = 128, with the store: 128 us, 6.8
+// TB/s, the copy rate; 2049 tokens, 28/4 heads, half of each head in interleaved
+// pairs: 6.7 us of 5.0 at the copy rate; 4096 tokens, 8/2 heads, d = 64: 4.1 us of
+// 1.6; a decode step of 64 tokens: 2.2 us, a launch's time.
+
 #include <cuda_bf16.h>
 
 #include <algorithm>

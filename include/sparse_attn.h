@@ -684,8 +684,9 @@ typedef struct sa_page_pool {
 /*
  * New tokens: the `tokens` rows of a packed or padded tensor.  Sequence b has
  * the span cu[b] .. cu[b+1] of them (cu NULL: tokens/batch each) and uses its
- * first counts[b] (NULL: all).  All arrays are device memory; an output may be
- * the input that it replaces.
+ * first counts[b] (NULL: all).  All arrays are device memory; the new lengths,
+ * owned pages, free count and start may replace the old ones; slots and
+ * token_positions share memory with no other array.
  */
 typedef struct sa_page_growth {
   const int32_t* cu;       /* [Bt + 1], not decreasing, or NULL               */

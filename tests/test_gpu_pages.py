@@ -122,6 +122,38 @@ def test_mixed(sa, seed, free):
     run(sa, s, spans, tokens, counts.tolist(), ended, start, status=sa.SA_DEV_NO_PAGES if short else 0)
 
 
+def test_new_state_apart_from_the_old(sa):
+    # many CTAs, whose first one writes the new state at once: the old one stays as it is
+    r = np.random.default_rng(3)
+    s = state(4, 20, 3, 32, 60, 900, spare=5, free=300)
+    counts = r.integers(0, 900, 20)
+    spans, tokens = spans_of(counts), int(counts.sum())
+    ended = (r.random(20) < 0.3).tolist()
+    start = r.integers(0, 5000, 20).tolist()
+    d, pool = to_gpu(sa, s)
+    saved = {k: v.clone() for k, v in d.items() if v is not None}
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = {k: torch.full_like(d[k], 9) for k in ("lens", "owned", "free_count")}
+    first, after, granted = torch.tensor(start, **i32), torch.zeros(20, **i32), torch.zeros(20, **i32)
+    slots, pos = torch.zeros(3, tokens, dtype=torch.int64, device="cuda"), torch.zeros(tokens, **i32)
+    cu = torch.tensor([0] + [e for _, e in spans], **i32)
+    ref = opg.grow(s["table"], s["lens"], s["owned"], s["free"], 32, spans, None, ended, start, tokens)
+    for _ in range(3):                                        # what it reads stays, so it can be done again
+        pool.grow(slots, cu=cu, ended=torch.tensor(ended, device="cuda"), start=first, positions=pos, granted=granted,
+                  lens_out=out["lens"], owned_out=out["owned"], free_count_out=out["free_count"], start_out=after)
+        np.testing.assert_array_equal(slots.cpu(), ref["slots"])
+        np.testing.assert_array_equal(pos.cpu(), ref["token_positions"])
+        np.testing.assert_array_equal(out["lens"].cpu(), ref["lens"])
+        np.testing.assert_array_equal(out["owned"].cpu(), ref["owned"])
+        np.testing.assert_array_equal(after.cpu(), ref["start"])
+        np.testing.assert_array_equal(granted.cpu(), ref["granted"])
+        np.testing.assert_array_equal(d["table"].cpu(), ref["table"])
+        assert int(out["free_count"]) == len(ref["free"])
+        for k in ("lens", "owned", "free_count"):
+            assert torch.equal(d[k], saved[k])
+    assert first.tolist() == start
+
+
 def test_a_pool_that_is_too_small(sa):
     # the second sequence wants more than there is; the third, which wants none, goes on; the fourth has to wait
     s = {"table": np.full((4, 1, 8), -1), "lens": np.array([[0], [0], [3], [0]]), "owned": np.array([[0], [0], [1], [0]]),

@@ -240,7 +240,7 @@ def _pool(sa, **kw):
 
 
 def _grow(sa, pool, ws=P, wsb=1 << 40, status=P, growth=True, **kw):
-    args = dict(cu=P, counts=P, ended=P, start=P, slots=P, token_positions=P, granted=P, lens_out=P, owned_out=P,
+    args = dict(cu=P, counts=P, ended=P, start=P, slots=8 * P, token_positions=16 * P, granted=P, lens_out=P, owned_out=P,
                 free_count_out=P, start_out=P, tokens=10)
     args.update(kw)
     g = sa.PageGrowth(**args)
@@ -263,7 +263,8 @@ def test_pools_are_refused_by_both_calls(sa, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(slots=None), 1), (dict(lens_out=None), 1), (dict(owned_out=None), 1), (dict(free_count_out=None), 1),
-    (dict(ws=None), 1), (dict(status=None), 1), (dict(ws=P + 64), 1), (dict(wsb=100), 1), (dict(slots=P + 4), 1),
+    (dict(ws=None), 1), (dict(status=None), 1), (dict(ws=P + 64), 1), (dict(wsb=100), 1), (dict(slots=8 * P + 4), 1),
+    (dict(slots=P), 1), (dict(slots=16 * P), 1), (dict(token_positions=P), 1), (dict(token_positions=8 * P + 40), 1),
     (dict(cu=P + 2), 1), (dict(granted=P + 1), 1), (dict(growth=False), 1), (dict(tokens=-1), 2),
     (dict(tokens=11, cu=None), 2), (dict(tokens=(1 << 30) + 1), 2)])
 def test_grow_refusals(sa, change, status):
