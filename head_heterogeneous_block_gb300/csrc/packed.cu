@@ -115,11 +115,12 @@ constexpr int kMaxWorkers = 256;      // CTAs that share the work: a tile has no
 constexpr int kJoinRows = 8;          // rows of a CTA's part of a join
 constexpr int64_t kL2Share = int64_t(64) << 20;   // keys and values that stay in L2: half of it
 
-// Registers of a thread by role, together the launch's 768 x 80: the control
-// warps give up what the output warps, a whole row each, need.
+// Registers of a thread by role, together the launch's 768 x 80: the others give up
+// what the output warps need.
+constexpr int kLaunchRegs = 80;
 constexpr int kControlRegs = 64, kSoftmaxRegs = 72, kOutRegs = 128;
 static_assert(128 * kControlRegs + kSoftmaxThreads * kSoftmaxRegs + kOutThreads * kOutRegs <=
-                  kThreads * 80,
+                  kThreads * kLaunchRegs,
               "a larger sum would wait forever");
 
 template <int D>
@@ -1615,6 +1616,15 @@ cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& 
   static_assert(kSmem <= 232448, "shared memory budget");
   static std::atomic<uint64_t> done{0};
   auto kern = packed_attention_kernel<D, kLse, kOne>;
+  // the roles' shares of the registers hold for this many at launch
+  static std::atomic<bool> counted{false};
+  if (!counted.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    counted.store(true, std::memory_order_relaxed);
+  }
   cudaError_t e = sa_paged::allow_shared(kern, kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, grid, kThreads, kSmem, st, tq, tk, tv, p);

@@ -70,7 +70,7 @@ struct GrowArgs {
   int32_t* dev_status;
 };
 size_t grow_workspace(int32_t batch, int32_t num_kv_heads);
-cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st);
+cudaError_t launch_grow(const GrowArgs& a, int sms, cudaStream_t st);
 
 struct RotaryArgs {
   const uint64_t* turns;              // [rot / 2]

@@ -441,7 +441,10 @@ sa_status sparse_attn_paged_grow(const sa_page_pool* pool, const sa_page_growth*
                     : 0;
   a.ws = ws;
   a.dev_status = dev_status;
-  return cuda_status(sa_paged::launch_grow(a, reinterpret_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  const sa_status n = sa_paged::sm_count(&sms);
+  if (n != SA_OK) return n;
+  return cuda_status(sa_paged::launch_grow(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -400,10 +400,10 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   if (kMode == kMany) {
-    // 256 tokens a CTA, two halves of the heads
-    const int32_t t = int32_t(blockIdx.x) * kSpread + tid % kSpread;
+    // 256 tokens at a time, two halves of the heads
     constexpr int kParts = kThreads / kSpread;
-    if (t < a.tokens)
+    for (int32_t t = int32_t(blockIdx.x) * kSpread + tid % kSpread; t < a.tokens;
+         t += int32_t(gridDim.x) * kSpread)
       place_heads(a, w, h, t, a.Hkv * (tid / kSpread) / kParts,
                   a.Hkv * (tid / kSpread + 1) / kParts, &bad_page);
   }
@@ -487,7 +487,7 @@ size_t grow_workspace(int32_t batch, int32_t num_kv_heads) {
   return 256 + up(size_t(batch) * 16) + size_t(batch) * num_kv_heads * 16;
 }
 
-cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st) {
+cudaError_t launch_grow(const GrowArgs& a, int sms, cudaStream_t st) {
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   Tables w{reinterpret_cast<Head*>(ws), reinterpret_cast<int4*>(ws + 256),
            reinterpret_cast<int4*>(ws + 256 + up(size_t(a.batch) * 16))};
@@ -507,7 +507,8 @@ cudaError_t launch_grow(const GrowArgs& a, cudaStream_t st) {
   if (inl) return cudaLaunchKernelEx(&cfg, grow_kernel<kInline>, a, w, 0);
   if (near) {
     const bool late = replaces(a);
-    cfg.gridDim = dim3(unsigned(blocks));
+    // (three CTAs fit on a processor)
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(blocks, 3 * sms)));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, grow_kernel<kMany>, a, w, int32_t(late));
     if (e != cudaSuccess || !late) return e;
     cfg.gridDim = dim3(unsigned((rows + kSpread - 1) / kSpread));

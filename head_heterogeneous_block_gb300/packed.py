@@ -6,7 +6,7 @@ import math
 
 import torch
 
-from . import PackedShape, _check, sparse_attn_packed_workspace_size
+from . import PackedShape, SparseAttnError, _check, sparse_attn_packed_workspace_size
 from ._device import NEEDS_WORKSPACE, DeviceOperator, calls
 
 
@@ -59,7 +59,13 @@ class PackedAttention(DeviceOperator):
         status = calls.packed(*self._sizes, q, k, v, cu_q, cu_k, out, lse, self._ws_ptr,
                               self._ws_bytes, self._status, self._handle())
         if status == NEEDS_WORKSPACE:
-            self._size(q.shape[0], cu_q.numel() - 1, k.shape[0])
+            # in powers of two, so that calls that grow step by step grow it a few times
+            sizes = q.shape[0], cu_q.numel() - 1, k.shape[0]
+            try:
+                self._size(*(1 << (max(n, least) - 1).bit_length()
+                             for n, least in zip(sizes, (8192, 64, 65536))))
+            except SparseAttnError:      # beyond what a call may have: as it is
+                self._size(*sizes)
             return self(q, k, v, cu_q, cu_k, out, lse)
         if status:
             _check(status, "sparse_attn_packed_forward")

@@ -270,3 +270,13 @@ def test_calls_of_other_sizes_one_behind_the_other(sa):
     assert int(att.dev_status.item()) == 0
     for x, o, y, (a, b) in zip(cases, outs, lse, todo):
         tp.check(tp.reference(*x), o, y, a, b, 64)
+
+
+def test_a_workspace_that_grows(sa):
+    att = sa.PackedAttention(8, 2, 64)
+    made = set()
+    for n in (1, 50, 300, 301, 302, 5000, 9000, 9001):
+        q, k, v, cq, ck = tp.inputs(40 + n % 7, [n], [n], 8, 2, 64, device="cuda")
+        tp.same(att(q, k, v, cq), run(sa, 8, 2, 64, q, k, v, cq, ck)[0])
+        made.add(att._ws_ptr)
+    assert len(made) <= 3 and int(att.dev_status.item()) == 0
