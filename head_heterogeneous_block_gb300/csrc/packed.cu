@@ -42,10 +42,11 @@
 // Softmax.  The reference m of a row is its maximum over the item's first
 // block, exchanged once between the groups; later weights may pass 1 and m
 // cancels in O / l.  bf16 has fp32's exponents, so that is exact until a sum
-// passes 2^126 (or O overflows).  An item with such a row is done again behind
-// the others: first Q K^T alone for the rows' true maxima, then as before with
-// these as m.  It costs 1.5 times an item, whatever the values, and nothing on the
-// common path.  The weights are rounded to bf16 for the tensor cores; the sum that
+// passes 2^126.  An item with such a row is done again behind the others: first
+// Q K^T alone for the rows' true maxima, then as before with these as m.  It costs
+// 1.5 times an item, whatever the values, and nothing on the common path.  Where O
+// overflows all the same (values near the end of fp32's range), it is done once
+// more, with m larger by log2 of the keys and one, so that no sum of weights passes 1.  The weights are rounded to bf16 for the tensor cores; the sum that
 // divides O adds the rounded ones, so that a row of one dominant weight gives its
 // value exactly.  The log-sum-exp adds the unrounded ones.
 //
@@ -62,7 +63,7 @@
 //
 // Measured (GB300; bf16 peak 1937 TFLOP/s, masked halves of blocks not counted as
 // work): a prompt of 32768 tokens, 32/8 heads, d = 128: 5.9 to 6.1 ms, 1440 to 1490
-// TFLOP/s, 75 to 77%; 16 prompts of 1 to 4096, 28/4 heads: 468 us, 1370 TFLOP/s, 71%;
+// TFLOP/s, 75 to 77%; 16 prompts of 1 to 4096, 28/4 heads: 471 us, 1360 TFLOP/s, 70%;
 // the chunks above: 1200 TFLOP/s, 62%; 24 prompts of 1 to 1024, 8/2 heads, d = 64:
 // 28 us; one of 41 tokens: 9.1 us; 16 tokens behind 128K keys, 64/8 heads: 118 us of
 // 79 at the copy rate.  With 16 prompts the tensor pipe is busy 49% of the time,
@@ -169,11 +170,12 @@ struct __align__(16) Item {
   int32_t head0, g;       // first query head, KV head
   int32_t mt;             // blocks before the first masked one
   int32_t pos;            // place in the batch of items
-  int32_t careful;        // kClean, kMaxima
+  int32_t careful;        // kClean, kMaxima, kSmall
   int32_t pad[3];
 };
 enum { kEnd = 0, kMarker = -1 };      // values of e.n that are not items
-enum { kClean = 1, kMaxima = 2 };     // done again: with V cleaned, and with true maxima
+// Done again: with V cleaned; with true maxima; with weights that add up to 1 at most.
+enum { kClean = 1, kMaxima = 2, kSmall = 4 };
 
 struct Shared {
   uint64_t q_full[2], q_empty[2];
@@ -590,6 +592,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       l += total[w][r][0];
       lx += total[w][r][1];
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;                // sees no key at all: 0
     const int c4 = tid / kJoinRows;
     const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -598,18 +601,18 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       const float4 z = __ldcg(po + int64_t(i) * (D / 4) * kRows);
       const float2 y = weight[i][r];
       if (y.y == 0.f) continue;
-      acc.x = fmaf(y.x, z.x * y.y, acc.x);
-      acc.y = fmaf(y.x, z.y * y.y, acc.y);
-      acc.z = fmaf(y.x, z.z * y.y, acc.z);
-      acc.w = fmaf(y.x, z.w * y.y, acc.w);
+      const float f = y.x * inv;                 // (all of them: 1; no sum overflows)
+      acc.x = fmaf(f, z.x * y.y, acc.x);
+      acc.y = fmaf(f, z.y * y.y, acc.y);
+      acc.z = fmaf(f, z.z * y.y, acc.z);
+      acc.w = fmaf(f, z.w * y.y, acc.w);
     }
     const int tok = row / p.tile_heads, head = row - tok * p.tile_heads;
     if (tok < cut.ntok) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;            // sees no key at all: 0
       const int64_t t = int64_t(cut.q0) + tok;
       const int32_t h = (round * (p.head_groups / rounds) + cut.hg) * p.tile_heads + head;
       *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = make_uint2(
-          pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       if (p.lse && c4 == 0)
         p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
     }
@@ -739,9 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Behind the only item of a CTA a role sees by itself whether it is to be done
   // again, 0.5 us before the producer could tell it.  (With a check like this
   // where a CTA has many items, the roles' loops came out 1 to 4% slower.)
+  uint32_t marks = 0;
   auto go_on = [&](bool* ok) -> bool {
     if (!kOne) return true;
-    *ok = wait_all(&sh->batch_done, 0, abort, p.wait_ns);
+    *ok = wait_all(&sh->batch_done, marks++ & 1, abort, p.wait_ns);
     return *ok && *(volatile int32_t*)&sh->any_again;
   };
 
@@ -903,23 +907,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             ended = true;
             break;
           }
-          for (int32_t w = 0; ok && w < pos / 32 + 1; ++w) {
-            uint32_t bits = *(volatile uint32_t*)&sh->again[w];
-            const uint32_t maxima = *(volatile uint32_t*)&sh->maxima[w];
-            sh->again[w] = sh->maxima[w] = 0;
-            while (ok && bits) {
-              const int at = __ffs(bits) - 1;
-              bits &= bits - 1;
-              const int32_t twice = (maxima >> at) & 1;
-              // (the next batch's first item may be in the other place)
-              fetch(sh->ids[32 * w + at], x + 1);
-              publish(sh->ids[32 * w + at], x + 1, 32 * w + at,
-                      kClean | (twice ? kMaxima : 0), true);
-              const Entry* e = &sh->ahead[(x + 1) & 1];
-              const int32_t g = sh->info[(ii - 1) % kNI].g, n = e->n;
-              const int32_t key0 = e->kbeg + e->b0 * kBK;
-              for (int32_t t = 0; ok && t < n + twice * n; ++t)
-                load_k(g, key0 + (t >= n ? t - n : t) * kBK);
+          int32_t careful = kClean;
+          for (bool some = true; ok && some;) {
+            some = false;
+            for (int32_t w = 0; ok && w < pos / 32 + 1; ++w) {
+              uint32_t bits = *(volatile uint32_t*)&sh->again[w];
+              const uint32_t maxima = *(volatile uint32_t*)&sh->maxima[w];
+              sh->again[w] = sh->maxima[w] = 0;
+              while (ok && bits) {
+                const int at = __ffs(bits) - 1;
+                bits &= bits - 1;
+                some = true;
+                const int32_t how = careful | ((maxima >> at) & 1 ? kMaxima : 0);
+                // (the next batch's first item may be in the other place)
+                fetch(sh->ids[32 * w + at], x + 1);
+                publish(sh->ids[32 * w + at], x + 1, 32 * w + at, how, true);
+                const Entry* e = &sh->ahead[(x + 1) & 1];
+                const int32_t g = sh->info[(ii - 1) % kNI].g, n = e->n;
+                const int32_t key0 = e->kbeg + e->b0 * kBK;
+                for (int32_t t = 0; ok && t < (how & kMaxima ? 2 * n : n); ++t)
+                  load_k(g, key0 + (t >= n ? t - n : t) * kBK);
+              }
+            }
+            if (careful & kSmall) break;       // that was the last time
+            careful = kClean | kMaxima | kSmall;
+            if (ok && some) {
+              special(kMarker);
+              if (ok) ok = mbar_wait(&sh->batch_done, batches & 1, abort, p.wait_ns);
+              ++batches;
             }
           }
         }
@@ -1254,6 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         m_used *= c;
+        if (careful & kSmall) m_used += float(33 - __clz(n * kBK));
       }
       // the normaliser in partial sums: of rounded weights, and of unrounded ones
       float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
@@ -1478,8 +1494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the range that the first pass keeps: the sum up to 2^126 (so that no
-      // weight overflowed) and O finite
-      if (!it.careful && live && some && !(in_range && fabsf(osum + osum2) <= 3.0e38f)) {
+      // weight overflowed) and O finite; the second one's O may overflow
+      const bool finite = fabsf(osum + osum2) <= 3.0e38f;
+      if (live && some && !(it.careful & kSmall) &&
+          (it.careful ? in_range && !finite : !(in_range && finite))) {
         const uint32_t bit = 1u << (it.pos & 31);
         if (kOne) *(volatile int32_t*)&sh->any_again = 1;
         atomicOr(&sh->again[it.pos >> 5], bit);

@@ -43,10 +43,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_twice(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Non-blocking: has the phase with this parity completed?
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -217,17 +213,6 @@ __device__ __forceinline__ void tma_store_2d_hint(const CUtensorMap* map, const 
       "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], "
       "%4;" ::"l"(map),
       "r"(smem_u32(src)), "r"(c0), "r"(c1), "l"(policy)
-      : "memory");
-}
-
-// The same for a 3-D map; neither c1 nor c2 may be negative.
-__device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap* map, const void* src,
-                                                  int32_t c0, int32_t c1, int32_t c2,
-                                                  uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], "
-      "[%1], %5;" ::"l"(map),
-      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
 

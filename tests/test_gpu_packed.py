@@ -280,3 +280,35 @@ def test_a_workspace_that_grows(sa):
         tp.same(att(q, k, v, cq), run(sa, 8, 2, 64, q, k, v, cq, ck)[0])
         made.add(att._ws_ptr)
     assert len(made) <= 3 and int(att.dev_status.item()) == 0
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([60], [60]), ([600, 40], [600, 40]), ([20], [4000]), ([1, 700, 40], [300, 900, 2500])])
+@pytest.mark.parametrize("masked", [False, True])
+def test_values_near_the_end_of_the_range(sa, lens_q, lens_k, masked):
+    # the mean of such values is finite, their sum is not; a NaN that the first sequence's last queries alone see
+    q, k, v, cq, ck = tp.inputs(50, lens_q, lens_k, 8, 2, 128, device="cuda")
+    v = (v.float() * 1.2e38).clamp(-3.3e38, 3.3e38).bfloat16()
+    ref = tp.reference(q, k, v, cq, ck)
+    seen = 0
+    if masked:
+        v[lens_k[0] - 1] = float("nan")
+        seen = lens_q[0]                  # (NaN in the last one of these only)
+    out, lse = run(sa, 8, 2, 128, q, k, v, cq, ck)
+    if masked:
+        assert out[seen - 1].isnan().all()
+        out[seen - 1], lse[seen - 1] = (torch.from_numpy(x[seen - 1]).cuda().to(t.dtype) for x, t in zip(ref, (out, lse)))
+    tp.check(ref, out, lse, lens_q, lens_k, 128)
+
+
+@pytest.mark.parametrize("power", [60, 115])
+def test_large_values_behind_a_late_key(sa, power):
+    # the late key's weight times its values overflows, and the sum of weights does not
+    n, d = 600, 64
+    q, k, v, cq, ck = tp.inputs(10, [n], [n], 2, 1, d, device="cuda")
+    q[..., 0] = 8.0
+    k[..., 0] = 0.0
+    k[400] = 0.0
+    k[400, :, 0] = power * 0.6931471805599453
+    v = (v.float() * 2.0 ** 90).bfloat16()
+    out, lse = run(sa, 2, 1, d, q, k, v, cq, ck)
+    tp.check(tp.reference(q, k, v, cq, ck), out, lse, [n], [n], d)
