@@ -46,9 +46,11 @@
 // Q K^T alone for the rows' true maxima, then as before with these as m.  It costs
 // 1.5 times an item, whatever the values, and nothing on the common path.  Where O
 // overflows all the same (values near the end of fp32's range), it is done once
-// more, with m larger by log2 of the keys and one, so that no sum of weights passes 1.  The weights are rounded to bf16 for the tensor cores; the sum that
-// divides O adds the rounded ones, so that a row of one dominant weight gives its
-// value exactly.  The log-sum-exp adds the unrounded ones.
+// more, with m larger by log2 of the keys and one, so that no sum of weights passes
+// 1.
+// The weights are rounded to bf16 for the tensor cores; their sum adds the
+// unrounded ones, in fp32, which the log-sum-exp needs anyway.  A dominant weight
+// is 1 either way.
 //
 // Masked places.  Scores of keys that a row does not see become -infinity
 // whatever they are.  Their values meet weights of 0 in the tensor core, which
@@ -193,8 +195,7 @@ struct Shared {
   int32_t ids[kBatch];    // items of the batch
   uint32_t again[kBatch / 32], maxima[kBatch / 32];   // to be done again; with true maxima
   float xch[2][4][kRows];
-  float sum[2][4][kRows];     // per softmax group: sums of rounded weights
-  float sum_x[2][4][kRows];   // and of unrounded ones, for the log-sum-exp
+  float sum[2][4][kRows];     // per softmax group: sums of weights
   float ref[2][kRows];        // the rows' references
   int64_t row_at[kRows];      // a tile's row in o, from its first
   int32_t any_again;      // one item: it is to be done again
@@ -219,7 +220,7 @@ struct Params {
   const Entry* entries;
   const int32_t* first;   // with ranges: [grid + 1] first entry of each CTA's share of a round
   float4* part_o;         // [slot][D / 4][128]
-  float4* part_ml;        // [slot][128]: reference, rounded sum, unrounded sum
+  float2* part_ml;        // [slot][128]: reference, sum
   int64_t v_st, v_sh, o_st, o_sh;
   int32_t total_q, total_k, batch, Hq, group, tile_heads, tile_tokens;
   int32_t head_groups;    // tiles' heads: Hq / tile_heads
@@ -518,7 +519,7 @@ struct JoinParams {
   const Header* header;
   const Cut* cuts;
   const float4* part_o;
-  const float4* part_ml;
+  const float2* part_ml;
   __nv_bfloat16* o;
   float* lse;
   int64_t o_st, o_sh;
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   constexpr int kUnits = kRows / kJoinRows;
   // a range's weight, and what its output is divided by, inverted
   __shared__ float2 weight[kMaxWorkers][kJoinRows];
-  __shared__ float top[kThreadsJ / 32][kJoinRows], total[kThreadsJ / 32][kJoinRows][2];
+  __shared__ float top[kThreadsJ / 32][kJoinRows], total[kThreadsJ / 32][kJoinRows];
   launch_dependents();
   wait_dependency();
   const int32_t rounds = __ldcg(&p.header->rounds);
@@ -550,10 +551,10 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     const int r = tid % kJoinRows, row = row0 + r;
     // the references and sums of this row's ranges: a thread has every
     // (threads / 8)-th of them
-    const float4* ml = p.part_ml + slot0 * kRows + row;
+    const float2* ml = p.part_ml + slot0 * kRows + row;
     float m = -INFINITY;
     for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
-      const float4 y = __ldcg(ml + int64_t(i) * kRows);
+      const float2 y = __ldcg(ml + int64_t(i) * kRows);
       // (a sum of 0: the row sees no key of this range)
       const float e = y.y == 0.f ? -INFINITY : y.x + log2f(y.y);
       m = fmaxf(m, e);
@@ -567,31 +568,21 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     m = top[0][r];
 #pragma unroll
     for (int w = 1; w < kThreadsJ / 32; ++w) m = fmaxf(m, top[w][r]);
-    float l = 0.f, lx = 0.f;
+    float l = 0.f;
     for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
       const float2 y = weight[i][r];
       // (every reference -infinity, or NaN: so is the result)
       const float w = y.y == 0.f ? 0.f : ex2(y.x - m);
       l += w;
-      lx = fmaf(w, __ldcg(ml + int64_t(i) * kRows).z * y.y, lx);
       weight[i][r] = make_float2(w, y.y);
     }
 #pragma unroll
-    for (int o = 8; o <= 16; o <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      lx += __shfl_xor_sync(0xffffffffu, lx, o);
-    }
-    if (lane < kJoinRows) {
-      total[warp][lane][0] = l;
-      total[warp][lane][1] = lx;
-    }
+    for (int o = 8; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane < kJoinRows) total[warp][lane] = l;
     __syncthreads();
-    l = lx = 0.f;
+    l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreadsJ / 32; ++w) {
-      l += total[w][r][0];
-      lx += total[w][r][1];
-    }
+    for (int w = 0; w < kThreadsJ / 32; ++w) l += total[w][r];
     const float inv = l == 0.f ? 0.f : 1.f / l;                // sees no key at all: 0
     const int c4 = tid / kJoinRows;
     const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
@@ -614,7 +605,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = make_uint2(
           pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       if (p.lse && c4 == 0)
-        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
+        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
     __syncthreads();                                         // before the weights change
   }
@@ -671,7 +662,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 }
 
 // kOne: each CTA has its one tile.
-template <int D, bool kLse, bool kOne>
+template <int D, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attention_kernel(const __grid_constant__ CUtensorMap tq,
                             const __grid_constant__ CUtensorMap tk,
@@ -1271,9 +1262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_used *= c;
         if (careful & kSmall) m_used += float(33 - __clz(n * kBK));
       }
-      // the normaliser in partial sums: of rounded weights, and of unrounded ones
+      // the weights' sum, in parts
       float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
-      float x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
       for (int32_t t = 0; t < n; ++t) {
         if (!wait_all(&sh->s_full[sst], sph, abort, p.wait_ns)) {
           ok = false;
@@ -1313,13 +1303,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             a0 = ex2(a0);
             a1 = ex2(a1);
             pk[x] = pack_bf16x2(a0, a1);
-            if (x & 1) {
-              add_bf16x2(sum2, sum3, pk[x]);
-              if (kLse) add2(x2, x3, a0, a1);
-            } else {
-              add_bf16x2(sum0, sum1, pk[x]);
-              if (kLse) add2(x0, x1, a0, a1);
-            }
+            if (x & 1)
+              add2(sum2, sum3, a0, a1);
+            else
+              add2(sum0, sum1, a0, a1);
           }
           tmem_st16(lanes + sst * kBK, pk);
         }
@@ -1337,7 +1324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       sh->sum[w][grp][row] = (sum0 + sum1) + (sum2 + sum3);
-      if (kLse) sh->sum_x[w][grp][row] = (x0 + x1) + (x2 + x3);
       if (grp == 0) sh->ref[w][row] = m_used;
       mbar_arrive(&sh->sum_full[w]);
       ++qi;
@@ -1379,9 +1365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float l = (sh->sum[w][0][row] + sh->sum[w][1][row]) +
                 (sh->sum[w][2][row] + sh->sum[w][3][row]);
-      float lx = kLse ? (sh->sum_x[w][0][row] + sh->sum_x[w][1][row]) +
-                            (sh->sum_x[w][2][row] + sh->sum_x[w][3][row])
-                      : 0.f;
       float m = sh->ref[w][row];
       mbar_arrive(&sh->sum_empty[w]);
       const int32_t lim = it.e.lim0 + tok;
@@ -1392,7 +1375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool in_range = l <= 0x1p126f;
       if (!some) {
         l = whole ? 1.f : 0.f;
-        lx = 0.f;
         m = -INFINITY;
       }
       const float inv = whole ? 1.f / l : 1.f;
@@ -1504,10 +1486,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!in_range) atomicOr(&sh->maxima[it.pos >> 5], bit);
       }
       if (!whole) {
-        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float4(m, l, lx, 0.f);
-      } else if (kLse && live) {
+        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float2(m, l);
+      } else if (p.lse && live) {
         p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
-            some ? (m + log2f(lx)) * 0.6931471805599453f : -INFINITY;
+            some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
@@ -1605,7 +1587,7 @@ Layout layout_of(const sa_packed_shape& s, int sms) {
   const int64_t head_groups = s.num_q_heads / sa_packed::tile_of(s).heads;
   const size_t slots =
       size_t(rounds_of(s.total_k * key_bytes(s), int32_t(head_groups)) * l.round_slots);
-  l.part_o = l.part_ml + up(slots * kRows * 16);
+  l.part_o = l.part_ml + up(slots * kRows * 8);
   l.end = l.part_o + up(slots * kRows * size_t(s.head_dim) * 4);
   return l;
 }
@@ -1626,14 +1608,14 @@ cudaError_t launch_kernel(Kernel* kern, unsigned grid, int threads, int smem, cu
   return cudaLaunchKernelEx(&cfg, kern, params...);
 }
 
-template <int D, bool kLse, bool kOne>
+template <int D, bool kOne>
 cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& tq,
                              const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using C = Cfg<D>;
   constexpr int kSmem = C::kData + int(sizeof(Shared));
   static_assert(kSmem <= 232448, "shared memory budget");
   static std::atomic<uint64_t> done{0};
-  auto kern = packed_attention_kernel<D, kLse, kOne>;
+  auto kern = packed_attention_kernel<D, kOne>;
   // the roles' shares of the registers hold for this many at launch
   static std::atomic<bool> counted{false};
   if (!counted.load(std::memory_order_relaxed)) {
@@ -1683,7 +1665,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   p.counter = &static_cast<Header*>(at(lay.header))->counter;
   p.entries = static_cast<const Entry*>(at(lay.entries));
   p.first = static_cast<const int32_t*>(at(lay.first));
-  p.part_ml = static_cast<float4*>(at(lay.part_ml));
+  p.part_ml = static_cast<float2*>(at(lay.part_ml));
   p.part_o = static_cast<float4*>(at(lay.part_o));
   p.v_st = s.v_stride_t;
   p.v_sh = s.num_kv_heads > 1 ? s.v_stride_h : 0;
@@ -1706,8 +1688,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   if (tiles * head_groups <= sms && (!ranges || key_blocks <= kDirectBlocks)) {
     p.mode = kDirect;
     const unsigned grid = unsigned(tiles * head_groups);
-    return a.lse ? launch_attention<D, true, true>(p, grid, tq, tk, tv, st)
-                 : launch_attention<D, false, true>(p, grid, tq, tk, tv, st);
+    return launch_attention<D, true>(p, grid, tq, tk, tv, st);
   }
   p.mode = ranges ? kRanges : kTiles;
   ScheduleParams sp;
@@ -1733,8 +1714,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   sp.dev_status = a.dev_status;
   cudaError_t e = launch_kernel(schedule_kernel, 1, kScheduleThreads, 0, st, sp);
   if (e != cudaSuccess) return e;
-  e = a.lse ? launch_attention<D, true, false>(p, unsigned(workers), tq, tk, tv, st)
-            : launch_attention<D, false, false>(p, unsigned(workers), tq, tk, tv, st);
+  e = launch_attention<D, false>(p, unsigned(workers), tq, tk, tv, st);
   if (e != cudaSuccess || !ranges) return e;
   JoinParams jp;
   jp.header = p.header;

@@ -4,10 +4,10 @@ of the oracle and derived tolerances.
 Tolerances.  With E = A (d + 8) 2^-23, A the largest sum |q k| scale over the
 row's keys, a score is off by at most E, and an unnormalised weight, relative to
 the row's reference, by 2 E + 2^-20 (the exponential).  It then rounds to bf16:
-2^-8.  The output divides by the sum of the rounded weights, so with e = 2 E +
-2^-20 + n 2^-23 (n keys' fp32 sums) + 2^-8 the weighted mean is off by at most
-e (sum p |v| + |o|) (1 + 2 e), plus half a step of bf16 of the value, 2^-8.
-The log-sum-exp adds unrounded weights: E + 2^-20 + n 2^-23 + 2^-22 |lse|.
+2^-8.  The output divides by the sum of the weights before or after that
+rounding, so with e = 2 E + 2^-20 + n 2^-23 (n keys' fp32 sums) + 2^-8 the
+weighted mean is off by at most e (sum p |v| + |o|) (1 + 2 e), plus half a step
+of bf16 of the value, 2^-8.  The log-sum-exp adds unrounded weights: E + 2^-20 + n 2^-23 + 2^-22 |lse|.
 A tile cut in r ranges rounds m + log2 l of each (|m| <= 2 (A + 10)): 2^-22 (A +
 10) more, relative, and r more sums.
 """
