@@ -115,6 +115,7 @@ constexpr int kScheduleThreads = 1024;
 constexpr int kSeqShared = 1024;      // sequences that stay in shared memory
 constexpr int kTileRegs = 4;          // tiles of a thread that it remembers
 constexpr int kMaxWorkers = 256;      // CTAs that share the work: a tile has no more ranges
+constexpr int kFew = 4;               // ranges that a thread joins by itself
 constexpr int kJoinRows = 8;          // rows of a CTA's part of a join
 constexpr int64_t kL2Share = int64_t(64) << 20;   // keys and values that stay in L2: half of it
 
@@ -514,7 +515,9 @@ __global__ void __launch_bounds__(kScheduleThreads)
 // 2^(m + log2 l), its output is divided by its own sum first, as that may be as
 // large as fp32 goes.  A CTA takes 8 rows of a tile, a thread four columns of one:
 // the weights of a row's ranges once, to shared memory, then the sums over ranges,
-// eight loads under way.
+// eight loads under way.  Of up to kFew ranges a thread loads and weighs all of its
+// row by itself, in one latency (the chunks of the header: 65 us with shared
+// memory's barriers between, 40 so).
 struct JoinParams {
   const Header* header;
   const Cut* cuts;
@@ -549,54 +552,75 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     if (row0 / p.tile_heads >= cut.ntok) continue;           // no query in these rows
     const int64_t slot0 = int64_t(round) * p.round_slots + cut.slot;
     const int r = tid % kJoinRows, row = row0 + r;
-    // the references and sums of this row's ranges: a thread has every
-    // (threads / 8)-th of them
-    const float2* ml = p.part_ml + slot0 * kRows + row;
-    float m = -INFINITY;
-    for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
-      const float2 y = __ldcg(ml + int64_t(i) * kRows);
-      // (a sum of 0: the row sees no key of this range)
-      const float e = y.y == 0.f ? -INFINITY : y.x + log2f(y.y);
-      m = fmaxf(m, e);
-      weight[i][r] = make_float2(e, y.y == 0.f ? 0.f : 1.f / y.y);
-    }
-    // lanes 8 apart have the same row
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-    if (lane < kJoinRows) top[warp][lane] = m;
-    __syncthreads();
-    m = top[0][r];
-#pragma unroll
-    for (int w = 1; w < kThreadsJ / 32; ++w) m = fmaxf(m, top[w][r]);
-    float l = 0.f;
-    for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
-      const float2 y = weight[i][r];
-      // (every reference -infinity, or NaN: so is the result)
-      const float w = y.y == 0.f ? 0.f : ex2(y.x - m);
-      l += w;
-      weight[i][r] = make_float2(w, y.y);
-    }
-#pragma unroll
-    for (int o = 8; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane < kJoinRows) total[warp][lane] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreadsJ / 32; ++w) l += total[w][r];
-    const float inv = l == 0.f ? 0.f : 1.f / l;                // sees no key at all: 0
     const int c4 = tid / kJoinRows;
+    const float2* ml = p.part_ml + slot0 * kRows + row;
     const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a range's weight f, and what its output is divided by, inverted
+    auto add = [&](const float4& z, float f, float inv) {
+      if (inv == 0.f) return;
+      acc.x = fmaf(f, z.x * inv, acc.x);
+      acc.y = fmaf(f, z.y * inv, acc.y);
+      acc.z = fmaf(f, z.z * inv, acc.z);
+      acc.w = fmaf(f, z.w * inv, acc.w);
+    };
+    // (a sum of 0: the row sees no key of this range)
+    auto log_of = [](const float2& y) { return y.y == 0.f ? -INFINITY : y.x + log2f(y.y); };
+    auto inverse = [](float x) { return x == 0.f ? 0.f : 1.f / x; };
+    // (every reference -infinity, or NaN: so is the result)
+    auto weigh = [&](float e, float inv) { return inv == 0.f ? 0.f : ex2(e - m); };
+    if (cut.ranges <= kFew) {
+      float2 y[kFew];
+      float4 z[kFew];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        y[i] = make_float2(0.f, 0.f);
+        z[i] = acc;
+        if (i >= cut.ranges) continue;
+        y[i] = __ldcg(ml + int64_t(i) * kRows);
+        z[i] = __ldcg(po + int64_t(i) * (D / 4) * kRows);
+      }
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        y[i] = make_float2(log_of(y[i]), inverse(y[i].y));
+        m = fmaxf(m, y[i].x);
+      }
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) l += y[i].x = weigh(y[i].x, y[i].y);
+      const float inv = inverse(l);                          // sees no key at all: 0
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) add(z[i], y[i].x * inv, y[i].y);
+    } else {
+      // the references and sums of this row's ranges: a thread has every
+      // (threads / 8)-th of them
+      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
+        const float2 y = __ldcg(ml + int64_t(i) * kRows);
+        weight[i][r] = make_float2(log_of(y), inverse(y.y));
+        m = fmaxf(m, weight[i][r].x);
+      }
+      // lanes 8 apart have the same row
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if (lane < kJoinRows) top[warp][lane] = m;
+      __syncthreads();
+      m = top[0][r];
+#pragma unroll
+      for (int w = 1; w < kThreadsJ / 32; ++w) m = fmaxf(m, top[w][r]);
+      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows)
+        l += weight[i][r].x = weigh(weight[i][r].x, weight[i][r].y);
+#pragma unroll
+      for (int o = 8; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane < kJoinRows) total[warp][lane] = l;
+      __syncthreads();
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kThreadsJ / 32; ++w) l += total[w][r];
+      const float inv = inverse(l);
 #pragma unroll 8
-    for (int32_t i = 0; i < cut.ranges; ++i) {
-      const float4 z = __ldcg(po + int64_t(i) * (D / 4) * kRows);
-      const float2 y = weight[i][r];
-      if (y.y == 0.f) continue;
-      const float f = y.x * inv;                 // (all of them: 1; no sum overflows)
-      acc.x = fmaf(f, z.x * y.y, acc.x);
-      acc.y = fmaf(f, z.y * y.y, acc.y);
-      acc.z = fmaf(f, z.z * y.y, acc.z);
-      acc.w = fmaf(f, z.w * y.y, acc.w);
+      for (int32_t i = 0; i < cut.ranges; ++i)
+        add(__ldcg(po + int64_t(i) * (D / 4) * kRows), weight[i][r].x * inv, weight[i][r].y);
+      __syncthreads();                                       // before the weights change
     }
     const int tok = row / p.tile_heads, head = row - tok * p.tile_heads;
     if (tok < cut.ntok) {
@@ -607,7 +631,6 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       if (p.lse && c4 == 0)
         p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    __syncthreads();                                         // before the weights change
   }
 }
 
@@ -1729,7 +1752,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   jp.tile_heads = p.tile_heads;
   jp.head_groups = p.head_groups;
   jp.round_slots = p.round_slots;
-  return launch_kernel(join_kernel<D>, unsigned(4 * workers), kJoinRows * D / 4, 0, st, jp);
+  return launch_kernel(join_kernel<D>, unsigned(8 * workers), kJoinRows * D / 4, 0, st, jp);
 }
 
 }  // namespace
