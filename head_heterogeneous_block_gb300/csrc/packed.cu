@@ -33,11 +33,20 @@
 //
 // Roles of the 24 warps: 0 producer (items, Q, K; it looks items up ahead and
 // loads the next one's Q while this one's K blocks are on their way), 1 issues
-// Q K^T into one of three S buffers of tensor memory, 2 producer of V, 3 issues
-// P V (P in tensor memory over its S, O accumulates in tensor memory), 4-19
-// softmax: four column groups of four warps, a thread has one row and a quarter
-// of its columns, 20-23 output: a thread has a row of O.  Registers are dealt out
-// by role.
+// Q K^T into one of two S buffers of tensor memory, 2 producer of V, 3 issues
+// P V (P in columns of its own, O accumulates in tensor memory), 4-19 softmax:
+// four column groups of four warps, a thread has one row and a quarter of its
+// columns, which it has in registers before it works on them, so that the S buffer
+// is free again; 20-23 output: a thread has a row of O.  Registers are dealt out by
+// role.
+//
+// Shared memory bounds d = 128: a block's Q K^T would read 64 KB there (8 KB a step
+// of 64 cycles, as much as there is), P V reads 32 KB and the copies write 64 KB,
+// 1250 cycles at 128 bytes each where the products take 1024.  So the output warps,
+// idle until an item's end, copy the Q of items of four blocks or more into tensor
+// memory, where Q K^T reads it from then on (blocks before that take it from shared
+// memory).  That leaves 64 columns for P: P V of a block has to be done before the
+// next block's P is stored.  d = 64, bound by softmax, has two P buffers instead.
 //
 // Softmax.  The reference m of a row is its maximum over the item's first
 // block, exchanged once between the groups; later weights may pass 1 and m
@@ -63,19 +72,27 @@
 // copies and MMAs drain, frees its tensor memory and exits.  No CTA waits for
 // another.
 //
-// Measured (GB300; bf16 peak 1937 TFLOP/s, masked halves of blocks not counted as
-// work): a prompt of 32768 tokens, 32/8 heads, d = 128: 5.9 to 6.1 ms, 1440 to 1490
-// TFLOP/s, 75 to 77%; 16 prompts of 1 to 4096, 28/4 heads: 471 us, 1360 TFLOP/s, 70%;
-// the chunks above: 1200 TFLOP/s, 62%; 24 prompts of 1 to 1024, 8/2 heads, d = 64:
-// 28 us; one of 41 tokens: 9.1 us; 16 tokens behind 128K keys, 64/8 heads: 118 us of
-// 79 at the copy rate.  With 16 prompts the tensor pipe is busy 49% of the time,
-// issue slots 48%: what is left is the chain from S through softmax and P V back to
-// the S buffer, of which three are in flight (512 columns hold no fourth), Q K^T's
-// operands in shared memory (a step of 128 x 128 x 16 takes some 100 cycles where 64
-// are ideal), and an item's ends.  Two sets of eight softmax warps on every other
-// block each came 3% slower for the 16 prompts and 1% for the long one.
+// Measured (GB300; 1937 TFLOP/s bf16, 1725 sustained under the power cap; masked
+// halves of blocks not counted as work): a prompt of 32768 tokens, 32/8 heads, d =
+// 128: 5.6 ms, 1570 TFLOP/s, 81%; 16 prompts of 1 to 4096, 28/4 heads: 438 us, 1460
+// TFLOP/s, 76%; the chunks above: 1300 TFLOP/s, 67%; 24 prompts of 1 to 1024, 8/2
+// heads, d = 64: 26.3 us; one of 41 tokens: 9.1 us; 16 tokens behind 128K keys, 64/8
+// heads: 118 us of 79 at the copy rate.
 //
-// The 16 prompts, step by step: 513 us with softmax warps that also write the output
+// The long prompt, the 16 and the chunks, step by step: 6030, 468 and 1368 us with P
+// over its S in three buffers, Q in shared memory and two sums, of the weights
+// before and after their rounding; 5800, 443 and 1310 with one sum (five
+// instructions a pair of weights instead of eight); 5570, 438 and 1265 with the
+// layout of now, and a join of few ranges in one latency.  (Two S buffers without
+// the copies of Q: 6120, 456 and 1360.)  What is left: P's columns, whose P V must be
+// done before the next P is stored, some 1000 cycles from P to that; and items'
+// ends.  Measured and not kept: pairs of CTAs on tiles of 256 rows, which share K
+// and V (6140 and 479: what one CTA signals the other takes 800 cycles, and the loop
+// crosses three times); P in two halves (5530, but 466); two sets of eight softmax
+// warps on every other block each (3% and 1% slower); one arrival a warp at P's
+// barrier (0.5% slower).
+//
+// Before that, the 16 prompts: 513 us with softmax warps that also write the output
 // and scan V in every block that the mask cuts; 505 with output warps; 482 with the
 // output through a buffer of its own instead of the items' Q stages, whose next
 // loads then waited for it; 468 with 64 columns of a row in registers at a time
@@ -105,6 +122,7 @@ constexpr int kBK = 128;              // keys of a block
 constexpr int kSoftmaxThreads = 512;
 constexpr int kOutThreads = 128;
 constexpr int kThreads = 128 + kSoftmaxThreads + kOutThreads;
+constexpr int kCopyBlocks = 4;        // key blocks of an item whose Q is copied (10: the same)
 constexpr int kNI = 4;                // item descriptions in flight
 constexpr int kBatch = 512;           // items between two looks at what is to be done again
 constexpr int kDirectBlocks = 8;      // key blocks of a tile that is not worth cutting
@@ -137,9 +155,14 @@ struct Cfg {
   static constexpr int kNQ = 2;
   static constexpr int kNK = D == 128 ? 2 : 4;      // 32 or 16 KB each
   static constexpr int kNV = kNK;
-  static constexpr int kNS = 3;
+  static constexpr int kNS = 2;
+  static constexpr int kNP = D == 128 ? 1 : 2;
+  static constexpr bool kCopyQ = D == 128;
   static constexpr int kCols = kBK / 4;             // S columns of a softmax group
-  static constexpr uint32_t kO = kNS * kBK;         // TMEM column of O
+  // columns of tensor memory: S, P, Q and O
+  static constexpr uint32_t kP = kNS * kBK;
+  static constexpr uint32_t kQ = kP + kNP * kBK / 2;
+  static constexpr uint32_t kO = kQ + (kCopyQ ? D / 2 : 0);
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kData = kNQ * kQBytes + (kNK + kNV) * kKVBytes + kQPanel;
 };
@@ -182,8 +205,12 @@ enum { kClean = 1, kMaxima = 2, kSmall = 4 };
 
 struct Shared {
   uint64_t q_full[2], q_empty[2];
+  // (k_empty, v_empty: where there are more stages than S buffers; otherwise S done
+  // frees the K stage and P V done the V stage, without a commit of its own)
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[3], p_full[3], pv_done[3];
+  uint64_t s_full[2], s_empty[2];
+  uint64_t p_full[2], pv_done[2];
+  uint64_t q_copied[2];   // items in turn, of those whose Q is copied to tensor memory
   uint64_t o_last;        // a phase per item: its last P V is complete
   uint64_t o_free;        // a phase per item: O is in registers
   uint64_t xch_bar;       // exchanges between the softmax groups
@@ -710,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->q_full[s], 1);
-      mbar_init(&sh->q_empty[s], 1);
+      mbar_init(&sh->q_empty[s], 1 + kOutThreads / 32);
+      mbar_init(&sh->q_copied[s], kOutThreads / 32);
       mbar_init(&sh->sum_full[s], kSoftmaxThreads);
       mbar_init(&sh->sum_empty[s], kOutThreads);
     }
@@ -722,6 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < C::kNS; ++s) {
       mbar_init(&sh->s_full[s], 1);
+      mbar_init(&sh->s_empty[s], kSoftmaxThreads / 32);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->p_full[s], kSoftmaxThreads);
       mbar_init(&sh->pv_done[s], 1);
     }
@@ -869,7 +900,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto load_k = [&](int32_t g, int32_t key) {
         const uint32_t ks = kiss % C::kNK;
-        if (!ready(&sh->k_empty[ks], kiss, C::kNK, true)) return;
+        uint64_t* empty = C::kNK == C::kNS ? &sh->s_full[ks] : &sh->k_empty[ks];
+        if (!ready(empty, kiss, C::kNK, true)) return;
         mbar_arrive_expect_tx(&sh->k_full[ks], C::kKVBytes);
 #pragma unroll
         for (int s = 0; s < C::kPanels; ++s)
@@ -981,7 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t t = 0; t < n; ++t) {
           const uint32_t vs = viss % C::kNV;
           if (viss >= uint32_t(C::kNV) &&
-              !mbar_wait(&sh->v_empty[vs], ((viss / C::kNV) - 1) & 1, abort, p.wait_ns)) {
+              !mbar_wait(C::kNV == 2 ? &sh->pv_done[vs] : &sh->v_empty[vs],
+                         ((viss / C::kNV) - 1) & 1, abort, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -1005,6 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     registers_dec<kControlRegs>();
     constexpr uint32_t idesc_qk = idesc_bf16(kRows, kBK, 0, 0);
     uint32_t ii = 0, qi = 0, stage = 0, phase = 0, kb = 0, kst = 0, kph = 0;
+    uint32_t copies = 0;                 // items whose Q is copied, so far
     bool ok = true;
     for (;; ++ii) {
       const int slot = ii % kNI;
@@ -1027,22 +1061,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ + qs * C::kQBytes), 16, 1024);
+      const bool copy = C::kCopyQ && n >= kCopyBlocks;
+      bool near = false;                 // Q is in tensor memory
       for (int32_t t = 0; t < blocks; ++t) {
-        // lane 0: K of this block; lane 1: P V of three blocks ago (same S buffer)
-        const bool reuse = kb >= 3;
+        // lane 0: K of this block; lane 1: S of two blocks ago is read; lane 2: Q
+        const bool reuse = kb >= 2;
         uint64_t* bar = &sh->k_full[kst];
         uint32_t par = kph;
         if (lane == 1 && reuse) {
-          bar = &sh->pv_done[stage];
+          bar = &sh->s_empty[stage];
           par = phase ^ 1u;
         }
+        if (lane == 2) {
+          bar = &sh->q_copied[copies & 1];
+          par = (copies >> 1) & 1;
+        }
         const uint32_t have = __ballot_sync(0xffffffffu, mbar_test(bar, par));
+        near = copy && (near || (have & 4u));
         if (!(have & 1u) && !warp_wait(&sh->k_full[kst], kph, abort, p.wait_ns)) {
           ok = false;
           break;
         }
         if (reuse && !(have & 2u) &&
-            !warp_wait(&sh->pv_done[stage], phase ^ 1u, abort, p.wait_ns)) {
+            !warp_wait(&sh->s_empty[stage], phase ^ 1u, abort, p.wait_ns)) {
           ok = false;
           break;
         }
@@ -1054,16 +1095,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qoff = (kk / 4) * C::kQPanel + (kk % 4) * 32;
             const uint32_t koff = (kk / 4) * C::kKVPanel + (kk % 4) * 32;
-            mma_ss(s_tmem, qdesc + uint64_t(qoff >> 4), kdesc + uint64_t(koff >> 4), idesc_qk,
-                   kk > 0 ? 1u : 0u);
+            const uint64_t b = kdesc + uint64_t(koff >> 4);
+            if (near)
+              mma_ts(s_tmem, tmem + C::kQ + kk * 8, b, idesc_qk, kk > 0 ? 1u : 0u);
+            else
+              mma_ss(s_tmem, qdesc + uint64_t(qoff >> 4), b, idesc_qk, kk > 0 ? 1u : 0u);
           }
           mma_commit(&sh->s_full[stage]);
-          mma_commit(&sh->k_empty[kst]);
+          if (C::kNK != C::kNS) mma_commit(&sh->k_empty[kst]);
           if (t == blocks - 1) mma_commit(&sh->q_empty[qs]);
         }
         __syncwarp();
         ++kb;
-        if (++stage == 3) {
+        if (++stage == uint32_t(C::kNS)) {
           stage = 0;
           phase ^= 1u;
         }
@@ -1074,6 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       ++qi;
+      copies += copy;
     }
     if (lane == 0) {
       if (!ok) raise_abort(sh, p);
@@ -1084,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- P V issuer
     registers_dec<kControlRegs>();
     constexpr uint32_t idesc_pv = idesc_bf16(kRows, D, 0, 1);   // P (TMEM), V MN-major
-    uint32_t ii = 0, qi = 0, stage = 0, phase = 0, vstage = 0, vphase = 0;
+    uint32_t ii = 0, qi = 0, pb = 0, vstage = 0, vphase = 0;
     bool ok = true;
     for (;; ++ii) {
       const int slot = ii % kNI;
@@ -1093,7 +1138,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const int32_t n = sh->info[slot].e.n;
-      const int32_t lead = sh->info[slot].careful & kMaxima ? n : 0;   // blocks without P V
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
       if (n == kEnd) break;
@@ -1101,13 +1145,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!go_on(&ok)) break;
         continue;
       }
-      for (int32_t t = 0; t < lead + n; ++t) {
-        const bool skip = t < lead, first = t == lead;
-        const bool need_o = first && qi > 0;   // the previous epilogue has read O
+      for (int32_t t = 0; t < n; ++t) {
+        const bool need_o = t == 0 && qi > 0;  // the previous epilogue has read O
         // lane 0: P, lane 1: V, lane 2: O
-        uint64_t* bar = &sh->p_full[stage];
-        uint32_t par = phase;
-        if (lane == 1 && !skip) {
+        const uint32_t pp = (pb >> 1) & 1;
+        uint64_t* bar = &sh->p_full[pb & 1];
+        uint32_t par = pp;
+        if (lane == 1) {
           bar = &sh->v_full[vstage];
           par = vphase;
         }
@@ -1116,11 +1160,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           par = (qi - 1) & 1;
         }
         const uint32_t have = __ballot_sync(0xffffffffu, mbar_test(bar, par));
-        if (!(have & 1u) && !warp_wait(&sh->p_full[stage], phase, abort, p.wait_ns)) {
+        if (!(have & 1u) && !warp_poll(&sh->p_full[pb & 1], pp, abort, p.wait_ns)) {
           ok = false;
           break;
         }
-        if (!skip && !(have & 2u) && !warp_wait(&sh->v_full[vstage], vphase, abort, p.wait_ns)) {
+        if (!(have & 2u) && !warp_wait(&sh->v_full[vstage], vphase, abort, p.wait_ns)) {
           ok = false;
           break;
         }
@@ -1129,35 +1173,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (skip) {
-          if (elect_one()) mma_commit(&sh->pv_done[stage]);
-        } else {
-          const uint64_t vdesc =
-              smem_desc_sw128(smem_u32(sV + vstage * C::kKVBytes), C::kKVPanel, 1024);
-          const uint32_t s_col = tmem + stage * kBK;
-          if (elect_one()) {
+        const uint32_t p_at = tmem + C::kP + pb % C::kNP * (kBK / 2);
+        const uint64_t vdesc =
+            smem_desc_sw128(smem_u32(sV + vstage * C::kKVBytes), C::kKVPanel, 1024);
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              // keys [16kk, 16kk+16) belong to group 16kk / kCols, whose P starts
-              // at that group's first S column
-              const int grp = (kk * 16) / C::kCols;
-              const uint32_t a_col = s_col + grp * C::kCols + (kk * 16 - grp * C::kCols) / 2;
-              mma_ts(tmem + C::kO, a_col, vdesc + uint64_t((kk * 16 * 128) >> 4), idesc_pv,
-                     (first && kk == 0) ? 0u : 1u);
-            }
-            mma_commit(&sh->v_empty[vstage]);
-            mma_commit(&sh->pv_done[stage]);
-            if (t == lead + n - 1) mma_commit(&sh->o_last);
-          }
-          if (++vstage == C::kNV) {
-            vstage = 0;
-            vphase ^= 1u;
-          }
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_ts(tmem + C::kO, p_at + kk * 8, vdesc + uint64_t((kk * 16 * 128) >> 4), idesc_pv,
+                   (t == 0 && kk == 0) ? 0u : 1u);
+          mma_commit(&sh->pv_done[pb & 1]);
+          if (C::kNV != 2) mma_commit(&sh->v_empty[vstage]);
+          if (t == n - 1) mma_commit(&sh->o_last);
         }
         __syncwarp();
-        if (++stage == 3) {
-          stage = 0;
-          phase ^= 1u;
+        ++pb;
+        if (++vstage == C::kNV) {
+          vstage = 0;
+          vphase ^= 1u;
         }
       }
       if (!ok) break;
@@ -1178,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + grp * C::kCols;
     const float c = p.scale_log2;
     uint32_t ii = 0, qi = 0, xn = 0;              // xn: uses of the exchange buffer
-    uint32_t sst = 0, sph = 0, vb = 0;            // S ring; V blocks
+    uint32_t sb = 0, vb = 0;                      // S blocks; those with P V
     bool ok = true;
 
     // The largest of this thread's scores.
@@ -1204,20 +1236,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++xn;
       return true;
     };
+    // S into registers; its buffer may be written again
     auto load_s = [&](float (&s)[C::kCols]) {
       uint32_t sr[32];
       static_assert(C::kCols == 32, "group width");
-      tmem_ld32(lanes + sst * kBK, sr);
+      tmem_ld32(lanes + (sb & 1) * kBK, sr);
       tmem_ld_wait(sr);
 #pragma unroll
       for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(sr[x]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->s_empty[sb & 1]);
     };
-    auto next_s = [&]() {
-      if (++sst == uint32_t(C::kNS)) {
-        sst = 0;
-        sph ^= 1u;
-      }
-    };
+    static_assert(C::kNS == 2, "S buffers in turn");
     // Infinities and NaN of a V block that the mask cuts become 0 in shared
     // memory (this thread's share of the stage); the item is marked.
     auto clean_v = [&](uint32_t item, uint32_t slot) {
@@ -1262,7 +1293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the rows' maxima over all blocks, without P V
         float mx = -INFINITY;
         for (int32_t t = 0; t < n; ++t) {
-          if (!wait_all(&sh->s_full[sst], sph, abort, p.wait_ns)) {
+          if (!wait_all(&sh->s_full[sb & 1], (sb >> 1) & 1, abort, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -1273,9 +1304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < C::kCols; ++x)
             if (t >= mt && x > vis0 - t * kBK) s[x] = -INFINITY;
           mx = fmaxf(mx, row_max(s));
-          tc_fence_before();
-          mbar_arrive(&sh->p_full[sst]);
-          next_s();
+          ++sb;
         }
         if (!ok) break;
         if (!exchange_max(mx, &m_used)) {
@@ -1288,7 +1317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the weights' sum, in parts
       float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
       for (int32_t t = 0; t < n; ++t) {
-        if (!wait_all(&sh->s_full[sst], sph, abort, p.wait_ns)) {
+        if (!wait_all(&sh->s_full[sb & 1], (sb >> 1) & 1, abort, p.wait_ns)) {
           ok = false;
           break;
         }
@@ -1331,12 +1360,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
               add2(sum0, sum1, a0, a1);
           }
-          tmem_st16(lanes + sst * kBK, pk);
+          // P V of kNP blocks before has read P
+          const uint32_t before = vb - 1 - C::kNP;
+          if (vb > uint32_t(C::kNP) &&
+              !wait_all(&sh->pv_done[before & 1], (before >> 1) & 1, abort, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          tmem_st16(lanes + C::kP - grp * (C::kCols / 2) + (vb - 1) % C::kNP * (kBK / 2), pk);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sh->p_full[sst]);
-        next_s();
+        mbar_arrive(&sh->p_full[(vb - 1) & 1]);
+        ++sb;
       }
       if (!ok) break;
       // the sums of this item, once the output warps have read those of the
@@ -1363,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = row / p.tile_heads;
     const int head = row - tok * p.tile_heads;
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + C::kO;
-    uint32_t ii = 0, qi = 0;
+    uint32_t ii = 0, qi = 0, copies = 0;
     bool ok = true;
     for (;; ++ii) {
       const uint32_t slot = ii % kNI;
@@ -1381,7 +1418,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!go_on(&ok)) break;
         continue;
       }
+      // Q of a longer item into tensor memory, where Q K^T reads it faster from then
+      // on (the last item's is done: its output is)
       const uint32_t w = qi & 1;
+      if (C::kCopyQ && n >= kCopyBlocks) {
+        if (!wait_all(&sh->q_full[w], (qi >> 1) & 1, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint8_t* from = sQ + w * C::kQBytes + row * 128;
+#pragma unroll 1
+        for (int s = 0; s < C::kPanels; ++s) {
+          uint32_t r[32];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint4 y =
+                *reinterpret_cast<const uint4*>(from + s * C::kQPanel + ((x ^ (row & 7)) << 4));
+            r[4 * x] = y.x;
+            r[4 * x + 1] = y.y;
+            r[4 * x + 2] = y.z;
+            r[4 * x + 3] = y.w;
+          }
+          tmem_st32(lanes - C::kO + C::kQ + 32 * s, r);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_copied[copies & 1]);
+        ++copies;
+      }
+      if (lane == 0) mbar_arrive(&sh->q_empty[w]);
       if (!wait_all(&sh->sum_full[w], (qi >> 1) & 1, abort, p.wait_ns)) {
         ok = false;
         break;
@@ -1520,6 +1587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) raise_abort(sh, p);
     tmem_ld_wait();
+    tmem_st_wait();
     tc_fence_before();
   }
 

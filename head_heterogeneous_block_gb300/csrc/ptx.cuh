@@ -111,6 +111,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// As warp_wait, polling all the time: a suspended thread wakes up late.
+__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0 && !mbar_test(bar, parity)) {
+    const uint64_t t0 = global_ns();
+    while (ok && !mbar_test(bar, parity)) ok = !*abort && global_ns() - t0 <= limit_ns;
+  }
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
 // Every lane waits; the warp gives up together if any lane gave up, so that
 // no lane goes on alone into a warp-collective (.sync.aligned) instruction.
 template <bool kShort = false>

@@ -312,3 +312,31 @@ def test_large_values_behind_a_late_key(sa, power):
     v = (v.float() * 2.0 ** 90).bfloat16()
     out, lse = run(sa, 2, 1, d, q, k, v, cq, ck)
     tp.check(tp.reference(q, k, v, cq, ck), out, lse, [n], [n], d)
+
+
+def test_two_objects_on_two_streams_at_once(sa):
+    # each with its workspace: lists, shares and joins of both under way together
+    todo = [([700, 3, 300], [700, 3, 300]), ([20, 5], [6000, 900])]
+    cases = [tp.inputs(60 + i, a, b, 8, 2, 128, device="cuda") for i, (a, b) in enumerate(todo)]
+    refs = [run(sa, 8, 2, 128, *x) for x in cases]
+    atts = [sa.PackedAttention(8, 2, 128) for _ in todo]
+    streams = [torch.cuda.Stream() for _ in todo]
+    torch.cuda.synchronize()
+    outs = [[] for _ in todo]
+    for _ in range(20):
+        for i, (x, att, s) in enumerate(zip(cases, atts, streams)):
+            with torch.cuda.stream(s):
+                outs[i].append(att(*x))
+    torch.cuda.synchronize()
+    for i, (ref, att) in enumerate(zip(refs, atts)):
+        assert int(att.dev_status.item()) == 0
+        for o in outs[i]:
+            tp.same(o, ref[0])
+
+
+def test_items_of_every_length_in_turn(sa):
+    # short items between long ones: Q comes from shared memory, from tensor memory and from both in turn
+    lens = [130, 1500, 40, 600, 129, 2000, 500, 5, 385, 900, 512, 513]
+    case(sa, 61, lens, lens, 4, 4, 128)
+    case(sa, 62, lens, [n + 300 * (i % 3) for i, n in enumerate(lens)], 32, 4, 128)
+    case(sa, 63, lens, lens, 4, 4, 64)

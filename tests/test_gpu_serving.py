@@ -193,3 +193,43 @@ def test_prompts_then_captured_steps(sa, hq, hkv, d, page, weights):
                 assert len(set(pos[b, h, :n])) == n and pos[b, h, n - 1] == int(s.start[b]) - 1
     for x in (s.cache, s.pool, s.rotary, s.attention):
         assert int(x.dev_status.item()) == 0
+
+
+FIRST_CALLS = """
+import torch, head_heterogeneous_block_gb300 as sa
+def captured(call):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    return graph, out
+torch.zeros(1, device="cuda")
+make = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+i32 = dict(dtype=torch.int32, device="cuda")
+for d, nq, nk in ((64, 300, 300), (128, 3000, 9000)):
+    q, k, cu = make(nq, 8, d), make(nk, 2, d), torch.tensor([0, 100, 300], **i32)
+    attention = sa.PackedAttention(8, 2, d)
+    graph, out = captured(lambda: attention(q, k, k, cu * (nq // 300), cu * (nk // 300)))
+    again = attention(q, k, k, cu * (nq // 300), cu * (nk // 300))
+    assert torch.equal(out, again) and int(attention.dev_status.item()) == 0
+rotary, positions = sa.Rotary(128), torch.arange(3000, **i32)
+graph, (a, b) = captured(lambda: rotary(q, k[:3000], positions))
+assert torch.equal(a, rotary(q, k[:3000], positions)[0])
+table, lens = torch.zeros(2, 2, 32, **i32), torch.zeros(2, 2, **i32)
+pool = sa.PagePool(table, lens, 16, num_pages=100)
+slots = torch.zeros(2, 300, dtype=torch.int64, device="cuda")
+graph, _ = captured(lambda: pool.grow(slots, cu))
+assert lens.tolist() == [[100, 100], [200, 200]] and int(pool.dev_status.item()) == 0
+assert len(set(slots.flatten().tolist())) == 600 and int(pool.free_count.item()) == 100 - 2 * 7 - 2 * 13
+print("right")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured(sa):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "right", r.stderr[-2000:]
