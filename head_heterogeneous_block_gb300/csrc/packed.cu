@@ -27,7 +27,7 @@
 //   order.  Head groups go round by round, so that a round's keys and values stay
 //   in L2: chunks of 509 tokens behind 32K to 64K, 64/8 heads: 1.36 ms, against
 //   1.43 from the counter (512 items of two lengths do not divide by 152) and
-//   1.53 with rounds of 100 MB instead of 50.
+//   1.53 with rounds of 100 MB instead of 50 (all three before the last steps below).
 // Where every tile gets a CTA of its own the CTAs find their tiles themselves and
 // there is no first launch.
 //
@@ -56,8 +56,7 @@
 // 1.5 times an item, whatever the values, and nothing on the common path.  Where O
 // overflows all the same (values near the end of fp32's range), it is done once
 // more, with m larger by log2 of the keys and one, so that no sum of weights passes
-// 1.
-// The weights are rounded to bf16 for the tensor cores; their sum adds the
+// 1.  The weights are rounded to bf16 for the tensor cores; their sum adds the
 // unrounded ones, in fp32, which the log-sum-exp needs anyway.  A dominant weight
 // is 1 either way.
 //
