@@ -51,14 +51,17 @@
 // Softmax.  The reference m of a row is its maximum over the item's first
 // block, exchanged once between the groups; later weights may pass 1 and m
 // cancels in O / l.  bf16 has fp32's exponents, so that is exact until a sum
-// passes 2^126.  An item with such a row is done again behind the others: first
-// Q K^T alone for the rows' true maxima, then as before with these as m.  It costs
-// 1.5 times an item, whatever the values, and nothing on the common path.  Where O
-// overflows all the same (values near the end of fp32's range), it is done once
-// more, with m larger by log2 of the keys and one, so that no sum of weights passes
-// 1.  The weights are rounded to bf16 for the tensor cores; their sum adds the
-// unrounded ones, in fp32, which the log-sum-exp needs anyway.  A dominant weight
-// is 1 either way.
+// passes 2^126.  The exponents S c - m are single fused operations, whose product is
+// not rounded as m is: a maximum's own weight is 2 to the rounding of m, which a
+// score of 2^30 takes out of the range.  An item with a row whose sum is not between
+// 2^-60 and 2^126 is done again behind the others: first Q K^T alone for the rows'
+// true maxima, then with these as m, large ones taken from the scores before the product
+// with c, so that a maximum weighs 1 whatever its size.  It costs 1.5 times an item,
+// whatever the values, and nothing on the common path.  Where O overflows all the same
+// (values near the end of fp32's range), it is done once more, with exponents less by
+// log2 of the keys and one, so that no sum of weights passes 1.  The weights are rounded
+// to bf16 for the tensor cores; their sum adds the unrounded ones, in fp32, which the
+// log-sum-exp needs anyway.  A dominant weight is 1 either way.
 //
 // Masked places.  Scores of keys that a row does not see become -infinity
 // whatever they are.  Their values meet weights of 0 in the tensor core, which
@@ -106,6 +109,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "packed.h"
 #include "paged.h"
@@ -247,7 +251,7 @@ struct Params {
   const Entry* entries;
   const int32_t* first;   // with ranges: [grid + 1] first entry of each CTA's share of a round
   float4* part_o;         // [slot][D / 4][128]
-  float2* part_ml;        // [slot][128]: reference, sum
+  float4* part_ml;        // [slot][128]: reference, sum, what exponents were less by
   int64_t v_st, v_sh, o_st, o_sh;
   int32_t total_q, total_k, batch, Hq, group, tile_heads, tile_tokens;
   int32_t head_groups;    // tiles' heads: Hq / tile_heads
@@ -538,8 +542,9 @@ __global__ void __launch_bounds__(kScheduleThreads)
 }
 
 // Joins the ranges of the tiles that were cut, in key order: a range's weight is
-// 2^(m + log2 l), its output is divided by its own sum first, as that may be as
-// large as fp32 goes.  A CTA takes 8 rows of a tile, a thread four columns of one:
+// 2^(m + log2 l), relative to the largest m first, as m may be too large for a sum's
+// logarithm to change it; its output is divided by its own sum first, as that may be
+// as large as fp32 goes.  A CTA takes 8 rows of a tile, a thread four columns of one:
 // the weights of a row's ranges once, to shared memory, then the sums over ranges,
 // eight loads under way.  Of up to kFew ranges a thread loads and weighs all of its
 // row by itself, in one latency (the chunks of the header: 65 us with shared
@@ -548,7 +553,7 @@ struct JoinParams {
   const Header* header;
   const Cut* cuts;
   const float4* part_o;
-  const float2* part_ml;
+  const float4* part_ml;
   __nv_bfloat16* o;
   float* lse;
   int64_t o_st, o_sh;
@@ -562,7 +567,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   constexpr int kUnits = kRows / kJoinRows;
   // a range's weight, and what its output is divided by, inverted
   __shared__ float2 weight[kMaxWorkers][kJoinRows];
-  __shared__ float top[kThreadsJ / 32][kJoinRows], total[kThreadsJ / 32][kJoinRows];
+  __shared__ float top_m[kThreadsJ / 32][kJoinRows], top[kThreadsJ / 32][kJoinRows],
+      total[kThreadsJ / 32][kJoinRows];
   launch_dependents();
   wait_dependency();
   const int32_t rounds = __ldcg(&p.header->rounds);
@@ -579,9 +585,11 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     const int64_t slot0 = int64_t(round) * p.round_slots + cut.slot;
     const int r = tid % kJoinRows, row = row0 + r;
     const int c4 = tid / kJoinRows;
-    const float2* ml = p.part_ml + slot0 * kRows + row;
+    const float4* ml = p.part_ml + slot0 * kRows + row;
     const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
-    float m = -INFINITY, l = 0.f;
+    // the largest reference, the largest logarithm of a range's weight beside it, and
+    // the weights' sum
+    float m = -INFINITY, e = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     // a range's weight f, and what its output is divided by, inverted
     auto add = [&](const float4& z, float f, float inv) {
@@ -592,25 +600,29 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       acc.w = fmaf(f, z.w * inv, acc.w);
     };
     // (a sum of 0: the row sees no key of this range)
-    auto log_of = [](const float2& y) { return y.y == 0.f ? -INFINITY : y.x + log2f(y.y); };
+    auto log_of = [&](const float4& y) {
+      return y.y == 0.f ? -INFINITY : (y.x - m) + (y.z + log2f(y.y));
+    };
     auto inverse = [](float x) { return x == 0.f ? 0.f : 1.f / x; };
     // (every reference -infinity, or NaN: so is the result)
-    auto weigh = [&](float e, float inv) { return inv == 0.f ? 0.f : ex2(e - m); };
+    auto weigh = [&](float x, float inv) { return inv == 0.f ? 0.f : ex2(x - e); };
     if (cut.ranges <= kFew) {
-      float2 y[kFew];
-      float4 z[kFew];
+      float4 y[kFew], z[kFew];
 #pragma unroll
       for (int i = 0; i < kFew; ++i) {
-        y[i] = make_float2(0.f, 0.f);
+        y[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         z[i] = acc;
         if (i >= cut.ranges) continue;
         y[i] = __ldcg(ml + int64_t(i) * kRows);
         z[i] = __ldcg(po + int64_t(i) * (D / 4) * kRows);
       }
 #pragma unroll
+      for (int i = 0; i < kFew; ++i) m = fmaxf(m, y[i].x);
+#pragma unroll
       for (int i = 0; i < kFew; ++i) {
-        y[i] = make_float2(log_of(y[i]), inverse(y[i].y));
-        m = fmaxf(m, y[i].x);
+        y[i].x = log_of(y[i]);
+        y[i].y = inverse(y[i].y);
+        e = fmaxf(e, y[i].x);
       }
 #pragma unroll
       for (int i = 0; i < kFew; ++i) l += y[i].x = weigh(y[i].x, y[i].y);
@@ -620,19 +632,26 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     } else {
       // the references and sums of this row's ranges: a thread has every
       // (threads / 8)-th of them
-      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
-        const float2 y = __ldcg(ml + int64_t(i) * kRows);
-        weight[i][r] = make_float2(log_of(y), inverse(y.y));
-        m = fmaxf(m, weight[i][r].x);
-      }
-      // lanes 8 apart have the same row
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if (lane < kJoinRows) top[warp][lane] = m;
-      __syncthreads();
-      m = top[0][r];
+      auto largest = [&](float x, float (&of)[kThreadsJ / 32][kJoinRows]) {
+        // lanes 8 apart have the same row
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        if (lane < kJoinRows) of[warp][lane] = x;
+        __syncthreads();
+        x = of[0][r];
 #pragma unroll
-      for (int w = 1; w < kThreadsJ / 32; ++w) m = fmaxf(m, top[w][r]);
+        for (int w = 1; w < kThreadsJ / 32; ++w) x = fmaxf(x, of[w][r]);
+        return x;
+      };
+      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows)
+        m = fmaxf(m, __ldcg(ml + int64_t(i) * kRows).x);
+      m = largest(m, top_m);
+      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
+        const float4 y = __ldcg(ml + int64_t(i) * kRows);
+        weight[i][r] = make_float2(log_of(y), inverse(y.y));
+        e = fmaxf(e, weight[i][r].x);
+      }
+      e = largest(e, top);
       for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows)
         l += weight[i][r].x = weigh(weight[i][r].x, weight[i][r].y);
 #pragma unroll
@@ -655,7 +674,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = make_uint2(
           pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       if (p.lse && c4 == 0)
-        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + (e + log2f(l))) * 0.6931471805599453f;
     }
   }
 }
@@ -703,6 +722,11 @@ __device__ __forceinline__ bool find_tile(const Params& p, int32_t tile, int lan
   }
   if (bad) atomicOr(p.dev_status, SA_DEV_BAD_COUNT);
   return found;
+}
+
+// What an item's exponents are less by, so that no sum of weights passes 1.
+__device__ __forceinline__ float less_of(int32_t blocks) {
+  return float(33 - __clz(blocks * kBK));
 }
 
 // Whether any of the two bf16 values is an infinity or NaN (an exponent of all ones).
@@ -1287,7 +1311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!go_on(&ok)) break;
         continue;
       }
-      float m_used = -INFINITY;
+      // the reference; with true maxima, what scores are less by before the product with
+      // c, and what exponents add after it
+      float m_used = -INFINITY, top = 0.f, last = 0.f;
       if (careful & kMaxima) {
         // the rows' maxima over all blocks, without P V
         float mx = -INFINITY;
@@ -1306,74 +1332,92 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++sb;
         }
         if (!ok) break;
-        if (!exchange_max(mx, &m_used)) {
+        if (!exchange_max(mx, &top)) {
           ok = false;
           break;
         }
-        m_used *= c;
-        if (careful & kSmall) m_used += float(33 - __clz(n * kBK));
+        m_used = top * c;
+        last = careful & kSmall ? -less_of(n) : 0.f;
+        // (below 2^20 the reference's rounding leaves 2^-5 of an exponent at most, and a
+        // row that is done again for another's sake keeps its bits)
+        if (!(careful & kSmall) && fabsf(m_used) <= 0x1p20f) {
+          last = -m_used;
+          top = 0.f;
+        }
       }
       // the weights' sum, in parts
       float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
-      for (int32_t t = 0; t < n; ++t) {
-        if (!wait_all(&sh->s_full[sb & 1], (sb >> 1) & 1, abort, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        float s[C::kCols];
-        load_s(s);
-        if (t >= mt) {
-          const int32_t vis = vis0 - t * kBK;
-#pragma unroll
-          for (int x = 0; x < C::kCols; ++x)
-            if (x > vis) s[x] = -INFINITY;
-          if (careful) {
-            if (!wait_all(&sh->v_full[vb % C::kNV], (vb / C::kNV) & 1, abort, p.wait_ns)) {
-              ok = false;
-              break;
-            }
-            clean_v(qi, slot);
-          }
-        }
-        ++vb;
-        if (t == 0 && !(careful & kMaxima)) {
-          if (!exchange_max(row_max(s), &m_used)) {
+      // (a loop of its own for items that are done again: it keeps the others' short)
+      auto weigh = [&](auto again) {
+        constexpr bool kAgain = decltype(again)::value;
+        for (int32_t t = 0; t < n; ++t) {
+          if (!wait_all(&sh->s_full[sb & 1], (sb >> 1) & 1, abort, p.wait_ns)) {
             ok = false;
-            break;
-          }
-          m_used *= c;
-        }
-        {
-          uint32_t pk[C::kCols / 2];
-          const float nm = -m_used;
-#pragma unroll
-          for (int x = 0; x < C::kCols / 2; ++x) {
-            float a0, a1;
-            fma2(a0, a1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
-            a0 = ex2(a0);
-            a1 = ex2(a1);
-            pk[x] = pack_bf16x2(a0, a1);
-            if (x & 1)
-              add2(sum2, sum3, a0, a1);
-            else
-              add2(sum0, sum1, a0, a1);
-          }
-          // P V of kNP blocks before has read P
-          const uint32_t before = vb - 1 - C::kNP;
-          if (vb > uint32_t(C::kNP) &&
-              !wait_all(&sh->pv_done[before & 1], (before >> 1) & 1, abort, p.wait_ns)) {
-            ok = false;
-            break;
+            return;
           }
           tc_fence_after();
-          tmem_st16(lanes + C::kP - grp * (C::kCols / 2) + (vb - 1) % C::kNP * (kBK / 2), pk);
+          float s[C::kCols];
+          load_s(s);
+          if (t >= mt) {
+            const int32_t vis = vis0 - t * kBK;
+#pragma unroll
+            for (int x = 0; x < C::kCols; ++x)
+              if (x > vis) s[x] = -INFINITY;
+            if (kAgain) {
+              if (!wait_all(&sh->v_full[vb % C::kNV], (vb / C::kNV) & 1, abort, p.wait_ns)) {
+                ok = false;
+                return;
+              }
+              clean_v(qi, slot);
+            }
+          }
+          ++vb;
+          if (t == 0 && !(kAgain && (careful & kMaxima))) {
+            if (!exchange_max(row_max(s), &m_used)) {
+              ok = false;
+              return;
+            }
+            m_used *= c;
+          }
+          if (kAgain && (careful & kMaxima)) {
+#pragma unroll
+            for (int x = 0; x < C::kCols; ++x) s[x] -= top;
+          }
+          {
+            uint32_t pk[C::kCols / 2];
+            const float nm = kAgain && (careful & kMaxima) ? last : -m_used;
+#pragma unroll
+            for (int x = 0; x < C::kCols / 2; ++x) {
+              float a0, a1;
+              fma2(a0, a1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              pk[x] = pack_bf16x2(a0, a1);
+              if (x & 1)
+                add2(sum2, sum3, a0, a1);
+              else
+                add2(sum0, sum1, a0, a1);
+            }
+            // P V of kNP blocks before has read P
+            const uint32_t before = vb - 1 - C::kNP;
+            if (vb > uint32_t(C::kNP) &&
+                !wait_all(&sh->pv_done[before & 1], (before >> 1) & 1, abort, p.wait_ns)) {
+              ok = false;
+              return;
+            }
+            tc_fence_after();
+            tmem_st16(lanes + C::kP - grp * (C::kCols / 2) + (vb - 1) % C::kNP * (kBK / 2), pk);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&sh->p_full[(vb - 1) & 1]);
+          ++sb;
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&sh->p_full[(vb - 1) & 1]);
-        ++sb;
-      }
+      };
+      if (careful)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
       if (!ok) break;
       // the sums of this item, once the output warps have read those of the
       // item before the last
@@ -1460,8 +1504,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = tok < it.e.ntok;                     // a query of the tile
       const bool some = lim >= it.e.b0 * kBK;                // that sees a key of the range
       const bool whole = it.e.slot < 0;
+      const float less = it.careful & kSmall ? less_of(n) : 0.f;
       // (a NaN is not in range either)
-      const bool in_range = l <= 0x1p126f;
+      const bool in_range = l >= 0x1p-60f && l <= 0x1p126f;
       if (!some) {
         l = whole ? 1.f : 0.f;
         m = -INFINITY;
@@ -1564,8 +1609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       }
-      // the range that the first pass keeps: the sum up to 2^126 (so that no
-      // weight overflowed) and O finite; the second one's O may overflow
+      // the range that the first pass keeps: the sum from 2^-60 (no weight that counts
+      // vanished) to 2^126 (none overflowed) and O finite; the second one's O may
+      // overflow
       const bool finite = fabsf(osum + osum2) <= 3.0e38f;
       if (live && some && !(it.careful & kSmall) &&
           (it.careful ? in_range && !finite : !(in_range && finite))) {
@@ -1575,10 +1621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!in_range) atomicOr(&sh->maxima[it.pos >> 5], bit);
       }
       if (!whole) {
-        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float2(m, l);
+        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float4(m, l, less, 0.f);
       } else if (p.lse && live) {
         p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
-            some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            some ? (m + (less + log2f(l))) * 0.6931471805599453f : -INFINITY;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
@@ -1677,7 +1723,7 @@ Layout layout_of(const sa_packed_shape& s, int sms) {
   const int64_t head_groups = s.num_q_heads / sa_packed::tile_of(s).heads;
   const size_t slots =
       size_t(rounds_of(s.total_k * key_bytes(s), int32_t(head_groups)) * l.round_slots);
-  l.part_o = l.part_ml + up(slots * kRows * 8);
+  l.part_o = l.part_ml + up(slots * kRows * 16);
   l.end = l.part_o + up(slots * kRows * size_t(s.head_dim) * 4);
   return l;
 }
@@ -1755,7 +1801,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   p.counter = &static_cast<Header*>(at(lay.header))->counter;
   p.entries = static_cast<const Entry*>(at(lay.entries));
   p.first = static_cast<const int32_t*>(at(lay.first));
-  p.part_ml = static_cast<float2*>(at(lay.part_ml));
+  p.part_ml = static_cast<float4*>(at(lay.part_ml));
   p.part_o = static_cast<float4*>(at(lay.part_o));
   p.v_st = s.v_stride_t;
   p.v_sh = s.num_kv_heads > 1 ? s.v_stride_h : 0;
