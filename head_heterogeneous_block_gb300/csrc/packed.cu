@@ -59,9 +59,13 @@
 // with c, so that a maximum weighs 1 whatever its size.  It costs 1.5 times an item,
 // whatever the values, and nothing on the common path.  Where O overflows all the same
 // (values near the end of fp32's range), it is done once more, with exponents less by
-// log2 of the keys and one, so that no sum of weights passes 1.  The weights are rounded
-// to bf16 for the tensor cores; their sum adds the unrounded ones, in fp32, which the
-// log-sum-exp needs anyway.  A dominant weight is 1 either way.
+// log2 of the keys and one, so that no sum of weights passes 1.
+//
+// The weights are rounded to bf16 for the tensor cores.  The sum that divides O adds
+// the rounded ones, in fp32: a row of one dominant key gives its value exactly,
+// wherever in the row the key is (a weight of 2^(s - m) behind the first block is no
+// power of two), where a sum of unrounded ones would leave the rounding, up to 2^-8,
+// in the output.  The log-sum-exp, where it is asked for, adds the unrounded ones.
 //
 // Masked places.  Scores of keys that a row does not see become -infinity
 // whatever they are.  Their values meet weights of 0 in the tensor core, which
@@ -226,7 +230,8 @@ struct Shared {
   int32_t ids[kBatch];    // items of the batch
   uint32_t again[kBatch / 32], maxima[kBatch / 32];   // to be done again; with true maxima
   float xch[2][4][kRows];
-  float sum[2][4][kRows];     // per softmax group: sums of weights
+  float sum[2][4][kRows];     // per softmax group: sums of rounded weights
+  float sum_x[2][4][kRows];   // and of unrounded ones, for the log-sum-exp
   float ref[2][kRows];        // the rows' references
   int64_t row_at[kRows];      // a tile's row in o, from its first
   int32_t any_again;      // one item: it is to be done again
@@ -251,7 +256,8 @@ struct Params {
   const Entry* entries;
   const int32_t* first;   // with ranges: [grid + 1] first entry of each CTA's share of a round
   float4* part_o;         // [slot][D / 4][128]
-  float4* part_ml;        // [slot][128]: reference, sum, what exponents were less by
+  float4* part_ml;        // [slot][128]: reference, sum, what exponents were less by,
+                          // sum of unrounded weights
   int64_t v_st, v_sh, o_st, o_sh;
   int32_t total_q, total_k, batch, Hq, group, tile_heads, tile_tokens;
   int32_t head_groups;    // tiles' heads: Hq / tile_heads
@@ -567,8 +573,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   constexpr int kUnits = kRows / kJoinRows;
   // a range's weight, and what its output is divided by, inverted
   __shared__ float2 weight[kMaxWorkers][kJoinRows];
-  __shared__ float top_m[kThreadsJ / 32][kJoinRows], top[kThreadsJ / 32][kJoinRows],
-      total[kThreadsJ / 32][kJoinRows];
+  __shared__ float top_m[kThreadsJ / 32][kJoinRows], top[kThreadsJ / 32][kJoinRows];
+  __shared__ float2 total[kThreadsJ / 32][kJoinRows];
   launch_dependents();
   wait_dependency();
   const int32_t rounds = __ldcg(&p.header->rounds);
@@ -588,8 +594,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     const float4* ml = p.part_ml + slot0 * kRows + row;
     const float4* po = p.part_o + (slot0 * (D / 4) + c4) * kRows + row;
     // the largest reference, the largest logarithm of a range's weight beside it, and
-    // the weights' sum
-    float m = -INFINITY, e = -INFINITY, l = 0.f;
+    // the sums of rounded and of unrounded weights
+    float m = -INFINITY, e = -INFINITY, l = 0.f, lx = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     // a range's weight f, and what its output is divided by, inverted
     auto add = [&](const float4& z, float f, float inv) {
@@ -625,7 +631,10 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
         e = fmaxf(e, y[i].x);
       }
 #pragma unroll
-      for (int i = 0; i < kFew; ++i) l += y[i].x = weigh(y[i].x, y[i].y);
+      for (int i = 0; i < kFew; ++i) {
+        l += y[i].x = weigh(y[i].x, y[i].y);
+        lx = fmaf(y[i].x, y[i].w * y[i].y, lx);
+      }
       const float inv = inverse(l);                          // sees no key at all: 0
 #pragma unroll
       for (int i = 0; i < kFew; ++i) add(z[i], y[i].x * inv, y[i].y);
@@ -652,15 +661,24 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
         e = fmaxf(e, weight[i][r].x);
       }
       e = largest(e, top);
-      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows)
-        l += weight[i][r].x = weigh(weight[i][r].x, weight[i][r].y);
+      for (int32_t i = tid / kJoinRows; i < cut.ranges; i += kThreadsJ / kJoinRows) {
+        const float w = weigh(weight[i][r].x, weight[i][r].y);
+        l += weight[i][r].x = w;
+        lx = fmaf(w, __ldcg(ml + int64_t(i) * kRows).w * weight[i][r].y, lx);
+      }
 #pragma unroll
-      for (int o = 8; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane < kJoinRows) total[warp][lane] = l;
+      for (int o = 8; o <= 16; o <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+        lx += __shfl_xor_sync(0xffffffffu, lx, o);
+      }
+      if (lane < kJoinRows) total[warp][lane] = make_float2(l, lx);
       __syncthreads();
-      l = 0.f;
+      l = lx = 0.f;
 #pragma unroll
-      for (int w = 0; w < kThreadsJ / 32; ++w) l += total[w][r];
+      for (int w = 0; w < kThreadsJ / 32; ++w) {
+        l += total[w][r].x;
+        lx += total[w][r].y;
+      }
       const float inv = inverse(l);
 #pragma unroll 8
       for (int32_t i = 0; i < cut.ranges; ++i)
@@ -674,7 +692,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
       *reinterpret_cast<uint2*>(p.o + t * p.o_st + h * p.o_sh + c4 * 4) = make_uint2(
           pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       if (p.lse && c4 == 0)
-        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + (e + log2f(l))) * 0.6931471805599453f;
+        p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + (e + log2f(lx))) * 0.6931471805599453f;
     }
   }
 }
@@ -734,8 +752,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
-// kOne: each CTA has its one tile.
-template <int D, bool kOne>
+// kLse: the log-sum-exps are written.  kOne: each CTA has its one tile.
+template <int D, bool kLse, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attention_kernel(const __grid_constant__ CUtensorMap tq,
                             const __grid_constant__ CUtensorMap tk,
@@ -1345,8 +1363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           top = 0.f;
         }
       }
-      // the weights' sum, in parts
-      float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+      // the sums of rounded weights and of unrounded ones, in parts
+      float sum0 = 0.f, sum1 = 0.f, x0 = 0.f, x1 = 0.f;
       // (a loop of its own for items that are done again: it keeps the others' short)
       auto weigh = [&](auto again) {
         constexpr bool kAgain = decltype(again)::value;
@@ -1393,10 +1411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               a0 = ex2(a0);
               a1 = ex2(a1);
               pk[x] = pack_bf16x2(a0, a1);
-              if (x & 1)
-                add2(sum2, sum3, a0, a1);
-              else
-                add2(sum0, sum1, a0, a1);
+              add_bf16x2(sum0, sum1, pk[x]);
+              if (kLse) add2(x0, x1, a0, a1);
             }
             // P V of kNP blocks before has read P
             const uint32_t before = vb - 1 - C::kNP;
@@ -1426,7 +1442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      sh->sum[w][grp][row] = (sum0 + sum1) + (sum2 + sum3);
+      sh->sum[w][grp][row] = sum0 + sum1;
+      if (kLse) sh->sum_x[w][grp][row] = x0 + x1;
       if (grp == 0) sh->ref[w][row] = m_used;
       mbar_arrive(&sh->sum_full[w]);
       ++qi;
@@ -1498,6 +1515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float l = (sh->sum[w][0][row] + sh->sum[w][1][row]) +
                 (sh->sum[w][2][row] + sh->sum[w][3][row]);
+      float lx = kLse ? (sh->sum_x[w][0][row] + sh->sum_x[w][1][row]) +
+                            (sh->sum_x[w][2][row] + sh->sum_x[w][3][row])
+                      : 0.f;
       float m = sh->ref[w][row];
       mbar_arrive(&sh->sum_empty[w]);
       const int32_t lim = it.e.lim0 + tok;
@@ -1509,6 +1529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool in_range = l >= 0x1p-60f && l <= 0x1p126f;
       if (!some) {
         l = whole ? 1.f : 0.f;
+        lx = 0.f;
         m = -INFINITY;
       }
       const float inv = whole ? 1.f / l : 1.f;
@@ -1621,10 +1642,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!in_range) atomicOr(&sh->maxima[it.pos >> 5], bit);
       }
       if (!whole) {
-        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float4(m, l, less, 0.f);
-      } else if (p.lse && live) {
+        if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float4(m, l, less, lx);
+      } else if (kLse && live) {
         p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
-            some ? (m + (less + log2f(l))) * 0.6931471805599453f : -INFINITY;
+            some ? (m + (less + log2f(lx))) * 0.6931471805599453f : -INFINITY;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->info_empty[slot]);
@@ -1744,14 +1765,14 @@ cudaError_t launch_kernel(Kernel* kern, unsigned grid, int threads, int smem, cu
   return cudaLaunchKernelEx(&cfg, kern, params...);
 }
 
-template <int D, bool kOne>
+template <int D, bool kLse, bool kOne>
 cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& tq,
                              const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using C = Cfg<D>;
   constexpr int kSmem = C::kData + int(sizeof(Shared));
   static_assert(kSmem <= 232448, "shared memory budget");
   static std::atomic<uint64_t> done{0};
-  auto kern = packed_attention_kernel<D, kOne>;
+  auto kern = packed_attention_kernel<D, kLse, kOne>;
   // the roles' shares of the registers hold for this many at launch
   static std::atomic<bool> counted{false};
   if (!counted.load(std::memory_order_relaxed)) {
@@ -1824,7 +1845,8 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   if (tiles * head_groups <= sms && (!ranges || key_blocks <= kDirectBlocks)) {
     p.mode = kDirect;
     const unsigned grid = unsigned(tiles * head_groups);
-    return launch_attention<D, true>(p, grid, tq, tk, tv, st);
+    return a.lse ? launch_attention<D, true, true>(p, grid, tq, tk, tv, st)
+                 : launch_attention<D, false, true>(p, grid, tq, tk, tv, st);
   }
   p.mode = ranges ? kRanges : kTiles;
   ScheduleParams sp;
@@ -1850,7 +1872,8 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   sp.dev_status = a.dev_status;
   cudaError_t e = launch_kernel(schedule_kernel, 1, kScheduleThreads, 0, st, sp);
   if (e != cudaSuccess) return e;
-  e = launch_attention<D, false>(p, unsigned(workers), tq, tk, tv, st);
+  e = a.lse ? launch_attention<D, true, false>(p, unsigned(workers), tq, tk, tv, st)
+            : launch_attention<D, false, false>(p, unsigned(workers), tq, tk, tv, st);
   if (e != cudaSuccess || !ranges) return e;
   JoinParams jp;
   jp.header = p.header;

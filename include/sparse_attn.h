@@ -841,7 +841,9 @@ sa_status sparse_attn_packed_workspace_size(const sa_packed_shape* shp, size_t* 
  *    needs no preparation and holds nothing between calls; calls that may run
  *    at the same time need one each.
  * Scores, softmax and sums are fp32; the weights are rounded to bf16 for the
- * product with the values, and their normaliser is the sum before that rounding.
+ * product with the values, and their normaliser is the sum after that rounding
+ * (a row of one dominant key gives that key's value exactly); lse is of the sum
+ * before it.
  * The same inputs give the same bits.
  * dev_status: SA_DEV_BAD_COUNT when cu_q or cu_k decreases or leaves
  * [0, total] (clamped), SA_DEV_TIMEOUT as in sparse_attn_forward (its limit is
