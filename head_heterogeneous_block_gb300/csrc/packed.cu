@@ -145,12 +145,14 @@ constexpr int kJoinRows = 8;          // rows of a CTA's part of a join
 constexpr int64_t kL2Share = int64_t(64) << 20;   // keys and values that stay in L2: half of it
 
 // Registers of a thread by role, together the launch's 768 x 80: the others give up
-// what the output warps need.
-constexpr int kLaunchRegs = 80;
+// what the output warps need.  80 is what 768 threads leave each of a processor's
+// 65536 registers, in eights, and so what the compiler has for them; a kernel that
+// it gave fewer is refused, as its output warps would wait for ever.
 constexpr int kControlRegs = 64, kSoftmaxRegs = 72, kOutRegs = 128;
-static_assert(128 * kControlRegs + kSoftmaxThreads * kSoftmaxRegs + kOutThreads * kOutRegs <=
-                  kThreads * kLaunchRegs,
-              "a larger sum would wait forever");
+constexpr int kAllRegs =
+    128 * kControlRegs + kSoftmaxThreads * kSoftmaxRegs + kOutThreads * kOutRegs;
+static_assert(kAllRegs <= kThreads * (65536 / kThreads / 8 * 8),
+              "more than a launch has: it would wait for ever");
 
 template <int D>
 struct Cfg {
@@ -1775,13 +1777,13 @@ cudaError_t launch_attention(const Params& p, unsigned grid, const CUtensorMap& 
   static_assert(kSmem <= 232448, "shared memory budget");
   static std::atomic<uint64_t> done{0};
   auto kern = packed_attention_kernel<D, kLse, kOne>;
-  // the roles' shares of the registers hold for this many at launch
+  // the roles' shares of the registers (which come in eights) need as many at launch
   static std::atomic<bool> counted{false};
   if (!counted.load(std::memory_order_relaxed)) {
     cudaFuncAttributes attr;
     const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    if (kThreads * ((attr.numRegs + 7) / 8 * 8) < kAllRegs) return cudaErrorInvalidKernelImage;
     counted.store(true, std::memory_order_relaxed);
   }
   cudaError_t e = sa_paged::allow_shared(kern, kSmem, done);
