@@ -3,12 +3,20 @@ frequencies and their scalings, and the operator class."""
 from __future__ import annotations
 
 import ctypes
+import decimal
 import math
+import operator
+from decimal import Decimal
 
 import torch
 
 from . import RotaryDesc, _check
 from ._device import DeviceOperator, calls
+
+
+# 64-bit fractions of a turn need more digits than a double has
+_DIGITS = decimal.Context(prec=80)
+_TWO_PI = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
 
 
 def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
@@ -28,6 +36,24 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
                     between them; values times ``attention_factor`` (0.1
                     ln(factor) + 1)
     """
+    freq, multiplier = _frequencies(rot_dim, base, scaling)
+    return [float(f) for f in freq], multiplier
+
+
+def _frequencies(rot_dim, base, scaling):
+    """As ``rotary_frequencies``, to 80 digits."""
+    with decimal.localcontext(_DIGITS):
+        return _scaled(rot_dim, base, scaling)
+
+
+def _turns(freq):
+    """Fractions of a turn a position, in 2^-64ths, of what ``_frequencies`` gives."""
+    with decimal.localcontext(_DIGITS):
+        return [int((f / _TWO_PI * 2**64).to_integral_value()) % 2**64 for f in freq]
+
+
+def _scaled(rot_dim, base, scaling):
+    rot_dim = operator.index(rot_dim)
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
     base = float(base)
@@ -46,21 +72,22 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
 
     multiplier = 1.0
     pairs = range(rot_dim // 2)
+    exact = Decimal(base)
     if kind == "ntk":
         factor = get("factor")
         if rot_dim > 2:
-            base *= factor ** (rot_dim / (rot_dim - 2))
-    freq = [base ** (-2.0 * i / rot_dim) for i in pairs]
+            exact *= Decimal(factor) ** (Decimal(rot_dim) / (rot_dim - 2))
+    freq = [exact ** (Decimal(-2 * i) / rot_dim) for i in pairs]
     if kind == "linear":
-        factor = get("factor")
+        factor = Decimal(get("factor"))
         freq = [f / factor for f in freq]
     elif kind == "wavelength":
-        factor, low, high, original = get("factor"), get("low"), get("high"), get("original")
+        factor, low, high, original = (Decimal(get(x)) for x in ("factor", "low", "high", "original"))
         if not low < high:
             raise ValueError("scaling 'low' must be below 'high'")
-        keep = [min(1.0, max(0.0, (f * original / (2 * math.pi) - low) / (high - low)))
+        keep = [min(Decimal(1), max(Decimal(0), (f * original / _TWO_PI - low) / (high - low)))
                 for f in freq]
-        freq = [f * x + f / factor * (1.0 - x) for f, x in zip(freq, keep)]
+        freq = [f * x + f / factor * (1 - x) for f, x in zip(freq, keep)]
     elif kind == "yarn":
         factor, original = get("factor"), get("original")
         fast, slow = get("beta_fast", 32.0), get("beta_slow", 1.0)
@@ -72,8 +99,9 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
             return rot_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
 
         lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot_dim - 1)
-        slowed = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in pairs]
-        freq = [f * (1.0 - x) + f / factor * x for f, x in zip(freq, slowed)]
+        slowed = [min(Decimal(1), max(Decimal(0), Decimal(i - lo) / max(hi - lo, Decimal("0.001"))))
+                  for i in pairs]
+        freq = [f * (1 - x) + f / Decimal(factor) * x for f, x in zip(freq, slowed)]
     elif kind not in ("none", "ntk"):
         raise ValueError(f"unknown scaling {kind!r}")
     if scaling:
@@ -94,12 +122,12 @@ class Rotary(DeviceOperator):
             raise ValueError("head_dim must be 64 or 128")
         if rot_dim % 16 or not 16 <= rot_dim <= head_dim:
             raise ValueError("rot_dim must be a multiple of 16 up to head_dim")
-        self.frequencies, self.factor = rotary_frequencies(rot_dim, base, scaling)
+        freq, self.factor = _frequencies(rot_dim, base, scaling)
+        self.frequencies = [float(f) for f in freq]
         super().__init__(device)
         self.head_dim, self.rot_dim, self.interleaved = head_dim, rot_dim, bool(interleaved)
-        # fractions of a turn a position, in 2^-64ths (as the signed 64-bit numbers of torch)
-        turns = [round(f / (2 * math.pi) * 2.0**64) % 2**64 for f in self.frequencies]
-        self.turns = torch.tensor([t - 2**64 if t >= 2**63 else t for t in turns],
+        # (as the signed 64-bit numbers of torch)
+        self.turns = torch.tensor([t - 2**64 if t >= 2**63 else t for t in _turns(freq)],
                                   dtype=torch.int64, device=self.device)
         self._desc = RotaryDesc(self.turns.data_ptr(), self.factor, head_dim, rot_dim,
                                 int(self.interleaved))
