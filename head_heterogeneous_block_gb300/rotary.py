@@ -34,7 +34,7 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
                     ``original`` positions, divided by factor below
                     ``beta_slow`` (1), blended in proportion to the pair's number
                     between them; values times ``attention_factor`` (0.1
-                    ln(factor) + 1)
+                    ln(factor) + 1, and 1 for factors up to 1)
     """
     freq, multiplier = _frequencies(rot_dim, base, scaling)
     return [float(f) for f in freq], multiplier
@@ -91,7 +91,7 @@ def _scaled(rot_dim, base, scaling):
     elif kind == "yarn":
         factor, original = get("factor"), get("original")
         fast, slow = get("beta_fast", 32.0), get("beta_slow", 1.0)
-        multiplier = get("attention_factor", 0.1 * math.log(factor) + 1.0)
+        multiplier = get("attention_factor", 0.1 * math.log(max(factor, 1.0)) + 1.0)
         if fast < slow:
             raise ValueError("scaling 'beta_fast' must not be below 'beta_slow'")
 

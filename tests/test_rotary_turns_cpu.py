@@ -78,3 +78,13 @@ def test_turns_are_right_to_their_last_bit(rot, base, scaling):
         assert abs(t - x / (2 * pi()) * 2 ** 64) <= Fraction(1, 2) + Fraction(1, 2 ** 60)
     # and the frequencies beside them are the nearest doubles
     assert rotary.rotary_frequencies(rot, base, given)[0] == [float(x) for x in ref]
+
+
+@pytest.mark.parametrize("factor", [1e-6, 0.5, 1.0])
+def test_yarn_leaves_values_alone_where_it_stretches_nothing(factor):
+    import __graft_entry__
+    __graft_entry__.build()
+    from head_heterogeneous_block_gb300.rotary import rotary_frequencies
+    scaling = {"type": "yarn", "factor": factor, "original": 4096}
+    assert rotary_frequencies(64, 10000.0, scaling)[1] == 1.0
+    assert rotary_frequencies(64, 10000.0, {**scaling, "attention_factor": 0.7})[1] == 0.7
