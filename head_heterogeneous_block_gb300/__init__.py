@@ -34,12 +34,13 @@ __all__ = [
     "RotaryDesc", "sparse_attn_rotary", "sparse_attn_rotary_store",
     "PackedShape", "sparse_attn_packed_forward", "sparse_attn_packed_workspace_size",
 ]
-# these classes need torch, which the C binding itself does not: `import *` asks
-# for it only where there is one
+# these classes need torch, which the C binding itself does not, and all but the
+# first native calls built for it: `import *` asks for them only where there are these
 _CLASSES = {"PagedCache": "paged", "PagePool": "pages", "Rotary": "rotary",
             "PackedAttention": "packed"}
 if (sys.modules["torch"] if "torch" in sys.modules else importlib.util.find_spec("torch")) is not None:
-    __all__.extend(_CLASSES)
+    __all__.extend(_CLASSES if os.path.exists(
+        os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "_calls.so")) else ["PagedCache"])
 
 SA_OK = 0
 SA_MODE_PREFILL, SA_MODE_DECODE = 0, 1

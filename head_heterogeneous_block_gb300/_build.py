@@ -3,8 +3,9 @@ calls of the torch classes beside it.
 
 Translation units are compiled in parallel into ``_build/`` and linked into
 ``head_heterogeneous_block_gb300/_lib/libsparse_attn.so`` and, where there is a
-torch, ``_lib/_calls.so``.  Rebuilds only what changed (by modification time of
-sources and headers).
+torch with its headers and Python's, ``_lib/_calls.so``; the library is built
+whatever becomes of the calls.  Rebuilds only what changed (by modification time
+of sources and headers).
 """
 from __future__ import annotations
 
@@ -52,9 +53,19 @@ def _newest_header() -> float:
 
 
 def _torch():
-    """The torch package's folder, found without importing it; None: there is none."""
+    """The torch package's folder, found without importing it; None: there is
+    none, or no headers to compile the native calls with."""
     spec = importlib.util.find_spec("torch")
-    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+    if not (spec and spec.submodule_search_locations):
+        return None
+    torch = spec.submodule_search_locations[0]
+    for header in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                   os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        if not os.path.exists(header):
+            sys.stderr.write(f"{header} is missing: PackedAttention, Rotary and PagePool are not "
+                             "built\n")
+            return None
+    return torch
 
 
 def _compile(cmd):
@@ -85,9 +96,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
             jobs.append(["g++", *common, "-fPIC", "-Wall", "-c", src, "-o", obj])
     torch = _torch()
     calls_obj = os.path.join(OBJ, "calls.o")
-    if torch is not None:
-        newest = max(os.path.getmtime(CALLS_SRC), hdr,
-                     os.path.getmtime(os.path.join(torch, "version.py")))
+    newest = max(os.path.getmtime(CALLS_SRC), hdr)
+    if torch is None:
+        # (calls of another library are not left beside the new one)
+        if os.path.exists(CALLS) and os.path.getmtime(CALLS) < newest:
+            os.remove(CALLS)
+    else:
+        newest = max(newest, os.path.getmtime(os.path.join(torch, "version.py")))
         if force or not os.path.exists(calls_obj) or os.path.getmtime(calls_obj) < newest:
             dirs = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
                     os.path.join(torch, "include", "torch", "csrc", "api", "include")]
@@ -95,6 +110,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
             jobs.insert(0, ["g++", "-O2", "-std=c++17", f"-I{INCLUDE}",
                             *(f"-isystem{d}" for d in dirs), "-fPIC", "-Wall", "-c", CALLS_SRC,
                             "-o", calls_obj])
+    failed = []
     if jobs:
         with ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
             results = list(ex.map(_compile, jobs))
@@ -102,14 +118,19 @@ def build(verbose: bool = False, force: bool = False) -> str:
         for c, r in results:
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(c) + "\n" + r.stdout + r.stderr)
-        if failed:
-            raise RuntimeError(f"compilation failed: {os.path.basename(failed[0][0][-3])}")
+        if any(c[-1] != calls_obj for c, _ in failed):
+            raise RuntimeError("compilation failed: " + next(
+                os.path.basename(c[-3]) for c, _ in failed if c[-1] != calls_obj))
     if jobs or not os.path.exists(LIB):
         link = [nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(link, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(LIB + ".tmp", LIB)
+    if failed:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        raise RuntimeError(f"compilation failed: {os.path.basename(CALLS_SRC)}")
     if torch is not None and (jobs or not os.path.exists(CALLS)):
         lib = os.path.join(torch, "lib")
         link = ["g++", "-shared", "-o", CALLS + ".tmp", calls_obj, f"-L{LIB_DIR}",
