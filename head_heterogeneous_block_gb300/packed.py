@@ -59,11 +59,12 @@ class PackedAttention(DeviceOperator):
         status = calls.packed(*self._sizes, q, k, v, cu_q, cu_k, out, lse, self._ws_ptr,
                               self._ws_bytes, self._status, self._handle())
         if status == NEEDS_WORKSPACE:
-            # in powers of two, so that calls that grow step by step grow it a few times
+            # in powers of two, so that calls that grow step by step grow it a few times (keys
+            # from their own number on: many of them need several times the workspace)
             sizes = q.shape[0], cu_q.numel() - 1, k.shape[0]
             try:
                 self._size(*(1 << (max(n, least) - 1).bit_length()
-                             for n, least in zip(sizes, (8192, 64, 65536))))
+                             for n, least in zip(sizes, (8192, 64, 1024))))
             except SparseAttnError:      # beyond what a call may have: as it is
                 self._size(*sizes)
             return self(q, k, v, cu_q, cu_k, out, lse)

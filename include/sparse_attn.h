@@ -827,8 +827,10 @@ typedef struct sa_packed_shape {
  * Workspace bytes of sparse_attn_packed_forward.  Host only, except that it
  * asks the current device for its number of processors.  A larger total_q,
  * total_k or batch never needs less, so one workspace can serve the largest of
- * many calls: some 20 MB (head_dim 128), up to 160 MB from a GB of keys and
- * values on, and 32 bytes for every 16 to 128 query rows.
+ * many calls: some 20 MB (head_dim 128; 11 with 64) where the keys and values of
+ * all heads are up to 64 MiB, up to 8 times that from just above 256 MiB on (8
+ * where the groups of query heads, of up to 16 heads of a KV head each, are a
+ * multiple of 8), and 32 bytes for every 16 to 128 query rows.
  */
 sa_status sparse_attn_packed_workspace_size(const sa_packed_shape* shp, size_t* bytes);
 
