@@ -20,6 +20,8 @@ namespace {
 
 struct Refused {};   // a Python exception is set
 
+constexpr int64_t kMaxStride = int64_t(1) << 38;   // elements
+
 [[noreturn]] void type_error(const char* name, const char* what) {
   PyErr_Format(PyExc_TypeError, "%s must be %s", name, what);
   throw Refused{};
@@ -40,19 +42,27 @@ void on_device(const at::Tensor& t, int64_t index, const char* name) {
     value_error("%s must be on cuda:%lld", name, static_cast<long long>(index));
 }
 
-// A bf16 [tokens, heads, d] view.
+// A bf16 [tokens, heads, d] view, whose rows are at least `least` elements apart.
 struct Rows {
   void* at = nullptr;
   int64_t tokens = 0;
   int64_t strides[2] = {0, 0};
 };
-Rows rows(PyObject* o, int64_t index, int64_t heads, int64_t d, const char* name) {
+Rows rows(PyObject* o, int64_t index, int64_t heads, int64_t d, int64_t least, const char* name) {
   const at::Tensor& t = tensor(o, name);
   if (t.scalar_type() != at::kBFloat16) type_error(name, "bfloat16");
   if (t.dim() != 3 || t.size(1) != heads || t.size(2) != d)
     value_error("%s must be [tokens, %lld, %lld]", name, static_cast<long long>(heads),
                 static_cast<long long>(d));
   if (t.stride(2) != 1) value_error("the last dimension of %s must be contiguous", name);
+  // (the stride of an extent of one is not used)
+  for (int i = 0; i < 2; ++i)
+    if (t.size(i) > 1 && (t.stride(i) % 8 || t.stride(i) < least || t.stride(i) >= kMaxStride))
+      value_error("%s has a stride of %lld elements between %s: it must be a multiple of 8, at least "
+                  "%lld and below 2^38", name, static_cast<long long>(t.stride(i)),
+                  i ? "heads" : "tokens", static_cast<long long>(least));
+  if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16)
+    value_error("%s must start on a 16-byte boundary", name);
   on_device(t, index, name);
   return Rows{t.data_ptr(), t.size(0), {t.stride(0), t.stride(1)}};
 }
@@ -120,14 +130,14 @@ PyObject* packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t index = number(a[0]), heads = number(a[1]), kv = number(a[2]), d = number(a[3]);
     const double scale = PyFloat_AsDouble(a[4]);
     if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
-    const Rows q = rows(a[8], index, heads, d, "q"), k = rows(a[9], index, kv, d, "k"),
-               v = rows(a[10], index, kv, d, "v");
+    const Rows q = rows(a[8], index, heads, d, d, "q"), k = rows(a[9], index, kv, d, d, "k"),
+               v = rows(a[10], index, kv, d, d, "v");
     if (v.tokens != k.tokens) value_error("k and v must have the same number of tokens");
     const int64_t ends = tensor(a[11], "cu_q").numel();
     if (ends < 2) value_error("cu_q must be [batch + 1]");
     const int32_t* cu_q = own_i32(a[11], index, ends, -1, "cu_q", true);
     const int32_t* cu_k = a[12] == Py_None ? cu_q : own_i32(a[12], index, ends, -1, "cu_k");
-    const Rows o = rows(a[13], index, heads, d, "out");
+    const Rows o = rows(a[13], index, heads, d, d, "out");
     if (o.tokens != q.tokens) value_error("out must have q's shape");
     float* lse = own<float>(a[14], index, at::kFloat, "torch.float32", q.tokens, heads, "lse");
     if (q.tokens > number(a[5]) || ends - 1 > number(a[6]) || k.tokens > number(a[7]))
@@ -167,8 +177,9 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 9, [&]() -> long {
     const int64_t index = number(a[1]), d = number(a[2]);
     const int64_t hq = heads_of(a[3], d, "q"), hkv = heads_of(a[4], d, "k");
-    const Rows q = rows(a[3], index, hq, d, "q"), k = rows(a[4], index, hkv, d, "k"),
-               qo = rows(a[6], index, hq, d, "q_out"), ko = rows(a[7], index, hkv, d, "k_out");
+    const Rows q = rows(a[3], index, hq, d, 0, "q"), k = rows(a[4], index, hkv, d, 0, "k"),
+               qo = rows(a[6], index, hq, d, d, "q_out"),
+               ko = rows(a[7], index, hkv, d, d, "k_out");
     if (k.tokens != q.tokens) value_error("q and k must have the same number of tokens");
     if (qo.tokens != q.tokens || ko.tokens != q.tokens)
       value_error("q_out and k_out must have the shapes of q and k");
@@ -185,12 +196,12 @@ PyObject* rotary_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 14, [&]() -> long {
     const int64_t index = number(a[1]), d = number(a[2]), hkv = number(a[3]);
     const int64_t hq = heads_of(a[4], d, "q");
-    const Rows q = rows(a[4], index, hq, d, "q"), k = rows(a[5], index, hkv, d, "k"),
-               v = rows(a[6], index, hkv, d, "v"), qo = rows(a[10], index, hq, d, "q_out");
+    const Rows q = rows(a[4], index, hq, d, 0, "q"), k = rows(a[5], index, hkv, d, 0, "k"),
+               v = rows(a[6], index, hkv, d, 0, "v"), qo = rows(a[10], index, hq, d, d, "q_out");
     if (k.tokens != q.tokens || v.tokens != q.tokens)
       value_error("q, k and v must have the same number of tokens");
     Rows ko;
-    if (a[11] != Py_None) ko = rows(a[11], index, hkv, d, "k_out");
+    if (a[11] != Py_None) ko = rows(a[11], index, hkv, d, d, "k_out");
     if (qo.tokens != q.tokens || (a[11] != Py_None && ko.tokens != q.tokens))
       value_error("q_out and k_out must have the shapes of q and k");
     const int32_t* positions = own_i32(a[7], index, q.tokens, -1, "positions", true);

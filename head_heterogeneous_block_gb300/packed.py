@@ -43,7 +43,8 @@ class PackedAttention(DeviceOperator):
 
     def __call__(self, q, k, v, cu_q, cu_k=None, out=None, lse=None, stream=None):
         """q bf16 [tokens, num_q_heads, d]; k, v bf16 [keys, num_kv_heads, d]
-        (any strides that are multiples of 8, d contiguous).  Sequence s has the
+        (strides multiples of 8, at least head_dim and below 2^38, d contiguous,
+        16-byte aligned; a head that several share is given once).  Sequence s has the
         rows ``cu_q[s]`` to ``cu_q[s + 1]`` of q and ``cu_k[s]`` to ``cu_k[s +
         1]`` of k and v (int32 [batch + 1]; ``cu_k``: ``cu_q`` by default).  Its
         queries are its last tokens: with n queries and m keys, query i sees the

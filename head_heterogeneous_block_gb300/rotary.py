@@ -143,10 +143,11 @@ class Rotary(DeviceOperator):
         return torch.empty(t.shape, dtype=torch.bfloat16, device=self.device)
 
     def __call__(self, q, k, positions, q_out=None, k_out=None, stream=None):
-        """q bf16 [tokens, num_q_heads, d], k bf16 [tokens, num_kv_heads, d] (any
-        strides that are multiples of 8, d contiguous) and positions int32
-        [tokens].  Returns (``q_out``, ``k_out``): new tensors without them;
-        each may be its input, which then changes in place."""
+        """q bf16 [tokens, num_q_heads, d], k bf16 [tokens, num_kv_heads, d]
+        (strides multiples of 8 below 2^38, 0 among them, d contiguous, 16-byte
+        aligned) and positions int32 [tokens].  Returns (``q_out``, ``k_out``:
+        their strides at least head_dim): new tensors without them; each may be
+        its input, which then changes in place."""
         if self._elsewhere(stream):
             return self._on(stream, lambda: self(q, k, positions, q_out, k_out))
         q_out = self._like(q) if q_out is None else q_out
