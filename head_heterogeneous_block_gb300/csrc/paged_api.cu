@@ -83,6 +83,21 @@ sa_status check_pool(const sa_page_pool* p) {
   return SA_OK;
 }
 
+// Whether two rows of d elements of a [tokens][heads] output share memory (strides at
+// least d where they are used).
+bool rows_share(int64_t tokens, int64_t heads, int64_t d, const int64_t* s) {
+  using Wide = __int128;
+  if (tokens <= 1 || heads <= 1 || s[0] >= Wide(heads - 1) * s[1] + d ||
+      s[1] >= Wide(tokens - 1) * s[0] + d)
+    return false;
+  // tokens lie between heads: h heads further is nearly t or t + 1 tokens further
+  for (int64_t h = 1; h < heads; ++h) {
+    const int64_t t = h * s[1] / s[0], over = h * s[1] - t * s[0];
+    if ((t < tokens && over < d) || (t + 1 < tokens && s[0] - over < d)) return true;
+  }
+  return false;
+}
+
 // Checks and arguments of the two rotary calls, but for the store's.
 sa_status rotary_args(const sa_rotary* rot, int32_t tokens, int32_t hq, int32_t hkv,
                       const int32_t* positions, const void* q, const int64_t* qs, const void* k,
@@ -117,6 +132,10 @@ sa_status rotary_args(const sa_rotary* rot, int32_t tokens, int32_t hq, int32_t 
     return SA_ERR_INVALID_ARG;
   a->kos[0] = a->kos[1] = 0;
   if (k_out && !strides(kos, hkv, rot->head_dim, a->kos)) return SA_ERR_INVALID_ARG;
+  // they would be written by two warps
+  if (rows_share(tokens, hq, rot->head_dim, a->qos) ||
+      (k_out && rows_share(tokens, hkv, rot->head_dim, a->kos)))
+    return SA_ERR_INVALID_ARG;
   auto same = [](const int64_t* x, const int64_t* y) { return x[0] == y[0] && x[1] == y[1]; };
   if (tokens > 0) {
     if ((q_out == q && !same(a->qs, a->qos)) || (k_out == k && !same(a->ks, a->kos)) ||
@@ -348,6 +367,8 @@ sa_status sparse_attn_rotary_store(const sa_rotary* rot, int32_t tokens, int32_t
   if (rot->head_dim != cache->head_dim) return SA_ERR_SHAPE;
   if (!v_strides || !dev_status || (tokens > 0 && (!v || !slots))) return SA_ERR_INVALID_ARG;
   if (!aligned(v, 16) || !aligned(slots, 8) || !aligned(dev_status, 4)) return SA_ERR_INVALID_ARG;
+  // (an output may be its own input, which v is not)
+  if (tokens > 0 && (q_out == v || k_out == v)) return SA_ERR_INVALID_ARG;
   for (int i = 0; i < 2; ++i) {
     const bool used = (i ? cache->num_kv_heads : tokens) > 1;
     if (used && (v_strides[i] < 0 || v_strides[i] % 8 || v_strides[i] >= kMaxStride))

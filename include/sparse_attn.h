@@ -764,8 +764,9 @@ typedef struct sa_rotary {
  *  - positions: device int32 [tokens], any value.
  * An angle is within 2^-24 of a half turn at any position; values are fp32,
  * rounded once to bf16.
- * Errors: INVALID_ARG (NULL, misalignment, strides, outputs of the same
- * address, factor), SHAPE (sizes), UNSUPPORTED (head_dim, rot_dim), CUDA.
+ * Errors: INVALID_ARG (NULL, misalignment, strides, an output whose rows share
+ * memory, outputs of the same address or of another's input, factor), SHAPE
+ * (sizes), UNSUPPORTED (head_dim, rot_dim), CUDA.
  */
 sa_status sparse_attn_rotary(const sa_rotary* rot, int32_t tokens, int32_t num_q_heads,
                              int32_t num_kv_heads, const int32_t* positions, const void* q,
