@@ -48,6 +48,13 @@ class DeviceOperator:
         # the streams that the status word and the workspace were allocated on
         self._status_stream = self._ws_stream = _raw_stream(self._index)
 
+    def _made(self):
+        """The end of a constructor: what it queued, and what its memory's last
+        owners had queued before, is done, so that a call may go to any stream."""
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
     def _need(self, need):
         """A workspace of at least ``need`` bytes; the device is current."""
         if need <= self._ws_bytes:

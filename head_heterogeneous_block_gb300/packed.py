@@ -28,6 +28,7 @@ class PackedAttention(DeviceOperator):
         self._tokens = self._batch = self._keys = 0
         with torch.cuda.device(self.device):
             self._size(tokens, batch, tokens if keys is None else keys)
+        self._made()
 
     def _size(self, tokens, batch, keys):
         """Grow the workspace to what calls of these sizes need, and those so

@@ -104,6 +104,11 @@ class PagedCache:
             self._size(num_q_heads, weights is not None)
         if weights is not None and self.slots <= MAX_EVICT_SLOTS and h <= MAX_EVICT_KV_HEADS:
             self._size()
+        # what was queued here, and by the last owners of its memory before, is done: a
+        # call may go to any stream
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     # -- helpers (a step's calls are short: checks are written out where a
     # call per check, or a message built for nothing, would cost more)

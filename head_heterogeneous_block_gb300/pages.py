@@ -56,9 +56,10 @@ class PagePool(DeviceOperator):
             self._own(weights, torch.float32, slots, "weights"),
             self._own(positions, i32, slots, "positions"), self.num_pages, page, max_pages, b, h)
         self._desc_ptr = ctypes.addressof(self._desc)
-        self._made = () if num_pages is None else (free_pages, free_count, owned)
+        self._own_tensors = () if num_pages is None else (free_pages, free_count, owned)
         with torch.cuda.device(self.device):
             self._need(sparse_attn_paged_grow_workspace_size(self._desc))
+        self._made()
 
     @classmethod
     def of(cls, cache):
@@ -93,7 +94,7 @@ class PagePool(DeviceOperator):
                 free_count_out, start_out))
         handle = self._handle()
         if handle != self._status_stream:
-            for t in self._made:
+            for t in self._own_tensors:
                 t.record_stream(self._stream(handle))
         status = calls.grow(self._desc_ptr, self._index, slots, cu, counts, ended, start,
                             positions, granted, lens_out, owned_out, free_count_out, start_out,

@@ -132,6 +132,7 @@ class Rotary(DeviceOperator):
         self._desc = RotaryDesc(self.turns.data_ptr(), self.factor, head_dim, rot_dim,
                                 int(self.interleaved))
         self._desc_ptr = ctypes.addressof(self._desc)
+        self._made()
 
     def _follow(self):
         handle = self._handle()
