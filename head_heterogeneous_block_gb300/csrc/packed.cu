@@ -142,6 +142,7 @@ constexpr int kTileRegs = 4;          // tiles of a thread that it remembers
 constexpr int kMaxWorkers = 256;      // CTAs that share the work: a tile has no more ranges
 constexpr int kFew = 4;               // ranges that a thread joins by itself
 constexpr int kJoinRows = 8;          // rows of a CTA's part of a join
+constexpr float kWeightless = -3.402823466e38f;   // reference of a range of weights 0 alone
 constexpr int64_t kL2Share = int64_t(64) << 20;   // keys and values that stay in L2: half of it
 
 // Registers of a thread by role, together the launch's 768 x 80: the others give up
@@ -687,6 +688,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
         add(__ldcg(po + int64_t(i) * (D / 4) * kRows), weight[i][r].x * inv, weight[i][r].y);
       __syncthreads();                                       // before the weights change
     }
+    if (l == 0.f && m == kWeightless) acc.x = acc.y = acc.z = acc.w = NAN;
     const int tok = row / p.tile_heads, head = row - tok * p.tile_heads;
     if (tok < cut.ntok) {
       const int64_t t = int64_t(cut.q0) + tok;
@@ -1028,6 +1030,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!in_range) atomicOr(&sh->maxima[it.pos >> 5], bit);
       }
       if (!whole) {
+        // (keys of which none weighs anything are not the same as none at all: a row of
+        // such ranges alone has no mean)
+        if (some && l == 0.f) m = kWeightless;
         if (live) p.part_ml[int64_t(it.e.slot) * kRows + row] = make_float4(m, l, less, lx);
       } else if (kLse && live) {
         p.lse[(int64_t(it.e.q0) + tok) * p.Hq + it.head0 + head] =
@@ -1157,11 +1162,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_used = top * c;
         last = careful & kSmall ? -less_of(n) : 0.f;
         // (below 2^20 the reference's rounding leaves 2^-5 of an exponent at most, and a
-        // row that is done again for another's sake keeps its bits)
+        // row that is done again for another's sake keeps its bits if its maximum was in
+        // the first block)
         if (!(careful & kSmall) && fabsf(m_used) <= 0x1p20f) {
           last = -m_used;
           top = 0.f;
         }
+        // (no score of the item is above -infinity: no weight above 0)
+        if (top == -INFINITY) top = 0.f;
       }
       // the sums of rounded weights and of unrounded ones, in parts
       float sum0 = 0.f, sum1 = 0.f, x0 = 0.f, x1 = 0.f;

@@ -81,3 +81,28 @@ def test_one_key_above_the_others(sa, lens_q, lens_k, at):  # noqa: F811
     ref = 64 * 30720.0 * 30848.0 / 8
     assert ((lse[first:].double() - ref).abs() <= 2.0 ** -22 * ref).all()
     check(out[:first], lse[:first], v, [first], [at] if first else [0], 64 * 30720.0 ** 2 / 8)
+
+
+@pytest.mark.parametrize("lens_q,lens_k,low", [([60], [60], 40), ([700], [700], 400), ([20], [4000], 1500),
+                                               ([20], [4000], 3990), ([100] * 50, [2000] * 50, 1100)])
+@pytest.mark.parametrize("by", ["infinity", "overflow"])
+def test_keys_whose_scores_are_minus_infinity(sa, by, lens_q, lens_k, low):  # noqa: F811
+    # They weigh nothing beside others, whole blocks and ranges of them too; a row that sees no other key has no mean
+    d = 64
+    q, k, v, cq, ck = tp.inputs(83, lens_q, lens_k, 4, 2, d, device="cuda")
+    q[..., 0] = 1.0 if by == "infinity" else 1e20
+    k[..., 0] = 0.0
+    at = [(sum(lens_k[:i]), n, m) for i, (n, m) in enumerate(zip(lens_q, lens_k))]
+    for first, _, _ in at:
+        k[first:first + low] = 0.0
+        k[first:first + low, :, 0] = -math.inf if by == "infinity" else -1e20
+    out, lse = run(sa, 4, 2, d, q, k, v, cq, ck)
+    # the same queries behind the other keys alone
+    keep = torch.cat([torch.arange(first + low, first + m) for first, _, m in at]).cuda()
+    rest = [m - low for m in lens_k]
+    ref = tp.reference(q, k[keep], v[keep], cq, tp.cu_of(rest).cuda())
+    sees = torch.cat([torch.arange(m - n, m) >= low for _, n, m in at])
+    assert out[~sees.cuda()].isnan().all() and (lse[~sees.cuda()] == -math.inf).all()
+    got, gl = out.clone(), lse.clone()
+    got[~sees.cuda()], gl[~sees.cuda()] = 0.0, -math.inf
+    tp.check(ref, got, gl, lens_q, rest, d)
