@@ -1850,7 +1850,7 @@ cudaError_t launch_d(const Args& a, int sms, cudaStream_t st, bool* encode_faile
   p.head_groups = int32_t(head_groups);
   p.by_head = s.total_k * key_bytes(s) > kL2Share;
   p.round_slots = int32_t(lay.round_slots);
-  p.scale_log2 = float(double(s.scale) * 1.4426950408889634);
+  p.scale_log2 = sa_packed::scale_log2(s);
   p.dev_status = a.dev_status;
   p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
   // every tile its own CTA, none worth cutting

@@ -35,6 +35,11 @@ inline Tile tile_of(const sa_packed_shape& s) {
   return t;
 }
 
+// The factor of the scores' exponents, base 2.
+inline float scale_log2(const sa_packed_shape& s) {
+  return float(double(s.scale) * 1.4426950408889634);
+}
+
 // Tiles that any lengths of these totals can make, at most.
 inline int64_t most_tiles(const sa_packed_shape& s) {
   const int64_t seqs = s.batch < s.total_q ? s.batch : s.total_q;

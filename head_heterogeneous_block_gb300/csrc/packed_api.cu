@@ -30,7 +30,8 @@ sa_status check_shape(const sa_packed_shape* s) {
   const int64_t heads = s->num_q_heads / sa_packed::tile_of(*s).heads;
   if (heads > (1 << 20) || (sa_packed::most_tiles(*s) + 4096) > (int64_t(1) << 30) / heads)
     return SA_ERR_SHAPE;
-  if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return SA_ERR_INVALID_ARG;
+  // (scores are scaled to base 2)
+  if (!(s->scale > 0.f) || !std::isfinite(sa_packed::scale_log2(*s))) return SA_ERR_INVALID_ARG;
   return SA_OK;
 }
 

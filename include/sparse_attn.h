@@ -821,7 +821,8 @@ typedef struct sa_packed_shape {
   int32_t num_q_heads;
   int32_t num_kv_heads;    /* divides num_q_heads                             */
   int32_t head_dim;        /* 64 or 128                                       */
-  float scale;             /* of the scores: positive and finite              */
+  float scale;             /* of the scores: positive and finite, also times
+                              log2 e                                          */
 } sa_packed_shape;
 
 /*
