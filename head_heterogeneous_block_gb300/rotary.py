@@ -77,7 +77,10 @@ def _scaled(rot_dim, base, scaling):
         factor = get("factor")
         if rot_dim > 2:
             exact *= Decimal(factor) ** (Decimal(rot_dim) / (rot_dim - 2))
-    freq = [exact ** (Decimal(-2 * i) / rot_dim) for i in pairs]
+    # (one root and its powers: a root each would take milliseconds)
+    step, freq = exact ** (Decimal(-2) / rot_dim), [Decimal(1)]
+    while len(freq) < len(pairs):
+        freq.append(freq[-1] * step)
     if kind == "linear":
         factor = Decimal(get("factor"))
         freq = [f / factor for f in freq]
