@@ -25,9 +25,11 @@
 //   shares, a CTA each; tiles at a share's end are cut, their ranges leave their
 //   reference, sums and unnormalised output, and a third launch joins them in key
 //   order.  Head groups go round by round, so that a round's keys and values stay
-//   in L2: chunks of 509 tokens behind 32K to 64K, 64/8 heads: 1.36 ms, against
+//   in L2: two chunks of 509 tokens behind 44K and 65K, 64/8 heads: 1.36 ms, against
 //   1.43 from the counter (512 items of two lengths do not divide by 152) and
 //   1.53 with rounds of 100 MB instead of 50 (all three before the last steps below).
+//   (The choice goes by the tensors' sizes, total keys against total queries: it is
+//   made on the host, where the lengths are not known.)
 // Where every tile gets a CTA of its own the CTAs find their tiles themselves and
 // there is no first launch.
 //
@@ -79,24 +81,27 @@
 // another.
 //
 // Measured (GB300; 1937 TFLOP/s bf16, 1725 sustained under the power cap; masked
-// halves of blocks not counted as work): a prompt of 32768 tokens, 32/8 heads, d =
-// 128: 5.6 ms, 1570 TFLOP/s, 81%; 16 prompts of 1 to 4096, 28/4 heads: 438 us, 1460
-// TFLOP/s, 76%; the chunks above: 1300 TFLOP/s, 67%; 24 prompts of 1 to 1024, 8/2
-// heads, d = 64: 26.3 us; one of 41 tokens: 9.1 us; 16 tokens behind 128K keys, 64/8
-// heads: 118 us of 79 at the copy rate.
+// halves of blocks not counted as work; with log-sum-exps; the lower times in runs of
+// milliseconds, the others under a load of seconds): a prompt of 32768 tokens, 32/8
+// heads, d = 128: 5.6 to 5.75 ms, 1530 to 1560 TFLOP/s, 79 to 81%; 16 prompts of 1 to
+// 4096 (29166 tokens in all), 28/4 heads: 427 to 455 us, 1150 to 1230 TFLOP/s, 60 to
+// 63%; the chunks above: 1200 to 1305 us, 1400 to 1520 TFLOP/s, 72 to 79%; 24 prompts
+// of 1 to 1024, 8/2 heads, d = 64: 28 us; one of 41 tokens: 9.2 us; 16 tokens behind
+// 128K keys, 64/8 heads: 125 us of 79 at the copy rate; a prompt of 32768, 32/8 heads,
+// d = 64: 4.0 ms, 1090 TFLOP/s, and 3.8 without log-sum-exps.
 //
 // The long prompt, the 16 and the chunks, step by step: 6030, 468 and 1368 us with P
-// over its S in three buffers, Q in shared memory and two sums, of the weights
-// before and after their rounding; 5800, 443 and 1310 with one sum (five
-// instructions a pair of weights instead of eight); 5570, 438 and 1265 with the
-// layout of now, and a join of few ranges in one latency.  (Two S buffers without
-// the copies of Q: 6120, 456 and 1360.)  What is left: P's columns, whose P V must be
-// done before the next P is stored, some 1000 cycles from P to that; and items'
-// ends.  Measured and not kept: pairs of CTAs on tiles of 256 rows, which share K
-// and V (6140 and 479: what one CTA signals the other takes 800 cycles, and the loop
-// crosses three times); P in two halves (5530, but 466); two sets of eight softmax
-// warps on every other block each (3% and 1% slower); one arrival a warp at P's
-// barrier (0.5% slower).
+// over its S in three buffers and Q in shared memory; 5740, 456 and 1305 with the
+// layout of now, and a join of few ranges in one latency.  (Two S buffers without the
+// copies of Q: 6120, 456 and 1360.)  The two sums of the weights take seven
+// instructions a pair of weights, one sum would take five: 5720, 448 and 1303 where two
+// took 5785, 460 and 1328.  What is left: P's columns, whose P V must be done before
+// the next P is stored, some 1000 cycles from P to that; and items' ends.  Measured and
+// not kept (with one sum: 5570, 438 and 1265 without them): pairs of CTAs on tiles of
+// 256 rows, which share K and V (6140 and 479: what one CTA signals the other takes 800
+// cycles, and the loop crosses three times); P in two halves (5530, but 466); two sets
+// of eight softmax warps on every other block each (3% and 1% slower); one arrival a
+// warp at P's barrier (0.5% slower); the sums behind P's store (4% slower).
 //
 // Before that, the 16 prompts: 513 us with softmax warps that also write the output
 // and scan V in every block that the mask cuts; 505 with output warps; 482 with the
@@ -104,7 +109,7 @@
 // loads then waited for it; 468 with 64 columns of a row in registers at a time
 // instead of all.  Items of one block (256 prompts of 32 tokens, 32/8 heads) take as
 // long as their output does: 84 us with TMA stores, whose reads of the buffer it
-// waited for, 68 with whole rows in registers, 61 with a short loop.
+// waited for, 68 with whole rows in registers, 61 with a short loop (67 with two sums).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
 // the weights of a row's ranges once, to shared memory, then the sums over ranges,
 // eight loads under way.  Of up to kFew ranges a thread loads and weighs all of its
 // row by itself, in one latency (the chunks of the header: 65 us with shared
-// memory's barriers between, 40 so).
+// memory's barriers between, 40 so, before it compared references first).
 struct JoinParams {
   const Header* header;
   const Cut* cuts;

@@ -17,11 +17,13 @@
 // warp works out its token's sines once for all of its heads; each lane works
 // out as many as there are lanes to share them and gets the rest from the
 // others.  Lanes behind `rot` pass their 16 elements on.
-
-// Measured (GB300): 32767 tokens, 32/8 heads, d = 128, with the store: 128 us, 6.8
+//
+// Measured (GB300): 32767 tokens, 32/8 heads, d = 128, with the store: 129 us, 6.8
 // TB/s, the copy rate; 2049 tokens, 28/4 heads, half of each head in interleaved
-// pairs: 6.7 us of 5.0 at the copy rate; 4096 tokens, 8/2 heads, d = 64: 4.1 us of
-// 1.6; a decode step of 64 tokens: 2.2 us, a launch's time.
+// pairs: 9.7 us from HBM, 6.7 with all in L2, of 5.0 at the copy rate: the chain from
+// a position to its sines stands before a warp's first load, which a call of many
+// waves does not see; 4096 tokens, 8/2 heads, d = 64: 4.9 and 4.2 us of 1.6; a decode
+// step of 64 tokens: 2.3 us, a launch's time.
 
 #include <cuda_bf16.h>
 
